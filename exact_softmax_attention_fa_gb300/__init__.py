@@ -16,7 +16,8 @@ import math
 from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: F401
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_bwd_deterministic", "fa_bwd_gqa_deterministic", "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_bwd_preprocess", "fa_bwd_preprocess_stats", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_bwd_host", "fa_fwd_bwd_host_device_bytes", "fa_fwd_host", "fa_fwd_host_device_bytes", "fa_get_device_status", "fa_get_device_status_detail", "fa_set_wait_limit_ns",
-           "fa_debug_timeout_probe", "fa_debug_skip_arrival", "forward", "backward", "FAError", "flops"]
+           "fa_debug_timeout_probe", "fa_debug_skip_arrival", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
+           "fa_norm_rope_bwd_workspace_size", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
 
 _SUPPORTED_D = (64, 128, 256)
 
@@ -342,6 +343,140 @@ def fa_fwd_host(q, k, v, o, lse, causal: bool, scale: float, device_buffer, stre
         float(scale), device_buffer.data_ptr(), device_buffer.numel(), _stream_handle(stream)))
 
 
+def rope_tables(rows: int, rot: int, base: float = 10000.0, device="cuda"):
+    """Cosines and sines of the position rotation, fp32 [rows, rot / 2] each: the
+    angle of pair i at position p is p * base^(-2 i / rot), formed in 64 bits."""
+    import torch
+    freq = torch.pow(torch.tensor(base, dtype=torch.float64),
+                     -torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq.to(device)[None, :]
+    return angle.cos().float(), angle.sin().float()
+
+
+def _check_on_current_device(named):
+    """Every tensor given is on the current CUDA device (the library launches there)."""
+    import torch
+    here = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError(f"{name} must be on the current CUDA device (cuda:{here}), got {t.device}")
+
+
+def _head_strides(name, t, shape):
+    """(batch, head, token) strides of a bf16 [B, H, N, d] tensor with contiguous rows."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.stride()[:3]
+
+
+def _norm_rope_args(shapes, strided, wq, wk, cos, sin, positions):
+    """Checks shared by the two directions; returns the host array of strides,
+    the weights' type flag, the tables' rows and rot."""
+    import ctypes
+    import torch
+    B, _, N, d = shapes[0]
+    strides = (ctypes.c_longlong * 9)()
+    for t, (name, x) in enumerate(strided):
+        if x is not None:
+            strides[3 * t:3 * t + 3] = _head_strides(name, x, shapes[t])
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk are given together or not at all")
+    if wq is not None:
+        for name, w in (("wq", wq), ("wk", wk)):
+            if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != wq.dtype:
+                raise TypeError(f"{name} must be float32 or bfloat16 (both weights the same), got {w.dtype}")
+            if tuple(w.shape) != (d,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous tensor of shape ({d},)")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin are given together or not at all")
+    rows = rot = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [rows, rot / 2] tensors of one shape")
+        for name, x in (("cos", cos), ("sin", sin)):
+            if x.dtype != torch.float32 or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor")
+        rows, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N)
+                                  or not positions.is_contiguous()):
+        raise ValueError(f"positions must be a contiguous int32 tensor of shape {(B, N)}")
+    return strides, int(wq is not None and wq.dtype == torch.bfloat16), rows, rot
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved: bool = False,
+                     eps: float = 1e-6, stream=None) -> None:
+    """fa_norm_rope_fwd of the C ABI: q_in [B, Hq, N, d], k_in, v_in [B, Hkv, N, d] with any
+    strides and contiguous rows (views of a packed projection); q, k, v contiguous.
+
+    wq, wk None: no norm. cos, sin (rope_tables) None: no rotation. v_in, v
+    None: no values. positions None: token n is at position n.
+    """
+    B, Hq, N, d = _dims(q_in)
+    qs, ks = (B, Hq, N, d), (B, int(k_in.shape[1]), N, d)
+    if (v_in is None) != (v is None):
+        raise ValueError("v_in and v are given together or not at all")
+    strides, w_bf16, rows, rot = _norm_rope_args((qs, ks, ks), (("q_in", q_in), ("k_in", k_in), ("v_in", v_in)), wq, wk,
+                                                 cos, sin, positions)
+    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks)):
+        if t is not None:
+            _check_bf16(name, t, shape)
+    _check_on_current_device((("q_in", q_in), ("k_in", k_in), ("v_in", v_in), ("wq", wq), ("wk", wk), ("cos", cos),
+                              ("sin", sin), ("positions", positions), ("q", q), ("k", k), ("v", v)))
+    check("fa_norm_rope_fwd", load().fa_norm_rope_fwd(
+        _ptr(q_in), _ptr(k_in), _ptr(v_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos), _ptr(sin), rows,
+        _ptr(positions), _ptr(q), _ptr(k), _ptr(v), B, Hq, ks[1], N, d, rot, int(bool(interleaved)), float(eps),
+        _stream_handle(stream)))
+
+
+def fa_norm_rope_bwd_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
+    return int(load().fa_norm_rope_bwd_workspace_size(B, Hq, Hkv, N, d))
+
+
+def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk, workspace,
+                     interleaved: bool = False, eps: float = 1e-6, stream=None) -> None:
+    """fa_norm_rope_bwd of the C ABI: dq [B, Hq, N, d], dk, dv [B, Hkv, N, d] contiguous (in); q_in,
+    k_in as in the forward; dq_in, dk_in, dv_in (out) with any strides that keep
+    their rows apart; dwq, dwk float32 [d] (out).
+
+    Without weights q_in, k_in, dwq, dwk and workspace are not used.
+    """
+    import ctypes
+    import torch
+    B, Hq, N, d = _dims(dq)
+    qs, ks = (B, Hq, N, d), (B, int(dk.shape[1]), N, d)
+    if (dv is None) != (dv_in is None):
+        raise ValueError("dv and dv_in are given together or not at all")
+    strides, w_bf16, rows, rot = _norm_rope_args((qs, ks, ks), (("dq_in", dq_in), ("dk_in", dk_in), ("dv_in", dv_in)),
+                                                 wq, wk, cos, sin, positions)
+    in_strides = (ctypes.c_longlong * 9)()
+    if wq is not None:
+        for t, (name, x, shape) in enumerate((("q_in", q_in, qs), ("k_in", k_in, ks))):
+            in_strides[3 * t:3 * t + 3] = _head_strides(name, x, shape)
+        for name, x in (("dwq", dwq), ("dwk", dwk)):
+            if x.dtype != torch.float32 or tuple(x.shape) != (d,) or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({d},)")
+    for name, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
+        if t is not None:
+            _check_bf16(name, t, shape)
+    _check_on_current_device((("dq", dq), ("dk", dk), ("dv", dv), ("q_in", q_in), ("k_in", k_in), ("wq", wq),
+                              ("wk", wk), ("cos", cos), ("sin", sin), ("positions", positions), ("dq_in", dq_in),
+                              ("dk_in", dk_in), ("dv_in", dv_in), ("dwq", dwq), ("dwk", dwk),
+                              ("workspace", workspace)))
+    check("fa_norm_rope_bwd", load().fa_norm_rope_bwd(
+        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(q_in), _ptr(k_in), in_strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos),
+        _ptr(sin), rows, _ptr(positions), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), strides, _ptr(dwq), _ptr(dwk), B, Hq,
+        ks[1], N, d, rot, int(bool(interleaved)), float(eps), *_ws(workspace), _stream_handle(stream)))
+
+
 def fa_get_device_status(stream=None) -> int:
     """Synchronise the stream; return and clear the device status (0 = FA_OK)."""
     return int(load().fa_get_device_status(_stream_handle(stream)))
@@ -409,6 +544,39 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
         fn = fa_bwd_deterministic if deterministic else fa_bwd
     fn(q, k, v, o, lse, do, dq, dk, dv, causal, scale, workspace, stream)
     return dq, dk, dv
+
+
+def norm_rope(q_in, k_in, v_in=None, wq=None, wk=None, cos=None, sin=None, positions=None, interleaved: bool = False,
+              eps: float = 1e-6, stream=None):
+    """Allocate q, k (and v) as [B, H, N, d] with torch and run fa_norm_rope_fwd: what `forward` and
+    the cache take, from the views of a packed projection."""
+    import torch
+    q, k = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) for x in (q_in, k_in))
+    v = None if v_in is None else torch.empty(v_in.shape, dtype=torch.bfloat16, device=v_in.device)
+    fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved, eps, stream)
+    return q, k, v
+
+
+def norm_rope_backward(dq, dk, dv, q_in, k_in, wq=None, wk=None, cos=None, sin=None, positions=None, out=None,
+                       interleaved: bool = False, eps: float = 1e-6, workspace=None, stream=None):
+    """Run fa_norm_rope_bwd on `backward`'s dq, dk, dv; returns (dq_in, dk_in, dv_in, dwq, dwk).
+
+    out: (dq_in, dk_in, dv_in) to write, e.g. the views of one packed gradient;
+    None allocates contiguous ones. dwq, dwk are float32 (None without weights).
+    """
+    import torch
+    B, Hq, N, d = _dims(dq)
+    if out is None:
+        out = (torch.empty_like(dq), torch.empty_like(dk), None if dv is None else torch.empty_like(dv))
+    dwq = dwk = None
+    if wq is not None:
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dq.device) for _ in range(2))
+        if workspace is None:
+            workspace = torch.empty(max(1, fa_norm_rope_bwd_workspace_size(B, Hq, int(dk.shape[1]), N, d)),
+                                    dtype=torch.uint8, device=dq.device)
+    fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, *out, dwq, dwk, workspace, interleaved, eps,
+                     stream)
+    return (*out, dwq, dwk)
 
 
 def flops(B: int, H: int, N: int, d: int, causal: bool, mode: str = "fwd") -> float:

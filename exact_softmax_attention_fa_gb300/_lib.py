@@ -24,6 +24,7 @@ STATUS_NAMES = {
     5: "FA_ERR_LAUNCH",
     6: "FA_ERR_TIMEOUT",
     7: "FA_ERR_CUDA",
+    8: "FA_ERR_INDEX",
 }
 
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -61,6 +62,12 @@ _SIGNATURES = {
                              ctypes.c_size_t, _vp]),
     "fa_fwd_bwd_host": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                  _c_int, _c_float, _vp, ctypes.c_size_t, _vp]),
+    "fa_norm_rope_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int,
+                                  _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _vp]),
+    "fa_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "fa_norm_rope_bwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
+                                  _vp, ctypes.c_size_t, _vp]),
     "fa_status_string": (ctypes.c_char_p, [_c_int]),
     "fa_get_device_status": (_c_int, [_vp]),
     "fa_get_device_status_detail": (_c_int, [_vp, _vp]),

@@ -120,8 +120,6 @@ DeviceState* device_state(fa_status_t* err) {
   return &s;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // [BH][N][d] bf16, boxes of 128 rows x 64 columns, 128-byte swizzle; rows
 // past N read as zero and are not written by stores.
 bool make_map(CUtensorMap* m, const void* base, int BH, int N, int d, unsigned box_rows = 128,
@@ -262,6 +260,8 @@ int choose_kv_chunks(long long BHkv, int g, int N, int d, int causal, int sms, s
   return best;
 }
 
+}  // namespace
+
 fa_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return FA_OK;
   if (e == cudaErrorLaunchFailure || e == cudaErrorInvalidConfiguration || e == cudaErrorLaunchOutOfResources ||
@@ -270,7 +270,14 @@ fa_status_t from_cuda(cudaError_t e) {
   return FA_ERR_CUDA;
 }
 
-}  // namespace
+fa_status_t device_info(DeviceInfo* out) {
+  fa_status_t st = FA_OK;
+  const DeviceState* ds = device_state(&st);
+  if (!ds) return st;
+  *out = DeviceInfo{ds->num_sms, ds->status, g_wait_limit_ns.load()};
+  return FA_OK;
+}
+
 }  // namespace fa
 
 using namespace fa;
@@ -289,6 +296,7 @@ const char* fa_status_string(fa_status_t s) {
     case FA_ERR_LAUNCH: return "FA_ERR_LAUNCH: kernel launch failed";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a device-side pipeline wait exceeded its limit";
     case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA runtime error";
+    case FA_ERR_INDEX: return "FA_ERR_INDEX: a position, length or page index on the device was out of range";
   }
   return "unknown fa_status_t";
 }

@@ -21,6 +21,8 @@ enum : uint32_t {
   WHERE_BWD_MMA = 12,
   WHERE_BWD_SOFTMAX = 13,
   WHERE_BWD_DQ = 14,
+  WHERE_NORM_ROPE = 21,
+  WHERE_NORM_ROPE_BWD = 22,
   WHERE_PROBE = 99,
 };
 
@@ -80,6 +82,15 @@ struct BwdLaunch {
 // set when the problem has no rows (fa_api.cu).
 fa_status_t check_common(int B, int H, int N, int d, int causal, float scale, bool* empty);
 
+// The current device as the operators outside fa_api.cu need it.
+struct DeviceInfo {
+  int num_sms;
+  uint32_t* status;  // device address of the status word
+  uint64_t wait_limit_ns;
+};
+fa_status_t device_info(DeviceInfo* out);
+fa_status_t from_cuda(cudaError_t e);
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Launchers (defined in the kernel translation units). Return cudaSuccess or
 // the launch error.

@@ -20,6 +20,15 @@ __device__ __forceinline__ void record_timeout(uint32_t* status, int* abort_flag
   *reinterpret_cast<volatile int*>(abort_flag) = 1;
 }
 
+// Record the first out-of-range index of the launch in the status word.
+__device__ __forceinline__ void record_bad_index(uint32_t* status, uint32_t where) {
+  if (atomicCAS(status, 0u, static_cast<uint32_t>(FA_ERR_INDEX)) == 0u) {
+    status[1] = where;
+    status[2] = blockIdx.x;
+    status[3] = threadIdx.x;
+  }
+}
+
 // Waits after an abort for work this CTA has already issued (TMA copies, MMAs
 // committed to a barrier). Such work always completes, so these waits do not
 // use the caller's wait limit, which may be a few milliseconds; they are still

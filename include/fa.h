@@ -57,7 +57,8 @@ typedef enum {
   FA_ERR_WORKSPACE = 4,   /* backward workspace missing or too small */
   FA_ERR_LAUNCH = 5,      /* a kernel launch failed */
   FA_ERR_TIMEOUT = 6,     /* a device-side pipeline wait gave up (see fa_get_device_status) */
-  FA_ERR_CUDA = 7         /* another CUDA runtime error */
+  FA_ERR_CUDA = 7,        /* another CUDA runtime error */
+  FA_ERR_INDEX = 8        /* a device-side position, length or page index was out of range (see fa_get_device_status) */
 } fa_status_t;
 
 /*
@@ -334,13 +335,75 @@ size_t fa_fwd_host_device_bytes(int B, int H, int N, int d); /* 0 for invalid or
 fa_status_t fa_fwd_host(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N, int d,
                         int causal, float scale, void* device_buffer, size_t device_bytes, cudaStream_t stream);
 
+/*
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass, from the layout a projection leaves to the attention's
+ * [B][H][N][d]. For a row x of d values (one token of one q or k head):
+ *   r = 1 / sqrt(mean(x^2) + eps),  z = x r w       (w per column, shared by
+ *   the heads; without weights z = x and no statistic is formed)
+ *   and for each rotated pair (a, b), i < rot / 2, with c = cos_t[pos][i],
+ *   s = sin_t[pos][i]:
+ *   y_a = z_a c - z_b s,   y_b = z_b c + z_a s;   columns >= rot: y = z.
+ * Everything is fp32, rounded once to bf16. v rows only change layout.
+ *   q_in, k_in, v_in : in, bf16; head h of token n of batch b starts at
+ *            base + b*strides[3t] + h*strides[3t+1] + n*strides[3t+2] elements
+ *            (t = 0 q, 1 k, 2 v), its d values contiguous. Strides are
+ *            non-negative multiples of 8; a dimension of size 1 may have any.
+ *            v_in and v may both be null (no values).
+ *   strides : HOST array of 9
+ *   wq, wk  : fp32 [d] (w_bf16 = 0) or bf16 [d] (w_bf16 = 1), 16-byte aligned,
+ *            or both null (no norm; eps is then ignored, else it must be
+ *            finite and > 0)
+ *   cos_t, sin_t : fp32 [table_rows][rot / 2], 16-byte aligned; null and
+ *            unused when rot = 0
+ *   positions : int32 [B][N] rows of the tables, or null: token n is at n (the
+ *            call then needs N <= table_rows). A position outside the tables
+ *            is recorded as FA_ERR_INDEX in the device status word and the
+ *            token's q and k rows are left unwritten.
+ *   rot     : rotated columns, a multiple of 16 from 0 to d
+ *   interleaved : 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)
+ *   q, k, v : out, bf16 [B][Hq][N][d], [B][Hkv][N][d]; they may not overlap
+ *            the inputs.
+ * Hkv need not divide Hq here; Hkv = 0 (queries alone) is allowed.
+ * B*N*(Hq + 2 Hkv) must be below 2^31.
+ */
+fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_in, const long long* strides,
+                             const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
+                             int table_rows, const int* positions, void* q, void* k, void* v, int B, int Hq, int Hkv,
+                             int N, int d, int rot, int interleaved, float eps, cudaStream_t stream);
+
+/*
+ * Gradients of fa_norm_rope_fwd. With g = (rotation)^T dy:
+ *   dw = sum over the rows of g x r,   h = g w,
+ *   dx = r (h - x r^2 mean(h x))                   (without weights dx = g)
+ *   dq, dk, dv     : in, bf16 [B][Hq][N][d], [B][Hkv][N][d], as fa_bwd writes
+ *   q_in, k_in     : in, as in the forward (may be null without weights)
+ *   dq_in, dk_in, dv_in : out, bf16, laid out by out_strides as q_in by
+ *            strides. The rows may not overlap (FA_ERR_INVALID_ARG where the
+ *            strides alone show it), nor the inputs.
+ *   dwq, dwk       : out, fp32 [d] (null without weights), overwritten
+ *   workspace      : fa_norm_rope_bwd_workspace_size() bytes, 256-byte
+ *            aligned, with weights (else it may be null)
+ * dw is summed in a fixed order: every output is bitwise reproducible on one
+ * kind of device. A token whose position is outside the tables adds nothing
+ * to dw, and its dq_in and dk_in rows are left unwritten.
+ */
+size_t fa_norm_rope_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d);
+fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
+                             const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
+                             const float* sin_t, int table_rows, const int* positions, void* dq_in, void* dk_in,
+                             void* dv_in, const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv,
+                             int N, int d, int rot, int interleaved, float eps, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* fa_status_string(fa_status_t status);
 
 /*
  * Synchronise `stream`, then read and clear the current device's status word.
  * Returns FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait gave up since the
- * last call, or FA_ERR_CUDA if the synchronisation failed.
+ * last call, FA_ERR_INDEX if a kernel met an index out of range (the first of
+ * the two is kept), or FA_ERR_CUDA if the synchronisation failed.
  */
 fa_status_t fa_get_device_status(cudaStream_t stream);
 
@@ -349,9 +412,10 @@ fa_status_t fa_get_device_status(cudaStream_t stream);
  * word[4] (host memory, owned by the caller): word[0] the status code,
  * word[1] the role of the thread whose wait gave up first (1-3: forward
  * load / MMA / softmax; 11-14: backward load / MMA / softmax / dQ drain;
- * 99: the self-test probe), word[2] its block index, word[3] its thread
- * index; all zero when no wait gave up. Returns FA_ERR_INVALID_ARG for a
- * null word.
+ * 99: the self-test probe) or that met the first bad index (21: norm and
+ * rotation; 22: its backward), word[2] its block index, word[3] its
+ * thread index; all zero when nothing was recorded. Returns
+ * FA_ERR_INVALID_ARG for a null word.
  */
 fa_status_t fa_get_device_status_detail(unsigned int* word, cudaStream_t stream);
 

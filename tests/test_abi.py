@@ -276,3 +276,58 @@ def test_debug_skip_hook_checks(lib):
     for good in (1, 2, 3, 11, 12, 13, 14):
         assert lib.fa_debug_skip_arrival(good) == OK
     assert lib.fa_debug_skip_arrival(0) == OK
+
+
+# ---------------------------------------------------------------------------
+# Per-head norm with position rotation: refusals before any CUDA call.
+# ---------------------------------------------------------------------------
+def strides9(*v):
+    return (ctypes.c_longlong * 9)(*(v or (6 * 64 * 8, 64, 6 * 64) * 3))
+
+
+def norm_rope(lib, ptr=P, v_in=P, v=P, st=None, wq=P, wk=P, w_bf16=0, cos=P, rows=100, pos=P, B=2, Hq=4, Hkv=1, N=8,
+              d=64, rot=64, inter=0, eps=1e-6):
+    return lib.fa_norm_rope_fwd(ptr, ptr, v_in, strides9() if st is None else st, wq, wk, w_bf16, cos, cos, rows, pos,
+                                ptr, ptr, v, B, Hq, Hkv, N, d, rot, inter, eps, None)
+
+
+def norm_rope_bwd(lib, ptr=P, x=P, st=None, out=None, w=P, dw=P, ws=P, ws_bytes=1 << 30, B=2, Hq=4, Hkv=1, N=8, d=64):
+    return lib.fa_norm_rope_bwd(ptr, ptr, ptr, x, x, strides9() if st is None else st, w, w, 0, P, P, 100, None, ptr,
+                                ptr, ptr, strides9() if out is None else out, dw, dw, B, Hq, Hkv, N, d, 64, 0, 1e-6, ws,
+                                ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(Hq=-1), dict(Hkv=-1), dict(N=-1), dict(rows=-1), dict(rot=-16),
+                                dict(rot=8), dict(rot=80), dict(inter=2), dict(w_bf16=2), dict(wq=0), dict(wk=0),
+                                dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(cos=0),
+                                dict(rows=0), dict(pos=0, rows=7), dict(ptr=0), dict(v_in=0), dict(v=0),
+                                dict(st=strides9(-8, 64, 512, 0, 0, 0, 0, 0, 0)), dict(B=1 << 20, N=1 << 10)])
+def test_norm_rope_invalid_arguments(lib, kw):
+    assert norm_rope(lib, **kw) == INVALID
+
+
+def test_norm_rope_alignment_and_sizes(lib):
+    for kw in (dict(ptr=P + 8), dict(v=P + 2), dict(cos=P + 4), dict(wq=P + 8), dict(pos=P + 2),
+               dict(st=strides9(6 * 64 * 8, 64, 6 * 64 + 4, 0, 0, 0, 0, 0, 0))):
+        assert norm_rope(lib, **kw) == MISALIGNED
+    for d in (32, 96, 512):
+        assert norm_rope(lib, d=d, rot=0) == UNSUPPORTED
+    assert norm_rope(lib, N=0, ptr=0) == OK and norm_rope(lib, B=0, ptr=0, st=strides9()) == OK
+    assert norm_rope(lib, Hq=0, Hkv=0) == OK
+
+
+def test_norm_rope_backward_checks(lib):
+    assert norm_rope_bwd(lib, ptr=0) == INVALID
+    assert norm_rope_bwd(lib, x=0) == INVALID
+    assert norm_rope_bwd(lib, dw=0) == INVALID
+    assert norm_rope_bwd(lib, dw=P + 2) == MISALIGNED
+    assert norm_rope_bwd(lib, ws=0) == WORKSPACE
+    size = lib.fa_norm_rope_bwd_workspace_size(2, 4, 1, 8, 64)
+    assert size > 0 and norm_rope_bwd(lib, ws_bytes=size - 1) == WORKSPACE
+    assert norm_rope_bwd(lib, ws=P + 128) == MISALIGNED
+    # rows that overlap: a broadcast head, heads closer than d, tokens inside a head's rows
+    good = (6 * 64 * 8, 64, 6 * 64)
+    for bad in ((6 * 64 * 8, 0, 6 * 64), (6 * 64 * 8, 32, 6 * 64), (6 * 64 * 8, 64, 3 * 64), (0, 64, 6 * 64)):
+        assert norm_rope_bwd(lib, out=strides9(*bad, *good, *good)) == INVALID
+    assert lib.fa_norm_rope_bwd_workspace_size(2, 4, 1, 8, 96) == 0
+    assert lib.fa_norm_rope_bwd_workspace_size(0, 4, 1, 8, 64) == 0
