@@ -17,7 +17,7 @@ from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: 
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_bwd_deterministic", "fa_bwd_gqa_deterministic", "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_bwd_preprocess", "fa_bwd_preprocess_stats", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_bwd_host", "fa_fwd_bwd_host_device_bytes", "fa_fwd_host", "fa_fwd_host_device_bytes", "fa_get_device_status", "fa_get_device_status_detail", "fa_set_wait_limit_ns",
            "fa_debug_timeout_probe", "fa_debug_skip_arrival", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
-           "fa_norm_rope_bwd_workspace_size", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
+           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_gather", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
 
 _SUPPORTED_D = (64, 128, 256)
 
@@ -475,6 +475,61 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
         _ptr(dq), _ptr(dk), _ptr(dv), _ptr(q_in), _ptr(k_in), in_strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos),
         _ptr(sin), rows, _ptr(positions), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), strides, _ptr(dwq), _ptr(dwk), B, Hq,
         ks[1], N, d, rot, int(bool(interleaved)), float(eps), *_ws(workspace), _stream_handle(stream)))
+
+
+def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts):
+    """Checks of a paged 8-bit cache; returns (B, Hkv, d, page, num_pages, max_pages)."""
+    import torch
+    if k_cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_cache must be [num_pages, Hkv, page, d] and page_table [B, max_pages]")
+    pages, Hkv, page, d = k_cache.shape
+    B, max_pages = page_table.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
+        if t.shape != k_cache.shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of k_cache's shape")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (pages, Hkv) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(pages, Hkv)}")
+    for name, t, shape in (("page_table", page_table, (B, max_pages)), ("lens", lens, (B,)), ("counts", counts, (B,))):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    _check_on_current_device((("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+                              ("page_table", page_table), ("lens", lens), ("counts", counts)))
+    return B, Hkv, d, page, pages, max_pages
+
+
+def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, counts=None, stream=None) -> None:
+    """fa_kv8_append of the C ABI: quantise k, v [B, Hkv, n, d] (bf16, contiguous) into the pages of
+    the last counts[b] (None: n) of lens[b] tokens of each sequence.
+
+    k_cache, v_cache: uint8 or float8_e4m3fn [num_pages, Hkv, page, d]; k_scale,
+    v_scale float32 [num_pages, Hkv]; page_table int32 [B, max_pages]; lens,
+    counts int32 [B].
+    """
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
+    n = _dims(k)[2]
+    for name, t in (("k", k), ("v", v)):
+        _check_bf16(name, t, (B, Hkv, n, d))
+    _check_on_current_device((("k", k), ("v", v)))
+    check("fa_kv8_append", load().fa_kv8_append(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), lens.data_ptr(), _ptr(counts), B, Hkv, n, d, page, pages, max_pages,
+        _stream_handle(stream)))
+
+
+def fa_kv8_gather(k_cache, v_cache, k_scale, v_scale, page_table, lens, k, v, stream=None) -> None:
+    """fa_kv8_gather of the C ABI: rows [0, min(lens[b], n)) of each sequence back as bf16 into
+    k, v [B, Hkv, n, d]; later rows are left as they were."""
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, None)
+    n = _dims(k)[2]
+    for name, t in (("k", k), ("v", v)):
+        _check_bf16(name, t, (B, Hkv, n, d))
+    _check_on_current_device((("k", k), ("v", v)))
+    check("fa_kv8_gather", load().fa_kv8_gather(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+        lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, n, d, page, pages, max_pages, _stream_handle(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:

@@ -23,6 +23,9 @@ enum : uint32_t {
   WHERE_BWD_DQ = 14,
   WHERE_NORM_ROPE = 21,
   WHERE_NORM_ROPE_BWD = 22,
+  WHERE_KV8_APPEND = 31,
+  WHERE_KV8_GATHER = 32,
+  WHERE_FWD_KV8 = 33,
   WHERE_PROBE = 99,
 };
 

@@ -396,6 +396,52 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
                              int N, int d, int rot, int interleaved, float eps, void* workspace,
                              size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * A paged key/value cache in 8 bits, for serving: e4m3 codes with one scale
+ * for each page (block of `page` tokens) and head.
+ *   k_cache, v_cache : uint8 [num_pages][Hkv][page][d], e4m3 codes, 16-byte
+ *            aligned; page is 16, 32, 64 or 128 (else FA_ERR_UNSUPPORTED)
+ *   k_scale, v_scale : fp32 [num_pages][Hkv]; a stored value is code * scale
+ *   page_table : int32 [B][max_pages]; entry p of row b is the page that holds
+ *            tokens p*page .. p*page + page - 1 of sequence b. Entries past
+ *            the sequence's last page are not read.
+ *   lens   : int32 [B], tokens of each sequence, the newest ones among them.
+ *            One call's own tokens (those it appends, or its queries) are the
+ *            last counts[b] of them; counts is int32 [B], or null: all n.
+ *            The same lens and counts thus serve the append and the attention
+ *            of one step.
+ *   max_pages * page stays below 2^31 - 256.
+ * All are device memory; the kernels read lens, counts and the table, so a
+ * captured graph replays with their current values. A length, count or page
+ * out of range is recorded as FA_ERR_INDEX in the device status word.
+ *
+ * fa_kv8_append writes tokens as they are quantised:
+ *   k, v : in, bf16 [B][Hkv][n][d]; rows 0 .. counts[b] - 1 are the tokens
+ *          lens[b] - counts[b] .. lens[b] - 1. Rows past counts[b] are not read.
+ *   A page's scale is the smallest power of two 2^e, -100 <= e <= 120, with
+ *   max |value| <= 448 * 2^e over the finite values written to the page (one
+ *   whose first token a call writes starts anew). A value is stored as the
+ *   e4m3 number nearest to value / scale (ties to even); infinities and NaN
+ *   are stored as NaN. Where a later token raises a page's scale, the codes
+ *   before it are divided by the same power of two (exact unless they become
+ *   subnormal). No value is off by more than 2^-4 of itself or 2^-10 of its
+ *   page's scale per rounding.
+ *   A sequence with counts[b] < 0, > n or > lens[b], or more tokens than
+ *   max_pages pages hold, is skipped whole; so are tokens whose page number is
+ *   outside the pool. Pages that a call writes must belong to one sequence.
+ * fa_kv8_gather reads a cache back:
+ *   k, v : out, bf16 [B][Hkv][n][d]; row j of sequence b, j < min(lens[b], n),
+ *          gets code * scale (exact for the scales fa_kv8_append writes, up to
+ *          the largest bf16 value). Rows past that are left as they were, and
+ *          so are rows whose page number is outside the pool.
+ */
+fa_status_t fa_kv8_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          const int* page_table, const int* lens, const int* counts, int B, int Hkv, int n, int d,
+                          int page, int num_pages, int max_pages, cudaStream_t stream);
+fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                          const int* page_table, const int* lens, void* k, void* v, int B, int Hkv, int n, int d,
+                          int page, int num_pages, int max_pages, cudaStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* fa_status_string(fa_status_t status);
 
@@ -413,7 +459,8 @@ fa_status_t fa_get_device_status(cudaStream_t stream);
  * word[1] the role of the thread whose wait gave up first (1-3: forward
  * load / MMA / softmax; 11-14: backward load / MMA / softmax / dQ drain;
  * 99: the self-test probe) or that met the first bad index (21: norm and
- * rotation; 22: its backward), word[2] its block index, word[3] its
+ * rotation; 22: its backward; 31, 32, 33: the 8-bit cache's append, gather
+ * and attention), word[2] its block index, word[3] its
  * thread index; all zero when nothing was recorded. Returns
  * FA_ERR_INVALID_ARG for a null word.
  */

@@ -331,3 +331,33 @@ def test_norm_rope_backward_checks(lib):
         assert norm_rope_bwd(lib, out=strides9(*bad, *good, *good)) == INVALID
     assert lib.fa_norm_rope_bwd_workspace_size(2, 4, 1, 8, 96) == 0
     assert lib.fa_norm_rope_bwd_workspace_size(0, 4, 1, 8, 64) == 0
+
+
+# ---------------------------------------------------------------------------
+# The paged 8-bit cache: refusals before any CUDA call.
+# ---------------------------------------------------------------------------
+def kv8_append(lib, kv=P, cache=P, scale=P, table=P, lens=P, counts=None, B=2, Hkv=2, n=4, d=64, page=16, pages=8, mp=4):
+    return lib.fa_kv8_append(kv, kv, cache, cache, scale, scale, table, lens, counts, B, Hkv, n, d, page, pages, mp,
+                             None)
+
+
+def kv8_gather(lib, kv=P, cache=P, scale=P, table=P, lens=P, counts=None, B=2, Hkv=2, n=4, d=64, page=16, pages=8, mp=4):
+    return lib.fa_kv8_gather(cache, cache, scale, scale, table, lens, kv, kv, B, Hkv, n, d, page, pages, mp, None)
+
+
+@pytest.mark.parametrize("call", [kv8_append, kv8_gather])
+def test_kv8_refusals(lib, call):
+    for kw in (dict(B=-1), dict(Hkv=-1), dict(n=-1), dict(pages=-1), dict(mp=-1), dict(pages=0), dict(mp=0), dict(kv=0),
+               dict(cache=0), dict(scale=0), dict(table=0), dict(lens=0), dict(Hkv=65536), dict(mp=1 << 27),
+               dict(n=(1 << 31) - 1), dict(B=1 << 20, n=1 << 16)):
+        assert call(lib, **kw) == INVALID, kw
+    for kw in (dict(d=96), dict(d=512), dict(page=8), dict(page=48), dict(page=256), dict(page=0)):
+        assert call(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(kv=P + 8), dict(cache=P + 8), dict(scale=P + 2), dict(table=P + 1), dict(lens=P + 2)):
+        assert call(lib, **kw) == MISALIGNED, kw
+    for kw in (dict(B=0), dict(Hkv=0), dict(n=0)):
+        assert call(lib, kv=0, cache=0, scale=0, table=0, lens=0, pages=0, mp=0, **kw) == OK, kw
+
+
+def test_kv8_append_checks_counts(lib):
+    assert kv8_append(lib, counts=P + 2) == MISALIGNED
