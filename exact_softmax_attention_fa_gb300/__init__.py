@@ -17,7 +17,8 @@ from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: 
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_bwd_deterministic", "fa_bwd_gqa_deterministic", "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_bwd_preprocess", "fa_bwd_preprocess_stats", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_bwd_host", "fa_fwd_bwd_host_device_bytes", "fa_fwd_host", "fa_fwd_host_device_bytes", "fa_get_device_status", "fa_get_device_status_detail", "fa_set_wait_limit_ns",
            "fa_debug_timeout_probe", "fa_debug_skip_arrival", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
-           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_gather", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
+           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_gather",
+           "fa_fwd_kv8", "fa_fwd_kv8_workspace_size", "KV8Cache", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
 
 _SUPPORTED_D = (64, 128, 256)
 
@@ -532,6 +533,32 @@ def fa_kv8_gather(k_cache, v_cache, k_scale, v_scale, page_table, lens, k, v, st
         lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, n, d, page, pages, max_pages, _stream_handle(stream)))
 
 
+def fa_fwd_kv8_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
+    return int(load().fa_fwd_kv8_workspace_size(B, Hq, Hkv, Nq, d))
+
+
+def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, causal: bool, scale: float,
+               counts=None, workspace=None, stream=None) -> None:
+    """fa_fwd_kv8 of the C ABI: attention of q [B, Hq, Nq, d] over the paged 8-bit cache into o (like
+    q) and lse float32 [B, Hq, Nq]; query i < counts[b] (None: Nq) stands at
+    position lens[b] - counts[b] + i of its sequence.
+
+    workspace is a CUDA uint8 tensor of at least fa_fwd_kv8_workspace_size() bytes.
+    """
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
+    Hq, Nq = _dims(q)[1:3]
+    if Hkv < 1 or Hq % Hkv != 0:
+        raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
+    for name, t in (("q", q), ("o", o)):
+        _check_bf16(name, t, (B, Hq, Nq, d))
+    _check_lse(lse, (B, Hq, Nq, d))
+    _check_on_current_device((("q", q), ("o", o), ("lse", lse), ("workspace", workspace)))
+    check("fa_fwd_kv8", load().fa_fwd_kv8(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), lens.data_ptr(), _ptr(counts), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page,
+        pages, max_pages, int(bool(causal)), float(scale), *_ws(workspace), _stream_handle(stream)))
+
+
 def fa_get_device_status(stream=None) -> int:
     """Synchronise the stream; return and clear the device status (0 = FA_OK)."""
     return int(load().fa_get_device_status(_stream_handle(stream)))
@@ -632,6 +659,78 @@ def norm_rope_backward(dq, dk, dv, q_in, k_in, wq=None, wk=None, cos=None, sin=N
     fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, *out, dwq, dwk, workspace, interleaved, eps,
                      stream)
     return (*out, dwq, dwk)
+
+
+def _on_stream(stream):
+    """torch's context for a stream given as None, a torch stream or a raw handle."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+class KV8Cache:
+    """A paged 8-bit key/value cache of B sequences and the calls that use it.
+
+    Holds the pools, scales, page table (each sequence's pages one after another
+    unless `page_table` and `num_pages` are given) and lengths, all on the device:
+    a decoding step (`append`, `attend`) can be captured into a CUDA graph.
+    """
+
+    def __init__(self, B: int, Hkv: int, d: int, max_tokens: int, page: int = 64, page_table=None, num_pages=None,
+                 device="cuda"):
+        import torch
+        max_pages = -(-max_tokens // page)
+        if page_table is None:
+            num_pages = B * max_pages
+            page_table = torch.arange(num_pages, dtype=torch.int32, device=device).view(B, max_pages)
+        elif num_pages is None:
+            raise ValueError("num_pages is needed with a page_table of your own")
+        self.page_table = page_table
+        self.k_cache, self.v_cache = (torch.empty(num_pages, Hkv, page, d, dtype=torch.uint8, device=device)
+                                      for _ in range(2))
+        self.k_scale, self.v_scale = (torch.ones(num_pages, Hkv, dtype=torch.float32, device=device) for _ in range(2))
+        self.lens = torch.zeros(B, dtype=torch.int32, device=device)
+        self._workspaces = {}
+
+    def _cache(self):
+        return self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.page_table, self.lens
+
+    def append(self, k, v, counts=None, stream=None) -> None:
+        """Lengthen each sequence by counts[b] (None: n) tokens and write k, v [B, Hkv, n, d] there."""
+        with _on_stream(stream):
+            self.lens.add_(int(k.shape[2]) if counts is None else counts)
+        fa_kv8_append(k, v, *self._cache(), counts, stream)
+
+    def gather(self, n: int, stream=None):
+        """The first n tokens' k, v as bf16 [B, Hkv, n, d], zero past a sequence's length."""
+        import torch
+        pages, Hkv, page, d = self.k_cache.shape
+        with _on_stream(stream):
+            k, v = (torch.zeros(self.lens.shape[0], Hkv, n, d, dtype=torch.bfloat16, device=self.lens.device)
+                    for _ in range(2))
+        fa_kv8_gather(*self._cache(), k, v, stream)
+        return k, v
+
+    def attend(self, q, causal: bool = True, scale: float | None = None, counts=None, stream=None):
+        """O, L of q [B, Hq, Nq, d], whose last rows are the cache's newest tokens (fa_fwd_kv8); rows
+        past counts[b] are zero. One workspace per shape and stream is kept; a
+        captured call has one of its own, in its graph's memory."""
+        import torch
+        B, Hq, Nq, d = _dims(q)
+        handle = _stream_handle(stream)
+        key = (Hq, Nq, handle)
+        with _on_stream(stream):
+            o = torch.empty_like(q) if counts is None else torch.zeros_like(q)
+            lse = torch.zeros((B, Hq, Nq), dtype=torch.float32, device=q.device)
+            workspace = self._workspaces.get(key)
+            capturing = torch.cuda.is_current_stream_capturing()
+            if workspace is None or capturing:
+                size = fa_fwd_kv8_workspace_size(B, Hq, int(self.k_cache.shape[1]), Nq, d)
+                workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
+                if not capturing:
+                    self._workspaces[key] = workspace
+        fa_fwd_kv8(q, *self._cache(), o, lse, causal, default_scale(d) if scale is None else scale, counts, workspace,
+                   handle)
+        return o, lse
 
 
 def flops(B: int, H: int, N: int, d: int, causal: bool, mode: str = "fwd") -> float:

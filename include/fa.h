@@ -442,6 +442,35 @@ fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float*
                           const int* page_table, const int* lens, void* k, void* v, int B, int Hkv, int n, int d,
                           int page, int num_pages, int max_pages, cudaStream_t stream);
 
+/*
+ * Attention over a paged 8-bit cache (see fa_kv8_append for its arguments):
+ * the forward pass of fa_fwd_splitkv with K = code * k_scale, V = code * v_scale,
+ * each sequence at its own length.
+ *   q, o : bf16 [B][Hq][Nq][d];  lse : fp32 [B][Hq][Nq], natural log
+ *   Hq   : a multiple of Hkv; query head h reads K/V head floor(h / (Hq / Hkv))
+ *   Query i < counts[b] (all Nq without counts) of sequence b stands at
+ *   position lens[b] - counts[b] + i. With causal = 1 it sees keys
+ *   j <= its position, else all lens[b]. A query that sees no key (lens[b] = 0,
+ *   or a position below 0) gets O = 0, L = -infinity. Rows past counts[b] are
+ *   neither read nor written. What a page holds behind lens[b] is never
+ *   used. A NaN code reaches every query that sees its token; one stored in V
+ *   may also reach the queries of this call that stand before it.
+ *   scales : positive, at most 2^126 (fa_kv8_append's are powers of two up to 2^120)
+ *   scale  : finite and > 0
+ *   workspace : fa_fwd_kv8_workspace_size() bytes, 256-byte aligned; the
+ *            parts of rows whose keys several SMs share. Calls that may run at
+ *            the same time need workspaces of their own.
+ * A length or count out of range is recorded as FA_ERR_INDEX and its sequence's
+ * rows are left unwritten; tokens on a page outside the pool are recorded and
+ * not seen. Results do not depend on timing: the same inputs on the same kind
+ * of device give the same bits.
+ */
+size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
+                       float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages, int max_pages,
+                       int causal, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* fa_status_string(fa_status_t status);
 

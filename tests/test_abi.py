@@ -361,3 +361,36 @@ def test_kv8_refusals(lib, call):
 
 def test_kv8_append_checks_counts(lib):
     assert kv8_append(lib, counts=P + 2) == MISALIGNED
+
+
+def fwd_kv8(lib, q=P, cache=P, scale_t=P, table=P, lens=P, counts=None, o=P, lse=P, B=2, Hq=4, Hkv=2, Nq=1, d=64, page=16,
+            pages=8, mp=4, causal=1, scale=0.125, ws=P, ws_bytes=1 << 30):
+    return lib.fa_fwd_kv8(q, cache, cache, scale_t, scale_t, table, lens, counts, o, lse, B, Hq, Hkv, Nq, d, page, pages,
+                          mp, causal, scale, ws, ws_bytes, None)
+
+
+def test_fwd_kv8_refusals(lib):
+    for kw in (dict(B=-1), dict(Hq=-4), dict(Hkv=-1), dict(Hkv=0), dict(Hkv=3), dict(Nq=-1), dict(pages=0), dict(mp=0),
+               dict(q=0), dict(cache=0), dict(scale_t=0), dict(table=0), dict(lens=0), dict(o=0), dict(lse=0),
+               dict(causal=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(mp=1 << 27), dict(B=1 << 15, Hq=1 << 10, Nq=1 << 8), dict(pages=1 << 30)):
+        assert fwd_kv8(lib, **kw) == INVALID, kw
+    for kw in (dict(d=96), dict(page=8), dict(page=256)):
+        assert fwd_kv8(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(q=P + 8), dict(cache=P + 8), dict(scale_t=P + 2), dict(table=P + 2), dict(counts=P + 1), dict(o=P + 2),
+               dict(lse=P + 2), dict(ws=P + 128)):
+        assert fwd_kv8(lib, **kw) == MISALIGNED, kw
+    size = lib.fa_fwd_kv8_workspace_size(2, 4, 2, 1, 64)
+    assert size > 0
+    for kw in (dict(ws=0), dict(ws_bytes=size - 1)):
+        assert fwd_kv8(lib, **kw) == WORKSPACE, kw
+    for kw in (dict(B=0), dict(Hq=0), dict(Hq=0, Hkv=0), dict(Nq=0)):
+        assert fwd_kv8(lib, q=0, cache=0, scale_t=0, table=0, lens=0, o=0, lse=0, ws=0, ws_bytes=0, **kw) == OK, kw
+
+
+def test_fwd_kv8_workspace_size(lib):
+    size = lib.fa_fwd_kv8_workspace_size
+    assert size(2, 4, 3, 1, 64) == 0 and size(0, 4, 2, 1, 64) == 0 and size(2, 4, 2, 0, 64) == 0
+    assert size(2, 4, 2, 1, 96) == 0
+    # it does not grow with the batch: parts belong to warps
+    assert size(1, 4, 2, 1, 128) == size(500, 4, 2, 1, 128) > 0
