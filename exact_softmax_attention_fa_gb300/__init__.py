@@ -11,6 +11,7 @@ memory and streams.
 
 from __future__ import annotations
 
+import ctypes
 import math
 
 from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: F401
@@ -25,8 +26,8 @@ _SUPPORTED_D = (64, 128, 256)
 
 def _stream_handle(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building torch's stream object takes longer than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -354,59 +355,67 @@ def rope_tables(rows: int, rot: int, base: float = 10000.0, device="cuda"):
     return angle.cos().float(), angle.sin().float()
 
 
-def _check_on_current_device(named):
+def _check_on_current_device(names: str, *tensors) -> None:
     """Every tensor given is on the current CUDA device (the library launches there)."""
     import torch
     here = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and (not t.is_cuda or t.device.index != here):
-            raise ValueError(f"{name} must be on the current CUDA device (cuda:{here}), got {t.device}")
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{names.split()[i]} must be on the current CUDA device (cuda:{here}), got {t.device}")
+
+
+def _check_tensor(name, t, dtype, shape) -> None:
+    """A contiguous tensor of this type and shape (None passes; where it is, is checked for all at once)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_Strides = ctypes.c_longlong * 9
 
 
 def _head_strides(name, t, shape):
     """(batch, head, token) strides of a bf16 [B, H, N, d] tensor with contiguous rows."""
     import torch
+    if t is None:
+        return 0, 0, 0
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.stride(3) != 1:
+    b, h, n, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.stride()[:3]
+    return b, h, n
 
 
-def _norm_rope_args(shapes, strided, wq, wk, cos, sin, positions):
-    """Checks shared by the two directions; returns the host array of strides,
-    the weights' type flag, the tables' rows and rot."""
-    import ctypes
+def _norm_rope_args(B, N, d, wq, wk, cos, sin, positions):
+    """Checks shared by the two directions; returns the weights' type flag, the tables' rows and rot."""
     import torch
-    B, _, N, d = shapes[0]
-    strides = (ctypes.c_longlong * 9)()
-    for t, (name, x) in enumerate(strided):
-        if x is not None:
-            strides[3 * t:3 * t + 3] = _head_strides(name, x, shapes[t])
     if (wq is None) != (wk is None):
         raise ValueError("wq and wk are given together or not at all")
+    w_bf16 = 0
     if wq is not None:
-        for name, w in (("wq", wq), ("wk", wk)):
-            if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != wq.dtype:
-                raise TypeError(f"{name} must be float32 or bfloat16 (both weights the same), got {w.dtype}")
-            if tuple(w.shape) != (d,) or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous tensor of shape ({d},)")
+        w_bf16 = int(wq.dtype == torch.bfloat16)
+        _check_tensor("wq", wq, torch.bfloat16 if w_bf16 else torch.float32, (d,))
+        _check_tensor("wk", wk, wq.dtype, (d,))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin are given together or not at all")
     rows = rot = 0
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must be [rows, rot / 2] tensors of one shape")
-        for name, x in (("cos", cos), ("sin", sin)):
-            if x.dtype != torch.float32 or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor")
-        rows, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
-    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N)
-                                  or not positions.is_contiguous()):
-        raise ValueError(f"positions must be a contiguous int32 tensor of shape {(B, N)}")
-    return strides, int(wq is not None and wq.dtype == torch.bfloat16), rows, rot
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [rows, rot / 2] tensors")
+        rows, rot = cos.shape
+        rot *= 2
+        _check_tensor("cos", cos, torch.float32, cos.shape)
+        _check_tensor("sin", sin, torch.float32, cos.shape)
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape != (B, N) or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of shape {(B, N)}")
+    return w_bf16, rows, rot
 
 
 def _ptr(t):
@@ -421,20 +430,25 @@ def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, int
     wq, wk None: no norm. cos, sin (rope_tables) None: no rotation. v_in, v
     None: no values. positions None: token n is at position n.
     """
-    B, Hq, N, d = _dims(q_in)
-    qs, ks = (B, Hq, N, d), (B, int(k_in.shape[1]), N, d)
+    import torch
+    if q_in.dim() != 4 or k_in.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hq, N, d = q_in.shape
+    Hkv = k_in.shape[1]
+    qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
     if (v_in is None) != (v is None):
         raise ValueError("v_in and v are given together or not at all")
-    strides, w_bf16, rows, rot = _norm_rope_args((qs, ks, ks), (("q_in", q_in), ("k_in", k_in), ("v_in", v_in)), wq, wk,
-                                                 cos, sin, positions)
-    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks)):
-        if t is not None:
-            _check_bf16(name, t, shape)
-    _check_on_current_device((("q_in", q_in), ("k_in", k_in), ("v_in", v_in), ("wq", wq), ("wk", wk), ("cos", cos),
-                              ("sin", sin), ("positions", positions), ("q", q), ("k", k), ("v", v)))
+    w_bf16, rows, rot = _norm_rope_args(B, N, d, wq, wk, cos, sin, positions)
+    strides = _Strides(*_head_strides("q_in", q_in, qs), *_head_strides("k_in", k_in, ks),
+                       *_head_strides("v_in", v_in, ks))
+    _check_tensor("q", q, torch.bfloat16, qs)
+    _check_tensor("k", k, torch.bfloat16, ks)
+    _check_tensor("v", v, torch.bfloat16, ks)
+    _check_on_current_device("q_in k_in v_in wq wk cos sin positions q k v", q_in, k_in, v_in, wq, wk, cos, sin,
+                             positions, q, k, v)
     check("fa_norm_rope_fwd", load().fa_norm_rope_fwd(
-        _ptr(q_in), _ptr(k_in), _ptr(v_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos), _ptr(sin), rows,
-        _ptr(positions), _ptr(q), _ptr(k), _ptr(v), B, Hq, ks[1], N, d, rot, int(bool(interleaved)), float(eps),
+        q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos), _ptr(sin), rows,
+        _ptr(positions), q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d, rot, int(bool(interleaved)), eps,
         _stream_handle(stream)))
 
 
@@ -450,32 +464,31 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
 
     Without weights q_in, k_in, dwq, dwk and workspace are not used.
     """
-    import ctypes
     import torch
-    B, Hq, N, d = _dims(dq)
-    qs, ks = (B, Hq, N, d), (B, int(dk.shape[1]), N, d)
+    if dq.dim() != 4 or dk.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hq, N, d = dq.shape
+    Hkv = dk.shape[1]
+    qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
     if (dv is None) != (dv_in is None):
         raise ValueError("dv and dv_in are given together or not at all")
-    strides, w_bf16, rows, rot = _norm_rope_args((qs, ks, ks), (("dq_in", dq_in), ("dk_in", dk_in), ("dv_in", dv_in)),
-                                                 wq, wk, cos, sin, positions)
-    in_strides = (ctypes.c_longlong * 9)()
+    w_bf16, rows, rot = _norm_rope_args(B, N, d, wq, wk, cos, sin, positions)
+    out_strides = _Strides(*_head_strides("dq_in", dq_in, qs), *_head_strides("dk_in", dk_in, ks),
+                           *_head_strides("dv_in", dv_in, ks))
+    strides = None
     if wq is not None:
-        for t, (name, x, shape) in enumerate((("q_in", q_in, qs), ("k_in", k_in, ks))):
-            in_strides[3 * t:3 * t + 3] = _head_strides(name, x, shape)
-        for name, x in (("dwq", dwq), ("dwk", dwk)):
-            if x.dtype != torch.float32 or tuple(x.shape) != (d,) or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({d},)")
-    for name, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
-        if t is not None:
-            _check_bf16(name, t, shape)
-    _check_on_current_device((("dq", dq), ("dk", dk), ("dv", dv), ("q_in", q_in), ("k_in", k_in), ("wq", wq),
-                              ("wk", wk), ("cos", cos), ("sin", sin), ("positions", positions), ("dq_in", dq_in),
-                              ("dk_in", dk_in), ("dv_in", dv_in), ("dwq", dwq), ("dwk", dwk),
-                              ("workspace", workspace)))
+        strides = _Strides(*_head_strides("q_in", q_in, qs), *_head_strides("k_in", k_in, ks))
+        _check_tensor("dwq", dwq, torch.float32, (d,))
+        _check_tensor("dwk", dwk, torch.float32, (d,))
+    _check_tensor("dq", dq, torch.bfloat16, qs)
+    _check_tensor("dk", dk, torch.bfloat16, ks)
+    _check_tensor("dv", dv, torch.bfloat16, ks)
+    _check_on_current_device("dq dk dv q_in k_in wq wk cos sin positions dq_in dk_in dv_in dwq dwk workspace", dq, dk,
+                             dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk, workspace)
     check("fa_norm_rope_bwd", load().fa_norm_rope_bwd(
-        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(q_in), _ptr(k_in), in_strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos),
-        _ptr(sin), rows, _ptr(positions), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), strides, _ptr(dwq), _ptr(dwk), B, Hq,
-        ks[1], N, d, rot, int(bool(interleaved)), float(eps), *_ws(workspace), _stream_handle(stream)))
+        dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos),
+        _ptr(sin), rows, _ptr(positions), dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in), out_strides, _ptr(dwq),
+        _ptr(dwk), B, Hq, Hkv, N, d, rot, int(bool(interleaved)), eps, *_ws(workspace), _stream_handle(stream)))
 
 
 def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts):
@@ -483,21 +496,18 @@ def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts):
     import torch
     if k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_cache must be [num_pages, Hkv, page, d] and page_table [B, max_pages]")
-    pages, Hkv, page, d = k_cache.shape
+    shape = k_cache.shape
+    pages, Hkv, page, d = shape
     B, max_pages = page_table.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
-            raise TypeError(f"{name} must be uint8 or float8_e4m3fn, got {t.dtype}")
-        if t.shape != k_cache.shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of k_cache's shape")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (pages, Hkv) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(pages, Hkv)}")
-    for name, t, shape in (("page_table", page_table, (B, max_pages)), ("lens", lens, (B,)), ("counts", counts, (B,))):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
-    _check_on_current_device((("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-                              ("page_table", page_table), ("lens", lens), ("counts", counts)))
+    if k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError(f"k_cache must be uint8 or float8_e4m3fn, got {k_cache.dtype}")
+    _check_tensor("k_cache", k_cache, k_cache.dtype, shape)
+    _check_tensor("v_cache", v_cache, k_cache.dtype, shape)
+    _check_tensor("k_scale", k_scale, torch.float32, (pages, Hkv))
+    _check_tensor("v_scale", v_scale, torch.float32, (pages, Hkv))
+    for name, t, want in (("page_table", page_table, (B, max_pages)), ("lens", lens, (B,)), ("counts", counts, (B,))):
+        if t is not None and (t.dtype != torch.int32 or t.shape != want or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {want}")
     return B, Hkv, d, page, pages, max_pages
 
 
@@ -509,11 +519,13 @@ def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
     v_scale float32 [num_pages, Hkv]; page_table int32 [B, max_pages]; lens,
     counts int32 [B].
     """
+    import torch
     B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
-    n = _dims(k)[2]
-    for name, t in (("k", k), ("v", v)):
-        _check_bf16(name, t, (B, Hkv, n, d))
-    _check_on_current_device((("k", k), ("v", v)))
+    n = k.shape[2] if k.dim() == 4 else 0
+    _check_tensor("k", k, torch.bfloat16, (B, Hkv, n, d))
+    _check_tensor("v", v, torch.bfloat16, (B, Hkv, n, d))
+    _check_on_current_device("k v k_cache v_cache k_scale v_scale page_table lens counts", k, v, k_cache, v_cache,
+                             k_scale, v_scale, page_table, lens, counts)
     check("fa_kv8_append", load().fa_kv8_append(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(), _ptr(counts), B, Hkv, n, d, page, pages, max_pages,
@@ -523,11 +535,13 @@ def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
 def fa_kv8_gather(k_cache, v_cache, k_scale, v_scale, page_table, lens, k, v, stream=None) -> None:
     """fa_kv8_gather of the C ABI: rows [0, min(lens[b], n)) of each sequence back as bf16 into
     k, v [B, Hkv, n, d]; later rows are left as they were."""
+    import torch
     B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, None)
-    n = _dims(k)[2]
-    for name, t in (("k", k), ("v", v)):
-        _check_bf16(name, t, (B, Hkv, n, d))
-    _check_on_current_device((("k", k), ("v", v)))
+    n = k.shape[2] if k.dim() == 4 else 0
+    _check_tensor("k", k, torch.bfloat16, (B, Hkv, n, d))
+    _check_tensor("v", v, torch.bfloat16, (B, Hkv, n, d))
+    _check_on_current_device("k_cache v_cache k_scale v_scale page_table lens k v", k_cache, v_cache, k_scale, v_scale,
+                             page_table, lens, k, v)
     check("fa_kv8_gather", load().fa_kv8_gather(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
         lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, n, d, page, pages, max_pages, _stream_handle(stream)))
@@ -545,18 +559,23 @@ def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, 
 
     workspace is a CUDA uint8 tensor of at least fa_fwd_kv8_workspace_size() bytes.
     """
+    import torch
     B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
-    Hq, Nq = _dims(q)[1:3]
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    _, Hq, Nq, _ = q.shape
     if Hkv < 1 or Hq % Hkv != 0:
         raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
-    for name, t in (("q", q), ("o", o)):
-        _check_bf16(name, t, (B, Hq, Nq, d))
-    _check_lse(lse, (B, Hq, Nq, d))
-    _check_on_current_device((("q", q), ("o", o), ("lse", lse), ("workspace", workspace)))
+    _check_tensor("q", q, torch.bfloat16, (B, Hq, Nq, d))
+    _check_tensor("o", o, torch.bfloat16, (B, Hq, Nq, d))
+    if lse.dtype != torch.float32 or lse.shape != (B, Hq, Nq) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor of shape [B, Hq, Nq]")
+    _check_on_current_device("q k_cache v_cache k_scale v_scale page_table lens counts o lse workspace", q, k_cache,
+                             v_cache, k_scale, v_scale, page_table, lens, counts, o, lse, workspace)
     check("fa_fwd_kv8", load().fa_fwd_kv8(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(), _ptr(counts), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page,
-        pages, max_pages, int(bool(causal)), float(scale), *_ws(workspace), _stream_handle(stream)))
+        pages, max_pages, int(bool(causal)), scale, *_ws(workspace), _stream_handle(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:
@@ -567,7 +586,6 @@ def fa_get_device_status(stream=None) -> int:
 def fa_get_device_status_detail(stream=None) -> tuple:
     """Synchronise the stream; return and clear the whole device status word:
     (code, role of the first wait that gave up, its block, its thread)."""
-    import ctypes
     word = (ctypes.c_uint * 4)()
     st = int(load().fa_get_device_status_detail(ctypes.addressof(word), _stream_handle(stream)))
     if st == 7:  # FA_ERR_CUDA: the synchronisation failed, the word was not read

@@ -95,6 +95,8 @@ def header_functions() -> list[str]:
 def load():
     """Load the built library (once) and declare every C signature."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -274,7 +274,7 @@ fa_status_t device_info(DeviceInfo* out) {
   fa_status_t st = FA_OK;
   const DeviceState* ds = device_state(&st);
   if (!ds) return st;
-  *out = DeviceInfo{ds->num_sms, ds->status, g_wait_limit_ns.load()};
+  *out = DeviceInfo{static_cast<int>(ds - g_dev), ds->num_sms, ds->status, g_wait_limit_ns.load()};
   return FA_OK;
 }
 

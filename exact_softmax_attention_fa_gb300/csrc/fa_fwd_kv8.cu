@@ -9,27 +9,31 @@
 // multiplied as they are stored and one reference m = max u_j keeps every P_j
 // in fp16's range however the pages' scales differ.
 //
-// Precision. e4m3 codes are exact in fp16. A query row is moved by a power of
-// two so that its largest |value| lies in [2^14, 2^15): its bf16 values are then
-// exact in fp16 down to 2^-28 of the largest. P_j (0 .. 2^14) is rounded to
-// fp16, 2^-11 relative and never coarser than 2^-30 of the row's largest; l
-// sums the unrounded values. All sums are fp32.
+// Products. The codes are the tensor core's operands as they are stored (e4m3,
+// fp32 sums: measured within 2^-23 of the sum of absolute products); what is
+// multiplied with them is split into e4m3 pieces that occupy columns of their
+// own, since a decoding call leaves most of an MMA's 8 columns empty anyway:
+//   a query value q 2^a (row maximum in [2^7, 2^8)) = qh + 2^-4 ql, exact down to
+//   2^-14 of the row's largest value, and within 2^-22 of it below;
+//   P (at most 448) = ph + 2^-4 pm + 2^-8 pl: 2^-12 relative, and never coarser
+//   than 2^-24 of the row's largest weight. l sums the unrounded weights.
+// (Converting the codes to fp16 for m16n8k16 products was measured first: 519
+// instructions per 16 keys at d = 128, most of them unpacking bytes, and 0.61 of
+// the HBM rate at B = 8, Hkv = 8, 32768 keys.)
 //
 // Bound: HBM, one byte per cached value. Each warp owns a run of consecutive
-// 16-key steps of the flattened list of (sequence, K/V head, row chunk) and
+// 32-key steps of the flattened list of (sequence, K/V head, row chunk) and
 // streams them through a ring of its own in shared memory: every lane copies
 // (cp.async) exactly the 16-byte pieces it will read back, so the ring needs no
-// barrier, has no bank conflicts and keeps (stages - 1) * 32 d bytes per warp
+// barrier, has no bank conflicts and keeps (stages - 1) * 64 d bytes per warp
 // in flight. Runs are of equal length whatever the sequences' lengths are; a
 // row whose keys are shared between warps is joined by kv8_combine_kernel.
 //
-// Products are m16n8k16 with the cache as the 16-row operand and 8 query rows
-// as columns (S^T = K Q^T, O^T = V^T P^T), the shape with the least padding for
-// the 1-16 rows of a K/V head that decoding has; the tensor pipe is a small
-// share of the time at one byte per value. The order of d within the product
-// is free, so a lane's 16 contiguous codes of a key are its fragments as they
-// are; V needs pairs of keys side by side, which one byte permute per word
-// gives on the way to fp16.
+// Products are m16n8k32 with the cache as the 16-row operand and the rows'
+// pieces as columns (S^T = K Q^T, O^T = V^T P^T). The order of d within S is free,
+// so a lane's 16 contiguous codes of a key are its fragments as they are; the
+// order of keys within O is free too, and V needs its 4 x 4 byte blocks turned
+// (two byte permutes a word) to have four keys of a column side by side.
 #include <algorithm>
 #include <cmath>
 
@@ -38,16 +42,15 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStepKeys = 16;
-constexpr int kMinSteps = 4;      // a warp's share is not cut below this
+constexpr int kStepKeys = 32;
+constexpr int kHalfKeys = 16;     // a page ends at a multiple of this
+constexpr int kMinSteps = 2;      // a warp's share is not cut below this
 constexpr int kMaxSms = 152;      // sizes the partials
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kSlack = 8.f;     // growth of a reference (base 2) absorbed without rescaling
-constexpr float kShift = 6.f;     // P <= 2^(kShift + kSlack) = 2^14
+constexpr float kSlack = 2.8f;    // growth of a reference (base 2) absorbed without rescaling
+constexpr float kShift = 6.f;     // P <= 2^(kShift + kSlack) < 448, the largest e4m3 value
 // l is kept times 2^-10: its terms lie between 2^(6 - 120 - 10) and
-// 2^(14 + 100 - 10) for the scales a cache holds, so neither one term nor 2^24
+// 2^(9 + 100 - 10) for the scales a cache holds, so neither one term nor 2^24
 // of them leave fp32's normal range.
 constexpr float kSumBias = 10.f;
 
@@ -59,19 +62,20 @@ struct Kv8Attn {
   float* part;             // [2 * warps][part_rows][d] unnormalised O of a run's part of a row
   float2* part_ml;         // [2 * warps][part_rows] its m and l
   uint32_t* status;
-  int Hq, Nq, g, rows, chunks, part_rows;  // rows = g * Nq per K/V head, in `chunks` of 8 NT
+  int Hq, Nq, g, rows, chunks, part_rows;  // rows = g * Nq per K/V head, in `chunks` of 4 NQ
   int causal;
   float scale_log2;
 };
 
-template <int D, int NT>
+// NQ: 8-column tiles of queries, 4 rows of two pieces each.
+template <int D, int NQ>
 struct Cfg {
-  static constexpr int CTAS = D <= 128 && NT == 1 ? 2 : 1;  // per SM
-  static constexpr int STAGE = 32 * D;                      // 16 keys and values
-  static constexpr int STAGES = (CTAS == 2 ? 12288 : 24576) / STAGE;
-  static constexpr int HEADER = 16;
+  static constexpr int WARPS = 1024 / D;       // one CTA per SM; three stages of every warp fill its shared memory
+  static constexpr int STAGE = 2 * kStepKeys * D;
+  static constexpr int STAGES = 3;
+  static constexpr int HEADER = 32;
   static constexpr int WARP_BYTES = STAGES * (STAGE + HEADER);
-  static constexpr int SMEM = kWarps * WARP_BYTES;
+  static constexpr int SMEM = WARPS * WARP_BYTES;
 };
 
 // Tokens of sequence b, or 0 where the stored length is out of range.
@@ -83,9 +87,8 @@ __device__ __forceinline__ int seq_count(const Kv8Cache& c, int b, int n) {
   const int count = c.counts ? __ldg(c.counts + b) : n;
   return count < 0 || count > n ? 0 : count;
 }
-__device__ __forceinline__ int seq_steps(const Kv8Cache& c, int b) {
-  return (seq_len(c, b) + kStepKeys - 1) / kStepKeys;
-}
+__device__ __forceinline__ int steps_of(int len) { return (len + kStepKeys - 1) / kStepKeys; }
+__device__ __forceinline__ int seq_steps(const Kv8Cache& c, int b) { return steps_of(seq_len(c, b)); }
 
 // Every lane: the steps of sequences [0, B) summed, and of those before `b`.
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -114,14 +117,14 @@ __device__ __forceinline__ long long first_step(long long total, int used, int w
 // A place in the flattened list of steps: (sequence, pair of K/V head and row
 // chunk, step of its keys).
 struct Cursor {
-  int b, pair, s, steps;
+  int b, pair, s, len;
   __device__ __forceinline__ void settle(const Kv8Cache& c, int pairs) {
-    while (b < c.B && s >= steps) {
-      s -= steps;
-      if (steps == 0 || ++pair == pairs) {
+    while (b < c.B && s >= steps_of(len)) {
+      s -= steps_of(len);
+      if (len == 0 || ++pair == pairs) {
         pair = 0;
         ++b;
-        steps = b < c.B ? seq_steps(c, b) : 0;
+        len = b < c.B ? seq_len(c, b) : 0;
       }
     }
   }
@@ -132,8 +135,8 @@ __device__ Cursor find_cursor(const Kv8Cache& c, int pairs, long long x) {
   const int lane = threadIdx.x & 31;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
     const int b = b0 + lane;
-    const int steps = b < c.B ? seq_steps(c, b) : 0;
-    long long incl = static_cast<long long>(steps) * pairs;
+    const int len = b < c.B ? seq_len(c, b) : 0;
+    long long incl = static_cast<long long>(steps_of(len)) * pairs;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -142,10 +145,10 @@ __device__ Cursor find_cursor(const Kv8Cache& c, int pairs, long long x) {
     const unsigned past = __ballot_sync(0xffffffffu, incl > x);
     if (past) {
       const int l = __ffs(past) - 1;
-      const int st = __shfl_sync(0xffffffffu, steps, l);
+      const int len_l = __shfl_sync(0xffffffffu, len, l), st = steps_of(len_l);
       const long long rem = x - (__shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(st) * pairs);
       const int pair = static_cast<int>(rem / st);
-      return Cursor{b0 + l, pair, static_cast<int>(rem - static_cast<long long>(pair) * st), st};
+      return Cursor{b0 + l, pair, static_cast<int>(rem - static_cast<long long>(pair) * st), len_l};
     }
     x -= __shfl_sync(0xffffffffu, incl, 31);
   }
@@ -175,11 +178,11 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   return v;
 }
 
-// D[16][8] += A[16][16] B[16][8], fp16 in, fp32 sums.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+// D[16][8] += A[16][32] B[32][8], e4m3 in, fp32 sums.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -189,10 +192,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+// The next e4m3 piece of two values: x, y <- 16 times what it leaves of them.
+__device__ __forceinline__ uint32_t take_piece(float& x, float& y) {
+  const uint32_t two = f32x2_to_e4m3x2(x, y);
+  const float2 f = e4m3x2_to_f32x2(two);
+  x = (x - f.x) * 16.f;
+  y = (y - f.y) * 16.f;
+  return two;
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -215,20 +221,21 @@ struct RowEnd {
   __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) kv8_attn_kernel(const __grid_constant__ Kv8Attn p) {
-  using C = Cfg<D, NT>;
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(const __grid_constant__ Kv8Attn p) {
+  using C = Cfg<D, NQ>;
   constexpr int KU = D / 64;                  // 16-byte pieces a lane reads of a key
   constexpr int VB = D == 64 ? 8 : 16;        // bytes of a value row per lane and piece
   constexpr int VU = D / (8 * VB);            // such pieces
   constexpr int MT = D / 16;                  // 16-row tiles of O^T
-  constexpr int V_AT = 16 * D;                // values' place in a stage
+  constexpr int V_AT = kStepKeys * D;         // values' place in a stage
+  constexpr int ROWS = 4 * NQ;
   extern __shared__ __align__(16) uint8_t smem[];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 2, c4 = lane & 3;
   const int pairs = p.c.Hkv * p.chunks;
-  const int warps = gridDim.x * kWarps;
+  const int warps = gridDim.x * C::WARPS;
   const int gid = warp * gridDim.x + blockIdx.x;  // few runs spread over the SMs
   long long total, before;
   step_totals(p.c, pairs, 0, &total, &before);
@@ -240,73 +247,74 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) kv8_attn_kernel(co
   const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
   const uint32_t headers = ring + C::STAGES * C::STAGE;
 
-  // Issue side: lane l looks up step 32 k + l of the run, one batch ahead of
-  // the copies (page numbers two batches ahead, as the scales depend on them).
+  // Issue side: lane 2 j + h looks up half h of step 16 k + j of the run, one
+  // batch ahead of the copies.
   Cursor cur = find_cursor(p.c, pairs, x0);
-  cur.s += lane;
+  cur.s += lane >> 1;
   cur.settle(p.c, pairs);
   struct Meta {
-    int slot, s, where;  // slot: page * Hkv + head, -1 for a bad page; where: b * pairs + pair
-    float sk, sv;
+    int slot, s, where;  // slot: page * Hkv + head; -1: a bad page, -2: behind the sequence; where: b * pairs + pair
   };
-  auto look_page = [&](Meta& m) {
+  auto look_up = [&](Meta& m) {
     m.slot = -2;
     if (cur.b < p.c.B) {
       m.s = cur.s;
       m.where = cur.b * pairs + cur.pair;
-      const int pid = __ldg(p.c.table + static_cast<size_t>(cur.b) * p.c.max_pages +
-                            (cur.s * kStepKeys >> p.c.page_log2));
-      m.slot = pid < 0 || pid >= p.c.num_pages ? -1 : pid * p.c.Hkv + cur.pair / p.chunks;
-      cur.s += 32;
+      const int key = cur.s * kStepKeys + (lane & 1) * kHalfKeys;
+      if (key < cur.len) {
+        const int pid = __ldg(p.c.table + static_cast<size_t>(cur.b) * p.c.max_pages + (key >> p.c.page_log2));
+        m.slot = pid < 0 || pid >= p.c.num_pages ? -1 : pid * p.c.Hkv + cur.pair / p.chunks;
+      }
+      cur.s += 16;
       cur.settle(p.c, pairs);
     }
   };
-  auto look_scales = [&](Meta& m) {
-    m.sk = m.sv = 1.f;
-    if (m.slot >= 0) {
-      m.sk = __ldg(p.c.scale[0] + m.slot);
-      m.sv = __ldg(p.c.scale[1] + m.slot);
-    }
-  };
   Meta now{}, next{};
-  look_page(next);
+  float sk = 1.f, sv = 1.f;
+  look_up(next);
   int issued = 0;
   auto issue = [&]() {
     if (issued < n_steps) {
-      const int l = issued & 31;
-      if (l == 0) {
+      const int j = 2 * (issued & 15);
+      if (j == 0) {
         now = next;
-        look_scales(now);
-        look_page(next);
+        sk = sv = 1.f;
+        if (now.slot >= 0) {
+          sk = __ldg(p.c.scale[0] + now.slot);
+          sv = __ldg(p.c.scale[1] + now.slot);
+        }
+        look_up(next);
       }
-      const int slot = __shfl_sync(0xffffffffu, now.slot, l);
-      const int s = __shfl_sync(0xffffffffu, now.s, l);
-      const bool live = slot >= 0;
-      const size_t row = (static_cast<size_t>(live ? slot : 0) << p.c.page_log2) +
-                         (s * kStepKeys & ((1 << p.c.page_log2) - 1));
-      const uint8_t* kp = p.c.code[0] + row * D;
-      const uint8_t* vp = p.c.code[1] + row * D;
+      const int s = __shfl_sync(0xffffffffu, now.s, j);
       const int st = issued % C::STAGES;
       const uint32_t at = ring + st * C::STAGE;
 #pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        cp_async16(at + (2 * u * 32 + lane) * 16, kp + i * D + u * 64 + c4 * 16, live);
-        cp_async16(at + ((2 * u + 1) * 32 + lane) * 16, kp + (i + 8) * D + u * 64 + c4 * 16, live);
-      }
+      for (int h = 0; h < 2; ++h) {
+        const int slot = __shfl_sync(0xffffffffu, now.slot, j + h);
+        const bool live = slot >= 0;
+        const size_t row = (static_cast<size_t>(live ? slot : 0) << p.c.page_log2) +
+                           (s * kStepKeys + h * kHalfKeys & ((1 << p.c.page_log2) - 1));
+        const uint8_t* kp = p.c.code[0] + row * D + i * D + c4 * 16;
+        const uint8_t* vp = p.c.code[1] + row * D + 2 * c4 * D + i * VB;
 #pragma unroll
-      for (int u = 0; u < VU; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 2 * c4 + (k & 1) + (k >> 1) * 8;
-          const uint32_t dst = at + V_AT + ((u * 4 + k) * 32 + lane) * VB;
-          const uint8_t* src = vp + key * D + u * 128 + i * VB;
-          if constexpr (VB == 16) cp_async16(dst, src, live); else cp_async8(dst, src, live);
+        for (int u = 0; u < KU; ++u) {
+          cp_async16(at + (((h * KU + u) * 2) * 32 + lane) * 16, kp + u * 64, live);
+          cp_async16(at + (((h * KU + u) * 2 + 1) * 32 + lane) * 16, kp + 8 * D + u * 64, live);
         }
-      if (lane == l) {
-        if (!live) record_bad_index(p.status, WHERE_FWD_KV8);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(headers + st * C::HEADER),
-                     "r"(__float_as_uint(now.sk)), "r"(__float_as_uint(now.sv)), "r"(live ? now.s : ~now.s),
-                     "r"(now.where)
+#pragma unroll
+        for (int u = 0; u < VU; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+            const uint32_t dst = at + V_AT + (((h * VU + u) * 4 + k) * 32 + lane) * VB;
+            const uint8_t* src = vp + ((k & 1) + (k >> 1) * 8) * D + u * 128;
+            if constexpr (VB == 16) cp_async16(dst, src, live); else cp_async8(dst, src, live);
+          }
+      }
+      if ((lane >> 1) == (issued & 15)) {
+        if (now.slot == -1) record_bad_index(p.status, WHERE_FWD_KV8);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(headers + st * C::HEADER + (lane & 1) * 16),
+                     "r"(__float_as_uint(sk)), "r"(__float_as_uint(sv)), "r"(now.slot),
+                     "r"(lane & 1 ? now.where : now.s)
                      : "memory");
       }
       ++issued;
@@ -316,32 +324,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) kv8_attn_kernel(co
 #pragma unroll 1
   for (int k = 0; k < C::STAGES - 1; ++k) issue();
 
-  // Compute side.
-  uint32_t qf[NT][KU][8];                     // the row chunk's queries as the B operand
-  float acc[NT][MT][4];                       // O^T
-  float m[NT][2], l[NT][2], qfac[NT][2];      // columns 2 c4, 2 c4 + 1: reference - kShift, sum, query's power of two
-  int limit[NT][2];                           // keys the row sees
+  // Compute side. Lane (i, c4) holds row c4 + 4 nt of the chunk for keys i,
+  // i + 8 of each half step, and the columns d_of(t), + 1 of its output.
+  uint32_t qf[NQ][KU * 4];             // pieces of the chunk's queries: column 2 r + piece
+  float acc[MT][NQ + 1][4];            // O^T: tile nt has pm beside ph of rows 4 nt .., the last tile every pl
+  float m[NQ], l[NQ], qfac[NQ];        // reference - kShift, sum, the query's power of two
+  int limit[NQ];                       // keys the row sees
   int where = -1, seg_first = 0, seg_last = 0, seg_len = 0, seg_index = -1;
 
-  auto row_place = [&](int w, int r, int* b, int* qi) -> size_t {  // row r of chunk `w`: its place in [B][Hq][Nq]
-    *b = w / pairs;
-    const int pair = w - *b * pairs, h = pair / p.chunks;
-    const int row = (pair - h * p.chunks) * 8 * NT + r;
+  auto row_place = [&](int w, int r, int* qi) -> size_t {  // row r of chunk `w`: its place in [B][Hq][Nq]
+    const int b = w / pairs, pair = w - b * pairs, h = pair / p.chunks;
+    const int row = (pair - h * p.chunks) * ROWS + r;
     *qi = row < p.rows ? row / p.g : INT_MAX;
-    return row < p.rows ? (static_cast<size_t>(*b) * p.Hq + h * p.g + row % p.g) * p.Nq + *qi : 0;
+    return row < p.rows ? (static_cast<size_t>(b) * p.Hq + h * p.g + row % p.g) * p.Nq + *qi : 0;
   };
 
   auto begin_rows = [&](int w, int s) {
     where = w;
     seg_first = s;
     ++seg_index;
-    int b, qi;
-    const int b0 = w / pairs;
-    seg_len = seq_len(p.c, b0);
-    const int count = seq_count(p.c, b0, p.Nq);
+    const int b = w / pairs;
+    seg_len = seq_len(p.c, b);
+    const int count = seq_count(p.c, b, p.Nq);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const size_t at = row_place(w, nt * 8 + i, &b, &qi);
+    for (int nt = 0; nt < NQ; ++nt) {
+      int qi;
+      const size_t at = row_place(w, nt * 4 + (i >> 1), &qi);
       const bool live = qi < count;
       uint4 raw[KU][2];
       uint32_t amax = 0;
@@ -359,68 +367,83 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) kv8_attn_kernel(co
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // exponent of the largest value; 2^-100 and below are left as they are
       const int x = max(static_cast<int>(amax >> 7) - 127, -100);
-      const float mul = exp2i(14 - x);
+      const float mul = exp2i(7 - x);
 #pragma unroll
       for (int u = 0; u < KU; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t w4[4] = {raw[u][e].x, raw[u][e].y, raw[u][e].z, raw[u][e].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack_bf16x2(w4[k]);
-            qf[nt][u][e * 4 + k] = pack_f16x2(f.x * mul, f.y * mul);
+          for (int k = 0; k < 4; k += 2) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float2 f = unpack_bf16x2(w4[k + y]);
+              f.x *= mul;
+              f.y *= mul;
+              // an infinity would saturate to a number
+              if (isinf(f.x)) f.x = NAN;
+              if (isinf(f.y)) f.y = NAN;
+              const uint32_t hi = take_piece(f.x, f.y);
+              word |= (i & 1 ? f32x2_to_e4m3x2(f.x, f.y) : hi) << (16 * y);
+            }
+            qf[nt][u * 4 + e * 2 + k / 2] = word;
           }
         }
-      const float fac = exp2i(x - 14);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        qfac[nt][j] = __shfl_sync(0xffffffffu, fac, (2 * c4 + j) * 4);
-        row_place(w, nt * 8 + 2 * c4 + j, &b, &qi);
-        limit[nt][j] = qi >= count ? 0 : p.causal ? min(seg_len, seg_len - count + qi + 1) : seg_len;
-        m[nt][j] = -INFINITY;
-        l[nt][j] = 0.f;
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[nt][t][k] = 0.f;
+      qfac[nt] = __shfl_sync(0xffffffffu, exp2i(x - 7), 8 * c4);
+      row_place(w, nt * 4 + c4, &qi);
+      limit[nt] = qi >= count ? 0 : p.causal ? min(seg_len, seg_len - count + qi + 1) : seg_len;
+      m[nt] = -INFINITY;
+      l[nt] = 0.f;
     }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int nt = 0; nt <= NQ; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[t][nt][k] = 0.f;
   };
 
-  // The lane's columns of O^T: 2 consecutive d per 16-row tile.
-  auto d_of = [&](int t) { return D == 256 ? (t >> 3) * 128 + i * 16 + 2 * (t & 7) : i * (D / 8) + 2 * t; };
+  // One value of O^T: its three pieces' sums. y: the second of the lane's two columns.
+  auto joined = [&](int t, int nt, int y) {
+    const float pl = acc[t][NQ][2 * y + (nt & 1)];
+    return fmaf(pl, 1.f / 256.f, fmaf(acc[t][nt][2 * y + 1], 1.f / 16.f, acc[t][nt][2 * y]));
+  };
 
   auto end_rows = [&]() {
-    const bool whole = seg_first == 0 && seg_last + 1 == (seg_len + kStepKeys - 1) / kStepKeys;
-    const int b0 = where / pairs;
-    const int count = seq_count(p.c, b0, p.Nq);
+    const bool whole = seg_first == 0 && seg_last + 1 == steps_of(seg_len);
+    const int count = seq_count(p.c, where / pairs, p.Nq);
+    constexpr int PER = D == 64 ? 8 : 16;  // consecutive columns a lane holds
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NQ; ++nt) {
+      float sum = l[nt];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int r = nt * 4 + c4;
+      int qi;
+      const size_t at = row_place(where, r, &qi);
+      if (qi >= count) continue;
+      if (whole) {
+        const RowEnd end(m[nt], sum);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float sum = l[nt][j];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int r = nt * 8 + 2 * c4 + j;
-        int b, qi;
-        const size_t at = row_place(where, r, &b, &qi);
-        if (qi >= count) continue;
-        if (whole) {
-          const RowEnd end(m[nt][j], sum);
+        for (int t = 0; t < MT; t += 4) {
+          uint32_t o[4];
 #pragma unroll
-          for (int t = 0; t < MT; ++t)
-            *reinterpret_cast<uint32_t*>(p.o + at * D + d_of(t)) =
-                pack_bf16x2(end(acc[nt][t][j]), end(acc[nt][t][2 + j]));
-          if (i == 0) p.lse[at] = end.lse;
-        } else {
-          const size_t slot = (static_cast<size_t>(gid) * 2 + (seg_index > 0)) * p.part_rows + r;
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            *reinterpret_cast<float2*>(p.part + slot * D + d_of(t)) = make_float2(acc[nt][t][j], acc[nt][t][2 + j]);
-          if (i == 0) p.part_ml[slot] = make_float2(m[nt][j], sum);
+          for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(end(joined(t + k, nt, 0)), end(joined(t + k, nt, 1)));
+          *reinterpret_cast<uint4*>(p.o + at * D + (t / 8) * 128 + i * PER + 2 * (t & 7)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
+        if (i == 0) p.lse[at] = end.lse;
+      } else {
+        const size_t slot = (static_cast<size_t>(gid) * 2 + (seg_index > 0)) * p.part_rows + r;
+#pragma unroll
+        for (int t = 0; t < MT; t += 2)
+          *reinterpret_cast<float4*>(p.part + slot * D + (t / 8) * 128 + i * PER + 2 * (t & 7)) =
+              make_float4(joined(t, nt, 0), joined(t, nt, 1), joined(t + 1, nt, 0), joined(t + 1, nt, 1));
+        if (i == 0) p.part_ml[slot] = make_float2(m[nt], sum);
       }
+    }
   };
 
 #pragma unroll 1
@@ -430,117 +453,131 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) kv8_attn_kernel(co
     issue();
     const int st = k % C::STAGES;
     const uint32_t at = ring + st * C::STAGE;
-    const uint4 head = ld_shared_v4(headers + st * C::HEADER);
-    const bool bad = static_cast<int>(head.z) < 0;
-    const int s = bad ? ~static_cast<int>(head.z) : static_cast<int>(head.z);
-    if (static_cast<int>(head.w) != where) {
+    const uint4 head[2] = {ld_shared_v4(headers + st * C::HEADER), ld_shared_v4(headers + st * C::HEADER + 16)};
+    const int s = static_cast<int>(head[0].w);
+    if (static_cast<int>(head[1].w) != where) {
       if (where >= 0) end_rows();
-      begin_rows(static_cast<int>(head.w), s);
+      begin_rows(static_cast<int>(head[1].w), s);
     }
     seg_last = s;
-    const float kf = __uint_as_float(head.x) * p.scale_log2;
-    // sv = 2^ev * mant
-    const int ev = min(max(static_cast<int>(head.y >> 23 & 255) - 127, -126), 126);
-    const float mant = __uint_as_float(head.y) * exp2i(-ev);
-    const float inv_sv = exp2i(-static_cast<int>(kSumBias)) / __uint_as_float(head.y);
 
-    float sc[NT][4];
+    float sc[2][NQ][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+      for (int nt = 0; nt < NQ; ++nt)
 #pragma unroll
-    for (int u = 0; u < KU; ++u) {
-      const uint4 ka = ld_shared_v4(at + (2 * u * 32 + lane) * 16);
-      const uint4 kb = ld_shared_v4(at + ((2 * u + 1) * 32 + lane) * 16);
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int e = 0; e < 4; ++e) sc[h][nt][e] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = e4m3x2_to_f16x2(wa[w] & 0xffffu), a2 = e4m3x2_to_f16x2(wa[w] >> 16);
-        const uint32_t a1 = e4m3x2_to_f16x2(wb[w] & 0xffffu), a3 = e4m3x2_to_f16x2(wb[w] >> 16);
+      for (int u = 0; u < KU; ++u) {
+        const uint4 a = ld_shared_v4(at + (((h * KU + u) * 2) * 32 + lane) * 16);
+        const uint4 b = ld_shared_v4(at + (((h * KU + u) * 2 + 1) * 32 + lane) * 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt], a0, a1, a2, a3, qf[nt][u][2 * w], qf[nt][u][2 * w + 1]);
+        for (int nt = 0; nt < NQ; ++nt) {
+          mma_e4m3(sc[h][nt], a.x, b.x, a.y, b.y, qf[nt][u * 4], qf[nt][u * 4 + 1]);
+          mma_e4m3(sc[h][nt], a.z, b.z, a.w, b.w, qf[nt][u * 4 + 2], qf[nt][u * 4 + 3]);
+        }
       }
     }
 
-    const int key = s * kStepKeys + i;
+    float t[2][NQ][2], inv_sv[2];  // u of keys i, i + 8 of each half
     bool grow = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < 2; ++h) {
+      const float kf = __uint_as_float(head[h].x) * p.scale_log2;
+      // log2 of the value scale: exact for a power of two
+      const int e = min(max(static_cast<int>(head[h].y >> 23 & 255) - 127, -126), 126);
+      const float ev = static_cast<float>(e) + log2f(__uint_as_float(head[h].y) * exp2i(-e));
+      inv_sv[h] = exp2i(-static_cast<int>(kSumBias)) / __uint_as_float(head[h].y);
+      const int key = s * kStepKeys + h * kHalfKeys + i;
+      const bool bad = static_cast<int>(head[h].z) == -1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool seen = !bad && key + (e >> 1) * 8 < limit[nt][e & 1];
-        sc[nt][e] = seen ? fmaf(sc[nt][e] * qfac[nt][e & 1], kf, static_cast<float>(ev)) : -INFINITY;
-        grow |= sc[nt][e] > m[nt][e & 1] + (kSlack + kShift);
-      }
-    if (__any_sync(0xffffffffu, grow)) {
+      for (int nt = 0; nt < NQ; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mx = fmaxf(sc[nt][j], sc[nt][2 + j]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kShift;
-          const float to = fmaxf(m[nt][j], mx);
-          const float alpha = to == -INFINITY ? 1.f : ex2_approx(m[nt][j] - to);
-          m[nt][j] = to;
-          l[nt][j] *= alpha;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            acc[nt][t][j] *= alpha;
-            acc[nt][t][2 + j] *= alpha;
-          }
+        for (int y = 0; y < 2; ++y) {
+          const float dot = fmaf(sc[h][nt][2 * y + 1], 1.f / 16.f, sc[h][nt][2 * y]) * qfac[nt];
+          t[h][nt][y] = !bad && key + 8 * y < limit[nt] ? fmaf(dot, kf, ev) : -INFINITY;
+          grow |= t[h][nt][y] > m[nt] + (kSlack + kShift);
         }
     }
-    uint32_t pf[NT][2];
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float pr[4];
+      for (int nt = 0; nt < NQ; ++nt) {
+        float mx = fmaxf(fmaxf(t[0][nt][0], t[0][nt][1]), fmaxf(t[1][nt][0], t[1][nt][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kShift;
+        const float to = fmaxf(m[nt], mx);
+        const float alpha = to == -INFINITY ? 1.f : ex2_approx(m[nt] - to);
+        m[nt] = to;
+        l[nt] *= alpha;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-        pr[e] = ex2_approx(sc[nt][e] - ref);
-        l[nt][e & 1] = fmaf(pr[e], inv_sv, l[nt][e & 1]);
+        for (int q = 0; q < MT; ++q) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[q][nt][e] *= alpha;
+          acc[q][NQ][nt] *= alpha;
+          acc[q][NQ][2 + nt] *= alpha;
+        }
       }
-      pf[nt][0] = transpose8(pack_f16x2(pr[0] * mant, pr[1] * mant));
-      pf[nt][1] = transpose8(pack_f16x2(pr[2] * mant, pr[3] * mant));
+    }
+
+    uint32_t pf[NQ + 1][2];  // pieces of the weights as the B operand: keys 2 c4, + 8, + 1, + 9 of column i
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t small = 0;
+#pragma unroll
+      for (int nt = 0; nt < NQ; ++nt) {
+        const float ref = m[nt] == -INFINITY ? 0.f : m[nt];
+        float a = ex2_approx(t[h][nt][0] - ref), b = ex2_approx(t[h][nt][1] - ref);
+        l[nt] = fmaf(a + b, inv_sv[h], l[nt]);
+        const uint32_t hi = take_piece(a, b);
+        const uint32_t mid = take_piece(a, b);
+        pf[nt][h] = transpose8(hi | mid << 16);
+        small |= f32x2_to_e4m3x2(a, b) << (16 * nt);
+      }
+      pf[NQ][h] = transpose8(small);
     }
 
     const bool tail = (s + 1) * kStepKeys > seg_len;
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
-      uint32_t v[4][VB / 4];
+      uint32_t v[2][4][VB / 4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t addr = at + V_AT + ((u * 4 + q) * 32 + lane) * VB;
-        if constexpr (VB == 16) {
-          const uint4 x = ld_shared_v4(addr);
-          v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
-        } else {
-          const uint2 x = ld_shared_v2(addr);
-          v[q][0] = x.x, v[q][1] = x.y;
-        }
-        // What lies behind the last token may be any bytes, NaN codes among
-        // them, and 0 * NaN is not 0.
-        if (tail && s * kStepKeys + 2 * c4 + (q & 1) + (q >> 1) * 8 >= seg_len) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int w = 0; w < VB / 4; ++w) v[q][w] = 0;
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t addr = at + V_AT + (((h * VU + u) * 4 + q) * 32 + lane) * VB;
+          if constexpr (VB == 16) {
+            const uint4 x = ld_shared_v4(addr);
+            v[h][q][0] = x.x, v[h][q][1] = x.y, v[h][q][2] = x.z, v[h][q][3] = x.w;
+          } else {
+            const uint2 x = ld_shared_v2(addr);
+            v[h][q][0] = x.x, v[h][q][1] = x.y;
+          }
+          // What lies behind the last token may be any bytes, NaN codes among
+          // them, and 0 * NaN is not 0.
+          if (tail && s * kStepKeys + h * kHalfKeys + 2 * c4 + (q & 1) + (q >> 1) * 8 >= seg_len) {
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) v[h][q][w] = 0;
+          }
         }
-      }
 #pragma unroll
       for (int w = 0; w < VB / 4; ++w) {
-        const uint32_t x0_ = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        const int t = (u * (VB / 4) + w) * 2;
-        const uint32_t a0 = e4m3x2_to_f16x2(x0_ & 0xffffu), a1 = e4m3x2_to_f16x2(x0_ >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(y0 & 0xffffu), a3 = e4m3x2_to_f16x2(y0 >> 16);
-        const uint32_t b0 = e4m3x2_to_f16x2(x1 & 0xffffu), b1 = e4m3x2_to_f16x2(x1 >> 16);
-        const uint32_t b2 = e4m3x2_to_f16x2(y1 & 0xffffu), b3 = e4m3x2_to_f16x2(y1 >> 16);
+        uint32_t a[2][4];  // columns 4 w .. 4 w + 3, keys 2 c4, + 8, + 1, + 9 of each half
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(acc[nt][t], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-          mma_f16(acc[nt][t + 1], b0, b1, b2, b3, pf[nt][0], pf[nt][1]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x0 = __byte_perm(v[h][0][w], v[h][2][w], 0x5140), x1 = __byte_perm(v[h][0][w], v[h][2][w], 0x7362);
+          const uint32_t y0 = __byte_perm(v[h][1][w], v[h][3][w], 0x5140), y1 = __byte_perm(v[h][1][w], v[h][3][w], 0x7362);
+          a[h][0] = __byte_perm(x0, y0, 0x5410);
+          a[h][1] = __byte_perm(x0, y0, 0x7632);
+          a[h][2] = __byte_perm(x1, y1, 0x5410);
+          a[h][3] = __byte_perm(x1, y1, 0x7632);
+        }
+        const int q = (u * (VB / 4) + w) * 2;
+#pragma unroll
+        for (int nt = 0; nt <= NQ; ++nt) {
+          mma_e4m3(acc[q][nt], a[0][0], a[0][1], a[1][0], a[1][1], pf[nt][0], pf[nt][1]);
+          mma_e4m3(acc[q + 1][nt], a[0][2], a[0][3], a[1][2], a[1][3], pf[nt][0], pf[nt][1]);
         }
       }
     }
@@ -614,28 +651,29 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   if (lane == 0) p.lse[at] = end.lse;
 }
 
-int row_tiles(int d, long long rows) { return d <= 128 && rows > 8 ? 2 : 1; }
+// 8-column tiles of a row chunk: two (8 rows) where the rows fill more than one
+// and the sums of both fit the registers.
+int query_tiles(int d, long long rows) { return d <= 128 && rows > 4 ? 2 : 1; }
 
 size_t part_bytes(int d, long long rows, size_t* ml_off) {
-  const int nt = row_tiles(d, rows);
-  const int ctas = d <= 128 && nt == 1 ? 2 : 1;
-  const size_t slots = static_cast<size_t>(2) * kMaxSms * ctas * kWarps * std::min<long long>(rows, 8 * nt);
+  const size_t slots = static_cast<size_t>(2) * kMaxSms * (1024 / d) * std::min<long long>(rows, 4 * query_tiles(d, rows));
   *ml_off = slots * d * sizeof(float);
   return *ml_off + slots * sizeof(float2);
 }
 
-template <int D, int NT>
-cudaError_t launch_t(Kv8Attn& a, int num_sms, cudaStream_t stream) {
-  using C = Cfg<D, NT>;
-  auto kern = kv8_attn_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+template <int D, int NQ>
+cudaError_t launch_t(Kv8Attn& a, const DeviceInfo& dev, cudaStream_t stream) {
+  using C = Cfg<D, NQ>;
+  auto kern = kv8_attn_kernel<D, NQ>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, dev.device, allowed);
   if (e != cudaSuccess) return e;
   // no more blocks than runs that the longest sequences the table allows could have
   const double most = static_cast<double>(a.c.B) * a.c.Hkv * a.chunks *
-                      ((static_cast<long long>(a.c.max_pages) << a.c.page_log2) / kStepKeys) / kMinSteps;
-  const int full = std::min(num_sms, kMaxSms) * C::CTAS;
+                      ((static_cast<long long>(a.c.max_pages) << a.c.page_log2) / kStepKeys + 1) / kMinSteps;
+  const int full = std::min(dev.num_sms, kMaxSms);
   const int grid = most < full ? std::max(1, static_cast<int>(most)) : full;
-  kern<<<grid, kThreads, C::SMEM, stream>>>(a);
+  kern<<<grid, C::WARPS * 32, C::SMEM, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -647,7 +685,7 @@ cudaError_t launch_t(Kv8Attn& a, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D>, a, grid * kWarps, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, kv8_combine_kernel<D>, a, grid * C::WARPS, 4 * NQ);
 }
 
 }  // namespace
@@ -696,18 +734,17 @@ fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, 
   a.Nq = Nq;
   a.g = Hq / Hkv;
   a.rows = a.g * Nq;
-  const int nt = row_tiles(d, a.rows);
-  a.chunks = (a.rows + 8 * nt - 1) / (8 * nt);
-  a.part_rows = std::min(a.rows, 8 * nt);
+  const int nq = query_tiles(d, a.rows);
+  a.chunks = (a.rows + 4 * nq - 1) / (4 * nq);
+  a.part_rows = std::min(a.rows, 4 * nq);
   part_bytes(d, a.rows, &ml_off);
   a.part = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ml_off);
   a.causal = causal;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  if (d == 64) return from_cuda(nt == 1 ? launch_t<64, 1>(a, dev.num_sms, stream) : launch_t<64, 2>(a, dev.num_sms, stream));
-  if (d == 128)
-    return from_cuda(nt == 1 ? launch_t<128, 1>(a, dev.num_sms, stream) : launch_t<128, 2>(a, dev.num_sms, stream));
-  return from_cuda(launch_t<256, 1>(a, dev.num_sms, stream));
+  if (d == 64) return from_cuda(nq == 1 ? launch_t<64, 1>(a, dev, stream) : launch_t<64, 2>(a, dev, stream));
+  if (d == 128) return from_cuda(nq == 1 ? launch_t<128, 1>(a, dev, stream) : launch_t<128, 2>(a, dev, stream));
+  return from_cuda(launch_t<256, 1>(a, dev, stream));
 }
 
 }  // extern "C"

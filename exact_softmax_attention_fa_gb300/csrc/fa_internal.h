@@ -2,6 +2,7 @@
 // translation units. Host-side only; no torch types anywhere.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -87,12 +88,23 @@ fa_status_t check_common(int B, int H, int N, int d, int causal, float scale, bo
 
 // The current device as the operators outside fa_api.cu need it.
 struct DeviceInfo {
-  int num_sms;
+  int device, num_sms;
   uint32_t* status;  // device address of the status word
   uint64_t wait_limit_ns;
 };
 fa_status_t device_info(DeviceInfo* out);
 fa_status_t from_cuda(cudaError_t e);
+// Allow a kernel its dynamic shared memory, once per device (`done`: a bit per
+// device, kept by the launcher): the attribute call costs about half a
+// microsecond, which short calls would pay every time.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = 1ull << device;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Launchers (defined in the kernel translation units). Return cudaSuccess or
