@@ -15,8 +15,9 @@
 // own, since a decoding call leaves most of an MMA's 8 columns empty anyway:
 //   a query value q 2^a (row maximum in [2^7, 2^8)) = qh + 2^-4 ql, exact down to
 //   2^-14 of the row's largest value, and within 2^-22 of it below;
-//   P (at most 448) = ph + 2^-4 pm + 2^-8 pl: 2^-12 relative, and never coarser
-//   than 2^-24 of the row's largest weight. l sums the unrounded weights.
+//   P (at most 448), rounded to fp16, = ph + 2^-4 pm + 2^-8 pl: 2^-11 relative, and
+//   never coarser than 2^-24 of the row's largest weight (fp16 so that the pieces
+//   are taken two at a time; l sums the unrounded weights).
 // (Converting the codes to fp16 for m16n8k16 products was measured first: 519
 // instructions per 16 keys at d = 128, most of them unpacking bytes, and 0.61 of
 // the HBM rate at B = 8, Hkv = 8, 32768 keys.)
@@ -155,11 +156,11 @@ __device__ Cursor find_cursor(const Kv8Cache& c, int pairs, long long x) {
   return Cursor{c.B, 0, 0, 0};
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -192,13 +193,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// The next e4m3 piece of two values: x, y <- 16 times what it leaves of them.
-__device__ __forceinline__ uint32_t take_piece(float& x, float& y) {
-  const uint32_t two = f32x2_to_e4m3x2(x, y);
-  const float2 f = e4m3x2_to_f32x2(two);
-  x = (x - f.x) * 16.f;
-  y = (y - f.y) * 16.f;
+// The next e4m3 piece of two fp16 values: v <- 16 times what it leaves of them
+// (exact: the piece and the rest together hold the value's 11 bits).
+__device__ __forceinline__ uint32_t take_piece(__half2& v) {
+  const uint32_t two = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
+  const uint32_t back = e4m3x2_to_f16x2(two);
+  v = __hmul2(__hsub2(v, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(16.f));
   return two;
+}
+__device__ __forceinline__ uint32_t last_piece(const __half2& v) {
+  return f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -270,7 +274,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
     }
   };
   Meta now{}, next{};
-  float sk = 1.f, sv = 1.f;
+  // c sk, log2 sv, 2^-kSumBias / sv of the half step; log2 sv = -inf hides a bad page's keys
+  float kf = 0.f, ev = 0.f, inv = 0.f;
   look_up(next);
   int issued = 0;
   auto issue = [&]() {
@@ -278,10 +283,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       const int j = 2 * (issued & 15);
       if (j == 0) {
         now = next;
-        sk = sv = 1.f;
+        kf = ev = inv = 0.f;
         if (now.slot >= 0) {
-          sk = __ldg(p.c.scale[0] + now.slot);
-          sv = __ldg(p.c.scale[1] + now.slot);
+          kf = __ldg(p.c.scale[0] + now.slot) * p.scale_log2;
+          const float sv = __ldg(p.c.scale[1] + now.slot);
+          const int e = min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
+          ev = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
+          inv = exp2i(-static_cast<int>(kSumBias)) / sv;
+        } else if (now.slot == -1) {
+          ev = -INFINITY;
+          record_bad_index(p.status, WHERE_FWD_KV8);
         }
         look_up(next);
       }
@@ -291,32 +302,37 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int slot = __shfl_sync(0xffffffffu, now.slot, j + h);
-        const bool live = slot >= 0;
-        const size_t row = (static_cast<size_t>(live ? slot : 0) << p.c.page_log2) +
-                           (s * kStepKeys + h * kHalfKeys & ((1 << p.c.page_log2) - 1));
-        const uint8_t* kp = p.c.code[0] + row * D + i * D + c4 * 16;
-        const uint8_t* vp = p.c.code[1] + row * D + 2 * c4 * D + i * VB;
+        const uint32_t kd = at + (h * KU * 2 * 32 + lane) * 16, vd = at + V_AT + (h * VU * 4 * 32 + lane) * VB;
+        if (slot >= 0) {
+          const size_t row = (static_cast<size_t>(slot) << p.c.page_log2) +
+                             (s * kStepKeys + h * kHalfKeys & ((1 << p.c.page_log2) - 1));
+          const uint8_t* kp = p.c.code[0] + row * D + i * D + c4 * 16;
+          const uint8_t* vp = p.c.code[1] + row * D + 2 * c4 * D + i * VB;
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-          cp_async16(at + (((h * KU + u) * 2) * 32 + lane) * 16, kp + u * 64, live);
-          cp_async16(at + (((h * KU + u) * 2 + 1) * 32 + lane) * 16, kp + 8 * D + u * 64, live);
-        }
-#pragma unroll
-        for (int u = 0; u < VU; ++u)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-            const uint32_t dst = at + V_AT + (((h * VU + u) * 4 + k) * 32 + lane) * VB;
-            const uint8_t* src = vp + ((k & 1) + (k >> 1) * 8) * D + u * 128;
-            if constexpr (VB == 16) cp_async16(dst, src, live); else cp_async8(dst, src, live);
+          for (int u = 0; u < KU; ++u) {
+            cp_async16(kd + 2 * u * 512, kp + u * 64);
+            cp_async16(kd + (2 * u + 1) * 512, kp + 8 * D + u * 64);
           }
+#pragma unroll
+          for (int u = 0; u < VU; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+              const uint8_t* src = vp + ((k & 1) + (k >> 1) * 8) * D + u * 128;
+              const uint32_t dst = vd + (u * 4 + k) * 32 * VB;
+              if constexpr (VB == 16) cp_async16(dst, src); else cp_async8(dst, src);
+            }
+        } else {  // a bad page or places behind the sequence: codes of 0
+#pragma unroll 1
+          for (int u = 0; u < 2 * KU; ++u) st_shared_v4(kd + u * 512, 0, 0, 0, 0);
+#pragma unroll 1
+          for (int u = 0; u < VU * 4 * VB / 4; ++u) st_shared_b32(vd + (u / (VB / 4)) * 32 * VB + u % (VB / 4) * 4, 0);
+        }
       }
-      if ((lane >> 1) == (issued & 15)) {
-        if (now.slot == -1) record_bad_index(p.status, WHERE_FWD_KV8);
+      if ((lane >> 1) == (issued & 15))
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(headers + st * C::HEADER + (lane & 1) * 16),
-                     "r"(__float_as_uint(sk)), "r"(__float_as_uint(sv)), "r"(now.slot),
+                     "r"(__float_as_uint(kf)), "r"(__float_as_uint(ev)), "r"(__float_as_uint(inv)),
                      "r"(lane & 1 ? now.where : now.s)
                      : "memory");
-      }
       ++issued;
     }
     cp_async_commit();
@@ -331,6 +347,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   float m[NQ], l[NQ], qfac[NQ];        // reference - kShift, sum, the query's power of two
   int limit[NQ];                       // keys the row sees
   int where = -1, seg_first = 0, seg_last = 0, seg_len = 0, seg_index = -1;
+  int seg_open = 0;                    // keys that every row of the chunk sees
 
   auto row_place = [&](int w, int r, int* qi) -> size_t {  // row r of chunk `w`: its place in [B][Hq][Nq]
     const int b = w / pairs, pair = w - b * pairs, h = pair / p.chunks;
@@ -346,6 +363,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
     const int b = w / pairs;
     seg_len = seq_len(p.c, b);
     const int count = seq_count(p.c, b, p.Nq);
+    seg_open = seg_len;
 #pragma unroll
     for (int nt = 0; nt < NQ; ++nt) {
       int qi;
@@ -384,15 +402,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
               // an infinity would saturate to a number
               if (isinf(f.x)) f.x = NAN;
               if (isinf(f.y)) f.y = NAN;
-              const uint32_t hi = take_piece(f.x, f.y);
-              word |= (i & 1 ? f32x2_to_e4m3x2(f.x, f.y) : hi) << (16 * y);
+              __half2 v = __floats2half2_rn(f.x, f.y);
+              const uint32_t hi = take_piece(v);
+              word |= (i & 1 ? last_piece(v) : hi) << (16 * y);
             }
             qf[nt][u * 4 + e * 2 + k / 2] = word;
           }
         }
       qfac[nt] = __shfl_sync(0xffffffffu, exp2i(x - 7), 8 * c4);
       row_place(w, nt * 4 + c4, &qi);
-      limit[nt] = qi >= count ? 0 : p.causal ? min(seg_len, seg_len - count + qi + 1) : seg_len;
+      limit[nt] = p.causal && qi < count ? min(seg_len, seg_len - count + qi + 1) : seg_len;
+      seg_open = min(seg_open, __reduce_min_sync(0xffffffffu, limit[nt]));
       m[nt] = -INFINITY;
       l[nt] = 0.f;
     }
@@ -480,26 +500,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       }
     }
 
-    float t[2][NQ][2], inv_sv[2];  // u of keys i, i + 8 of each half
-    bool grow = false;
+    float t[2][NQ][2];  // u of keys i, i + 8 of each half
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float kf = __uint_as_float(head[h].x) * p.scale_log2;
-      // log2 of the value scale: exact for a power of two
-      const int e = min(max(static_cast<int>(head[h].y >> 23 & 255) - 127, -126), 126);
-      const float ev = static_cast<float>(e) + log2f(__uint_as_float(head[h].y) * exp2i(-e));
-      inv_sv[h] = exp2i(-static_cast<int>(kSumBias)) / __uint_as_float(head[h].y);
-      const int key = s * kStepKeys + h * kHalfKeys + i;
-      const bool bad = static_cast<int>(head[h].z) == -1;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int nt = 0; nt < NQ; ++nt)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float dot = fmaf(sc[h][nt][2 * y + 1], 1.f / 16.f, sc[h][nt][2 * y]) * qfac[nt];
-          t[h][nt][y] = !bad && key + 8 * y < limit[nt] ? fmaf(dot, kf, ev) : -INFINITY;
-          grow |= t[h][nt][y] > m[nt] + (kSlack + kShift);
+          t[h][nt][y] = fmaf(dot, __uint_as_float(head[h].x), __uint_as_float(head[h].y));
         }
+    if ((s + 1) * kStepKeys > seg_open) {  // some row does not see every key of this step
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (s * kStepKeys + h * kHalfKeys + i + 8 * y >= limit[nt]) t[h][nt][y] = -INFINITY;
     }
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NQ; ++nt)
+      grow |= fmaxf(fmaxf(t[0][nt][0], t[0][nt][1]), fmaxf(t[1][nt][0], t[1][nt][1])) > m[nt] + (kSlack + kShift);
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NQ; ++nt) {
@@ -528,17 +551,31 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
 #pragma unroll
       for (int nt = 0; nt < NQ; ++nt) {
         const float ref = m[nt] == -INFINITY ? 0.f : m[nt];
-        float a = ex2_approx(t[h][nt][0] - ref), b = ex2_approx(t[h][nt][1] - ref);
-        l[nt] = fmaf(a + b, inv_sv[h], l[nt]);
-        const uint32_t hi = take_piece(a, b);
-        const uint32_t mid = take_piece(a, b);
+        const float a = ex2_approx(t[h][nt][0] - ref), b = ex2_approx(t[h][nt][1] - ref);
+        l[nt] = fmaf(a + b, __uint_as_float(head[h].z), l[nt]);
+        __half2 v = __floats2half2_rn(a, b);
+        const uint32_t hi = take_piece(v);
+        const uint32_t mid = take_piece(v);
         pf[nt][h] = transpose8(hi | mid << 16);
-        small |= f32x2_to_e4m3x2(a, b) << (16 * nt);
+        small |= last_piece(v) << (16 * nt);
       }
       pf[NQ][h] = transpose8(small);
     }
 
-    const bool tail = (s + 1) * kStepKeys > seg_len;
+    // What lies behind the last token may be any bytes, NaN codes among them,
+    // and 0 * NaN is not 0.
+    if ((s + 1) * kStepKeys > seg_len) {
+#pragma unroll 1
+      for (int q = 0; q < 8; ++q) {
+        const int key = s * kStepKeys + (q >> 2) * kHalfKeys + 2 * c4 + (q & 1) + (q >> 1 & 1) * 8;
+        if (key < seg_len) continue;
+#pragma unroll 1
+        for (int u = 0; u < VU; ++u)
+#pragma unroll 1
+          for (int w = 0; w < VB; w += 4)
+            st_shared_b32(at + V_AT + ((((q >> 2) * VU + u) * 4 + (q & 3)) * 32 + lane) * VB + w, 0);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
       uint32_t v[2][4][VB / 4];
@@ -553,12 +590,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
           } else {
             const uint2 x = ld_shared_v2(addr);
             v[h][q][0] = x.x, v[h][q][1] = x.y;
-          }
-          // What lies behind the last token may be any bytes, NaN codes among
-          // them, and 0 * NaN is not 0.
-          if (tail && s * kStepKeys + h * kHalfKeys + 2 * c4 + (q & 1) + (q >> 1) * 8 >= seg_len) {
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) v[h][q][w] = 0;
           }
         }
 #pragma unroll

@@ -37,6 +37,12 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
 // Nearest e4m3 codes of two values (ties to even, saturating; NaN stays NaN).
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
