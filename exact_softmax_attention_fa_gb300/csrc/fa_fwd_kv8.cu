@@ -24,17 +24,16 @@
 //
 // Bound: HBM, one byte per cached value. Each warp owns a run of consecutive
 // 32-key steps of the flattened list of (sequence, K/V head, row chunk) and
-// streams them through a ring of its own in shared memory: every lane copies
-// (cp.async) exactly the 16-byte pieces it will read back, so the ring needs no
-// barrier, has no bank conflicts and keeps (stages - 1) * 64 d bytes per warp
-// in flight. Runs are of equal length whatever the sequences' lengths are; a
-// row whose keys are shared between warps is joined by kv8_combine_kernel.
+// streams them (cp.async, 16 keys of a page are 16 d contiguous bytes) through a
+// ring of its own in shared memory, so no warp waits for another and
+// (stages - 1) * 64 d bytes per warp are in flight. Runs are of equal length
+// whatever the sequences' lengths are; a row whose keys are shared between
+// warps is joined by kv8_combine_kernel.
 //
 // Products are m16n8k32 with the cache as the 16-row operand and the rows'
-// pieces as columns (S^T = K Q^T, O^T = V^T P^T). The order of d within S is free,
-// so a lane's 16 contiguous codes of a key are its fragments as they are; the
-// order of keys within O is free too, and V needs its 4 x 4 byte blocks turned
-// (two byte permutes a word) to have four keys of a column side by side.
+// pieces as columns (S^T = K Q^T, O^T = V^T P^T). A matrix load gives K's
+// fragments as they are. V is loaded transposed in 16-bit units, which leaves
+// two adjacent columns of a key together; one byte permute a word parts them.
 #include <algorithm>
 #include <cmath>
 
@@ -159,9 +158,6 @@ __device__ Cursor find_cursor(const Kv8Cache& c, int pairs, long long x) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -173,16 +169,26 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+// Four 8 x 8 matrices of 16-bit values; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ uint4 ldmatrix4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 ldmatrix4_trans(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
   return v;
 }
 
 // D[16][8] += A[16][32] B[32][8], e4m3 in, fp32 sums.
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -228,10 +234,7 @@ struct RowEnd {
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(const __grid_constant__ Kv8Attn p) {
   using C = Cfg<D, NQ>;
-  constexpr int KU = D / 64;                  // 16-byte pieces a lane reads of a key
-  constexpr int VB = D == 64 ? 8 : 16;        // bytes of a value row per lane and piece
-  constexpr int VU = D / (8 * VB);            // such pieces
-  constexpr int MT = D / 16;                  // 16-row tiles of O^T
+  constexpr int MT = D / 16;                  // 16-byte column blocks; 16-row tiles of O^T
   constexpr int V_AT = kStepKeys * D;         // values' place in a stage
   constexpr int ROWS = 4 * NQ;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -277,7 +280,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   // c sk, log2 sv, 2^-kSumBias / sv of the half step; log2 sv = -inf hides a bad page's keys
   float kf = 0.f, ev = 0.f, inv = 0.f;
   look_up(next);
-  int issued = 0;
+  // A stage holds rows of D bytes, keys then values; the 16-byte pieces of a row
+  // are XORed with its key, so that eight keys' pieces of one block lie in
+  // different banks. Pass q of a half step brings its bytes 512 q + 16 lane.
+  auto swizzle = [](int key) -> uint32_t { return (D == 64 ? key >> 1 & 3 : key & 7) << 4; };
+  auto place = [&](int q) -> uint32_t { return (lane * 16 + q * 512) ^ swizzle(lane / MT + q * (512 / D)); };
+  int issued = 0, in_stage = 0;
   auto issue = [&]() {
     if (issued < n_steps) {
       const int j = 2 * (issued & 15);
@@ -297,35 +305,30 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
         look_up(next);
       }
       const int s = __shfl_sync(0xffffffffu, now.s, j);
-      const int st = issued % C::STAGES;
+      const int st = in_stage;
+      in_stage = in_stage + 1 == C::STAGES ? 0 : in_stage + 1;
       const uint32_t at = ring + st * C::STAGE;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int slot = __shfl_sync(0xffffffffu, now.slot, j + h);
-        const uint32_t kd = at + (h * KU * 2 * 32 + lane) * 16, vd = at + V_AT + (h * VU * 4 * 32 + lane) * VB;
         if (slot >= 0) {
           const size_t row = (static_cast<size_t>(slot) << p.c.page_log2) +
                              (s * kStepKeys + h * kHalfKeys & ((1 << p.c.page_log2) - 1));
-          const uint8_t* kp = p.c.code[0] + row * D + i * D + c4 * 16;
-          const uint8_t* vp = p.c.code[1] + row * D + 2 * c4 * D + i * VB;
+          const uint8_t* kp = p.c.code[0] + row * D + lane * 16;
+          const uint8_t* vp = p.c.code[1] + row * D + lane * 16;
 #pragma unroll
-          for (int u = 0; u < KU; ++u) {
-            cp_async16(kd + 2 * u * 512, kp + u * 64);
-            cp_async16(kd + (2 * u + 1) * 512, kp + 8 * D + u * 64);
+          for (int q = 0; q < D / 32; ++q) {
+            const uint32_t dst = at + h * kHalfKeys * D + place(q);
+            cp_async16(dst, kp + q * 512);
+            cp_async16(dst + V_AT, vp + q * 512);
           }
-#pragma unroll
-          for (int u = 0; u < VU; ++u)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-              const uint8_t* src = vp + ((k & 1) + (k >> 1) * 8) * D + u * 128;
-              const uint32_t dst = vd + (u * 4 + k) * 32 * VB;
-              if constexpr (VB == 16) cp_async16(dst, src); else cp_async8(dst, src);
-            }
         } else {  // a bad page or places behind the sequence: codes of 0
 #pragma unroll 1
-          for (int u = 0; u < 2 * KU; ++u) st_shared_v4(kd + u * 512, 0, 0, 0, 0);
-#pragma unroll 1
-          for (int u = 0; u < VU * 4 * VB / 4; ++u) st_shared_b32(vd + (u / (VB / 4)) * 32 * VB + u % (VB / 4) * 4, 0);
+          for (int q = 0; q < D / 32; ++q) {
+            const uint32_t dst = at + h * kHalfKeys * D + place(q);
+            st_shared_v4(dst, 0, 0, 0, 0);
+            st_shared_v4(dst + V_AT, 0, 0, 0, 0);
+          }
         }
       }
       if ((lane >> 1) == (issued & 15))
@@ -341,8 +344,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   for (int k = 0; k < C::STAGES - 1; ++k) issue();
 
   // Compute side. Lane (i, c4) holds row c4 + 4 nt of the chunk for keys i,
-  // i + 8 of each half step, and the columns d_of(t), + 1 of its output.
-  uint32_t qf[NQ][KU * 4];             // pieces of the chunk's queries: column 2 r + piece
+  // i + 8 of each half step, and columns 16 t + 2 i, + 1 of its output.
+  uint32_t qf[NQ][D / 16];             // pieces of the chunk's queries: column 2 r + piece
   float acc[MT][NQ + 1][4];            // O^T: tile nt has pm beside ph of rows 4 nt .., the last tile every pl
   float m[NQ], l[NQ], qfac[NQ];        // reference - kShift, sum, the query's power of two
   int limit[NQ];                       // keys the row sees
@@ -369,46 +372,37 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       int qi;
       const size_t at = row_place(w, nt * 4 + (i >> 1), &qi);
       const bool live = qi < count;
-      uint4 raw[KU][2];
+      uint2 raw[MT];  // columns 16 t + 4 c4 .. + 3
       uint32_t amax = 0;
 #pragma unroll
-      for (int u = 0; u < KU; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          raw[u][e] = live ? __ldg(reinterpret_cast<const uint4*>(p.q + at * D + u * 64 + c4 * 16) + e)
-                           : make_uint4(0, 0, 0, 0);
-          const uint32_t w4[4] = {raw[u][e].x, raw[u][e].y, raw[u][e].z, raw[u][e].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
-        }
+      for (int t = 0; t < MT; ++t) {
+        raw[t] = live ? __ldg(reinterpret_cast<const uint2*>(p.q + at * D + t * 16 + c4 * 4)) : make_uint2(0, 0);
+        amax = max(amax, max(raw[t].x & 0x7fffu, (raw[t].x >> 16) & 0x7fffu));
+        amax = max(amax, max(raw[t].y & 0x7fffu, (raw[t].y >> 16) & 0x7fffu));
+      }
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // exponent of the largest value; 2^-100 and below are left as they are
       const int x = max(static_cast<int>(amax >> 7) - 127, -100);
       const float mul = exp2i(7 - x);
 #pragma unroll
-      for (int u = 0; u < KU; ++u)
+      for (int t = 0; t < MT; ++t) {
+        const uint32_t w2[2] = {raw[t].x, raw[t].y};
+        uint32_t word = 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t w4[4] = {raw[u][e].x, raw[u][e].y, raw[u][e].z, raw[u][e].w};
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float2 f = unpack_bf16x2(w4[k + y]);
-              f.x *= mul;
-              f.y *= mul;
-              // an infinity would saturate to a number
-              if (isinf(f.x)) f.x = NAN;
-              if (isinf(f.y)) f.y = NAN;
-              __half2 v = __floats2half2_rn(f.x, f.y);
-              const uint32_t hi = take_piece(v);
-              word |= (i & 1 ? last_piece(v) : hi) << (16 * y);
-            }
-            qf[nt][u * 4 + e * 2 + k / 2] = word;
-          }
+        for (int y = 0; y < 2; ++y) {
+          float2 f = unpack_bf16x2(w2[y]);
+          f.x *= mul;
+          f.y *= mul;
+          // an infinity would saturate to a number
+          if (isinf(f.x)) f.x = NAN;
+          if (isinf(f.y)) f.y = NAN;
+          __half2 v = __floats2half2_rn(f.x, f.y);
+          const uint32_t hi = take_piece(v);
+          word |= (i & 1 ? last_piece(v) : hi) << (16 * y);
         }
+        qf[nt][t] = word;
+      }
       qfac[nt] = __shfl_sync(0xffffffffu, exp2i(x - 7), 8 * c4);
       row_place(w, nt * 4 + c4, &qi);
       limit[nt] = p.causal && qi < count ? min(seg_len, seg_len - count + qi + 1) : seg_len;
@@ -433,7 +427,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   auto end_rows = [&]() {
     const bool whole = seg_first == 0 && seg_last + 1 == steps_of(seg_len);
     const int count = seq_count(p.c, where / pairs, p.Nq);
-    constexpr int PER = D == 64 ? 8 : 16;  // consecutive columns a lane holds
 #pragma unroll
     for (int nt = 0; nt < NQ; ++nt) {
       float sum = l[nt];
@@ -447,31 +440,35 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       if (whole) {
         const RowEnd end(m[nt], sum);
 #pragma unroll
-        for (int t = 0; t < MT; t += 4) {
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(end(joined(t + k, nt, 0)), end(joined(t + k, nt, 1)));
-          *reinterpret_cast<uint4*>(p.o + at * D + (t / 8) * 128 + i * PER + 2 * (t & 7)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        for (int t = 0; t < MT; ++t)
+          *reinterpret_cast<uint32_t*>(p.o + at * D + t * 16 + 2 * i) =
+              pack_bf16x2(end(joined(t, nt, 0)), end(joined(t, nt, 1)));
         if (i == 0) p.lse[at] = end.lse;
       } else {
         const size_t slot = (static_cast<size_t>(gid) * 2 + (seg_index > 0)) * p.part_rows + r;
 #pragma unroll
-        for (int t = 0; t < MT; t += 2)
-          *reinterpret_cast<float4*>(p.part + slot * D + (t / 8) * 128 + i * PER + 2 * (t & 7)) =
-              make_float4(joined(t, nt, 0), joined(t, nt, 1), joined(t + 1, nt, 0), joined(t + 1, nt, 1));
+        for (int t = 0; t < MT; ++t)
+          *reinterpret_cast<float2*>(p.part + slot * D + t * 16 + 2 * i) =
+              make_float2(joined(t, nt, 0), joined(t, nt, 1));
         if (i == 0) p.part_ml[slot] = make_float2(m[nt], sum);
       }
     }
   };
 
+  // rows of the matrix loads: K's four are (keys 0-7, 8-15) x (block, next one), V's four groups of 8 keys
+  const int mat = lane >> 3, mrow = lane & 7;
+  const uint32_t k_row = ((mat & 1) * 8 + mrow) * D + (((mat >> 1) << 4) ^ swizzle(mrow));
+  const uint32_t v_row = (mat * 8 + mrow) * D + swizzle(mrow);
+  auto block = [](int j) -> uint32_t { return (j & 7) << 4; };  // its place in a row: XORed; every eighth: 128 bytes on
+
+  int out_stage = 0;
 #pragma unroll 1
   for (int k = 0; k < n_steps; ++k) {
     cp_async_wait<C::STAGES - 2>();
-    __syncwarp();  // the step's header is written, the last step's has been read
+    __syncwarp();  // every lane's copies of the step are there, and the last step has been read
     issue();
-    const int st = k % C::STAGES;
+    const int st = out_stage;
+    out_stage = out_stage + 1 == C::STAGES ? 0 : out_stage + 1;
     const uint32_t at = ring + st * C::STAGE;
     const uint4 head[2] = {ld_shared_v4(headers + st * C::HEADER), ld_shared_v4(headers + st * C::HEADER + 16)};
     const int s = static_cast<int>(head[0].w);
@@ -481,24 +478,51 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
     }
     seg_last = s;
 
+    // The matrix loads stand in groups ahead of the products that use them: they
+    // are ordered against the copies, so the compiler moves none of them.
+    constexpr int KG = MT < 8 ? MT / 2 : 4;  // column block pairs a group
     float sc[2][NQ][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int nt = 0; nt < NQ; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[h][nt][e] = 0.f;
 #pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        const uint4 a = ld_shared_v4(at + (((h * KU + u) * 2) * 32 + lane) * 16);
-        const uint4 b = ld_shared_v4(at + (((h * KU + u) * 2 + 1) * 32 + lane) * 16);
+    for (int j0 = 0; j0 < MT; j0 += 2 * KG) {
+      uint4 kb[KG][2];
 #pragma unroll
-        for (int nt = 0; nt < NQ; ++nt) {
-          mma_e4m3(sc[h][nt], a.x, b.x, a.y, b.y, qf[nt][u * 4], qf[nt][u * 4 + 1]);
-          mma_e4m3(sc[h][nt], a.z, b.z, a.w, b.w, qf[nt][u * 4 + 2], qf[nt][u * 4 + 3]);
-        }
-      }
+      for (int j = 0; j < KG; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          kb[j][h] = ldmatrix4(at + h * kHalfKeys * D + (j0 + 2 * j) / 8 * 128 + (k_row ^ block(j0 + 2 * j)));
+#pragma unroll
+      for (int j = 0; j < KG; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NQ; ++nt)
+            mma_e4m3(sc[h][nt], kb[j][h].x, kb[j][h].y, kb[j][h].z, kb[j][h].w, qf[nt][j0 + 2 * j],
+                     qf[nt][j0 + 2 * j + 1]);
     }
+    // What lies behind the last token may be any bytes, NaN codes among them,
+    // and 0 * NaN is not 0.
+    if ((s + 1) * kStepKeys > seg_len) {
+#pragma unroll 1
+      for (int q = 0; q < 2 * (D / 32); ++q) {
+        const int key = (q & 1) * kHalfKeys + lane / MT + (q >> 1) * (512 / D);
+        if (s * kStepKeys + key >= seg_len) st_shared_v4(at + V_AT + (q & 1) * kHalfKeys * D + place(q >> 1), 0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+    constexpr int VG = 4;  // column blocks a group
+    uint4 vb[2][VG];
+    auto load_v = [&](int j0, uint4 (&v)[VG]) {
+#pragma unroll
+      for (int j = 0; j < VG; ++j)
+        v[j] = ldmatrix4_trans(at + V_AT + (j0 + j) / 8 * 128 + (v_row ^ block(j0 + j)));
+    };
+    load_v(0, vb[0]);
 
     float t[2][NQ][2];  // u of keys i, i + 8 of each half
 #pragma unroll
@@ -562,54 +586,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       pf[NQ][h] = transpose8(small);
     }
 
-    // What lies behind the last token may be any bytes, NaN codes among them,
-    // and 0 * NaN is not 0.
-    if ((s + 1) * kStepKeys > seg_len) {
-#pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        const int key = s * kStepKeys + (q >> 2) * kHalfKeys + 2 * c4 + (q & 1) + (q >> 1 & 1) * 8;
-        if (key < seg_len) continue;
-#pragma unroll 1
-        for (int u = 0; u < VU; ++u)
-#pragma unroll 1
-          for (int w = 0; w < VB; w += 4)
-            st_shared_b32(at + V_AT + ((((q >> 2) * VU + u) * 4 + (q & 3)) * 32 + lane) * VB + w, 0);
-      }
-    }
 #pragma unroll
-    for (int u = 0; u < VU; ++u) {
-      uint32_t v[2][4][VB / 4];
+    for (int j0 = 0; j0 < MT; j0 += VG) {
+      if (j0 + VG < MT) load_v(j0 + VG, vb[(j0 / VG + 1) & 1]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < VG; ++j) {
+        // word q: keys 8 q + 2 c4, + 1 of columns 16 (j0 + j) + 2 i, + 1
+        const uint4 v = vb[(j0 / VG) & 1][j];
+        const uint32_t a0 = __byte_perm(v.x, v.y, 0x6240), a1 = __byte_perm(v.x, v.y, 0x7351);
+        const uint32_t a2 = __byte_perm(v.z, v.w, 0x6240), a3 = __byte_perm(v.z, v.w, 0x7351);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t addr = at + V_AT + (((h * VU + u) * 4 + q) * 32 + lane) * VB;
-          if constexpr (VB == 16) {
-            const uint4 x = ld_shared_v4(addr);
-            v[h][q][0] = x.x, v[h][q][1] = x.y, v[h][q][2] = x.z, v[h][q][3] = x.w;
-          } else {
-            const uint2 x = ld_shared_v2(addr);
-            v[h][q][0] = x.x, v[h][q][1] = x.y;
-          }
-        }
-#pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        uint32_t a[2][4];  // columns 4 w .. 4 w + 3, keys 2 c4, + 8, + 1, + 9 of each half
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x0 = __byte_perm(v[h][0][w], v[h][2][w], 0x5140), x1 = __byte_perm(v[h][0][w], v[h][2][w], 0x7362);
-          const uint32_t y0 = __byte_perm(v[h][1][w], v[h][3][w], 0x5140), y1 = __byte_perm(v[h][1][w], v[h][3][w], 0x7362);
-          a[h][0] = __byte_perm(x0, y0, 0x5410);
-          a[h][1] = __byte_perm(x0, y0, 0x7632);
-          a[h][2] = __byte_perm(x1, y1, 0x5410);
-          a[h][3] = __byte_perm(x1, y1, 0x7632);
-        }
-        const int q = (u * (VB / 4) + w) * 2;
-#pragma unroll
-        for (int nt = 0; nt <= NQ; ++nt) {
-          mma_e4m3(acc[q][nt], a[0][0], a[0][1], a[1][0], a[1][1], pf[nt][0], pf[nt][1]);
-          mma_e4m3(acc[q + 1][nt], a[0][2], a[0][3], a[1][2], a[1][3], pf[nt][0], pf[nt][1]);
-        }
+        for (int nt = 0; nt <= NQ; ++nt) mma_e4m3(acc[j0 + j][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
       }
     }
   }
