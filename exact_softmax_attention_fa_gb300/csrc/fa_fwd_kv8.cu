@@ -73,8 +73,8 @@ struct Cfg {
   static constexpr int WARPS = 1024 / D;       // one CTA per SM; three stages of every warp fill its shared memory
   static constexpr int STAGE = 2 * kStepKeys * D;
   static constexpr int STAGES = 3;
-  static constexpr int HEADER = 32;
-  static constexpr int WARP_BYTES = STAGES * (STAGE + HEADER);
+  static constexpr int TABLE = 2 * 32 * 16;    // two batches of half steps: what look_up and the scales gave
+  static constexpr int WARP_BYTES = STAGES * STAGE + TABLE;
   static constexpr int SMEM = WARPS * WARP_BYTES;
 };
 
@@ -252,10 +252,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   const int n_steps = static_cast<int>(first_step(total, used, gid + 1) - x0);
 
   const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
-  const uint32_t headers = ring + C::STAGES * C::STAGE;
+  const uint32_t table = ring + C::STAGES * C::STAGE;
 
-  // Issue side: lane 2 j + h looks up half h of step 16 k + j of the run, one
-  // batch ahead of the copies.
+  // Issue side: lane 2 j + h looks up half h of step 16 k + j of the run, its
+  // page one batch of 16 steps ahead of the copies, its scales with the batch's
+  // first copy; they go to the table when that step's data has come.
   Cursor cur = find_cursor(p.c, pairs, x0);
   cur.s += lane >> 1;
   cur.settle(p.c, pairs);
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
     }
   };
   Meta now{}, next{};
-  // c sk, log2 sv, 2^-kSumBias / sv of the half step; log2 sv = -inf hides a bad page's keys
-  float kf = 0.f, ev = 0.f, inv = 0.f;
+  float sk = 1.f, sv = 1.f;
+  bool fresh = false;  // the batch's scales are on their way
   look_up(next);
   // A stage holds rows of D bytes, keys then values; the 16-byte pieces of a row
   // are XORed with its key, so that eight keys' pieces of one block lie in
@@ -291,16 +292,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       const int j = 2 * (issued & 15);
       if (j == 0) {
         now = next;
-        kf = ev = inv = 0.f;
+        fresh = true;
         if (now.slot >= 0) {
-          kf = __ldg(p.c.scale[0] + now.slot) * p.scale_log2;
-          const float sv = __ldg(p.c.scale[1] + now.slot);
-          const int e = min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
-          ev = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
-          inv = exp2i(-static_cast<int>(kSumBias)) / sv;
-        } else if (now.slot == -1) {
-          ev = -INFINITY;
-          record_bad_index(p.status, WHERE_FWD_KV8);
+          sk = __ldg(p.c.scale[0] + now.slot);
+          sv = __ldg(p.c.scale[1] + now.slot);
         }
         look_up(next);
       }
@@ -331,14 +326,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
           }
         }
       }
-      if ((lane >> 1) == (issued & 15))
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(headers + st * C::HEADER + (lane & 1) * 16),
-                     "r"(__float_as_uint(kf)), "r"(__float_as_uint(ev)), "r"(__float_as_uint(inv)),
-                     "r"(lane & 1 ? now.where : now.s)
-                     : "memory");
       ++issued;
     }
     cp_async_commit();
+  };
+  // c sk, log2 sv (-inf hides a bad page's keys), 2^-kSumBias / sv, and s or where
+  auto write_table = [&]() {
+    float kf = 0.f, ev = 0.f, inv = 0.f;
+    if (now.slot >= 0) {
+      const int e = min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
+      kf = sk * p.scale_log2;
+      ev = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
+      inv = exp2i(-static_cast<int>(kSumBias)) / sv;
+    } else if (now.slot == -1) {
+      ev = -INFINITY;
+      record_bad_index(p.status, WHERE_FWD_KV8);
+    }
+    st_shared_v4(table + ((issued - 1 & 16) * 2 + lane) * 16, __float_as_uint(kf), __float_as_uint(ev),
+                 __float_as_uint(inv), lane & 1 ? now.where : now.s);
+    fresh = false;
   };
 #pragma unroll 1
   for (int k = 0; k < C::STAGES - 1; ++k) issue();
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
     for (int nt = 0; nt < NQ; ++nt) {
       int qi;
       const size_t at = row_place(w, nt * 4 + (i >> 1), &qi);
-      const bool live = qi < count;
+      const bool live = qi < p.Nq;  // rows past the count too: their loads then wait for no other
       uint2 raw[MT];  // columns 16 t + 4 c4 .. + 3
       uint32_t amax = 0;
 #pragma unroll
@@ -461,19 +467,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   const uint32_t v_row = (mat * 8 + mrow) * D + swizzle(mrow);
   auto block = [](int j) -> uint32_t { return (j & 7) << 4; };  // its place in a row: XORed; every eighth: 128 bytes on
 
+  // the first rows' queries, while the first copies are under way
+  begin_rows(__shfl_sync(0xffffffffu, now.where, 0), __shfl_sync(0xffffffffu, now.s, 0));
   int out_stage = 0;
 #pragma unroll 1
   for (int k = 0; k < n_steps; ++k) {
     cp_async_wait<C::STAGES - 2>();
+    if (fresh) write_table();
     __syncwarp();  // every lane's copies of the step are there, and the last step has been read
     issue();
     const int st = out_stage;
     out_stage = out_stage + 1 == C::STAGES ? 0 : out_stage + 1;
     const uint32_t at = ring + st * C::STAGE;
-    const uint4 head[2] = {ld_shared_v4(headers + st * C::HEADER), ld_shared_v4(headers + st * C::HEADER + 16)};
+    const uint32_t entry = table + (k & 31) * 32;
+    const uint4 head[2] = {ld_shared_v4(entry), ld_shared_v4(entry + 16)};
     const int s = static_cast<int>(head[0].w);
     if (static_cast<int>(head[1].w) != where) {
-      if (where >= 0) end_rows();
+      end_rows();
       begin_rows(static_cast<int>(head[1].w), s);
     }
     seg_last = s;
@@ -600,7 +610,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       }
     }
   }
-  if (where >= 0) end_rows();
+  end_rows();
   cp_async_wait<0>();
 }
 
@@ -611,58 +621,58 @@ template <int D>
 __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant__ Kv8Attn p, int warps, int per_chunk) {
   constexpr int LANES = D / 4, GROUPS = 128 / LANES;
   __shared__ float4 red[128];
-  __shared__ float red_l[GROUPS];
+  __shared__ float2 red_ml[GROUPS];
   const int row = blockIdx.x % p.rows;
   const int bh = blockIdx.x / p.rows, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
   const int qi = row / p.g;
-  griddep_wait();  // launched to overlap the kernel that writes the parts
+  // Lengths and counts are inputs of the kernel this one overlaps, so they can
+  // be read before its parts are there.
   const bool bad_len = seq_len(p.c, b) != __ldg(p.c.lens + b);
   const bool bad_count = p.c.counts && seq_count(p.c, b, p.Nq) != __ldg(p.c.counts + b);
-  if ((bad_len || bad_count) && threadIdx.x == 0) record_bad_index(p.status, WHERE_FWD_KV8);
-  if (bad_len || bad_count || qi >= seq_count(p.c, b, p.Nq)) return;
   const int pairs = p.c.Hkv * p.chunks, steps = seq_steps(p.c, b);
   const size_t at = (static_cast<size_t>(b) * p.Hq + h * p.g + row % p.g) * p.Nq + qi;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const bool live = !bad_len && !bad_count && qi < seq_count(p.c, b, p.Nq);
+  long long total, before;
+  step_totals(p.c, pairs, b, &total, &before);
+  const int used = max(1, used_warps(total, warps));
+  const int chunk = row / per_chunk, r = row - chunk * per_chunk;
+  const long long s0 = before + static_cast<long long>(h * p.chunks + chunk) * steps, s1 = s0 + steps - 1;
+  griddep_wait();
+  if ((bad_len || bad_count) && threadIdx.x == 0) record_bad_index(p.status, WHERE_FWD_KV8);
+  if (!live) return;
   if (steps == 0) {
     if (group == 0) *reinterpret_cast<uint2*>(p.o + at * D + lane * 4) = make_uint2(0, 0);
     if (threadIdx.x == 0) p.lse[at] = -INFINITY;
     return;
   }
-  long long total, before;
-  step_totals(p.c, pairs, b, &total, &before);
-  const int used = used_warps(total, warps);
-  const int chunk = row / per_chunk, r = row - chunk * per_chunk;
-  const long long s0 = before + static_cast<long long>(h * p.chunks + chunk) * steps, s1 = s0 + steps - 1;
   // the warp that holds step x: the largest w with first_step(w) <= x
   const int w0 = static_cast<int>(((s0 + 1) * used - 1) / total), w1 = static_cast<int>(((s1 + 1) * used - 1) / total);
   if (w0 == w1) return;
-  auto slot = [&](int w) {
-    return (static_cast<size_t>(w) * 2 + (w == w0 && s0 > first_step(total, used, w) ? 1 : 0)) * p.part_rows + r;
-  };
-  float m = -INFINITY;
-  for (int w = w0 + (threadIdx.x & 31); w <= w1; w += 32) m = fmaxf(m, p.part_ml[slot(w)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
+  // Each group of threads joins every GROUPS-th part as it comes, then the
+  // groups are joined in order.
+  const int late = s0 > first_step(total, used, w0) ? 1 : 0;  // the row's first part is its warp's last
+  float m = -INFINITY, l = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  auto join = [&](float mx, float lx, const float4& x) {
+    const float to = fmaxf(m, mx);
+    const float ref = to == -INFINITY ? 0.f : to;
+    const float wa = ex2_approx(m - ref), wx = ex2_approx(mx - ref);
+    m = to;
+    l = l * wa + lx * wx;
+    a.x = a.x * wa + x.x * wx, a.y = a.y * wa + x.y * wx, a.z = a.z * wa + x.z * wx, a.w = a.w * wa + x.w * wx;
+  };
+#pragma unroll 4
   for (int w = w0 + group; w <= w1; w += GROUPS) {
-    const size_t sl = slot(w);
-    const float2 ml = p.part_ml[sl];
-    const float wt = ex2_approx(ml.x - ref);
-    const float4 x = *reinterpret_cast<const float4*>(p.part + sl * D + lane * 4);
-    l = fmaf(wt, ml.y, l);
-    a.x = fmaf(wt, x.x, a.x), a.y = fmaf(wt, x.y, a.y), a.z = fmaf(wt, x.z, a.z), a.w = fmaf(wt, x.w, a.w);
+    const size_t slot = (static_cast<size_t>(w) * 2 + (w == w0 ? late : 0)) * p.part_rows + r;
+    const float2 ml = p.part_ml[slot];
+    join(ml.x, ml.y, *reinterpret_cast<const float4*>(p.part + slot * D + lane * 4));
   }
   red[threadIdx.x] = a;
-  if (lane == 0) red_l[group] = l;
+  if (lane == 0) red_ml[group] = make_float2(m, l);
   __syncthreads();
   if (group > 0) return;
-  for (int u = 1; u < GROUPS; ++u) {
-    const float4 x = red[u * LANES + lane];
-    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-    l += red_l[u];
-  }
+  for (int u = 1; u < GROUPS; ++u) join(red_ml[u].x, red_ml[u].y, red[u * LANES + lane]);
   const RowEnd end(m, l);
   *reinterpret_cast<uint2*>(p.o + at * D + lane * 4) =
       make_uint2(pack_bf16x2(end(a.x), end(a.y)), pack_bf16x2(end(a.z), end(a.w)));

@@ -452,7 +452,7 @@ fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float*
  *   position lens[b] - counts[b] + i. With causal = 1 it sees keys
  *   j <= its position, else all lens[b]. A query that sees no key (lens[b] = 0,
  *   or a position below 0) gets O = 0, L = -infinity. Rows past counts[b] are
- *   neither read nor written. What a page holds behind lens[b] is never
+ *   not written, and what they hold is of no effect. What a page holds behind lens[b] is never
  *   used. A NaN code reaches every query that sees its token; one stored in V
  *   may also reach the queries of this call that stand before it.
  *   scales : positive, at most 2^126 (fa_kv8_append's are powers of two up to 2^120)
