@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "fa_internal.h"
+#include "fa_kv8_attn.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -261,6 +262,18 @@ int choose_kv_chunks(long long BHkv, int g, int N, int d, int causal, int sms, s
 }
 
 }  // namespace
+
+bool make_cache_map(CUtensorMap* m, const void* base, int d, int page, long long slots) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(slots)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page) * d};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(std::min(d, 128)), static_cast<cuuint32_t>(page), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 fa_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return FA_OK;

@@ -37,7 +37,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "fa_kv8.cuh"
+#include "fa_kv8_attn.cuh"
 
 namespace fa {
 namespace {
@@ -45,26 +45,13 @@ namespace {
 constexpr int kStepKeys = 32;
 constexpr int kHalfKeys = 16;     // a page ends at a multiple of this
 constexpr int kMinSteps = 2;      // a warp's share is not cut below this
-constexpr int kMaxSms = 152;      // sizes the partials
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kSlack = 2.8f;    // growth of a reference (base 2) absorbed without rescaling
-constexpr float kShift = 6.f;     // P <= 2^(kShift + kSlack) < 448, the largest e4m3 value
-// l is kept times 2^-10: its terms lie between 2^(6 - 120 - 10) and
-// 2^(9 + 100 - 10) for the scales a cache holds, so neither one term nor 2^24
-// of them leave fp32's normal range.
-constexpr float kSumBias = 10.f;
+constexpr float kSlack = 2.8f;    // growth of a reference (base 2) absorbed: P <= 2^(kShift + kSlack) < 448
 
-struct Kv8Attn {
-  Kv8Cache c;
-  const __nv_bfloat16* q;  // [B][Hq][Nq][d]
-  __nv_bfloat16* o;
-  float* lse;              // [B][Hq][Nq]
-  float* part;             // [2 * warps][part_rows][d] unnormalised O of a run's part of a row
-  float2* part_ml;         // [2 * warps][part_rows] its m and l
+struct Kv8Attn : Kv8Call {
+  float* part;     // [2 * warps][part_rows][d] unnormalised O of a run's part of a row
+  float2* part_ml; // [2 * warps][part_rows] its m and l
   uint32_t* status;
-  int Hq, Nq, g, rows, chunks, part_rows;  // rows = g * Nq per K/V head, in `chunks` of 4 NQ
-  int causal;
-  float scale_log2;
+  int rows, chunks, part_rows;  // rows = g * Nq per K/V head, in `chunks` of 4 NQ
 };
 
 // NQ: 8-column tiles of queries, 4 rows of two pieces each.
@@ -78,24 +65,10 @@ struct Cfg {
   static constexpr int SMEM = WARPS * WARP_BYTES;
 };
 
-// Tokens of sequence b, or 0 where the stored length is out of range.
-__device__ __forceinline__ int seq_len(const Kv8Cache& c, int b) {
-  const int len = __ldg(c.lens + b);
-  return len < 0 || len > (static_cast<long long>(c.max_pages) << c.page_log2) ? 0 : len;
-}
-__device__ __forceinline__ int seq_count(const Kv8Cache& c, int b, int n) {
-  const int count = c.counts ? __ldg(c.counts + b) : n;
-  return count < 0 || count > n ? 0 : count;
-}
 __device__ __forceinline__ int steps_of(int len) { return (len + kStepKeys - 1) / kStepKeys; }
 __device__ __forceinline__ int seq_steps(const Kv8Cache& c, int b) { return steps_of(seq_len(c, b)); }
 
-// Every lane: the steps of sequences [0, B) summed, and of those before `b`.
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+// Every lane: the steps of all sequences summed, and of those before `b`.
 __device__ __forceinline__ void step_totals(const Kv8Cache& c, int pairs, int b, long long* total, long long* before) {
   long long t = 0, u = 0;
   for (int i = threadIdx.x & 31; i < c.B; i += 32) {
@@ -210,26 +183,6 @@ __device__ __forceinline__ uint32_t take_piece(__half2& v) {
 __device__ __forceinline__ uint32_t last_piece(const __half2& v) {
   return f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
 }
-__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
-
-// x / (l 2^kSumBias) and ln of the row's sum, for sums near either end of
-// fp32's range; a row that saw no key has l = 0: O = 0, L = -inf.
-struct RowEnd {
-  float a, b, lse;
-  __device__ __forceinline__ RowEnd(float m, float l) {
-    const int e = static_cast<int>(__float_as_uint(l) >> 23 & 255) - 127;  // l >= 0
-    a = l == 0.f ? 0.f : 1.f;
-    b = 1.f;
-    if (l != 0.f && e < 127) {  // not infinite, not NaN
-      b = exp2i(-e);
-      a = exp2i(-static_cast<int>(kSumBias)) / (l * b);
-    } else if (l != 0.f) {
-      a = 1.f / l;
-    }
-    lse = l == 0.f ? -INFINITY : (m + kSumBias + log2f(l)) * kLn2;
-  }
-  __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
-};
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(const __grid_constant__ Kv8Attn p) {
@@ -679,6 +632,10 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   if (lane == 0) p.lse[at] = end.lse;
 }
 
+// More query rows per K/V head than this take the 128-row tiles of
+// fa_fwd_kv8_tile.cu.
+constexpr int kTileRows = 16;
+
 // 8-column tiles of a row chunk: two (8 rows) where the rows fill more than one
 // and the sums of both fit the registers.
 int query_tiles(int d, long long rows) { return d <= 128 && rows > 4 ? 2 : 1; }
@@ -726,8 +683,9 @@ extern "C" {
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || Hq % Hkv != 0) return 0;
   if (d != 64 && d != 128 && d != 256) return 0;
+  const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
   size_t off;
-  return part_bytes(d, static_cast<long long>(Hq / Hkv) * Nq, &off);
+  return rows > kTileRows ? kv8_tile_workspace(d) : part_bytes(d, rows, &off);
 }
 
 fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -757,19 +715,20 @@ fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, 
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.status = dev.status;
   a.Hq = Hq;
   a.Nq = Nq;
   a.g = Hq / Hkv;
+  a.causal = causal;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   a.rows = a.g * Nq;
+  if (a.rows > kTileRows) return launch_kv8_tiles(a, d, workspace, dev, stream);
+  a.status = dev.status;
   const int nq = query_tiles(d, a.rows);
   a.chunks = (a.rows + 4 * nq - 1) / (4 * nq);
   a.part_rows = std::min(a.rows, 4 * nq);
   part_bytes(d, a.rows, &ml_off);
   a.part = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ml_off);
-  a.causal = causal;
-  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   if (d == 64) return from_cuda(nq == 1 ? launch_t<64, 1>(a, dev, stream) : launch_t<64, 2>(a, dev, stream));
   if (d == 128) return from_cuda(nq == 1 ? launch_t<128, 1>(a, dev, stream) : launch_t<128, 2>(a, dev, stream));
   return from_cuda(launch_t<256, 1>(a, dev, stream));

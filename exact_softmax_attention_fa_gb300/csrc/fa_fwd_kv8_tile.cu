@@ -1,0 +1,923 @@
+// Attention over the paged 8-bit cache for many query rows per K/V head: chunks
+// of a prompt, on tcgen05 (fa_fwd_kv8.cu has the mathematics and the kernel for
+// few rows).
+//
+// A CTA owns NT tiles of 128 query rows (rows of a K/V head's group, position by
+// position) and streams 128-key tiles of the cache past them, as the dense
+// forward does; what differs is how the codes reach the tensor core:
+//   S = Q K^T  : kind::f8f6f4. K's codes are the operand as TMA brings them. A
+//       query row, moved by a power of two so that its largest |value| lies in
+//       [2^7, 2^8), is the sum of two e4m3 pieces qh + ql, accumulated into the
+//       same S: exact for values down to 2^-10 of the row's largest, within
+//       2^-18 of it below. Two e4m3 products cost what one fp16 product would,
+//       and K needs no conversion and half the shared memory.
+//   O += P V   : kind::f16. A weight keeps fp16's 2^-11 and range (small weights
+//       of a long row together matter, and e4m3 pieces end at 2^-18 of the
+//       largest), so V's codes, exact in fp16, are converted by a warpgroup
+//       of their own from a staging ring into the swizzled operand tile.
+// Key and value scales enter as in fa_fwd_kv8.cu: u = c sk (q . k8) + log2 sv per
+// 16-key group, P = 2^(u - m), l = sum P / sv.
+//
+// Roles: warpgroups 0 and 1 softmax, correction and epilogue of one query tile
+// each (and its Q pieces), warpgroup 2 converts V, warp 12 looks up pages and
+// loads, one thread of warp 13 issues MMAs. Registers are moved to the softmax
+// warpgroups (setmaxnreg).
+//
+// Bound: tensor cores, and the softmax's exponentials behind them. Work: every
+// CTA takes an equal run of the flattened list of (sequence, K/V head, row
+// tiles, key tile); a row block that CTAs share is joined by
+// kv8_tile_combine_kernel. So neither ragged lengths nor few row blocks against
+// long caches leave SMs idle.
+#include <algorithm>
+#include <cmath>
+
+#include "fa_kv8.cuh"
+#include "fa_kv8_attn.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kConvThreads = 128;
+constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kScaleSlots = 8;  // tiles whose scales are kept; more than are in flight
+constexpr int kMinTiles = 2;    // a CTA's run is not cut below this
+constexpr float kSlack = 8.f;   // P <= 2^(kShift + kSlack) = 2^14, fp16
+// Registers a thread after the split: 256 x 184 + 128 x 88 + 128 x 56 = 512 x 128.
+constexpr int kRegsSoftmax = 184, kRegsConv = 88, kRegsIssue = 56;
+
+template <int D>
+struct TileCfg {
+  static constexpr int NT = D <= 128 ? 2 : 1;
+  static constexpr int ROWS = NT * 128;
+  static constexpr int Q_BYTES = 2 * 128 * D;     // two pieces of a query tile
+  static constexpr int K_BYTES = 128 * D;         // codes of a key tile
+  static constexpr int V_BYTES = 2 * 128 * D;     // fp16 values
+  static constexpr int KST = D == 64 ? 4 : (D == 128 ? 3 : 2);
+  static constexpr int VST = D == 64 ? 3 : (D == 128 ? 2 : 1);
+  static constexpr int SST = D == 64 ? 4 : (D == 128 ? 2 : 1);  // staged value codes
+  static constexpr bool P_ALIAS = D == 128;
+  __host__ __device__ static constexpr uint32_t s_col(int t) { return D == 256 ? 0u : uint32_t(t) * 128u; }
+  __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + uint32_t(t) * D; }
+  __host__ __device__ static constexpr uint32_t p_col(int t) {
+    return D == 64 ? 384u + uint32_t(t) * 64u : (D == 128 ? uint32_t(t) * 128u : 128u);
+  }
+  static constexpr int SMEM = NT * Q_BYTES + KST * K_BYTES + VST * V_BYTES + SST * K_BYTES + 1024;
+};
+
+struct TileLaunch : Kv8Call {
+  CUtensorMap tmK;         // the key codes: {d, page, pages * Hkv}
+  float* part;             // [2 * CTAs][ROWS][d]
+  float2* part_ml;         // [2 * CTAs][ROWS]
+  int4* run;               // [CTAs]: where each CTA's run starts (b, h, block, tile)
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct TileShared {
+  uint64_t q_full[2], q_taken[2];
+  uint64_t k_full[4], k_empty[4], st_full[4], st_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t scale_full[kScaleSlots];
+  uint64_t mma_drain;
+  float4 scale[kScaleSlots][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
+  int4 start;
+  int n_tiles;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Row blocks of sequence b, and the key tiles that rows < `rows` of it see.
+__device__ __forceinline__ int tiles_seen(int len, int count, int rows, int g, int causal) {
+  const int last = (rows - 1) / g;  // position of the last row among the new tokens
+  const int keys = causal ? min(len, max(0, len - count + last + 1)) : len;
+  return (keys + 127) / 128;
+}
+
+// A row block, and the part of a run that lies in it.
+template <int D>
+struct Walk {
+  static constexpr int ROWS = TileCfg<D>::ROWS;
+  int b, h, blk, s;           // s: the first key tile of the run in this block
+  int len, count, blocks;     // of sequence b
+  int tiles;                  // key tiles of the block
+  __device__ __forceinline__ void load(const TileLaunch& p) {
+    const bool in = b < p.c.B;
+    len = in ? seq_len(p.c, b) : 0;
+    count = in ? seq_count(p.c, b, p.Nq) : 0;
+    blocks = (count * p.g + ROWS - 1) / ROWS;
+  }
+  __device__ __forceinline__ int tiles_of(const TileLaunch& p, int block) const {
+    return tiles_seen(len, count, min(count * p.g, (block + 1) * ROWS), p.g, p.causal);
+  }
+  __device__ __forceinline__ void settle(const TileLaunch& p) {  // after s moved on
+    while (b < p.c.B && s >= tiles) {
+      s -= tiles;
+      if (++blk >= blocks) {
+        blk = 0;
+        if (blocks == 0 || ++h >= p.c.Hkv) {
+          h = 0;
+          ++b;
+          load(p);
+        }
+      }
+      tiles = blk < blocks ? tiles_of(p, blk) : 0;
+    }
+  }
+  __device__ __forceinline__ void begin(const TileLaunch& p, const int4& at) {
+    b = at.x, h = at.y, blk = at.z, s = at.w;
+    load(p);
+    tiles = blk < blocks ? tiles_of(p, blk) : 0;
+  }
+  // Key tiles (relative to s) that tile t of the block sees within n tiles of the run: the last one's index.
+  __device__ __forceinline__ int last_tile(const TileLaunch& p, int t, int n) const {
+    const int r0 = blk * ROWS + t * 128, live = min(count * p.g - r0, 128);
+    if (live <= 0) return -1;
+    return min(tiles_seen(len, count, r0 + live, p.g, p.causal), s + n) - 1 - s;
+  }
+};
+
+// All lanes of one warp: the tiles of every block summed, and the block that
+// holds tile number x of them (x < 0: the total alone).
+template <int D>
+__device__ long long tile_search(const TileLaunch& p, long long x, int4* at) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0;
+  Walk<D> w;
+  for (int b = 0; b < p.c.B; ++b) {
+    w.b = b;
+    w.load(p);
+    long long one = 0;  // tiles of the sequence's blocks for one K/V head
+    for (int blk = lane; blk < w.blocks; blk += 32) one += w.tiles_of(p, blk);
+    one = warp_sum(one);
+    const long long here = one * p.c.Hkv;
+    if (x >= 0 && x < total + here) {
+      long long rem = x - total;
+      const int h = static_cast<int>(rem / one);
+      rem -= h * one;
+      for (int b0 = 0;; b0 += 32) {  // the block within the head
+        const int blk = b0 + lane;
+        int incl = blk < w.blocks ? w.tiles_of(p, blk) : 0;
+        const int own = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, incl > rem);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          const int before = __shfl_sync(0xffffffffu, incl - own, l);
+          *at = make_int4(b, h, b0 + l, static_cast<int>(rem) - before);
+          return x;
+        }
+        rem -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    total += here;
+  }
+  return total;
+}
+
+// CTAs that share `total` tiles, and the first tile of CTA c of them.
+__device__ __forceinline__ int used_ctas(long long total, int ctas) {
+  const long long most = (total + kMinTiles - 1) / kMinTiles;
+  return most < ctas ? static_cast<int>(most) : ctas;
+}
+__device__ __forceinline__ long long first_tile(long long total, int used, int c) { return total * c / used; }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, fp32 sums
+__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptors (fields as in make_idesc_bf16_f32): e4m3 x e4m3 and
+// fp16 x fp16, whose format fields are both 0.
+__host__ __device__ constexpr uint32_t make_idesc_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
+         ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+// Descriptor of a K-major tile with rows of 64 bytes, 64-byte swizzle (8-row atoms of 512 bytes).
+__device__ __forceinline__ uint64_t make_smem_desc_sw64(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= 1ull << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 4ull << 61;
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---------------------------------------------------------------------------
+// Pages, scales and loads (one warp)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void load_role(const TileLaunch& p, TileShared& sh, uint8_t* sK, uint8_t* sStage) {
+  using C = TileCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t lim = p.wait_limit_ns;
+  constexpr int ROW_BYTES = D < 128 ? D : 128;  // a key's codes in one column chunk of the operand tile
+  const int page = 1 << p.c.page_log2, pages = 128 >> p.c.page_log2;
+  const int n = sh.n_tiles;
+  if (lane == 0) tma_prefetch_desc(&p.tmK);
+  // Lane 8 j + g looks up 16-key group g of tile 4 k + j, one batch of 4 tiles ahead.
+  Walk<D> cur;
+  cur.begin(p, sh.start);
+  cur.s += lane >> 3;
+  cur.settle(p);
+  auto look_up = [&]() -> int {  // page * Hkv + head; -1: a bad page, -2: behind the sequence
+    int slot = -2;
+    if (cur.b < p.c.B) {
+      const int key = cur.s * 128 + (lane & 7) * 16;
+      if (key < cur.len) {
+        const int pid = __ldg(p.c.table + static_cast<size_t>(cur.b) * p.c.max_pages + (key >> p.c.page_log2));
+        slot = pid < 0 || pid >= p.c.num_pages ? -1 : pid * p.c.Hkv + cur.h;
+      }
+      cur.s += 4;
+      cur.settle(p);
+    }
+    return slot;
+  };
+  int next = look_up(), now = -2;
+  float4 entry = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool ok = true;
+  int k_issued = 0, st_issued = 0;
+  for (int i = 0; i < n; ++i) {
+    const int j0 = (i & 3) * 8;
+    if (j0 == 0) {
+      now = next;
+      entry = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (now >= 0) {
+        const float sk = __ldg(p.c.scale[0] + now), sv = __ldg(p.c.scale[1] + now);
+        const int e = min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
+        entry = make_float4(sk * p.scale_log2, static_cast<float>(e) + log2f(sv * exp2i(-e)),
+                            exp2i(-static_cast<int>(kSumBias)) / sv, 1.f);
+      } else if (now == -1) {
+        entry.y = -INFINITY;  // its keys are not seen
+        record_bad_index(p.status, WHERE_FWD_KV8);
+      }
+      next = look_up();
+    }
+    const int ks = i % C::KST;
+    if (i >= C::KST) ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], ((i / C::KST) - 1) & 1, &sh.abort_flag, lim));
+    if (!ok) break;
+    const int slot8 = i % kScaleSlots;
+    if (lane >= j0 && lane < j0 + 8) {
+      sh.scale[slot8][lane - j0] = entry;
+      mbar_arrive(&sh.scale_full[slot8]);
+    }
+    // lane p < pages: page p of the tile
+    const int slot = __shfl_sync(0xffffffffu, now, j0 + (lane * page / 16 & 7));
+    const bool live = lane < pages && slot >= 0;
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * page * D;
+    uint8_t* kd = sK + ks * C::K_BYTES;
+    // S of a bad page's keys has to be a number
+    for (unsigned bad = __ballot_sync(0xffffffffu, lane < pages && slot == -1); bad; bad &= bad - 1) {
+      const int first = (__ffs(bad) - 1) * page * ROW_BYTES;
+      for (int c = 0; c < D / ROW_BYTES; ++c)
+        for (int u = lane * 16; u < page * ROW_BYTES; u += 512)
+          st_shared_v4(smem_u32(kd) + c * (128 * 128) + first + u, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[ks], bytes);
+    __syncwarp();
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < D / ROW_BYTES; ++c)
+        tma_load_3d(kd + c * (128 * 128) + lane * page * ROW_BYTES, &p.tmK, &sh.k_full[ks], c * 128, 0, slot);
+    }
+    ++k_issued;
+    const int ss = i % C::SST;
+    if (i >= C::SST) ok = __all_sync(0xffffffffu, mbar_wait(&sh.st_empty[ss], ((i / C::SST) - 1) & 1, &sh.abort_flag, lim));
+    if (!ok) break;
+    if (lane == 0) mbar_arrive_expect_tx(&sh.st_full[ss], bytes);
+    __syncwarp();
+    if (live)
+      bulk_load(sStage + ss * C::K_BYTES + lane * page * D, p.c.code[1] + (static_cast<size_t>(slot) << p.c.page_log2) * D,
+                page * D, &sh.st_full[ss]);
+    ++st_issued;
+  }
+  if (!ok && lane == 0) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_LOAD);
+  __syncwarp();
+  // the copies already issued land before the CTA can exit
+  if (lane == 0) {
+    for (int i = max(0, k_issued - C::KST); i < k_issued; ++i) drain_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, lim);
+    for (int i = max(0, st_issued - C::SST); i < st_issued; ++i)
+      drain_wait(&sh.st_full[i % C::SST], (i / C::SST) & 1, lim);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Value codes -> fp16 operand tiles (one warpgroup)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void convert_role(const TileLaunch& p, TileShared& sh, uint8_t* sStage, uint8_t* sV) {
+  using C = TileCfg<D>;
+  constexpr int UNITS = D / 8;                     // 8 codes (16 bytes of fp16) each
+  constexpr int PASSES = 128 * UNITS / kConvThreads;
+  constexpr int PASS_ROWS = kConvThreads / UNITS;
+  const int tid = threadIdx.x & 127;
+  const int unit = tid % UNITS, row0 = tid / UNITS;
+  const uint64_t lim = p.wait_limit_ns;
+  const int n = sh.n_tiles;
+  Walk<D> w;
+  w.begin(p, sh.start);
+  bool ok = true;
+  for (int i = 0; i < n && ok; ++i) {
+    if (i > 0) {
+      ++w.s;
+      w.settle(p);
+    }
+    const int ss = i % C::SST, vs = i % C::VST, sl = i % kScaleSlots;
+    ok = mbar_wait(&sh.scale_full[sl], (i / kScaleSlots) & 1, &sh.abort_flag, lim) &&
+         mbar_wait(&sh.st_full[ss], (i / C::SST) & 1, &sh.abort_flag, lim) &&
+         (i < C::VST || mbar_wait(&sh.v_empty[vs], ((i / C::VST) - 1) & 1, &sh.abort_flag, lim));
+    if (!ok) break;
+    // Keys behind the sequence and on bad pages: 0 (what lies there may be NaN codes, and 0 * NaN is not 0).
+    const int rows = w.len - w.s * 128;
+    uint32_t seen = 0;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) seen |= (sh.scale[sl][g].w != 0.f ? 1u : 0u) << g;
+    const uint8_t* src = sStage + ss * C::K_BYTES + row0 * D + unit * 8;
+    const uint32_t dst = smem_u32(sV + vs * C::V_BYTES) + (unit / 8) * (128 * 128);
+#pragma unroll 8
+    for (int q = 0; q < PASSES; ++q) {
+      const int row = row0 + q * PASS_ROWS;
+      uint2 v = *reinterpret_cast<const uint2*>(src + q * PASS_ROWS * D);
+      if (row >= rows || !(seen >> (row >> 4) & 1)) v = make_uint2(0, 0);
+      st_shared_v4(dst + sw128_offset(row, unit & 7), e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
+                   e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
+    }
+    mbar_arrive(&sh.st_empty[ss]);
+    fence_proxy_async_smem();
+    mbar_arrive(&sh.v_full[vs]);
+  }
+  if (!ok) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_CONVERT);
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuer (one thread)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
+  using C = TileCfg<D>;
+  constexpr uint32_t kIdescS = make_idesc_f32(128, 128, false);
+  constexpr uint32_t kIdescPV = make_idesc_f32(128, D, true);
+  const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
+  const uint64_t lim = p.wait_limit_ns;
+  int left = sh.n_tiles;
+  auto issue_s = [&](int t, int i) {
+    const uint64_t qd = make_smem_desc_sw128(q_addr + t * C::Q_BYTES, 16, 1024);
+    const uint32_t ka = k_addr + (i % C::KST) * C::K_BYTES;
+    const uint64_t kd = D == 64 ? make_smem_desc_sw64(ka) : make_smem_desc_sw128(ka, 16, 1024);
+#pragma unroll
+    for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) {
+        // a row of Q holds 128 bytes per chunk: both pieces (d = 64), or a piece's 128 columns
+        const int qs = piece * (D / 32) + ks;
+        const uint32_t qoff = (qs >> 2) * (128 * 128) + (qs & 3) * 32, koff = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+        umma_ss_f8(tmem + C::s_col(t), desc_add(qd, qoff), desc_add(kd, koff), kIdescS, qs > 0 ? 1u : 0u);
+      }
+    umma_commit(&sh.s_full[t]);
+  };
+  auto issue_pv = [&](int t, int i, bool first) {
+    const uint64_t vd = make_smem_desc_sw128(v_addr + (i % C::VST) * C::V_BYTES, 128 * 128, 1024);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
+              (!first || ks > 0) ? 1u : 0u);
+    umma_commit(&sh.pv_done[t]);
+  };
+  auto fail = [&]() {
+    record_timeout(p.status, &sh.abort_flag, WHERE_KV8_MMA);
+    drain_mmas(&sh.mma_drain, lim);
+  };
+  Walk<D> w;
+  w.begin(p, sh.start);
+  int i = 0;            // running tile
+  int cnt[2] = {0, 0};  // running S / P / PV count per query tile
+  for (int seg = 0; left > 0; ++seg) {
+    const int n = min(left, w.tiles - w.s);
+    int last[2] = {-1, -1};
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      last[t] = w.last_tile(p, t, n);
+      if (!mbar_wait(&sh.q_full[t], seg & 1, &sh.abort_flag, lim)) return fail();
+      mbar_arrive(&sh.q_taken[t]);
+    }
+    if (!mbar_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, &sh.abort_flag, lim)) return fail();
+    tc_fence_after_sync();
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      if (last[t] < 0) continue;
+      // S_t(0) overwrites S_t / P_t of the segment before: its last PV must be done
+      if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim)) return fail();
+      tc_fence_after_sync();
+      issue_s(t, i);
+    }
+    umma_commit(&sh.k_empty[i % C::KST]);
+    for (int j = 0; j < n; ++j, ++i) {
+      const int vs = i % C::VST;
+      if (!mbar_wait(&sh.v_full[vs], (i / C::VST) & 1, &sh.abort_flag, lim)) return fail();
+      const bool more = j + 1 < n;
+      if (more) {
+        if (!mbar_wait(&sh.k_full[(i + 1) % C::KST], ((i + 1) / C::KST) & 1, &sh.abort_flag, lim)) return fail();
+      }
+      tc_fence_after_sync();
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) {
+        if (j > last[t]) continue;
+        if (!mbar_wait(&sh.p_full[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+        // PV_t(0) overwrites O_t: the segment before has to have read it
+        if (j == 0 && seg > 0 && !mbar_wait(&sh.o_free[t], (seg - 1) & 1, &sh.abort_flag, lim)) return fail();
+        tc_fence_after_sync();
+        issue_pv(t, i, j == 0);
+        if (j + 1 <= last[t]) {
+          // d = 128: S_t(j + 1) overwrites the columns P_t(j) is read from
+          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+          tc_fence_after_sync();
+          issue_s(t, i + 1);
+        }
+      }
+      if (more) umma_commit(&sh.k_empty[(i + 1) % C::KST]);
+      umma_commit(&sh.v_empty[vs]);
+    }
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t)
+      if (last[t] >= 0) cnt[t] += last[t] + 1;
+    left -= n;
+    w.s += n;
+    w.settle(p);
+  }
+  drain_mmas(&sh.mma_drain, lim);
+}
+
+// ---------------------------------------------------------------------------
+// Q pieces, softmax, correction and epilogue (warpgroup t owns query tile t)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint32_t tmem, int t) {
+  using C = TileCfg<D>;
+  const int r = threadIdx.x & 127;
+  const uint32_t lane_base = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
+  const uint32_t tS = tmem + lane_base + C::s_col(t);
+  const uint32_t tP = tmem + lane_base + C::p_col(t);
+  const uint32_t tO = tmem + lane_base + C::o_col(t);
+  const uint32_t q_dst = smem_u32(sQ + t * C::Q_BYTES);
+  const uint64_t lim = p.wait_limit_ns;
+  Walk<D> w;
+  w.begin(p, sh.start);
+  int left = sh.n_tiles, i0 = 0, cnt = 0;
+  // After a timed-out wait a warp stops working but keeps arriving, so barrier counts stay matched.
+  bool alive = true;
+  for (int seg = 0; left > 0; ++seg) {
+    const int n = min(left, w.tiles - w.s);
+    const int last = w.last_tile(p, t, n);
+    const int row = w.blk * C::ROWS + t * 128 + r;
+    const int qi = row / p.g;
+    const bool live = qi < w.count;
+    const size_t at = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row % p.g) * p.Nq + qi;
+    const int limit = p.causal ? min(w.len, w.len - w.count + qi + 1) : w.len;  // keys the row sees
+    // The MMA thread has taken note of the segment before (else an idle tile's
+    // warpgroup could run two arrivals ahead of its parity wait).
+    if (alive && seg > 0) {
+      alive = __all_sync(0xffffffffu, mbar_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim));
+      if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
+    }
+    float qfac = 0.f;
+    if (alive && last >= 0) {
+      // The row's Q pieces; S of the segment before is complete, so its tile is free.
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * D);
+      uint32_t amax = 0;
+#pragma unroll 4
+      for (int u = 0; u < D / 8; ++u) {
+        const uint4 v = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+      }
+      const int x = max(static_cast<int>(amax >> 7) - 127, -100);
+      const float mul = exp2i(7 - x);
+      qfac = exp2i(x - 7);
+#pragma unroll 1
+      for (int u = 0; u < D / 16; ++u) {  // 16 columns: one 16-byte unit of each piece
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 v = live ? __ldg(src + 2 * u + e) : make_uint4(0, 0, 0, 0);
+          const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            uint32_t a = 0, b = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float2 f = unpack_bf16x2(w4[k + y]);
+              f.x *= mul;
+              f.y *= mul;
+              if (isinf(f.x)) f.x = NAN;  // an infinity would saturate to a number
+              if (isinf(f.y)) f.y = NAN;
+              const uint32_t h2 = f32x2_to_e4m3x2(f.x, f.y);
+              const float2 back = e4m3x2_to_f32x2(h2);
+              a |= h2 << (16 * y);
+              b |= f32x2_to_e4m3x2(f.x - back.x, f.y - back.y) << (16 * y);
+            }
+            hi[e * 2 + k / 2] = a;
+            lo[e * 2 + k / 2] = b;
+          }
+        }
+        const int uh = u, ul = u + D / 16;  // unit numbers along [qh | ql]
+        st_shared_v4(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(r, uh & 7), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(r, ul & 7), lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    mbar_arrive(&sh.q_full[t]);
+
+    float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
+    for (int j = 0; j <= last; ++j) {
+      const int i = i0 + j, sl = i % kScaleSlots;
+      alive = alive && __all_sync(0xffffffffu, mbar_wait(&sh.scale_full[sl], (i / kScaleSlots) & 1, &sh.abort_flag, lim) &&
+                                                   mbar_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim));
+      if (!alive) {
+        record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
+        break;
+      }
+      tc_fence_after_sync();
+      float s[128];
+      {
+        uint32_t a[32], b[32], c[32], d[32];
+        tmem_ld32(tS + 0, a);
+        tmem_ld32(tS + 32, b);
+        tmem_ld32(tS + 64, c);
+        tmem_ld32(tS + 96, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          s[k] = __uint_as_float(a[k]);
+          s[32 + k] = __uint_as_float(b[k]);
+          s[64 + k] = __uint_as_float(c[k]);
+          s[96 + k] = __uint_as_float(d[k]);
+        }
+      }
+      const int key0 = (w.s + j) * 128;
+      if (__any_sync(0xffffffffu, key0 + 128 > limit)) {
+        const int lim_col = limit - key0;
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= lim_col) s[k] = -INFINITY;
+      }
+      // max of u over the tile, a 16-key group at a time: its factor is positive
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 sc = sh.scale[sl][g];
+        float gm = fmaxf(s[16 * g], s[16 * g + 1]);
+#pragma unroll
+        for (int k = 2; k < 16; k += 2) gm = fmax3(gm, s[16 * g + k], s[16 * g + k + 1]);
+        mx = fmaxf(mx, fmaf(gm, fmaxf(qfac * sc.x, 1e-36f), sc.y));
+      }
+      const bool move = __any_sync(0xffffffffu, mx > m + (kShift + kSlack));
+      const float m_ref = move ? fmaxf(m, mx - kShift) : m;
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      const float alpha = ex2_approx(m - m_use);  // 0 on the first tile, 1 when the reference is kept
+      l *= alpha;
+      uint32_t pk[32];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float4 sc = sh.scale[sl][half * 4 + g];
+          const float a = fmaxf(qfac * sc.x, 1e-36f), b = sc.y - m_use;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = half * 64 + g * 16 + 2 * k;
+            const float2 x = ffma2_bcast(s[c], s[c + 1], a, b);
+            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum = fadd2(sum, e);
+            pk[g * 8 + k] = pack_f16x2(e.x, e.y);
+          }
+          l = fmaf(sum.x + sum.y, sc.z, l);
+        }
+        tmem_st32(tP + 32 * half, pk);
+      }
+      if (j > 0 && move) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(tO + c, o);
+        }
+      }
+      m = m_ref;
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&sh.p_full[t]);
+    }
+
+    const bool active = last >= 0;
+    if (alive && active) {
+      alive = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[t], (cnt + last) & 1, &sh.abort_flag, lim));
+      if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
+    }
+    tc_fence_after_sync();
+    if (alive) {
+      const bool whole = n == w.tiles;
+      const RowEnd end(m, l);
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + t * 128 + r;
+      if (active) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
+          if (!live) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + c);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = pack_bf16x2(end(__uint_as_float(o[8 * u + 2 * k])), end(__uint_as_float(o[8 * u + 2 * k + 1])));
+              dst[u] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part + slot * D + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
+                                   __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
+          }
+        }
+      } else if (live && whole) {  // none of the tile's rows sees a key
+        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.o + at * D)[c] = make_uint4(0, 0, 0, 0);
+      } else if (live) {  // this part of the keys is behind every row of the tile
+        for (int c = 0; c < D / 4; ++c) reinterpret_cast<float4*>(p.part + slot * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (live) {
+        if (whole) p.lse[at] = end.lse; else p.part_ml[slot] = make_float2(m, l);
+      }
+    }
+    tc_fence_before_sync();
+    mbar_arrive(&sh.o_free[t]);
+    if (active) cnt += last + 1;
+    i0 += n;
+    left -= n;
+    w.s += n;
+    w.settle(p);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_constant__ TileLaunch p) {
+  using C = TileCfg<D>;
+  extern __shared__ uint8_t smem_dyn[];
+  __shared__ TileShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + C::NT * C::Q_BYTES;
+  uint8_t* sV = sK + C::KST * C::K_BYTES;
+  uint8_t* sStage = sV + C::VST * C::V_BYTES;
+  const int warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.q_full[t], 128);
+      mbar_init(&sh.q_taken[t], 1);
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_full[t], 128);
+      mbar_init(&sh.pv_done[t], 1);
+      mbar_init(&sh.o_free[t], 128);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.st_full[i], 1);
+      mbar_init(&sh.st_empty[i], kConvThreads);
+      mbar_init(&sh.v_full[i], kConvThreads);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh.scale_full[i], 8);
+    mbar_init(&sh.mma_drain, 1);
+    sh.abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kLoadWarp) {  // the CTA's run
+    const long long total = tile_search<D>(p, -1, nullptr);
+    const int c = blockIdx.x, used = used_ctas(total, gridDim.x);
+    const long long x0 = c < used ? first_tile(total, used, c) : 0, x1 = c < used ? first_tile(total, used, c + 1) : 0;
+    int4 at = make_int4(p.c.B, 0, 0, 0);
+    if (x1 > x0) tile_search<D>(p, x0, &at);
+    if (lane_id() == 0) {
+      sh.start = at;
+      sh.n_tiles = static_cast<int>(x1 - x0);
+      p.run[c] = at;
+    }
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  if (warp < 8) {
+    regs_inc<kRegsSoftmax>();
+    if (warp < 4 * C::NT) softmax_role<D>(p, sh, sQ, tmem, warp >> 2);
+  } else if (warp < 12) {
+    regs_dec<kRegsConv>();
+    convert_role<D>(p, sh, sStage, sV);
+  } else {
+    regs_dec<kRegsIssue>();
+    if (warp == kLoadWarp) load_role<D>(p, sh, sK, sStage);
+    if (warp == kMmaWarp && lane_id() == 0) mma_role<D>(p, sh, sQ, sK, sV, tmem);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the row blocks that CTAs shared. blockIdx.x = c > 0: the block that the
+// runs of CTAs c - 1 and c meet in, if c - 1 is the first that holds a part
+// of it; blockIdx.y: 8 of its rows. blockIdx.x = 0: sequences whose lengths or
+// counts are out of range, and rows that see no key at all.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p, int ctas) {
+  using C = TileCfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  if (blockIdx.x == 0) {
+    for (int b = blockIdx.y; b < p.c.B; b += gridDim.y) {
+      const int len = seq_len(p.c, b), count = seq_count(p.c, b, p.Nq);
+      if (len != __ldg(p.c.lens + b) || (p.c.counts && count != __ldg(p.c.counts + b))) {
+        if (threadIdx.x == 0) record_bad_index(p.status, WHERE_FWD_KV8);
+        continue;
+      }
+      // whole blocks without a key: all of them without tokens, the first ones where queries stand before the sequence
+      const int none = len == 0 ? count : p.causal ? max(0, count - len) : 0;
+      if (none == 0) continue;
+      const int rows = count * p.g;
+      for (int blk = 0; blk * C::ROWS < rows; ++blk) {
+        const int end = min(rows, (blk + 1) * C::ROWS);
+        if (tiles_seen(len, count, end, p.g, p.causal) > 0) break;
+        for (int x = warp; x < (end - blk * C::ROWS) * p.c.Hkv; x += 8) {
+          const int row = blk * C::ROWS + x / p.c.Hkv, h = x % p.c.Hkv;
+          const size_t at = (static_cast<size_t>(b) * p.Hq + h * p.g + row % p.g) * p.Nq + row / p.g;
+          for (int c = lane; c < D / 8; c += 32) reinterpret_cast<uint4*>(p.o + at * D)[c] = make_uint4(0, 0, 0, 0);
+          if (lane == 0) p.lse[at] = -INFINITY;
+        }
+      }
+    }
+    return;
+  }
+  const int c = blockIdx.x;
+  const int4 at = p.run[c];
+  if (at.x >= p.c.B || at.w == 0) return;  // nothing is shared at this boundary
+  __shared__ long long total_s;
+  if (warp == 0) {
+    const long long total = tile_search<D>(p, -1, nullptr);
+    if (lane == 0) total_s = total;
+  }
+  __syncthreads();
+  const long long total = total_s;
+  const int used = used_ctas(total, ctas);
+  const long long begin = first_tile(total, used, c) - at.w;  // the block's first tile
+  // the CTA that holds tile x: the largest with first_tile <= x
+  const int c0 = static_cast<int>(((begin + 1) * used - 1) / total);
+  if (c0 != c - 1) return;
+  Walk<D> w;
+  w.begin(p, at);
+  const int c1 = static_cast<int>(((begin + w.tiles) * used - 1) / total);
+  const int late = begin > first_tile(total, used, c0) ? 1 : 0;  // the block is not the first of c0's run
+  const int rb = blockIdx.y * 8 + warp, row = w.blk * C::ROWS + rb;
+  const int qi = row / p.g;
+  if (qi >= w.count) return;
+  constexpr int PER = D / 32;
+  float m = -INFINITY, l = 0.f, a[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) a[k] = 0.f;
+#pragma unroll 2
+  for (int u = c0; u <= c1; ++u) {
+    const size_t slot = (static_cast<size_t>(u) * 2 + (u == c0 ? late : 0)) * C::ROWS + rb;
+    const float2 ml = p.part_ml[slot];
+    const float* src = p.part + slot * D + lane * PER;
+    const float to = fmaxf(m, ml.x), ref = to == -INFINITY ? 0.f : to;
+    const float wa = ex2_approx(m - ref), wx = ex2_approx(ml.x - ref);
+    m = to;
+    l = l * wa + ml.y * wx;
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(src + k);
+      a[k] = a[k] * wa + x.x * wx;
+      a[k + 1] = a[k + 1] * wa + x.y * wx;
+    }
+  }
+  const RowEnd end(m, l);
+  const size_t out = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row % p.g) * p.Nq + qi;
+#pragma unroll
+  for (int k = 0; k < PER; k += 2)
+    *reinterpret_cast<uint32_t*>(p.o + out * D + lane * PER + k) = pack_bf16x2(end(a[k]), end(a[k + 1]));
+  if (lane == 0) p.lse[out] = end.lse;
+}
+
+template <int D>
+size_t tile_part_bytes(size_t* ml_off, size_t* run_off) {
+  const size_t rows = static_cast<size_t>(2) * kMaxSms * TileCfg<D>::ROWS;
+  *ml_off = rows * D * sizeof(float);
+  *run_off = *ml_off + rows * sizeof(float2);
+  return *run_off + kMaxSms * sizeof(int4);
+}
+
+template <int D>
+cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
+  using C = TileCfg<D>;
+  auto kern = kv8_tile_kernel<D>;
+  static std::atomic<uint64_t> allowed{0};
+  if (!(allowed.load(std::memory_order_relaxed) >> dev.device & 1)) {
+    // The register split hands out what the block was launched with: a build
+    // that gave its threads fewer would leave the softmax warps waiting.
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs * kThreads < 256 * kRegsSoftmax + 128 * kRegsConv + 128 * kRegsIssue)
+      return cudaErrorLaunchOutOfResources;
+  }
+  cudaError_t e = allow_smem(kern, C::SMEM, dev.device, allowed);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(dev.num_sms, kMaxSms);
+  kern<<<grid, kThreads, C::SMEM, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, C::ROWS / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_tile_combine_kernel<D>, a, grid);
+}
+
+}  // namespace
+
+size_t kv8_tile_workspace(int d) {
+  size_t ml, run;
+  return d == 64 ? tile_part_bytes<64>(&ml, &run) : d == 128 ? tile_part_bytes<128>(&ml, &run) : tile_part_bytes<256>(&ml, &run);
+}
+
+fa_status_t launch_kv8_tiles(const Kv8Call& call, int d, void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
+  TileLaunch a{};
+  static_cast<Kv8Call&>(a) = call;
+  if (!make_cache_map(&a.tmK, call.c.code[0], d, 1 << call.c.page_log2,
+                      static_cast<long long>(call.c.num_pages) * call.c.Hkv))
+    return FA_ERR_CUDA;
+  a.status = dev.status;
+  a.wait_limit_ns = dev.wait_limit_ns;
+  size_t ml = 0, run = 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (d == 64) tile_part_bytes<64>(&ml, &run);
+  if (d == 128) tile_part_bytes<128>(&ml, &run);
+  if (d == 256) tile_part_bytes<256>(&ml, &run);
+  a.part = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + ml);
+  a.run = reinterpret_cast<int4*>(ws + run);
+  if (d == 64) return from_cuda(launch_tiles<64>(a, dev, stream));
+  if (d == 128) return from_cuda(launch_tiles<128>(a, dev, stream));
+  return from_cuda(launch_tiles<256>(a, dev, stream));
+}
+
+}  // namespace fa

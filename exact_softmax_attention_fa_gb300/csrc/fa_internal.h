@@ -27,6 +27,10 @@ enum : uint32_t {
   WHERE_KV8_APPEND = 31,
   WHERE_KV8_GATHER = 32,
   WHERE_FWD_KV8 = 33,
+  WHERE_KV8_LOAD = 41,
+  WHERE_KV8_CONVERT = 42,
+  WHERE_KV8_MMA = 43,
+  WHERE_KV8_SOFTMAX = 44,
   WHERE_PROBE = 99,
 };
 

@@ -1,0 +1,77 @@
+// What the two kernels of the attention over the 8-bit cache share
+// (fa_fwd_kv8.cu: few query rows per K/V head, fa_fwd_kv8_tile.cu: many).
+#pragma once
+
+#include "fa_kv8.cuh"
+
+namespace fa {
+
+constexpr int kMaxSms = 152;      // sizes the partial results
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kShift = 6.f;     // a reference lies this far (base 2) below its row's maximum
+// l is kept times 2^-10: its terms lie between 2^(6 - 120 - 10) and
+// 2^(14 + 100 - 10) for the scales a cache holds, so neither one term nor 2^22
+// of them leave fp32's normal range.
+constexpr float kSumBias = 10.f;
+
+// One call, as both kernels take it.
+struct Kv8Call {
+  Kv8Cache c;
+  const __nv_bfloat16* q;  // [B][Hq][Nq][d]
+  __nv_bfloat16* o;
+  float* lse;              // [B][Hq][Nq]
+  int Hq, Nq, g, causal;   // g query heads per K/V head
+  float scale_log2;
+};
+
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Tokens of sequence b, or 0 where the stored length is out of range.
+__device__ __forceinline__ int seq_len(const Kv8Cache& c, int b) {
+  const int len = __ldg(c.lens + b);
+  return len < 0 || len > (static_cast<long long>(c.max_pages) << c.page_log2) ? 0 : len;
+}
+__device__ __forceinline__ int seq_count(const Kv8Cache& c, int b, int n) {
+  const int count = c.counts ? __ldg(c.counts + b) : n;
+  return count < 0 || count > n ? 0 : count;
+}
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// x / (l 2^kSumBias) and ln of the row's sum, for sums near either end of
+// fp32's range; a row that saw no key has l = 0: O = 0, L = -inf.
+struct RowEnd {
+  float a, b, lse;
+  __device__ __forceinline__ RowEnd(float m, float l) {
+    const int e = static_cast<int>(__float_as_uint(l) >> 23 & 255) - 127;  // l >= 0
+    a = l == 0.f ? 0.f : 1.f;
+    b = 1.f;
+    if (l != 0.f && e < 127) {  // not infinite, not NaN
+      b = exp2i(-e);
+      a = exp2i(-static_cast<int>(kSumBias)) / (l * b);
+    } else if (l != 0.f) {
+      a = 1.f / l;
+    }
+    lse = l == 0.f ? -INFINITY : (m + kSumBias + log2f(l)) * kLn2;
+  }
+  __device__ __forceinline__ float operator()(float x) const { return a == 0.f ? 0.f : x * a * b; }
+};
+
+// fa_fwd_kv8_tile.cu
+size_t kv8_tile_workspace(int d);
+fa_status_t launch_kv8_tiles(const Kv8Call& call, int d, void* workspace, const DeviceInfo& dev, cudaStream_t stream);
+
+// fa_api.cu: tensor map {d, page, slots} of the cache's codes, boxes of one page and at most 128 columns,
+// swizzled by the row's bytes (64 or 128).
+bool make_cache_map(CUtensorMap* m, const void* base, int d, int page, long long slots);
+
+}  // namespace fa

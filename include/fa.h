@@ -489,7 +489,8 @@ fa_status_t fa_get_device_status(cudaStream_t stream);
  * load / MMA / softmax; 11-14: backward load / MMA / softmax / dQ drain;
  * 99: the self-test probe) or that met the first bad index (21: norm and
  * rotation; 22: its backward; 31, 32, 33: the 8-bit cache's append, gather
- * and attention), word[2] its block index, word[3] its
+ * and attention; 41-44: waits of the attention's load / convert / MMA /
+ * softmax), word[2] its block index, word[3] its
  * thread index; all zero when nothing was recorded. Returns
  * FA_ERR_INVALID_ARG for a null word.
  */
