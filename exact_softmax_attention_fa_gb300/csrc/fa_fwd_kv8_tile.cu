@@ -30,6 +30,7 @@
 // long caches leave SMs idle.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "fa_kv8.cuh"
 #include "fa_kv8_attn.cuh"
@@ -85,6 +86,19 @@ struct TileShared {
   int n_tiles;
   uint32_t tmem_base;
   int abort_flag;
+};
+
+// A place in a ring of N stages and the parity of its phase.
+template <int N>
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == N) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // Row blocks of sequence b, and the key tiles that rows < `rows` of it see.
@@ -193,14 +207,34 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, fp32 sums
-__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, fp32 sums; the operands lie AOFF
+// and BOFF bytes behind their descriptors. (The sums are formed here: as values
+// of their own the compiler keeps every product's descriptor in registers over
+// the whole loop, and the issuing thread, which has few, reloads them one by one.)
+template <int AOFF, int BOFF, bool ACC>
+__device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                           uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "add.u32 x, %1, %6;\n\tadd.u32 y, %3, %7;\n\t"
+      "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+      "setp.ne.b32 p, %8, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(AOFF >> 4), "n"(BOFF >> 4), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], fp16 operands, fp32 sums; offsets likewise.
+template <int ACOL, int BOFF>
+__device__ __forceinline__ void umma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+      "add.u32 x, %1, %6;\n\tadd.u32 y, %2, %7;\n\t"
+      "mov.b64 b, {y, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(ACOL), "n"(BOFF >> 4)
       : "memory");
 }
 
@@ -382,35 +416,46 @@ __device__ void convert_role(const TileLaunch& p, TileShared& sh, uint8_t* sStag
 // ---------------------------------------------------------------------------
 // MMA issuer (one thread)
 // ---------------------------------------------------------------------------
+// S of one tile: step QS multiplies 32 columns of a piece (the first D / 32
+// steps: qh). A row of Q holds 128 bytes per chunk of 128 rows: both pieces
+// (d = 64), or 128 columns of one; a row of K its 64, or 128 columns.
+template <int D, int... QS>
+__device__ __forceinline__ void issue_s_steps(std::integer_sequence<int, QS...>, uint32_t d, uint32_t q_lo, uint32_t q_hi,
+                                              uint32_t k_lo, uint32_t k_hi, uint32_t idesc) {
+  (umma_ss_f8<(QS >> 2) * (128 * 128) + (QS & 3) * 32,
+              (QS % (D / 32) >> 2) * (128 * 128) + (QS % (D / 32) & 3) * 32, (QS > 0)>(d, q_lo, q_hi, k_lo, k_hi, idesc),
+   ...);
+}
+// O += P V over 128 keys, 16 a step.
+template <int... KS>
+__device__ __forceinline__ void issue_pv_steps(std::integer_sequence<int, KS...>, uint32_t d, uint32_t p_tmem,
+                                               uint32_t v_lo, uint32_t v_hi, uint32_t idesc, uint32_t accumulate) {
+  (umma_ts_f16<KS * 8, KS * 2048>(d, p_tmem, v_lo, v_hi, idesc, KS > 0 ? 1u : accumulate), ...);
+}
+
 template <int D>
 __device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
   using C = TileCfg<D>;
   constexpr uint32_t kIdescS = make_idesc_f32(128, 128, false);
   constexpr uint32_t kIdescPV = make_idesc_f32(128, D, true);
-  const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
+  const uint64_t q_desc = make_smem_desc_sw128(smem_u32(sQ), 16, 1024);
+  const uint64_t k_desc = D == 64 ? make_smem_desc_sw64(smem_u32(sK)) : make_smem_desc_sw128(smem_u32(sK), 16, 1024);
+  const uint64_t v_desc = make_smem_desc_sw128(smem_u32(sV), 128 * 128, 1024);
   const uint64_t lim = p.wait_limit_ns;
-  int left = sh.n_tiles;
-  auto issue_s = [&](int t, int i) {
-    const uint64_t qd = make_smem_desc_sw128(q_addr + t * C::Q_BYTES, 16, 1024);
-    const uint32_t ka = k_addr + (i % C::KST) * C::K_BYTES;
-    const uint64_t kd = D == 64 ? make_smem_desc_sw64(ka) : make_smem_desc_sw128(ka, 16, 1024);
-#pragma unroll
-    for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) {
-        // a row of Q holds 128 bytes per chunk: both pieces (d = 64), or a piece's 128 columns
-        const int qs = piece * (D / 32) + ks;
-        const uint32_t qoff = (qs >> 2) * (128 * 128) + (qs & 3) * 32, koff = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-        umma_ss_f8(tmem + C::s_col(t), desc_add(qd, qoff), desc_add(kd, koff), kIdescS, qs > 0 ? 1u : 0u);
-      }
+  Ring<C::KST> k;  // the stage of the key tile that the next S takes
+  Ring<C::VST> v;  // the stage of the value tile that the next PV takes
+  const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32), k_hi = static_cast<uint32_t>(k_desc >> 32);
+  const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
+  auto issue_s = [&](int t) {
+    const uint32_t q_lo = static_cast<uint32_t>(q_desc) + t * (C::Q_BYTES >> 4);
+    const uint32_t k_lo = static_cast<uint32_t>(k_desc) + k.stage * (C::K_BYTES >> 4);
+    issue_s_steps<D>(std::make_integer_sequence<int, 2 * (D / 32)>{}, tmem + C::s_col(t), q_lo, q_hi, k_lo, k_hi, kIdescS);
     umma_commit(&sh.s_full[t]);
   };
-  auto issue_pv = [&](int t, int i, bool first) {
-    const uint64_t vd = make_smem_desc_sw128(v_addr + (i % C::VST) * C::V_BYTES, 128 * 128, 1024);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
-              (!first || ks > 0) ? 1u : 0u);
+  auto issue_pv = [&](int t, bool first) {
+    const uint32_t v_lo = static_cast<uint32_t>(v_desc) + v.stage * (C::V_BYTES >> 4);
+    issue_pv_steps(std::make_integer_sequence<int, 8>{}, tmem + C::o_col(t), tmem + C::p_col(t), v_lo, v_hi, kIdescPV,
+                   first ? 0u : 1u);
     umma_commit(&sh.pv_done[t]);
   };
   auto fail = [&]() {
@@ -419,7 +464,7 @@ __device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8
   };
   Walk<D> w;
   w.begin(p, sh.start);
-  int i = 0;            // running tile
+  int left = sh.n_tiles;
   int cnt[2] = {0, 0};  // running S / P / PV count per query tile
   for (int seg = 0; left > 0; ++seg) {
     const int n = min(left, w.tiles - w.s);
@@ -430,7 +475,10 @@ __device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8
       if (!mbar_wait(&sh.q_full[t], seg & 1, &sh.abort_flag, lim)) return fail();
       mbar_arrive(&sh.q_taken[t]);
     }
-    if (!mbar_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, &sh.abort_flag, lim)) return fail();
+    left -= n;
+    w.s += n;
+    w.settle(p);
+    if (!mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
 #pragma unroll
     for (int t = 0; t < C::NT; ++t) {
@@ -438,41 +486,37 @@ __device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8
       // S_t(0) overwrites S_t / P_t of the segment before: its last PV must be done
       if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
-      issue_s(t, i);
+      issue_s(t);
     }
-    umma_commit(&sh.k_empty[i % C::KST]);
-    for (int j = 0; j < n; ++j, ++i) {
-      const int vs = i % C::VST;
-      if (!mbar_wait(&sh.v_full[vs], (i / C::VST) & 1, &sh.abort_flag, lim)) return fail();
+    umma_commit(&sh.k_empty[k.stage]);
+    k.next();
+    for (int j = 0; j < n; ++j) {
+      if (!mbar_wait(&sh.v_full[v.stage], v.phase, &sh.abort_flag, lim)) return fail();
       const bool more = j + 1 < n;
-      if (more) {
-        if (!mbar_wait(&sh.k_full[(i + 1) % C::KST], ((i + 1) / C::KST) & 1, &sh.abort_flag, lim)) return fail();
-      }
-      tc_fence_after_sync();
+      if (more && !mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return fail();
 #pragma unroll
       for (int t = 0; t < C::NT; ++t) {
         if (j > last[t]) continue;
-        if (!mbar_wait(&sh.p_full[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+        if (!mbar_wait(&sh.p_full[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
         // PV_t(0) overwrites O_t: the segment before has to have read it
         if (j == 0 && seg > 0 && !mbar_wait(&sh.o_free[t], (seg - 1) & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
-        issue_pv(t, i, j == 0);
-        if (j + 1 <= last[t]) {
+        issue_pv(t, j == 0);
+        if (j < last[t]) {
           // d = 128: S_t(j + 1) overwrites the columns P_t(j) is read from
-          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
           tc_fence_after_sync();
-          issue_s(t, i + 1);
+          issue_s(t);
         }
+        ++cnt[t];
       }
-      if (more) umma_commit(&sh.k_empty[(i + 1) % C::KST]);
-      umma_commit(&sh.v_empty[vs]);
+      if (more) {
+        umma_commit(&sh.k_empty[k.stage]);
+        k.next();
+      }
+      umma_commit(&sh.v_empty[v.stage]);
+      v.next();
     }
-#pragma unroll
-    for (int t = 0; t < C::NT; ++t)
-      if (last[t] >= 0) cnt[t] += last[t] + 1;
-    left -= n;
-    w.s += n;
-    w.settle(p);
   }
   drain_mmas(&sh.mma_drain, lim);
 }
