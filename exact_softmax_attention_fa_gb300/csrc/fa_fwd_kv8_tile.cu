@@ -41,7 +41,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kConvThreads = 128;
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
-constexpr int kScaleSlots = 8;  // tiles whose scales are kept; more than are in flight
 constexpr int kMinTiles = 2;    // a CTA's run is not cut below this
 constexpr float kSlack = 8.f;   // P <= 2^(kShift + kSlack) = 2^14, fp16
 // Registers a thread after the split: 256 x 184 + 128 x 88 + 128 x 56 = 512 x 128.
@@ -56,6 +55,7 @@ struct TileCfg {
   static constexpr int V_BYTES = 2 * 128 * D;     // fp16 values
   static constexpr int KST = D == 64 ? 4 : (D == 128 ? 3 : 2);
   static constexpr int VST = D == 64 ? 3 : (D == 128 ? 2 : 1);
+  static constexpr int SLOTS = KST + 2;  // tiles whose scales are kept: a tile's are read before the key ring comes round
   static constexpr int SST = D == 64 ? 4 : (D == 128 ? 2 : 1);  // staged value codes
   static constexpr bool P_ALIAS = D == 128;
   __host__ __device__ static constexpr uint32_t s_col(int t) { return D == 256 ? 0u : uint32_t(t) * 128u; }
@@ -70,18 +70,20 @@ struct TileLaunch : Kv8Call {
   CUtensorMap tmK;         // the key codes: {d, page, pages * Hkv}
   float* part;             // [2 * CTAs][ROWS][d]
   float2* part_ml;         // [2 * CTAs][ROWS]
-  int4* run;               // [CTAs]: where each CTA's run starts (b, h, block, tile)
+  int4* run;               // [CTAs][2]: where each CTA's run starts (b, h, block, tile); the block's holders
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
 
+template <int D>
 struct TileShared {
+  static constexpr int SLOTS = TileCfg<D>::SLOTS;
   uint64_t q_full[2], q_taken[2];
   uint64_t k_full[4], k_empty[4], st_full[4], st_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
-  uint64_t scale_full[kScaleSlots];
+  uint64_t scale_full[SLOTS];
   uint64_t mma_drain;
-  float4 scale[kScaleSlots][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
+  float4 scale[SLOTS][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
   int4 start;
   int n_tiles;
   uint32_t tmem_base;
@@ -256,6 +258,28 @@ __device__ __forceinline__ uint64_t make_smem_desc_sw64(uint32_t smem_addr) {
   return d;
 }
 
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+}
+// One arrival for a warp's lanes: 32 of them on one barrier are 32 passes of
+// the shared-memory pipe, which the tensor core's operands need.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -269,7 +293,7 @@ __device__ __forceinline__ void regs_dec() {
 // Pages, scales and loads (one warp)
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ void load_role(const TileLaunch& p, TileShared& sh, uint8_t* sK, uint8_t* sStage) {
+__device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, uint8_t* sStage) {
   using C = TileCfg<D>;
   const int lane = threadIdx.x & 31;
   const uint64_t lim = p.wait_limit_ns;
@@ -316,9 +340,9 @@ __device__ void load_role(const TileLaunch& p, TileShared& sh, uint8_t* sK, uint
       next = look_up();
     }
     const int ks = i % C::KST;
-    if (i >= C::KST) ok = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], ((i / C::KST) - 1) & 1, &sh.abort_flag, lim));
+    if (i >= C::KST) ok = warp_wait(&sh.k_empty[ks], ((i / C::KST) - 1) & 1, &sh.abort_flag, lim);
     if (!ok) break;
-    const int slot8 = i % kScaleSlots;
+    const int slot8 = i % C::SLOTS;
     if (lane >= j0 && lane < j0 + 8) {
       sh.scale[slot8][lane - j0] = entry;
       mbar_arrive(&sh.scale_full[slot8]);
@@ -346,7 +370,7 @@ __device__ void load_role(const TileLaunch& p, TileShared& sh, uint8_t* sK, uint
     }
     ++k_issued;
     const int ss = i % C::SST;
-    if (i >= C::SST) ok = __all_sync(0xffffffffu, mbar_wait(&sh.st_empty[ss], ((i / C::SST) - 1) & 1, &sh.abort_flag, lim));
+    if (i >= C::SST) ok = warp_wait(&sh.st_empty[ss], ((i / C::SST) - 1) & 1, &sh.abort_flag, lim);
     if (!ok) break;
     if (lane == 0) mbar_arrive_expect_tx(&sh.st_full[ss], bytes);
     __syncwarp();
@@ -369,7 +393,7 @@ __device__ void load_role(const TileLaunch& p, TileShared& sh, uint8_t* sK, uint
 // Value codes -> fp16 operand tiles (one warpgroup)
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ void convert_role(const TileLaunch& p, TileShared& sh, uint8_t* sStage, uint8_t* sV) {
+__device__ void convert_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sStage, uint8_t* sV) {
   using C = TileCfg<D>;
   constexpr int UNITS = D / 8;                     // 8 codes (16 bytes of fp16) each
   constexpr int PASSES = 128 * UNITS / kConvThreads;
@@ -386,10 +410,10 @@ __device__ void convert_role(const TileLaunch& p, TileShared& sh, uint8_t* sStag
       ++w.s;
       w.settle(p);
     }
-    const int ss = i % C::SST, vs = i % C::VST, sl = i % kScaleSlots;
-    ok = mbar_wait(&sh.scale_full[sl], (i / kScaleSlots) & 1, &sh.abort_flag, lim) &&
-         mbar_wait(&sh.st_full[ss], (i / C::SST) & 1, &sh.abort_flag, lim) &&
-         (i < C::VST || mbar_wait(&sh.v_empty[vs], ((i / C::VST) - 1) & 1, &sh.abort_flag, lim));
+    const int ss = i % C::SST, vs = i % C::VST, sl = i % C::SLOTS;
+    ok = warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim) &&
+         warp_wait(&sh.st_full[ss], (i / C::SST) & 1, &sh.abort_flag, lim) &&
+         (i < C::VST || warp_wait(&sh.v_empty[vs], ((i / C::VST) - 1) & 1, &sh.abort_flag, lim));
     if (!ok) break;
     // Keys behind the sequence and on bad pages: 0 (what lies there may be NaN codes, and 0 * NaN is not 0).
     const int rows = w.len - w.s * 128;
@@ -406,9 +430,9 @@ __device__ void convert_role(const TileLaunch& p, TileShared& sh, uint8_t* sStag
       st_shared_v4(dst + sw128_offset(row, unit & 7), e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
                    e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
     }
-    mbar_arrive(&sh.st_empty[ss]);
+    warp_arrive(&sh.st_empty[ss]);
     fence_proxy_async_smem();
-    mbar_arrive(&sh.v_full[vs]);
+    warp_arrive(&sh.v_full[vs]);
   }
   if (!ok) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_CONVERT);
 }
@@ -434,7 +458,7 @@ __device__ __forceinline__ void issue_pv_steps(std::integer_sequence<int, KS...>
 }
 
 template <int D>
-__device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
+__device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
   using C = TileCfg<D>;
   constexpr uint32_t kIdescS = make_idesc_f32(128, 128, false);
   constexpr uint32_t kIdescPV = make_idesc_f32(128, D, true);
@@ -525,9 +549,9 @@ __device__ void mma_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint8
 // Q pieces, softmax, correction and epilogue (warpgroup t owns query tile t)
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, uint32_t tmem, int t) {
+__device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint32_t tmem, int t) {
   using C = TileCfg<D>;
-  const int r = threadIdx.x & 127;
+  const int r = threadIdx.x & 127, lane = r & 31;
   const uint32_t lane_base = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
   const uint32_t tS = tmem + lane_base + C::s_col(t);
   const uint32_t tP = tmem + lane_base + C::p_col(t);
@@ -550,63 +574,71 @@ __device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, u
     // The MMA thread has taken note of the segment before (else an idle tile's
     // warpgroup could run two arrivals ahead of its parity wait).
     if (alive && seg > 0) {
-      alive = __all_sync(0xffffffffu, mbar_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim));
+      alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim);
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     float qfac = 0.f;
     if (alive && last >= 0) {
-      // The row's Q pieces; S of the segment before is complete, so its tile is free.
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * D);
-      uint32_t amax = 0;
+      // The warp's 32 rows as Q pieces, 8 columns a lane (whole lines a load);
+      // S of the segment before is complete, so the tile is free.
+      constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes a row, rows a pass
+      const int col = lane % LPR, warp_row = r & ~31;
 #pragma unroll 4
-      for (int u = 0; u < D / 8; ++u) {
-        const uint4 v = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+      for (int q = 0; q < 32 / RPP; ++q) {
+        const int pr = q * RPP + lane / LPR;  // row of the warp
+        const int row_q = w.blk * C::ROWS + t * 128 + warp_row + pr, qi_q = row_q / p.g;
+        const size_t at_q = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row_q % p.g) * p.Nq + qi_q;
+        const uint4 v = qi_q < w.count ? __ldg(reinterpret_cast<const uint4*>(p.q + at_q * D) + col) : make_uint4(0, 0, 0, 0);
         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+        uint32_t amax = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
-      }
-      const int x = max(static_cast<int>(amax >> 7) - 127, -100);
-      const float mul = exp2i(7 - x);
-      qfac = exp2i(x - 7);
-#pragma unroll 1
-      for (int u = 0; u < D / 16; ++u) {  // 16 columns: one 16-byte unit of each piece
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint4 v = live ? __ldg(src + 2 * u + e) : make_uint4(0, 0, 0, 0);
-          const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int x = max(static_cast<int>(amax >> 7) - 127, -100);
+        const float mul = exp2i(7 - x);
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            uint32_t a = 0, b = 0;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float2 f = unpack_bf16x2(w4[k + y]);
-              f.x *= mul;
-              f.y *= mul;
-              if (isinf(f.x)) f.x = NAN;  // an infinity would saturate to a number
-              if (isinf(f.y)) f.y = NAN;
-              const uint32_t h2 = f32x2_to_e4m3x2(f.x, f.y);
-              const float2 back = e4m3x2_to_f32x2(h2);
-              a |= h2 << (16 * y);
-              b |= f32x2_to_e4m3x2(f.x - back.x, f.y - back.y) << (16 * y);
-            }
-            hi[e * 2 + k / 2] = a;
-            lo[e * 2 + k / 2] = b;
-          }
+        for (int k = 0; k < 4; ++k) {
+          float2 f = unpack_bf16x2(w4[k]);
+          f.x *= mul;
+          f.y *= mul;
+          if (isinf(f.x)) f.x = NAN;  // an infinity would saturate to a number
+          if (isinf(f.y)) f.y = NAN;
+          const uint32_t h2 = f32x2_to_e4m3x2(f.x, f.y);
+          const float2 back = e4m3x2_to_f32x2(h2);
+          hi[k >> 1] |= h2 << (16 * (k & 1));
+          lo[k >> 1] |= f32x2_to_e4m3x2(f.x - back.x, f.y - back.y) << (16 * (k & 1));
         }
-        const int uh = u, ul = u + D / 16;  // unit numbers along [qh | ql]
-        st_shared_v4(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(r, uh & 7), hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(r, ul & 7), lo[0], lo[1], lo[2], lo[3]);
+        // unit numbers along the row [qh | ql]; a lane has half a unit of each
+        const int uh = col >> 1, ul = uh + D / 16;
+        st_shared_v2(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(warp_row + pr, uh & 7) + (col & 1) * 8, hi[0], hi[1]);
+        st_shared_v2(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(warp_row + pr, ul & 7) + (col & 1) * 8, lo[0], lo[1]);
+        // the thread that owns the row keeps its power of two
+        const float fac = exp2i(x - 7);
+#pragma unroll
+        for (int u = 0; u < RPP; ++u) {
+          const float got = __shfl_sync(0xffffffffu, fac, u * LPR);
+          if (lane == q * RPP + u) qfac = got;
+        }
       }
       fence_proxy_async_smem();
     }
-    mbar_arrive(&sh.q_full[t]);
+    warp_arrive(&sh.q_full[t]);
 
     float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
     for (int j = 0; j <= last; ++j) {
-      const int i = i0 + j, sl = i % kScaleSlots;
-      alive = alive && __all_sync(0xffffffffu, mbar_wait(&sh.scale_full[sl], (i / kScaleSlots) & 1, &sh.abort_flag, lim) &&
-                                                   mbar_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim));
+      const int i = i0 + j, sl = i % C::SLOTS;
+      alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
+      // factors and offsets of the 16-key groups, read while S is being formed
+      float fg[8], eg[8];
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float2 sc = *reinterpret_cast<const float2*>(&sh.scale[sl][g]);
+        fg[g] = fmaxf(qfac * sc.x, 1e-36f);
+        eg[g] = sc.y;
+      }
+      alive = alive && warp_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim);
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
         break;
@@ -639,11 +671,13 @@ __device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, u
       float mx = -INFINITY;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        const float4 sc = sh.scale[sl][g];
-        float gm = fmaxf(s[16 * g], s[16 * g + 1]);
+        float ga = fmaxf(s[16 * g], s[16 * g + 1]), gb = fmaxf(s[16 * g + 2], s[16 * g + 3]);
 #pragma unroll
-        for (int k = 2; k < 16; k += 2) gm = fmax3(gm, s[16 * g + k], s[16 * g + k + 1]);
-        mx = fmaxf(mx, fmaf(gm, fmaxf(qfac * sc.x, 1e-36f), sc.y));
+        for (int k = 4; k < 16; k += 4) {
+          ga = fmax3(ga, s[16 * g + k], s[16 * g + k + 1]);
+          gb = fmax3(gb, s[16 * g + k + 2], s[16 * g + k + 3]);
+        }
+        mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fg[g], eg[g]));
       }
       const bool move = __any_sync(0xffffffffu, mx > m + (kShift + kSlack));
       const float m_ref = move ? fmaxf(m, mx - kShift) : m;
@@ -684,12 +718,12 @@ __device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, u
       m = m_ref;
       tmem_st_wait();
       tc_fence_before_sync();
-      mbar_arrive(&sh.p_full[t]);
+      warp_arrive(&sh.p_full[t]);
     }
 
     const bool active = last >= 0;
     if (alive && active) {
-      alive = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[t], (cnt + last) & 1, &sh.abort_flag, lim));
+      alive = warp_wait(&sh.pv_done[t], (cnt + last) & 1, &sh.abort_flag, lim);
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     tc_fence_after_sync();
@@ -697,42 +731,56 @@ __device__ void softmax_role(const TileLaunch& p, TileShared& sh, uint8_t* sQ, u
       const bool whole = n == w.tiles;
       const RowEnd end(m, l);
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + t * 128 + r;
-      if (active) {
+      // 128 bytes of each of the warp's 32 rows at a time (32 fp32 or 64 bf16
+      // columns) through its own 4 KB of the Q tile, whose last S is complete:
+      // stores of whole lines. Row i's pieces are XORed as in the tiles.
+      const uint32_t stage = q_dst + (r >> 5) * 4096;
+      const int cols = whole ? 64 : 32;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D; c += cols) {
+        __syncwarp();
+#pragma unroll 1
+        for (int half = 0; half < (whole ? 2 : 1); ++half) {
           uint32_t o[32];
-          tmem_ld32(tO + c, o);
+          tmem_ld32(tO + c + 32 * half, o);
           tmem_ld_wait();
-          if (!live) continue;
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + c);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t x[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 x[k] = pack_bf16x2(end(__uint_as_float(o[8 * u + 2 * k])), end(__uint_as_float(o[8 * u + 2 * k + 1])));
-              dst[u] = make_uint4(x[0], x[1], x[2], x[3]);
+              st_shared_v4(stage + sw128_offset(lane, half * 4 + u), x[0], x[1], x[2], x[3]);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part + slot * D + c);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              dst[u] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
-                                   __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
+              st_shared_v4(stage + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
           }
         }
-      } else if (live && whole) {  // none of the tile's rows sees a key
-        for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(p.o + at * D)[c] = make_uint4(0, 0, 0, 0);
-      } else if (live) {  // this part of the keys is behind every row of the tile
-        for (int c = 0; c < D / 4; ++c) reinterpret_cast<float4*>(p.part + slot * D)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {  // four rows a pass
+          const int pr = q * 4 + (lane >> 3);
+          uint4 v = ld_shared_v4(stage + sw128_offset(pr, lane & 7));
+          const int row_q = row - lane + pr, qi_q = row_q / p.g;
+          if (qi_q >= w.count) continue;
+          if (!active) v = make_uint4(0, 0, 0, 0);  // no row of the tile sees a key of this part
+          if (whole) {
+            const size_t at_q = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row_q % p.g) * p.Nq + qi_q;
+            *(reinterpret_cast<uint4*>(p.o + at_q * D + c) + (lane & 7)) = v;
+          } else {
+            *(reinterpret_cast<uint4*>(p.part + (slot - lane + pr) * D + c) + (lane & 7)) = v;
+          }
+        }
       }
       if (live) {
         if (whole) p.lse[at] = end.lse; else p.part_ml[slot] = make_float2(m, l);
       }
     }
     tc_fence_before_sync();
-    mbar_arrive(&sh.o_free[t]);
+    warp_arrive(&sh.o_free[t]);
     if (active) cnt += last + 1;
     i0 += n;
     left -= n;
@@ -745,7 +793,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_constant__ TileLaunch p) {
   using C = TileCfg<D>;
   extern __shared__ uint8_t smem_dyn[];
-  __shared__ TileShared sh;
+  __shared__ TileShared<D> sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::NT * C::Q_BYTES;
@@ -755,22 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.q_full[t], 128);
+      mbar_init(&sh.q_full[t], 4);
       mbar_init(&sh.q_taken[t], 1);
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_full[t], 128);
+      mbar_init(&sh.p_full[t], 4);
       mbar_init(&sh.pv_done[t], 1);
-      mbar_init(&sh.o_free[t], 128);
+      mbar_init(&sh.o_free[t], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
       mbar_init(&sh.st_full[i], 1);
-      mbar_init(&sh.st_empty[i], kConvThreads);
-      mbar_init(&sh.v_full[i], kConvThreads);
+      mbar_init(&sh.st_empty[i], kConvThreads / 32);
+      mbar_init(&sh.v_full[i], kConvThreads / 32);
       mbar_init(&sh.v_empty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&sh.scale_full[i], 8);
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&sh.scale_full[i], 8);
     mbar_init(&sh.mma_drain, 1);
     sh.abort_flag = 0;
     fence_mbarrier_init();
@@ -784,7 +832,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     if (lane_id() == 0) {
       sh.start = at;
       sh.n_tiles = static_cast<int>(x1 - x0);
-      p.run[c] = at;
+      // for the joining kernel: the CTAs that hold the block the run starts in,
+      // and whether it is not the first block of the first of them
+      int4 held = make_int4(c, c, 0, 0);
+      if (x1 > x0 && at.w > 0) {
+        Walk<D> w;
+        w.begin(p, at);
+        const long long begin = x0 - at.w;  // the CTA that holds tile x: the largest with first_tile <= x
+        held.x = static_cast<int>(((begin + 1) * used - 1) / total);
+        held.y = static_cast<int>(((begin + w.tiles) * used - 1) / total);
+        held.z = begin > first_tile(total, used, held.x) ? 1 : 0;
+        held.w = w.count;
+      }
+      p.run[2 * c] = at;
+      p.run[2 * c + 1] = held;
     }
   }
   if (warp == kMmaWarp) {
@@ -815,10 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
 
 // Joins the row blocks that CTAs shared. blockIdx.x = c > 0: the block that the
 // runs of CTAs c - 1 and c meet in, if c - 1 is the first that holds a part
-// of it; blockIdx.y: 8 of its rows. blockIdx.x = 0: sequences whose lengths or
+// of it; blockIdx.y: 32 of its rows. blockIdx.x = 0: sequences whose lengths or
 // counts are out of range, and rows that see no key at all.
 template <int D>
-__global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p, int ctas) {
+__global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p) {
   using C = TileCfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
@@ -847,53 +908,51 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_cons
     return;
   }
   const int c = blockIdx.x;
-  const int4 at = p.run[c];
-  if (at.x >= p.c.B || at.w == 0) return;  // nothing is shared at this boundary
-  __shared__ long long total_s;
-  if (warp == 0) {
-    const long long total = tile_search<D>(p, -1, nullptr);
-    if (lane == 0) total_s = total;
+  const int4 at = p.run[2 * c], held = p.run[2 * c + 1];
+  const int c0 = held.x, c1 = held.y, count = held.w;
+  if (c0 != c - 1) return;  // nothing is shared at this boundary, or another one's blocks join it
+  // A warp joins four rows side by side, part by part.
+  constexpr int PER = D / 32, SIDE = 4;
+  const int rb = blockIdx.y * 32 + warp * SIDE;
+  float m[SIDE], l[SIDE], a[SIDE][PER];
+#pragma unroll
+  for (int e = 0; e < SIDE; ++e) {
+    m[e] = -INFINITY;
+    l[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) a[e][k] = 0.f;
   }
-  __syncthreads();
-  const long long total = total_s;
-  const int used = used_ctas(total, ctas);
-  const long long begin = first_tile(total, used, c) - at.w;  // the block's first tile
-  // the CTA that holds tile x: the largest with first_tile <= x
-  const int c0 = static_cast<int>(((begin + 1) * used - 1) / total);
-  if (c0 != c - 1) return;
-  Walk<D> w;
-  w.begin(p, at);
-  const int c1 = static_cast<int>(((begin + w.tiles) * used - 1) / total);
-  const int late = begin > first_tile(total, used, c0) ? 1 : 0;  // the block is not the first of c0's run
-  const int rb = blockIdx.y * 8 + warp, row = w.blk * C::ROWS + rb;
-  const int qi = row / p.g;
-  if (qi >= w.count) return;
-  constexpr int PER = D / 32;
-  float m = -INFINITY, l = 0.f, a[PER];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) a[k] = 0.f;
-#pragma unroll 2
   for (int u = c0; u <= c1; ++u) {
-    const size_t slot = (static_cast<size_t>(u) * 2 + (u == c0 ? late : 0)) * C::ROWS + rb;
-    const float2 ml = p.part_ml[slot];
-    const float* src = p.part + slot * D + lane * PER;
-    const float to = fmaxf(m, ml.x), ref = to == -INFINITY ? 0.f : to;
-    const float wa = ex2_approx(m - ref), wx = ex2_approx(ml.x - ref);
-    m = to;
-    l = l * wa + ml.y * wx;
+    const size_t slot = (static_cast<size_t>(u) * 2 + (u == c0 ? held.z : 0)) * C::ROWS + rb;
+    float2 ml[SIDE], x[SIDE][PER / 2];
 #pragma unroll
-    for (int k = 0; k < PER; k += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + k);
-      a[k] = a[k] * wa + x.x * wx;
-      a[k + 1] = a[k + 1] * wa + x.y * wx;
+    for (int e = 0; e < SIDE; ++e) {
+      ml[e] = p.part_ml[slot + e];
+#pragma unroll
+      for (int k = 0; k < PER / 2; ++k)
+        x[e][k] = *reinterpret_cast<const float2*>(p.part + (slot + e) * D + lane * PER + 2 * k);
+    }
+#pragma unroll
+    for (int e = 0; e < SIDE; ++e) {
+      const float to = fmaxf(m[e], ml[e].x), ref = to == -INFINITY ? 0.f : to;
+      const float wa = ex2_approx(m[e] - ref), wx = ex2_approx(ml[e].x - ref);
+      m[e] = to;
+      l[e] = l[e] * wa + ml[e].y * wx;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) a[e][k] = a[e][k] * wa + (k & 1 ? x[e][k / 2].y : x[e][k / 2].x) * wx;
     }
   }
-  const RowEnd end(m, l);
-  const size_t out = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row % p.g) * p.Nq + qi;
 #pragma unroll
-  for (int k = 0; k < PER; k += 2)
-    *reinterpret_cast<uint32_t*>(p.o + out * D + lane * PER + k) = pack_bf16x2(end(a[k]), end(a[k + 1]));
-  if (lane == 0) p.lse[out] = end.lse;
+  for (int e = 0; e < SIDE; ++e) {
+    const int row = at.z * C::ROWS + rb + e, qi = row / p.g;
+    if (qi >= count) break;
+    const RowEnd end(m[e], l[e]);
+    const size_t out = (static_cast<size_t>(at.x) * p.Hq + at.y * p.g + row % p.g) * p.Nq + qi;
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+      *reinterpret_cast<uint32_t*>(p.o + out * D + lane * PER + k) = pack_bf16x2(end(a[e][k]), end(a[e][k + 1]));
+    if (lane == 0) p.lse[out] = end.lse;
+  }
 }
 
 template <int D>
@@ -901,7 +960,7 @@ size_t tile_part_bytes(size_t* ml_off, size_t* run_off) {
   const size_t rows = static_cast<size_t>(2) * kMaxSms * TileCfg<D>::ROWS;
   *ml_off = rows * D * sizeof(float);
   *run_off = *ml_off + rows * sizeof(float2);
-  return *run_off + kMaxSms * sizeof(int4);
+  return *run_off + 2 * kMaxSms * sizeof(int4);
 }
 
 template <int D>
@@ -925,7 +984,7 @@ cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stre
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, C::ROWS / 8);
+  cfg.gridDim = dim3(grid, C::ROWS / 32);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -933,7 +992,7 @@ cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_tile_combine_kernel<D>, a, grid);
+  return cudaLaunchKernelEx(&cfg, kv8_tile_combine_kernel<D>, a);
 }
 
 }  // namespace
