@@ -20,8 +20,7 @@
 //
 // Roles: warpgroups 0 and 1 softmax, correction and epilogue of one query tile
 // each (and its Q pieces), warpgroup 2 converts V, warp 12 looks up pages and
-// loads, one thread of warp 13 issues MMAs. Registers are moved to the softmax
-// warpgroups (setmaxnreg).
+// loads, one thread of warp 13 issues MMAs.
 //
 // Bound: tensor cores, and the softmax's exponentials behind them. Work: every
 // CTA takes an equal run of the flattened list of (sequence, K/V head, row
@@ -38,14 +37,11 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 448;
 constexpr int kConvThreads = 128;
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr int kMinTiles = 2;    // a CTA's run is not cut below this
 constexpr float kSlack = 8.f;   // P <= 2^(kShift + kSlack) = 2^14, fp16
-// Registers a thread after the split: 256 x 184 + 128 x 88 + 128 x 56 = 512 x 128.
-constexpr int kRegsSoftmax = 184, kRegsConv = 88, kRegsIssue = 56;
-
 template <int D>
 struct TileCfg {
   static constexpr int NT = D <= 128 ? 2 : 1;
@@ -278,15 +274,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------------------
@@ -630,79 +617,90 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     for (int j = 0; j <= last; ++j) {
       const int i = i0 + j, sl = i % C::SLOTS;
       alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
-      // factors and offsets of the 16-key groups, read while S is being formed
-      float fg[8], eg[8];
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float2 sc = *reinterpret_cast<const float2*>(&sh.scale[sl][g]);
-        fg[g] = fmaxf(qfac * sc.x, 1e-36f);
-        eg[g] = sc.y;
-      }
       alive = alive && warp_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim);
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
         break;
       }
       tc_fence_after_sync();
-      float s[128];
-      {
-        uint32_t a[32], b[32], c[32], d[32];
-        tmem_ld32(tS + 0, a);
-        tmem_ld32(tS + 32, b);
-        tmem_ld32(tS + 64, c);
-        tmem_ld32(tS + 96, d);
-        tmem_ld_wait();
+      // The row of S stays in tensor memory and is read twice, 32 columns at a
+      // time with the next 32 on their way: once for its maximum, once for the
+      // weights. Holding all 128 in registers unrolls everything: the loop then
+      // leaves the instruction cache, where the MMA thread's has to be found.
+      const int lim_col = limit - (w.s + j) * 128;
+      if (__any_sync(0xffffffffu, lim_col < 128)) {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(tS + c, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          s[k] = __uint_as_float(a[k]);
-          s[32 + k] = __uint_as_float(b[k]);
-          s[64 + k] = __uint_as_float(c[k]);
-          s[96 + k] = __uint_as_float(d[k]);
+          for (int k = 0; k < 32; ++k)
+            if (c + k >= lim_col) x[k] = __float_as_uint(-INFINITY);
+          tmem_st32(tS + c, x);
         }
+        tmem_st_wait();
       }
-      const int key0 = (w.s + j) * 128;
-      if (__any_sync(0xffffffffu, key0 + 128 > limit)) {
-        const int lim_col = limit - key0;
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k >= lim_col) s[k] = -INFINITY;
-      }
-      // max of u over the tile, a 16-key group at a time: its factor is positive
+      // 16-key groups: u = S fg + eg; a group's factor is positive, so its
+      // largest u is that of its largest S.
+      uint32_t xa[32], xb[32];
+      tmem_ld32(tS, xa);
       float mx = -INFINITY;
+      auto max_of = [&](const uint32_t (&x)[32], int g0) {
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        float ga = fmaxf(s[16 * g], s[16 * g + 1]), gb = fmaxf(s[16 * g + 2], s[16 * g + 3]);
+        for (int h = 0; h < 2; ++h) {
+          const float2 sc = *reinterpret_cast<const float2*>(&sh.scale[sl][g0 + h]);
+          auto f = [&](int k) { return __uint_as_float(x[16 * h + k]); };
+          float ga = fmaxf(f(0), f(1)), gb = fmaxf(f(2), f(3));
 #pragma unroll
-        for (int k = 4; k < 16; k += 4) {
-          ga = fmax3(ga, s[16 * g + k], s[16 * g + k + 1]);
-          gb = fmax3(gb, s[16 * g + k + 2], s[16 * g + k + 3]);
+          for (int k = 4; k < 16; k += 4) {
+            ga = fmax3(ga, f(k), f(k + 1));
+            gb = fmax3(gb, f(k + 2), f(k + 3));
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fmaxf(qfac * sc.x, 1e-36f), sc.y));
         }
-        mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fg[g], eg[g]));
+      };
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        tmem_ld_wait();
+        tmem_ld32(tS + c + 32, xb);
+        max_of(xa, c / 16);
+        tmem_ld_wait();
+        tmem_ld32(tS + (c ? 0 : 64), xa);  // at the end the first columns again
+        max_of(xb, c / 16 + 2);
       }
       const bool move = __any_sync(0xffffffffu, mx > m + (kShift + kSlack));
       const float m_ref = move ? fmaxf(m, mx - kShift) : m;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m - m_use);  // 0 on the first tile, 1 when the reference is kept
       l *= alpha;
-      uint32_t pk[32];
+      // P (16 columns of packed pairs) overwrites, at d = 128, columns of S that have been read
+      auto weigh = [&](const uint32_t (&x)[32], int g0) {
+        uint32_t pk[16];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 sc = sh.scale[sl][half * 4 + g];
+        for (int h = 0; h < 2; ++h) {
+          const float4 sc = sh.scale[sl][g0 + h];
           const float a = fmaxf(qfac * sc.x, 1e-36f), b = sc.y - m_use;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int c = half * 64 + g * 16 + 2 * k;
-            const float2 x = ffma2_bcast(s[c], s[c + 1], a, b);
-            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            const float2 u = ffma2_bcast(__uint_as_float(x[16 * h + 2 * k]), __uint_as_float(x[16 * h + 2 * k + 1]), a, b);
+            const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
             sum = fadd2(sum, e);
-            pk[g * 8 + k] = pack_f16x2(e.x, e.y);
+            pk[8 * h + k] = pack_f16x2(e.x, e.y);
           }
           l = fmaf(sum.x + sum.y, sc.z, l);
         }
-        tmem_st32(tP + 32 * half, pk);
+        tmem_st16(tP + 8 * g0, pk);
+      };
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        tmem_ld_wait();
+        tmem_ld32(tS + c + 32, xb);
+        weigh(xa, c / 16);
+        tmem_ld_wait();
+        if (c == 0) tmem_ld32(tS + 64, xa);
+        weigh(xb, c / 16 + 2);
       }
       if (j > 0 && move) {
 #pragma unroll 1
@@ -857,15 +855,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   if (warp < 8) {
-    regs_inc<kRegsSoftmax>();
     if (warp < 4 * C::NT) softmax_role<D>(p, sh, sQ, tmem, warp >> 2);
   } else if (warp < 12) {
-    regs_dec<kRegsConv>();
     convert_role<D>(p, sh, sStage, sV);
-  } else {
-    regs_dec<kRegsIssue>();
-    if (warp == kLoadWarp) load_role<D>(p, sh, sK, sStage);
-    if (warp == kMmaWarp && lane_id() == 0) mma_role<D>(p, sh, sQ, sK, sV, tmem);
+  } else if (warp == kLoadWarp) {
+    load_role<D>(p, sh, sK, sStage);
+  } else if (lane_id() == 0) {
+    mma_role<D>(p, sh, sQ, sK, sV, tmem);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -968,15 +964,6 @@ cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stre
   using C = TileCfg<D>;
   auto kern = kv8_tile_kernel<D>;
   static std::atomic<uint64_t> allowed{0};
-  if (!(allowed.load(std::memory_order_relaxed) >> dev.device & 1)) {
-    // The register split hands out what the block was launched with: a build
-    // that gave its threads fewer would leave the softmax warps waiting.
-    cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs * kThreads < 256 * kRegsSoftmax + 128 * kRegsConv + 128 * kRegsIssue)
-      return cudaErrorLaunchOutOfResources;
-  }
   cudaError_t e = allow_smem(kern, C::SMEM, dev.device, allowed);
   if (e != cudaSuccess) return e;
   const int grid = std::min(dev.num_sms, kMaxSms);
