@@ -6,11 +6,12 @@
 // The rotation is orthogonal, so the gradient turns back by the same angle.
 //
 // Both are HBM-bound: a row of d bf16 is read once and written once (the
-// backward reads dy and x). One row is held by d / 8 lanes of a warp, 16 bytes
-// a lane, so a warp's loads and stores are whole 128-byte lines and the row
-// sums are shuffles inside the lane group. A lane group takes kHeads heads of
-// one token: their loads are issued together (bytes in flight), and the
-// token's cosines and sines are read once for all of them.
+// backward reads dy and x). One row is held by d / 8 lanes of a warp, as two
+// groups of four columns each: for half-split pairs the group and its partner
+// half a rotation further, so that a pair is turned inside its lane with one
+// sine and cosine for both members, and the row sums are the only shuffles. A
+// lane group takes several heads of one token: their loads are issued together
+// (bytes in flight), and the token's angles are read once for all of them.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,8 +26,11 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;            // heads of one token per lane group
-constexpr int kMaxBwdBlocks = 608;   // partial sums of dw: 4 blocks on each of 152 SMs
+constexpr int kHeads = 4;            // heads of one token per lane group, forward
+constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward: kBwdSide at a time
+constexpr int kBwdSide = 2;
+constexpr int kBwdPerSm = 2;         // blocks of the backward on an SM
+constexpr int kMaxBwdBlocks = kBwdPerSm * 152;  // partial sums of dw, for q and k each
 
 struct NormRope {
   // t = 0 q, 1 k, 2 v: the strided side (the projection) and the [B][H][N][d] side
@@ -42,85 +46,90 @@ struct NormRope {
   const float* sin_t;
   const int* positions;
   uint32_t* status;
-  float* part;                 // backward: [2][blocks][d] partial dw
+  float* part;                 // backward: partial dw [blocks[0] + blocks[1]][d]
+  int blocks[3];               // backward: blocks for q, k and v, in this order
   float* dw[2];
   int N, tokens, H[3], chunks[3];  // chunks: lane groups a token needs for q, k, v
   int rot, half, table_rows;
   float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack_bf16x2(w[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
+// Two groups of four columns: pairs 0, 1 and pairs 2, 3 (two columns an operation).
+struct Cols {
+  float2 f[4];
+  __device__ __forceinline__ void unpack(const uint2& a, const uint2& b) {
+    f[0] = unpack_bf16x2(a.x), f[1] = unpack_bf16x2(a.y), f[2] = unpack_bf16x2(b.x), f[3] = unpack_bf16x2(b.y);
+  }
+  __device__ __forceinline__ uint2 pack(int g) const {
+    return make_uint2(pack_bf16x2(f[2 * g].x, f[2 * g].y), pack_bf16x2(f[2 * g + 1].x, f[2 * g + 1].y));
+  }
+};
 
 // A lane's place in its group, the columns it holds and what turns them.
 template <int D, bool INTER>
 struct Lane {
   static constexpr int LPR = D / 8;  // lanes per row
-  int j;             // lane within the group: columns 8j .. 8j + 7
   uint32_t mask;     // the group's lanes
+  int a, b;          // first column of each of its two groups of four
   bool turned;       // its columns are rotated
-  int partner;       // warp lane holding the other member of each pair (half-split pairs)
-  float sign;        // half-split: -1 for the first member (y_a = z_a c - z_b s), +1 for the second
-  float c[8], s[8];  // interleaved: entries 0-3
+  int angle;         // first entry of the table's row it needs
+  // half-split: cosine and sine of pairs (column a + i, column b + i), i = 0, 1 and 2, 3;
+  // interleaved: of pairs (2 i, 2 i + 1) of the eight, i = 0 .. 3
+  float2 c[2], s[2];
 
   __device__ __forceinline__ void init(const NormRope& p) {
-    const int lane = threadIdx.x & 31;
-    j = lane % LPR;
+    const int lane = threadIdx.x & 31, j = lane % LPR;
     mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (lane - j);
-    turned = j * 8 < p.rot;
-    const bool first = j * 8 < p.half;
-    partner = turned ? lane + (first ? p.half / 8 : -(p.half / 8)) : lane;
-    sign = first ? -1.f : 1.f;
+    turned = 8 * j < p.rot;
+    if (INTER || !turned) {  // eight neighbours; rows of rot columns are half-split over lanes 0 .. rot / 8 - 1
+      a = 8 * j;
+      b = a + 4;
+    } else {
+      a = 4 * j;
+      b = a + p.half;
+    }
+    angle = 4 * j;
   }
 
   __device__ __forceinline__ void load_angles(const NormRope& p, int pos) {
     if (!turned) return;
-    const size_t row = static_cast<size_t>(pos) * p.half;
-    if (INTER) {
-      const float4 a = ldg_f4(p.cos_t + row + j * 4), b = ldg_f4(p.sin_t + row + j * 4);
-      c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-      s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
-    } else {
-      const int i0 = j * 8 < p.half ? j * 8 : j * 8 - p.half;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 a = ldg_f4(p.cos_t + row + i0 + 4 * q), b = ldg_f4(p.sin_t + row + i0 + 4 * q);
-        c[4 * q] = a.x, c[4 * q + 1] = a.y, c[4 * q + 2] = a.z, c[4 * q + 3] = a.w;
-        s[4 * q] = b.x, s[4 * q + 1] = b.y, s[4 * q + 2] = b.z, s[4 * q + 3] = b.w;
-      }
-    }
+    const size_t at = static_cast<size_t>(pos) * p.half + angle;
+    const float4 x = ldg_f4(p.cos_t + at), y = ldg_f4(p.sin_t + at);
+    c[0] = make_float2(x.x, x.y), c[1] = make_float2(x.z, x.w);
+    s[0] = make_float2(y.x, y.y), s[1] = make_float2(y.z, y.w);
   }
 
-  // z <- R z (BACK: R^T z). Every lane of the group calls it.
+  // z <- R z (BACK: R^T z)
   template <bool BACK>
-  __device__ __forceinline__ void rotate(const NormRope& p, float (&z)[8]) const {
-    if (p.rot == 0) return;
-    if (INTER) {
-      if (!turned) return;
+  __device__ __forceinline__ void rotate(Cols& z) const {
+    if (!turned) return;
+    const float back = BACK ? -1.f : 1.f;
+    if (INTER) {  // (x, y) -> (x, y) c + (-y, x) s
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = z[2 * i], b = z[2 * i + 1], sn = BACK ? -s[i] : s[i];
-        z[2 * i] = a * c[i] - b * sn;
-        z[2 * i + 1] = b * c[i] + a * sn;
+        const float cc = i & 1 ? c[i / 2].y : c[i / 2].x, ss = (i & 1 ? s[i / 2].y : s[i / 2].x) * back;
+        z.f[i] = fma2(z.f[i], both(cc), fmul2(make_float2(z.f[i].y, z.f[i].x), make_float2(-ss, ss)));
       }
     } else {
-      const float sg = BACK ? -sign : sign;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(mask, z[i], partner);
-        if (turned) z[i] = z[i] * c[i] + sg * o * s[i];
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = z.f[i], y = z.f[2 + i], ss = make_float2(s[i].x * back, s[i].y * back);
+        z.f[i] = fma2(x, c[i], fmul2(y, make_float2(-ss.x, -ss.y)));
+        z.f[2 + i] = fma2(y, c[i], fmul2(x, ss));
       }
     }
   }
@@ -130,24 +139,36 @@ struct Lane {
     for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
     return v;
   }
-};
 
-__device__ __forceinline__ void load_weights(const NormRope& p, int kind, int j, float (&w)[8]) {
-  if (p.w_bf16) {
-    unpack8(__ldg(static_cast<const uint4*>(p.w[kind]) + j), w);
-  } else {
-    const float4 a = ldg_f4(static_cast<const float*>(p.w[kind]) + 8 * j);
-    const float4 b = ldg_f4(static_cast<const float*>(p.w[kind]) + 8 * j + 4);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, uint2 (&x)[2]) const {
+    x[0] = __ldg(reinterpret_cast<const uint2*>(row + a));
+    x[1] = __ldg(reinterpret_cast<const uint2*>(row + b));
   }
-}
+  __device__ __forceinline__ void store(__nv_bfloat16* row, const uint2& x, const uint2& y) const {
+    *reinterpret_cast<uint2*>(row + a) = x;
+    *reinterpret_cast<uint2*>(row + b) = y;
+  }
+  __device__ __forceinline__ void load_weights(const NormRope& p, int kind, float2 (&w)[4]) const {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int col = g ? b : a;
+      if (p.w_bf16) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.w[kind]) + col));
+        w[2 * g] = unpack_bf16x2(v.x), w[2 * g + 1] = unpack_bf16x2(v.y);
+      } else {
+        const float4 v = ldg_f4(static_cast<const float*>(p.w[kind]) + col);
+        w[2 * g] = make_float2(v.x, v.y), w[2 * g + 1] = make_float2(v.z, v.w);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ int position(const NormRope& p, int token, int n) {
   return p.positions ? __ldg(p.positions + token) : n;
 }
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
+template <int D, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
   Lane<D, INTER> L;
   L.init(p);
   const int upt = p.chunks[0] + p.chunks[1] + p.chunks[2];
@@ -159,167 +180,189 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const __grid_co
   while (ch >= p.chunks[kind]) ch -= p.chunks[kind++];
   const int b = token / p.N, n = token - b * p.N;
   const int h0 = ch * kHeads, nh = min(kHeads, p.H[kind] - h0);
-  const __nv_bfloat16* src = p.x[kind] + b * p.xs[kind][0] + h0 * p.xs[kind][1] + n * p.xs[kind][2] + L.j * 8;
-  uint4 raw[kHeads];
+  const __nv_bfloat16* src = p.x[kind] + b * p.xs[kind][0] + h0 * p.xs[kind][1] + n * p.xs[kind][2];
+  uint2 raw[kHeads][2];
 #pragma unroll
   for (int u = 0; u < kHeads; ++u)
-    if (u < nh) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + u * p.xs[kind][1]));
+    if (u < nh) L.load(src + u * p.xs[kind][1], raw[u]);
   const size_t head = static_cast<size_t>(b) * p.H[kind] + h0;
-  __nv_bfloat16* dst = p.y[kind] + (head * p.N + n) * D + L.j * 8;
+  __nv_bfloat16* dst = p.y[kind] + (head * p.N + n) * D;
   const size_t step = static_cast<size_t>(p.N) * D;
   if (kind == 2) {
 #pragma unroll
     for (int u = 0; u < kHeads; ++u)
-      if (u < nh) *reinterpret_cast<uint4*>(dst + u * step) = raw[u];
+      if (u < nh) L.store(dst + u * step, raw[u][0], raw[u][1]);
     return;
   }
   if (p.rot > 0) {
     const int pos = position(p, token, n);
     if (pos < 0 || pos >= p.table_rows) {
-      if (L.j == 0) record_bad_index(p.status, WHERE_NORM_ROPE);
+      if (L.angle == 0) record_bad_index(p.status, WHERE_NORM_ROPE);
       return;
     }
     L.load_angles(p, pos);
   }
-  const bool norm = p.w[0] != nullptr;
-  float w[8];
-  if (norm) load_weights(p, kind, L.j, w);
+  float2 w[4];
+  if (NORM) L.load_weights(p, kind, w);
 #pragma unroll
   for (int u = 0; u < kHeads; ++u) {
     if (u >= nh) break;
-    float z[8];
-    unpack8(raw[u], z);
-    if (norm) {
-      float ss = 0.f;
+    Cols z;
+    z.unpack(raw[u][0], raw[u][1]);
+    if (NORM) {
+      float2 ss = fmul2(z.f[0], z.f[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(z[i], z[i], ss);
-      const float r = rsqrtf(L.sum(ss) * (1.f / D) + p.eps);
+      for (int i = 1; i < 4; ++i) ss = fma2(z.f[i], z.f[i], ss);
+      const float r = rsqrtf(L.sum(ss.x + ss.y) * (1.f / D) + p.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = z[i] * r * w[i];
+      for (int i = 0; i < 4; ++i) z.f[i] = fmul2(fmul2(z.f[i], both(r)), w[i]);
     }
-    L.template rotate<false>(p, z);
-    *reinterpret_cast<uint4*>(dst + u * step) = pack8(z);
+    L.template rotate<false>(z);
+    L.store(dst + u * step, z.pack(0), z.pack(1));
   }
 }
 
-// Persistent: a block walks the q rows, then the k rows, then copies the v
-// rows. Each lane sums dw of its 8 columns over the rows it meets; the block's
-// lane groups are added in order, and norm_rope_dw_kernel adds the blocks in
-// order, so dw does not depend on timing.
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
-  constexpr int GROUPS = kThreads / (D / 8);
+// Persistent: the blocks are shared out over q, k and v by their work, and a
+// lane group takes up to kBwdHeads heads of one token, two at a time with the
+// next two on their way. Each lane sums dw of its 8 columns over the rows it
+// meets; the block's lane groups are added in order, and norm_rope_dw_kernel
+// adds the blocks in order, so dw does not depend on timing.
+template <int D, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
+  constexpr int GROUPS = kThreads / (D / 8), SIDE = kBwdSide;
   __shared__ float red[GROUPS][D];
   griddep_launch_dependents();
   Lane<D, INTER> L;
   L.init(p);
   const int group = threadIdx.x / L.LPR;
-  const bool norm = p.w[0] != nullptr;
-  const size_t step = static_cast<size_t>(p.N) * D;
-  for (int kind = 0; kind < 3; ++kind) {
-    const long long units = static_cast<long long>(p.tokens) * p.chunks[kind];
-    float dw[8] = {}, w[8];
-    if (norm && kind < 2) load_weights(p, kind, L.j, w);
-    for (long long unit = static_cast<long long>(blockIdx.x) * GROUPS + group; unit < units;
-         unit += static_cast<long long>(gridDim.x) * GROUPS) {
-      const int token = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(p.chunks[kind]));
-      const int ch = static_cast<int>(unit) - token * p.chunks[kind];
-      const int b = token / p.N, n = token - b * p.N;
-      const int h0 = ch * kHeads, nh = min(kHeads, p.H[kind] - h0);
-      const __nv_bfloat16* gy = p.dy[kind] + ((static_cast<size_t>(b) * p.H[kind] + h0) * p.N + n) * D + L.j * 8;
-      __nv_bfloat16* out = p.dx[kind] + b * p.ds[kind][0] + h0 * p.ds[kind][1] + n * p.ds[kind][2] + L.j * 8;
-      const __nv_bfloat16* src =
-          norm && kind < 2 ? p.x[kind] + b * p.xs[kind][0] + h0 * p.xs[kind][1] + n * p.xs[kind][2] + L.j * 8 : nullptr;
-      uint4 rg[kHeads], rx[kHeads];
+  int block = blockIdx.x, kind = 0;
+  while (block >= p.blocks[kind]) block -= p.blocks[kind++];
+  const int chunks = p.chunks[kind], heads = p.H[kind], n_blocks = p.blocks[kind];
+  const long long units = static_cast<long long>(p.tokens) * chunks;
+  const long long step = static_cast<long long>(p.N) * D, x_step = p.xs[kind][1], d_step = p.ds[kind][1];
+  const bool norm = NORM && kind < 2;
+  float2 dw[4], w[4];
 #pragma unroll
-      for (int u = 0; u < kHeads; ++u)
-        if (u < nh) {
-          rg[u] = __ldg(reinterpret_cast<const uint4*>(gy + u * step));
-          if (src) rx[u] = __ldg(reinterpret_cast<const uint4*>(src + u * p.xs[kind][1]));
+  for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
+  if (norm) L.load_weights(p, kind, w);
+#pragma unroll 1
+  for (long long unit = static_cast<long long>(block) * GROUPS + group; unit < units;
+       unit += static_cast<long long>(n_blocks) * GROUPS) {
+    const int token = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks));
+    const int h0 = (static_cast<int>(unit) - token * chunks) * kBwdHeads, nh = min(kBwdHeads, heads - h0);
+    const int b = token / p.N, n = token - b * p.N;
+    const __nv_bfloat16* gy = p.dy[kind] + (static_cast<size_t>(b) * heads + h0) * step + static_cast<size_t>(n) * D;
+    const __nv_bfloat16* src = norm ? p.x[kind] + b * p.xs[kind][0] + h0 * x_step + n * p.xs[kind][2] : nullptr;
+    __nv_bfloat16* out = p.dx[kind] + b * p.ds[kind][0] + h0 * d_step + n * p.ds[kind][2];
+    uint2 g_raw[SIDE][2], x_raw[SIDE][2];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u)
+        if (h + u < nh) {
+          L.load(gy + (h + u) * step, g_raw[u]);
+          if (norm) L.load(src + (h + u) * x_step, x_raw[u]);
         }
-      if (kind == 2) {
-#pragma unroll
-        for (int u = 0; u < kHeads; ++u)
-          if (u < nh) *reinterpret_cast<uint4*>(out + u * p.ds[kind][1]) = rg[u];
+    };
+    fetch(0);
+    if (kind < 2 && p.rot > 0) {
+      const int pos = position(p, token, n);
+      if (pos < 0 || pos >= p.table_rows) {
+        if (L.angle == 0) record_bad_index(p.status, WHERE_NORM_ROPE_BWD);
         continue;
       }
-      if (p.rot > 0) {
-        const int pos = position(p, token, n);
-        if (pos < 0 || pos >= p.table_rows) {
-          if (L.j == 0) record_bad_index(p.status, WHERE_NORM_ROPE_BWD);
+      L.load_angles(p, pos);
+    }
+#pragma unroll 1
+    for (int h = 0; h < nh; h += SIDE) {
+      uint2 g_now[SIDE][2], x_now[SIDE][2];
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          g_now[u][e] = g_raw[u][e];
+          if (norm) x_now[u][e] = x_raw[u][e];
+        }
+      fetch(h + SIDE);
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u) {
+        if (h + u >= nh) break;
+        __nv_bfloat16* row = out + (h + u) * d_step;
+        if (kind == 2) {
+          L.store(row, g_now[u][0], g_now[u][1]);
           continue;
         }
-        L.load_angles(p, pos);
-      }
+        Cols g;
+        g.unpack(g_now[u][0], g_now[u][1]);
+        L.template rotate<true>(g);
+        if (NORM) {
+          Cols x, gw;
+          x.unpack(x_now[u][0], x_now[u][1]);
+          float2 ss = fmul2(x.f[0], x.f[0]), hx = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < kHeads; ++u) {
-        if (u >= nh) break;
-        float g[8];
-        unpack8(rg[u], g);
-        L.template rotate<true>(p, g);
-        if (norm) {
-          float x[8], ss = 0.f, hx = 0.f;
-          unpack8(rx[u], x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(x[i], x[i], ss);
-            hx = fmaf(g[i] * w[i], x[i], hx);
+          for (int i = 0; i < 4; ++i) {
+            if (i > 0) ss = fma2(x.f[i], x.f[i], ss);
+            gw.f[i] = fmul2(g.f[i], w[i]);
+            hx = fma2(gw.f[i], x.f[i], hx);
           }
-          const float r = rsqrtf(L.sum(ss) * (1.f / D) + p.eps);
-          const float m = L.sum(hx) * (1.f / D) * r * r;
+          const float r = rsqrtf(L.sum(ss.x + ss.y) * (1.f / D) + p.eps);
+          const float m = -L.sum(hx.x + hx.y) * (1.f / D) * r * r * r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dw[i] = fmaf(g[i] * r, x[i], dw[i]);
-            g[i] = r * (g[i] * w[i] - x[i] * m);
+          for (int i = 0; i < 4; ++i) {
+            dw[i] = fma2(fmul2(g.f[i], both(r)), x.f[i], dw[i]);
+            g.f[i] = fma2(gw.f[i], both(r), fmul2(x.f[i], both(m)));
           }
         }
-        *reinterpret_cast<uint4*>(out + u * p.ds[kind][1]) = pack8(g);
+        L.store(row, g.pack(0), g.pack(1));
       }
     }
-    if (norm && kind < 2) {
+  }
+  if (norm) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) red[group][L.j * 8 + i] = dw[i];
-      __syncthreads();
-      for (int col = threadIdx.x; col < D; col += kThreads) {
-        float t = 0.f;
-        for (int g = 0; g < GROUPS; ++g) t += red[g][col];
-        p.part[(static_cast<size_t>(kind) * gridDim.x + blockIdx.x) * D + col] = t;
-      }
-      __syncthreads();
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float2*>(&red[group][(i < 2 ? L.a : L.b - 4) + 2 * i]) = dw[i];
+    __syncthreads();
+    for (int col = threadIdx.x; col < D; col += kThreads) {
+      float t = 0.f;
+      for (int g = 0; g < GROUPS; ++g) t += red[g][col];
+      p.part[static_cast<size_t>(blockIdx.x) * D + col] = t;
     }
   }
 }
 
-// dw[kind][col] = sum over the blocks of their partial sums, in block order
-// within each of 8 interleaved runs, in 64 bits. One block per 32 columns.
-__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* __restrict__ part, float* dwq, float* dwk,
-                                                           int blocks, int D) {
-  __shared__ double red[8][32];
+// dw[kind][col] = sum over the blocks of their partial sums, in 32 interleaved
+// runs of them in block order, in 64 bits. One block per 32 columns.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, float* dwq, float* dwk,
+                                                            int q_blocks, int k_blocks, int D) {
+  __shared__ double red[32][32];
   griddep_wait();  // launched to overlap the pass that writes the partial sums
   const int col = blockIdx.x * 32 + threadIdx.x, kind = blockIdx.y;
+  const int begin = kind ? q_blocks : 0, end = kind ? q_blocks + k_blocks : q_blocks;
   double t = 0.0;
-  for (int i = threadIdx.y; i < blocks; i += 8) t += part[(static_cast<size_t>(kind) * blocks + i) * D + col];
+#pragma unroll 4
+  for (int i = begin + threadIdx.y; i < end; i += 32) t += part[static_cast<size_t>(i) * D + col];
   red[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
   if (threadIdx.y == 0) {
-    for (int i = 1; i < 8; ++i) t += red[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) t += red[i][threadIdx.x];
     (kind ? dwk : dwq)[col] = static_cast<float>(t);
   }
 }
 
 template <bool BACK>
 cudaError_t launch_norm_rope(const NormRope& a, int d, int interleaved, int blocks, cudaStream_t stream) {
-#define FA_NORM_ROPE(D)                                                                        \
-  if (d == D) {                                                                                \
-    auto kern = BACK ? (interleaved ? norm_rope_bwd_kernel<D, true> : norm_rope_bwd_kernel<D, false>) \
-                     : (interleaved ? norm_rope_fwd_kernel<D, true> : norm_rope_fwd_kernel<D, false>); \
-    kern<<<blocks, kThreads, 0, stream>>>(a);                                                  \
-    return cudaGetLastError();                                                                 \
+#define FA_NORM_ROPE_KERNEL(D, I, N) (BACK ? norm_rope_bwd_kernel<D, I, N> : norm_rope_fwd_kernel<D, I, N>)
+#define FA_NORM_ROPE(D)                                                                                     \
+  if (d == D) {                                                                                             \
+    auto kern = a.w[0] ? (interleaved ? FA_NORM_ROPE_KERNEL(D, true, true) : FA_NORM_ROPE_KERNEL(D, false, true)) \
+                       : (interleaved ? FA_NORM_ROPE_KERNEL(D, true, false) : FA_NORM_ROPE_KERNEL(D, false, false)); \
+    kern<<<blocks, kThreads, 0, stream>>>(a);                                                               \
+    return cudaGetLastError();                                                                              \
   }
   FA_NORM_ROPE(64)
   FA_NORM_ROPE(128)
   FA_NORM_ROPE(256)
 #undef FA_NORM_ROPE
+#undef FA_NORM_ROPE_KERNEL
   return cudaErrorInvalidValue;
 }
 
@@ -340,7 +383,7 @@ bool rows_apart(const int (&size)[3], const long long (&stride)[3], int d) {
 // Checks and arguments shared by the two directions.
 fa_status_t prepare(const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
                     const float* sin_t, int table_rows, const int* positions, int B, int Hq, int Hkv, int N, int d,
-                    int rot, int interleaved, float eps, bool with_v, bool* empty, NormRope* a) {
+                    int rot, int interleaved, float eps, bool with_v, int heads, bool* empty, NormRope* a) {
   if (B < 0 || Hq < 0 || Hkv < 0 || N < 0 || table_rows < 0) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
   if (rot < 0 || rot > d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
@@ -368,7 +411,7 @@ fa_status_t prepare(const long long* strides, const void* wq, const void* wk, in
   a->H[0] = Hq;
   a->H[1] = Hkv;
   a->H[2] = with_v ? Hkv : 0;
-  for (int t = 0; t < 3; ++t) a->chunks[t] = (a->H[t] + kHeads - 1) / kHeads;
+  for (int t = 0; t < 3; ++t) a->chunks[t] = (a->H[t] + heads - 1) / heads;
   a->rot = rot;
   a->half = rot / 2;
   a->table_rows = table_rows;
@@ -388,10 +431,17 @@ fa_status_t take_strides(const long long* s, int t, int B, int H, int N, long lo
   return FA_OK;
 }
 
-int bwd_blocks(const NormRope& a, int d, int num_sms) {
-  const int groups = kThreads / (d / 8);
-  const long long most = static_cast<long long>(a.tokens) * std::max(a.chunks[0], std::max(a.chunks[1], a.chunks[2]));
-  return static_cast<int>(std::min<long long>((most + groups - 1) / groups, std::min(4 * num_sms, kMaxBwdBlocks)));
+// Blocks for q, k and v: all that fit the device at once, by the bytes each
+// moves (q and k three rows a head with weights, else two), no more than
+// there are lane groups to fill. A kind without rows has none.
+void share_blocks(NormRope* a, int d, int num_sms) {
+  const int groups = kThreads / (d / 8), all = std::min(kBwdPerSm * num_sms, kMaxBwdBlocks);
+  double work[3], sum = 0.0;
+  for (int t = 0; t < 3; ++t) sum += work[t] = static_cast<double>(a->H[t]) * (a->w[0] && t < 2 ? 3 : 2);
+  for (int t = 0; t < 3; ++t) {
+    const long long most = (static_cast<long long>(a->tokens) * a->chunks[t] + groups - 1) / groups;
+    a->blocks[t] = static_cast<int>(std::min<long long>(most, std::max(1, static_cast<int>(all * work[t] / sum))));
+  }
 }
 
 }  // namespace
@@ -409,7 +459,7 @@ fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_i
   bool empty = false;
   if ((v_in == nullptr) != (v == nullptr)) return FA_ERR_INVALID_ARG;
   fa_status_t st = prepare(strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv, N, d, rot,
-                           interleaved, eps, v != nullptr, &empty, &a);
+                           interleaved, eps, v != nullptr, kHeads, &empty, &a);
   if (st != FA_OK || empty) return st;
   const void* in[3] = {q_in, k_in, v_in};
   void* out[3] = {q, k, v};
@@ -447,7 +497,7 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
   bool empty = false;
   if ((dv == nullptr) != (dv_in == nullptr)) return FA_ERR_INVALID_ARG;
   fa_status_t st = prepare(wq ? strides : out_strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv,
-                           N, d, rot, interleaved, eps, dv != nullptr, &empty, &a);
+                           N, d, rot, interleaved, eps, dv != nullptr, kBwdHeads, &empty, &a);
   if (st != FA_OK) return st;
   const bool norm = wq != nullptr;
   if (norm) {  // dw of no rows is still written: 0
@@ -492,19 +542,20 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
   }
   a.status = dev.status;
   a.part = static_cast<float*>(workspace);
-  const int blocks = bwd_blocks(a, d, dev.num_sms);
-  cudaError_t e = launch_norm_rope<true>(a, d, interleaved, blocks, stream);
+  share_blocks(&a, d, dev.num_sms);
+  cudaError_t e = launch_norm_rope<true>(a, d, interleaved, a.blocks[0] + a.blocks[1] + a.blocks[2], stream);
   if (e != cudaSuccess || !norm) return from_cuda(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(d / 32, 2);
-  cfg.blockDim = dim3(32, 8);
+  cfg.blockDim = dim3(32, 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return from_cuda(cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.part), dwq, dwk, blocks, d));
+  return from_cuda(cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.part), dwq, dwk,
+                                      a.blocks[0], a.blocks[1], d));
 }
 
 }  // extern "C"
