@@ -355,71 +355,91 @@ def rope_tables(rows: int, rot: int, base: float = 10000.0, device="cuda"):
     return angle.cos().float(), angle.sin().float()
 
 
-def _check_on_current_device(names: str, *tensors) -> None:
-    """Every tensor given is on the current CUDA device (the library launches there)."""
+# The wrappers below are called once per layer and token, so their checks are
+# written for the call that passes them: one expression over the tensors'
+# attributes. Only a call that fails it is looked at tensor by tensor, for its
+# message.
+def _refuse(named):
+    """Raise for the first of (name, tensor, dtypes, shape, contiguous) that is not as it should be."""
     import torch
+    for name, t, dtypes, shape, contiguous in named:
+        if t is None:
+            continue
+        if t.dtype not in dtypes:  # as for the other entry points: TypeError for values, ValueError for the rest
+            values = torch.bfloat16 in dtypes or torch.uint8 in dtypes or torch.float8_e4m3fn in dtypes
+            raise (TypeError if values else ValueError)(f"{name} must be {' or '.join(str(x)[6:] for x in dtypes)}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
     here = torch.cuda.current_device()
-    for i, t in enumerate(tensors):
+    for name, t, *_ in named:
         if t is not None and t.get_device() != here:
-            raise ValueError(f"{names.split()[i]} must be on the current CUDA device (cuda:{here}), got {t.device}")
+            raise ValueError(f"{name} must be on the current CUDA device (cuda:{here}), got {t.device}")
+    raise ValueError("tensors of one call must have matching types, shapes and devices")
 
 
-def _check_tensor(name, t, dtype, shape) -> None:
-    """A contiguous tensor of this type and shape (None passes; where it is, is checked for all at once)."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+def _devices(*tensors):
+    """Their CUDA devices (None for a tensor not given; -1: not on a GPU)."""
+    return {t.get_device() for t in tensors if t is not None}
 
 
 _Strides = ctypes.c_longlong * 9
-
-
-def _head_strides(name, t, shape):
-    """(batch, head, token) strides of a bf16 [B, H, N, d] tensor with contiguous rows."""
-    import torch
-    if t is None:
-        return 0, 0, 0
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    b, h, n, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return b, h, n
-
-
-def _norm_rope_args(B, N, d, wq, wk, cos, sin, positions):
-    """Checks shared by the two directions; returns the weights' type flag, the tables' rows and rot."""
-    import torch
-    if (wq is None) != (wk is None):
-        raise ValueError("wq and wk are given together or not at all")
-    w_bf16 = 0
-    if wq is not None:
-        w_bf16 = int(wq.dtype == torch.bfloat16)
-        _check_tensor("wq", wq, torch.bfloat16 if w_bf16 else torch.float32, (d,))
-        _check_tensor("wk", wk, wq.dtype, (d,))
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin are given together or not at all")
-    rows = rot = 0
-    if cos is not None:
-        if cos.dim() != 2:
-            raise ValueError("cos and sin must be [rows, rot / 2] tensors")
-        rows, rot = cos.shape
-        rot *= 2
-        _check_tensor("cos", cos, torch.float32, cos.shape)
-        _check_tensor("sin", sin, torch.float32, cos.shape)
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape != (B, N) or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 tensor of shape {(B, N)}")
-    return w_bf16, rows, rot
+_NO_STRIDES = (0, 0, 0, 1)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _norm_rope_named(B, Hq, Hkv, N, d, qkv, strided, w, cos, sin, positions, dw, workspace):
+    import torch
+    bf, f32 = (torch.bfloat16,), (torch.float32,)
+    qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
+    named = [(n, t, bf, s, True) for (n, t), s in zip(qkv, (qs, ks, ks))]
+    named += [(n, t, bf, qs if n.lstrip("d")[0] == "q" else ks, False) for n, t in strided]
+    named += [(n, t, (torch.float32, torch.bfloat16) if w[0][1] is None else (w[0][1].dtype,), (d,), True) for n, t in w]
+    if cos is not None:
+        named += [(n, t, f32, cos.shape, True) for n, t in (("cos", cos), ("sin", sin))]
+    named += [(n, t, f32, (d,), True) for n, t in dw]
+    if positions is not None:
+        named.append(("positions", positions, (torch.int32,), (B, N), True))
+    if workspace is not None:
+        named.append(("workspace", workspace, (torch.uint8,), workspace.shape, True))
+    return named
+
+
+def _norm_rope_tables(wq, wk, cos, sin):
+    """The weights' type flag, the tables' rows and rot."""
+    import torch
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk are given together or not at all")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin are given together or not at all")
+    w_bf16 = 0
+    if wq is not None:
+        if wq.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"wq must be float32 or bfloat16, got {wq.dtype}")
+        w_bf16 = int(wq.dtype == torch.bfloat16)
+    if cos is None:
+        return w_bf16, 0, 0
+    if cos.dim() != 2:
+        raise ValueError("cos and sin must be [rows, rot / 2] tensors")
+    rows, half = cos.shape
+    return w_bf16, rows, 2 * half
+
+
+def _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d):
+    """Are the tensors the two directions share as they should be?"""
+    import torch
+    return ((wq is None or (wk.dtype == wq.dtype and wq.shape == wk.shape == (d,) and wq.is_contiguous()
+                            and wk.is_contiguous()))
+            and (cos is None or (cos.dtype == sin.dtype == torch.float32 and cos.shape == sin.shape
+                                 and cos.is_contiguous() and sin.is_contiguous()))
+            and (positions is None or (positions.dtype == torch.int32 and positions.shape == (B, N)
+                                       and positions.is_contiguous())))
 
 
 def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved: bool = False,
@@ -431,25 +451,29 @@ def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, int
     None: no values. positions None: token n is at position n.
     """
     import torch
-    if q_in.dim() != 4 or k_in.dim() != 4:
+    bf = torch.bfloat16
+    qs, ks = q_in.shape, k_in.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("expected [B, H, N, d] tensors")
-    B, Hq, N, d = q_in.shape
-    Hkv = k_in.shape[1]
-    qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
     if (v_in is None) != (v is None):
         raise ValueError("v_in and v are given together or not at all")
-    w_bf16, rows, rot = _norm_rope_args(B, N, d, wq, wk, cos, sin, positions)
-    strides = _Strides(*_head_strides("q_in", q_in, qs), *_head_strides("k_in", k_in, ks),
-                       *_head_strides("v_in", v_in, ks))
-    _check_tensor("q", q, torch.bfloat16, qs)
-    _check_tensor("k", k, torch.bfloat16, ks)
-    _check_tensor("v", v, torch.bfloat16, ks)
-    _check_on_current_device("q_in k_in v_in wq wk cos sin positions q k v", q_in, k_in, v_in, wq, wk, cos, sin,
-                             positions, q, k, v)
+    B, Hq, N, d = qs
+    Hkv = ks[1]
+    w_bf16, rows, rot = _norm_rope_tables(wq, wk, cos, sin)
+    sq, sk, sv = q_in.stride(), k_in.stride(), _NO_STRIDES if v_in is None else v_in.stride()
+    if not (q_in.dtype == k_in.dtype == q.dtype == k.dtype == bf and q.shape == qs and k.shape == ks
+            and ks == (B, Hkv, N, d) and sq[3] == sk[3] == 1 and q.is_contiguous() and k.is_contiguous()
+            and (v is None or (v_in.dtype == v.dtype == bf and v_in.shape == v.shape == ks and sv[3] == 1
+                               and v.is_contiguous()))
+            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d)
+            and _devices(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v) == {torch.cuda.current_device()}):
+        _refuse(_norm_rope_named(B, Hq, Hkv, N, d, (("q", q), ("k", k), ("v", v)),
+                                 (("q_in", q_in), ("k_in", k_in), ("v_in", v_in)), (("wq", wq), ("wk", wk)), cos, sin,
+                                 positions, (), None))
     check("fa_norm_rope_fwd", load().fa_norm_rope_fwd(
-        q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos), _ptr(sin), rows,
-        _ptr(positions), q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d, rot, int(bool(interleaved)), eps,
-        _stream_handle(stream)))
+        q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(wq), _ptr(wk), w_bf16,
+        _ptr(cos), _ptr(sin), rows, _ptr(positions), q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d, rot,
+        1 if interleaved else 0, eps, _stream_handle(stream)))
 
 
 def fa_norm_rope_bwd_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
@@ -465,49 +489,68 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
     Without weights q_in, k_in, dwq, dwk and workspace are not used.
     """
     import torch
-    if dq.dim() != 4 or dk.dim() != 4:
+    bf = torch.bfloat16
+    qs, ks = dq.shape, dk.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("expected [B, H, N, d] tensors")
-    B, Hq, N, d = dq.shape
-    Hkv = dk.shape[1]
-    qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
     if (dv is None) != (dv_in is None):
         raise ValueError("dv and dv_in are given together or not at all")
-    w_bf16, rows, rot = _norm_rope_args(B, N, d, wq, wk, cos, sin, positions)
-    out_strides = _Strides(*_head_strides("dq_in", dq_in, qs), *_head_strides("dk_in", dk_in, ks),
-                           *_head_strides("dv_in", dv_in, ks))
-    strides = None
-    if wq is not None:
-        strides = _Strides(*_head_strides("q_in", q_in, qs), *_head_strides("k_in", k_in, ks))
-        _check_tensor("dwq", dwq, torch.float32, (d,))
-        _check_tensor("dwk", dwk, torch.float32, (d,))
-    _check_tensor("dq", dq, torch.bfloat16, qs)
-    _check_tensor("dk", dk, torch.bfloat16, ks)
-    _check_tensor("dv", dv, torch.bfloat16, ks)
-    _check_on_current_device("dq dk dv q_in k_in wq wk cos sin positions dq_in dk_in dv_in dwq dwk workspace", dq, dk,
-                             dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk, workspace)
+    B, Hq, N, d = qs
+    Hkv = ks[1]
+    w_bf16, rows, rot = _norm_rope_tables(wq, wk, cos, sin)
+    if wq is None:
+        q_in = k_in = dwq = dwk = None
+    sq, sk, sv = dq_in.stride(), dk_in.stride(), _NO_STRIDES if dv is None else dv_in.stride()
+    xq, xk = (_NO_STRIDES, _NO_STRIDES) if wq is None else (q_in.stride(), k_in.stride())
+    if not (dq.dtype == dk.dtype == dq_in.dtype == dk_in.dtype == bf and dq_in.shape == qs and dk_in.shape == ks
+            and ks == (B, Hkv, N, d) and sq[3] == sk[3] == 1 and dq.is_contiguous() and dk.is_contiguous()
+            and (dv is None or (dv_in.dtype == dv.dtype == bf and dv_in.shape == dv.shape == ks and sv[3] == 1
+                                and dv.is_contiguous()))
+            and (wq is None or (q_in.dtype == k_in.dtype == bf and q_in.shape == qs and k_in.shape == ks
+                                and xq[3] == xk[3] == 1 and dwq.dtype == dwk.dtype == torch.float32
+                                and dwq.shape == dwk.shape == (d,) and dwq.is_contiguous() and dwk.is_contiguous()))
+            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d)
+            and _devices(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk,
+                         workspace) == {torch.cuda.current_device()}):
+        _refuse(_norm_rope_named(B, Hq, Hkv, N, d, (("dq", dq), ("dk", dk), ("dv", dv)),
+                                 (("dq_in", dq_in), ("dk_in", dk_in), ("dv_in", dv_in), ("q_in", q_in), ("k_in", k_in)),
+                                 (("wq", wq), ("wk", wk)), cos, sin, positions, (("dwq", dwq), ("dwk", dwk)), workspace))
     check("fa_norm_rope_bwd", load().fa_norm_rope_bwd(
-        dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), strides, _ptr(wq), _ptr(wk), w_bf16, _ptr(cos),
-        _ptr(sin), rows, _ptr(positions), dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in), out_strides, _ptr(dwq),
-        _ptr(dwk), B, Hq, Hkv, N, d, rot, int(bool(interleaved)), eps, *_ws(workspace), _stream_handle(stream)))
+        dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), _Strides(*xq[:3], *xk[:3]), _ptr(wq), _ptr(wk),
+        w_bf16, _ptr(cos), _ptr(sin), rows, _ptr(positions), dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in),
+        _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(dwq), _ptr(dwk), B, Hq, Hkv, N, d, rot, 1 if interleaved else 0, eps,
+        *_ws(workspace), _stream_handle(stream)))
 
 
-def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts):
-    """Checks of a paged 8-bit cache; returns (B, Hkv, d, page, num_pages, max_pages)."""
+def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, *rows):
+    """Checks of a paged 8-bit cache and of the call's own bf16 tensors (name, tensor, heads,
+    tokens); returns (B, Hkv, d, page, num_pages, max_pages)."""
     import torch
-    if k_cache.dim() != 4 or page_table.dim() != 2:
+    shape, B_pages = k_cache.shape, page_table.shape
+    if len(shape) != 4 or len(B_pages) != 2:
         raise ValueError("k_cache must be [num_pages, Hkv, page, d] and page_table [B, max_pages]")
-    shape = k_cache.shape
     pages, Hkv, page, d = shape
-    B, max_pages = page_table.shape
-    if k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
-        raise TypeError(f"k_cache must be uint8 or float8_e4m3fn, got {k_cache.dtype}")
-    _check_tensor("k_cache", k_cache, k_cache.dtype, shape)
-    _check_tensor("v_cache", v_cache, k_cache.dtype, shape)
-    _check_tensor("k_scale", k_scale, torch.float32, (pages, Hkv))
-    _check_tensor("v_scale", v_scale, torch.float32, (pages, Hkv))
-    for name, t, want in (("page_table", page_table, (B, max_pages)), ("lens", lens, (B,)), ("counts", counts, (B,))):
-        if t is not None and (t.dtype != torch.int32 or t.shape != want or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {want}")
+    B, max_pages = B_pages
+    i32, per_head = torch.int32, (pages, Hkv)
+    tensors = [t for _, t, _, _ in rows]
+    if not (v_cache.dtype == k_cache.dtype and v_cache.shape == shape and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+            and k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.shape == v_scale.shape == per_head
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and page_table.dtype == lens.dtype == i32 and page_table.is_contiguous() and lens.shape == (B,)
+            and lens.is_contiguous()
+            and (counts is None or (counts.dtype == i32 and counts.shape == (B,) and counts.is_contiguous()))
+            and all([t.dtype == torch.bfloat16 and t.shape == (B, heads, n, d) and t.is_contiguous()
+                     for _, t, heads, n in rows])
+            and _devices(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, *tensors)
+            == {torch.cuda.current_device()}):
+        code = (torch.uint8, torch.float8_e4m3fn)
+        _refuse([("k_cache", k_cache, code, shape, True), ("v_cache", v_cache, (k_cache.dtype,), shape, True),
+                 ("k_scale", k_scale, (torch.float32,), per_head, True),
+                 ("v_scale", v_scale, (torch.float32,), per_head, True),
+                 ("page_table", page_table, (i32,), B_pages, True), ("lens", lens, (i32,), (B,), True),
+                 ("counts", counts, (i32,), (B,), True)]
+                + [(name, t, (torch.bfloat16,), (B, heads, n, d), True) for name, t, heads, n in rows])
     return B, Hkv, d, page, pages, max_pages
 
 
@@ -519,13 +562,11 @@ def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
     v_scale float32 [num_pages, Hkv]; page_table int32 [B, max_pages]; lens,
     counts int32 [B].
     """
-    import torch
-    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
-    n = k.shape[2] if k.dim() == 4 else 0
-    _check_tensor("k", k, torch.bfloat16, (B, Hkv, n, d))
-    _check_tensor("v", v, torch.bfloat16, (B, Hkv, n, d))
-    _check_on_current_device("k v k_cache v_cache k_scale v_scale page_table lens counts", k, v, k_cache, v_cache,
-                             k_scale, v_scale, page_table, lens, counts)
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    n, heads = k.shape[2], k_cache.shape[1]
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts,
+                                                  ("k", k, heads, n), ("v", v, heads, n))
     check("fa_kv8_append", load().fa_kv8_append(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(), _ptr(counts), B, Hkv, n, d, page, pages, max_pages,
@@ -535,13 +576,11 @@ def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
 def fa_kv8_gather(k_cache, v_cache, k_scale, v_scale, page_table, lens, k, v, stream=None) -> None:
     """fa_kv8_gather of the C ABI: rows [0, min(lens[b], n)) of each sequence back as bf16 into
     k, v [B, Hkv, n, d]; later rows are left as they were."""
-    import torch
-    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, None)
-    n = k.shape[2] if k.dim() == 4 else 0
-    _check_tensor("k", k, torch.bfloat16, (B, Hkv, n, d))
-    _check_tensor("v", v, torch.bfloat16, (B, Hkv, n, d))
-    _check_on_current_device("k_cache v_cache k_scale v_scale page_table lens k v", k_cache, v_cache, k_scale, v_scale,
-                             page_table, lens, k, v)
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    n, heads = k.shape[2], k_cache.shape[1]
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, None,
+                                                  ("k", k, heads, n), ("v", v, heads, n))
     check("fa_kv8_gather", load().fa_kv8_gather(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
         lens.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, n, d, page, pages, max_pages, _stream_handle(stream)))
@@ -560,22 +599,21 @@ def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, 
     workspace is a CUDA uint8 tensor of at least fa_fwd_kv8_workspace_size() bytes.
     """
     import torch
-    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts)
     if q.dim() != 4:
         raise ValueError("expected [B, H, N, d] tensors")
     _, Hq, Nq, _ = q.shape
+    B, Hkv, d, page, pages, max_pages = _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts,
+                                                  ("q", q, Hq, Nq), ("o", o, Hq, Nq))
     if Hkv < 1 or Hq % Hkv != 0:
         raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
-    _check_tensor("q", q, torch.bfloat16, (B, Hq, Nq, d))
-    _check_tensor("o", o, torch.bfloat16, (B, Hq, Nq, d))
-    if lse.dtype != torch.float32 or lse.shape != (B, Hq, Nq) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 tensor of shape [B, Hq, Nq]")
-    _check_on_current_device("q k_cache v_cache k_scale v_scale page_table lens counts o lse workspace", q, k_cache,
-                             v_cache, k_scale, v_scale, page_table, lens, counts, o, lse, workspace)
+    if not (lse.dtype == torch.float32 and lse.shape == (B, Hq, Nq) and lse.is_contiguous()
+            and _devices(q, lse, workspace) == {q.get_device()}):
+        _refuse((("lse", lse, (torch.float32,), (B, Hq, Nq), True),
+                 ("workspace", workspace, (torch.uint8,), () if workspace is None else workspace.shape, True)))
     check("fa_fwd_kv8", load().fa_fwd_kv8(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(), _ptr(counts), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page,
-        pages, max_pages, int(bool(causal)), scale, *_ws(workspace), _stream_handle(stream)))
+        pages, max_pages, 1 if causal else 0, scale, *_ws(workspace), _stream_handle(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:
