@@ -52,19 +52,13 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_const
   const int p = start / PAGE + t;  // page of the sequence
   const int first = max(start, p * PAGE), last = min(len, (p + 1) * PAGE);
   if (first >= last) return;
-  const int pid = __ldg(c.table + static_cast<size_t>(b) * c.max_pages + p);
-  if (pid < 0 || pid >= c.num_pages) {
-    if (threadIdx.x == 0) record_bad_index(status, WHERE_KV8_APPEND);
-    return;
-  }
   const int held = first - p * PAGE, end = last - p * PAGE;  // places [held, end) are written
-  const size_t slot = static_cast<size_t>(pid) * c.Hkv + h;
-  const float s_old = held > 0 ? c.scale[kv][slot] : 0.f;
   const int col = (threadIdx.x % LPR) * 8, row0 = threadIdx.x / LPR;
   const __nv_bfloat16* src =
       (kv ? v : k) + ((static_cast<size_t>(b) * c.Hkv + h) * n + (first - start)) * D + col;
+  const int pid = __ldg(c.table + static_cast<size_t>(b) * c.max_pages + p);
+  // The rows do not wait for the page's number: two latencies less a block.
   uint4 raw[PASSES];
-  uint32_t amax = 0;  // bits of the largest finite |value| (bf16 patterns order as integers)
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int place = row0 + i * ROWS;
@@ -72,6 +66,13 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_const
     if (place >= held && place < end)
       raw[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(place - held) * D));
   }
+  if (pid < 0 || pid >= c.num_pages) {
+    if (threadIdx.x == 0) record_bad_index(status, WHERE_KV8_APPEND);
+    return;
+  }
+  const size_t slot = static_cast<size_t>(pid) * c.Hkv + h;
+  const float s_old = held > 0 ? c.scale[kv][slot] : 0.f;
+  uint32_t amax = 0;  // bits of the largest finite |value| (bf16 patterns order as integers)
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
