@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
 
 // Joins the row blocks that CTAs shared. blockIdx.x = c > 0: the block that the
 // runs of CTAs c - 1 and c meet in, if c - 1 is the first that holds a part
-// of it; blockIdx.y: 32 of its rows. blockIdx.x = 0: sequences whose lengths or
+// of it; blockIdx.y: 8 of its rows. blockIdx.x = 0: sequences whose lengths or
 // counts are out of range, and rows that see no key at all.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p) {
@@ -907,48 +907,40 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_cons
   const int4 at = p.run[2 * c], held = p.run[2 * c + 1];
   const int c0 = held.x, c1 = held.y, count = held.w;
   if (c0 != c - 1) return;  // nothing is shared at this boundary, or another one's blocks join it
-  // A warp joins four rows side by side, part by part.
-  constexpr int PER = D / 32, SIDE = 4;
-  const int rb = blockIdx.y * 32 + warp * SIDE;
-  float m[SIDE], l[SIDE], a[SIDE][PER];
+  // A warp joins a row, four parts on their way at a time.
+  constexpr int PER = D / 32;
+  const int rb = blockIdx.y * 8 + warp, row = at.z * C::ROWS + rb, qi = row / p.g;
+  if (qi >= count) return;
+  float m = -INFINITY, l = 0.f, a[PER];
 #pragma unroll
-  for (int e = 0; e < SIDE; ++e) {
-    m[e] = -INFINITY;
-    l[e] = 0.f;
+  for (int k = 0; k < PER; ++k) a[k] = 0.f;
+  for (int u0 = c0; u0 <= c1; u0 += 4) {
+    float2 ml[4], x[4][PER / 2];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) a[e][k] = 0.f;
-  }
-  for (int u = c0; u <= c1; ++u) {
-    const size_t slot = (static_cast<size_t>(u) * 2 + (u == c0 ? held.z : 0)) * C::ROWS + rb;
-    float2 ml[SIDE], x[SIDE][PER / 2];
+    for (int e = 0; e < 4; ++e) {
+      const int u = min(u0 + e, c1);
+      const size_t slot = (static_cast<size_t>(u) * 2 + (u == c0 ? held.z : 0)) * C::ROWS + rb;
+      ml[e] = p.part_ml[slot];
 #pragma unroll
-    for (int e = 0; e < SIDE; ++e) {
-      ml[e] = p.part_ml[slot + e];
-#pragma unroll
-      for (int k = 0; k < PER / 2; ++k)
-        x[e][k] = *reinterpret_cast<const float2*>(p.part + (slot + e) * D + lane * PER + 2 * k);
+      for (int k = 0; k < PER / 2; ++k) x[e][k] = *reinterpret_cast<const float2*>(p.part + slot * D + lane * PER + 2 * k);
     }
 #pragma unroll
-    for (int e = 0; e < SIDE; ++e) {
-      const float to = fmaxf(m[e], ml[e].x), ref = to == -INFINITY ? 0.f : to;
-      const float wa = ex2_approx(m[e] - ref), wx = ex2_approx(ml[e].x - ref);
-      m[e] = to;
-      l[e] = l[e] * wa + ml[e].y * wx;
+    for (int e = 0; e < 4; ++e) {
+      if (u0 + e > c1) break;
+      const float to = fmaxf(m, ml[e].x), ref = to == -INFINITY ? 0.f : to;
+      const float wa = ex2_approx(m - ref), wx = ex2_approx(ml[e].x - ref);
+      m = to;
+      l = l * wa + ml[e].y * wx;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) a[e][k] = a[e][k] * wa + (k & 1 ? x[e][k / 2].y : x[e][k / 2].x) * wx;
+      for (int k = 0; k < PER; ++k) a[k] = a[k] * wa + (k & 1 ? x[e][k / 2].y : x[e][k / 2].x) * wx;
     }
   }
+  const RowEnd end(m, l);
+  const size_t out = (static_cast<size_t>(at.x) * p.Hq + at.y * p.g + row % p.g) * p.Nq + qi;
 #pragma unroll
-  for (int e = 0; e < SIDE; ++e) {
-    const int row = at.z * C::ROWS + rb + e, qi = row / p.g;
-    if (qi >= count) break;
-    const RowEnd end(m[e], l[e]);
-    const size_t out = (static_cast<size_t>(at.x) * p.Hq + at.y * p.g + row % p.g) * p.Nq + qi;
-#pragma unroll
-    for (int k = 0; k < PER; k += 2)
-      *reinterpret_cast<uint32_t*>(p.o + out * D + lane * PER + k) = pack_bf16x2(end(a[e][k]), end(a[e][k + 1]));
-    if (lane == 0) p.lse[out] = end.lse;
-  }
+  for (int k = 0; k < PER; k += 2)
+    *reinterpret_cast<uint32_t*>(p.o + out * D + lane * PER + k) = pack_bf16x2(end(a[k]), end(a[k + 1]));
+  if (lane == 0) p.lse[out] = end.lse;
 }
 
 template <int D>
@@ -971,7 +963,7 @@ cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stre
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, C::ROWS / 32);
+  cfg.gridDim = dim3(grid, C::ROWS / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
