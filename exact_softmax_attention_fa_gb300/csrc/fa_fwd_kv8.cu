@@ -342,21 +342,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // exponent of the largest value; 2^-100 and below are left as they are
-      const int x = max(static_cast<int>(amax >> 7) - 127, -100);
-      const float mul = exp2i(7 - x);
+      const int x = min(max(static_cast<int>(amax >> 7) - 127, -100), 127);
+      const float mul = query_factor(amax, 7 - x);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const uint32_t w2[2] = {raw[t].x, raw[t].y};
         uint32_t word = 0;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float2 f = unpack_bf16x2(w2[y]);
-          f.x *= mul;
-          f.y *= mul;
-          // an infinity would saturate to a number
-          if (isinf(f.x)) f.x = NAN;
-          if (isinf(f.y)) f.y = NAN;
-          __half2 v = __floats2half2_rn(f.x, f.y);
+          const float2 f = unpack_bf16x2(w2[y]);
+          __half2 v = __floats2half2_rn(f.x * mul, f.y * mul);
           const uint32_t hi = take_piece(v);
           word |= (i & 1 ? last_piece(v) : hi) << (16 * y);
         }

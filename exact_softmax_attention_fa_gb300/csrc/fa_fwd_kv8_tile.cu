@@ -149,46 +149,91 @@ struct Walk {
   }
 };
 
-// All lanes of one warp: the tiles of every block summed, and the block that
-// holds tile number x of them (x < 0: the total alone).
-template <int D>
-__device__ long long tile_search(const TileLaunch& p, long long x, int4* at) {
-  const int lane = threadIdx.x & 31;
-  long long total = 0;
-  Walk<D> w;
-  for (int b = 0; b < p.c.B; ++b) {
-    w.b = b;
-    w.load(p);
-    long long one = 0;  // tiles of the sequence's blocks for one K/V head
-    for (int blk = lane; blk < w.blocks; blk += 32) one += w.tiles_of(p, blk);
-    one = warp_sum(one);
-    const long long here = one * p.c.Hkv;
-    if (x >= 0 && x < total + here) {
-      long long rem = x - total;
-      const int h = static_cast<int>(rem / one);
-      rem -= h * one;
-      for (int b0 = 0;; b0 += 32) {  // the block within the head
-        const int blk = b0 + lane;
-        int incl = blk < w.blocks ? w.tiles_of(p, blk) : 0;
-        const int own = incl;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, incl > rem);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          const int before = __shfl_sync(0xffffffffu, incl - own, l);
-          *at = make_int4(b, h, b0 + l, static_cast<int>(rem) - before);
-          return x;
-        }
-        rem -= __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    total += here;
+// Row `row` of the group of K/V head w.h: position and place in [B][Hq][Nq], for
+// rows a fixed step apart.
+struct RowPlace {
+  int qi, hg, g, dq, dr, Nq;
+  size_t head;
+  template <class W>
+  __device__ __forceinline__ RowPlace(const TileLaunch& p, const W& w, int row, int step) {
+    g = p.g;
+    qi = row / g;
+    hg = row - qi * g;
+    dq = step / g;
+    dr = step - dq * g;
+    Nq = p.Nq;
+    head = static_cast<size_t>(w.b) * p.Hq + w.h * g;
   }
-  return total;
+  __device__ __forceinline__ void next() {
+    qi += dq;
+    hg += dr;
+    if (hg >= g) {
+      hg -= g;
+      ++qi;
+    }
+  }
+  __device__ __forceinline__ size_t index() const { return (head + hg) * Nq + qi; }
+};
+
+// Key tiles of all blocks of sequence b for one K/V head (lane l of a warp: sequence b).
+template <int D>
+__device__ __forceinline__ int sequence_tiles(const TileLaunch& p, int b) {
+  Walk<D> w;
+  w.b = b;
+  w.load(p);
+  int n = 0;
+  for (int blk = 0; blk < w.blocks; ++blk) n += w.tiles_of(p, blk);
+  return n;
+}
+
+// All lanes of one warp: the tiles of every block summed.
+template <int D>
+__device__ long long tile_total(const TileLaunch& p) {
+  long long total = 0;
+  for (int b = threadIdx.x & 31; b < p.c.B; b += 32) total += static_cast<long long>(sequence_tiles<D>(p, b)) * p.c.Hkv;
+  return warp_sum(total);
+}
+
+// All lanes of one warp: the block (and tile of it) that tile x of the list is.
+template <int D>
+__device__ int4 tile_search(const TileLaunch& p, long long x) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0;; b0 += 32) {
+    const int one = b0 + lane < p.c.B ? sequence_tiles<D>(p, b0 + lane) : 0;
+    long long incl = static_cast<long long>(one) * p.c.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > x);
+    if (!past) {
+      x -= __shfl_sync(0xffffffffu, incl, 31);
+      continue;
+    }
+    const int l = __ffs(past) - 1, per_head = __shfl_sync(0xffffffffu, one, l);
+    long long rem = x - (__shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(per_head) * p.c.Hkv);
+    Walk<D> w;
+    w.b = b0 + l;
+    w.load(p);
+    const int h = static_cast<int>(rem / per_head);
+    rem -= static_cast<long long>(h) * per_head;
+    for (int k0 = 0;; k0 += 32) {  // the block within the head
+      const int own = k0 + lane < w.blocks ? w.tiles_of(p, k0 + lane) : 0;
+      int in = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, in > rem);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        return make_int4(w.b, h, k0 + k, static_cast<int>(rem) - __shfl_sync(0xffffffffu, in - own, k));
+      }
+      rem -= __shfl_sync(0xffffffffu, in, 31);
+    }
+  }
 }
 
 // CTAs that share `total` tiles, and the first tile of CTA c of them.
@@ -565,48 +610,58 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     float qfac = 0.f;
-    if (alive && last >= 0) {
+    // rows are in order: a warp without a live one has nothing to bring or store
+    const bool warp_live = w.blk * C::ROWS + t * 128 + (r & ~31) < w.count * p.g;
+    if (alive && last >= 0 && warp_live) {
       // The warp's 32 rows as Q pieces, 8 columns a lane (whole lines a load);
       // S of the segment before is complete, so the tile is free.
       constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes a row, rows a pass
+      constexpr int PASSES = 32 / RPP, BATCH = PASSES < 8 ? PASSES : 8;  // a batch's loads are issued together
       const int col = lane % LPR, warp_row = r & ~31;
-#pragma unroll 4
-      for (int q = 0; q < 32 / RPP; ++q) {
-        const int pr = q * RPP + lane / LPR;  // row of the warp
-        const int row_q = w.blk * C::ROWS + t * 128 + warp_row + pr, qi_q = row_q / p.g;
-        const size_t at_q = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row_q % p.g) * p.Nq + qi_q;
-        const uint4 v = qi_q < w.count ? __ldg(reinterpret_cast<const uint4*>(p.q + at_q * D) + col) : make_uint4(0, 0, 0, 0);
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        uint32_t amax = 0;
+      RowPlace at_q(p, w, w.blk * C::ROWS + t * 128 + warp_row + lane / LPR, RPP);
+#pragma unroll 1
+      for (int q0 = 0; q0 < PASSES; q0 += BATCH) {
+        uint4 raw[BATCH];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int x = max(static_cast<int>(amax >> 7) - 127, -100);
-        const float mul = exp2i(7 - x);
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float2 f = unpack_bf16x2(w4[k]);
-          f.x *= mul;
-          f.y *= mul;
-          if (isinf(f.x)) f.x = NAN;  // an infinity would saturate to a number
-          if (isinf(f.y)) f.y = NAN;
-          const uint32_t h2 = f32x2_to_e4m3x2(f.x, f.y);
-          const float2 back = e4m3x2_to_f32x2(h2);
-          hi[k >> 1] |= h2 << (16 * (k & 1));
-          lo[k >> 1] |= f32x2_to_e4m3x2(f.x - back.x, f.y - back.y) << (16 * (k & 1));
+        for (int q = 0; q < BATCH; ++q) {
+          raw[q] = make_uint4(0, 0, 0, 0);
+          if (at_q.qi < w.count) raw[q] = __ldg(reinterpret_cast<const uint4*>(p.q + at_q.index() * D) + col);
+          at_q.next();
         }
-        // unit numbers along the row [qh | ql]; a lane has half a unit of each
-        const int uh = col >> 1, ul = uh + D / 16;
-        st_shared_v2(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(warp_row + pr, uh & 7) + (col & 1) * 8, hi[0], hi[1]);
-        st_shared_v2(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(warp_row + pr, ul & 7) + (col & 1) * 8, lo[0], lo[1]);
-        // the thread that owns the row keeps its power of two
-        const float fac = exp2i(x - 7);
 #pragma unroll
-        for (int u = 0; u < RPP; ++u) {
-          const float got = __shfl_sync(0xffffffffu, fac, u * LPR);
-          if (lane == q * RPP + u) qfac = got;
+        for (int q = 0; q < BATCH; ++q) {
+          const int pr = (q0 + q) * RPP + lane / LPR;  // row of the warp
+          const uint32_t w4[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+          uint32_t amax = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // exponent of the largest value; 2^-100 and below are left as they are
+          const int x = min(max(static_cast<int>(amax >> 7) - 127, -100), 127);
+          const float mul = query_factor(amax, 7 - x);
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack_bf16x2(w4[k]);
+            const __half2 v = __floats2half2_rn(f.x * mul, f.y * mul);
+            const uint32_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
+            const uint32_t back = e4m3x2_to_f16x2(h2);
+            const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+            hi[k >> 1] |= h2 << (16 * (k & 1));
+            lo[k >> 1] |= f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest)) << (16 * (k & 1));
+          }
+          // unit numbers along the row [qh | ql]; a lane has half a unit of each
+          const int uh = col >> 1, ul = uh + D / 16;
+          st_shared_v2(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(warp_row + pr, uh & 7) + (col & 1) * 8, hi[0], hi[1]);
+          st_shared_v2(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(warp_row + pr, ul & 7) + (col & 1) * 8, lo[0], lo[1]);
+          // the thread that owns the row keeps its power of two
+          const float fac = exp2i(x - 7);
+#pragma unroll
+          for (int u = 0; u < RPP; ++u) {
+            const float got = __shfl_sync(0xffffffffu, fac, u * LPR);
+            if (lane == (q0 + q) * RPP + u) qfac = got;
+          }
         }
       }
       fence_proxy_async_smem();
@@ -725,7 +780,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     tc_fence_after_sync();
-    if (alive) {
+    if (alive && warp_live) {
       const bool whole = n == w.tiles;
       const RowEnd end(m, l);
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + t * 128 + r;
@@ -734,6 +789,17 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       // stores of whole lines. Row i's pieces are XORed as in the tiles.
       const uint32_t stage = q_dst + (r >> 5) * 4096;
       const int cols = whole ? 64 : 32;
+      // the rows this lane stores, four rows a pass
+      uint8_t* to[8];
+      RowPlace at_q(p, w, row - lane + (lane >> 3), 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        to[q] = nullptr;
+        if (at_q.qi < w.count)
+          to[q] = (whole ? reinterpret_cast<uint8_t*>(p.o + at_q.index() * D)
+                         : reinterpret_cast<uint8_t*>(p.part + (slot - lane + q * 4 + (lane >> 3)) * D)) + (lane & 7) * 16;
+        at_q.next();
+      }
 #pragma unroll 1
       for (int c = 0; c < D; c += cols) {
         __syncwarp();
@@ -758,19 +824,12 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           }
         }
         __syncwarp();
+        // 128 bytes a pass and row; none of a part whose keys no row of the tile sees: 0
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {  // four rows a pass
-          const int pr = q * 4 + (lane >> 3);
-          uint4 v = ld_shared_v4(stage + sw128_offset(pr, lane & 7));
-          const int row_q = row - lane + pr, qi_q = row_q / p.g;
-          if (qi_q >= w.count) continue;
-          if (!active) v = make_uint4(0, 0, 0, 0);  // no row of the tile sees a key of this part
-          if (whole) {
-            const size_t at_q = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row_q % p.g) * p.Nq + qi_q;
-            *(reinterpret_cast<uint4*>(p.o + at_q * D + c) + (lane & 7)) = v;
-          } else {
-            *(reinterpret_cast<uint4*>(p.part + (slot - lane + pr) * D + c) + (lane & 7)) = v;
-          }
+        for (int q = 0; q < 8; ++q) {
+          uint4 v = ld_shared_v4(stage + sw128_offset(q * 4 + (lane >> 3), lane & 7));
+          if (!active) v = make_uint4(0, 0, 0, 0);
+          if (to[q]) *reinterpret_cast<uint4*>(to[q] + c / cols * 128) = v;
         }
       }
       if (live) {
@@ -822,11 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     fence_mbarrier_init();
   }
   if (warp == kLoadWarp) {  // the CTA's run
-    const long long total = tile_search<D>(p, -1, nullptr);
+    const long long total = tile_total<D>(p);
     const int c = blockIdx.x, used = used_ctas(total, gridDim.x);
     const long long x0 = c < used ? first_tile(total, used, c) : 0, x1 = c < used ? first_tile(total, used, c + 1) : 0;
     int4 at = make_int4(p.c.B, 0, 0, 0);
-    if (x1 > x0) tile_search<D>(p, x0, &at);
+    if (x1 > x0) at = tile_search<D>(p, x0);
     if (lane_id() == 0) {
       sh.start = at;
       sh.n_tiles = static_cast<int>(x1 - x0);

@@ -26,6 +26,14 @@ struct Kv8Call {
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// What a query row is multiplied with before it is split into e4m3 pieces:
+// 2^e, or NaN for a row that holds an infinity or NaN (amax: bits of its largest
+// |bf16|), whose scores are infinite or NaN and whose output is NaN either way;
+// the pieces would saturate.
+__device__ __forceinline__ float query_factor(uint32_t amax, int e) {
+  return amax >= 0x7f80u ? __int_as_float(0x7fc00000) : exp2i(e);
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
