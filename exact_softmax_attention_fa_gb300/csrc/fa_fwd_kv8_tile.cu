@@ -71,6 +71,25 @@ struct TileLaunch : Kv8Call {
   uint64_t wait_limit_ns;
 };
 
+// How `total` tiles are dealt: runs of per + 1 tiles to the first `more` CTAs, of
+// per tiles to the others.
+struct Deal {
+  long long per, more;
+  int used;
+  Deal() = default;
+  __device__ __forceinline__ Deal(long long total, int ctas) {
+    const long long most = (total + kMinTiles - 1) / kMinTiles;
+    used = most < ctas ? static_cast<int>(most) : ctas;
+    per = used > 0 ? total / used : 0;
+    more = total - per * used;
+  }
+  __device__ __forceinline__ long long first(int c) const { return c >= used ? per * used + more : c * per + min(static_cast<long long>(c), more); }
+  __device__ __forceinline__ int holder(long long x) const {
+    const long long head = more * (per + 1);
+    return static_cast<int>(x < head ? x / (per + 1) : more + (x - head) / per);
+  }
+};
+
 template <int D>
 struct TileShared {
   static constexpr int SLOTS = TileCfg<D>::SLOTS;
@@ -79,8 +98,12 @@ struct TileShared {
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t scale_full[SLOTS];
   uint64_t mma_drain;
+  uint64_t join_ml[4], join_o[4], join_done[4];  // two halves of the keys: per warp pair
+  float2 half_ml[2][TileCfg<D>::NT == 2 ? 128 : 1];
   float4 scale[SLOTS][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
   int4 start;
+  float qfac[TileCfg<D>::NT][128];
+  Deal deal;
   int n_tiles;
   uint32_t tmem_base;
   int abort_flag;
@@ -175,31 +198,36 @@ struct RowPlace {
   __device__ __forceinline__ size_t index() const { return (head + hg) * Nq + qi; }
 };
 
-// Key tiles of all blocks of sequence b for one K/V head (lane l of a warp: sequence b).
+// Key tiles of all blocks of sequence b for one K/V head.
 template <int D>
 __device__ __forceinline__ int sequence_tiles(const TileLaunch& p, int b) {
+  constexpr int ROWS = TileCfg<D>::ROWS;
   Walk<D> w;
   w.b = b;
   w.load(p);
-  int n = 0;
-  for (int blk = 0; blk < w.blocks; ++blk) n += w.tiles_of(p, blk);
+  if (!p.causal) return w.blocks * ((w.len + 127) / 128);
+  // a block sees the keys up to its last row's position, which moves by ROWS / g a block
+  const int step = ROWS / p.g, part = ROWS - step * p.g;
+  int n = 0, pos = (ROWS - 1) / p.g, rest = ROWS - 1 - pos * p.g;
+  for (int blk = 0; blk < w.blocks; ++blk) {
+    n += (min(w.len, max(0, w.len - w.count + min(pos, w.count - 1) + 1)) + 127) / 128;
+    pos += step;
+    rest += part;
+    if (rest >= p.g) {
+      rest -= p.g;
+      ++pos;
+    }
+  }
   return n;
 }
 
-// All lanes of one warp: the tiles of every block summed.
+// All lanes of one warp: the block (and tile of it) that tile x of the list is;
+// first: sequence_tiles of sequence `lane` (0 behind the last).
 template <int D>
-__device__ long long tile_total(const TileLaunch& p) {
-  long long total = 0;
-  for (int b = threadIdx.x & 31; b < p.c.B; b += 32) total += static_cast<long long>(sequence_tiles<D>(p, b)) * p.c.Hkv;
-  return warp_sum(total);
-}
-
-// All lanes of one warp: the block (and tile of it) that tile x of the list is.
-template <int D>
-__device__ int4 tile_search(const TileLaunch& p, long long x) {
+__device__ int4 tile_search(const TileLaunch& p, int first, long long x) {
   const int lane = threadIdx.x & 31;
   for (int b0 = 0;; b0 += 32) {
-    const int one = b0 + lane < p.c.B ? sequence_tiles<D>(p, b0 + lane) : 0;
+    const int one = b0 == 0 ? first : b0 + lane < p.c.B ? sequence_tiles<D>(p, b0 + lane) : 0;
     long long incl = static_cast<long long>(one) * p.c.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,13 +263,6 @@ __device__ int4 tile_search(const TileLaunch& p, long long x) {
     }
   }
 }
-
-// CTAs that share `total` tiles, and the first tile of CTA c of them.
-__device__ __forceinline__ int used_ctas(long long total, int ctas) {
-  const long long most = (total + kMinTiles - 1) / kMinTiles;
-  return most < ctas ? static_cast<int>(most) : ctas;
-}
-__device__ __forceinline__ long long first_tile(long long total, int used, int c) { return total * c / used; }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -332,7 +353,6 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   constexpr int ROW_BYTES = D < 128 ? D : 128;  // a key's codes in one column chunk of the operand tile
   const int page = 1 << p.c.page_log2, pages = 128 >> p.c.page_log2;
   const int n = sh.n_tiles;
-  if (lane == 0) tma_prefetch_desc(&p.tmK);
   // Lane 8 j + g looks up 16-key group g of tile 4 k + j, one batch of 4 tiles ahead.
   Walk<D> cur;
   cur.begin(p, sh.start);
@@ -489,7 +509,7 @@ __device__ __forceinline__ void issue_pv_steps(std::integer_sequence<int, KS...>
   (umma_ts_f16<KS * 8, KS * 2048>(d, p_tmem, v_lo, v_hi, idesc, KS > 0 ? 1u : accumulate), ...);
 }
 
-template <int D>
+template <int D, bool HALVES>
 __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
   using C = TileCfg<D>;
   constexpr uint32_t kIdescS = make_idesc_f32(128, 128, false);
@@ -534,6 +554,36 @@ __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, ui
     left -= n;
     w.s += n;
     w.settle(p);
+    if constexpr (HALVES) {
+      // Slot j % 2 takes key tile j: S(j) into it, P(j) from it, then S(j + 2).
+      auto start_s = [&](int t) -> bool {
+        if (!mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return false;
+        // S_t overwrites the columns the slot's P before is read from
+        if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim)) return false;
+        tc_fence_after_sync();
+        issue_s(t);
+        umma_commit(&sh.k_empty[k.stage]);
+        k.next();
+        return true;
+      };
+      if (!start_s(0) || (n > 1 && !start_s(1))) return fail();
+      for (int j0 = 0; j0 < n; j0 += 2) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j0 + t >= n) continue;
+          if (!mbar_wait(&sh.v_full[v.stage], v.phase, &sh.abort_flag, lim)) return fail();
+          if (!mbar_wait(&sh.p_full[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
+          if (j0 == 0 && seg > 0 && !mbar_wait(&sh.o_free[t], (seg - 1) & 1, &sh.abort_flag, lim)) return fail();
+          tc_fence_after_sync();
+          issue_pv(t, j0 == 0);
+          umma_commit(&sh.v_empty[v.stage]);
+          v.next();
+          ++cnt[t];
+          if (j0 + t + 2 < n && !start_s(t)) return fail();
+        }
+      }
+      continue;
+    }
     if (!mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
 #pragma unroll
@@ -580,7 +630,7 @@ __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, ui
 // ---------------------------------------------------------------------------
 // Q pieces, softmax, correction and epilogue (warpgroup t owns query tile t)
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool HALVES>
 __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint32_t tmem, int t) {
   using C = TileCfg<D>;
   const int r = threadIdx.x & 127, lane = r & 31;
@@ -590,6 +640,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
   const uint32_t tO = tmem + lane_base + C::o_col(t);
   const uint32_t q_dst = smem_u32(sQ + t * C::Q_BYTES);
   const uint64_t lim = p.wait_limit_ns;
+  constexpr int STEP = HALVES ? 2 : 1;
   Walk<D> w;
   w.begin(p, sh.start);
   int left = sh.n_tiles, i0 = 0, cnt = 0;
@@ -597,8 +648,12 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
   bool alive = true;
   for (int seg = 0; left > 0; ++seg) {
     const int n = min(left, w.tiles - w.s);
-    const int last = w.last_tile(p, t, n);
-    const int row = w.blk * C::ROWS + t * 128 + r;
+    const int row0 = w.blk * C::ROWS + (HALVES ? 0 : t * 128);
+    const int row = row0 + r;
+    // the warpgroup's key tiles of this part of the run: j0, j0 + STEP, ... <= last
+    const int j0 = HALVES ? t : 0;
+    const int last = HALVES ? (t < n ? n - 1 : -1) : w.last_tile(p, t, n);
+    const int turns = last < 0 ? 0 : (last - j0) / STEP + 1;
     const int qi = row / p.g;
     const bool live = qi < w.count;
     const size_t at = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row % p.g) * p.Nq + qi;
@@ -606,22 +661,28 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     // The MMA thread has taken note of the segment before (else an idle tile's
     // warpgroup could run two arrivals ahead of its parity wait).
     if (alive && seg > 0) {
-      alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim);
+      alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim) &&
+              (!HALVES || t == 0 || warp_wait(&sh.join_done[r >> 5], (seg - 1) & 1, &sh.abort_flag, lim));
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     float qfac = 0.f;
     // rows are in order: a warp without a live one has nothing to bring or store
-    const bool warp_live = w.blk * C::ROWS + t * 128 + (r & ~31) < w.count * p.g;
+    const bool warp_live = row0 + (r & ~31) < w.count * p.g;
     if (alive && last >= 0 && warp_live) {
-      // The warp's 32 rows as Q pieces, 8 columns a lane (whole lines a load);
-      // S of the segment before is complete, so the tile is free.
+      // The warp's 32 rows as Q pieces, 8 columns a lane (whole lines a load); S of
+      // the segment before is complete, so the tile is free.
       constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes a row, rows a pass
       constexpr int PASSES = 32 / RPP, BATCH = PASSES < 8 ? PASSES : 8;  // a batch's loads are issued together
       const int col = lane % LPR, warp_row = r & ~31;
-      RowPlace at_q(p, w, w.blk * C::ROWS + t * 128 + warp_row + lane / LPR, RPP);
+      // unit numbers along the row [qh | ql]; a lane has half a unit of each
+      const int uh = col >> 1, ul = uh + D / 16;
+      const uint32_t hi_at = q_dst + (uh >> 3) * (128 * 128) + (col & 1) * 8;
+      const uint32_t lo_at = q_dst + (ul >> 3) * (128 * 128) + (col & 1) * 8;
+      RowPlace at_q(p, w, row0 + warp_row + lane / LPR, RPP);
 #pragma unroll 1
       for (int q0 = 0; q0 < PASSES; q0 += BATCH) {
         uint4 raw[BATCH];
+        uint32_t amax[BATCH];  // bits of the row's largest |value|
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
           raw[q] = make_uint4(0, 0, 0, 0);
@@ -630,16 +691,22 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
         }
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
-          const int pr = (q0 + q) * RPP + lane / LPR;  // row of the warp
           const uint32_t w4[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
-          uint32_t amax = 0;
+          amax[q] = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+          for (int k = 0; k < 4; ++k) amax[q] = max(amax[q], max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+        }
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int q = 0; q < BATCH; ++q) amax[q] = max(amax[q], __shfl_xor_sync(0xffffffffu, amax[q], o));
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+          const int in_tile = warp_row + (q0 + q) * RPP + lane / LPR;
+          const uint32_t w4[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
           // exponent of the largest value; 2^-100 and below are left as they are
-          const int x = min(max(static_cast<int>(amax >> 7) - 127, -100), 127);
-          const float mul = query_factor(amax, 7 - x);
+          const int x = min(max(static_cast<int>(amax[q] >> 7) - 127, -100), 127);
+          const float mul = query_factor(amax[q], 7 - x);
           uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -651,33 +718,31 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
             hi[k >> 1] |= h2 << (16 * (k & 1));
             lo[k >> 1] |= f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest)) << (16 * (k & 1));
           }
-          // unit numbers along the row [qh | ql]; a lane has half a unit of each
-          const int uh = col >> 1, ul = uh + D / 16;
-          st_shared_v2(q_dst + (uh >> 3) * (128 * 128) + sw128_offset(warp_row + pr, uh & 7) + (col & 1) * 8, hi[0], hi[1]);
-          st_shared_v2(q_dst + (ul >> 3) * (128 * 128) + sw128_offset(warp_row + pr, ul & 7) + (col & 1) * 8, lo[0], lo[1]);
-          // the thread that owns the row keeps its power of two
-          const float fac = exp2i(x - 7);
-#pragma unroll
-          for (int u = 0; u < RPP; ++u) {
-            const float got = __shfl_sync(0xffffffffu, fac, u * LPR);
-            if (lane == (q0 + q) * RPP + u) qfac = got;
-          }
+          st_shared_v2(hi_at + sw128_offset(in_tile, uh & 7), hi[0], hi[1]);
+          st_shared_v2(lo_at + sw128_offset(in_tile, ul & 7), lo[0], lo[1]);
+          if (col == 0) sh.qfac[t][in_tile] = exp2i(x - 7);
         }
       }
+      __syncwarp();
+      qfac = sh.qfac[t][r];  // the row's power of two
       fence_proxy_async_smem();
     }
     warp_arrive(&sh.q_full[t]);
 
     float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
-    for (int j = 0; j <= last; ++j) {
+    for (int j = j0, turn = cnt; j <= last; j += STEP, ++turn) {
       const int i = i0 + j, sl = i % C::SLOTS;
       alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
-      alive = alive && warp_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim);
+      alive = alive && warp_wait(&sh.s_full[t], turn & 1, &sh.abort_flag, lim);
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
         break;
       }
       tc_fence_after_sync();
+      if (!warp_live) {  // nobody reads what its rows of P give
+        warp_arrive(&sh.p_full[t]);
+        continue;
+      }
       // The row of S stays in tensor memory and is read twice, 32 columns at a
       // time with the next 32 on their way: once for its maximum, once for the
       // weights. Holding all 128 in registers unrolls everything: the loop then
@@ -757,7 +822,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
         if (c == 0) tmem_ld32(tS + 64, xa);
         weigh(xb, c / 16 + 2);
       }
-      if (j > 0 && move) {
+      if (j > j0 && move) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -776,14 +841,56 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
 
     const bool active = last >= 0;
     if (alive && active) {
-      alive = warp_wait(&sh.pv_done[t], (cnt + last) & 1, &sh.abort_flag, lim);
+      alive = warp_wait(&sh.pv_done[t], (cnt + turns - 1) & 1, &sh.abort_flag, lim);
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     tc_fence_after_sync();
-    if (alive && warp_live) {
+    float own = 1.f;  // what this warpgroup's O is multiplied with
+    // 4 KB per warp in each 16 KB of both Q tiles, whose last S is complete:
+    // the warp's own rows of them
+    const uint32_t area = smem_u32(sQ) + (r >> 5) * 4096;
+    if constexpr (HALVES) {
+      // The two halves of the keys: both warps of the same rows learn the other's
+      // m and l; the second leaves its O in shared memory, the first goes on
+      // with the sum.
+      const int quarter = r >> 5;
+      sh.half_ml[t][r] = make_float2(m, l);
+      warp_arrive(&sh.join_ml[quarter]);
+      if (alive) {
+        alive = warp_wait(&sh.join_ml[quarter], seg & 1, &sh.abort_flag, lim);
+        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
+      }
+      if (alive) {
+        const float2 other = sh.half_ml[t ^ 1][r];
+        const float both = fmaxf(m, other.x), ref = both == -INFINITY ? 0.f : both;
+        own = ex2_approx(m - ref);
+        l = l * own + other.y * ex2_approx(other.x - ref);
+        m = both;
+      }
+      if (t == 1) {
+        if (alive && warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = active ? __float_as_uint(__uint_as_float(o[k]) * own) : 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              st_shared_v4(area + c * 512 + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
+        }
+        warp_arrive(&sh.join_o[quarter]);
+      } else if (alive) {
+        alive = warp_wait(&sh.join_o[quarter], seg & 1, &sh.abort_flag, lim);
+        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
+      }
+    }
+    if (alive && warp_live && !(HALVES && t == 1)) {
       const bool whole = n == w.tiles;
       const RowEnd end(m, l);
-      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + t * 128 + r;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + (HALVES ? 0 : t * 128) + r;
       // 128 bytes of each of the warp's 32 rows at a time (32 fp32 or 64 bf16
       // columns) through its own 4 KB of the Q tile, whose last S is complete:
       // stores of whole lines. Row i's pieces are XORed as in the tiles.
@@ -808,6 +915,16 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           uint32_t o[32];
           tmem_ld32(tO + c + 32 * half, o);
           tmem_ld_wait();
+          if constexpr (HALVES) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint4 x = ld_shared_v4(area + (c + 32 * half) * 512 + sw128_offset(lane, u));
+              o[4 * u] = __float_as_uint(fmaf(__uint_as_float(o[4 * u]), own, __uint_as_float(x.x)));
+              o[4 * u + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 1]), own, __uint_as_float(x.y)));
+              o[4 * u + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 2]), own, __uint_as_float(x.z)));
+              o[4 * u + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 3]), own, __uint_as_float(x.w)));
+            }
+          }
           if (whole) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -838,7 +955,8 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     }
     tc_fence_before_sync();
     warp_arrive(&sh.o_free[t]);
-    if (active) cnt += last + 1;
+    if (HALVES && t == 0) warp_arrive(&sh.join_done[r >> 5]);
+    cnt += turns;
     i0 += n;
     left -= n;
     w.s += n;
@@ -846,7 +964,28 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
   }
 }
 
+// For the joining kernel: where the run starts, the CTAs that hold the block it
+// starts in, and whether that is not the first block of the first of them.
 template <int D>
+__device__ void note_run(const TileLaunch& p, const TileShared<D>& sh) {
+  const int c = blockIdx.x;
+  const int4 at = sh.start;
+  int4 held = make_int4(c, c, 0, 0);
+  if (sh.n_tiles > 0 && at.w > 0) {
+    Walk<D> w;
+    w.begin(p, at);
+    const Deal deal = sh.deal;
+    const long long begin = deal.first(c) - at.w;  // of the block
+    held.x = deal.holder(begin);
+    held.y = deal.holder(begin + w.tiles - 1);
+    held.z = begin > deal.first(held.x) ? 1 : 0;
+    held.w = w.count;
+  }
+  p.run[2 * c] = at;
+  p.run[2 * c + 1] = held;
+}
+
+template <int D, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_constant__ TileLaunch p) {
   using C = TileCfg<D>;
   extern __shared__ uint8_t smem_dyn[];
@@ -877,32 +1016,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&sh.scale_full[i], 8);
     mbar_init(&sh.mma_drain, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.join_ml[i], 2);
+      mbar_init(&sh.join_o[i], 1);
+      mbar_init(&sh.join_done[i], 1);
+    }
     sh.abort_flag = 0;
     fence_mbarrier_init();
   }
   if (warp == kLoadWarp) {  // the CTA's run
-    const long long total = tile_total<D>(p);
-    const int c = blockIdx.x, used = used_ctas(total, gridDim.x);
-    const long long x0 = c < used ? first_tile(total, used, c) : 0, x1 = c < used ? first_tile(total, used, c + 1) : 0;
+    if (lane_id() == 0) tma_prefetch_desc(&p.tmK);
+    const int lane = threadIdx.x & 31;
+    const int first = lane < p.c.B ? sequence_tiles<D>(p, lane) : 0;
+    long long total = static_cast<long long>(first) * p.c.Hkv;
+    for (int b = lane + 32; b < p.c.B; b += 32) total += static_cast<long long>(sequence_tiles<D>(p, b)) * p.c.Hkv;
+    const Deal deal(warp_sum(total), gridDim.x);
+    const long long x0 = deal.first(blockIdx.x), x1 = deal.first(blockIdx.x + 1);
     int4 at = make_int4(p.c.B, 0, 0, 0);
-    if (x1 > x0) at = tile_search<D>(p, x0);
-    if (lane_id() == 0) {
+    if (x1 > x0) at = tile_search<D>(p, first, x0);
+    if (lane == 0) {
       sh.start = at;
       sh.n_tiles = static_cast<int>(x1 - x0);
-      // for the joining kernel: the CTAs that hold the block the run starts in,
-      // and whether it is not the first block of the first of them
-      int4 held = make_int4(c, c, 0, 0);
-      if (x1 > x0 && at.w > 0) {
-        Walk<D> w;
-        w.begin(p, at);
-        const long long begin = x0 - at.w;  // the CTA that holds tile x: the largest with first_tile <= x
-        held.x = static_cast<int>(((begin + 1) * used - 1) / total);
-        held.y = static_cast<int>(((begin + w.tiles) * used - 1) / total);
-        held.z = begin > first_tile(total, used, held.x) ? 1 : 0;
-        held.w = w.count;
-      }
-      p.run[2 * c] = at;
-      p.run[2 * c + 1] = held;
+      sh.deal = deal;
     }
   }
   if (warp == kMmaWarp) {
@@ -914,13 +1049,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   if (warp < 8) {
-    if (warp < 4 * C::NT) softmax_role<D>(p, sh, sQ, tmem, warp >> 2);
+    if (warp < 4 * C::NT) softmax_role<D, HALVES>(p, sh, sQ, tmem, warp >> 2);
   } else if (warp < 12) {
     convert_role<D>(p, sh, sStage, sV);
   } else if (warp == kLoadWarp) {
     load_role<D>(p, sh, sK, sStage);
   } else if (lane_id() == 0) {
-    mma_role<D>(p, sh, sQ, sK, sV, tmem);
+    note_run<D>(p, sh);  // Q takes longer to come
+    mma_role<D, HALVES>(p, sh, sQ, sK, sV, tmem);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -1010,10 +1146,10 @@ size_t tile_part_bytes(size_t* ml_off, size_t* run_off) {
   return *run_off + 2 * kMaxSms * sizeof(int4);
 }
 
-template <int D>
+template <int D, bool HALVES>
 cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stream) {
   using C = TileCfg<D>;
-  auto kern = kv8_tile_kernel<D>;
+  auto kern = kv8_tile_kernel<D, HALVES>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(kern, C::SMEM, dev.device, allowed);
   if (e != cudaSuccess) return e;
@@ -1056,9 +1192,11 @@ fa_status_t launch_kv8_tiles(const Kv8Call& call, int d, void* workspace, const 
   a.part = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + ml);
   a.run = reinterpret_cast<int4*>(ws + run);
-  if (d == 64) return from_cuda(launch_tiles<64>(a, dev, stream));
-  if (d == 128) return from_cuda(launch_tiles<128>(a, dev, stream));
-  return from_cuda(launch_tiles<256>(a, dev, stream));
+  // one tile of rows: both slots take it, with every other key tile each
+  const bool halves = static_cast<long long>(call.g) * call.Nq <= 128;
+  if (d == 64) return from_cuda(halves ? launch_tiles<64, true>(a, dev, stream) : launch_tiles<64, false>(a, dev, stream));
+  if (d == 128) return from_cuda(halves ? launch_tiles<128, true>(a, dev, stream) : launch_tiles<128, false>(a, dev, stream));
+  return from_cuda(launch_tiles<256, false>(a, dev, stream));
 }
 
 }  // namespace fa
