@@ -37,7 +37,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kConvThreads = 128;
 constexpr int kLoadWarp = 12, kMmaWarp = 13;
 constexpr int kMinTiles = 2;    // a CTA's run is not cut below this
@@ -53,12 +53,10 @@ struct TileCfg {
   static constexpr int VST = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int SLOTS = KST + 2;  // tiles whose scales are kept: a tile's are read before the key ring comes round
   static constexpr int SST = D == 64 ? 4 : (D == 128 ? 2 : 1);  // staged value codes
-  static constexpr bool P_ALIAS = D == 128;
-  __host__ __device__ static constexpr uint32_t s_col(int t) { return D == 256 ? 0u : uint32_t(t) * 128u; }
+  // tensor memory: per slot two 64-key buffers of S (the weights P take the first
+  // 32 columns of the S they come from), then O
+  __host__ __device__ static constexpr uint32_t s_col(int t, int buf) { return uint32_t(t) * 128u + uint32_t(buf) * 64u; }
   __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + uint32_t(t) * D; }
-  __host__ __device__ static constexpr uint32_t p_col(int t) {
-    return D == 64 ? 384u + uint32_t(t) * 64u : (D == 128 ? uint32_t(t) * 128u : 128u);
-  }
   static constexpr int SMEM = NT * Q_BYTES + KST * K_BYTES + VST * V_BYTES + SST * K_BYTES + 1024;
 };
 
@@ -95,9 +93,9 @@ struct TileShared {
   static constexpr int SLOTS = TileCfg<D>::SLOTS;
   uint64_t q_full[2], q_taken[2];
   uint64_t k_full[4], k_empty[4], st_full[4], st_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];  // [slot][buffer of S]
   uint64_t scale_full[SLOTS];
-  uint64_t mma_drain;
+  uint64_t mma_drain[2];
   uint64_t join_ml[4], join_o[4], join_done[4];  // two halves of the keys: per warp pair
   float2 half_ml[2][TileCfg<D>::NT == 2 ? 128 : 1];
   float4 scale[SLOTS][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
@@ -502,129 +500,111 @@ __device__ __forceinline__ void issue_s_steps(std::integer_sequence<int, QS...>,
               (QS % (D / 32) >> 2) * (128 * 128) + (QS % (D / 32) & 3) * 32, (QS > 0)>(d, q_lo, q_hi, k_lo, k_hi, idesc),
    ...);
 }
-// O += P V over 128 keys, 16 a step.
+// O += P V over 64 keys, 16 a step.
 template <int... KS>
 __device__ __forceinline__ void issue_pv_steps(std::integer_sequence<int, KS...>, uint32_t d, uint32_t p_tmem,
                                                uint32_t v_lo, uint32_t v_hi, uint32_t idesc, uint32_t accumulate) {
   (umma_ts_f16<KS * 8, KS * 2048>(d, p_tmem, v_lo, v_hi, idesc, KS > 0 ? 1u : accumulate), ...);
 }
 
+// Slot t takes its key tiles in half steps of 64 keys, f = 0, 1, ... of a part of
+// the run; step f's S and P lie in buffer f % 2. S(f + 1) is there before the
+// softmax of step f ends, so a slot's chain is its softmax alone: PV(f) and, into
+// the buffer that it has read, S(f + 2) run beside the softmax of f + 1.
 template <int D, bool HALVES>
-__device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem) {
+__device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV, uint32_t tmem, int t) {
   using C = TileCfg<D>;
-  constexpr uint32_t kIdescS = make_idesc_f32(128, 128, false);
+  constexpr uint32_t kIdescS = make_idesc_f32(128, 64, false);
   constexpr uint32_t kIdescPV = make_idesc_f32(128, D, true);
-  const uint64_t q_desc = make_smem_desc_sw128(smem_u32(sQ), 16, 1024);
+  const uint64_t q_desc = make_smem_desc_sw128(smem_u32(sQ + t * C::Q_BYTES), 16, 1024);
   const uint64_t k_desc = D == 64 ? make_smem_desc_sw64(smem_u32(sK)) : make_smem_desc_sw128(smem_u32(sK), 16, 1024);
   const uint64_t v_desc = make_smem_desc_sw128(smem_u32(sV), 128 * 128, 1024);
   const uint64_t lim = p.wait_limit_ns;
-  Ring<C::KST> k;  // the stage of the key tile that the next S takes
-  Ring<C::VST> v;  // the stage of the value tile that the next PV takes
-  const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32), k_hi = static_cast<uint32_t>(k_desc >> 32);
-  const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
-  auto issue_s = [&](int t) {
-    const uint32_t q_lo = static_cast<uint32_t>(q_desc) + t * (C::Q_BYTES >> 4);
-    const uint32_t k_lo = static_cast<uint32_t>(k_desc) + k.stage * (C::K_BYTES >> 4);
-    issue_s_steps<D>(std::make_integer_sequence<int, 2 * (D / 32)>{}, tmem + C::s_col(t), q_lo, q_hi, k_lo, k_hi, kIdescS);
-    umma_commit(&sh.s_full[t]);
+  const uint32_t q_lo = static_cast<uint32_t>(q_desc), q_hi = static_cast<uint32_t>(q_desc >> 32);
+  const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32), v_hi = static_cast<uint32_t>(v_desc >> 32);
+  constexpr uint32_t kKeyHalf = (64 * (D < 128 ? D : 128)) >> 4, kValueHalf = (64 * 128) >> 4;  // of a column chunk
+  Ring<C::KST> k;       // the stages of the tiles whose S and PV come next
+  Ring<C::VST> v;
+  uint32_t par = 0;     // parity of the buffers' use by PV, which S is one or none ahead of
+  bool used = false;    // the buffers have been used
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &sh.abort_flag, lim); };
+  auto skip_k = [&]() {
+    if (HALVES) return k.next(), true;
+    const bool ok = wait(&sh.k_full[k.stage], k.phase);
+    if (ok) mbar_arrive(&sh.k_empty[k.stage]);
+    k.next();
+    return ok;
   };
-  auto issue_pv = [&](int t, bool first) {
-    const uint32_t v_lo = static_cast<uint32_t>(v_desc) + v.stage * (C::V_BYTES >> 4);
-    issue_pv_steps(std::make_integer_sequence<int, 8>{}, tmem + C::o_col(t), tmem + C::p_col(t), v_lo, v_hi, kIdescPV,
-                   first ? 0u : 1u);
-    umma_commit(&sh.pv_done[t]);
+  auto skip_v = [&]() {
+    if (HALVES) return v.next(), true;
+    const bool ok = wait(&sh.v_full[v.stage], v.phase);
+    if (ok) mbar_arrive(&sh.v_empty[v.stage]);
+    v.next();
+    return ok;
   };
-  auto fail = [&]() {
-    record_timeout(p.status, &sh.abort_flag, WHERE_KV8_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+  auto issue_s = [&](int b, bool read, uint32_t parity) -> bool {
+    if (b == 0 && !wait(&sh.k_full[k.stage], k.phase)) return false;
+    if (read && !wait(&sh.pv_done[t][b], parity)) return false;  // the P that was there
+    tc_fence_after_sync();
+    issue_s_steps<D>(std::make_integer_sequence<int, 2 * (D / 32)>{}, tmem + C::s_col(t, b), q_lo, q_hi,
+                     static_cast<uint32_t>(k_desc) + k.stage * (C::K_BYTES >> 4) + b * kKeyHalf, k_hi, kIdescS);
+    umma_commit(&sh.s_full[t][b]);
+    if (b == 1) {
+      umma_commit(&sh.k_empty[k.stage]);
+      k.next();
+    }
+    return true;
+  };
+  auto issue_pv = [&](int b, bool first) -> bool {
+    if (b == 0 && !wait(&sh.v_full[v.stage], v.phase)) return false;
+    if (!wait(&sh.p_full[t][b], par)) return false;
+    tc_fence_after_sync();
+    issue_pv_steps(std::make_integer_sequence<int, 4>{}, tmem + C::o_col(t), tmem + C::s_col(t, b),
+                   static_cast<uint32_t>(v_desc) + v.stage * (C::V_BYTES >> 4) + b * kValueHalf, v_hi, kIdescPV, first ? 0u : 1u);
+    umma_commit(&sh.pv_done[t][b]);
+    if (b == 1) {
+      umma_commit(&sh.v_empty[v.stage]);
+      v.next();
+    }
+    return true;
   };
   Walk<D> w;
   w.begin(p, sh.start);
   int left = sh.n_tiles;
-  int cnt[2] = {0, 0};  // running S / P / PV count per query tile
-  for (int seg = 0; left > 0; ++seg) {
+  bool ok = true;
+  for (int seg = 0; ok && left > 0; ++seg) {
     const int n = min(left, w.tiles - w.s);
-    int last[2] = {-1, -1};
-#pragma unroll
-    for (int t = 0; t < C::NT; ++t) {
-      last[t] = w.last_tile(p, t, n);
-      if (!mbar_wait(&sh.q_full[t], seg & 1, &sh.abort_flag, lim)) return fail();
-      mbar_arrive(&sh.q_taken[t]);
-    }
+    const int turns = HALVES ? (n + 1 - t) / 2 : w.last_tile(p, t, n) + 1;
+    ok = wait(&sh.q_full[t], seg & 1);
+    if (ok) mbar_arrive(&sh.q_taken[t]);
     left -= n;
     w.s += n;
     w.settle(p);
-    if constexpr (HALVES) {
-      // Slot j % 2 takes key tile j: S(j) into it, P(j) from it, then S(j + 2).
-      auto start_s = [&](int t) -> bool {
-        if (!mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return false;
-        // S_t overwrites the columns the slot's P before is read from
-        if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim)) return false;
-        tc_fence_after_sync();
-        issue_s(t);
-        umma_commit(&sh.k_empty[k.stage]);
-        k.next();
-        return true;
-      };
-      if (!start_s(0) || (n > 1 && !start_s(1))) return fail();
-      for (int j0 = 0; j0 < n; j0 += 2) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j0 + t >= n) continue;
-          if (!mbar_wait(&sh.v_full[v.stage], v.phase, &sh.abort_flag, lim)) return fail();
-          if (!mbar_wait(&sh.p_full[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
-          if (j0 == 0 && seg > 0 && !mbar_wait(&sh.o_free[t], (seg - 1) & 1, &sh.abort_flag, lim)) return fail();
-          tc_fence_after_sync();
-          issue_pv(t, j0 == 0);
-          umma_commit(&sh.v_empty[v.stage]);
-          v.next();
-          ++cnt[t];
-          if (j0 + t + 2 < n && !start_s(t)) return fail();
-        }
-      }
-      continue;
-    }
-    if (!mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
-#pragma unroll
-    for (int t = 0; t < C::NT; ++t) {
-      if (last[t] < 0) continue;
-      // S_t(0) overwrites S_t / P_t of the segment before: its last PV must be done
-      if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim)) return fail();
-      tc_fence_after_sync();
-      issue_s(t);
+    if (HALVES && t == 1) skip_k(), skip_v();
+    if (ok && turns > 0) {
+      ok = issue_s(0, used, par ^ 1) && issue_s(1, used, par ^ 1);
+      // PV(0) overwrites O: the part before has to have read it
+      if (ok && seg > 0) ok = wait(&sh.o_free[t], (seg - 1) & 1);
     }
-    umma_commit(&sh.k_empty[k.stage]);
-    k.next();
-    for (int j = 0; j < n; ++j) {
-      if (!mbar_wait(&sh.v_full[v.stage], v.phase, &sh.abort_flag, lim)) return fail();
-      const bool more = j + 1 < n;
-      if (more && !mbar_wait(&sh.k_full[k.stage], k.phase, &sh.abort_flag, lim)) return fail();
+    for (int j = 0; ok && j < turns; ++j) {
+      const bool more = j + 1 < turns;
+      if (HALVES && more) skip_k();
 #pragma unroll
-      for (int t = 0; t < C::NT; ++t) {
-        if (j > last[t]) continue;
-        if (!mbar_wait(&sh.p_full[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
-        // PV_t(0) overwrites O_t: the segment before has to have read it
-        if (j == 0 && seg > 0 && !mbar_wait(&sh.o_free[t], (seg - 1) & 1, &sh.abort_flag, lim)) return fail();
-        tc_fence_after_sync();
-        issue_pv(t, j == 0);
-        if (j < last[t]) {
-          // d = 128: S_t(j + 1) overwrites the columns P_t(j) is read from
-          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], cnt[t] & 1, &sh.abort_flag, lim)) return fail();
-          tc_fence_after_sync();
-          issue_s(t);
-        }
-        ++cnt[t];
+      for (int b = 0; b < 2; ++b) {
+        ok = ok && issue_pv(b, j == 0 && b == 0);
+        if (more) ok = ok && issue_s(b, true, par);
       }
-      if (more) {
-        umma_commit(&sh.k_empty[k.stage]);
-        k.next();
-      }
-      umma_commit(&sh.v_empty[v.stage]);
-      v.next();
+      if (HALVES && more) skip_v();
+      par ^= 1;
     }
+    used = used || turns > 0;
+    // tiles that only the other slot's rows see; in halves: the other slot's last
+    for (int j = turns; !HALVES && ok && j < n; ++j) ok = skip_k() && skip_v();
+    if (HALVES && turns > 0 && (n - 1) % 2 != t) skip_k(), skip_v();
   }
-  drain_mmas(&sh.mma_drain, lim);
+  if (!ok) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_MMA);
+  drain_mmas(&sh.mma_drain[t], lim);
 }
 
 // ---------------------------------------------------------------------------
@@ -635,8 +615,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
   using C = TileCfg<D>;
   const int r = threadIdx.x & 127, lane = r & 31;
   const uint32_t lane_base = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
-  const uint32_t tS = tmem + lane_base + C::s_col(t);
-  const uint32_t tP = tmem + lane_base + C::p_col(t);
+  const uint32_t tS = tmem + lane_base + C::s_col(t, 0);
   const uint32_t tO = tmem + lane_base + C::o_col(t);
   const uint32_t q_dst = smem_u32(sQ + t * C::Q_BYTES);
   const uint64_t lim = p.wait_limit_ns;
@@ -730,41 +709,34 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     warp_arrive(&sh.q_full[t]);
 
     float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
-    for (int j = j0, turn = cnt; j <= last; j += STEP, ++turn) {
-      const int i = i0 + j, sl = i % C::SLOTS;
-      alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
-      alive = alive && warp_wait(&sh.s_full[t], turn & 1, &sh.abort_flag, lim);
+    for (int f = 0; f < 2 * turns; ++f) {  // 64 keys
+      const int j = j0 + (f >> 1) * STEP, i = i0 + j, sl = i % C::SLOTS, buf = f & 1, g = 4 * buf;
+      if (buf == 0) alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
+      alive = alive && warp_wait(&sh.s_full[t][buf], (cnt + (f >> 1)) & 1, &sh.abort_flag, lim);
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
         break;
       }
       tc_fence_after_sync();
       if (!warp_live) {  // nobody reads what its rows of P give
-        warp_arrive(&sh.p_full[t]);
+        warp_arrive(&sh.p_full[t][buf]);
         continue;
       }
-      // The row of S stays in tensor memory and is read twice, 32 columns at a
-      // time with the next 32 on their way: once for its maximum, once for the
-      // weights. Holding all 128 in registers unrolls everything: the loop then
-      // leaves the instruction cache, where the MMA thread's has to be found.
-      const int lim_col = limit - (w.s + j) * 128;
-      if (__any_sync(0xffffffffu, lim_col < 128)) {
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(tS + c, x);
-          tmem_ld_wait();
+      const uint32_t tSb = tS + buf * 64;
+      uint32_t xa[32], xb[32];
+      tmem_ld32(tSb, xa);
+      tmem_ld32(tSb + 32, xb);
+      tmem_ld_wait();
+      const int lim_col = limit - (w.s + j) * 128 - buf * 64;
+      if (__any_sync(0xffffffffu, lim_col < 64)) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c + k >= lim_col) x[k] = __float_as_uint(-INFINITY);
-          tmem_st32(tS + c, x);
+        for (int k = 0; k < 32; ++k) {
+          if (k >= lim_col) xa[k] = __float_as_uint(-INFINITY);
+          if (32 + k >= lim_col) xb[k] = __float_as_uint(-INFINITY);
         }
-        tmem_st_wait();
       }
       // 16-key groups: u = S fg + eg; a group's factor is positive, so its
       // largest u is that of its largest S.
-      uint32_t xa[32], xb[32];
-      tmem_ld32(tS, xa);
       float mx = -INFINITY;
       auto max_of = [&](const uint32_t (&x)[32], int g0) {
 #pragma unroll
@@ -780,22 +752,15 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fmaxf(qfac * sc.x, 1e-36f), sc.y));
         }
       };
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        tmem_ld_wait();
-        tmem_ld32(tS + c + 32, xb);
-        max_of(xa, c / 16);
-        tmem_ld_wait();
-        tmem_ld32(tS + (c ? 0 : 64), xa);  // at the end the first columns again
-        max_of(xb, c / 16 + 2);
-      }
+      max_of(xa, g);
+      max_of(xb, g + 2);
       const bool move = __any_sync(0xffffffffu, mx > m + (kShift + kSlack));
       const float m_ref = move ? fmaxf(m, mx - kShift) : m;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      const float alpha = ex2_approx(m - m_use);  // 0 on the first tile, 1 when the reference is kept
+      const float alpha = ex2_approx(m - m_use);  // 0 on the first step, 1 when the reference is kept
       l *= alpha;
-      // P (16 columns of packed pairs) overwrites, at d = 128, columns of S that have been read
-      auto weigh = [&](const uint32_t (&x)[32], int g0) {
+      // P (packed pairs) overwrites columns of S that have been read
+      auto weigh = [&](const uint32_t (&x)[32], int g0, uint32_t to) {
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -811,20 +776,16 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           }
           l = fmaf(sum.x + sum.y, sc.z, l);
         }
-        tmem_st16(tP + 8 * g0, pk);
+        tmem_st16(to, pk);
       };
+      weigh(xa, g, tSb);
+      weigh(xb, g + 2, tSb + 16);
+      if (f > 0 && move) {
+        // O has to hold the step before
+        alive = warp_wait(&sh.pv_done[t][buf ^ 1], (cnt + ((f - 1) >> 1)) & 1, &sh.abort_flag, lim);
+        tc_fence_after_sync();
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        tmem_ld_wait();
-        tmem_ld32(tS + c + 32, xb);
-        weigh(xa, c / 16);
-        tmem_ld_wait();
-        if (c == 0) tmem_ld32(tS + 64, xa);
-        weigh(xb, c / 16 + 2);
-      }
-      if (j > j0 && move) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; alive && c < D; c += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c, o);
           tmem_ld_wait();
@@ -836,12 +797,12 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       m = m_ref;
       tmem_st_wait();
       tc_fence_before_sync();
-      warp_arrive(&sh.p_full[t]);
+      warp_arrive(&sh.p_full[t][buf]);
     }
 
     const bool active = last >= 0;
     if (alive && active) {
-      alive = warp_wait(&sh.pv_done[t], (cnt + turns - 1) & 1, &sh.abort_flag, lim);
+      alive = warp_wait(&sh.pv_done[t][1], (cnt + turns - 1) & 1, &sh.abort_flag, lim);
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
     tc_fence_after_sync();
@@ -1001,21 +962,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.q_full[t], 4);
       mbar_init(&sh.q_taken[t], 1);
-      mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_full[t], 4);
-      mbar_init(&sh.pv_done[t], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.s_full[t][b], 1);
+        mbar_init(&sh.p_full[t][b], 4);
+        mbar_init(&sh.pv_done[t][b], 1);
+      }
       mbar_init(&sh.o_free[t], 4);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_empty[i], HALVES ? 1 : C::NT);
       mbar_init(&sh.st_full[i], 1);
       mbar_init(&sh.st_empty[i], kConvThreads / 32);
       mbar_init(&sh.v_full[i], kConvThreads / 32);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.v_empty[i], HALVES ? 1 : C::NT);
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&sh.scale_full[i], 8);
-    mbar_init(&sh.mma_drain, 1);
+    mbar_init(&sh.mma_drain[0], 1);
+    mbar_init(&sh.mma_drain[1], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.join_ml[i], 2);
       mbar_init(&sh.join_o[i], 1);
@@ -1054,9 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     convert_role<D>(p, sh, sStage, sV);
   } else if (warp == kLoadWarp) {
     load_role<D>(p, sh, sK, sStage);
-  } else if (lane_id() == 0) {
-    note_run<D>(p, sh);  // Q takes longer to come
-    mma_role<D, HALVES>(p, sh, sQ, sK, sV, tmem);
+  } else if (lane_id() == 0 && warp < kMmaWarp + C::NT) {
+    if (warp == kMmaWarp) note_run<D>(p, sh);  // Q takes longer to come
+    mma_role<D, HALVES>(p, sh, sQ, sK, sV, tmem, warp - kMmaWarp);
   }
   __syncwarp();
   tc_fence_before_sync();
