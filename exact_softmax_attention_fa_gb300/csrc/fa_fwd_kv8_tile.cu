@@ -472,13 +472,26 @@ __device__ void convert_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sS
     for (int g = 0; g < 8; ++g) seen |= (sh.scale[sl][g].w != 0.f ? 1u : 0u) << g;
     const uint8_t* src = sStage + ss * C::K_BYTES + row0 * D + unit * 8;
     const uint32_t dst = smem_u32(sV + vs * C::V_BYTES) + (unit / 8) * (128 * 128);
-#pragma unroll 8
-    for (int q = 0; q < PASSES; ++q) {
-      const int row = row0 + q * PASS_ROWS;
-      uint2 v = *reinterpret_cast<const uint2*>(src + q * PASS_ROWS * D);
-      if (row >= rows || !(seen >> (row >> 4) & 1)) v = make_uint2(0, 0);
-      st_shared_v4(dst + sw128_offset(row, unit & 7), e4m3x2_to_f16x2(v.x & 0xffffu), e4m3x2_to_f16x2(v.x >> 16),
-                   e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
+    // rows row0 + q PASS_ROWS; the swizzle repeats every 8 rows
+    constexpr int PERIOD = PASS_ROWS < 8 ? 8 / PASS_ROWS : 1;
+    uint32_t at[PERIOD];
+#pragma unroll
+    for (int q = 0; q < PERIOD; ++q) at[q] = dst + sw128_offset(row0 + q * PASS_ROWS, unit & 7);
+    auto convert = [&](int q, uint2 v) {
+      st_shared_v4(at[q % PERIOD] + (q / PERIOD) * (PERIOD * PASS_ROWS * 128), e4m3x2_to_f16x2(v.x & 0xffffu),
+                   e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y & 0xffffu), e4m3x2_to_f16x2(v.y >> 16));
+    };
+    if (rows >= 128 && seen == 0xffu) {
+#pragma unroll 4  // 2 and 16: the same time; more code than the loop needs slows the softmax's fetching
+      for (int q = 0; q < PASSES; ++q) convert(q, *reinterpret_cast<const uint2*>(src + q * PASS_ROWS * D));
+    } else {
+#pragma unroll 2
+      for (int q = 0; q < PASSES; ++q) {
+        const int row = row0 + q * PASS_ROWS;
+        uint2 v = *reinterpret_cast<const uint2*>(src + q * PASS_ROWS * D);
+        if (row >= rows || !(seen >> (row >> 4) & 1)) v = make_uint2(0, 0);
+        convert(q, v);
+      }
     }
     warp_arrive(&sh.st_empty[ss]);
     fence_proxy_async_smem();
