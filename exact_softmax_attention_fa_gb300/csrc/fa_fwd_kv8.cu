@@ -628,8 +628,13 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
 }
 
 // More query rows per K/V head than this take the 128-row tiles of
-// fa_fwd_kv8_tile.cu.
-constexpr int kTileRows = 16;
+// fa_fwd_kv8_tile.cu. This kernel reads the cache once per chunk of rows; the
+// tiles' time hardly depends on the rows below 128. B = 8, Hkv = 8, 16384 keys
+// (and B = 1, Hkv = 8, 4096 keys), rows: this kernel / tiles, us:
+//   d =  64: 16: 64 / 74 (15 / 20)    24: 94 / 74 (16 / 21)
+//   d = 128: 8: 59 / 95 (17 / 23)     16: 102 / 94 (21 / 23)   24: 143 / 97 (23 / 23)
+//   d = 256: 8: 182 / 182 (22 / 29)   12: 262 / 184 (23 / 30)  16: 343 / 184 (23 / 30)
+constexpr int tile_rows(int d) { return d == 256 ? 8 : 16; }
 
 // 8-column tiles of a row chunk: two (8 rows) where the rows fill more than one
 // and the sums of both fit the registers.
@@ -680,7 +685,7 @@ size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   if (d != 64 && d != 128 && d != 256) return 0;
   const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
   size_t off;
-  return rows > kTileRows ? kv8_tile_workspace(d) : part_bytes(d, rows, &off);
+  return rows > tile_rows(d) ? kv8_tile_workspace(d) : part_bytes(d, rows, &off);
 }
 
 fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -716,7 +721,7 @@ fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, 
   a.causal = causal;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   a.rows = a.g * Nq;
-  if (a.rows > kTileRows) return launch_kv8_tiles(a, d, workspace, dev, stream);
+  if (a.rows > tile_rows(d)) return launch_kv8_tiles(a, d, workspace, dev, stream);
   a.status = dev.status;
   const int nq = query_tiles(d, a.rows);
   a.chunks = (a.rows + 4 * nq - 1) / (4 * nq);

@@ -6,7 +6,7 @@ n keys: a weight is rounded to fp16, half a step or 2^-11 of itself, and its
 pieces hold that exactly or to 2^-24 of the row's largest weight; exp2 is within 2^-22, n terms are summed in fp32 in runs of 16 (at most n 2^-24). A
 score is a sum of d exact products in fp32 by the tensor core (two units of 2^-23
 for each of d / 16 steps, and four for its scaling) of query values that are
-exact or within e max|q|: e = 2^-22 up to 16 rows per K/V head, whose two e4m3
+exact or within e max|q|: e = 2^-22 up to 16 rows per K/V head (8 at d = 256), whose two e4m3
 pieces are summed apart with a factor of 2^4 between them, and 2^-18 above,
 where they are not. So it is off by at most
   delta = scale max_j ((d/16 + 4) 2^-22 sum |q k_j| + e max|q| sum |k_j|),
@@ -69,7 +69,7 @@ def compare(p, q, lens, counts, causal, scale, o, lse, table=None):
     """Check every row of every sequence against the definition."""
     B, Hq, Nq, d = q.shape
     Hkv = p.code[0].shape[1]
-    e_q = 2.0 ** -22 if Hq // Hkv * Nq <= 16 else 2.0 ** -18
+    e_q = 2.0 ** -22 if Hq // Hkv * Nq <= (8 if d == 256 else 16) else 2.0 ** -18
     o, lse = to_host64(o), lse.double().cpu().numpy()
     for b in range(B):
         n, c = lens[b], Nq if counts is None else counts[b]
@@ -147,6 +147,29 @@ def test_many_ragged_sequences(B):
 @pytest.mark.parametrize("d,page,Hq,Nq", [(128, 64, 4, 1), (64, 16, 8, 2), (256, 32, 2, 1), (128, 16, 2, 70)])
 def test_long_caches_shared_by_many_warps(d, page, Hq, Nq):
     check(2, Hq, 1, Nq, d, page, [9001, 4500], [Nq, Nq], True, BASE_SEED + d + page)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,page,Hq,Hkv,Nq,lens", [
+    (128, 64, 6, 2, 17, [5000, 130, 0]),    # 51 rows: one tile of rows, runs of an odd and an even number of key tiles
+    (64, 16, 4, 4, 97, [2049, 1, 1300]),    # 97 rows
+    (128, 128, 5, 1, 60, [4100, 300, 77]),  # 300 rows: two blocks, positions shared between tiles
+    (64, 32, 2, 2, 300, [3333, 300]),       # 300 rows of one head
+    (256, 32, 3, 1, 100, [3000, 700]),      # 300 rows, one tile a block
+])
+def test_chunks_shared_by_many_blocks(causal, d, page, Hq, Hkv, Nq, lens):
+    counts = [min(Nq, n) for n in lens]
+    counts[1] = min(counts[1], 5)
+    check(len(lens), Hq, Hkv, Nq, d, page, lens, counts, causal, BASE_SEED + d + Nq)
+
+
+@pytest.mark.parametrize("Nq", [33, 90])
+def test_chunks_of_many_ragged_sequences(Nq):
+    rng = np.random.default_rng(Nq)
+    lens = [int(x) for x in rng.integers(0, 400, 40)]
+    lens[0] = lens[-1] = 0
+    counts = [int(rng.integers(0, min(Nq, n) + 1)) for n in lens]
+    check(40, 4, 2, Nq, 64, 16, lens, counts, True, BASE_SEED + Nq)
 
 
 @pytest.mark.parametrize("Nq", [1, 40])
