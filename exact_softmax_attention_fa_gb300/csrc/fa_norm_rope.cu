@@ -25,7 +25,8 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kFwdThreads = 128;     // 256: 69.3 instead of 66.7 us (B = 2, N = 8192, 16 heads, d = 128)
+constexpr int kThreads = 256;        // backward
 constexpr int kHeads = 4;            // heads of one token per lane group, forward
 constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward: kBwdSide at a time
 constexpr int kBwdSide = 2;
@@ -168,11 +169,11 @@ __device__ __forceinline__ int position(const NormRope& p, int token, int n) {
 }
 
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
+__global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
   Lane<D, INTER> L;
   L.init(p);
   const int upt = p.chunks[0] + p.chunks[1] + p.chunks[2];
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / L.LPR) + threadIdx.x / L.LPR;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kFwdThreads / L.LPR) + threadIdx.x / L.LPR;
   if (unit >= static_cast<long long>(p.tokens) * upt) return;  // whole lane groups leave
   const int token = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(upt));
   int ch = static_cast<int>(unit) - token * upt;
@@ -355,7 +356,7 @@ cudaError_t launch_norm_rope(const NormRope& a, int d, int interleaved, int bloc
   if (d == D) {                                                                                             \
     auto kern = a.w[0] ? (interleaved ? FA_NORM_ROPE_KERNEL(D, true, true) : FA_NORM_ROPE_KERNEL(D, false, true)) \
                        : (interleaved ? FA_NORM_ROPE_KERNEL(D, true, false) : FA_NORM_ROPE_KERNEL(D, false, false)); \
-    kern<<<blocks, kThreads, 0, stream>>>(a);                                                               \
+    kern<<<blocks, BACK ? kThreads : kFwdThreads, 0, stream>>>(a);                                          \
     return cudaGetLastError();                                                                              \
   }
   FA_NORM_ROPE(64)
@@ -476,7 +477,7 @@ fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_i
   st = device_info(&dev);
   if (st != FA_OK) return st;
   a.status = dev.status;
-  const int groups = kThreads / (d / 8);
+  const int groups = kFwdThreads / (d / 8);
   const long long units = static_cast<long long>(a.tokens) * (a.chunks[0] + a.chunks[1] + a.chunks[2]);
   return from_cuda(launch_norm_rope<false>(a, d, interleaved, static_cast<int>((units + groups - 1) / groups), stream));
 }
