@@ -2,9 +2,9 @@
 // of a prompt, on tcgen05 (fa_fwd_kv8.cu has the mathematics and the kernel for
 // few rows).
 //
-// A CTA owns NT tiles of 128 query rows (rows of a K/V head's group, position by
-// position) and streams 128-key tiles of the cache past them, as the dense
-// forward does; what differs is how the codes reach the tensor core:
+// A CTA holds blocks of up to two tiles of 128 query rows (rows of a K/V head's
+// group, position by position) and streams 128-key tiles of the cache past them,
+// as the dense forward does; what differs is how the codes reach the tensor core:
 //   S = Q K^T  : kind::f8f6f4. K's codes are the operand as TMA brings them. A
 //       query row, moved by a power of two so that its largest |value| lies in
 //       [2^7, 2^8), is the sum of two e4m3 pieces qh + ql, accumulated into the
@@ -18,13 +18,29 @@
 // Key and value scales enter as in fa_fwd_kv8.cu: u = c sk (q . k8) + log2 sv per
 // 16-key group, P = 2^(u - m), l = sum P / sv.
 //
-// Roles: warpgroups 0 and 1 softmax, correction and epilogue of one query tile
-// each (and its Q pieces), warpgroup 2 converts V, warp 12 looks up pages and
-// loads, one thread of warp 13 issues MMAs.
+// Roles: warpgroups 0 and 1 Q pieces, softmax, correction and epilogue of one
+// slot each, warpgroup 2 converts V, warp 12 looks up pages and loads, one thread
+// each of warps 13 and 14 issues the MMAs of a slot. A slot is a tile of 128 rows;
+// where the rows of a K/V head fill only one (decoding a few tokens of a group),
+// both slots take it with every other key tile each, and the CTA joins them
+// (128 rows, B = 8, Hkv = 8, 16384 keys, d = 128: 129 us with one slot, 101 so).
+// d = 256 has tensor memory for one slot.
 //
-// Bound: tensor cores, and the softmax's exponentials behind them. Work: every
-// CTA takes an equal run of the flattened list of (sequence, K/V head, row
-// tiles, key tile); a row block that CTAs share is joined by
+// Softmax steps are 64 keys, with two buffers of S per slot: S(f + 1) is formed
+// beside the softmax of step f, so a slot waits for neither product. (128-key steps
+// with one buffer: the chain S, softmax, PV of a slot bound, 232 us for 1024 queries
+// on 16384 keys, B = 2, 16 heads on 4, d = 128; now 205. One thread issuing for
+// both slots: 369, it spends more time between MMAs than the steps leave it.)
+//
+// Bound: shared memory, at that size at 0.61 of the tensor rate. Two slots take
+// some 3600 cycles for 128 keys. The tensor core alone would take 2477 (measured;
+// 2049 with 128-column S, for which tensor memory has no second buffer): a
+// 64-column S reads 6 KB of operands per 48 cycles. With V's conversion and the
+// loads that makes 370 KB, 2900 cycles at 128 bytes each. A CTA's fixed work (the
+// search for its run, Q pieces, the epilogue) takes 10 us, most of a small call.
+//
+// Work: every CTA takes an equal run of the flattened list of (sequence, K/V
+// head, row block, key tile); a row block that CTAs share is joined by
 // kv8_tile_combine_kernel. So neither ragged lengths nor few row blocks against
 // long caches leave SMs idle.
 #include <algorithm>
@@ -44,7 +60,7 @@ constexpr int kMinTiles = 2;    // a CTA's run is not cut below this
 constexpr float kSlack = 8.f;   // P <= 2^(kShift + kSlack) = 2^14, fp16
 template <int D>
 struct TileCfg {
-  static constexpr int NT = D <= 128 ? 2 : 1;
+  static constexpr int NT = D <= 128 ? 2 : 1;     // slots
   static constexpr int ROWS = NT * 128;
   static constexpr int Q_BYTES = 2 * 128 * D;     // two pieces of a query tile
   static constexpr int K_BYTES = 128 * D;         // codes of a key tile
@@ -81,7 +97,9 @@ struct Deal {
     per = used > 0 ? total / used : 0;
     more = total - per * used;
   }
-  __device__ __forceinline__ long long first(int c) const { return c >= used ? per * used + more : c * per + min(static_cast<long long>(c), more); }
+  __device__ __forceinline__ long long first(int c) const {  // tile of CTA c's run
+    return c >= used ? per * used + more : c * per + min(static_cast<long long>(c), more);
+  }
   __device__ __forceinline__ int holder(long long x) const {
     const long long head = more * (per + 1);
     return static_cast<int>(x < head ? x / (per + 1) : more + (x - head) / per);
@@ -98,7 +116,7 @@ struct TileShared {
   uint64_t mma_drain[2];
   uint64_t join_ml[4], join_o[4], join_done[4];  // two halves of the keys: per warp pair
   float2 half_ml[2][TileCfg<D>::NT == 2 ? 128 : 1];
-  float4 scale[SLOTS][8];  // c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
+  float4 scale[SLOTS][4][2];  // of the 8 groups of 16 keys: c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
   int4 start;
   float qfac[TileCfg<D>::NT][128];
   Deal deal;
@@ -394,7 +412,8 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
     if (!ok) break;
     const int slot8 = i % C::SLOTS;
     if (lane >= j0 && lane < j0 + 8) {
-      sh.scale[slot8][lane - j0] = entry;
+      float* to = reinterpret_cast<float*>(sh.scale[slot8]) + lane - j0;
+      to[0] = entry.x, to[8] = entry.y, to[16] = entry.z, to[24] = entry.w;
       mbar_arrive(&sh.scale_full[slot8]);
     }
     // lane p < pages: page p of the tile
@@ -467,9 +486,9 @@ __device__ void convert_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sS
     if (!ok) break;
     // Keys behind the sequence and on bad pages: 0 (what lies there may be NaN codes, and 0 * NaN is not 0).
     const int rows = w.len - w.s * 128;
-    uint32_t seen = 0;
-#pragma unroll
-    for (int g = 0; g < 8; ++g) seen |= (sh.scale[sl][g].w != 0.f ? 1u : 0u) << g;
+    const float4 sa = sh.scale[sl][3][0], sb = sh.scale[sl][3][1];
+    const uint32_t seen = (sa.x != 0.f) | (sa.y != 0.f) << 1 | (sa.z != 0.f) << 2 | (sa.w != 0.f) << 3 |
+                          (sb.x != 0.f) << 4 | (sb.y != 0.f) << 5 | (sb.z != 0.f) << 6 | (sb.w != 0.f) << 7;
     const uint8_t* src = sStage + ss * C::K_BYTES + row0 * D + unit * 8;
     const uint32_t dst = smem_u32(sV + vs * C::V_BYTES) + (unit / 8) * (128 * 128);
     // rows row0 + q PASS_ROWS; the swizzle repeats every 8 rows
@@ -723,7 +742,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
 
     float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
     for (int f = 0; f < 2 * turns; ++f) {  // 64 keys
-      const int j = j0 + (f >> 1) * STEP, i = i0 + j, sl = i % C::SLOTS, buf = f & 1, g = 4 * buf;
+      const int j = j0 + (f >> 1) * STEP, i = i0 + j, sl = i % C::SLOTS, buf = f & 1;
       if (buf == 0) alive = alive && warp_wait(&sh.scale_full[sl], (i / C::SLOTS) & 1, &sh.abort_flag, lim);
       alive = alive && warp_wait(&sh.s_full[t][buf], (cnt + (f >> 1)) & 1, &sh.abort_flag, lim);
       if (!alive) {
@@ -751,48 +770,49 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       // 16-key groups: u = S fg + eg; a group's factor is positive, so its
       // largest u is that of its largest S.
       float mx = -INFINITY;
-      auto max_of = [&](const uint32_t (&x)[32], int g0) {
+      float4 fg = sh.scale[sl][0][buf];
+      const float4 eg = sh.scale[sl][1][buf];
+      fg.x = fmaxf(qfac * fg.x, 1e-36f), fg.y = fmaxf(qfac * fg.y, 1e-36f);
+      fg.z = fmaxf(qfac * fg.z, 1e-36f), fg.w = fmaxf(qfac * fg.w, 1e-36f);
+      auto max_of = [&](const uint32_t (&x)[32], int h, float fac, float add) {
+        auto f = [&](int k) { return __uint_as_float(x[16 * h + k]); };
+        float ga = fmaxf(f(0), f(1)), gb = fmaxf(f(2), f(3));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 sc = *reinterpret_cast<const float2*>(&sh.scale[sl][g0 + h]);
-          auto f = [&](int k) { return __uint_as_float(x[16 * h + k]); };
-          float ga = fmaxf(f(0), f(1)), gb = fmaxf(f(2), f(3));
-#pragma unroll
-          for (int k = 4; k < 16; k += 4) {
-            ga = fmax3(ga, f(k), f(k + 1));
-            gb = fmax3(gb, f(k + 2), f(k + 3));
-          }
-          mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fmaxf(qfac * sc.x, 1e-36f), sc.y));
+        for (int k = 4; k < 16; k += 4) {
+          ga = fmax3(ga, f(k), f(k + 1));
+          gb = fmax3(gb, f(k + 2), f(k + 3));
         }
+        mx = fmaxf(mx, fmaf(fmaxf(ga, gb), fac, add));
       };
-      max_of(xa, g);
-      max_of(xb, g + 2);
+      max_of(xa, 0, fg.x, eg.x);
+      max_of(xa, 1, fg.y, eg.y);
+      max_of(xb, 0, fg.z, eg.z);
+      max_of(xb, 1, fg.w, eg.w);
       const bool move = __any_sync(0xffffffffu, mx > m + (kShift + kSlack));
       const float m_ref = move ? fmaxf(m, mx - kShift) : m;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m - m_use);  // 0 on the first step, 1 when the reference is kept
       l *= alpha;
       // P (packed pairs) overwrites columns of S that have been read
-      auto weigh = [&](const uint32_t (&x)[32], int g0, uint32_t to) {
-        uint32_t pk[16];
+      const float4 zg = sh.scale[sl][2][buf];
+      uint32_t pk[16];
+      auto weigh = [&](const uint32_t (&x)[32], int h, float a, float b, float z) {
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 sc = sh.scale[sl][g0 + h];
-          const float a = fmaxf(qfac * sc.x, 1e-36f), b = sc.y - m_use;
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 u = ffma2_bcast(__uint_as_float(x[16 * h + 2 * k]), __uint_as_float(x[16 * h + 2 * k + 1]), a, b);
-            const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-            sum = fadd2(sum, e);
-            pk[8 * h + k] = pack_f16x2(e.x, e.y);
-          }
-          l = fmaf(sum.x + sum.y, sc.z, l);
+        for (int k = 0; k < 8; ++k) {
+          const float2 u = ffma2_bcast(__uint_as_float(x[16 * h + 2 * k]), __uint_as_float(x[16 * h + 2 * k + 1]), a, b);
+          const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+          sum = fadd2(sum, e);
+          pk[8 * h + k] = pack_f16x2(e.x, e.y);
         }
-        tmem_st16(to, pk);
+        l = fmaf(sum.x + sum.y, z, l);
       };
-      weigh(xa, g, tSb);
-      weigh(xb, g + 2, tSb + 16);
+      weigh(xa, 0, fg.x, eg.x - m_use, zg.x);
+      weigh(xa, 1, fg.y, eg.y - m_use, zg.y);
+      tmem_st16(tSb, pk);
+      weigh(xb, 0, fg.z, eg.z - m_use, zg.z);
+      weigh(xb, 1, fg.w, eg.w - m_use, zg.w);
+      tmem_st16(tSb + 16, pk);
       if (f > 0 && move) {
         // O has to hold the step before
         alive = warp_wait(&sh.pv_done[t][buf ^ 1], (cnt + ((f - 1) >> 1)) & 1, &sh.abort_flag, lim);
