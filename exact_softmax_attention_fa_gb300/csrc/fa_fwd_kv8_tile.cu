@@ -217,15 +217,16 @@ struct RowPlace {
 
 // Key tiles of all blocks of sequence b for one K/V head.
 template <int D>
-__device__ __forceinline__ int sequence_tiles(const TileLaunch& p, int b) {
+__device__ __forceinline__ long long sequence_tiles(const TileLaunch& p, int b) {
   constexpr int ROWS = TileCfg<D>::ROWS;
   Walk<D> w;
   w.b = b;
   w.load(p);
-  if (!p.causal) return w.blocks * ((w.len + 127) / 128);
+  if (!p.causal) return static_cast<long long>(w.blocks) * ((w.len + 127) / 128);
   // a block sees the keys up to its last row's position, which moves by ROWS / g a block
   const int step = ROWS / p.g, part = ROWS - step * p.g;
-  int n = 0, pos = (ROWS - 1) / p.g, rest = ROWS - 1 - pos * p.g;
+  long long n = 0;
+  int pos = (ROWS - 1) / p.g, rest = ROWS - 1 - pos * p.g;
   for (int blk = 0; blk < w.blocks; ++blk) {
     n += (min(w.len, max(0, w.len - w.count + min(pos, w.count - 1) + 1)) + 127) / 128;
     pos += step;
@@ -241,11 +242,11 @@ __device__ __forceinline__ int sequence_tiles(const TileLaunch& p, int b) {
 // All lanes of one warp: the block (and tile of it) that tile x of the list is;
 // first: sequence_tiles of sequence `lane` (0 behind the last).
 template <int D>
-__device__ int4 tile_search(const TileLaunch& p, int first, long long x) {
+__device__ int4 tile_search(const TileLaunch& p, long long first, long long x) {
   const int lane = threadIdx.x & 31;
   for (int b0 = 0;; b0 += 32) {
-    const int one = b0 == 0 ? first : b0 + lane < p.c.B ? sequence_tiles<D>(p, b0 + lane) : 0;
-    long long incl = static_cast<long long>(one) * p.c.Hkv;
+    const long long one = b0 == 0 ? first : b0 + lane < p.c.B ? sequence_tiles<D>(p, b0 + lane) : 0;
+    long long incl = one * p.c.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -256,13 +257,14 @@ __device__ int4 tile_search(const TileLaunch& p, int first, long long x) {
       x -= __shfl_sync(0xffffffffu, incl, 31);
       continue;
     }
-    const int l = __ffs(past) - 1, per_head = __shfl_sync(0xffffffffu, one, l);
-    long long rem = x - (__shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(per_head) * p.c.Hkv);
+    const int l = __ffs(past) - 1;
+    const long long per_head = __shfl_sync(0xffffffffu, one, l);
+    long long rem = x - (__shfl_sync(0xffffffffu, incl, l) - per_head * p.c.Hkv);
     Walk<D> w;
     w.b = b0 + l;
     w.load(p);
     const int h = static_cast<int>(rem / per_head);
-    rem -= static_cast<long long>(h) * per_head;
+    rem -= h * per_head;
     for (int k0 = 0;; k0 += 32) {  // the block within the head
       const int own = k0 + lane < w.blocks ? w.tiles_of(p, k0 + lane) : 0;
       int in = own;
@@ -1025,9 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   if (warp == kLoadWarp) {  // the CTA's run
     if (lane_id() == 0) tma_prefetch_desc(&p.tmK);
     const int lane = threadIdx.x & 31;
-    const int first = lane < p.c.B ? sequence_tiles<D>(p, lane) : 0;
-    long long total = static_cast<long long>(first) * p.c.Hkv;
-    for (int b = lane + 32; b < p.c.B; b += 32) total += static_cast<long long>(sequence_tiles<D>(p, b)) * p.c.Hkv;
+    const long long first = lane < p.c.B ? sequence_tiles<D>(p, lane) : 0;
+    long long total = first * p.c.Hkv;
+    for (int b = lane + 32; b < p.c.B; b += 32) total += sequence_tiles<D>(p, b) * p.c.Hkv;
     const Deal deal(warp_sum(total), gridDim.x);
     const long long x0 = deal.first(blockIdx.x), x1 = deal.first(blockIdx.x + 1);
     int4 at = make_int4(p.c.B, 0, 0, 0);
