@@ -11,6 +11,7 @@ memory and streams.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -381,6 +382,12 @@ def _refuse(named):
     raise ValueError("tensors of one call must have matching types, shapes and devices")
 
 
+def _bytes(workspace):
+    """Is the workspace, if given, one run of bytes?"""
+    import torch
+    return workspace is None or (workspace.dtype == torch.uint8 and workspace.is_contiguous())
+
+
 def _devices(*tensors):
     """Their CUDA devices (None for a tensor not given; -1: not on a GPU)."""
     return {t.get_device() for t in tensors if t is not None}
@@ -510,6 +517,7 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
                                 and xq[3] == xk[3] == 1 and dwq.dtype == dwk.dtype == torch.float32
                                 and dwq.shape == dwk.shape == (d,) and dwq.is_contiguous() and dwk.is_contiguous()))
             and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d)
+            and _bytes(workspace)
             and _devices(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk,
                          workspace) == {torch.cuda.current_device()}):
         _refuse(_norm_rope_named(B, Hq, Hkv, N, d, (("dq", dq), ("dk", dk), ("dv", dv)),
@@ -607,7 +615,7 @@ def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, 
     if Hkv < 1 or Hq % Hkv != 0:
         raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
     if not (lse.dtype == torch.float32 and lse.shape == (B, Hq, Nq) and lse.is_contiguous()
-            and _devices(q, lse, workspace) == {q.get_device()}):
+            and _bytes(workspace) and _devices(q, lse, workspace) == {q.get_device()}):
         _refuse((("lse", lse, (torch.float32,), (B, Hq, Nq), True),
                  ("workspace", workspace, (torch.uint8,), () if workspace is None else workspace.shape, True)))
     check("fa_fwd_kv8", load().fa_fwd_kv8(
@@ -689,8 +697,9 @@ def norm_rope(q_in, k_in, v_in=None, wq=None, wk=None, cos=None, sin=None, posit
     """Allocate q, k (and v) as [B, H, N, d] with torch and run fa_norm_rope_fwd: what `forward` and
     the cache take, from the views of a packed projection."""
     import torch
-    q, k = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) for x in (q_in, k_in))
-    v = None if v_in is None else torch.empty(v_in.shape, dtype=torch.bfloat16, device=v_in.device)
+    with _on_stream(stream):
+        q, k = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) for x in (q_in, k_in))
+        v = None if v_in is None else torch.empty(v_in.shape, dtype=torch.bfloat16, device=v_in.device)
     fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved, eps, stream)
     return q, k, v
 
@@ -704,22 +713,26 @@ def norm_rope_backward(dq, dk, dv, q_in, k_in, wq=None, wk=None, cos=None, sin=N
     """
     import torch
     B, Hq, N, d = _dims(dq)
-    if out is None:
-        out = (torch.empty_like(dq), torch.empty_like(dk), None if dv is None else torch.empty_like(dv))
     dwq = dwk = None
-    if wq is not None:
-        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dq.device) for _ in range(2))
-        if workspace is None:
-            workspace = torch.empty(max(1, fa_norm_rope_bwd_workspace_size(B, Hq, int(dk.shape[1]), N, d)),
-                                    dtype=torch.uint8, device=dq.device)
+    with _on_stream(stream):
+        if out is None:
+            out = (torch.empty_like(dq), torch.empty_like(dk), None if dv is None else torch.empty_like(dv))
+        if wq is not None:
+            dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dq.device) for _ in range(2))
+            if workspace is None:
+                workspace = torch.empty(max(1, fa_norm_rope_bwd_workspace_size(B, Hq, int(dk.shape[1]), N, d)),
+                                        dtype=torch.uint8, device=dq.device)
     fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, *out, dwq, dwk, workspace, interleaved, eps,
                      stream)
     return (*out, dwq, dwk)
 
 
 def _on_stream(stream):
-    """torch's context for a stream given as None, a torch stream or a raw handle."""
+    """torch's context for a stream given as None, a torch stream or a raw handle: what is allocated
+    in it may be freed while that stream still uses it."""
     import torch
+    if stream is None:
+        return contextlib.nullcontext()
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
@@ -751,10 +764,16 @@ class KV8Cache:
         return self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.page_table, self.lens
 
     def append(self, k, v, counts=None, stream=None) -> None:
-        """Lengthen each sequence by counts[b] (None: n) tokens and write k, v [B, Hkv, n, d] there."""
+        """Lengthen each sequence by counts[b] (None: n) tokens and write k, v [B, Hkv, n, d] there.
+        A call that is refused leaves the lengths as they were."""
+        new = int(k.shape[2]) if counts is None else counts
         with _on_stream(stream):
-            self.lens.add_(int(k.shape[2]) if counts is None else counts)
-        fa_kv8_append(k, v, *self._cache(), counts, stream)
+            self.lens.add_(new)
+            try:
+                fa_kv8_append(k, v, *self._cache(), counts, stream)
+            except Exception:
+                self.lens.sub_(new)
+                raise
 
     def gather(self, n: int, stream=None):
         """The first n tokens' k, v as bf16 [B, Hkv, n, d], zero past a sequence's length."""
@@ -775,8 +794,9 @@ class KV8Cache:
         handle = _stream_handle(stream)
         key = (Hq, Nq, handle)
         with _on_stream(stream):
-            o = torch.empty_like(q) if counts is None else torch.zeros_like(q)
-            lse = torch.zeros((B, Hq, Nq), dtype=torch.float32, device=q.device)
+            make = torch.empty if counts is None else torch.zeros
+            o = make(q.shape, dtype=q.dtype, device=q.device)
+            lse = make((B, Hq, Nq), dtype=torch.float32, device=q.device)
             workspace = self._workspaces.get(key)
             capturing = torch.cuda.is_current_stream_capturing()
             if workspace is None or capturing:

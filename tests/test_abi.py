@@ -394,3 +394,14 @@ def test_fwd_kv8_workspace_size(lib):
     assert size(2, 4, 2, 1, 96) == 0
     # it does not grow with the batch: parts belong to warps
     assert size(1, 4, 2, 1, 128) == size(500, 4, 2, 1, 128) > 0
+
+
+def test_a_refused_append_leaves_the_cache_lengths():
+    import torch
+    import exact_softmax_attention_fa_gb300 as fa
+    cache = fa.KV8Cache(2, 1, 64, 32, page=16, device="cpu")
+    k = torch.zeros(2, 1, 3, 64, dtype=torch.bfloat16)
+    for bad, counts in ((k, None), (k.float(), None), (k[:, :, :, :32], None), (k, torch.ones(2, dtype=torch.int32))):
+        with pytest.raises(Exception):  # not on a CUDA device, and of the wrong type or shape
+            cache.append(bad, bad, counts)
+        assert cache.lens.tolist() == [0, 0]

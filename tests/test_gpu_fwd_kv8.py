@@ -413,3 +413,57 @@ def test_tensors_are_checked():
     assert e.value.status == 1
     assert c.attend(torch.empty(1, 4, 0, 64, dtype=torch.bfloat16, device="cuda"))[0].shape == (1, 4, 0, 64)
     assert fa.fa_get_device_status() == 0
+
+
+def test_workspaces_are_one_run_of_bytes():
+    import torch
+    import exact_softmax_attention_fa_gb300 as fa
+    c = fa.KV8Cache(1, 2, 64, 32, 16)
+    q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(1, 4, 1, device="cuda")
+    size = fa.fa_fwd_kv8_workspace_size(1, 4, 2, 1, 64)
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for ws in (one.expand(size), torch.zeros(2 * size, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_kv8(q, *c._cache(), o, lse, True, 0.125, None, ws)
+    k = q[:, :2].contiguous()
+    w = torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        fa.norm_rope_backward(q, k, None, q, k, w, w, workspace=one.expand(1 << 20))
+    assert fa.fa_get_device_status() == 0
+
+
+def test_the_chain_on_a_stream_of_its_own_while_others_allocate():
+    import torch
+    import exact_softmax_attention_fa_gb300 as fa
+    gen = torch.Generator(device="cuda").manual_seed(BASE_SEED)
+    B, Hq, Hkv, N, d = 2, 8, 2, 700, 128
+    x = torch.randn(B, Hq + 2 * Hkv, N, d, generator=gen, device="cuda").bfloat16()
+    wq, wk = (torch.randn(d, generator=gen, device="cuda") for _ in range(2))
+    cos, sin = fa.rope_tables(N, d)
+    xq, xk, xv = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    caches = []  # made on the current stream, so they stay until the side stream is done
+
+    def chain(stream):
+        q, k, v = fa.norm_rope(xq, xk, xv, wq, wk, cos, sin, stream=stream)
+        cache = fa.KV8Cache(B, Hkv, d, N)
+        caches.append(cache)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        cache.append(k, v, stream=stream)
+        o, lse = cache.attend(q, stream=stream)
+        return (o, lse, *fa.norm_rope_backward(o, k, v, xq, xk, wq, wk, cos, sin, stream=stream))
+
+    want = chain(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    runs = []
+    for _ in range(8):
+        runs.append(chain(side))
+        for size in (1 << 20, 1 << 22):  # what the chain has freed is not handed out here
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    side.synchronize()
+    torch.cuda.synchronize()
+    for got in runs:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert fa.fa_get_device_status() == 0
