@@ -115,7 +115,7 @@ struct TileShared {
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];  // [slot][buffer of S]
   uint64_t scale_full[SLOTS];
   uint64_t mma_drain[2];
-  uint64_t join_ml[4], join_o[4], join_done[4];  // two halves of the keys: per warp pair
+  uint64_t join_ml[4], join_o[2][4];  // two halves of the keys: per warp pair
   float2 half_ml[2][TileCfg<D>::NT == 2 ? 128 : 1];
   float4 scale[SLOTS][4][2];  // of the 8 groups of 16 keys: c sk, log2 sv, 2^-kSumBias / sv, seen (1 or 0)
   int4 start;
@@ -354,6 +354,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
 }
+// The four warps of softmax warpgroup t; they all come, also after a timeout.
+__device__ __forceinline__ void warpgroup_sync(int t) { named_barrier_sync(1 + t, 128); }
 // One arrival for a warp's lanes: 32 of them on one barrier are 32 passes of
 // the shared-memory pipe, which the tensor core's operands need.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -675,26 +677,27 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     // The MMA thread has taken note of the segment before (else an idle tile's
     // warpgroup could run two arrivals ahead of its parity wait).
     if (alive && seg > 0) {
-      alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim) &&
-              (!HALVES || t == 0 || warp_wait(&sh.join_done[r >> 5], (seg - 1) & 1, &sh.abort_flag, lim));
+      alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim);
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     }
-    float qfac = 0.f;
-    // rows are in order: a warp without a live one has nothing to bring or store
-    const bool warp_live = row0 + (r & ~31) < w.count * p.g;
-    if (alive && last >= 0 && warp_live) {
-      // The warp's 32 rows as Q pieces, 8 columns a lane (whole lines a load); S of
-      // the segment before is complete, so the tile is free.
+    // rows are in order: a warp without a live one has nothing to weigh or store
+    const int live_rows = min(128, w.count * p.g - row0);
+    const bool warp_live = (r & ~31) < live_rows;
+    if (seg > 0) warpgroup_sync(t);  // the Q tile has served every warp's epilogue
+    if (alive && last >= 0) {
+      // Rows as Q pieces, 8 columns a lane (whole lines a load); S of the segment
+      // before is complete, so the tile is free. The warps take turns, whatever rows
+      // are live; rows up to the last live warp's 32nd are 0.
       constexpr int LPR = D / 8, RPP = 32 / LPR;  // lanes a row, rows a pass
-      constexpr int PASSES = 32 / RPP, BATCH = PASSES < 8 ? PASSES : 8;  // a batch's loads are issued together
-      const int col = lane % LPR, warp_row = r & ~31;
+      constexpr int BATCH = 32 / RPP < 8 ? 32 / RPP : 8;  // a batch's loads are issued together
+      const int col = lane % LPR, passes = (live_rows + 31) / 32 * (32 / RPP);
       // unit numbers along the row [qh | ql]; a lane has half a unit of each
       const int uh = col >> 1, ul = uh + D / 16;
       const uint32_t hi_at = q_dst + (uh >> 3) * (128 * 128) + (col & 1) * 8;
       const uint32_t lo_at = q_dst + (ul >> 3) * (128 * 128) + (col & 1) * 8;
-      RowPlace at_q(p, w, row0 + warp_row + lane / LPR, RPP);
+      RowPlace at_q(p, w, row0 + (r >> 5) * RPP + lane / LPR, 4 * RPP);
 #pragma unroll 1
-      for (int q0 = 0; q0 < PASSES; q0 += BATCH) {
+      for (int q0 = r >> 5; q0 < passes; q0 += 4 * BATCH) {
         uint4 raw[BATCH];
         uint32_t amax[BATCH];  // bits of the row's largest |value|
 #pragma unroll
@@ -716,7 +719,8 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           for (int q = 0; q < BATCH; ++q) amax[q] = max(amax[q], __shfl_xor_sync(0xffffffffu, amax[q], o));
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
-          const int in_tile = warp_row + (q0 + q) * RPP + lane / LPR;
+          if (q0 + 4 * q >= passes) break;
+          const int in_tile = (q0 + 4 * q) * RPP + lane / LPR;
           const uint32_t w4[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
           // exponent of the largest value; 2^-100 and below are left as they are
           const int x = min(max(static_cast<int>(amax[q] >> 7) - 127, -100), 127);
@@ -737,11 +741,11 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
           if (col == 0) sh.qfac[t][in_tile] = exp2i(x - 7);
         }
       }
-      __syncwarp();
-      qfac = sh.qfac[t][r];  // the row's power of two
       fence_proxy_async_smem();
     }
     warp_arrive(&sh.q_full[t]);
+    warpgroup_sync(t);
+    const float qfac = sh.qfac[t][r];  // the row's power of two
 
     float m = -INFINITY, l = 0.f;  // reference - kShift, sum of P / sv
     for (int f = 0; f < 2 * turns; ++f) {  // 64 keys
@@ -845,114 +849,104 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     float own = 1.f;  // what this warpgroup's O is multiplied with
     // 4 KB per warp in each 16 KB of both Q tiles, whose last S is complete:
     // the warp's own rows of them
-    const uint32_t area = smem_u32(sQ) + (r >> 5) * 4096;
+    const int quarter = r >> 5;
+    const uint32_t area = smem_u32(sQ) + quarter * 4096;
     if constexpr (HALVES) {
       // The two halves of the keys: both warps of the same rows learn the other's
-      // m and l; the second leaves its O in shared memory, the first goes on
-      // with the sum.
-      const int quarter = r >> 5;
+      // m and l; each leaves the other's half of its O's columns in the other's Q
+      // tile and goes on with the sum of its own half.
       sh.half_ml[t][r] = make_float2(m, l);
       warp_arrive(&sh.join_ml[quarter]);
-      if (alive) {
-        alive = warp_wait(&sh.join_ml[quarter], seg & 1, &sh.abort_flag, lim);
-        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
-      }
-      if (alive) {
+      alive = alive && warp_wait(&sh.join_ml[quarter], seg & 1, &sh.abort_flag, lim);
+      if (alive && warp_live) {
         const float2 other = sh.half_ml[t ^ 1][r];
         const float both = fmaxf(m, other.x), ref = both == -INFINITY ? 0.f : both;
         own = ex2_approx(m - ref);
         l = l * own + other.y * ex2_approx(other.x - ref);
         m = both;
-      }
-      if (t == 1) {
-        if (alive && warp_live) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_ld_wait();
+        for (int c = (t ^ 1) * (D / 2); c < ((t ^ 1) + 1) * (D / 2); c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = active ? __float_as_uint(__uint_as_float(o[k]) * own) : 0u;
+          for (int k = 0; k < 32; ++k) o[k] = active ? __float_as_uint(__uint_as_float(o[k]) * own) : 0u;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_shared_v4(area + c * 512 + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          }
+          for (int u = 0; u < 8; ++u)
+            st_shared_v4(area + c * 512 + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
         }
-        warp_arrive(&sh.join_o[quarter]);
-      } else if (alive) {
-        alive = warp_wait(&sh.join_o[quarter], seg & 1, &sh.abort_flag, lim);
-        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
       }
+      warp_arrive(&sh.join_o[t][quarter]);
     }
-    if (alive && warp_live && !(HALVES && t == 1)) {
+    if (alive && warp_live) {
       const bool whole = n == w.tiles;
-      const RowEnd end(m, l);
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (seg > 0)) * C::ROWS + (HALVES ? 0 : t * 128) + r;
-      // 128 bytes of each of the warp's 32 rows at a time (32 fp32 or 64 bf16
-      // columns) through its own 4 KB of the Q tile, whose last S is complete:
-      // stores of whole lines. Row i's pieces are XORed as in the tiles.
-      const uint32_t stage = q_dst + (r >> 5) * 4096;
-      const int cols = whole ? 64 : 32;
-      // the rows this lane stores, four rows a pass
-      uint8_t* to[8];
-      RowPlace at_q(p, w, row - lane + (lane >> 3), 4);
+      // 32 columns of the warp's 32 rows at a time through its own 4 KB of the Q
+      // tile: stores of 64 (bf16) or 128 bytes of a row, eight or four rows a pass.
+      // Row i's pieces are XORed as in the tiles.
+      const uint32_t stage = q_dst + quarter * 4096;
+      const int sub = whole ? lane & 3 : lane & 7, r_in = whole ? lane >> 2 : lane >> 3, step = whole ? 8 : 4;
+      uint8_t* to[8];  // where the lane stores
+      RowPlace at_q(p, w, row - lane + r_in, step);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         to[q] = nullptr;
-        if (at_q.qi < w.count)
+        if (q * step < 32 && at_q.qi < w.count)
           to[q] = (whole ? reinterpret_cast<uint8_t*>(p.o + at_q.index() * D)
-                         : reinterpret_cast<uint8_t*>(p.part + (slot - lane + q * 4 + (lane >> 3)) * D)) + (lane & 7) * 16;
+                         : reinterpret_cast<uint8_t*>(p.part + (slot - lane + q * 4 + r_in) * D)) + sub * 16;
         at_q.next();
       }
+      if constexpr (HALVES) alive = warp_wait(&sh.join_o[t ^ 1][quarter], seg & 1, &sh.abort_flag, lim);
+      const RowEnd end(m, l);
 #pragma unroll 1
-      for (int c = 0; c < D; c += cols) {
-        __syncwarp();
-#pragma unroll 1
-        for (int half = 0; half < (whole ? 2 : 1); ++half) {
-          uint32_t o[32];
-          tmem_ld32(tO + c + 32 * half, o);
-          tmem_ld_wait();
-          if constexpr (HALVES) {
+      for (int c = HALVES ? t * (D / 2) : 0; alive && c < (HALVES ? (t + 1) * (D / 2) : D); c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c, o);
+        tmem_ld_wait();
+        if constexpr (HALVES) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const uint4 x = ld_shared_v4(area + (c + 32 * half) * 512 + sw128_offset(lane, u));
-              o[4 * u] = __float_as_uint(fmaf(__uint_as_float(o[4 * u]), own, __uint_as_float(x.x)));
-              o[4 * u + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 1]), own, __uint_as_float(x.y)));
-              o[4 * u + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 2]), own, __uint_as_float(x.z)));
-              o[4 * u + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 3]), own, __uint_as_float(x.w)));
-            }
-          }
-          if (whole) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                x[k] = pack_bf16x2(end(__uint_as_float(o[8 * u + 2 * k])), end(__uint_as_float(o[8 * u + 2 * k + 1])));
-              st_shared_v4(stage + sw128_offset(lane, half * 4 + u), x[0], x[1], x[2], x[3]);
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_shared_v4(stage + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          for (int u = 0; u < 8; ++u) {
+            const uint4 x = ld_shared_v4(area + c * 512 + sw128_offset(lane, u));
+            if (!active) o[4 * u] = o[4 * u + 1] = o[4 * u + 2] = o[4 * u + 3] = 0;
+            o[4 * u] = __float_as_uint(fmaf(__uint_as_float(o[4 * u]), own, __uint_as_float(x.x)));
+            o[4 * u + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 1]), own, __uint_as_float(x.y)));
+            o[4 * u + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 2]), own, __uint_as_float(x.z)));
+            o[4 * u + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * u + 3]), own, __uint_as_float(x.w)));
           }
         }
+        __syncwarp();  // the columns before have left
+        if (whole) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = pack_bf16x2(end(__uint_as_float(o[8 * u + 2 * k])), end(__uint_as_float(o[8 * u + 2 * k + 1])));
+            st_shared_v4(stage + sw128_offset(lane, u), x[0], x[1], x[2], x[3]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            st_shared_v4(stage + sw128_offset(lane, u), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        }
         __syncwarp();
-        // 128 bytes a pass and row; none of a part whose keys no row of the tile sees: 0
+        uint4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q * step < 32) v[q] = ld_shared_v4(stage + sw128_offset(q * step + r_in, sub));
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          uint4 v = ld_shared_v4(stage + sw128_offset(q * 4 + (lane >> 3), lane & 7));
-          if (!active) v = make_uint4(0, 0, 0, 0);
-          if (to[q]) *reinterpret_cast<uint4*>(to[q] + c / cols * 128) = v;
+          if (!HALVES && !active) v[q] = make_uint4(0, 0, 0, 0);  // a part whose keys no row of the tile sees
+          if (to[q]) *reinterpret_cast<uint4*>(to[q] + c * (whole ? 2 : 4)) = v[q];
         }
       }
-      if (live) {
+      if (live && !(HALVES && t == 1)) {
         if (whole) p.lse[at] = end.lse; else p.part_ml[slot] = make_float2(m, l);
       }
     }
+    if (HALVES && !alive) record_timeout(p.status, &sh.abort_flag, WHERE_KV8_SOFTMAX);
     tc_fence_before_sync();
     warp_arrive(&sh.o_free[t]);
-    if (HALVES && t == 0) warp_arrive(&sh.join_done[r >> 5]);
     cnt += turns;
     i0 += n;
     left -= n;
@@ -1018,8 +1012,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
     mbar_init(&sh.mma_drain[1], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.join_ml[i], 2);
-      mbar_init(&sh.join_o[i], 1);
-      mbar_init(&sh.join_done[i], 1);
+      mbar_init(&sh.join_o[0][i], 1);
+      mbar_init(&sh.join_o[1][i], 1);
     }
     sh.abort_flag = 0;
     fence_mbarrier_init();
