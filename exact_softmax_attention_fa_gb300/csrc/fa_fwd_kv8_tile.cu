@@ -1152,7 +1152,8 @@ cudaError_t launch_tiles(TileLaunch& a, const DeviceInfo& dev, cudaStream_t stre
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, C::ROWS / 8);
+  const long long rows = std::min<long long>(C::ROWS, static_cast<long long>(a.g) * a.Nq);  // of a block
+  cfg.gridDim = dim3(grid, static_cast<unsigned>((rows + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
