@@ -636,9 +636,9 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
 // fa_fwd_kv8_tile.cu. This kernel reads the cache once per chunk of rows; the
 // tiles' time hardly depends on the rows below 128. B = 8, Hkv = 8, 16384 keys
 // (and B = 1, Hkv = 8, 4096 keys), rows: this kernel / tiles, us:
-//   d =  64: 16: 64 / 74 (15 / 20)    24: 94 / 74 (16 / 21)
-//   d = 128: 8: 59 / 95 (17 / 23)     16: 102 / 94 (21 / 23)   24: 143 / 97 (23 / 23)
-//   d = 256: 8: 182 / 182 (22 / 29)   12: 262 / 184 (23 / 30)  16: 343 / 184 (23 / 30)
+//   d =  64: 16: 64 / 76 (15 / 19)    24: 94 / 76 (16 / 20)
+//   d = 128: 8: 59 / 92 (17 / 21)     16: 101 / 91 (21 / 20)   24: 142 / 92 (23 / 21)
+//   d = 256: 8: 182 / 173 (22 / 26)   12: 263 / 173 (23 / 26)  16: 345 / 173 (23 / 27)
 constexpr int tile_rows(int d) { return d == 256 ? 8 : 16; }
 
 // 8-column tiles of a row chunk: two (8 rows) where the rows fill more than one

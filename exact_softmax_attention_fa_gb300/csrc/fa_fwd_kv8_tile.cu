@@ -29,7 +29,7 @@
 // Softmax steps are 64 keys, with two buffers of S per slot: S(f + 1) is formed
 // beside the softmax of step f, so a slot waits for neither product. (128-key steps
 // with one buffer: the chain S, softmax, PV of a slot bound, 232 us for 1024 queries
-// on 16384 keys, B = 2, 16 heads on 4, d = 128; now 204. One thread issuing for
+// on 16384 keys, B = 2, 16 heads on 4, d = 128; now 203. One thread issuing for
 // both slots: 369, it spends more time between MMAs than the steps leave it.)
 //
 // Bound: shared memory, at that size at 0.62 of the tensor rate (1180 TFLOP/s). Two
@@ -37,8 +37,8 @@
 // (measured; 2049 with 128-column S, for which tensor memory has no second buffer),
 // and reads operands for 58% of the time (a 64-column S: 6 KB per 48 cycles);
 // loads, stores and tensor-memory reads take the same memory for 32%. A CTA's
-// fixed work (the search for its run, Q pieces, the epilogue) takes 10 us, most of
-// a small call (24 us for 32 rows of 8 heads against 4096 keys).
+// fixed work (the search for its run, Q pieces, the epilogue) takes 8 us, most of
+// a small call (21 us for 32 rows of 8 heads against 4096 keys).
 //
 // Work: every CTA takes an equal run of the flattened list of (sequence, K/V
 // head, row block, key tile); a row block that CTAs share is joined by
