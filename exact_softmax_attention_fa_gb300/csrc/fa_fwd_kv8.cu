@@ -615,11 +615,19 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
     l = l * wa + lx * wx;
     a.x = a.x * wa + x.x * wx, a.y = a.y * wa + x.y * wx, a.z = a.z * wa + x.z * wx, a.w = a.w * wa + x.w * wx;
   };
-#pragma unroll 4
-  for (int w = w0 + group; w <= w1; w += GROUPS) {
-    const size_t slot = (static_cast<size_t>(w) * 2 + (w == w0 ? late : 0)) * p.part_rows + r;
-    const float2 ml = p.part_ml[slot];
-    join(ml.x, ml.y, *reinterpret_cast<const float4*>(p.part + slot * D + lane * 4));
+  for (int w = w0 + group; w <= w1; w += 4 * GROUPS) {  // four on their way at a time
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int v = min(w + e * GROUPS, w1);
+      const size_t slot = (static_cast<size_t>(v) * 2 + (v == w0 ? late : 0)) * p.part_rows + r;
+      ml[e] = p.part_ml[slot];
+      x[e] = *reinterpret_cast<const float4*>(p.part + slot * D + lane * 4);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (w + e * GROUPS <= w1) join(ml[e].x, ml[e].y, x[e]);
   }
   red[threadIdx.x] = a;
   if (lane == 0) red_ml[group] = make_float2(m, l);
