@@ -30,9 +30,9 @@
 // (stages - 1) * 64 d bytes per warp are in flight. Runs are of equal length
 // whatever the sequences' lengths are; a row whose keys are shared between
 // warps is joined by kv8_combine_kernel. Measured: B = 8, 32 heads on 8, 32768 keys,
-// d = 128, pages of 64: 90 us, 6.0 TB/s; B = 16, 32 heads, ragged up to 8192 keys,
+// d = 128, pages of 64: 89 us, 6.1 TB/s; B = 16, 32 heads, ragged up to 8192 keys,
 // d = 64, pages of 32: 54 us, 5.2 TB/s (a step of d = 64 has half the bytes
-// for the same instructions); one sequence of 1000 keys: 9.7 us, two launches and
+// for the same instructions); one sequence of 1000 keys: 9.2 us, two launches and
 // the walk length, page number, codes.
 //
 // Products are m16n8k32 with the cache as the 16-row operand and the rows'

@@ -17,7 +17,11 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kGatherThreads = 64;  // 256: 70.1 instead of 68.4 us for the long cache below
+// Threads of an append block: each holds eight rows' 16 bytes of a page where the
+// limits allow (more threads leave the block's fixed latencies to fewer bytes: with
+// 256, 8192 tokens as below took 34 us in pages of 64 and 57 in pages of 16).
+constexpr int append_threads(int d, int page) { return page * d / 64 < 32 ? 32 : page * d / 64 > 512 ? 512 : page * d / 64; }
 constexpr int kMinExp = -100, kMaxExp = 120;
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
@@ -34,18 +38,19 @@ __device__ __forceinline__ int scale_exp(float amax) {
 // or value (z = 1) cache. Every thread holds 8 columns of PASSES rows: the
 // rows are read once, their maximum is reduced over the block, and the codes
 // are formed from the registers. Bound: HBM, 3 bytes a value; 8192 tokens of 4
-// sequences with 8 heads of 128 (ragged, pages of 64) take 34.5 us, 4.8 TB/s: a
+// sequences with 8 heads of 128 (ragged, pages of 64) take 30.7 us, 5.4 TB/s: a
 // block's bytes are all on their way at once, but its reduction and its stores
-// stand behind one another and only the other blocks of its SM fill the gap. One
-// token for each of 64 sequences: 5.3 us, three dependent latencies (length, page
-// number, codes and scale).
+// stand behind one another, and the other blocks of its SM fill the gap. One token
+// for each of 64 sequences: 5 us, three dependent latencies (length, page number,
+// codes and scale).
 template <int D, int PAGE>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_constant__ Kv8Cache c,
+__global__ void __launch_bounds__(append_threads(D, PAGE)) kv8_append_kernel(const __grid_constant__ Kv8Cache c,
                                                               const __nv_bfloat16* __restrict__ k,
                                                               const __nv_bfloat16* __restrict__ v, int n, int touched,
                                                               uint32_t* status) {
-  constexpr int LPR = D / 8;             // threads per row
-  constexpr int ROWS = kThreads / LPR;   // rows per pass
+  constexpr int THREADS = append_threads(D, PAGE);
+  constexpr int LPR = D / 8;            // threads per row
+  constexpr int ROWS = THREADS / LPR;   // rows per pass
   constexpr int PASSES = (PAGE + ROWS - 1) / ROWS;
   const int b = blockIdx.x / touched, t = blockIdx.x - b * touched, h = blockIdx.y, kv = blockIdx.z;
   const int len = __ldg(c.lens + b), count = c.counts ? __ldg(c.counts + b) : n;
@@ -88,12 +93,12 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_const
       amax = max(amax, hi < 0x7f80u ? hi : 0u);
     }
   }
-  __shared__ uint32_t red[kThreads / 32];
+  __shared__ uint32_t red[THREADS / 32];
   amax = __reduce_max_sync(0xffffffffu, amax);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = amax;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) amax = max(amax, red[i]);
+  for (int i = 0; i < THREADS / 32; ++i) amax = max(amax, red[i]);
   const int e_new = amax ? scale_exp(__uint_as_float(amax << 16)) : kMinExp;
   const float s = held > 0 ? fmaxf(s_old, exp2i(e_new)) : exp2i(e_new);
   uint8_t* dst = c.code[kv] + slot * PAGE * D + col;
@@ -133,15 +138,15 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_const
 // Reads rows [0, min(lens[b], n)) back as bf16 [B][Hkv][n][d]. A thread holds
 // 16 columns (16 bytes in, 32 out) of kRows rows, whose loads are issued
 // together; a page may end between any two of them. Bound: HBM, 3 bytes a value:
-// 4 sequences of 16384 tokens, 8 heads of 128: 70 us, 5.7 TB/s.
+// 4 sequences of 16384 tokens, 8 heads of 128: 68 us, 5.9 TB/s.
 constexpr int kRows = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv8_gather_kernel(const __grid_constant__ Kv8Cache c,
+__global__ void __launch_bounds__(kGatherThreads) kv8_gather_kernel(const __grid_constant__ Kv8Cache c,
                                                               __nv_bfloat16* __restrict__ k,
                                                               __nv_bfloat16* __restrict__ v, int n, int tiles,
                                                               uint32_t* status) {
-  constexpr int LPR = D / 16, ROWS = kThreads / LPR;
+  constexpr int LPR = D / 16, ROWS = kGatherThreads / LPR;
   const int b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles, h = blockIdx.y, kv = blockIdx.z;
   int len = __ldg(c.lens + b);
   const long long most = static_cast<long long>(c.max_pages) << c.page_log2;
@@ -196,22 +201,22 @@ cudaError_t launch_append(const Kv8Cache& c, const void* k, const void* v, int n
   const auto* kk = static_cast<const __nv_bfloat16*>(k);
   const auto* vv = static_cast<const __nv_bfloat16*>(v);
   switch (page) {
-    case 16: kv8_append_kernel<D, 16><<<grid, kThreads, 0, stream>>>(c, kk, vv, n, touched, status); break;
-    case 32: kv8_append_kernel<D, 32><<<grid, kThreads, 0, stream>>>(c, kk, vv, n, touched, status); break;
-    case 64: kv8_append_kernel<D, 64><<<grid, kThreads, 0, stream>>>(c, kk, vv, n, touched, status); break;
-    default: kv8_append_kernel<D, 128><<<grid, kThreads, 0, stream>>>(c, kk, vv, n, touched, status); break;
+    case 16: kv8_append_kernel<D, 16><<<grid, append_threads(D, 16), 0, stream>>>(c, kk, vv, n, touched, status); break;
+    case 32: kv8_append_kernel<D, 32><<<grid, append_threads(D, 32), 0, stream>>>(c, kk, vv, n, touched, status); break;
+    case 64: kv8_append_kernel<D, 64><<<grid, append_threads(D, 64), 0, stream>>>(c, kk, vv, n, touched, status); break;
+    default: kv8_append_kernel<D, 128><<<grid, append_threads(D, 128), 0, stream>>>(c, kk, vv, n, touched, status); break;
   }
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_gather(const Kv8Cache& c, void* k, void* v, int n, uint32_t* status, cudaStream_t stream) {
-  constexpr int ROWS = kThreads / (D / 16) * kRows;
+  constexpr int ROWS = kGatherThreads / (D / 16) * kRows;
   const long long held = static_cast<long long>(c.max_pages) << c.page_log2;
   const int rows = held < n ? static_cast<int>(held) : n;
   const int tiles = (rows + ROWS - 1) / ROWS;
   const dim3 grid(static_cast<unsigned>(c.B) * tiles, c.Hkv, 2);
-  kv8_gather_kernel<D><<<grid, kThreads, 0, stream>>>(c, static_cast<__nv_bfloat16*>(k),
+  kv8_gather_kernel<D><<<grid, kGatherThreads, 0, stream>>>(c, static_cast<__nv_bfloat16*>(k),
                                                       static_cast<__nv_bfloat16*>(v), n, tiles, status);
   return cudaGetLastError();
 }
