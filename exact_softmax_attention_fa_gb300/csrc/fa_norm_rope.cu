@@ -13,8 +13,8 @@
 // lane group takes several heads of one token: their loads are issued together
 // (bytes in flight), and the token's angles are read once for all of them.
 //
-// At B = 2, N = 8192, 16 heads for q, k and v, d = 128: forward 67 us, 6.1 TB/s or
-// 0.89 of the copy rate; backward 113 us, 4.8 TB/s. The backward holds dy, x and the
+// At B = 2, N = 8192, 16 heads for q, k and v, d = 128: forward 65 us, 6.3 TB/s or
+// 0.92 of the copy rate; backward 113 us, 4.8 TB/s. The backward holds dy, x and the
 // dw of its columns in registers, which leaves 16 warps an SM; it waits for
 // loads (more rows on their way, more or fewer warps, and a unit's first rows
 // fetched behind the unit before all measured within 2%).
@@ -31,7 +31,7 @@
 namespace fa {
 namespace {
 
-constexpr int kFwdThreads = 128;     // 256: 69.3 instead of 66.7 us (B = 2, N = 8192, 16 heads, d = 128)
+constexpr int kFwdThreads = 64;      // 256: 69.3, 128: 67.3 instead of 65.0 us (B = 2, N = 8192, 16 heads, d = 128)
 constexpr int kThreads = 256;        // backward
 constexpr int kHeads = 4;            // heads of one token per lane group, forward
 constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward: kBwdSide at a time
@@ -175,7 +175,7 @@ __device__ __forceinline__ int position(const NormRope& p, int token, int n) {
 }
 
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kFwdThreads, 8) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
+__global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
   Lane<D, INTER> L;
   L.init(p);
   const int upt = p.chunks[0] + p.chunks[1] + p.chunks[2];
