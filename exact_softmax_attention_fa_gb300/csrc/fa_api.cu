@@ -287,7 +287,8 @@ fa_status_t device_info(DeviceInfo* out) {
   fa_status_t st = FA_OK;
   const DeviceState* ds = device_state(&st);
   if (!ds) return st;
-  *out = DeviceInfo{static_cast<int>(ds - g_dev), ds->num_sms, ds->status, g_wait_limit_ns.load()};
+  *out = DeviceInfo{static_cast<int>(ds - g_dev), ds->num_sms, ds->status, g_wait_limit_ns.load(),
+                    g_debug_skip.load()};
   return FA_OK;
 }
 
@@ -687,6 +688,10 @@ fa_status_t fa_debug_skip_arrival(unsigned int role) {
     case WHERE_BWD_MMA:
     case WHERE_BWD_SOFTMAX:
     case WHERE_BWD_DQ:
+    case WHERE_KV8_LOAD:
+    case WHERE_KV8_CONVERT:
+    case WHERE_KV8_MMA:
+    case WHERE_KV8_SOFTMAX:
       g_debug_skip.store(role);
       return FA_OK;
     default:

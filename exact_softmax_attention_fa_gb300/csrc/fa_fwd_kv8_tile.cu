@@ -84,6 +84,7 @@ struct TileLaunch : Kv8Call {
   int4* run;               // [CTAs][2]: where each CTA's run starts (b, h, block, tile); the block's holders
   uint32_t* status;
   uint64_t wait_limit_ns;
+  uint32_t debug_skip;     // test hook, see fa_kernel_common.cuh
 };
 
 // How `total` tiles are dealt: runs of per + 1 tiles to the first `more` CTAs, of
@@ -430,6 +431,7 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
     const bool live = lane < pages && slot >= 0;
     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * page * D;
     uint8_t* kd = sK + ks * C::K_BYTES;
+    const bool skip = debug_skip_here(p.debug_skip, WHERE_KV8_LOAD, i == 0);  // test hook
     // S of a bad page's keys has to be a number
     for (unsigned bad = __ballot_sync(0xffffffffu, lane < pages && slot == -1); bad; bad &= bad - 1) {
       const int first = (__ffs(bad) - 1) * page * ROW_BYTES;
@@ -439,9 +441,9 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
       fence_proxy_async_smem();
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[ks], bytes);
+    if (lane == 0 && !skip) mbar_arrive_expect_tx(&sh.k_full[ks], bytes);
     __syncwarp();
-    if (live) {
+    if (live && !skip) {
 #pragma unroll
       for (int c = 0; c < D / ROW_BYTES; ++c)
         tma_load_3d(kd + c * (128 * 128) + lane * page * ROW_BYTES, &p.tmK, &sh.k_full[ks], c * 128, 0, slot);
@@ -461,7 +463,8 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   __syncwarp();
   // the copies already issued land before the CTA can exit
   if (lane == 0) {
-    for (int i = max(0, k_issued - C::KST); i < k_issued; ++i) drain_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, lim);
+    const int first = debug_skip_here(p.debug_skip, WHERE_KV8_LOAD, true) ? 1 : 0;
+    for (int i = max(first, k_issued - C::KST); i < k_issued; ++i) drain_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, lim);
     for (int i = max(0, st_issued - C::SST); i < st_issued; ++i)
       drain_wait(&sh.st_full[i % C::SST], (i / C::SST) & 1, lim);
   }
@@ -997,8 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
       mbar_init(&sh.q_full[t], 4);
       mbar_init(&sh.q_taken[t], 1);
       for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.s_full[t][b], 1);
-        mbar_init(&sh.p_full[t][b], 4);
+        const bool first = t == 0 && b == 0;
+        mbar_init(&sh.s_full[t][b], 1 + (first ? debug_extra(p.debug_skip, WHERE_KV8_MMA) : 0u));
+        mbar_init(&sh.p_full[t][b], 4 + (first ? debug_extra(p.debug_skip, WHERE_KV8_SOFTMAX) : 0u));
         mbar_init(&sh.pv_done[t][b], 1);
       }
       mbar_init(&sh.o_free[t], 4);
@@ -1008,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
       mbar_init(&sh.k_empty[i], HALVES ? 1 : C::NT);
       mbar_init(&sh.st_full[i], 1);
       mbar_init(&sh.st_empty[i], kConvThreads / 32);
-      mbar_init(&sh.v_full[i], kConvThreads / 32);
+      mbar_init(&sh.v_full[i], kConvThreads / 32 + (i == 0 ? debug_extra(p.debug_skip, WHERE_KV8_CONVERT) : 0u));
       mbar_init(&sh.v_empty[i], HALVES ? 1 : C::NT);
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&sh.scale_full[i], 8);
@@ -1187,6 +1191,7 @@ fa_status_t launch_kv8_tiles(const Kv8Call& call, int d, void* workspace, const 
     return FA_ERR_CUDA;
   a.status = dev.status;
   a.wait_limit_ns = dev.wait_limit_ns;
+  a.debug_skip = dev.debug_skip;
   size_t ml = 0, run = 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (d == 64) tile_part_bytes<64>(&ml, &run);

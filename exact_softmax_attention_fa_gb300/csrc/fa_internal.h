@@ -95,6 +95,7 @@ struct DeviceInfo {
   int device, num_sms;
   uint32_t* status;  // device address of the status word
   uint64_t wait_limit_ns;
+  uint32_t debug_skip;  // test hook: role (WHERE_*) whose first arrival block 0 leaves out; 0 = none
 };
 fa_status_t device_info(DeviceInfo* out);
 fa_status_t from_cuda(cudaError_t e);

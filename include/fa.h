@@ -516,9 +516,10 @@ fa_status_t fa_debug_timeout_probe(unsigned long long limit_ns, cudaStream_t str
 /*
  * Failure-detection test hook for the real kernels. Off (0) by default. With
  * a role code of fa_get_device_status_detail (1-3 forward load / MMA /
- * softmax; 11-14 backward load / MMA / softmax / dQ drain), block 0 of every
+ * softmax; 11-14 backward load / MMA / softmax / dQ drain; 41-44 load /
+ * conversion / MMA / softmax of fa_fwd_kv8's many-row kernel), block 0 of every
  * later launch of a kernel that has that role misses one of that role's
- * hand-offs: a load role leaves out one of its TMA copies; for an MMA,
+ * hand-offs: a load role leaves out one of its copies; for an MMA, conversion,
  * softmax or dQ-drain role, one barrier it signals is set up to expect one
  * arrival more than the role makes. Either way the bounded wait on that
  * barrier gives up after the wait limit: the launch records

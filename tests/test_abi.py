@@ -405,3 +405,11 @@ def test_a_refused_append_leaves_the_cache_lengths():
         with pytest.raises(Exception):  # not on a CUDA device, and of the wrong type or shape
             cache.append(bad, bad, counts)
         assert cache.lens.tolist() == [0, 0]
+
+
+def test_the_cache_attention_has_roles_of_its_own_for_the_skip_hook(lib):
+    for bad in (21, 31, 33, 40, 45):
+        assert lib.fa_debug_skip_arrival(bad) == INVALID
+    for good in (41, 42, 43, 44):
+        assert lib.fa_debug_skip_arrival(good) == OK
+    assert lib.fa_debug_skip_arrival(0) == OK

@@ -467,3 +467,25 @@ def test_the_chain_on_a_stream_of_its_own_while_others_allocate():
     for got in runs:
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert fa.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("Hq,Nq,d", [(4, 20, 128), (4, 80, 128), (2, 40, 64), (2, 40, 256)])
+@pytest.mark.parametrize("role", [41, 42, 43, 44])
+def test_a_wait_that_nothing_ends_gives_up_and_the_next_call_is_right(role, Hq, Nq, d):
+    import exact_softmax_attention_fa_gb300 as fa
+    lens = [1500, 300]
+    p = filled(2, 1, d, 32, lens, BASE_SEED + role)
+    qb, q = bf16(p.rng, 2, Hq, Nq, d)
+    assert fa.fa_get_device_status_detail() == (0, 0, 0, 0)
+    try:
+        fa.fa_set_wait_limit_ns(2_000_000)
+        fa.fa_debug_skip_arrival(role)
+        call(p, qb, lens, None, True, scale_f32(d))
+        code, where, block, _thread = fa.fa_get_device_status_detail()
+    finally:
+        fa.fa_debug_skip_arrival(0)
+        fa.fa_set_wait_limit_ns(0)
+    assert code == 6 and where in (41, 42, 43, 44) and block == 0
+    o, lse = call(p, qb, lens, None, True, scale_f32(d))
+    assert fa.fa_get_device_status_detail() == (0, 0, 0, 0)
+    compare(p, q, lens, None, True, scale_f32(d), o, lse)
