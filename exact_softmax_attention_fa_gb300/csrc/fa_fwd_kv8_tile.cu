@@ -532,7 +532,7 @@ __device__ void convert_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sS
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one thread)
+// MMA issuer (one thread per slot)
 // ---------------------------------------------------------------------------
 // S of one tile: step QS multiplies 32 columns of a piece (the first D / 32
 // steps: qh). A row of Q holds 128 bytes per chunk of 128 rows: both pieces
@@ -681,7 +681,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
     const bool live = qi < w.count;
     const size_t at = (static_cast<size_t>(w.b) * p.Hq + w.h * p.g + row % p.g) * p.Nq + qi;
     const int limit = p.causal ? min(w.len, w.len - w.count + qi + 1) : w.len;  // keys the row sees
-    // The MMA thread has taken note of the segment before (else an idle tile's
+    // The MMA thread has taken note of the segment before (else an idle slot's
     // warpgroup could run two arrivals ahead of its parity wait).
     if (alive && seg > 0) {
       alive = warp_wait(&sh.q_taken[t], (seg - 1) & 1, &sh.abort_flag, lim);
