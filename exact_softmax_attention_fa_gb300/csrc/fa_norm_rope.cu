@@ -14,7 +14,7 @@
 // (bytes in flight), and the token's angles are read once for all of them.
 //
 // At B = 2, N = 8192, 16 heads for q, k and v, d = 128: forward 65 us, 6.3 TB/s or
-// 0.92 of the copy rate; backward 113 us, 4.8 TB/s. The backward holds dy, x and the
+// 0.92 of the copy rate; backward 111 us, 4.9 TB/s. The backward holds dy, x and the
 // dw of its columns in registers, which leaves 16 warps an SM; it waits for
 // loads (more rows on their way, more or fewer warps, and a unit's first rows
 // fetched behind the unit before all measured within 2%).
@@ -439,12 +439,13 @@ fa_status_t take_strides(const long long* s, int t, int B, int H, int N, long lo
 }
 
 // Blocks for q, k and v: all that fit the device at once, by the bytes each
-// moves (q and k three rows a head with weights, else two), no more than
+// moves (q and k three rows a head with weights, else two; v's two then count 2.2,
+// its blocks else end 7 us behind the others of a 113 us call), no more than
 // there are lane groups to fill. A kind without rows has none.
 void share_blocks(NormRope* a, int d, int num_sms) {
   const int groups = kThreads / (d / 8), all = std::min(kBwdPerSm * num_sms, kMaxBwdBlocks);
   double work[3], sum = 0.0;
-  for (int t = 0; t < 3; ++t) sum += work[t] = static_cast<double>(a->H[t]) * (a->w[0] && t < 2 ? 3 : 2);
+  for (int t = 0; t < 3; ++t) sum += work[t] = a->H[t] * (!a->w[0] ? 2.0 : t < 2 ? 3.0 : 2.2);
   for (int t = 0; t < 3; ++t) {
     const long long most = (static_cast<long long>(a->tokens) * a->chunks[t] + groups - 1) / groups;
     a->blocks[t] = static_cast<int>(std::min<long long>(most, std::max(1, static_cast<int>(all * work[t] / sum))));
