@@ -787,23 +787,22 @@ class KV8Cache:
 
     def attend(self, q, causal: bool = True, scale: float | None = None, counts=None, stream=None):
         """O, L of q [B, Hq, Nq, d], whose last rows are the cache's newest tokens (fa_fwd_kv8); rows
-        past counts[b] are zero. One workspace per shape and stream is kept; a
-        captured call has one of its own, in its graph's memory."""
+        past counts[b] are zero. One workspace per stream is kept, as large as the
+        calls so far needed; a captured call has one of its own, in its graph's memory."""
         import torch
         B, Hq, Nq, d = _dims(q)
         handle = _stream_handle(stream)
-        key = (Hq, Nq, handle)
+        size = max(1, fa_fwd_kv8_workspace_size(B, Hq, int(self.k_cache.shape[1]), Nq, d))
         with _on_stream(stream):
             make = torch.empty if counts is None else torch.zeros
             o = make(q.shape, dtype=q.dtype, device=q.device)
             lse = make((B, Hq, Nq), dtype=torch.float32, device=q.device)
-            workspace = self._workspaces.get(key)
+            workspace = self._workspaces.get(handle)
             capturing = torch.cuda.is_current_stream_capturing()
-            if workspace is None or capturing:
-                size = fa_fwd_kv8_workspace_size(B, Hq, int(self.k_cache.shape[1]), Nq, d)
-                workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
+            if workspace is None or workspace.numel() < size or capturing:
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
                 if not capturing:
-                    self._workspaces[key] = workspace
+                    self._workspaces[handle] = workspace
         fa_fwd_kv8(q, *self._cache(), o, lse, causal, default_scale(d) if scale is None else scale, counts, workspace,
                    handle)
         return o, lse

@@ -489,3 +489,22 @@ def test_a_wait_that_nothing_ends_gives_up_and_the_next_call_is_right(role, Hq, 
     o, lse = call(p, qb, lens, None, True, scale_f32(d))
     assert fa.fa_get_device_status_detail() == (0, 0, 0, 0)
     compare(p, q, lens, None, True, scale_f32(d), o, lse)
+
+
+def test_a_cache_keeps_one_workspace_per_stream():
+    import torch
+    import exact_softmax_attention_fa_gb300 as fa
+    gen = torch.Generator(device="cuda").manual_seed(BASE_SEED + 3)
+    cache = fa.KV8Cache(2, 2, 64, 700)
+    k = torch.randn(2, 2, 700, 64, generator=gen, device="cuda").bfloat16()
+    cache.append(k, k)
+    got = {}
+    for Nq in (1, 40, 3, 300, 40, 1):
+        q = torch.randn(2, 4, Nq, 64, generator=torch.Generator(device="cuda").manual_seed(Nq), device="cuda").bfloat16()
+        o, lse = cache.attend(q)
+        if Nq in got:
+            assert torch.equal(o, got[Nq][0]) and torch.equal(lse, got[Nq][1])
+        got[Nq] = o, lse
+    assert len(cache._workspaces) == 1
+    assert cache._workspaces.popitem()[1].numel() == max(fa.fa_fwd_kv8_workspace_size(2, 4, 2, n, 64) for n in got)
+    assert fa.fa_get_device_status() == 0
