@@ -31,7 +31,7 @@
 // whatever the sequences' lengths are; a row whose keys are shared between
 // warps is joined by kv8_combine_kernel. Measured: B = 8, 32 heads on 8, 32768 keys,
 // d = 128, pages of 64: 89 us, 6.1 TB/s; B = 16, 32 heads, ragged up to 8192 keys,
-// d = 64, pages of 32: 54 us, 5.2 TB/s (a step of d = 64 has half the bytes
+// d = 64, pages of 32: 55 us, 5.1 TB/s (a step of d = 64 has half the bytes
 // for the same instructions); one sequence of 1000 keys: 9.2 us, two launches and
 // the walk length, page number, codes.
 //
@@ -80,21 +80,29 @@ struct Cfg {
 __device__ __forceinline__ int steps_of(int len) { return (len + kStepKeys - 1) / kStepKeys; }
 __device__ __forceinline__ int seq_steps(const Kv8Cache& c, int b) { return steps_of(seq_len(c, b)); }
 
-// Every lane: the steps of all sequences summed, and of those before `b`.
-__device__ __forceinline__ void step_totals(const Kv8Cache& c, int pairs, int b, long long* total, long long* before) {
+// Every lane: the steps of all sequences summed, and of those before `b`; how
+// many sequences have any.
+__device__ __forceinline__ void step_totals(const Kv8Cache& c, int pairs, int b, long long* total, long long* before,
+                                            int* live) {
   long long t = 0, u = 0;
+  int n = 0;
   for (int i = threadIdx.x & 31; i < c.B; i += 32) {
-    const long long s = static_cast<long long>(seq_steps(c, i)) * pairs;
+    const int one = seq_steps(c, i);
+    const long long s = static_cast<long long>(one) * pairs;
     t += s;
     if (i < b) u += s;
+    n += one > 0;
   }
   *total = warp_sum(t);
   *before = warp_sum(u);
+  *live = __reduce_add_sync(0xffffffffu, n);
 }
 
-// Warps that share `total` steps, and the first step of warp w of them.
-__device__ __forceinline__ int used_warps(long long total, int warps) {
-  const long long most = (total + kMinSteps - 1) / kMinSteps;
+// Warps that share `total` steps of `pieces` row chunks (a chunk's start and end
+// cost several steps: the shortest get a warp each, 13 sequences of two keys at
+// d = 256 11.5 instead of 18.5 us), and the first step of warp w.
+__device__ __forceinline__ int used_warps(long long total, long long pieces, int warps) {
+  const long long most = max((total + kMinSteps - 1) / kMinSteps, min(total, pieces));
   return most < warps ? static_cast<int>(most) : warps;
 }
 __device__ __forceinline__ long long first_step(long long total, int used, int w) { return total * w / used; }
@@ -210,8 +218,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::WARPS * 32, 1) kv8_attn_kernel(con
   const int warps = gridDim.x * C::WARPS;
   const int gid = warp * gridDim.x + blockIdx.x;  // few runs spread over the SMs
   long long total, before;
-  step_totals(p.c, pairs, 0, &total, &before);
-  const int used = used_warps(total, warps);
+  int live;
+  step_totals(p.c, pairs, 0, &total, &before, &live);
+  const int used = used_warps(total, static_cast<long long>(live) * pairs, warps);
   if (gid >= used) return;
   const long long x0 = first_step(total, used, gid);
   const int n_steps = static_cast<int>(first_step(total, used, gid + 1) - x0);
@@ -594,8 +603,9 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const bool live = !bad_len && !bad_count && qi < seq_count(p.c, b, p.Nq);
   long long total, before;
-  step_totals(p.c, pairs, b, &total, &before);
-  const int used = max(1, used_warps(total, warps));
+  int some;
+  step_totals(p.c, pairs, b, &total, &before, &some);
+  const int used = max(1, used_warps(total, static_cast<long long>(some) * pairs, warps));
   const int chunk = row / per_chunk, r = row - chunk * per_chunk;
   const long long s0 = before + static_cast<long long>(h * p.chunks + chunk) * steps, s1 = s0 + steps - 1;
   griddep_wait();
