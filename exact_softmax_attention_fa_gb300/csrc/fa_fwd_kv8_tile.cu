@@ -67,6 +67,12 @@ struct TileCfg {
   static constexpr int K_BYTES = 128 * D;         // codes of a key tile
   static constexpr int V_BYTES = 2 * 128 * D;     // fp16 values
   static constexpr int KST = D == 64 ? 4 : (D == 128 ? 3 : 2);
+  // Barriers of the copies of K: tile i's is number i % K_BARS. Where the slots take every other
+  // tile each, a slot waits for the copies of its own tiles only, and copies land in any order, so
+  // the tile before it on a barrier has to be one it has waited for: an even number of tiles before.
+  // (With one barrier a stage at d = 128, tile 4's wait could pass on the phase before tile 1's.)
+  static constexpr int K_BARS = D == 64 ? 4 : (D == 128 ? 6 : 2);
+  static_assert(K_BARS % KST == 0 && K_BARS % 2 == 0, "a slot's waits would meet the other slot's copies");
   static constexpr int VST = D == 64 ? 3 : (D == 128 ? 2 : 1);
   static constexpr int SLOTS = KST + 2;  // tiles whose scales are kept: a tile's are read before the key ring comes round
   static constexpr int SST = D == 64 ? 4 : (D == 128 ? 2 : 1);  // staged value codes
@@ -114,7 +120,7 @@ template <int D>
 struct TileShared {
   static constexpr int SLOTS = TileCfg<D>::SLOTS;
   uint64_t q_full[2], q_taken[2];
-  uint64_t k_full[4], k_empty[4], st_full[4], st_empty[4], v_full[4], v_empty[4];
+  uint64_t k_full[TileCfg<D>::K_BARS], k_empty[4], st_full[4], st_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];  // [slot][buffer of S]
   uint64_t scale_full[SLOTS];
   uint64_t mma_drain[2];
@@ -418,6 +424,7 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
       next = look_up();
     }
     const int ks = i % C::KST;
+    uint64_t* k_full = &sh.k_full[i % C::K_BARS];
     if (i >= C::KST) ok = warp_wait(&sh.k_empty[ks], ((i / C::KST) - 1) & 1, &sh.abort_flag, lim);
     if (!ok) break;
     const int slot8 = i % C::SLOTS;
@@ -441,12 +448,12 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
       fence_proxy_async_smem();
     }
     __syncwarp();
-    if (lane == 0 && !skip) mbar_arrive_expect_tx(&sh.k_full[ks], bytes);
+    if (lane == 0 && !skip) mbar_arrive_expect_tx(k_full, bytes);
     __syncwarp();
     if (live && !skip) {
 #pragma unroll
       for (int c = 0; c < D / ROW_BYTES; ++c)
-        tma_load_3d(kd + c * (128 * 128) + lane * page * ROW_BYTES, &p.tmK, &sh.k_full[ks], c * 128, 0, slot);
+        tma_load_3d(kd + c * (128 * 128) + lane * page * ROW_BYTES, &p.tmK, k_full, c * 128, 0, slot);
     }
     ++k_issued;
     const int ss = i % C::SST;
@@ -464,7 +471,7 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   // the copies already issued land before the CTA can exit
   if (lane == 0) {
     const int first = debug_skip_here(p.debug_skip, WHERE_KV8_LOAD, true) ? 1 : 0;
-    for (int i = max(first, k_issued - C::KST); i < k_issued; ++i) drain_wait(&sh.k_full[i % C::KST], (i / C::KST) & 1, lim);
+    for (int i = max(first, k_issued - C::KST); i < k_issued; ++i) drain_wait(&sh.k_full[i % C::K_BARS], (i / C::K_BARS) & 1, lim);
     for (int i = max(0, st_issued - C::SST); i < st_issued; ++i)
       drain_wait(&sh.st_full[i % C::SST], (i / C::SST) & 1, lim);
   }
@@ -568,15 +575,16 @@ __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, ui
   const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32), v_hi = static_cast<uint32_t>(v_desc >> 32);
   constexpr uint32_t kKeyHalf = (64 * (D < 128 ? D : 128)) >> 4, kValueHalf = (64 * 128) >> 4;  // of a column chunk
   Ring<C::KST> k;       // the stages of the tiles whose S and PV come next
+  Ring<C::K_BARS> kb;   // the barrier of k's copy
   Ring<C::VST> v;
   uint32_t par = 0;     // parity of the buffers' use by PV, which S is one or none ahead of
   bool used = false;    // the buffers have been used
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &sh.abort_flag, lim); };
   auto skip_k = [&]() {
-    if (HALVES) return k.next(), true;
-    const bool ok = wait(&sh.k_full[k.stage], k.phase);
-    if (ok) mbar_arrive(&sh.k_empty[k.stage]);
+    const bool ok = HALVES || wait(&sh.k_full[kb.stage], kb.phase);
+    if (!HALVES && ok) mbar_arrive(&sh.k_empty[k.stage]);
     k.next();
+    kb.next();
     return ok;
   };
   auto skip_v = [&]() {
@@ -587,7 +595,7 @@ __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, ui
     return ok;
   };
   auto issue_s = [&](int b, bool read, uint32_t parity) -> bool {
-    if (b == 0 && !wait(&sh.k_full[k.stage], k.phase)) return false;
+    if (b == 0 && !wait(&sh.k_full[kb.stage], kb.phase)) return false;
     if (read && !wait(&sh.pv_done[t][b], parity)) return false;  // the P that was there
     tc_fence_after_sync();
     issue_s_steps<D>(std::make_integer_sequence<int, 2 * (D / 32)>{}, tmem + C::s_col(t, b), q_lo, q_hi,
@@ -596,6 +604,7 @@ __device__ void mma_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ, ui
     if (b == 1) {
       umma_commit(&sh.k_empty[k.stage]);
       k.next();
+      kb.next();
     }
     return true;
   };
@@ -1007,8 +1016,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
       }
       mbar_init(&sh.o_free[t], 4);
     }
+    for (int i = 0; i < C::K_BARS; ++i) mbar_init(&sh.k_full[i], 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], HALVES ? 1 : C::NT);
       mbar_init(&sh.st_full[i], 1);
       mbar_init(&sh.st_empty[i], kConvThreads / 32);
