@@ -390,9 +390,11 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   cur.begin(p, sh.start);
   cur.s += lane >> 3;
   cur.settle(p);
+  int next_id = -1, last_id = -1, last_most = kNoScale;  // of the value scales: sequence and head
   auto look_up = [&]() -> int {  // page * Hkv + head; -1: a bad page, -2: behind the sequence
     int slot = -2;
     if (cur.b < p.c.B) {
+      next_id = cur.b * p.c.Hkv + cur.h;
       const int key = cur.s * 128 + (lane & 7) * 16;
       if (key < cur.len) {
         const int pid = __ldg(p.c.table + static_cast<size_t>(cur.b) * p.c.max_pages + (key >> p.c.page_log2));
@@ -412,11 +414,13 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
     if (j0 == 0) {
       now = next;
       entry = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sk = 0.f, sv = 0.f;
+      if (now >= 0) sk = __ldg(p.c.scale[0] + now), sv = __ldg(p.c.scale[1] + now);
+      const int e = now >= 0 ? scale_exponent(sv) : kNoScale;
+      const int most = largest_of_id(e, next_id, &last_id, &last_most);
       if (now >= 0) {
-        const float sk = __ldg(p.c.scale[0] + now), sv = __ldg(p.c.scale[1] + now);
-        const int e = min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
-        entry = make_float4(sk * p.scale_log2, static_cast<float>(e) + log2f(sv * exp2i(-e)),
-                            exp2i(-static_cast<int>(kSumBias)) / sv, 1.f);
+        const ValueScale v(sv, e, most);
+        entry = make_float4(sk * p.scale_log2, v.log2_sv, v.inv, 1.f);
       } else if (now == -1) {
         entry.y = -INFINITY;  // its keys are not seen
         record_bad_index(p.status, WHERE_FWD_KV8);
@@ -815,7 +819,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
       const float m_ref = move ? fmaxf(m, mx - kShift) : m;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m - m_use);  // 0 on the first step, 1 when the reference is kept
-      l *= alpha;
+      if (move) l = scale_sum(l, m - m_use, alpha);
       // P (packed pairs) overwrites columns of S that have been read
       const float4 zg = sh.scale[sl][2][buf];
       uint32_t pk[16];
@@ -878,7 +882,7 @@ __device__ void softmax_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sQ
         const float2 other = sh.half_ml[t ^ 1][r];
         const float both = fmaxf(m, other.x), ref = both == -INFINITY ? 0.f : both;
         own = ex2_approx(m - ref);
-        l = l * own + other.y * ex2_approx(other.x - ref);
+        l = add_sums(l, m - ref, own, other.y, other.x - ref, ex2_approx(other.x - ref));
         m = both;
 #pragma unroll 1
         for (int c = (t ^ 1) * (D / 2); c < ((t ^ 1) + 1) * (D / 2); c += 32) {
@@ -1139,8 +1143,8 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_cons
       if (u0 + e > c1) break;
       const float to = fmaxf(m, ml[e].x), ref = to == -INFINITY ? 0.f : to;
       const float wa = ex2_approx(m - ref), wx = ex2_approx(ml[e].x - ref);
+      l = add_sums(l, m - ref, wa, ml[e].y, ml[e].x - ref, wx);
       m = to;
-      l = l * wa + ml[e].y * wx;
 #pragma unroll
       for (int k = 0; k < PER; ++k) a[k] = a[k] * wa + (k & 1 ? x[e][k / 2].y : x[e][k / 2].x) * wx;
     }

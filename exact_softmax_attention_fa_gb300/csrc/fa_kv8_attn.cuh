@@ -2,6 +2,8 @@
 // (fa_fwd_kv8.cu: few query rows per K/V head, fa_fwd_kv8_tile.cu: many).
 #pragma once
 
+#include <climits>
+
 #include "fa_kv8.cuh"
 
 namespace fa {
@@ -13,6 +15,14 @@ constexpr float kShift = 6.f;     // a reference lies this far (base 2) below it
 // 2^(14 + 100 - 10) for the scales a cache holds, so neither one term nor 2^22
 // of them leave fp32's normal range.
 constexpr float kSumBias = 10.f;
+// A value scale enters the weights P_j = 2^(t_j + log2 sv_j - m) and, as 1 / sv_j, the
+// sum. Its exponent is held to at least kMinScaleExp (a page of zeros has that, and
+// below it the terms of l overflow) and to at most kScaleSpread below the largest one
+// that the run has met in its sequence and head: with scales further apart the weights
+// of the smaller one, and with them their part of l, would leave fp32's range. What is
+// lost is the size of values below 2^-91, and of values below 2^-89 of the
+// sequence's largest.
+constexpr int kMinScaleExp = -100, kScaleSpread = 90;
 
 // One call, as both kernels take it.
 struct Kv8Call {
@@ -55,6 +65,61 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
+// log2 of a value scale and 2^-kSumBias / sv, as a run takes them; most: the largest
+// exponent that it has met.
+struct ValueScale {
+  float log2_sv, inv;
+  __device__ __forceinline__ ValueScale(float sv, int e, int most) {
+    const int least = max(most - kScaleSpread, kMinScaleExp);
+    if (e < least) {
+      log2_sv = static_cast<float>(least);
+      inv = exp2i(-static_cast<int>(kSumBias) - least);
+    } else {
+      log2_sv = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
+      inv = exp2i(-static_cast<int>(kSumBias)) / sv;
+    }
+  }
+};
+// Exponent of a value scale (rounded down; -126 for all smaller ones).
+__device__ __forceinline__ int scale_exponent(float sv) {
+  return min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
+}
+// Lanes hold consecutive groups of a run, each with its exponent (kNoScale: none) and
+// the sequence and head (`id`) it belongs to: the largest exponent of this id among
+// them and, where it is the id of the lanes before, last_id, among those; or kNoScale
+// where no exponent is to be raised, as nearly always. The later groups count too:
+// one softmax step takes several of them with one reference.
+constexpr int kNoScale = -1000;
+__device__ __forceinline__ int largest_of_id(int e, int id, int* last_id, int* last_most) {
+  const int hi = max(__reduce_max_sync(0xffffffffu, e), *last_most);
+  const int lo = __reduce_min_sync(0xffffffffu, e == kNoScale ? INT_MAX : e);
+  const int tail = __shfl_sync(0xffffffffu, id, 31);
+  const int tail_most = __reduce_max_sync(0xffffffffu, id == tail ? e : kNoScale);
+  int most = kNoScale;
+  if (lo < kMinScaleExp || (lo != INT_MAX && hi - lo > kScaleSpread)) {
+    most = __reduce_max_sync(__match_any_sync(0xffffffffu, id), e);
+    if (id == *last_id) most = max(most, *last_most);
+  }
+  *last_most = tail == *last_id ? max(*last_most, tail_most) : tail_most;
+  *last_id = tail;
+  return most;
+}
+
+// l 2^d, d <= 0 (exp2_d: 2^d): in two steps where 2^d alone would leave fp32's range; a
+// sum of small value scales that meets a far larger one is as large as its factor is small.
+__device__ __forceinline__ float scale_sum(float l, float d, float exp2_d) {
+  if (d < -100.f && l > 0.f) {
+    const float half = ex2_approx(0.5f * d);
+    return l * half * half;
+  }
+  return l * exp2_d;
+}
+// a 2^da + b 2^db likewise (wa, wb: 2^da, 2^db).
+__device__ __forceinline__ float add_sums(float a, float da, float wa, float b, float db, float wb) {
+  if (fminf(da, db) < -100.f && a > 0.f && b > 0.f) return scale_sum(a, da, wa) + scale_sum(b, db, wb);
+  return a * wa + b * wb;
+}
+
 // x / (l 2^kSumBias) and ln of the row's sum, for sums near either end of
 // fp32's range; a row that saw no key has l = 0: O = 0, L = -inf.
 struct RowEnd {
@@ -67,7 +132,7 @@ struct RowEnd {
       b = exp2i(-e);
       a = exp2i(-static_cast<int>(kSumBias)) / (l * b);
     } else if (l != 0.f) {
-      a = 1.f / l;
+      a = 1.f / l + (l - l);  // NaN, not 0, for an infinite sum
     }
     lse = l == 0.f ? -INFINITY : (m + kSumBias + log2f(l)) * kLn2;
   }

@@ -455,7 +455,11 @@ fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float*
  *   not written, and what they hold is of no effect. What a page holds behind lens[b] is never
  *   used. A NaN code reaches every query that sees its token; one stored in V
  *   may also reach the queries of this call that stand before it.
- *   scales : positive, at most 2^126 (fa_kv8_append's are powers of two up to 2^120)
+ *   scales : positive, at most 2^126 (fa_kv8_append's are powers of two from 2^-100 to
+ *            2^120). A value scale may be 0; one below 2^-100, or below 2^-90 of another
+ *            of its sequence and head, may count as that: values below 2^-91, and values
+ *            below 2^-89 of the largest one (448 * its page's scale, if that is more),
+ *            are then off by as much as they are. Their weights are not.
  *   scale  : finite and > 0
  *   workspace : fa_fwd_kv8_workspace_size() bytes, 256-byte aligned; the
  *            parts of rows whose keys several SMs share. Calls that may run at
