@@ -19,8 +19,8 @@ from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: 
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_bwd_deterministic", "fa_bwd_gqa_deterministic", "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_bwd_preprocess", "fa_bwd_preprocess_stats", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_bwd_host", "fa_fwd_bwd_host_device_bytes", "fa_fwd_host", "fa_fwd_host_device_bytes", "fa_get_device_status", "fa_get_device_status_detail", "fa_set_wait_limit_ns",
            "fa_debug_timeout_probe", "fa_debug_skip_arrival", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
-           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_gather",
-           "fa_fwd_kv8", "fa_fwd_kv8_workspace_size", "KV8Cache", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
+           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_advance", "fa_kv8_gather",
+           "fa_fwd_kv8", "fa_fwd_kv8_filled", "fa_fwd_kv8_workspace_size", "KV8Cache", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
 
 _SUPPORTED_D = (64, 128, 256)
 
@@ -581,6 +581,22 @@ def fa_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, lens, co
         _stream_handle(stream)))
 
 
+def fa_kv8_advance(lens, counts, taken, n: int, page: int, max_pages: int, stream=None) -> None:
+    """fa_kv8_advance of the C ABI: lens[b] += counts[b] (None: n) where the sequence can take them, with
+    taken[b] the tokens it takes: what fa_kv8_append then needs as its counts. int32 [B] each."""
+    import torch
+    i32, shape = torch.int32, lens.shape
+    if not (lens.dtype == taken.dtype == i32 and len(shape) == 1 and taken.shape == shape and lens.is_contiguous()
+            and taken.is_contiguous()
+            and (counts is None or (counts.dtype == i32 and counts.shape == shape and counts.is_contiguous()))
+            and _devices(lens, counts, taken) == {torch.cuda.current_device()}):
+        if len(shape) != 1:
+            raise ValueError("lens must be an int32 [B] tensor")
+        _refuse([(name, t, (i32,), shape, True) for name, t in (("lens", lens), ("counts", counts), ("taken", taken))])
+    check("fa_kv8_advance", load().fa_kv8_advance(lens.data_ptr(), _ptr(counts), taken.data_ptr(), shape[0], n, page,
+                                                  max_pages, _stream_handle(stream)))
+
+
 def fa_kv8_gather(k_cache, v_cache, k_scale, v_scale, page_table, lens, k, v, stream=None) -> None:
     """fa_kv8_gather of the C ABI: rows [0, min(lens[b], n)) of each sequence back as bf16 into
     k, v [B, Hkv, n, d]; later rows are left as they were."""
@@ -606,6 +622,20 @@ def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, 
 
     workspace is a CUDA uint8 tensor of at least fa_fwd_kv8_workspace_size() bytes.
     """
+    _fwd_kv8("fa_fwd_kv8", q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, causal, scale, counts,
+             workspace, stream)
+
+
+def fa_fwd_kv8_filled(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, causal: bool, scale: float,
+                      counts=None, workspace=None, stream=None) -> None:
+    """fa_fwd_kv8_filled of the C ABI: fa_fwd_kv8, with zeros in the rows of o and lse that have no result (past
+    counts[b], or of a sequence whose length or count is out of range)."""
+    _fwd_kv8("fa_fwd_kv8_filled", q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, causal, scale, counts,
+             workspace, stream)
+
+
+def _fwd_kv8(name, q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, causal, scale, counts, workspace,
+             stream):
     import torch
     if q.dim() != 4:
         raise ValueError("expected [B, H, N, d] tensors")
@@ -618,7 +648,7 @@ def fa_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, lse, 
             and _bytes(workspace) and _devices(q, lse, workspace) == {q.get_device()}):
         _refuse((("lse", lse, (torch.float32,), (B, Hq, Nq), True),
                  ("workspace", workspace, (torch.uint8,), () if workspace is None else workspace.shape, True)))
-    check("fa_fwd_kv8", load().fa_fwd_kv8(
+    check(name, getattr(load(), name)(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), lens.data_ptr(), _ptr(counts), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, d, page,
         pages, max_pages, 1 if causal else 0, scale, *_ws(workspace), _stream_handle(stream)))
@@ -741,7 +771,8 @@ class KV8Cache:
 
     Holds the pools, scales, page table (each sequence's pages one after another
     unless `page_table` and `num_pages` are given) and lengths, all on the device:
-    a decoding step (`append`, `attend`) can be captured into a CUDA graph.
+    a decoding step (`append`, `attend`) can be captured into a CUDA graph. `lens` may be
+    set by the caller, to values from 0 to max_pages * page.
     """
 
     def __init__(self, B: int, Hkv: int, d: int, max_tokens: int, page: int = 64, page_table=None, num_pages=None,
@@ -758,6 +789,7 @@ class KV8Cache:
                                       for _ in range(2))
         self.k_scale, self.v_scale = (torch.ones(num_pages, Hkv, dtype=torch.float32, device=device) for _ in range(2))
         self.lens = torch.zeros(B, dtype=torch.int32, device=device)
+        self._taken = torch.zeros_like(self.lens)
         self._workspaces = {}
 
     def _cache(self):
@@ -765,14 +797,17 @@ class KV8Cache:
 
     def append(self, k, v, counts=None, stream=None) -> None:
         """Lengthen each sequence by counts[b] (None: n) tokens and write k, v [B, Hkv, n, d] there.
-        A call that is refused leaves the lengths as they were."""
-        new = int(k.shape[2]) if counts is None else counts
+
+        A sequence that would outgrow its pages (max_tokens, rounded up to whole ones), or whose counts[b] is not
+        from 0 to n, is left as it was: its tokens are dropped, and FA_ERR_INDEX
+        is in the device status (fa_get_device_status). A call that is refused leaves all lengths as they were."""
         with _on_stream(stream):
-            self.lens.add_(new)
+            fa_kv8_advance(self.lens, counts, self._taken, int(k.shape[2]), self.k_cache.shape[2],
+                           self.page_table.shape[1], stream)
             try:
-                fa_kv8_append(k, v, *self._cache(), counts, stream)
+                fa_kv8_append(k, v, *self._cache(), self._taken, stream)
             except Exception:
-                self.lens.sub_(new)
+                self.lens.sub_(self._taken)
                 raise
 
     def gather(self, n: int, stream=None):
@@ -786,25 +821,25 @@ class KV8Cache:
         return k, v
 
     def attend(self, q, causal: bool = True, scale: float | None = None, counts=None, stream=None):
-        """O, L of q [B, Hq, Nq, d], whose last rows are the cache's newest tokens (fa_fwd_kv8); rows
-        past counts[b] are zero. One workspace per stream is kept, as large as the
+        """O, L of q [B, Hq, Nq, d], whose last rows are the cache's newest tokens (fa_fwd_kv8). Rows
+        that have no result are zero in both: those past counts[b], and those of a sequence whose length or
+        count is out of range (FA_ERR_INDEX in the device status). One workspace per stream is kept, as large as the
         calls so far needed; a captured call has one of its own, in its graph's memory."""
         import torch
         B, Hq, Nq, d = _dims(q)
         handle = _stream_handle(stream)
         size = max(1, fa_fwd_kv8_workspace_size(B, Hq, int(self.k_cache.shape[1]), Nq, d))
         with _on_stream(stream):
-            make = torch.empty if counts is None else torch.zeros
-            o = make(q.shape, dtype=q.dtype, device=q.device)
-            lse = make((B, Hq, Nq), dtype=torch.float32, device=q.device)
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
             workspace = self._workspaces.get(handle)
             capturing = torch.cuda.is_current_stream_capturing()
             if workspace is None or workspace.numel() < size or capturing:
                 workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
                 if not capturing:
                     self._workspaces[handle] = workspace
-        fa_fwd_kv8(q, *self._cache(), o, lse, causal, default_scale(d) if scale is None else scale, counts, workspace,
-                   handle)
+        fa_fwd_kv8_filled(q, *self._cache(), o, lse, causal, default_scale(d) if scale is None else scale, counts,
+                          workspace, handle)
         return o, lse
 
 

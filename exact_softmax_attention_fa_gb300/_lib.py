@@ -70,11 +70,14 @@ _SIGNATURES = {
                                   _vp, ctypes.c_size_t, _vp]),
     "fa_kv8_append": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                _c_int, _c_int, _vp]),
+    "fa_kv8_advance": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
     "fa_kv8_gather": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                _c_int, _vp]),
     "fa_fwd_kv8_workspace_size": (ctypes.c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "fa_fwd_kv8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                             _c_int, _c_int, _c_int, _c_int, _c_float, _vp, ctypes.c_size_t, _vp]),
+    "fa_fwd_kv8_filled": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                   _c_int, _c_int, _c_int, _c_int, _c_float, _vp, ctypes.c_size_t, _vp]),
     "fa_status_string": (ctypes.c_char_p, [_c_int]),
     "fa_get_device_status": (_c_int, [_vp]),
     "fa_get_device_status_detail": (_c_int, [_vp, _vp]),

@@ -615,6 +615,10 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   const int used = max(1, used_warps(total, static_cast<long long>(some) * pairs, warps));
   const int chunk = row / per_chunk, r = row - chunk * per_chunk;
   const long long s0 = before + static_cast<long long>(h * p.chunks + chunk) * steps, s1 = s0 + steps - 1;
+  if (!live && p.fill) {  // no other kernel of the call writes the row
+    if (group == 0) *reinterpret_cast<uint2*>(p.o + at * D + lane * 4) = make_uint2(0, 0);
+    if (threadIdx.x == 0) p.lse[at] = 0.f;
+  }
   griddep_wait();
   if ((bad_len || bad_count) && threadIdx.x == 0) record_bad_index(p.status, WHERE_FWD_KV8);
   if (!live) return;
@@ -725,11 +729,13 @@ size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
   return rows > tile_rows(d) ? kv8_tile_workspace(d) : part_bytes(d, rows, &off);
 }
 
-fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
-                       const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
-                       float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages, int max_pages,
-                       int causal, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+static fa_status_t run_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, const int* page_table, const int* lens, const int* counts,
+                               void* o, float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages,
+                               int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes,
+                               int fill, cudaStream_t stream) {
   Kv8Attn a{};
+  a.fill = fill;
   bool empty = false;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
@@ -769,6 +775,23 @@ fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, 
   if (d == 64) return from_cuda(nq == 1 ? launch_t<64, 1>(a, dev, stream) : launch_t<64, 2>(a, dev, stream));
   if (d == 128) return from_cuda(nq == 1 ? launch_t<128, 1>(a, dev, stream) : launch_t<128, 2>(a, dev, stream));
   return from_cuda(launch_t<256, 1>(a, dev, stream));
+}
+
+fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
+                       float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages, int max_pages,
+                       int causal, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return run_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, o, lse, B, Hq, Hkv, Nq, d, page,
+                     num_pages, max_pages, causal, scale, workspace, workspace_bytes, 0, stream);
+}
+
+fa_status_t fa_fwd_kv8_filled(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
+                              float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages,
+                              int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+  return run_fwd_kv8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, o, lse, B, Hq, Hkv, Nq, d, page,
+                     num_pages, max_pages, causal, scale, workspace, workspace_bytes, 1, stream);
 }
 
 }  // extern "C"

@@ -1084,6 +1084,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// Rows past a sequence's count, and all of one whose length or count is out of
+// range: zeros, a warp a row over the whole grid. No other kernel of the call writes
+// them, so this runs beside the main one.
+template <int D>
+__device__ __forceinline__ void fill_rows(const TileLaunch& p) {
+  const int lane = threadIdx.x & 31;
+  const long long all = static_cast<long long>(gridDim.x) * gridDim.y * 8;
+  const long long first = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 8 + (threadIdx.x >> 5);
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    int none = 0;  // of sequence b0 + lane: rows a head
+    if (b0 + lane < p.c.B) {
+      const int len = seq_len(p.c, b0 + lane), count = seq_count(p.c, b0 + lane, p.Nq);
+      const bool bad = len != __ldg(p.c.lens + b0 + lane) || (p.c.counts && count != __ldg(p.c.counts + b0 + lane));
+      none = bad ? p.Nq : p.Nq - count;
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, none > 0); left; left &= left - 1) {
+      const int l = __ffs(left) - 1, rows = __shfl_sync(0xffffffffu, none, l);
+      for (long long x = first; x < static_cast<long long>(rows) * p.Hq; x += all) {
+        const long long h = x / rows;
+        const size_t at = (static_cast<size_t>(b0 + l) * p.Hq + h) * p.Nq + (p.Nq - rows) + (x - h * rows);
+        if (lane < D / 8) reinterpret_cast<uint4*>(p.o + at * D)[lane] = make_uint4(0, 0, 0, 0);
+        if (lane == 0) p.lse[at] = 0.f;
+      }
+    }
+  }
+}
+
 // Joins the row blocks that CTAs shared. blockIdx.x = c > 0: the block that the
 // runs of CTAs c - 1 and c meet in, if c - 1 is the first that holds a part
 // of it; blockIdx.y: 8 of its rows. blockIdx.x = 0: sequences whose lengths or
@@ -1092,6 +1119,7 @@ template <int D>
 __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p) {
   using C = TileCfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.fill) fill_rows<D>(p);
   griddep_wait();
   if (blockIdx.x == 0) {
     for (int b = blockIdx.y; b < p.c.B; b += gridDim.y) {

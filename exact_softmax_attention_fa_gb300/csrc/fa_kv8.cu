@@ -135,6 +135,19 @@ __global__ void __launch_bounds__(append_threads(D, PAGE)) kv8_append_kernel(con
   if (threadIdx.x == 0) c.scale[kv][slot] = s;
 }
 
+// Lengths for an append that refuses no sequence any more: one latency, beside which
+// its few bytes do not count.
+__global__ void __launch_bounds__(128) kv8_advance_kernel(int* lens, const int* counts, int* taken, int B, int n,
+                                                          long long most, uint32_t* status) {
+  const int b = blockIdx.x * 128 + threadIdx.x;
+  if (b >= B) return;
+  const int len = lens[b], count = counts ? counts[b] : n;
+  const bool ok = count >= 0 && count <= n && len >= 0 && static_cast<long long>(len) + count <= most;
+  if (!ok) record_bad_index(status, WHERE_KV8_APPEND);
+  if (ok) lens[b] = len + count;
+  taken[b] = ok ? count : 0;
+}
+
 // Reads rows [0, min(lens[b], n)) back as bf16 [B][Hkv][n][d]. A thread holds
 // 16 columns (16 bytes in, 32 out) of kRows rows, whose loads are issued
 // together; a page may end between any two of them. Bound: HBM, 3 bytes a value:
@@ -279,6 +292,22 @@ fa_status_t fa_kv8_append(const void* k, const void* v, void* k_cache, void* v_c
     case 128: return from_cuda(launch_append<128>(c, k, v, n, dev.status, stream));
     default: return from_cuda(launch_append<256>(c, k, v, n, dev.status, stream));
   }
+}
+
+fa_status_t fa_kv8_advance(int* lens, const int* counts, int* taken, int B, int n, int page, int max_pages,
+                           cudaStream_t stream) {
+  if (B < 0 || n < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  const long long most = static_cast<long long>(max_pages) * page;
+  if (n > INT32_MAX - 256 || most > INT32_MAX - 256) return FA_ERR_INVALID_ARG;
+  if (B == 0) return FA_OK;
+  if (!lens || !taken) return FA_ERR_INVALID_ARG;
+  if (!aligned(lens, 4) || !aligned(counts, 4) || !aligned(taken, 4)) return FA_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const fa_status_t st = device_info(&dev);
+  if (st != FA_OK) return st;
+  kv8_advance_kernel<<<(B - 1) / 128 + 1, 128, 0, stream>>>(lens, counts, taken, B, n, most, dev.status);
+  return from_cuda(cudaGetLastError());
 }
 
 fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,

@@ -32,6 +32,7 @@ struct Kv8Call {
   float* lse;              // [B][Hq][Nq]
   int Hq, Nq, g, causal;   // g query heads per K/V head
   float scale_log2;
+  int fill;                // rows without a result are set to 0
 };
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }

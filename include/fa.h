@@ -429,6 +429,14 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
  *   A sequence with counts[b] < 0, > n or > lens[b], or more tokens than
  *   max_pages pages hold, is skipped whole; so are tokens whose page number is
  *   outside the pool. Pages that a call writes must belong to one sequence.
+ * fa_kv8_advance lengthens the sequences for a following fa_kv8_append, whose counts
+ * it makes, so that a sequence whose tokens the append would refuse keeps its
+ * length:
+ *   lens   : in, out, int32 [B], tokens before and after
+ *   counts : int32 [B] new tokens of each sequence, or null: n
+ *   taken  : out, int32 [B]: counts[b], and 0 for a sequence with counts[b] < 0 or
+ *            > n, lens[b] < 0, or more than max_pages * page tokens in the end, which is
+ *            recorded as FA_ERR_INDEX (role 31) and whose length stays
  * fa_kv8_gather reads a cache back:
  *   k, v : out, bf16 [B][Hkv][n][d]; row j of sequence b, j < min(lens[b], n),
  *          gets code * scale (exact for the scales fa_kv8_append writes, up to
@@ -438,6 +446,8 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
 fa_status_t fa_kv8_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                           const int* page_table, const int* lens, const int* counts, int B, int Hkv, int n, int d,
                           int page, int num_pages, int max_pages, cudaStream_t stream);
+fa_status_t fa_kv8_advance(int* lens, const int* counts, int* taken, int B, int n, int page, int max_pages,
+                           cudaStream_t stream);
 fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                           const int* page_table, const int* lens, void* k, void* v, int B, int Hkv, int n, int d,
                           int page, int num_pages, int max_pages, cudaStream_t stream);
@@ -466,7 +476,8 @@ fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float*
  *            the same time need workspaces of their own.
  * A length or count out of range is recorded as FA_ERR_INDEX and its sequence's
  * rows are left unwritten; tokens on a page outside the pool are recorded and
- * not seen. Results do not depend on timing: the same inputs on the same kind
+ * not seen. fa_fwd_kv8_filled leaves no row unwritten: those past counts[b] and those of
+ * a sequence whose length or count is out of range get O = 0, L = 0. Results do not depend on timing: the same inputs on the same kind
  * of device give the same bits.
  */
 size_t fa_fwd_kv8_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
@@ -474,6 +485,12 @@ fa_status_t fa_fwd_kv8(const void* q, const void* k_cache, const void* v_cache, 
                        const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
                        float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages, int max_pages,
                        int causal, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+fa_status_t fa_fwd_kv8_filled(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, const int* page_table, const int* lens, const int* counts, void* o,
+                              float* lse, int B, int Hq, int Hkv, int Nq, int d, int page, int num_pages,
+                              int max_pages, int causal, float scale, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* fa_status_string(fa_status_t status);

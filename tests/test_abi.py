@@ -413,3 +413,25 @@ def test_the_cache_attention_has_roles_of_its_own_for_the_skip_hook(lib):
     for good in (41, 42, 43, 44):
         assert lib.fa_debug_skip_arrival(good) == OK
     assert lib.fa_debug_skip_arrival(0) == OK
+
+
+def kv8_advance(lib, lens=P, counts=None, taken=P, B=2, n=4, page=16, mp=4):
+    return lib.fa_kv8_advance(lens, counts, taken, B, n, page, mp, None)
+
+
+def test_kv8_advance_refusals(lib):
+    for kw in (dict(B=-1), dict(n=-1), dict(mp=-1), dict(lens=0), dict(taken=0), dict(mp=1 << 27), dict(n=(1 << 31) - 1)):
+        assert kv8_advance(lib, **kw) == INVALID, kw
+    for page in (0, 8, 48, 256):
+        assert kv8_advance(lib, page=page) == UNSUPPORTED
+    for kw in (dict(lens=P + 2), dict(counts=P + 1), dict(taken=P + 2)):
+        assert kv8_advance(lib, **kw) == MISALIGNED, kw
+    assert kv8_advance(lib, B=0, lens=0, taken=0) == OK
+
+
+def test_fwd_kv8_filled_has_the_checks_of_fwd_kv8(lib):
+    def call(q=P, ws_bytes=1 << 30, causal=1, Hkv=2, d=64):
+        return lib.fa_fwd_kv8_filled(q, P, P, P, P, P, P, None, P, P, 2, 4, Hkv, 1, d, 16, 8, 4, causal, 0.125, P, ws_bytes, None)
+
+    assert call(q=0) == INVALID and call(causal=2) == INVALID and call(Hkv=3) == INVALID
+    assert call(d=96) == UNSUPPORTED and call(q=P + 8) == MISALIGNED and call(ws_bytes=16) == WORKSPACE
