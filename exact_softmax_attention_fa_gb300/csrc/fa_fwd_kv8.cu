@@ -364,6 +364,12 @@ __global__ void __maxnreg__((Cfg<D, NQ>::REGS)) kv8_attn_kernel(const __grid_con
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         raw[t] = live ? __ldg(reinterpret_cast<const uint2*>(p.q + at * D + t * 16 + c4 * 4)) : make_uint2(0, 0);
+      }
+      // The warp's references move together, so a row past the count would show in the others' last bits.
+      const bool past = qi >= count;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (past) raw[t] = make_uint2(0, 0);
         amax = max(amax, max(raw[t].x & 0x7fffu, (raw[t].x >> 16) & 0x7fffu));
         amax = max(amax, max(raw[t].y & 0x7fffu, (raw[t].y >> 16) & 0x7fffu));
       }
