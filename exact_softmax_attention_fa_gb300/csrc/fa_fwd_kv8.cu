@@ -641,11 +641,13 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   const int late = s0 > first_step(total, used, w0) ? 1 : 0;  // the row's first part is its warp's last
   float m = -INFINITY, l = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float low = INFINITY;  // smallest reference of a part that saw keys
   auto join = [&](float mx, float lx, const float4& x) {
     const float to = fmaxf(m, mx);
     const float ref = to == -INFINITY ? 0.f : to;
     const float wa = ex2_approx(m - ref), wx = ex2_approx(mx - ref);
-    l = add_sums(l, m - ref, wa, lx, mx - ref, wx);
+    l = l * wa + lx * wx;
+    low = fminf(low, lx > 0.f ? mx : INFINITY);
     m = to;
     a.x = a.x * wa + x.x * wx, a.y = a.y * wa + x.y * wx, a.z = a.z * wa + x.z * wx, a.w = a.w * wa + x.w * wx;
   };
@@ -663,11 +665,26 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
     for (int e = 0; e < 4; ++e)
       if (w + e * GROUPS <= w1) join(ml[e].x, ml[e].y, x[e]);
   }
+  if (m - low > 100.f) {  // a part's factor may have left fp32's range, its sum is added again
+    l = 0.f;
+#pragma unroll 1
+    for (int w = w0 + group; w <= w1; w += GROUPS) {
+      const float2 ml = p.part_ml[(static_cast<size_t>(w) * 2 + (w == w0 ? late : 0)) * p.part_rows + r];
+      l += scale_sum(ml.y, ml.x - m, ex2_approx(ml.x - m));
+    }
+  }
   red[threadIdx.x] = a;
   if (lane == 0) red_ml[group] = make_float2(m, l);
   __syncthreads();
   if (group > 0) return;
+  const float l0 = l, m0 = m;
+  low = l > 0.f ? m : INFINITY;
   for (int u = 1; u < GROUPS; ++u) join(red_ml[u].x, red_ml[u].y, red[u * LANES + lane]);
+  if (m - low > 100.f) {
+    l = scale_sum(l0, m0 - m, ex2_approx(m0 - m));
+#pragma unroll 1
+    for (int u = 1; u < GROUPS; ++u) l += scale_sum(red_ml[u].y, red_ml[u].x - m, ex2_approx(red_ml[u].x - m));
+  }
   const RowEnd end(m, l);
   *reinterpret_cast<uint2*>(p.o + at * D + lane * 4) =
       make_uint2(pack_bf16x2(end(a.x), end(a.y)), pack_bf16x2(end(a.z), end(a.w)));
