@@ -258,7 +258,7 @@ __global__ void __maxnreg__((Cfg<D, NQ>::REGS)) kv8_attn_kernel(const __grid_con
   Meta now{}, next{};
   float sk = 1.f, sv = 1.f;
   bool fresh = false;  // the batch's scales are on their way
-  int last_where = -1, last_most = kNoScale;
+  ScaleRun scales;
   look_up(next);
   // A stage holds rows of D bytes, keys then values; the 16-byte pieces of a row
   // are XORed with its key, so that eight keys' pieces of one block lie in
@@ -312,13 +312,9 @@ __global__ void __maxnreg__((Cfg<D, NQ>::REGS)) kv8_attn_kernel(const __grid_con
   // c sk, log2 sv (-inf hides a bad page's keys), 2^-kSumBias / sv, and s or where
   auto write_table = [&]() {
     float kf = 0.f, ev = 0.f, inv = 0.f;
-    const int e = now.slot >= 0 ? scale_exponent(sv) : kNoScale;
-    const int most = largest_of_id(e, now.where, &last_where, &last_most);
+    scales.take(now.slot >= 0, sv, now.where, &ev, &inv);
     if (now.slot >= 0) {
-      const ValueScale v(sv, e, most);
       kf = sk * p.scale_log2;
-      ev = v.log2_sv;
-      inv = v.inv;
     } else if (now.slot == -1) {
       ev = -INFINITY;
       record_bad_index(p.status, WHERE_FWD_KV8);

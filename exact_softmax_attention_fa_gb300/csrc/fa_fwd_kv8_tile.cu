@@ -390,7 +390,8 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   cur.begin(p, sh.start);
   cur.s += lane >> 3;
   cur.settle(p);
-  int next_id = -1, last_id = -1, last_most = kNoScale;  // of the value scales: sequence and head
+  int next_id = -1;  // sequence and head
+  ScaleRun scales;
   auto look_up = [&]() -> int {  // page * Hkv + head; -1: a bad page, -2: behind the sequence
     int slot = -2;
     if (cur.b < p.c.B) {
@@ -407,36 +408,22 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
   };
   int next = look_up(), now = -2;
   float4 entry = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sk = 0.f, sv = 0.f;
+  int now_id = -1;
   bool ok = true;
   int k_issued = 0, st_issued = 0;
   for (int i = 0; i < n; ++i) {
     const int j0 = (i & 3) * 8;
     if (j0 == 0) {
       now = next;
-      entry = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sk = 0.f, sv = 0.f;
+      now_id = next_id;
       if (now >= 0) sk = __ldg(p.c.scale[0] + now), sv = __ldg(p.c.scale[1] + now);
-      const int e = now >= 0 ? scale_exponent(sv) : kNoScale;
-      const int most = largest_of_id(e, next_id, &last_id, &last_most);
-      if (now >= 0) {
-        const ValueScale v(sv, e, most);
-        entry = make_float4(sk * p.scale_log2, v.log2_sv, v.inv, 1.f);
-      } else if (now == -1) {
-        entry.y = -INFINITY;  // its keys are not seen
-        record_bad_index(p.status, WHERE_FWD_KV8);
-      }
       next = look_up();
     }
     const int ks = i % C::KST;
     uint64_t* k_full = &sh.k_full[i % C::K_BARS];
     if (i >= C::KST) ok = warp_wait(&sh.k_empty[ks], ((i / C::KST) - 1) & 1, &sh.abort_flag, lim);
     if (!ok) break;
-    const int slot8 = i % C::SLOTS;
-    if (lane >= j0 && lane < j0 + 8) {
-      float* to = reinterpret_cast<float*>(sh.scale[slot8]) + lane - j0;
-      to[0] = entry.x, to[8] = entry.y, to[16] = entry.z, to[24] = entry.w;
-      mbar_arrive(&sh.scale_full[slot8]);
-    }
     // lane p < pages: page p of the tile
     const int slot = __shfl_sync(0xffffffffu, now, j0 + (lane * page / 16 & 7));
     const bool live = lane < pages && slot >= 0;
@@ -460,6 +447,23 @@ __device__ void load_role(const TileLaunch& p, TileShared<D>& sh, uint8_t* sK, u
         tma_load_3d(kd + c * (128 * 128) + lane * page * ROW_BYTES, &p.tmK, k_full, c * 128, 0, slot);
     }
     ++k_issued;
+    if (j0 == 0) {  // the scales, while K is on its way
+      entry = make_float4(0.f, 0.f, 0.f, 0.f);
+      scales.take(now >= 0, sv, now_id, &entry.y, &entry.z);
+      if (now >= 0) {
+        entry.x = sk * p.scale_log2;
+        entry.w = 1.f;
+      } else if (now == -1) {
+        entry.y = -INFINITY;  // its keys are not seen
+        record_bad_index(p.status, WHERE_FWD_KV8);
+      }
+    }
+    const int slot8 = i % C::SLOTS;
+    if (lane >= j0 && lane < j0 + 8) {
+      float* to = reinterpret_cast<float*>(sh.scale[slot8]) + lane - j0;
+      to[0] = entry.x, to[8] = entry.y, to[16] = entry.z, to[24] = entry.w;
+      mbar_arrive(&sh.scale_full[slot8]);
+    }
     const int ss = i % C::SST;
     if (i >= C::SST) ok = warp_wait(&sh.st_empty[ss], ((i / C::SST) - 1) & 1, &sh.abort_flag, lim);
     if (!ok) break;
@@ -1084,28 +1088,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_tile_kernel(const __grid_cons
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Rows past a sequence's count, and all of one whose length or count is out of
-// range: zeros, a warp a row over the whole grid. No other kernel of the call writes
-// them, so this runs beside the main one.
+// Rows that the main kernel does not write, so that this runs beside it: rows
+// without a key in row blocks without one (all of a sequence without tokens, the first ones
+// where queries stand before the sequence), and with `fill` those past a
+// sequence's count and all of one whose length or count is out of range. A warp a
+// row, the warps of the first blocks (as many as there are sequences, or those of
+// blockIdx.x = 0) shared out over the sequences.
 template <int D>
-__device__ __forceinline__ void fill_rows(const TileLaunch& p) {
+__device__ __forceinline__ void write_other_rows(const TileLaunch& p) {
+  using C = TileCfg<D>;
   const int lane = threadIdx.x & 31;
-  const long long all = static_cast<long long>(gridDim.x) * gridDim.y * 8;
-  const long long first = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 8 + (threadIdx.x >> 5);
-  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-    int none = 0;  // of sequence b0 + lane: rows a head
-    if (b0 + lane < p.c.B) {
-      const int len = seq_len(p.c, b0 + lane), count = seq_count(p.c, b0 + lane, p.Nq);
-      const bool bad = len != __ldg(p.c.lens + b0 + lane) || (p.c.counts && count != __ldg(p.c.counts + b0 + lane));
-      none = bad ? p.Nq : p.Nq - count;
+  const int per_x = gridDim.y * 8, nx = min(static_cast<int>(gridDim.x), (p.c.B - 1) / per_x + 1);
+  const int warps = nx * per_x, share = max(1, warps / p.c.B);
+  auto write = [&](size_t at, float lse) {
+    if (lane < D / 8) reinterpret_cast<uint4*>(p.o + at * D)[lane] = make_uint4(0, 0, 0, 0);
+    if (lane == 0) p.lse[at] = lse;
+  };
+  for (int k = blockIdx.x * per_x + blockIdx.y * 8 + (threadIdx.x >> 5); k / share < p.c.B; k += warps) {
+    const int b = k / share, part = k - b * share;
+    const int len = seq_len(p.c, b), count = seq_count(p.c, b, p.Nq);
+    const bool bad = len != __ldg(p.c.lens + b) || (p.c.counts && count != __ldg(p.c.counts + b));
+    if (bad && part == 0 && lane == 0) record_bad_index(p.status, WHERE_FWD_KV8);
+    const size_t head0 = static_cast<size_t>(b) * p.Hq;
+    const int past = !p.fill ? 0 : bad ? p.Nq : p.Nq - count;  // rows a head
+    for (long long x = part; x < static_cast<long long>(past) * p.Hq; x += share) {
+      const long long h = x / past;
+      write((head0 + h) * p.Nq + (p.Nq - past) + (x - h * past), 0.f);
     }
-    for (unsigned left = __ballot_sync(0xffffffffu, none > 0); left; left &= left - 1) {
-      const int l = __ffs(left) - 1, rows = __shfl_sync(0xffffffffu, none, l);
-      for (long long x = first; x < static_cast<long long>(rows) * p.Hq; x += all) {
-        const long long h = x / rows;
-        const size_t at = (static_cast<size_t>(b0 + l) * p.Hq + h) * p.Nq + (p.Nq - rows) + (x - h * rows);
-        if (lane < D / 8) reinterpret_cast<uint4*>(p.o + at * D)[lane] = make_uint4(0, 0, 0, 0);
-        if (lane == 0) p.lse[at] = 0.f;
+    if (bad || (len > 0 && !(p.causal && count > len))) continue;
+    const int rows = count * p.g;
+    for (int blk = 0; blk * C::ROWS < rows; ++blk) {
+      const int end = min(rows, (blk + 1) * C::ROWS);
+      if (tiles_seen(len, count, end, p.g, p.causal) > 0) break;
+      for (int x = part; x < (end - blk * C::ROWS) * p.c.Hkv; x += share) {
+        const int row = blk * C::ROWS + x / p.c.Hkv, h = x % p.c.Hkv;
+        write((head0 + h * p.g + row % p.g) * p.Nq + row / p.g, -INFINITY);
       }
     }
   }
@@ -1113,38 +1130,15 @@ __device__ __forceinline__ void fill_rows(const TileLaunch& p) {
 
 // Joins the row blocks that CTAs shared. blockIdx.x = c > 0: the block that the
 // runs of CTAs c - 1 and c meet in, if c - 1 is the first that holds a part
-// of it; blockIdx.y: 8 of its rows. blockIdx.x = 0: sequences whose lengths or
-// counts are out of range, and rows that see no key at all.
+// of it; blockIdx.y: 8 of its rows.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_constant__ TileLaunch p) {
   using C = TileCfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (p.fill) fill_rows<D>(p);
+  // (a grid has thousands of blocks: the others compute nothing here)
+  if (blockIdx.x * gridDim.y * 8 < static_cast<unsigned>(p.c.B)) write_other_rows<D>(p);
   griddep_wait();
-  if (blockIdx.x == 0) {
-    for (int b = blockIdx.y; b < p.c.B; b += gridDim.y) {
-      const int len = seq_len(p.c, b), count = seq_count(p.c, b, p.Nq);
-      if (len != __ldg(p.c.lens + b) || (p.c.counts && count != __ldg(p.c.counts + b))) {
-        if (threadIdx.x == 0) record_bad_index(p.status, WHERE_FWD_KV8);
-        continue;
-      }
-      // whole blocks without a key: all of them without tokens, the first ones where queries stand before the sequence
-      const int none = len == 0 ? count : p.causal ? max(0, count - len) : 0;
-      if (none == 0) continue;
-      const int rows = count * p.g;
-      for (int blk = 0; blk * C::ROWS < rows; ++blk) {
-        const int end = min(rows, (blk + 1) * C::ROWS);
-        if (tiles_seen(len, count, end, p.g, p.causal) > 0) break;
-        for (int x = warp; x < (end - blk * C::ROWS) * p.c.Hkv; x += 8) {
-          const int row = blk * C::ROWS + x / p.c.Hkv, h = x % p.c.Hkv;
-          const size_t at = (static_cast<size_t>(b) * p.Hq + h * p.g + row % p.g) * p.Nq + row / p.g;
-          for (int c = lane; c < D / 8; c += 32) reinterpret_cast<uint4*>(p.o + at * D)[c] = make_uint4(0, 0, 0, 0);
-          if (lane == 0) p.lse[at] = -INFINITY;
-        }
-      }
-    }
-    return;
-  }
+  if (blockIdx.x == 0) return;
   const int c = blockIdx.x;
   const int4 at = p.run[2 * c], held = p.run[2 * c + 1];
   const int c0 = held.x, c1 = held.y, count = held.w;
@@ -1154,6 +1148,7 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_cons
   const int rb = blockIdx.y * 8 + warp, row = at.z * C::ROWS + rb, qi = row / p.g;
   if (qi >= count) return;
   float m = -INFINITY, l = 0.f, a[PER];
+  float low = INFINITY;  // smallest reference of a part that saw keys
 #pragma unroll
   for (int k = 0; k < PER; ++k) a[k] = 0.f;
   for (int u0 = c0; u0 <= c1; u0 += 4) {
@@ -1171,10 +1166,19 @@ __global__ void __launch_bounds__(256) kv8_tile_combine_kernel(const __grid_cons
       if (u0 + e > c1) break;
       const float to = fmaxf(m, ml[e].x), ref = to == -INFINITY ? 0.f : to;
       const float wa = ex2_approx(m - ref), wx = ex2_approx(ml[e].x - ref);
-      l = add_sums(l, m - ref, wa, ml[e].y, ml[e].x - ref, wx);
+      l = l * wa + ml[e].y * wx;
+      low = fminf(low, ml[e].y > 0.f ? ml[e].x : INFINITY);
       m = to;
 #pragma unroll
       for (int k = 0; k < PER; ++k) a[k] = a[k] * wa + (k & 1 ? x[e][k / 2].y : x[e][k / 2].x) * wx;
+    }
+  }
+  if (m - low > 100.f) {  // a part's factor may have left fp32's range, its sum is added again
+    l = 0.f;
+#pragma unroll 1
+    for (int u = c0; u <= c1; ++u) {
+      const float2 ml = p.part_ml[(static_cast<size_t>(u) * 2 + (u == c0 ? held.z : 0)) * C::ROWS + rb];
+      l += scale_sum(ml.y, ml.x - m, ex2_approx(ml.x - m));
     }
   }
   const RowEnd end(m, l);

@@ -2,8 +2,6 @@
 // (fa_fwd_kv8.cu: few query rows per K/V head, fa_fwd_kv8_tile.cu: many).
 #pragma once
 
-#include <climits>
-
 #include "fa_kv8.cuh"
 
 namespace fa {
@@ -66,45 +64,36 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// log2 of a value scale and 2^-kSumBias / sv, as a run takes them; most: the largest
-// exponent that it has met.
-struct ValueScale {
-  float log2_sv, inv;
-  __device__ __forceinline__ ValueScale(float sv, int e, int most) {
-    const int least = max(most - kScaleSpread, kMinScaleExp);
-    if (e < least) {
-      log2_sv = static_cast<float>(least);
-      inv = exp2i(-static_cast<int>(kSumBias) - least);
-    } else {
-      log2_sv = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
-      inv = exp2i(-static_cast<int>(kSumBias)) / sv;
-    }
-  }
-};
 // Exponent of a value scale (rounded down; -126 for all smaller ones).
 __device__ __forceinline__ int scale_exponent(float sv) {
   return min(max(static_cast<int>(__float_as_uint(sv) >> 23 & 255) - 127, -126), 126);
 }
-// Lanes hold consecutive groups of a run, each with its exponent (kNoScale: none) and
-// the sequence and head (`id`) it belongs to: the largest exponent of this id among
-// them and, where it is the id of the lanes before, last_id, among those; or kNoScale
-// where no exponent is to be raised, as nearly always. The later groups count too:
-// one softmax step takes several of them with one reference.
-constexpr int kNoScale = -1000;
-__device__ __forceinline__ int largest_of_id(int e, int id, int* last_id, int* last_most) {
-  const int hi = max(__reduce_max_sync(0xffffffffu, e), *last_most);
-  const int lo = __reduce_min_sync(0xffffffffu, e == kNoScale ? INT_MAX : e);
-  const int tail = __shfl_sync(0xffffffffu, id, 31);
-  const int tail_most = __reduce_max_sync(0xffffffffu, id == tail ? e : kNoScale);
-  int most = kNoScale;
-  if (lo < kMinScaleExp || (lo != INT_MAX && hi - lo > kScaleSpread)) {
-    most = __reduce_max_sync(__match_any_sync(0xffffffffu, id), e);
-    if (id == *last_id) most = max(most, *last_most);
+
+// log2 of the value scales of a run's 16-key groups and 2^-kSumBias / sv, 32
+// consecutive groups at a time, one a lane; `id`: the group's sequence and head.
+struct ScaleRun {
+  int id = -1, most = -1000;  // of the last lane's id so far: the largest exponent
+  __device__ __forceinline__ void take(bool has, float sv, int group_id, float* log2_sv, float* inv) {
+    const int e = scale_exponent(sv);
+    if (has) {
+      *log2_sv = static_cast<float>(e) + log2f(sv * exp2i(-e));  // exact for a power of two
+      *inv = exp2i(-static_cast<int>(kSumBias)) / sv;
+    }
+    const bool near = !has || (group_id == id && e <= most && e >= max(most - kScaleSpread, kMinScaleExp));
+    if (__all_sync(0xffffffffu, near)) return;
+    // A new id or a larger scale, or one to hold. The later groups of an id count too:
+    // one softmax step takes several of them with one reference.
+    int own = __reduce_max_sync(__match_any_sync(0xffffffffu, group_id), has ? e : -1000);
+    if (group_id == id) own = max(own, most);
+    id = __shfl_sync(0xffffffffu, group_id, 31);
+    most = __shfl_sync(0xffffffffu, own, 31);
+    const int least = max(own - kScaleSpread, kMinScaleExp);
+    if (has && e < least) {
+      *log2_sv = static_cast<float>(least);
+      *inv = exp2i(-static_cast<int>(kSumBias) - least);
+    }
   }
-  *last_most = tail == *last_id ? max(*last_most, tail_most) : tail_most;
-  *last_id = tail;
-  return most;
-}
+};
 
 // l 2^d, d <= 0 (exp2_d: 2^d): in two steps where 2^d alone would leave fp32's range; a
 // sum of small value scales that meets a far larger one is as large as its factor is small.

@@ -133,19 +133,21 @@ def test_a_call_refused_on_the_host_leaves_the_lengths():
     assert fa.fa_get_device_status() == 0
 
 
-@pytest.mark.parametrize("B", [3, 70])
+@pytest.mark.parametrize("B", [3, 70, 2500])
 @pytest.mark.parametrize("Hq,Nq,d", [(4, 1, 128), (2, 3, 256), (4, 40, 64), (2, 300, 128), (1, 200, 256)])
 def test_filled_rows(B, Hq, Nq, d):
     """Where there is a result it is fa_fwd_kv8's, bit for bit; everywhere else O = 0, L = 0."""
     import exact_softmax_attention_fa_gb300 as fa
     import torch
     gen = torch.Generator(device="cuda").manual_seed(BASE_SEED + B + Nq)
-    n = 320
+    if B > 100 and Nq * d > 3000:
+        pytest.skip("many sequences: the short ones are enough")
+    n = 320 if B <= 100 else 48
     cache = fa.KV8Cache(B, 1, d, n, page=32)
     cache.append(*(randn(gen, B, 1, n, d) for _ in range(2)))
     lens = torch.randint(0, n + 1, (B,), generator=gen, device="cuda").to(torch.int32)
     counts = torch.randint(0, Nq + 1, (B,), generator=gen, device="cuda").to(torch.int32)
-    lens[0], counts[1], counts[2] = n + 1, Nq + 1, 0
+    lens[0], counts[1], counts[2] = cache.page_table.shape[1] * 32 + 1, Nq + 1, 0
     q = randn(gen, B, Hq, Nq, d)
     ws = torch.empty(fa.fa_fwd_kv8_workspace_size(B, Hq, 1, Nq, d), dtype=torch.uint8, device="cuda")
     got = []

@@ -157,10 +157,10 @@ def walk(d, halves, parts, moves, dead_warps=0):
     for i in range(total):
         if i >= KST:
             r.wait("load", ("k_empty", i % KST), i // KST - 1)
-        scale_write[i] = r.step("load")
-        r.arrive("load", ("scale_full", i % SLOTS), i // SLOTS)
         k_issue[i] = r.arrive("load", ("k_full", i % KB), i // KB)        # the expected bytes
         r.arrive(None, ("k_full", i % KB), i // KB, (k_issue[i],))        # the copy lands
+        scale_write[i] = r.step("load")
+        r.arrive("load", ("scale_full", i % SLOTS), i // SLOTS)
         if i >= SST:
             r.wait("load", ("st_empty", i % SST), i // SST - 1)
         stage_issue[i] = r.arrive("load", ("st_full", i % SST), i // SST)
