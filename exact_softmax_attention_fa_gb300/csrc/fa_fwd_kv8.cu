@@ -14,7 +14,7 @@
 // multiplied with them is split into e4m3 pieces that occupy columns of their
 // own, since a decoding call leaves most of an MMA's 8 columns empty anyway:
 //   a query value q 2^a (row maximum in [2^7, 2^8)) = qh + 2^-4 ql, exact down to
-//   2^-14 of the row's largest value, and within 2^-22 of it below;
+//   2^-13 of the row's largest value, and within 2^-21 of it below;
 //   P (at most 448), rounded to fp16, = ph + 2^-4 pm + 2^-8 pl: 2^-11 relative, and
 //   never coarser than 2^-24 of the row's largest weight (fp16 so that the pieces
 //   are taken two at a time; l sums the unrounded weights).
@@ -30,9 +30,9 @@
 // (stages - 1) * 64 d bytes per warp are in flight. Runs are of equal length
 // whatever the sequences' lengths are; a row whose keys are shared between
 // warps is joined by kv8_combine_kernel. Measured: B = 8, 32 heads on 8, 32768 keys,
-// d = 128, pages of 64: 89 us, 6.1 TB/s; B = 16, 32 heads, ragged up to 8192 keys,
+// d = 128, pages of 64: 90 us, 6.0 TB/s; B = 16, 32 heads, ragged up to 8192 keys,
 // d = 64, pages of 32: 55 us, 5.1 TB/s (a step of d = 64 has half the bytes
-// for the same instructions); one sequence of 1000 keys: 9.2 us, two launches and
+// for the same instructions); one sequence of 1000 keys: 9.6 us, two launches and
 // the walk length, page number, codes.
 //
 // Products are m16n8k32 with the cache as the 16-row operand and the rows'
@@ -691,9 +691,13 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
 // fa_fwd_kv8_tile.cu. This kernel reads the cache once per chunk of rows; the
 // tiles' time hardly depends on the rows below 128. B = 8, Hkv = 8, 16384 keys
 // (and B = 1, Hkv = 8, 4096 keys), rows: this kernel / tiles, us:
-//   d =  64: 16: 64 / 76 (15 / 19)    24: 94 / 76 (16 / 20)
-//   d = 128: 8: 59 / 92 (17 / 21)     16: 101 / 91 (21 / 20)   24: 142 / 92 (23 / 21)
-//   d = 256: 8: 182 / 173 (22 / 26)   12: 263 / 173 (23 / 26)  16: 345 / 173 (23 / 27)
+//   d =  64: 8: 39 / 73 (13.9 / 19.0)    16: 62 / 73 (14.3 / 19.1)    24: 87 / 73 (16.5 / 19.1)
+//   d = 128: 8: 57 / 89 (17.4 / 20.6)    12: 97 / 89 (19.0 / 20.0)    16: 99 / 89 (19.5 / 20.3)
+//            24: 142 / 89 (22.0 / 20.7)
+//   d = 256: 8: 178 / 174 (17.5 / 24.9)  12: 260 / 174 (20.6 / 25.0)  16: 339 / 174 (20.5 / 25.2)
+// At d = 128 the tiles would be a tenth faster on the long caches from 9 rows on; up to
+// 16 stay here for the short calls and because the tiles hold a query's small
+// columns 16 times as coarsely. So do 8 at d = 256.
 constexpr int tile_rows(int d) { return d == 256 ? 8 : 16; }
 
 // 8-column tiles of a row chunk: two (8 rows) where the rows fill more than one

@@ -8,11 +8,11 @@
 //   S = Q K^T  : kind::f8f6f4. K's codes are the operand as TMA brings them. A
 //       query row, moved by a power of two so that its largest |value| lies in
 //       [2^7, 2^8), is the sum of two e4m3 pieces qh + ql, accumulated into the
-//       same S: exact for values down to 2^-10 of the row's largest, within
-//       2^-18 of it below. Two e4m3 products cost what one fp16 product would,
+//       same S: exact for values down to 2^-9 of the row's largest, within
+//       2^-17 of it below. Two e4m3 products cost what one fp16 product would,
 //       and K needs no conversion and half the shared memory.
 //   O += P V   : kind::f16. A weight keeps fp16's 2^-11 and range (small weights
-//       of a long row together matter, and e4m3 pieces end at 2^-18 of the
+//       of a long row together matter, and e4m3 pieces end at 2^-17 of the
 //       largest), so V's codes, exact in fp16, are converted by a warpgroup
 //       of their own from a staging ring into the swizzled operand tile.
 // Key and value scales enter as in fa_fwd_kv8.cu: u = c sk (q . k8) + log2 sv per
@@ -23,22 +23,22 @@
 // each of warps 13 and 14 issues the MMAs of a slot. A slot is a tile of 128 rows;
 // where the rows of a K/V head fill only one (decoding a few tokens of a group),
 // both slots take it with every other key tile each, and the CTA joins them
-// (128 rows, B = 8, Hkv = 8, 16384 keys, d = 128: 129 us with one slot, 101 so).
+// (128 rows, B = 8, Hkv = 8, 16384 keys, d = 128: 129 us with one slot, 97 so).
 // d = 256 has tensor memory for one slot.
 //
 // Softmax steps are 64 keys, with two buffers of S per slot: S(f + 1) is formed
 // beside the softmax of step f, so a slot waits for neither product. (128-key steps
 // with one buffer: the chain S, softmax, PV of a slot bound, 232 us for 1024 queries
-// on 16384 keys, B = 2, 16 heads on 4, d = 128; now 203. One thread issuing for
+// on 16384 keys, B = 2, 16 heads on 4, d = 128; now 208. One thread issuing for
 // both slots: 369, it spends more time between MMAs than the steps leave it.)
 //
-// Bound: shared memory, at that size at 0.62 of the tensor rate (1180 TFLOP/s). Two
+// Bound: shared memory, at that size at 0.60 of the tensor rate (1160 TFLOP/s). Two
 // slots take some 3600 cycles for 128 keys. The tensor core alone would take 2477
 // (measured; 2049 with 128-column S, for which tensor memory has no second buffer),
-// and reads operands for 58% of the time (a 64-column S: 6 KB per 48 cycles);
-// loads, stores and tensor-memory reads take the same memory for 32%. A CTA's
-// fixed work (the search for its run, Q pieces, the epilogue) takes 8 us, most of
-// a small call (21 us for 32 rows of 8 heads against 4096 keys).
+// and reads operands for 59% of the time (a 64-column S: 6 KB per 48 cycles);
+// loads, stores and tensor-memory reads take the same memory for 27%. A CTA's
+// fixed work (the search for its run, Q pieces, the epilogue) takes 8 us of a small
+// call's 21 (32 rows of 8 heads against 4096 keys).
 //
 // Work: every CTA takes an equal run of the flattened list of (sequence, K/V
 // head, row block, key tile); a row block that CTAs share is joined by

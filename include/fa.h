@@ -471,6 +471,11 @@ fa_status_t fa_kv8_gather(const void* k_cache, const void* v_cache, const float*
  *            below 2^-89 of the largest one (448 * its page's scale, if that is more),
  *            are then off by as much as they are. Their weights are not.
  *   scale  : finite and > 0
+ *   Roundings besides fp32's and the outputs': each weight to fp16 (2^-11 of it, or
+ *            2^-24 of the row's largest weight times its value scale) before it
+ *            multiplies a value, not in the sum that divides; a query value to 2^-21 of its row's largest with up to 16
+ *            rows (Hq / Hkv * Nq) per K/V head, 8 at d = 256, and to 2^-17 with more,
+ *            where it has more bits than that.
  *   workspace : fa_fwd_kv8_workspace_size() bytes, 256-byte aligned; the
  *            parts of rows whose keys several SMs share. Calls that may run at
  *            the same time need workspaces of their own.
