@@ -115,15 +115,10 @@ __device__ __forceinline__ float add_sums(float a, float da, float wa, float b, 
 struct RowEnd {
   float a, b, lse;
   __device__ __forceinline__ RowEnd(float m, float l) {
-    const int e = static_cast<int>(__float_as_uint(l) >> 23 & 255) - 127;  // l >= 0
-    a = l == 0.f ? 0.f : 1.f;
-    b = 1.f;
-    if (l != 0.f && e < 127) {  // not infinite, not NaN
-      b = exp2i(-e);
-      a = exp2i(-static_cast<int>(kSumBias)) / (l * b);
-    } else if (l != 0.f) {
-      a = 1.f / l + (l - l);  // NaN, not 0, for an infinite sum
-    }
+    const int e = min(static_cast<int>(__float_as_uint(l) >> 23 & 255) - 127, 126);  // l >= 0
+    b = exp2i(-e);
+    // l - l: NaN, not 0, for an infinite sum
+    a = l == 0.f ? 0.f : exp2i(-static_cast<int>(kSumBias)) / (l * b) + (l - l);
     lse = l == 0.f ? -INFINITY : (m + kSumBias + log2f(l)) * kLn2;
   }
   __device__ __forceinline__ float operator()(float x) const { return a == 0.f ? 0.f : x * a * b; }
