@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 
 from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: F401
 
@@ -296,6 +297,31 @@ def _check_host(name, t, shape, dtype):
         raise ValueError(f"{name} must be a contiguous {dtype} CPU tensor of shape {shape}")
 
 
+# Host tensors of calls in flight. torch hands a page-locked tensor that the
+# caller has dropped out again at once: it knows nothing of the library's copies.
+_in_flight = []
+_in_flight_lock = threading.Lock()
+
+
+def _drop_finished() -> None:
+    with _in_flight_lock:
+        _in_flight[:] = [call for call in _in_flight if not call[0].query()]
+
+
+def _hold(stream, *tensors) -> None:
+    """Keep a call's host tensors until the stream has done its work (looked at by the next such call and
+    by fa_get_device_status). A captured call's tensors are the caller's to keep, as long as the graph."""
+    import torch
+    with _on_stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            return
+        event = torch.cuda.Event()
+        event.record()
+    _drop_finished()
+    with _in_flight_lock:
+        _in_flight.append((event, tensors))
+
+
 def fa_fwd_bwd_host(q, k, v, do, o, lse, dq, dk, dv, causal: bool, scale: float, device_buffer,
                     stream=None) -> None:
     """fa_fwd_bwd_host of the C ABI: forward and backward of CPU tensors.
@@ -305,7 +331,8 @@ def fa_fwd_bwd_host(q, k, v, do, o, lse, dq, dk, dv, causal: bool, scale: float,
     (pin_memory) let the library overlap the copies with the kernels.
     device_buffer is a CUDA uint8 tensor of at least
     fa_fwd_bwd_host_device_bytes(B, H, N, d) bytes. Asynchronous on `stream`:
-    the outputs are valid once the stream has synchronised.
+    the outputs are valid once the stream has synchronised. The host tensors
+    may be dropped before that, but not written to.
     """
     import torch
     shape = _dims(q)
@@ -319,6 +346,7 @@ def fa_fwd_bwd_host(q, k, v, do, o, lse, dq, dk, dv, causal: bool, scale: float,
         q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), B, H, N, d, int(bool(causal)), float(scale), device_buffer.data_ptr(),
         device_buffer.numel(), _stream_handle(stream)))
+    _hold(stream, q, k, v, do, o, lse, dq, dk, dv)
 
 
 def fa_fwd_host_device_bytes(B: int, H: int, N: int, d: int) -> int:
@@ -344,6 +372,7 @@ def fa_fwd_host(q, k, v, o, lse, causal: bool, scale: float, device_buffer, stre
     check("fa_fwd_host", load().fa_fwd_host(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, N, d, int(bool(causal)),
         float(scale), device_buffer.data_ptr(), device_buffer.numel(), _stream_handle(stream)))
+    _hold(stream, q, k, v, o, lse)
 
 
 def rope_tables(rows: int, rot: int, base: float = 10000.0, device="cuda"):
@@ -656,7 +685,9 @@ def _fwd_kv8(name, q, k_cache, v_cache, k_scale, v_scale, page_table, lens, o, l
 
 def fa_get_device_status(stream=None) -> int:
     """Synchronise the stream; return and clear the device status (0 = FA_OK)."""
-    return int(load().fa_get_device_status(_stream_handle(stream)))
+    st = int(load().fa_get_device_status(_stream_handle(stream)))
+    _drop_finished()
+    return st
 
 
 def fa_get_device_status_detail(stream=None) -> tuple:
@@ -664,6 +695,7 @@ def fa_get_device_status_detail(stream=None) -> tuple:
     (code, role of the first wait that gave up, its block, its thread)."""
     word = (ctypes.c_uint * 4)()
     st = int(load().fa_get_device_status_detail(ctypes.addressof(word), _stream_handle(stream)))
+    _drop_finished()
     if st == 7:  # FA_ERR_CUDA: the synchronisation failed, the word was not read
         check("fa_get_device_status_detail", st)
     return tuple(int(x) for x in word)
