@@ -145,12 +145,10 @@ def ragged(B, longest, seed):
 FEW = {64: 47000, 128: 30000, 256: 15000}
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("page,g,Nq", [(16, 1, 1), (128, 4, 1), (64, 8, 1), (32, 3, 2), (16, 4, 4)])
+@pytest.mark.parametrize("d,page,g,Nq", [(d, *x) for d in (64, 128, 256) for x in ((16, 1, 1), (128, 4, 1), (64, 8, 1), (32, 3, 2))] +
+                         [(64, 16, 4, 4), (128, 16, 4, 4)])
 def test_few_rows_a_head(d, page, g, Nq):
     # 40 steps a warp: the ring of three or four stages wraps ten times, the page batches of 16 steps twice
-    if g * Nq > ROWS_FEW[d]:
-        pytest.skip("these rows take the other kernel at this d")
     lens = [max(n, Nq) for n in ragged(10, FEW[d], d + page)]
     check(8 * g, 8, Nq, d, page, lens, True, BASE_SEED + d + g, 40)
 

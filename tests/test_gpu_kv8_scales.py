@@ -84,12 +84,10 @@ ROWS = [(4, 1), (8, 2), (4, 20), (3, 100)]  # 4 and 16 rows; one tile, two tiles
 
 
 @pytest.mark.parametrize("Hq,Nq", ROWS)
-@pytest.mark.parametrize("exp", [-np.inf, -140, -126, -120, -101, -100, 121, 126])
-@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("d,exp", [(d, e) for d in (64, 128) for e in (-np.inf, -140, -126, -120, -101, -100, 121, 126)] +
+                         [(256, e) for e in (-np.inf, -126, 126)])
 def test_many_equal_weights_at_the_ends_of_the_scales_range(d, exp, Hq, Nq):
     # 4096 keys of the same score: their sum is 2^12 whatever the scale is
-    if d == 256 and exp not in (-np.inf, -126, 126):
-        pytest.skip("two ends are enough at d = 256")
     rng = np.random.default_rng(BASE_SEED + int(max(exp, -200)) + 200)
     pages, page = 64, 64
     code = tokens(rng, pages, page, d)
@@ -111,11 +109,9 @@ ORDERS = {
 
 @pytest.mark.parametrize("Hq,Nq", ROWS)
 @pytest.mark.parametrize("order", list(ORDERS))
-@pytest.mark.parametrize("lo,hi", [(-126, 110), (-100, -8), (-100, 0), (-100, 60), (0, 120)])
-@pytest.mark.parametrize("n", [330, 20000])
+@pytest.mark.parametrize("n,lo,hi", [(330, -126, 110), (330, -100, -8), (330, -100, 0), (330, -100, 60), (330, 0, 120),
+                                     (20000, -100, 60)])  # the last: parts that several SMs join
 def test_pages_whose_value_scales_lie_far_apart(n, lo, hi, order, Hq, Nq):
-    if n > 1000 and (lo, hi) != (-100, 60):
-        pytest.skip("one pair of scales is enough for the parts that several SMs join")
     d, page = (64, 16) if n < 1000 else (128, 64)
     rng = np.random.default_rng(BASE_SEED + n + lo + hi + Hq)
     pages = -(-n // page)
