@@ -20,7 +20,8 @@ from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: 
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_bwd_deterministic", "fa_bwd_gqa_deterministic", "fa_bwd_workspace_size", "fa_bwd_gqa_workspace_size", "fa_bwd_preprocess", "fa_bwd_preprocess_stats", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_dkdv", "fa_bwd_dq", "fa_bwd_noalloc", "fa_fwd_bwd_host", "fa_fwd_bwd_host_device_bytes", "fa_fwd_host", "fa_fwd_host_device_bytes", "fa_get_device_status", "fa_get_device_status_detail", "fa_set_wait_limit_ns",
            "fa_debug_timeout_probe", "fa_debug_skip_arrival", "fa_norm_rope_fwd", "fa_norm_rope_bwd",
-           "fa_norm_rope_bwd_workspace_size", "fa_kv8_append", "fa_kv8_advance", "fa_kv8_gather",
+           "fa_norm_rope_bwd_workspace_size", "fa_norm_rope_axes_fwd", "fa_norm_rope_axes_bwd", "fa_packed_plan_size", "fa_packed_plan", "fa_fwd_packed", "fa_bwd_packed",
+           "fa_bwd_packed_workspace_size", "PackedPlan", "forward_packed", "backward_packed", "fa_kv8_append", "fa_kv8_advance", "fa_kv8_gather",
            "fa_fwd_kv8", "fa_fwd_kv8_filled", "fa_fwd_kv8_workspace_size", "KV8Cache", "rope_tables", "norm_rope", "norm_rope_backward", "forward", "backward", "FAError", "flops"]
 
 _SUPPORTED_D = (64, 128, 256)
@@ -430,7 +431,7 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _norm_rope_named(B, Hq, Hkv, N, d, qkv, strided, w, cos, sin, positions, dw, workspace):
+def _norm_rope_named(B, Hq, Hkv, N, d, qkv, strided, w, cos, sin, positions, dw, workspace, axes=None):
     import torch
     bf, f32 = (torch.bfloat16,), (torch.float32,)
     qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
@@ -441,7 +442,8 @@ def _norm_rope_named(B, Hq, Hkv, N, d, qkv, strided, w, cos, sin, positions, dw,
         named += [(n, t, f32, cos.shape, True) for n, t in (("cos", cos), ("sin", sin))]
     named += [(n, t, f32, (d,), True) for n, t in dw]
     if positions is not None:
-        named.append(("positions", positions, (torch.int32,), (B, N), True))
+        planes = () if axes is None else (max(1, positions.dim() and positions.shape[0]),)
+        named.append(("positions", positions, (torch.int32,), (*planes, B, N), True))
     if workspace is not None:
         named.append(("workspace", workspace, (torch.uint8,), workspace.shape, True))
     return named
@@ -467,15 +469,26 @@ def _norm_rope_tables(wq, wk, cos, sin):
     return w_bf16, rows, 2 * half
 
 
-def _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d):
+def _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d, axes=None):
     """Are the tensors the two directions share as they should be?"""
     import torch
     return ((wq is None or (wk.dtype == wq.dtype and wq.shape == wk.shape == (d,) and wq.is_contiguous()
                             and wk.is_contiguous()))
             and (cos is None or (cos.dtype == sin.dtype == torch.float32 and cos.shape == sin.shape
                                  and cos.is_contiguous() and sin.is_contiguous()))
-            and (positions is None or (positions.dtype == torch.int32 and positions.shape == (B, N)
-                                       and positions.is_contiguous())))
+            and (positions is None or (positions.dtype == torch.int32 and positions.is_contiguous()
+                                       and positions.shape[-2:] == (B, N)
+                                       and len(positions.shape) == (2 if axes is None else 3))))
+
+
+def _axes(axes, positions, rot):
+    """The C arguments for the axes: the bytes, one a pair, and how many planes the positions have."""
+    if positions is None:
+        raise ValueError("positions are needed for a rotation by axes: int32 [axes, B, N]")
+    axes = bytes(axes)
+    if 2 * len(axes) != rot:
+        raise ValueError(f"axes has {len(axes)} entries, expected one for each of the {rot // 2} rotated pairs")
+    return axes, positions.shape[0]
 
 
 def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved: bool = False,
@@ -486,6 +499,17 @@ def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, int
     wq, wk None: no norm. cos, sin (rope_tables) None: no rotation. v_in, v
     None: no values. positions None: token n is at position n.
     """
+    _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, None, q, k, v, interleaved, eps, stream)
+
+
+def fa_norm_rope_axes_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v, interleaved: bool = False,
+                          eps: float = 1e-6, stream=None) -> None:
+    """fa_norm_rope_axes_fwd of the C ABI: fa_norm_rope_fwd with positions int32 [axes, B, N] and axes, a sequence
+    of whole numbers (or bytes, which need no conversion): the axis of each of the rot / 2 pairs."""
+    _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v, interleaved, eps, stream)
+
+
+def _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v, interleaved, eps, stream):
     import torch
     bf = torch.bfloat16
     qs, ks = q_in.shape, k_in.shape
@@ -501,15 +525,18 @@ def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, int
             and ks == (B, Hkv, N, d) and sq[3] == sk[3] == 1 and q.is_contiguous() and k.is_contiguous()
             and (v is None or (v_in.dtype == v.dtype == bf and v_in.shape == v.shape == ks and sv[3] == 1
                                and v.is_contiguous()))
-            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d)
+            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d, axes)
             and _devices(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v) == {torch.cuda.current_device()}):
         _refuse(_norm_rope_named(B, Hq, Hkv, N, d, (("q", q), ("k", k), ("v", v)),
                                  (("q_in", q_in), ("k_in", k_in), ("v_in", v_in)), (("wq", wq), ("wk", wk)), cos, sin,
-                                 positions, (), None))
-    check("fa_norm_rope_fwd", load().fa_norm_rope_fwd(
+                                 positions, (), None, axes))
+    name, by_axes = "fa_norm_rope_fwd", ()
+    if axes is not None:
+        name, by_axes = "fa_norm_rope_axes_fwd", _axes(axes, positions, rot)
+    check(name, getattr(load(), name)(
         q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(wq), _ptr(wk), w_bf16,
-        _ptr(cos), _ptr(sin), rows, _ptr(positions), q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d, rot,
-        1 if interleaved else 0, eps, _stream_handle(stream)))
+        _ptr(cos), _ptr(sin), rows, _ptr(positions), *by_axes, q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d,
+        rot, 1 if interleaved else 0, eps, _stream_handle(stream)))
 
 
 def fa_norm_rope_bwd_workspace_size(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
@@ -524,6 +551,19 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
 
     Without weights q_in, k_in, dwq, dwk and workspace are not used.
     """
+    _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, None, dq_in, dk_in, dv_in, dwq, dwk, workspace,
+                   interleaved, eps, stream)
+
+
+def fa_norm_rope_axes_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq_in, dk_in, dv_in, dwq, dwk,
+                          workspace, interleaved: bool = False, eps: float = 1e-6, stream=None) -> None:
+    """fa_norm_rope_axes_bwd of the C ABI: fa_norm_rope_bwd with positions and axes as fa_norm_rope_axes_fwd."""
+    _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq_in, dk_in, dv_in, dwq, dwk, workspace,
+                   interleaved, eps, stream)
+
+
+def _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq_in, dk_in, dv_in, dwq, dwk, workspace,
+                   interleaved, eps, stream):
     import torch
     bf = torch.bfloat16
     qs, ks = dq.shape, dk.shape
@@ -545,18 +585,101 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
             and (wq is None or (q_in.dtype == k_in.dtype == bf and q_in.shape == qs and k_in.shape == ks
                                 and xq[3] == xk[3] == 1 and dwq.dtype == dwk.dtype == torch.float32
                                 and dwq.shape == dwk.shape == (d,) and dwq.is_contiguous() and dwk.is_contiguous()))
-            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d)
+            and _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d, axes)
             and _bytes(workspace)
             and _devices(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in, dk_in, dv_in, dwq, dwk,
                          workspace) == {torch.cuda.current_device()}):
         _refuse(_norm_rope_named(B, Hq, Hkv, N, d, (("dq", dq), ("dk", dk), ("dv", dv)),
                                  (("dq_in", dq_in), ("dk_in", dk_in), ("dv_in", dv_in), ("q_in", q_in), ("k_in", k_in)),
-                                 (("wq", wq), ("wk", wk)), cos, sin, positions, (("dwq", dwq), ("dwk", dwk)), workspace))
-    check("fa_norm_rope_bwd", load().fa_norm_rope_bwd(
+                                 (("wq", wq), ("wk", wk)), cos, sin, positions, (("dwq", dwq), ("dwk", dwk)), workspace,
+                                 axes))
+    name, by_axes = "fa_norm_rope_bwd", ()
+    if axes is not None:
+        name, by_axes = "fa_norm_rope_axes_bwd", _axes(axes, positions, rot)
+    check(name, getattr(load(), name)(
         dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), _Strides(*xq[:3], *xk[:3]), _ptr(wq), _ptr(wk),
-        w_bf16, _ptr(cos), _ptr(sin), rows, _ptr(positions), dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in),
+        w_bf16, _ptr(cos), _ptr(sin), rows, _ptr(positions), *by_axes, dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in),
         _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(dwq), _ptr(dwk), B, Hq, Hkv, N, d, rot, 1 if interleaved else 0, eps,
         *_ws(workspace), _stream_handle(stream)))
+
+
+def fa_packed_plan_size(B: int, rows: int) -> int:
+    return int(load().fa_packed_plan_size(B, rows))
+
+
+def fa_packed_plan(cu_seqlens, rows: int, causal: bool, plan, stream=None) -> None:
+    """fa_packed_plan of the C ABI: list the work of a batch of packed sequences, rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 of `rows` (int32 [B + 1]), into plan (a CUDA uint8 tensor of at least
+    fa_packed_plan_size(B, rows) bytes)."""
+    import torch
+    if not (cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] > 0
+            and cu_seqlens.is_contiguous() and plan.dtype == torch.uint8 and plan.is_contiguous()
+            and _devices(cu_seqlens, plan) == {torch.cuda.current_device()}):
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be an int32 [B + 1] tensor")
+        _refuse((("cu_seqlens", cu_seqlens, (torch.int32,), cu_seqlens.shape, True),
+                 ("plan", plan, (torch.uint8,), plan.shape, True)))
+    check("fa_packed_plan", load().fa_packed_plan(cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, rows,
+                                                  1 if causal else 0, *_ws(plan), _stream_handle(stream)))
+
+
+_RowStrides4, _RowStrides5, _RowStrides3 = ctypes.c_longlong * 8, ctypes.c_longlong * 10, ctypes.c_longlong * 6
+
+
+def _packed_dims(q, k, plan, rows_of_k, lse, *rest):
+    """(rows, Hq, Hkv, d) of a call over packed sequences, after the checks of its tensors: rest and
+    rows_of_k are (name, tensor) of q's and of k's shape."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("expected [rows, H, d] tensors")
+    rows, Hq, d = qs = q.shape
+    Hkv, ks, bf = k.shape[1], (rows, k.shape[1], d), torch.bfloat16
+    if Hkv < 1 or Hq % Hkv != 0:
+        raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
+    of_q, of_k = [t for _, t in rest], [t for _, t in rows_of_k]
+    if not (q.dtype == bf and all([t.dtype == bf and t.shape == qs and t.stride(2) == 1 for t in of_q])
+            and all([t.dtype == bf and t.shape == ks and t.stride(2) == 1 for t in of_k]) and q.stride(2) == 1
+            and lse.dtype == torch.float32 and lse.shape == (Hq, rows) and lse.is_contiguous()
+            and plan.dtype == torch.uint8 and plan.is_contiguous()
+            and _devices(q, plan, lse, *of_q, *of_k) == {torch.cuda.current_device()}):
+        _refuse([("q", q, (bf,), qs, False)] + [(n, t, (bf,), qs, False) for n, t in rest]
+                + [(n, t, (bf,), ks, False) for n, t in rows_of_k]
+                + [("lse", lse, (torch.float32,), (Hq, rows), True), ("plan", plan, (torch.uint8,), plan.shape, True)])
+    return rows, Hq, Hkv, d
+
+
+def fa_fwd_packed(q, k, v, o, lse, plan, causal: bool, scale: float, fill: bool = False, stream=None) -> None:
+    """fa_fwd_packed of the C ABI: q, o [rows, Hq, d], k, v [rows, Hkv, d] with any strides and contiguous
+    last dimension (views of a packed projection), lse float32 [Hq, rows]; plan a PackedPlan (or the
+    tensor that fa_packed_plan filled) of the same rows. fill: zeros in the rows of no sequence."""
+    plan = getattr(plan, "buffer", plan)
+    rows, Hq, Hkv, d = _packed_dims(q, k, plan, (("k", k), ("v", v)), lse, ("o", o))
+    check("fa_fwd_packed", load().fa_fwd_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _RowStrides4(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), o.data_ptr(), lse.data_ptr(),
+        plan.data_ptr(), rows, Hq, Hkv, d, 1 if causal else 0, scale, 1 if fill else 0, _stream_handle(stream)))
+
+
+def fa_bwd_packed_workspace_size(rows: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().fa_bwd_packed_workspace_size(rows, Hq, Hkv, d))
+
+
+def fa_bwd_packed(q, k, v, o, lse, do, dq, dk, dv, plan, causal: bool, scale: float, workspace, fill: bool = False,
+                  stream=None) -> None:
+    """fa_bwd_packed of the C ABI: q, o, do, dq [rows, Hq, d] and k, v, dk, dv [rows, Hkv, d] with any strides
+    and contiguous last dimension (dq, dk, dv may be the views of one packed gradient), lse and plan as
+    in the forward, workspace a CUDA uint8 tensor of at least fa_bwd_packed_workspace_size() bytes."""
+    plan = getattr(plan, "buffer", plan)
+    rows, Hq, Hkv, d = _packed_dims(q, k, plan, (("k", k), ("v", v), ("dk", dk), ("dv", dv)), lse, ("o", o), ("do", do),
+                                    ("dq", dq))
+    if not (_bytes(workspace) and _devices(q, workspace) == {q.get_device()}):
+        _refuse((("workspace", workspace, (workspace.dtype,) if _bytes(workspace) else (), workspace.shape, True),))
+    check("fa_bwd_packed", load().fa_bwd_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+        _RowStrides5(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2], *do.stride()[:2]),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _RowStrides3(*dq.stride()[:2], *dk.stride()[:2], *dv.stride()[:2]),
+        plan.data_ptr(), rows, Hq, Hkv, d, 1 if causal else 0, scale, 1 if fill else 0, *_ws(workspace),
+        _stream_handle(stream)))
 
 
 def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, *rows):
@@ -754,21 +877,78 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
     return dq, dk, dv
 
 
+class PackedPlan:
+    """Where the sequences of a packed batch lie, for forward_packed and backward_packed.
+
+    cu_seqlens: int32 [B + 1] on the device; sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the
+    `rows` rows of q, k, v. Make one for each batch and use it in every layer and both directions, on any
+    stream that is ordered behind the one it was made on. `update` takes the next batch's lengths into the
+    same memory, so that a captured graph of a step can be replayed with them.
+    """
+
+    def __init__(self, cu_seqlens, rows: int, causal: bool = True, stream=None):
+        import torch
+        self.rows, self.causal, self.B = rows, causal, cu_seqlens.shape[0] - 1
+        with _on_stream(stream):
+            self.buffer = torch.empty(max(1, fa_packed_plan_size(max(0, self.B), max(0, rows))), dtype=torch.uint8,
+                                      device=cu_seqlens.device)
+        fa_packed_plan(cu_seqlens, rows, causal, self.buffer, stream)
+
+    def update(self, cu_seqlens, stream=None) -> None:
+        """List the work of other lengths of the same number of sequences (or fewer) and rows."""
+        fa_packed_plan(cu_seqlens, self.rows, self.causal, self.buffer, stream)
+
+
+def forward_packed(q, k, v, plan, causal: bool | None = None, scale: float | None = None, stream=None):
+    """O [rows, Hq, d] (bf16) and L [Hq, rows] (fp32) of packed sequences (fa_fwd_packed): q [rows, Hq, d], k, v
+    [rows, Hkv, d], plan a PackedPlan, whose mask is taken unless `causal` is given. Rows of no sequence
+    become zeros."""
+    import torch
+    rows, Hq, d = q.shape
+    with _on_stream(stream):
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
+    fa_fwd_packed(q, k, v, o, lse, plan, plan.causal if causal is None else causal,
+                  default_scale(d) if scale is None else scale, True, stream)
+    return o, lse
+
+
+def backward_packed(q, k, v, o, lse, do, plan, causal: bool | None = None, scale: float | None = None, out=None,
+                    workspace=None, stream=None):
+    """Run fa_bwd_packed on forward_packed's outputs; returns (dq, dk, dv), zeros in the rows of no sequence.
+
+    out: (dq, dk, dv) to write, e.g. the views of one packed gradient; None allocates contiguous ones.
+    """
+    import torch
+    rows, Hq, d = q.shape
+    with _on_stream(stream):
+        if out is None:
+            out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in (q, k, v))
+        if workspace is None:
+            workspace = torch.empty(max(1, fa_bwd_packed_workspace_size(rows, Hq, int(k.shape[1]), d)),
+                                    dtype=torch.uint8, device=q.device)
+    fa_bwd_packed(q, k, v, o, lse, do, *out, plan, plan.causal if causal is None else causal,
+                  default_scale(d) if scale is None else scale, workspace, True, stream)
+    return out
+
+
 def norm_rope(q_in, k_in, v_in=None, wq=None, wk=None, cos=None, sin=None, positions=None, interleaved: bool = False,
-              eps: float = 1e-6, stream=None):
+              eps: float = 1e-6, stream=None, axes=None):
     """Allocate q, k (and v) as [B, H, N, d] with torch and run fa_norm_rope_fwd: what `forward` and
-    the cache take, from the views of a packed projection."""
+    the cache take, from the views of a packed projection. With axes (the axis of each rotated pair) and
+    positions [axes, B, N], fa_norm_rope_axes_fwd."""
     import torch
     with _on_stream(stream):
         q, k = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) for x in (q_in, k_in))
         v = None if v_in is None else torch.empty(v_in.shape, dtype=torch.bfloat16, device=v_in.device)
-    fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved, eps, stream)
+    _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v, interleaved, eps, stream)
     return q, k, v
 
 
 def norm_rope_backward(dq, dk, dv, q_in, k_in, wq=None, wk=None, cos=None, sin=None, positions=None, out=None,
-                       interleaved: bool = False, eps: float = 1e-6, workspace=None, stream=None):
-    """Run fa_norm_rope_bwd on `backward`'s dq, dk, dv; returns (dq_in, dk_in, dv_in, dwq, dwk).
+                       interleaved: bool = False, eps: float = 1e-6, workspace=None, stream=None, axes=None):
+    """Run fa_norm_rope_bwd (fa_norm_rope_axes_bwd with axes) on `backward`'s dq, dk, dv; returns (dq_in, dk_in,
+    dv_in, dwq, dwk).
 
     out: (dq_in, dk_in, dv_in) to write, e.g. the views of one packed gradient;
     None allocates contiguous ones. dwq, dwk are float32 (None without weights).
@@ -784,8 +964,8 @@ def norm_rope_backward(dq, dk, dv, q_in, k_in, wq=None, wk=None, cos=None, sin=N
             if workspace is None:
                 workspace = torch.empty(max(1, fa_norm_rope_bwd_workspace_size(B, Hq, int(dk.shape[1]), N, d)),
                                         dtype=torch.uint8, device=dq.device)
-    fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, *out, dwq, dwk, workspace, interleaved, eps,
-                     stream)
+    _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, *out, dwq, dwk, workspace, interleaved,
+                   eps, stream)
     return (*out, dwq, dwk)
 
 

@@ -68,6 +68,19 @@ _SIGNATURES = {
     "fa_norm_rope_bwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _vp, _vp,
                                   _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
                                   _vp, ctypes.c_size_t, _vp]),
+    "fa_norm_rope_axes_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _vp, ctypes.c_char_p, _c_int,
+                                       _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
+                                       _vp]),
+    "fa_norm_rope_axes_bwd": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _vp,
+                                       ctypes.c_char_p, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                                       _c_int, _c_int, _c_int, _c_int, _c_float, _vp, ctypes.c_size_t, _vp]),
+    "fa_packed_plan_size": (ctypes.c_size_t, [_c_int, _c_int]),
+    "fa_packed_plan": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, ctypes.c_size_t, _vp]),
+    "fa_fwd_packed": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
+                               _c_int, _vp]),
+    "fa_bwd_packed_workspace_size": (ctypes.c_size_t, [_c_int, _c_int, _c_int, _c_int]),
+    "fa_bwd_packed": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                               _c_int, _c_int, _c_float, _c_int, _vp, ctypes.c_size_t, _vp]),
     "fa_kv8_append": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                _c_int, _c_int, _vp]),
     "fa_kv8_advance": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),

@@ -151,13 +151,6 @@ bool make_map_f32_acc(CUtensorMap* m, void* base, int BH, int Npad, int d) {
 }
 
 
-// Grouped K/V heads: Hkv >= 1 dividing Hq (nothing to check when Hq == 0).
-fa_status_t check_heads(int Hq, int Hkv) {
-  if (Hkv < 0) return FA_ERR_INVALID_ARG;
-  if (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
 int round_up_128(int n) { return (n + 127) / 128 * 128; }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -262,6 +255,28 @@ int choose_kv_chunks(long long BHkv, int g, int N, int d, int causal, int sms, s
 }
 
 }  // namespace
+
+// Grouped K/V heads: Hkv >= 1 dividing Hq (nothing to check when Hq == 0).
+fa_status_t check_heads(int Hq, int Hkv) {
+  if (Hkv < 0) return FA_ERR_INVALID_ARG;
+  if (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+bool make_rows_map(CUtensorMap* m, const void* base, int rows, int heads, int d, const long long (&strides)[2],
+                   unsigned box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  // a dimension of size 1 may have any stride: nothing is stepped over
+  cuuint64_t bytes[2] = {static_cast<cuuint64_t>(rows > 1 ? strides[0] : d) * 2,
+                         static_cast<cuuint64_t>(heads > 1 ? strides[1] : d) * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, bytes, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool make_cache_map(CUtensorMap* m, const void* base, int d, int page, long long slots) {
   auto enc = encode_fn();

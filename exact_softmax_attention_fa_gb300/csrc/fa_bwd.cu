@@ -51,6 +51,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -104,10 +105,11 @@ struct BwdShared {
 // accumulate over all of them. Causal items are numbered most-work-first (key
 // tile j meets T - j query tiles per head); non-causal items of one chunk are
 // adjacent (Q/dO reuse in L2).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 struct BwdWork {
   int bh, c, j, i0, T, nq, gs, q0;
-  __device__ BwdWork(int item, int BHkv, int N, int g, int chunks) {
+  __device__ BwdWork(int item, const BwdLaunch& p) {
+    const int BHkv = p.BHkv, N = p.N, g = p.group, chunks = p.chunks;
     T = (N + 127) / 128;
     int unit;  // bh * chunks + c
     if (CAUSAL) {
@@ -124,6 +126,9 @@ struct BwdWork {
     i0 = CAUSAL ? j : 0;
     nq = T - i0;
   }
+  // the sequence's length and first row
+  __device__ __forceinline__ int len(const BwdLaunch& p) const { return p.N; }
+  static constexpr int row0 = 0;
   __device__ int n_iter() const { return gs * nq; }
   // (query head, query tile) of a step of the query stream, advanced in order
   // (no per-step division on the softmax warps' path)
@@ -138,6 +143,50 @@ struct BwdWork {
     }
   }
 };
+
+// The same over packed sequences: an entry of the plan's list is a sequence's
+// key tile j, every K/V head and chunk of it an item. The list is ordered by
+// the query tiles that see a key tile.
+template <bool CAUSAL>
+struct BwdWork<CAUSAL, true> {
+  int bh, c, j, i0, T, nq, gs, q0, row0, n;
+  __device__ BwdWork(int item, const BwdLaunch& p) {
+    const uint32_t chunks = __ldg(p.sched + 4), units = p.BHkv * chunks;
+    const int e = static_cast<int>(static_cast<uint32_t>(item) / units);
+    const uint32_t unit = static_cast<uint32_t>(item) - e * units;
+    const int4 x = __ldg(packed_tiles(p.plan) + e);
+    row0 = x.x;
+    n = x.y;
+    T = (n + 127) >> 7;
+    j = CAUSAL ? T - 1 - x.z : x.z;
+    bh = static_cast<int>(unit / chunks);
+    c = static_cast<int>(unit - bh * chunks);
+    gs = p.group / static_cast<int>(chunks);
+    q0 = bh * p.group + c * gs;
+    i0 = CAUSAL ? j : 0;
+    nq = T - i0;
+  }
+  __device__ __forceinline__ int len(const BwdLaunch&) const { return n; }
+  __device__ int n_iter() const { return gs * nq; }
+  struct Pos {
+    int bh, i;
+  };
+  __device__ Pos first() const { return Pos{q0, i0}; }
+  __device__ void advance(Pos& p) const {
+    if (++p.i == T) {
+      p.i = i0;
+      ++p.bh;
+    }
+  }
+};
+
+template <bool RAG>
+__device__ __forceinline__ int bwd_total_items(const BwdLaunch& p) {
+  if constexpr (RAG)
+    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BHkv * static_cast<int>(__ldg(p.sched + 4)) : 0;
+  else
+    return p.BHkv * p.chunks * ((p.N + 127) / 128);
+}
 
 // Dynamic schedule (fa_kernel_common.cuh): items are claimed from sched[0..1]
 // of the workspace, so CTAs that run ahead take more items and causal items
@@ -255,7 +304,7 @@ __global__ void __launch_bounds__(256) bwd_post_kernel(const float* __restrict__
 // V_j once every MMA of the previous item has completed (they read the old
 // K_j/V_j), then the remaining Q_i/dO_i tiles through the ring (global tile
 // counter g).
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG>
 __device__ void bwd_load_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQ,
                               uint8_t* sdO) {
   using C = BwdCfg<HD>;
@@ -263,35 +312,34 @@ __device__ void bwd_load_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, ui
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
   tma_prefetch_desc(&p.tmdO);
-  tma_prefetch_desc(&p.tmdQacc);
-  const int T = (p.N + 127) / 128;
-  const int total = p.BHkv * p.chunks * T;
+  if (!RAG) tma_prefetch_desc(&p.tmdQacc);
+  const int total = bwd_total_items<RAG>(p);
   const uint64_t lim = p.wait_limit_ns;
   int g = 0, items = 0, issued = 0, kv_issued = 0;
   bool aborted = false;
-  auto load_qdo = [&](int gg, int i, int bh) -> bool {
+  auto load_qdo = [&](int gg, int row, int bh) -> bool {
     const int s = gg % C::QST;
     if (gg >= C::QST && !mbar_wait(&sh.qdo_empty[s], ((gg / C::QST) - 1) & 1, &sh.abort_flag, lim)) return false;
     mbar_arrive_expect_tx(&sh.qdo_full[s], 2 * C::TILE_BYTES);
 #pragma unroll
     for (int c = 0; c < C::CHUNKS; ++c) {
-      tma_load_3d(sQ + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmQ, &sh.qdo_full[s], c * 64, i * 128, bh);
-      tma_load_3d(sdO + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmdO, &sh.qdo_full[s], c * 64, i * 128, bh);
+      tma_load_3d(sQ + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmQ, &sh.qdo_full[s], c * 64, row, bh);
+      tma_load_3d(sdO + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmdO, &sh.qdo_full[s], c * 64, row, bh);
     }
     ++issued;
     return true;
   };
-  int item = blockIdx.x;  // the grid never exceeds the item count
+  int item = blockIdx.x;
   while (!aborted) {
     if (!publish_item(sh, items, item, lim)) {
       aborted = true;
       break;
     }
     if (item >= total) break;
-    const BwdWork<CAUSAL> wk(item, p.BHkv, p.N, p.group, p.chunks);
+    const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
-    typename BwdWork<CAUSAL>::Pos pos = wk.first();
-    if (!load_qdo(g, pos.i, pos.bh)) {
+    typename BwdWork<CAUSAL, RAG>::Pos pos = wk.first();
+    if (!load_qdo(g, wk.row0 + pos.i * 128, pos.bh)) {
       aborted = true;
       break;
     }
@@ -303,14 +351,14 @@ __device__ void bwd_load_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, ui
       mbar_arrive_expect_tx(&sh.kv_full, 2 * C::TILE_BYTES);
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c) {
-        tma_load_3d(sK + c * C::CHUNK_BYTES, &p.tmK, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
-        tma_load_3d(sV + c * C::CHUNK_BYTES, &p.tmV, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
+        tma_load_3d(sK + c * C::CHUNK_BYTES, &p.tmK, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
+        tma_load_3d(sV + c * C::CHUNK_BYTES, &p.tmV, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
       }
       ++kv_issued;
     }
     for (int n = 1; n < n_iter; ++n) {
       wk.advance(pos);
-      if (!load_qdo(g + n, pos.i, pos.bh)) {
+      if (!load_qdo(g + n, wk.row0 + pos.i * 128, pos.bh)) {
         aborted = true;
         break;
       }
@@ -337,7 +385,7 @@ __device__ void bwd_load_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, ui
 //   dP^T(n+1) -> B        after the dQ_n drain
 // An item's first dV/dK (which overwrite the accumulators) wait until the
 // previous item's epilogue has read dK/dV out of TMEM.
-template <int HD, bool CAUSAL, bool DQ>
+template <int HD, bool CAUSAL, bool DQ, bool RAG>
 __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQ,
                              uint8_t* sdO, uint8_t* sDS, uint32_t tmem) {
   using C = BwdCfg<HD>;
@@ -347,11 +395,22 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
   const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV), q_addr = smem_u32(sQ), do_addr = smem_u32(sdO),
                  ds_addr = smem_u32(sDS);
   const uint64_t lim = p.wait_limit_ns;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BHkv * p.chunks * T;
+  const int total = bwd_total_items<RAG>(p);
+
+  // Packed sequences: the whole warp walks the items (it clears the rows of Q
+  // and dO behind a sequence's last query), one lane issues.
+  const bool lead = !RAG || lane_id() == 0;
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
+    return RAG ? __all_sync(0xffffffffu, ok) : ok;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) umma_commit(bar);
+  };
 
   // D[tmem] = A (128 x HD, K-major) * B (128 x HD, K-major)^T
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_addr) {
+    if (!lead) return;
     const uint64_t ad = make_smem_desc_sw128(a_addr, 16, 1024), bd = make_smem_desc_sw128(b_addr, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
@@ -361,60 +420,81 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+    if (lead) drain_mmas(&sh.mma_drain, lim);
   };
 
   int g = 0, items = 0;
   while (true) {
-    const int item = take_item(sh, items, lim);
+    const int item = RAG ? take_item_warp(sh, items, lim) : take_item(sh, items, lim);
     if (item < 0) return fail();
     if (item >= total) break;
-    const BwdWork<CAUSAL> wk(item, p.BHkv, p.N, p.group, p.chunks);
+    const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int s0 = g % C::QST;
-    if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) ||
-        !mbar_wait(&sh.qdo_full[s0], (g / C::QST) & 1, &sh.abort_flag, lim))
+    typename BwdWork<CAUSAL, RAG>::Pos pos = wk.first();
+    // Steps of 16 queries of tile i in the products over queries. A sequence's
+    // last tile ends in rows of the next one, whatever they hold: whole steps of
+    // them are left out, and those in the last step taken are cleared (their
+    // weights are 0, but 0 * NaN).
+    auto take_tile = [&](int slot, int i) -> int {
+      if constexpr (RAG) {
+        const int held = wk.n - i * 128;
+        if (held >= 128) return 8;
+        const int steps = (held + 15) >> 4;
+        clear_rows<C::CHUNKS, C::CHUNK_BYTES>(q_addr + slot * C::TILE_BYTES, held, 16 * steps);
+        clear_rows<C::CHUNKS, C::CHUNK_BYTES>(do_addr + slot * C::TILE_BYTES, held, 16 * steps);
+        return steps;
+      }
+      return 8;
+    };
+    if (!wait(&sh.kv_full, items & 1) ||
+        !wait(&sh.qdo_full[s0], (g / C::QST) & 1))
       return fail();
+    int steps = take_tile(s0, pos.i), next_steps = 8;
     // Region A held the previous item's last P^T, region B its last dQ.
-    if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
+    if (g > 0 && !wait(&sh.pv_done, (g - 1) & 1)) return fail();
     tc_fence_after_sync();
     issue_sq(C::REG_A, k_addr, q_addr + s0 * C::TILE_BYTES);  // S^T(first)
-    umma_commit(&sh.s_full);
-    if (DQ && g > 0 && !mbar_wait(&sh.dq_free, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
+    commit(&sh.s_full);
+    if (DQ && g > 0 && !wait(&sh.dq_free, (g - 1) & 1)) return fail();
     tc_fence_after_sync();
     issue_sq(C::REG_B, v_addr, do_addr + s0 * C::TILE_BYTES);  // dP^T(first)
-    umma_commit(&sh.dp_full);
+    commit(&sh.dp_full);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const int s = g % C::QST;
       const bool has_next = n + 1 < n_iter;
       const int s1 = (g + 1) % C::QST;
       const uint32_t qa = q_addr + s * C::TILE_BYTES, doa = do_addr + s * C::TILE_BYTES;
-      if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
-      if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.pa_ready, g & 1)) return fail();
+      if (n == 0 && items > 0 && !wait(&sh.acc_free, (items - 1) & 1)) return fail();
       tc_fence_after_sync();
       // dV += P^T dO_n; P^T (bf16) sits in columns [0,32) and [64,96) of region A
       const uint64_t dod = make_smem_desc_sw128(doa, C::CHUNK_BYTES, 1024);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dod, ks * 2048), kIdescAcc,
+        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DV_COL, tmem + C::REG_A + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dod, ks * 2048), kIdescAcc,
                 (n > 0 || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.pv_done);
+      commit(&sh.pv_done);
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
-        if (!mbar_wait(&sh.qdo_full[s1], ((g + 1) / C::QST) & 1, &sh.abort_flag, lim)) return fail();
-        if (!mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
+        if (!wait(&sh.qdo_full[s1], ((g + 1) / C::QST) & 1)) return fail();
+        if constexpr (RAG) {
+          wk.advance(pos);
+          next_steps = take_tile(s1, pos.i);
+        }
+        if (!wait(&sh.pv_done, g & 1)) return fail();
         tc_fence_after_sync();
         issue_sq(C::REG_A, k_addr, q_addr + s1 * C::TILE_BYTES);
-        umma_commit(&sh.s_full);
+        commit(&sh.s_full);
       }
-      if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.ds_ready, g & 1)) return fail();
       tc_fence_after_sync();
       // dK += dS^T Q_n
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qa, C::CHUNK_BYTES, 1024);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048),
+        if (lead && (!RAG || ks < steps)) umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048),
                 kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
       if constexpr (DQ) {
         // dQ_n into region B. d = 128: dQ_n^T = K_j^T dS^T (head-dim columns on
@@ -431,22 +511,23 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
           else
             umma_ss(tmem + C::REG_B, ds_mn, k_mn, kIdescDq, ks > 0 ? 1u : 0u);
         }
-        umma_commit(&sh.dq_full);
+        commit(&sh.dq_full);
       }
-      umma_commit(&sh.qdo_empty[s]);
+      commit(&sh.qdo_empty[s]);
       if (has_next) {
-        if (DQ && !mbar_wait(&sh.dq_free, g & 1, &sh.abort_flag, lim)) return fail();
+        if (DQ && !wait(&sh.dq_free, g & 1)) return fail();
         tc_fence_after_sync();
         issue_sq(C::REG_B, v_addr, do_addr + s1 * C::TILE_BYTES);  // dP^T(n+1) over the drained dQ_n
-        umma_commit(&sh.dp_full);
+        commit(&sh.dp_full);
       }
+      if constexpr (RAG) steps = next_steps;
     }
-    umma_commit(&sh.acc_done);
+    commit(&sh.acc_done);
     ++items;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  drain_mmas(&sh.mma_drain, lim);
+  if (lead) drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w (w = 0, 1) owns query columns [64w, 64w + 64) of every tile:
@@ -456,7 +537,7 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
 // the drain's reductions overlap dP^T(n+1) and dV(n+1). After an item's last
 // tile, warpgroup 0 writes dK_j and warpgroup 1 dV_j straight from TMEM to
 // global memory while the MMA warp already starts the next item.
-template <int HD, bool CAUSAL, bool DQ>
+template <int HD, bool CAUSAL, bool DQ, bool RAG>
 __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS, float* sLD, uint8_t* sDQ,
                                  uint32_t tmem, int w) {
   using C = BwdCfg<HD>;
@@ -471,8 +552,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   const uint32_t bar_id = 1 + w;
   const uint32_t tA = tmem + lane_base + C::REG_A + 64 * w;
   const uint32_t tB = tmem + lane_base + C::REG_B + 64 * w;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BHkv * p.chunks * T;
+  const int total = bwd_total_items<RAG>(p);
   bool alive = true;
   constexpr bool kPrefetchStats = !DQ && HD == 128;
   // P^T of the current tile as the bf16 pairs written to TMEM, kept from
@@ -481,7 +561,14 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
 
   // L2 / D of query tile i of head bh for this warpgroup's 64 columns:
   // thread r < 64 loads L2[r], thread r >= 64 loads D[r - 64] * scale.
-  auto fetch_ld = [&](int bh, int i) -> float {
+  // Queries behind a packed sequence's last one get L2 = +inf (weight 0) and D = 0.
+  auto fetch_ld = [&](const BwdWork<CAUSAL, RAG>& wk, int bh, int i) -> float {
+    if constexpr (RAG) {
+      const int q = i * 128 + 64 * w + (r & 63);
+      if (q >= wk.n) return r < 64 ? INFINITY : 0.f;
+      const size_t at = static_cast<size_t>(bh) * p.N + wk.row0 + q;
+      return r < 64 ? __ldg(p.lse2 + at) : __ldg(p.D + at) * sc;
+    }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * 128 + 64 * w;
     return r < 64 ? __ldg(p.lse2 + row + r) : __ldg(p.D + row + (r - 64)) * sc;
   };
@@ -495,7 +582,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   // log2e - L2), written back to TMEM as bf16. After a timed-out wait a warp
   // stops working but still passes every named barrier, so the warpgroup's
   // barrier counts stay matched.
-  auto phase_a = [&](const BwdWork<CAUSAL>& wk, int i, int g) {
+  auto phase_a = [&](const BwdWork<CAUSAL, RAG>& wk, int i, int g) {
     // The 64 base-2 logsumexps of this warpgroup's queries, read from smem
     // while S^T is still being computed (read in the loop they sit on the
     // phase's critical path: measured ~800 of ~1600 cycles at d = 128). Only
@@ -522,8 +609,10 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     }
     // Only the key-tail tile and the causal diagonal tile need masking:
     // query (64w + c) sees key r only if 64w + c >= r.
-    const bool key_valid = wk.j * 128 + r < p.N;
-    const bool masked = !key_valid || (CAUSAL && i == wk.j);
+    const bool key_valid = wk.j * 128 + r < wk.len(p);
+    // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
+    const int c_hi = RAG ? wk.len(p) - i * 128 - 64 * w : 64;
+    const bool masked = !key_valid || (CAUSAL && i == wk.j) || (RAG && c_hi < 64);
     const int c_lo = !key_valid ? 64 : ((CAUSAL && i == wk.j) ? r - 64 * w : 0);
     // Three passes over the row (exponent arguments, exponentials, bf16
     // pairs) give the scheduler long runs of independent instructions.
@@ -542,7 +631,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     if (masked) {
 #pragma unroll
       for (int c = 0; c < 64; ++c)
-        if (c < c_lo) pv[c] = 0.f;
+        if (c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
@@ -553,7 +642,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   };
 
   // ---- phase B: dS^T = P^T o (dP^T - D) * scale -> smem (bf16, swizzled)
-  auto phase_b = [&](int g) {
+  auto phase_b = [&](const BwdWork<CAUSAL, RAG>& wk, int i, int g) {
     // the scaled D values, read from smem while dP^T is still being computed
     // (as the logsumexps in phase A)
     float4 dvv[kPrefetchStats ? 16 : 1];
@@ -584,6 +673,14 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
         const float2 ds23 = fmul2(p23, g23);
         dk[c4 / 2] = pack_bf16x2(ds01.x, ds01.y);
         dk[c4 / 2 + 1] = pack_bf16x2(ds23.x, ds23.y);
+      }
+      if constexpr (RAG) {
+        // dP of queries behind the sequence's last may be infinite or NaN
+        const int held = wk.len(p) - i * 128 - 64 * w - 32 * h;
+        if (held < 32) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -645,14 +742,22 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   // writes key row r, rows past N are skipped. One chunk per group: fp32 TMEM
   // -> bf16 -> dk / dv. Several: the chunk's fp32 partial sum goes to the
   // workspace, and the post kernel adds the chunks in a fixed order.
-  auto epilogue = [&](const BwdWork<CAUSAL>& wk, int items) {
+  auto epilogue = [&](const BwdWork<CAUSAL, RAG>& wk, int items) {
     wait_all(&sh.acc_done, items & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     const int key = wk.j * 128 + r;
     const uint32_t t = tmem + lane_base + (w == 0 ? C::DK_COL : C::DV_COL);
-    const size_t row = static_cast<size_t>(wk.bh) * p.N + key;
-    if (p.chunks == 1) {
-      __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv) + row * HD;
+    const bool written = key < wk.len(p);
+    const size_t row = static_cast<size_t>(wk.bh) * p.N + wk.row0 + key;
+    const int chunks = RAG ? p.group / wk.gs : p.chunks;
+    if (chunks == 1) {
+      __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv);
+      if constexpr (RAG) {
+        const long long* st = w == 0 ? p.dk_strides : p.dv_strides;
+        dst += static_cast<long long>(wk.row0 + key) * st[0] + wk.bh * st[1];
+      } else {
+        dst += row * HD;
+      }
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         uint32_t v[32];
@@ -662,7 +767,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
-        if (key < p.N) {
+        if (written) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             *reinterpret_cast<uint4*>(dst + c + 8 * u) =
@@ -673,7 +778,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
         }
       }
     } else {
-      const size_t part_len = static_cast<size_t>(p.chunks) * p.BHkv * p.N * HD;
+      const size_t part_len = static_cast<size_t>(chunks) * p.BHkv * p.N * HD;
       float* part = p.kv_part + (w == 0 ? 0 : part_len) + (static_cast<size_t>(wk.c) * p.BHkv * p.N + row) * HD;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
@@ -684,7 +789,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
-        if (key < p.N) {
+        if (written) {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             *reinterpret_cast<uint4*>(part + c + 4 * u) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
@@ -710,23 +815,23 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   int item = next_item(0);
   float ld = 0.f;
   if (item < total) {
-    const BwdWork<CAUSAL> wk0(item, p.BHkv, p.N, p.group, p.chunks);
-    ld = fetch_ld(wk0.q0, wk0.i0);
+    const BwdWork<CAUSAL, RAG> wk0(item, p);
+    ld = fetch_ld(wk0, wk0.q0, wk0.i0);
   }
   while (item < total) {
-    const BwdWork<CAUSAL> wk(item, p.BHkv, p.N, p.group, p.chunks);
+    const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     if (items > 0) named_barrier_sync(bar_id, 128);  // the previous item's L2 / D reads are done
     sLD[w * 128 + r] = ld;
     named_barrier_sync(bar_id, 128);
-    typename BwdWork<CAUSAL>::Pos cur = wk.first();
+    typename BwdWork<CAUSAL, RAG>::Pos cur = wk.first();
     phase_a(wk, cur.i, g);
     for (int n = 0; n < n_iter; ++n) {
       const bool has_next = n + 1 < n_iter;
-      typename BwdWork<CAUSAL>::Pos nxt = cur;
+      typename BwdWork<CAUSAL, RAG>::Pos nxt = cur;
       wk.advance(nxt);
-      const float next_ld = has_next ? fetch_ld(nxt.bh, nxt.i) : 0.f;  // lands during phase B
-      phase_b(g + n);
+      const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
+      phase_b(wk, cur.i, g + n);
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         sLD[w * 128 + r] = next_ld;
@@ -738,8 +843,8 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     }
     const int item_next = next_item(items + 1);
     if (item_next < total) {
-      const BwdWork<CAUSAL> wk1(item_next, p.BHkv, p.N, p.group, p.chunks);
-      ld = fetch_ld(wk1.q0, wk1.i0);  // lands during the epilogue
+      const BwdWork<CAUSAL, RAG> wk1(item_next, p);
+      ld = fetch_ld(wk1, wk1.q0, wk1.i0);  // lands during the epilogue
     }
     epilogue(wk, items);
     g += n_iter;
@@ -749,7 +854,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   if (DQ && !C::DQ_T && r == 0) tma_store_wait_all();  // reduce-adds complete before the CTA can exit
 }
 
-template <int HD, bool CAUSAL, bool DQ>
+template <int HD, bool CAUSAL, bool DQ, bool RAG>
 __global__ void __launch_bounds__(kThreads, 1) fa_bwd_kernel(const __grid_constant__ BwdLaunch p) {
   using C = BwdCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
@@ -802,11 +907,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_kernel(const __grid_consta
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) bwd_load_role<HD, CAUSAL>(p, sh, sK, sV, sQ, sdO);
+    if (lane_id() == 0) bwd_load_role<HD, CAUSAL, RAG>(p, sh, sK, sV, sQ, sdO);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
+    if (RAG || lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ, RAG>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
   } else {
-    bwd_softmax_role<HD, CAUSAL, DQ>(p, sh, sDS, sLD, sDQ, tmem, wg);
+    bwd_softmax_role<HD, CAUSAL, DQ, RAG>(p, sh, sDS, sLD, sDQ, tmem, wg);
   }
 
   tc_fence_before_sync();
@@ -826,13 +931,14 @@ cudaError_t launch_pre_t(const BwdLaunch& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int HD, bool CAUSAL, bool DQ>
+template <int HD, bool CAUSAL, bool DQ, bool RAG = false>
 cudaError_t launch_main_t(const BwdLaunch& a, cudaStream_t stream) {
   using C = BwdCfg<HD>;
-  auto kern = fa_bwd_kernel<HD, CAUSAL, DQ>;
+  auto kern = fa_bwd_kernel<HD, CAUSAL, DQ, RAG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int T = (a.N + 127) / 128;
+  // Packed sequences: the plan, on the device, knows how many items there are.
+  const int T = RAG ? a.N : (a.N + 127) / 128;
   const long long items = static_cast<long long>(a.BH) * T;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
@@ -866,6 +972,10 @@ cudaError_t launch_bwd_pre(const BwdLaunch& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_bwd_main(const BwdLaunch& a, cudaStream_t stream) {
+  if (a.plan && a.d == 64)
+    return a.causal ? launch_main_t<64, true, false, true>(a, stream) : launch_main_t<64, false, false, true>(a, stream);
+  if (a.plan && a.d == 128)
+    return a.causal ? launch_main_t<128, true, false, true>(a, stream) : launch_main_t<128, false, false, true>(a, stream);
   switch (a.d) {
     case 64:
       if (a.deterministic)

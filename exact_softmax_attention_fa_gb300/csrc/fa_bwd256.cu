@@ -47,6 +47,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -93,10 +94,13 @@ struct Shared256 {
 // (query head bh*g + t), the 64-row query tiles i0 .. T64-1 (causal:
 // i0 = 2j). Causal items are numbered most-work-first; the two halves of a
 // key tile are adjacent (they read the same query stream).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 struct Work256 {
   int bh, j, h, i0, T64, g;
-  __device__ Work256(int item, int BHkv, int N, int group) {
+  static constexpr int row0 = 0;  // the sequence's first row
+  __device__ __forceinline__ int len(const BwdLaunch& p) const { return p.N; }
+  __device__ Work256(int item, const BwdLaunch& p) {
+    const int BHkv = p.BHkv, N = p.N, group = p.group;
     const int T = (N + 127) / 128;
     T64 = (N + 63) / 64;
     if (CAUSAL) {
@@ -126,7 +130,46 @@ struct Work256 {
   }
 };
 
-__device__ __forceinline__ int total_items256(const BwdLaunch& p) { return p.BHkv * ((p.N + 127) / 128) * 2; }
+// The same over packed sequences: an entry of the plan's list is a sequence's
+// key tile j, both halves of every K/V head of it items.
+template <bool CAUSAL>
+struct Work256<CAUSAL, true> {
+  int bh, j, h, i0, T64, g, row0, n;
+  __device__ __forceinline__ int len(const BwdLaunch&) const { return n; }
+  __device__ Work256(int item, const BwdLaunch& p) {
+    const uint32_t units = 2 * p.BHkv;
+    const int e = static_cast<int>(static_cast<uint32_t>(item) / units);
+    const int rem = item - e * static_cast<int>(units);
+    const int4 x = __ldg(packed_tiles(p.plan) + e);
+    row0 = x.x;
+    n = x.y;
+    T64 = (n + 63) >> 6;
+    j = CAUSAL ? ((n + 127) >> 7) - 1 - x.z : x.z;
+    bh = rem >> 1;
+    h = rem & 1;
+    i0 = CAUSAL ? 2 * j : 0;
+    g = p.group;
+  }
+  __device__ int n_iter() const { return g * (T64 - i0); }
+  struct Pos {
+    int bh, i;
+  };
+  __device__ Pos first() const { return Pos{bh * g, i0}; }
+  __device__ void advance(Pos& p) const {
+    if (++p.i == T64) {
+      p.i = i0;
+      ++p.bh;
+    }
+  }
+};
+
+template <bool RAG>
+__device__ __forceinline__ int total_items256(const BwdLaunch& p) {
+  if constexpr (RAG)
+    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BHkv * 2 : 0;
+  else
+    return p.BHkv * ((p.N + 127) / 128) * 2;
+}
 
 // Smem address of chunk c (0..3, 64 columns of the head dimension) of a
 // query tile's Q (or dO) for an item of half h: in the h half's slot or in
@@ -138,7 +181,7 @@ __device__ __forceinline__ uint32_t half_chunk(uint32_t h_slot, uint32_t o_slot,
 // TMA producer (one thread). Per query tile: Q's h half, Q's other half,
 // dO's other half, dO's h half (the order in which their slots free up);
 // per item K_j and V_j once every MMA of the previous item has completed.
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQh, uint8_t* sQo,
                           uint8_t* sDOh, uint8_t* sDOo) {
   using C = Cfg256;
@@ -146,48 +189,49 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
   tma_prefetch_desc(&p.tmdO);
-  const int total = total_items256(p);
+  const int total = total_items256<RAG>(p);
   const uint64_t lim = p.wait_limit_ns;
   int g = 0, items = 0, kv_issued = 0;
   int issued = 0;  // query tiles whose four half tiles were all issued
   int parts = 0;   // half tiles of tile `issued` issued before an abort (0..3)
   bool aborted = false;
   // the two 64-column chunks of half `half` of a 64-row tile of `map`
-  auto load_half = [&](uint64_t* bar, uint8_t* dst, const CUtensorMap* map, int half, int i, int bh) {
+  auto load_half = [&](uint64_t* bar, uint8_t* dst, const CUtensorMap* map, int half, int row, int bh) {
     mbar_arrive_expect_tx(bar, C::HALF_BYTES);
-    tma_load_3d(dst, map, bar, 128 * half, i * C::BQ, bh);
-    tma_load_3d(dst + C::Q_CHUNK, map, bar, 128 * half + 64, i * C::BQ, bh);
+    tma_load_3d(dst, map, bar, 128 * half, row, bh);
+    tma_load_3d(dst + C::Q_CHUNK, map, bar, 128 * half + 64, row, bh);
   };
-  auto load_tile = [&](int n, const typename Work256<CAUSAL>::Pos& pos, int h) -> bool {
+  auto load_tile = [&](int n, const typename Work256<CAUSAL, RAG>::Pos& pos, int h, int row0) -> bool {
+    const int row = row0 + pos.i * C::BQ;
     const int s = n % C::QH_SLOTS;
     parts = 0;
     if (n >= C::QH_SLOTS && !mbar_wait(&sh.qh_empty[s], ((n / C::QH_SLOTS) - 1) & 1, &sh.abort_flag, lim))
       return false;
-    load_half(&sh.qh_full[s], sQh + s * C::HALF_BYTES, &p.tmQ, h, pos.i, pos.bh);
+    load_half(&sh.qh_full[s], sQh + s * C::HALF_BYTES, &p.tmQ, h, row, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.qo_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.qo_full, sQo, &p.tmQ, 1 - h, pos.i, pos.bh);
+    load_half(&sh.qo_full, sQo, &p.tmQ, 1 - h, row, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.doo_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.doo_full, sDOo, &p.tmdO, 1 - h, pos.i, pos.bh);
+    load_half(&sh.doo_full, sDOo, &p.tmdO, 1 - h, row, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.doh_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.doh_full, sDOh, &p.tmdO, h, pos.i, pos.bh);
+    load_half(&sh.doh_full, sDOh, &p.tmdO, h, row, pos.bh);
     parts = 0;
     ++issued;
     return true;
   };
-  int item = blockIdx.x;  // the grid never exceeds the item count
+  int item = blockIdx.x;
   while (!aborted) {
     if (!publish_item(sh, items, item, lim)) {
       aborted = true;
       break;
     }
     if (item >= total) break;
-    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
+    const Work256<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
-    typename Work256<CAUSAL>::Pos pos = wk.first();
-    if (!load_tile(g, pos, wk.h)) {
+    typename Work256<CAUSAL, RAG>::Pos pos = wk.first();
+    if (!load_tile(g, pos, wk.h, wk.row0)) {
       aborted = true;
       break;
     }
@@ -200,14 +244,14 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
       mbar_arrive_expect_tx(&sh.kv_full, 2 * C::KV_BYTES);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        tma_load_3d(sK + c * C::KV_CHUNK, &p.tmK, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
-        tma_load_3d(sV + c * C::KV_CHUNK, &p.tmV, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
+        tma_load_3d(sK + c * C::KV_CHUNK, &p.tmK, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
+        tma_load_3d(sV + c * C::KV_CHUNK, &p.tmV, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
       }
       ++kv_issued;
     }
     for (int n = 1; n < n_iter; ++n) {
       wk.advance(pos);
-      if (!load_tile(g + n, pos, wk.h)) {
+      if (!load_tile(g + n, pos, wk.h, wk.row0)) {
         aborted = true;
         break;
       }
@@ -237,7 +281,7 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
 }
 
 // One thread issues every MMA (order in the file header).
-template <bool CAUSAL, bool DQ>
+template <bool CAUSAL, bool DQ, bool RAG>
 __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQh, uint8_t* sQo,
                          uint8_t* sDOh, uint8_t* sDOo, uint8_t* sDS, uint32_t tmem) {
   using C = Cfg256;
@@ -247,15 +291,26 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
   const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV), qh_addr = smem_u32(sQh), qo_addr = smem_u32(sQo),
                  doh_addr = smem_u32(sDOh), doo_addr = smem_u32(sDOo), ds_addr = smem_u32(sDS);
   const uint64_t lim = p.wait_limit_ns;
-  const int total = total_items256(p);
+  const int total = total_items256<RAG>(p);
+  // Packed sequences: the whole warp walks the items (it clears the rows of Q
+  // and dO behind a sequence's last query), one lane issues.
+  const bool lead = !RAG || lane_id() == 0;
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
+    return RAG ? __all_sync(0xffffffffu, ok) : ok;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) umma_commit(bar);
+  };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+    if (lead) drain_mmas(&sh.mma_drain, lim);
   };
 
   // D[tmem] = A (128 keys x 256, K-major, resident) * B (64 queries x 256,
   // K-major, in the h and other-half slots)^T, chunks of 64 columns in order.
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_h, uint32_t b_o, int h) {
+    if (!lead) return;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint64_t ad = make_smem_desc_sw128(a_addr + c * C::KV_CHUNK, 16, 1024);
@@ -266,99 +321,119 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
     }
   };
   auto wait_s_operands = [&](int n) -> bool {
-    return mbar_wait(&sh.qh_full[n % C::QH_SLOTS], (n / C::QH_SLOTS) & 1, &sh.abort_flag, lim) &&
-           mbar_wait(&sh.qo_full, n & 1, &sh.abort_flag, lim);
+    return wait(&sh.qh_full[n % C::QH_SLOTS], (n / C::QH_SLOTS) & 1) &&
+           wait(&sh.qo_full, n & 1);
   };
   auto wait_dp_operands = [&](int n) -> bool {
-    return mbar_wait(&sh.doo_full, n & 1, &sh.abort_flag, lim) && mbar_wait(&sh.doh_full, n & 1, &sh.abort_flag, lim);
+    return wait(&sh.doo_full, n & 1) && wait(&sh.doh_full, n & 1);
   };
   auto issue_s = [&](int n, int h) {
     issue_sq(C::REG_S, k_addr, qh_addr + (n % C::QH_SLOTS) * C::HALF_BYTES, qo_addr, h);
-    umma_commit(&sh.s_full);
-    umma_commit(&sh.qo_empty);  // the other half of Q_n is read by S^T(n) only
+    commit(&sh.s_full);
+    commit(&sh.qo_empty);  // the other half of Q_n is read by S^T(n) only
   };
   auto issue_dp = [&](int h) {
     issue_sq(C::REG_DP, v_addr, doh_addr, doo_addr, h);
-    umma_commit(&sh.dp_full);
-    umma_commit(&sh.doo_empty);
+    commit(&sh.dp_full);
+    commit(&sh.doo_empty);
   };
 
   int g = 0, items = 0;
   while (true) {
-    const int item = take_item(sh, items, lim);
+    const int item = RAG ? take_item_warp(sh, items, lim) : take_item(sh, items, lim);
     if (item < 0) return fail();
     if (item >= total) break;
-    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
+    const Work256<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int h = wk.h;
-    if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) || !wait_s_operands(g)) return fail();
+    typename Work256<CAUSAL, RAG>::Pos pos = wk.first();
+    // Steps of 16 queries of tile i in the products over queries (fa_bwd.cu):
+    // the rows behind a sequence's last query are left out, or cleared where a
+    // step holds some of both.
+    auto tile_steps = [&](int i) -> int { return RAG ? min(4, (wk.len(p) - i * C::BQ + 15) >> 4) : 4; };
+    auto clear_tail = [&](uint32_t half_tile, int i) {
+      if constexpr (RAG) {
+        const int held = wk.n - i * C::BQ;
+        if (held < C::BQ) clear_rows<2, C::Q_CHUNK>(half_tile, held, (held + 15) / 16 * 16);
+      }
+    };
+    if (!wait(&sh.kv_full, items & 1) || !wait_s_operands(g)) return fail();
     // S^T overwrites the previous item's last P^T: dV must have read it.
-    if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
+    if (g > 0 && !wait(&sh.pv_done, (g - 1) & 1)) return fail();
     tc_fence_after_sync();
+    clear_tail(qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES, pos.i);
     issue_s(g, h);
     // dP^T overwrites the previous item's last dP^T, which phase B read
     // before ds_ready (waited for in the previous item's last step).
     if (!wait_dp_operands(g)) return fail();
+    clear_tail(doh_addr, pos.i);
+    int steps = tile_steps(pos.i);
     tc_fence_after_sync();
     issue_dp(h);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const bool has_next = n + 1 < n_iter;
-      if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.pa_ready, g & 1)) return fail();
       // the first dV / dK of an item overwrite the accumulators: the previous
       // item's epilogue must have read them
-      if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (n == 0 && items > 0 && !wait(&sh.acc_free, (items - 1) & 1)) return fail();
       tc_fence_after_sync();
       // dV half += P^T dO_n[:, h]; P^T (bf16) in columns [0,16) and [32,48) of REG_S
       const uint64_t dod = make_smem_desc_sw128(doh_addr, C::Q_CHUNK, 1024);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048),
+        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048),
                 kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.pv_done);
-      umma_commit(&sh.doh_empty);
+      commit(&sh.pv_done);
+      commit(&sh.doh_empty);
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
-        if (!wait_s_operands(g + 1) || !mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
+        if (!wait_s_operands(g + 1) || !wait(&sh.pv_done, g & 1)) return fail();
         tc_fence_after_sync();
+        if constexpr (RAG) {
+          wk.advance(pos);
+          clear_tail(qh_addr + ((g + 1) % C::QH_SLOTS) * C::HALF_BYTES, pos.i);
+        }
         issue_s(g + 1, h);
       }
-      if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.ds_ready, g & 1)) return fail();
       tc_fence_after_sync();
       // dK half += dS^T Q_n[:, h]
       const uint32_t qh = qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES;
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qh, C::Q_CHUNK, 1024);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc,
+        if (lead && (!RAG || ks < steps)) umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc,
                 (n > 0 || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.qh_empty[g % C::QH_SLOTS]);
+      commit(&sh.qh_empty[g % C::QH_SLOTS]);
       if constexpr (DQ) {
         // dQ_n^T half = K_j[:, h]^T dS^T into buffer g & 1, once the drain of
         // tile g - 2 has read it
         const int b = g & 1;
-        if (g >= 2 && !mbar_wait(&sh.dq_free[b], ((g >> 1) - 1) & 1, &sh.abort_flag, lim)) return fail();
+        if (g >= 2 && !wait(&sh.dq_free[b], ((g >> 1) - 1) & 1)) return fail();
         tc_fence_after_sync();
         const uint64_t kd = make_smem_desc_sw128(k_addr + 2 * h * C::KV_CHUNK, C::KV_CHUNK, 1024);
         const uint64_t dsm = make_smem_desc_sw128(ds_addr, C::DS_BYTES, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           umma_ss(tmem + C::dq_col(b), desc_add(kd, ks * 2048), desc_add(dsm, ks * 2048), kIdescDq, ks > 0 ? 1u : 0u);
-        umma_commit(&sh.dq_full[b]);
+        commit(&sh.dq_full[b]);
       }
       if (has_next) {
         // dP^T(n+1): phase B(n) has read dP^T(n) (ds_ready above)
         if (!wait_dp_operands(g + 1)) return fail();
+        clear_tail(doh_addr, pos.i);
+        steps = tile_steps(pos.i);
         tc_fence_after_sync();
         issue_dp(h);
       }
     }
-    umma_commit(&sh.acc_done);
+    commit(&sh.acc_done);
     ++items;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  drain_mmas(&sh.mma_drain, lim);
+  if (lead) drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w (w = 0, 1) owns queries [32w, 32w + 32) of every 64-row tile;
@@ -366,7 +441,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
 // 128h + r in the dQ drain. Order per tile n: B(n), A(n+1), drain(n). After
 // an item's last tile warpgroup 0 writes its dK half and warpgroup 1 its dV
 // half straight from TMEM.
-template <bool CAUSAL, bool DQ>
+template <bool CAUSAL, bool DQ, bool RAG>
 __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, float* sLD, uint32_t tmem, int w) {
   using C = Cfg256;
   const int r = threadIdx.x & 127;
@@ -379,12 +454,20 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   const uint32_t bar_id = 1 + w;
   const uint32_t tA = tmem + lane_base + C::REG_S + 32 * w;
   const uint32_t tB = tmem + lane_base + C::REG_DP + 32 * w;
-  const int total = total_items256(p);
+  const int total = total_items256<RAG>(p);
   bool alive = true;
   uint32_t pk[16];  // P^T of the current tile (bf16 pairs, as written to TMEM): dS uses the same rounding
 
   // thread r < 32 loads L2 of query 32w + r of the tile, 32 <= r < 64 its scaled D
-  auto fetch_ld = [&](int bh, int i) -> float {
+  // Queries behind a packed sequence's last one get L2 = +inf (weight 0) and D = 0.
+  auto fetch_ld = [&](const Work256<CAUSAL, RAG>& wk, int bh, int i) -> float {
+    if constexpr (RAG) {
+      const int q = i * C::BQ + 32 * w + (r & 31);
+      if (r >= 64) return 0.f;
+      if (q >= wk.n) return r < 32 ? INFINITY : 0.f;
+      const size_t at = static_cast<size_t>(bh) * p.N + wk.row0 + q;
+      return r < 32 ? __ldg(p.lse2 + at) : __ldg(p.D + at) * sc;
+    }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * C::BQ + 32 * w;
     if (r < 32) return __ldg(p.lse2 + row + r);
     if (r < 64) return __ldg(p.D + row + (r - 32)) * sc;
@@ -397,7 +480,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   };
 
   // ---- phase A of query tile i (global tile g): P^T -> TMEM (bf16)
-  auto phase_a = [&](const Work256<CAUSAL>& wk, int i, int g) {
+  auto phase_a = [&](const Work256<CAUSAL, RAG>& wk, int i, int g) {
     wait_all(&sh.s_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t a[32];
@@ -406,7 +489,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     // key 128j + r is seen by query 64i + 32w + c if it exists and (causal)
     // is not after the query: c >= c_lo
     const int key = wk.j * 128 + r;
-    const bool key_valid = key < p.N;
+    const bool key_valid = key < wk.len(p);
+    // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
+    const int c_hi = RAG ? wk.len(p) - i * C::BQ - 32 * w : 32;
     const int c_lo = CAUSAL ? key - i * C::BQ - 32 * w : 0;
     float pv[32];
 #pragma unroll
@@ -421,10 +506,10 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) pv[c] = ex2_approx(pv[c]);
-    if (!key_valid || (CAUSAL && c_lo > 0)) {
+    if (!key_valid || (CAUSAL && c_lo > 0) || (RAG && c_hi < 32)) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (!key_valid || c < c_lo) pv[c] = 0.f;
+        if (!key_valid || c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
     }
 #pragma unroll
     for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
@@ -435,7 +520,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   };
 
   // ---- phase B: dS^T = P^T o (dP^T - D) * scale -> smem row r, queries [32w, 32w + 32)
-  auto phase_b = [&](int g) {
+  auto phase_b = [&](const Work256<CAUSAL, RAG>& wk, int i, int g) {
     wait_all(&sh.dp_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t dpv[32];
@@ -453,6 +538,14 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
       const float2 ds23 = fmul2(p23, g23);
       dk[c4 / 2] = pack_bf16x2(ds01.x, ds01.y);
       dk[c4 / 2 + 1] = pack_bf16x2(ds23.x, ds23.y);
+    }
+    if constexpr (RAG) {
+      // dP of queries behind the sequence's last may be infinite or NaN
+      const int held = wk.len(p) - i * C::BQ - 32 * w;
+      if (held < 32) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
+      }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -481,12 +574,18 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 
   // ---- item epilogue: w = 0 writes the dK half, w = 1 the dV half; thread r
   // writes key row r (rows past N are skipped)
-  auto epilogue = [&](const Work256<CAUSAL>& wk, int items) {
+  auto epilogue = [&](const Work256<CAUSAL, RAG>& wk, int items) {
     wait_all(&sh.acc_done, items & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     const int key = wk.j * 128 + r;
     const uint32_t t = tmem + lane_base + (w == 0 ? C::DK_COL : C::DV_COL);
-    __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv) + (static_cast<size_t>(wk.bh) * p.N + key) * C::HD + 128 * wk.h;
+    __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv) + 128 * wk.h;
+    if constexpr (RAG) {
+      const long long* st = w == 0 ? p.dk_strides : p.dv_strides;
+      dst += static_cast<long long>(wk.row0 + key) * st[0] + wk.bh * st[1];
+    } else {
+      dst += (static_cast<size_t>(wk.bh) * p.N + key) * C::HD;
+    }
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
       uint32_t v[32];
@@ -496,7 +595,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
         tc_fence_before_sync();
         mbar_arrive(&sh.acc_free);
       }
-      if (key < p.N) {
+      if (key < wk.len(p)) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           *reinterpret_cast<uint4*>(dst + c + 8 * u) =
@@ -523,24 +622,24 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   int item = next_item(0);
   float ld = 0.f;
   if (item < total) {
-    const Work256<CAUSAL> wk0(item, p.BHkv, p.N, p.group);
-    const typename Work256<CAUSAL>::Pos f0 = wk0.first();
-    ld = fetch_ld(f0.bh, f0.i);
+    const Work256<CAUSAL, RAG> wk0(item, p);
+    const typename Work256<CAUSAL, RAG>::Pos f0 = wk0.first();
+    ld = fetch_ld(wk0, f0.bh, f0.i);
   }
   while (item < total) {
-    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
+    const Work256<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     if (items > 0) named_barrier_sync(bar_id, 128);  // the previous item's L2 / D reads are done
     if (r < 64) sLD[w * 64 + r] = ld;
     named_barrier_sync(bar_id, 128);
-    typename Work256<CAUSAL>::Pos cur = wk.first();
+    typename Work256<CAUSAL, RAG>::Pos cur = wk.first();
     phase_a(wk, cur.i, g);
     for (int n = 0; n < n_iter; ++n) {
       const bool has_next = n + 1 < n_iter;
-      typename Work256<CAUSAL>::Pos nxt = cur;
+      typename Work256<CAUSAL, RAG>::Pos nxt = cur;
       wk.advance(nxt);
-      const float next_ld = has_next ? fetch_ld(nxt.bh, nxt.i) : 0.f;  // lands during phase B
-      phase_b(g + n);
+      const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
+      phase_b(wk, cur.i, g + n);
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         if (r < 64) sLD[w * 64 + r] = next_ld;
@@ -552,9 +651,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     }
     const int item_next = next_item(items + 1);
     if (item_next < total) {
-      const Work256<CAUSAL> wk1(item_next, p.BHkv, p.N, p.group);
-      const typename Work256<CAUSAL>::Pos f1 = wk1.first();
-      ld = fetch_ld(f1.bh, f1.i);  // lands during the epilogue
+      const Work256<CAUSAL, RAG> wk1(item_next, p);
+      const typename Work256<CAUSAL, RAG>::Pos f1 = wk1.first();
+      ld = fetch_ld(wk1, f1.bh, f1.i);  // lands during the epilogue
     }
     epilogue(wk, items);
     g += n_iter;
@@ -563,7 +662,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   }
 }
 
-template <bool CAUSAL, bool DQ>
+template <bool CAUSAL, bool DQ, bool RAG>
 __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_constant__ BwdLaunch p) {
   using C = Cfg256;
   extern __shared__ uint8_t smem_dyn[];
@@ -623,11 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_con
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) load_role<CAUSAL>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo);
+    if (lane_id() == 0) load_role<CAUSAL, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) mma_role<CAUSAL, DQ>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
+    if (RAG || lane_id() == 0) mma_role<CAUSAL, DQ, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
   } else {
-    softmax_role<CAUSAL, DQ>(p, sh, sDS, sLD, tmem, warp >> 2);
+    softmax_role<CAUSAL, DQ, RAG>(p, sh, sDS, sLD, tmem, warp >> 2);
   }
 
   tc_fence_before_sync();
@@ -636,12 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_con
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <bool CAUSAL, bool DQ>
+template <bool CAUSAL, bool DQ, bool RAG = false>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
-  auto kern = fa_bwd256_kernel<CAUSAL, DQ>;
+  auto kern = fa_bwd256_kernel<CAUSAL, DQ, RAG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg256::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(a.BHkv) * ((a.N + 127) / 128) * 2;
+  // Packed sequences: the plan, on the device, knows how many items there are.
+  const long long items = static_cast<long long>(a.BHkv) * (RAG ? a.N : (a.N + 127) / 128) * 2;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
   kern<<<static_cast<unsigned>(grid), kThreads, Cfg256::SMEM_BYTES, stream>>>(a);
@@ -651,6 +751,7 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_bwd_main_d256(const BwdLaunch& a, cudaStream_t stream) {
+  if (a.plan) return a.causal ? launch_t<true, false, true>(a, stream) : launch_t<false, false, true>(a, stream);
   if (a.deterministic)
     return a.causal ? launch_t<true, false>(a, stream) : launch_t<false, false>(a, stream);
   return a.causal ? launch_t<true, true>(a, stream) : launch_t<false, true>(a, stream);

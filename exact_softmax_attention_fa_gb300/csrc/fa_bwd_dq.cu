@@ -31,6 +31,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -80,10 +81,13 @@ struct DqShared {
 // Work item: query tile i of query head bh; key tiles 0 .. nkv-1 (causal:
 // the tiles up to the diagonal). Causal items are numbered most-work-first;
 // non-causal items of one head are adjacent (K/V reuse in L2).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 struct DqWork {
   int bh, i, nkv;
-  __device__ DqWork(int item, int BH, int N) {
+  static constexpr int row0 = 0;  // the sequence's first row
+  __device__ __forceinline__ int len(const BwdLaunch& p) const { return p.N; }
+  __device__ DqWork(int item, const BwdLaunch& p) {
+    const int BH = p.BH, N = p.N;
     const int T = (N + 127) / 128;
     if (CAUSAL) {
       i = T - 1 - item / BH;
@@ -97,9 +101,34 @@ struct DqWork {
   }
 };
 
+// The same over packed sequences: an entry of the plan's list is a sequence's
+// query tile, every query head of it an item.
+template <bool CAUSAL>
+struct DqWork<CAUSAL, true> {
+  int bh, i, nkv, row0, n;
+  __device__ __forceinline__ int len(const BwdLaunch&) const { return n; }
+  __device__ DqWork(int item, const BwdLaunch& p) {
+    const int e = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(p.BH));
+    const int4 x = __ldg(packed_tiles(p.plan) + e);
+    bh = item - e * p.BH;
+    row0 = x.x;
+    n = x.y;
+    i = x.z;
+    nkv = CAUSAL ? i + 1 : (n + 127) >> 7;
+  }
+};
+
+template <bool RAG>
+__device__ __forceinline__ int dq_total_items(const BwdLaunch& p) {
+  if constexpr (RAG)
+    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BH : 0;
+  else
+    return p.BH * ((p.N + 127) / 128);
+}
+
 // TMA producer (one thread): Q_i and dO_i once per item, after the previous
 // item's last S and dP products have read them; K_j, V_j through the ring.
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG>
 __device__ void dq_load_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8_t* sdO, uint8_t* sK,
                              uint8_t* sV) {
   using C = DqCfg<HD>;
@@ -107,40 +136,39 @@ __device__ void dq_load_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint
   tma_prefetch_desc(&p.tmdO);
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
   const uint64_t lim = p.wait_limit_ns;
   int u = 0, kv = 0, q_issued = 0;  // kv: K/V tiles loaded
   bool k_extra = false;              // K of tile kv issued, its V not (abort in between)
   bool aborted = false;
-  auto load_kv = [&](int j, int kvh) -> bool {
+  auto load_kv = [&](int row, int kvh) -> bool {
     const int ks = kv % C::KST, vs = kv % C::VST;
     if (kv >= C::KST && !mbar_wait(&sh.k_empty[ks], ((kv / C::KST) - 1) & 1, &sh.abort_flag, lim)) return false;
     mbar_arrive_expect_tx(&sh.k_full[ks], C::TILE_BYTES);
 #pragma unroll
     for (int c = 0; c < C::CHUNKS; ++c)
-      tma_load_3d(sK + ks * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmK, &sh.k_full[ks], c * 64, j * 128, kvh);
+      tma_load_3d(sK + ks * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmK, &sh.k_full[ks], c * 64, row, kvh);
     k_extra = true;
     if (kv >= C::VST && !mbar_wait(&sh.v_empty[vs], ((kv / C::VST) - 1) & 1, &sh.abort_flag, lim)) return false;
     mbar_arrive_expect_tx(&sh.v_full[vs], C::TILE_BYTES);
 #pragma unroll
     for (int c = 0; c < C::CHUNKS; ++c)
-      tma_load_3d(sV + vs * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmV, &sh.v_full[vs], c * 64, j * 128, kvh);
+      tma_load_3d(sV + vs * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmV, &sh.v_full[vs], c * 64, row, kvh);
     ++kv;
     k_extra = false;
     return true;
   };
-  int item = blockIdx.x;  // the grid never exceeds the item count
+  int item = blockIdx.x;
   while (!aborted) {
     if (!publish_item(sh, u, item, lim)) {
       aborted = true;
       break;
     }
     if (item >= total) break;
-    const DqWork<CAUSAL> wk(item, p.BH, p.N);
+    const DqWork<CAUSAL, RAG> wk(item, p);
     const int kvh = wk.bh / p.group;  // grouped K/V heads
     // The first K/V tile loads while the previous item still reads Q_i, dO_i.
-    if (!load_kv(0, kvh) || (u > 0 && !mbar_wait(&sh.q_free, (u - 1) & 1, &sh.abort_flag, lim))) {
+    if (!load_kv(wk.row0, kvh) || (u > 0 && !mbar_wait(&sh.q_free, (u - 1) & 1, &sh.abort_flag, lim))) {
       aborted = true;
       break;
     }
@@ -148,12 +176,12 @@ __device__ void dq_load_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint
       mbar_arrive_expect_tx(&sh.q_full, 2 * C::TILE_BYTES);
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c) {
-        tma_load_3d(sQ + c * C::CHUNK_BYTES, &p.tmQ, &sh.q_full, c * 64, wk.i * 128, wk.bh);
-        tma_load_3d(sdO + c * C::CHUNK_BYTES, &p.tmdO, &sh.q_full, c * 64, wk.i * 128, wk.bh);
+        tma_load_3d(sQ + c * C::CHUNK_BYTES, &p.tmQ, &sh.q_full, c * 64, wk.row0 + wk.i * 128, wk.bh);
+        tma_load_3d(sdO + c * C::CHUNK_BYTES, &p.tmdO, &sh.q_full, c * 64, wk.row0 + wk.i * 128, wk.bh);
       }
       ++q_issued;
     }
-    for (int j = 1; j < wk.nkv && !aborted; ++j) aborted = !load_kv(j, kvh);
+    for (int j = 1; j < wk.nkv && !aborted; ++j) aborted = !load_kv(wk.row0 + j * 128, kvh);
     ++u;
     if (!aborted) item = claim_item(p.sched + 2);
   }
@@ -176,7 +204,7 @@ __device__ void dq_load_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint
 //            of tile t-1 (whose dS sat there) is done (overlaps A(t), B(t))
 //   dP(t+1)  once phase B(t) has read dP(t)        (overlaps the rest of B(t))
 //   dQ += dS(t) K_j   once phase B(t) wrote dS(t)  (overlaps phase A(t+1))
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG>
 __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8_t* sdO, uint8_t* sK, uint8_t* sV,
                             uint32_t tmem) {
   using C = DqCfg<HD>;
@@ -184,11 +212,22 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   constexpr uint32_t kIdescDq = make_idesc_bf16_f32(128, HD, false, true);    // A = dS (TMEM), B = K_j MN-major
   const uint32_t q_addr = smem_u32(sQ), do_addr = smem_u32(sdO), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
   const uint64_t lim = p.wait_limit_ns;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
+
+  // Packed sequences: the whole warp walks the items (it clears the rows of K
+  // behind a sequence's last key), one lane issues.
+  const bool lead = !RAG || lane_id() == 0;
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
+    return RAG ? __all_sync(0xffffffffu, ok) : ok;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) umma_commit(bar);
+  };
 
   // D[tmem] = A (128 x HD, K-major) * B (128 x HD, K-major)^T
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_addr) {
+    if (!lead) return;
     const uint64_t ad = make_smem_desc_sw128(a_addr, 16, 1024), bd = make_smem_desc_sw128(b_addr, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
@@ -198,7 +237,7 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+    if (lead) drain_mmas(&sh.mma_drain, lim);
   };
 
   // S(t) into buffer t & 1, which tile t - 2 used.
@@ -207,70 +246,82 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   // including the product of tile t - 2 whose dS sat in buffer t & 1.
   auto issue_s = [&](int t, int kvi, int done_tile) -> bool {  // kvi: the tile's index in the K/V stream
     const int stage = kvi % C::KST;
-    if (!mbar_wait(&sh.k_full[stage], (kvi / C::KST) & 1, &sh.abort_flag, lim)) return false;
-    if (t >= 2 && !mbar_wait(&sh.dq_done, done_tile & 1, &sh.abort_flag, lim)) return false;
+    if (!wait(&sh.k_full[stage], (kvi / C::KST) & 1)) return false;
+    if (t >= 2 && !wait(&sh.dq_done, done_tile & 1)) return false;
     tc_fence_after_sync();
     issue_sq(C::s_col(t & 1), q_addr, k_addr + stage * C::TILE_BYTES);
-    umma_commit(&sh.s_full[t & 1]);
+    commit(&sh.s_full[t & 1]);
     return true;
   };
   // dP(t) over dP(t - 1): wait until phase B(t - 1) loaded it.
   auto issue_dp = [&](int t, int kvi) -> bool {
     const int stage = kvi % C::VST;
-    if (!mbar_wait(&sh.v_full[stage], (kvi / C::VST) & 1, &sh.abort_flag, lim)) return false;
-    if (t >= 1 && !mbar_wait(&sh.dp_free, (t - 1) & 1, &sh.abort_flag, lim)) return false;
+    if (!wait(&sh.v_full[stage], (kvi / C::VST) & 1)) return false;
+    if (t >= 1 && !wait(&sh.dp_free, (t - 1) & 1)) return false;
     tc_fence_after_sync();
     issue_sq(C::DP_COL, do_addr, v_addr + stage * C::TILE_BYTES);
-    umma_commit(&sh.dp_full);
-    umma_commit(&sh.v_empty[stage]);  // V_j is read by dP(j) only
+    commit(&sh.dp_full);
+    commit(&sh.v_empty[stage]);  // V_j is read by dP(j) only
     return true;
   };
 
   int u = 0, kv = 0, t = 0;
   while (true) {
-    const int item = take_item(sh, u, lim);
+    const int item = RAG ? take_item_warp(sh, u, lim) : take_item(sh, u, lim);
     if (item < 0) return fail();
     if (item >= total) break;
-    const DqWork<CAUSAL> wk(item, p.BH, p.N);
-    if (!mbar_wait(&sh.q_full, u & 1, &sh.abort_flag, lim) || !issue_s(t, kv, t - 1) || !issue_dp(t, kv))
+    const DqWork<CAUSAL, RAG> wk(item, p);
+    if (!wait(&sh.q_full, u & 1) || !issue_s(t, kv, t - 1) || !issue_dp(t, kv))
       return fail();
-    if (wk.nkv == 1) umma_commit(&sh.q_free);
+    if (wk.nkv == 1) commit(&sh.q_free);
     // Per tile t: S(t+1) as soon as its K tile is in, dP(t+1) once phase B(t)
     // has read dP(t), dQ += dS(t) K once phase B(t) has written dS(t).
     for (int j = 0; j < wk.nkv; ++j, ++kv, ++t) {
       const int s = kv % C::KST;
       if (j + 1 < wk.nkv) {
         if (!issue_s(t + 1, kv + 1, t - 1) || !issue_dp(t + 1, kv + 1)) return fail();
-        if (j + 2 == wk.nkv) umma_commit(&sh.q_free);  // the item's last S and dP are issued
+        if (j + 2 == wk.nkv) commit(&sh.q_free);  // the item's last S and dP are issued
       }
-      if (!mbar_wait(&sh.ds_ready[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.ds_ready[t & 1], (t >> 1) & 1)) return fail();
       // the first dQ product of an item overwrites the accumulator: the
       // previous item's epilogue must have read it
-      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (j == 0 && u > 0 && !wait(&sh.acc_free, (u - 1) & 1)) return fail();
       tc_fence_after_sync();
       // dS (bf16 pairs) sits in columns [0, 32) and [64, 96) of S buffer t & 1:
       // keys 16 ks .. 16 ks + 15 are 8 columns at 64 (ks / 4) + 8 (ks % 4)
+      // A sequence's last key tile ends in rows of the next one, whatever they
+      // hold: whole steps of 16 keys are left out of the product, and the rows of
+      // the last step taken are cleared (their dS is 0, but 0 * NaN). S(j) has
+      // read the tile; its columns of those keys are masked.
+      int steps = 8;
+      if constexpr (RAG) {
+        const int held = wk.n - j * 128;
+        if (held < 128) {
+          steps = (held + 15) >> 4;
+          clear_rows<C::CHUNKS, C::CHUNK_BYTES>(k_addr + s * C::TILE_BYTES, held, 16 * steps);
+        }
+      }
       const uint64_t kd = make_smem_desc_sw128(k_addr + s * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048),
+        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048),
                 kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.dq_done);
-      umma_commit(&sh.k_empty[s]);
+      commit(&sh.dq_done);
+      commit(&sh.k_empty[s]);
     }
-    umma_commit(&sh.acc_done);
+    commit(&sh.acc_done);
     ++u;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  drain_mmas(&sh.mma_drain, lim);
+  if (lead) drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w owns key columns [64w, 64w + 64) of every tile; thread r owns
 // query row r. Phase A: P = 2^(S scale log2e - L2_r) (bf16-rounded, kept in
 // registers). Phase B: dS = P o (dP scale - D_r scale) into the dS tile. At
 // the end of an item warpgroup w writes dQ columns [w d/2, (w+1) d/2).
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG>
 __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem, int w) {
   using C = DqCfg<HD>;
   const int r = threadIdx.x & 127;
@@ -281,8 +332,7 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
   const uint32_t tS0 = tmem + lane_base + C::S_COL + 64 * w;  // + 128 for buffer 1
   const uint32_t tDP = tmem + lane_base + C::DP_COL + 64 * w;
   const uint32_t bar_id = 1 + w;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
   bool alive = true;
   uint32_t pk[32];  // P of the current tile, bf16 pairs
 
@@ -305,11 +355,12 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
   int u = 0, t = 0;
   int item = next_item(0);
   while (item < total) {
-    const DqWork<CAUSAL> wk(item, p.BH, p.N);
+    const DqWork<CAUSAL, RAG> wk(item, p);
     const int row = wk.i * 128 + r;
-    const size_t srow = static_cast<size_t>(wk.bh) * p.Npad + row;
-    const float l2 = __ldg(p.lse2 + srow);  // +inf on padding rows: their P is 0
-    const float dsc = __ldg(p.D + srow) * sc;
+    const bool held = !RAG || row < wk.len(p);
+    const size_t srow = RAG ? static_cast<size_t>(wk.bh) * p.N + wk.row0 + row : static_cast<size_t>(wk.bh) * p.Npad + row;
+    const float l2 = held ? __ldg(p.lse2 + srow) : INFINITY;  // +inf on padding rows: their P is 0
+    const float dsc = held ? __ldg(p.D + srow) * sc : 0.f;
     for (int j = 0; j < wk.nkv; ++j, ++t) {
       // ---- phase A
       wait_all(&sh.s_full[t & 1], (t >> 1) & 1, WHERE_BWD_SOFTMAX);
@@ -330,7 +381,7 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
 
         // key 128j + 64w + c is seen if it is < N and (causal) <= the query row
         const int kbase = j * 128 + 64 * w;
-        int c_hi = std::min(64, p.N - kbase);
+        int c_hi = std::min(64, wk.len(p) - kbase);
         if (CAUSAL && j == wk.i) c_hi = std::min(c_hi, r - 64 * w + 1);
         const bool masked = c_hi < 64;
 #pragma unroll
@@ -376,6 +427,14 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
             ds[16 * h + c4 / 2 + 1] = pack_bf16x2(d23.x, d23.y);
           }
         }
+        if constexpr (RAG) {
+          // dP of keys behind the sequence's last may be infinite or NaN
+          const int keys = wk.len(p) - j * 128 - 64 * w;
+          if (keys < 64) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ds[c] &= (2 * c < keys ? 0xFFFFu : 0u) | (2 * c + 1 < keys ? 0xFFFF0000u : 0u);
+          }
+        }
         tmem_st32(tS0 + 128u * uint32_t(t & 1), ds);
         tmem_st_wait();
         tc_fence_before_sync();
@@ -387,7 +446,11 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
     wait_all(&sh.acc_done, u & 1, WHERE_BWD_SOFTMAX);
     if (alive) {
       const uint32_t tq = tmem + lane_base + C::DQ_COL + w * (HD / 2);
-      __nv_bfloat16* dst = p.dq + (static_cast<size_t>(wk.bh) * p.N + row) * HD + w * (HD / 2);
+      __nv_bfloat16* dst = p.dq + w * (HD / 2);
+      if constexpr (RAG)
+        dst += static_cast<long long>(wk.row0 + row) * p.dq_strides[0] + wk.bh * p.dq_strides[1];
+      else
+        dst += (static_cast<size_t>(wk.bh) * p.N + row) * HD;
 #pragma unroll
       for (int c = 0; c < HD / 2; c += 32) {
         uint32_t v[32];
@@ -397,7 +460,7 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
-        if (row < p.N) {
+        if (row < wk.len(p)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4*>(dst + c + 8 * q) =
@@ -413,7 +476,7 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
   }
 }
 
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG>
 __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_constant__ BwdLaunch p) {
   using C = DqCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
@@ -463,11 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_con
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) dq_load_role<HD, CAUSAL>(p, sh, sQ, sdO, sK, sV);
+    if (lane_id() == 0) dq_load_role<HD, CAUSAL, RAG>(p, sh, sQ, sdO, sK, sV);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) dq_mma_role<HD, CAUSAL>(p, sh, sQ, sdO, sK, sV, tmem);
+    if (RAG || lane_id() == 0) dq_mma_role<HD, CAUSAL, RAG>(p, sh, sQ, sdO, sK, sV, tmem);
   } else {
-    dq_softmax_role<HD, CAUSAL>(p, sh, tmem, warp >> 2);
+    dq_softmax_role<HD, CAUSAL, RAG>(p, sh, tmem, warp >> 2);
   }
 
   tc_fence_before_sync();
@@ -479,13 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_con
   if (threadIdx.x == 0) griddep_wait();
 }
 
-template <int HD, bool CAUSAL>
+template <int HD, bool CAUSAL, bool RAG = false>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using C = DqCfg<HD>;
-  auto kern = fa_bwd_dq_kernel<HD, CAUSAL>;
+  auto kern = fa_bwd_dq_kernel<HD, CAUSAL, RAG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(a.BH) * ((a.N + 127) / 128);
+  // Packed sequences: the plan, on the device, knows how many items there are.
+  const long long items = static_cast<long long>(a.BH) * (RAG ? a.N : (a.N + 127) / 128);
   const long long grid = items < a.num_sms ? items : a.num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -503,6 +567,8 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_bwd_dq(const BwdLaunch& a, cudaStream_t stream) {
+  if (a.plan && a.d == 64) return a.causal ? launch_t<64, true, true>(a, stream) : launch_t<64, false, true>(a, stream);
+  if (a.plan && a.d == 128) return a.causal ? launch_t<128, true, true>(a, stream) : launch_t<128, false, true>(a, stream);
   switch (a.d) {
     case 64: return a.causal ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
     case 128: return a.causal ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);

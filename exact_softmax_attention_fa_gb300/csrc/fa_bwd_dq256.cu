@@ -38,6 +38,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -72,10 +73,13 @@ struct Dq256Shared {
 // Work item: query tile i of query head bh; key tiles 0 .. nkv-1 (causal:
 // up to the diagonal). Causal items are numbered most-work-first; non-causal
 // items of one head are adjacent (K/V reuse in L2).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 struct Dq256Work {
   int bh, i, nkv;
-  __device__ Dq256Work(int item, int BH, int N) {
+  static constexpr int row0 = 0;  // the sequence's first row
+  __device__ __forceinline__ int len(const BwdLaunch& p) const { return p.N; }
+  __device__ Dq256Work(int item, const BwdLaunch& p) {
+    const int BH = p.BH, N = p.N;
     const int T = (N + 127) / 128;
     if (CAUSAL) {
       i = T - 1 - item / BH;
@@ -88,6 +92,31 @@ struct Dq256Work {
     }
   }
 };
+
+// The same over packed sequences: an entry of the plan's list is a sequence's
+// query tile, every query head of it an item.
+template <bool CAUSAL>
+struct Dq256Work<CAUSAL, true> {
+  int bh, i, nkv, row0, n;
+  __device__ __forceinline__ int len(const BwdLaunch&) const { return n; }
+  __device__ Dq256Work(int item, const BwdLaunch& p) {
+    const int e = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(p.BH));
+    const int4 x = __ldg(packed_tiles(p.plan) + e);
+    bh = item - e * p.BH;
+    row0 = x.x;
+    n = x.y;
+    i = x.z;
+    nkv = CAUSAL ? i + 1 : (n + 127) >> 7;
+  }
+};
+
+template <bool RAG>
+__device__ __forceinline__ int dq_total_items(const BwdLaunch& p) {
+  if constexpr (RAG)
+    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BH : 0;
+  else
+    return p.BH * ((p.N + 127) / 128);
+}
 
 // The chunk stream of one item, in the MMA's reading order: K_0 and V_0
 // (4 chunks each), then per key tile t: K_{t+1}, K_t, V_{t+1} (the first and
@@ -118,43 +147,43 @@ struct ChunkStream {
 // TMA producer (one thread): per item K_0, then Q_i and dO_i once the
 // previous item's last S and dP products have read theirs, then the rest of
 // the chunk stream through the ring.
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 __device__ void dq256_load_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ, uint8_t* sdO, uint8_t* sRing) {
   using C = Dq256Cfg;
   tma_prefetch_desc(&p.tmQ);
   tma_prefetch_desc(&p.tmdO);
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
   const uint64_t lim = p.wait_limit_ns;
   int u = 0, pos = 0, q_issued = 0;  // pos: ring chunks issued
   bool aborted = false;
-  auto load_chunk = [&](const ChunkStream& cs, int k, int kvh) -> bool {
+  auto load_chunk = [&](const ChunkStream& cs, int k, int row0, int kvh) -> bool {
     int tensor, tile, col;
     cs.at(k, tensor, tile, col);
     const int s = pos % C::RING;
     if (pos >= C::RING && !mbar_wait(&sh.ring_empty[s], ((pos / C::RING) - 1) & 1, &sh.abort_flag, lim)) return false;
     mbar_arrive_expect_tx(&sh.ring_full[s], C::CHUNK_BYTES);
-    tma_load_3d(sRing + s * C::CHUNK_BYTES, tensor == 0 ? &p.tmK : &p.tmV, &sh.ring_full[s], col * 64, tile * 128, kvh);
+    tma_load_3d(sRing + s * C::CHUNK_BYTES, tensor == 0 ? &p.tmK : &p.tmV, &sh.ring_full[s], col * 64, row0 + tile * 128,
+                kvh);
     ++pos;
     return true;
   };
-  int item = blockIdx.x;  // the grid never exceeds the item count
+  int item = blockIdx.x;
   while (!aborted) {
     if (!publish_item(sh, u, item, lim)) {
       aborted = true;
       break;
     }
     if (item >= total) break;
-    const Dq256Work<CAUSAL> wk(item, p.BH, p.N);
+    const Dq256Work<CAUSAL, RAG> wk(item, p);
     const int kvh = wk.bh / p.group;  // grouped K/V heads
     const ChunkStream cs{wk.nkv};
     const int n = cs.count();
     int k = 0;
     // K_0 loads while the previous item still reads Q_i, dO_i. V_0 follows
     // Q_i: its last chunks wait for S(0) to free ring slots, and S(0) needs Q_i.
-    for (; k < 4 && !aborted; ++k) aborted = !load_chunk(cs, k, kvh);
+    for (; k < 4 && !aborted; ++k) aborted = !load_chunk(cs, k, wk.row0, kvh);
     if (aborted || (u > 0 && !mbar_wait(&sh.q_free, (u - 1) & 1, &sh.abort_flag, lim))) {
       aborted = true;
       break;
@@ -168,12 +197,12 @@ __device__ void dq256_load_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t off = c * C::CHUNK_BYTES + hh * (C::CHUNK_BYTES / 2);
-          tma_load_3d(sQ + off, &p.tmQ, &sh.q_full, c * 64, wk.i * 128 + 64 * hh, wk.bh);
-          tma_load_3d(sdO + off, &p.tmdO, &sh.q_full, c * 64, wk.i * 128 + 64 * hh, wk.bh);
+          tma_load_3d(sQ + off, &p.tmQ, &sh.q_full, c * 64, wk.row0 + wk.i * 128 + 64 * hh, wk.bh);
+          tma_load_3d(sdO + off, &p.tmdO, &sh.q_full, c * 64, wk.row0 + wk.i * 128 + 64 * hh, wk.bh);
         }
       ++q_issued;
     }
-    for (; k < n && !aborted; ++k) aborted = !load_chunk(cs, k, kvh);
+    for (; k < n && !aborted; ++k) aborted = !load_chunk(cs, k, wk.row0, kvh);
     if (aborted) break;
     ++u;
     item = claim_item(p.sched + 2);
@@ -187,7 +216,7 @@ __device__ void dq256_load_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ
 }
 
 // One thread issues every MMA (order in the file header).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ, uint8_t* sdO, uint8_t* sRing,
                                uint32_t tmem) {
   using C = Dq256Cfg;
@@ -195,15 +224,24 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
   constexpr uint32_t kIdescDq = make_idesc_bf16_f32(128, 128, false, true);   // A = dS (TMEM), B = K MN-major
   const uint32_t q_addr = smem_u32(sQ), do_addr = smem_u32(sdO), ring_addr = smem_u32(sRing);
   const uint64_t lim = p.wait_limit_ns;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
+  // Packed sequences: the whole warp walks the items (it clears the rows of K
+  // behind a sequence's last key), one lane issues.
+  const bool lead = !RAG || lane_id() == 0;
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
+    return RAG ? __all_sync(0xffffffffu, ok) : ok;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) umma_commit(bar);
+  };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+    if (lead) drain_mmas(&sh.mma_drain, lim);
   };
   int pos = 0;  // ring chunks consumed
   auto wait_chunk = [&](int k) -> bool {
-    return mbar_wait(&sh.ring_full[k % C::RING], (k / C::RING) & 1, &sh.abort_flag, lim);
+    return wait(&sh.ring_full[k % C::RING], (k / C::RING) & 1);
   };
   auto slot_addr = [&](int k) -> uint32_t { return ring_addr + (k % C::RING) * C::CHUNK_BYTES; };
   // D = A (128 x 256 resident, K-major) * (4 ring chunks, K-major)^T; each
@@ -217,79 +255,88 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
       const uint64_t bd = make_smem_desc_sw128(slot_addr(pos), 16, 1024);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        umma_ss(tmem + d_col, desc_add(ad, ks * 32), desc_add(bd, ks * 32), kIdescSq, (c > 0 || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.ring_empty[pos % C::RING]);
+        if (lead) umma_ss(tmem + d_col, desc_add(ad, ks * 32), desc_add(bd, ks * 32), kIdescSq, (c > 0 || ks > 0) ? 1u : 0u);
+      commit(&sh.ring_empty[pos % C::RING]);
     }
     return true;
   };
   // dQ += dS K_t: two N = 128 halves of the head dimension, each reading an
   // even-aligned pair of ring chunks as one MN-major B operand.
-  auto issue_dq = [&](bool first) -> bool {
+  // held: keys of the sequence from tile t on (fa_bwd_dq.cu: those behind its last
+  // are left out, or cleared where a step of 16 holds some of both).
+  auto issue_dq = [&](bool first, int held) -> bool {
+    const int steps = RAG ? min(8, (held + 15) >> 4) : 8;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half, pos += 2) {
       if (!wait_chunk(pos) || !wait_chunk(pos + 1)) return false;
+      if constexpr (RAG) {
+        if (held < 128) {
+          clear_rows<1, C::CHUNK_BYTES>(slot_addr(pos), held, 16 * steps);
+          clear_rows<1, C::CHUNK_BYTES>(slot_addr(pos + 1), held, 16 * steps);
+        }
+      }
       tc_fence_after_sync();
       const uint64_t kd = make_smem_desc_sw128(slot_addr(pos), C::CHUNK_BYTES, 1024);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8,
+        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8,
                 desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
-      umma_commit(&sh.ring_empty[pos % C::RING]);
-      umma_commit(&sh.ring_empty[(pos + 1) % C::RING]);
+      commit(&sh.ring_empty[pos % C::RING]);
+      commit(&sh.ring_empty[(pos + 1) % C::RING]);
     }
     return true;
   };
 
   int u = 0, t = 0;  // items, key tiles (global)
   while (true) {
-    const int item = take_item(sh, u, lim);
+    const int item = RAG ? take_item_warp(sh, u, lim) : take_item(sh, u, lim);
     if (item < 0) return fail();
     if (item >= total) break;
-    const Dq256Work<CAUSAL> wk(item, p.BH, p.N);
-    if (!mbar_wait(&sh.q_full, u & 1, &sh.abort_flag, lim)) return fail();
+    const Dq256Work<CAUSAL, RAG> wk(item, p);
+    if (!wait(&sh.q_full, u & 1)) return fail();
     // S(first): the previous item's last dQ product has read dS from the dP
     // columns, and phase A read its S, before that product was issued.
-    if (t > 0 && !mbar_wait(&sh.s_free, (t - 1) & 1, &sh.abort_flag, lim)) return fail();
+    if (t > 0 && !wait(&sh.s_free, (t - 1) & 1)) return fail();
     tc_fence_after_sync();
     if (!issue_sq(C::S_COL, q_addr)) return fail();
-    umma_commit(&sh.s_full);
+    commit(&sh.s_full);
     // dP(first) overwrites the previous item's last dS: its dQ product is done
-    if (t > 0 && !mbar_wait(&sh.dq_done, (t - 1) & 1, &sh.abort_flag, lim)) return fail();
+    if (t > 0 && !wait(&sh.dq_done, (t - 1) & 1)) return fail();
     tc_fence_after_sync();
     if (!issue_sq(C::DP_COL, do_addr)) return fail();
-    umma_commit(&sh.dp_full);
-    if (wk.nkv == 1) umma_commit(&sh.q_free);
+    commit(&sh.dp_full);
+    if (wk.nkv == 1) commit(&sh.q_free);
     for (int j = 0; j < wk.nkv; ++j, ++t) {
       const bool has_next = j + 1 < wk.nkv;
       if (has_next) {
         // S(t+1) once phase A(t) has read S(t)
-        if (!mbar_wait(&sh.s_free, t & 1, &sh.abort_flag, lim)) return fail();
+        if (!wait(&sh.s_free, t & 1)) return fail();
         tc_fence_after_sync();
         if (!issue_sq(C::S_COL, q_addr)) return fail();
-        umma_commit(&sh.s_full);
+        commit(&sh.s_full);
       }
-      if (!mbar_wait(&sh.ds_ready, t & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.ds_ready, t & 1)) return fail();
       // the first dQ product of an item overwrites the accumulator: the
       // previous item's epilogue must have read it
-      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (j == 0 && u > 0 && !wait(&sh.acc_free, (u - 1) & 1)) return fail();
       tc_fence_after_sync();
-      if (!issue_dq(j == 0)) return fail();
-      umma_commit(&sh.dq_done);
+      if (!issue_dq(j == 0, wk.len(p) - j * 128)) return fail();
+      commit(&sh.dq_done);
       if (has_next) {
         // dP(t+1) overwrites dS(t): wait for the dQ product to have read it
-        if (!mbar_wait(&sh.dq_done, t & 1, &sh.abort_flag, lim)) return fail();
+        if (!wait(&sh.dq_done, t & 1)) return fail();
         tc_fence_after_sync();
         if (!issue_sq(C::DP_COL, do_addr)) return fail();
-        umma_commit(&sh.dp_full);
-        if (j + 2 == wk.nkv) umma_commit(&sh.q_free);  // the item's last S and dP are issued
+        commit(&sh.dp_full);
+        if (j + 2 == wk.nkv) commit(&sh.q_free);  // the item's last S and dP are issued
       }
     }
-    umma_commit(&sh.acc_done);
+    commit(&sh.acc_done);
     ++u;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  drain_mmas(&sh.mma_drain, lim);
+  if (lead) drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w owns key columns [64w, 64w + 64) of every key tile; thread r
@@ -297,7 +344,7 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
 // kept in registers). Phase B: dS = P o (dP scale - D_r scale) into the dP
 // columns. At the end of an item warpgroup w writes dQ columns
 // [128w, 128w + 128).
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t tmem, int w) {
   using C = Dq256Cfg;
   const int r = threadIdx.x & 127;
@@ -308,8 +355,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
   const uint32_t tS = tmem + lane_base + C::S_COL + 64 * w;
   const uint32_t tDP = tmem + lane_base + C::DP_COL + 64 * w;
   const uint32_t bar_id = 1 + w;
-  const int T = (p.N + 127) / 128;
-  const int total = p.BH * T;
+  const int total = dq_total_items<RAG>(p);
   bool alive = true;
   uint32_t pk[32];  // P of the current tile, bf16 pairs
 
@@ -331,11 +377,12 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
   int u = 0, t = 0;
   int item = next_item(0);
   while (item < total) {
-    const Dq256Work<CAUSAL> wk(item, p.BH, p.N);
+    const Dq256Work<CAUSAL, RAG> wk(item, p);
     const int row = wk.i * 128 + r;
-    const size_t srow = static_cast<size_t>(wk.bh) * p.Npad + row;
-    const float l2 = __ldg(p.lse2 + srow);  // +inf on padding rows: their P is 0
-    const float dsc = __ldg(p.D + srow) * sc;
+    const bool held = !RAG || row < wk.len(p);
+    const size_t srow = RAG ? static_cast<size_t>(wk.bh) * p.N + wk.row0 + row : static_cast<size_t>(wk.bh) * p.Npad + row;
+    const float l2 = held ? __ldg(p.lse2 + srow) : INFINITY;  // +inf on padding rows: their P is 0
+    const float dsc = held ? __ldg(p.D + srow) * sc : 0.f;
     for (int j = 0; j < wk.nkv; ++j, ++t) {
       // ---- phase A: P of this warpgroup's 64 keys; S is released once read
       wait_all(&sh.s_full, t & 1, WHERE_BWD_SOFTMAX);
@@ -354,7 +401,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
         }
         // key 128j + 64w + c is seen if it is < N and (causal) <= the query row
         const int kbase = j * 128 + 64 * w;
-        int c_hi = min(64, p.N - kbase);
+        int c_hi = min(64, wk.len(p) - kbase);
         if (CAUSAL && j == wk.i) c_hi = min(c_hi, row - kbase + 1);
         const bool masked = c_hi < 64;
 #pragma unroll
@@ -396,6 +443,14 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
             ds[16 * h2 + c4 / 2 + 1] = pack_bf16x2(d23.x, d23.y);
           }
         }
+        if constexpr (RAG) {
+          // dP of keys behind the sequence's last may be infinite or NaN
+          const int keys = wk.len(p) - j * 128 - 64 * w;
+          if (keys < 64) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ds[c] &= (2 * c < keys ? 0xFFFFu : 0u) | (2 * c + 1 < keys ? 0xFFFF0000u : 0u);
+          }
+        }
         tmem_st32(tDP, ds);
         tmem_st_wait();
         tc_fence_before_sync();
@@ -407,7 +462,11 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
     wait_all(&sh.acc_done, u & 1, WHERE_BWD_SOFTMAX);
     if (alive) {
       const uint32_t tq = tmem + lane_base + C::DQ_COL + w * 128;
-      __nv_bfloat16* dst = p.dq + (static_cast<size_t>(wk.bh) * p.N + row) * C::HD + w * 128;
+      __nv_bfloat16* dst = p.dq + w * 128;
+      if constexpr (RAG)
+        dst += static_cast<long long>(wk.row0 + row) * p.dq_strides[0] + wk.bh * p.dq_strides[1];
+      else
+        dst += (static_cast<size_t>(wk.bh) * p.N + row) * C::HD;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t v[32];
@@ -417,7 +476,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
-        if (row < p.N) {
+        if (row < wk.len(p)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4*>(dst + c + 8 * q) =
@@ -433,7 +492,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
   }
 }
 
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG>
 __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_constant__ BwdLaunch p) {
   using C = Dq256Cfg;
   extern __shared__ uint8_t smem_dyn[];
@@ -477,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) dq256_load_role<CAUSAL>(p, sh, sQ, sdO, sRing);
+    if (lane_id() == 0) dq256_load_role<CAUSAL, RAG>(p, sh, sQ, sdO, sRing);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) dq256_mma_role<CAUSAL>(p, sh, sQ, sdO, sRing, tmem);
+    if (RAG || lane_id() == 0) dq256_mma_role<CAUSAL, RAG>(p, sh, sQ, sdO, sRing, tmem);
   } else {
-    dq256_softmax_role<CAUSAL>(p, sh, tmem, warp >> 2);
+    dq256_softmax_role<CAUSAL, RAG>(p, sh, tmem, warp >> 2);
   }
 
   tc_fence_before_sync();
@@ -493,13 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_
   if (threadIdx.x == 0) griddep_wait();
 }
 
-template <bool CAUSAL>
+template <bool CAUSAL, bool RAG = false>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using C = Dq256Cfg;
-  auto kern = fa_bwd_dq256_kernel<CAUSAL>;
+  auto kern = fa_bwd_dq256_kernel<CAUSAL, RAG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(a.BH) * ((a.N + 127) / 128);
+  // Packed sequences: the plan, on the device, knows how many items there are.
+  const long long items = static_cast<long long>(a.BH) * (RAG ? a.N : (a.N + 127) / 128);
   const long long grid = items < a.num_sms ? items : a.num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -517,6 +577,7 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_bwd_dq256(const BwdLaunch& a, cudaStream_t stream) {
+  if (a.plan) return a.causal ? launch_t<true, true>(a, stream) : launch_t<false, true>(a, stream);
   return a.causal ? launch_t<true>(a, stream) : launch_t<false>(a, stream);
 }
 

@@ -1,6 +1,7 @@
 // Forward pass of exact softmax attention for sm_103a: the kernel templates,
-// instantiated by fa_fwd.cu (one head per tile) and fa_fwd_pack.cu (grouped
-// query heads packed into a tile).
+// instantiated by fa_fwd.cu (one head per tile), fa_fwd_pack.cu (grouped
+// query heads packed into a tile) and fa_fwd_ragged.cu (packed sequences of
+// different lengths).
 //
 // Method (web pages on FlashAttention-2):
 //   "FlashAttention 2: ..." reading note (papers.chlience.com) 5.1-5.2 and the
@@ -47,6 +48,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -108,7 +110,7 @@ __device__ __forceinline__ int heads_per_tile(const FwdLaunch& p) {
 // causal mask (the last query tiles see the most keys); non-causal items of
 // one head are adjacent (K/V reuse in L2). Key-tile indices inside an item
 // are relative to kv0.
-template <int NT, bool CAUSAL, bool PACK>
+template <int NT, bool CAUSAL, bool PACK, bool RAG>
 struct FwdWork {
   int bh, s, kv0;
   int qt[NT];       // query tile indices
@@ -150,6 +152,53 @@ struct FwdWork {
       nkv = max(nkv, last + 1);
     }
   }
+  // Where slot t's query tile and the item's key tile j lie, as TMA coordinates
+  __device__ __forceinline__ int q_row(const FwdLaunch& p, int t) const { return qt[t] * rows_per_head<PACK>(p); }
+  __device__ __forceinline__ int q_head(int) const { return bh; }
+  __device__ __forceinline__ int kv_row(int j) const { return (kv0 + j) * 128; }
+  // grouped K/V heads: query head bh reads K/V head bh / g
+  __device__ __forceinline__ int kv_head(const FwdLaunch& p) const { return bh / p.group; }
+  // queries and keys of the item's sequence
+  __device__ __forceinline__ int n_queries(const FwdLaunch& p) const { return p.Nq; }
+  __device__ __forceinline__ int n_keys(const FwdLaunch& p) const { return p.Nk; }
+};
+
+// Work item over packed sequences (RAG): an entry of the plan's list, ordered
+// by work, and one or two query heads. Where the group is even (or a CTA holds
+// one query tile) an entry is one 128-row tile, and the two slots take the same
+// tile of two heads of a group: both see the same keys, so neither waits for
+// the other, and a sequence of one tile fills both. Else an entry is two
+// neighbouring tiles of one head.
+template <int NT, bool CAUSAL>
+struct FwdWork<NT, CAUSAL, false, true> {
+  static constexpr int kv0 = 0, s = 0;  // one key range
+  int bh, hs;                           // slot t's head is bh + t * hs
+  int row0, len;                        // the sequence's first row and length
+  int qt[NT], last_kv[NT], nkv;
+  __device__ FwdWork(int item, const FwdLaunch& p) {
+    const bool heads = NT > 1 && p.pair_heads;
+    const int units = heads ? p.BH / 2 : p.BH;
+    const int e = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(units));
+    const int4 x = __ldg((NT == 1 || heads ? packed_tiles(p.plan) : packed_pairs(p.plan)) + e);
+    row0 = x.x;
+    len = x.y;
+    hs = heads ? 1 : 0;
+    bh = (item - e * units) << hs;
+    const int T = (len + 127) >> 7;
+    nkv = 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      qt[t] = heads || NT == 1 ? x.z : 2 * x.z + t;
+      last_kv[t] = qt[t] < T ? (CAUSAL ? qt[t] : T - 1) : -1;
+      nkv = max(nkv, last_kv[t] + 1);
+    }
+  }
+  __device__ __forceinline__ int q_row(const FwdLaunch&, int t) const { return row0 + qt[t] * 128; }
+  __device__ __forceinline__ int q_head(int t) const { return bh + t * hs; }
+  __device__ __forceinline__ int kv_row(int j) const { return row0 + j * 128; }
+  __device__ __forceinline__ int kv_head(const FwdLaunch& p) const { return bh / p.group; }
+  __device__ __forceinline__ int n_queries(const FwdLaunch&) const { return len; }
+  __device__ __forceinline__ int n_keys(const FwdLaunch&) const { return len; }
 };
 
 // Persistent schedule: CTA b of G takes items in rounds k = 0, 1, ...; round
@@ -158,8 +207,12 @@ struct FwdWork {
 // similar total.
 __device__ __forceinline__ int sched_item(int k, int b, int G) { return k * G + ((k & 1) ? G - 1 - b : b); }
 
-template <bool PACK>
+template <bool PACK, bool RAG>
 __device__ __forceinline__ int total_items(const FwdLaunch& p, int NT) {
+  if constexpr (RAG) {
+    if (!packed_plan_ok(p.plan, p.Nq)) return 0;
+    return NT > 1 && !p.pair_heads ? p.plan->n_pairs * p.BH : p.plan->n_tiles * (p.BH / (NT > 1 ? 2 : 1));
+  }
   const int rph = rows_per_head<PACK>(p);
   const int Tq = (p.Nq + rph - 1) / rph;
   return (p.BH / heads_per_tile<PACK>(p)) * ((Tq + NT - 1) / NT) * p.splits;
@@ -175,14 +228,14 @@ __device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap* map, int c
 // ---------------------------------------------------------------------------
 // TMA producer (one thread)
 // ---------------------------------------------------------------------------
-template <int HD, bool CAUSAL, bool PACK>
+template <int HD, bool CAUSAL, bool PACK, bool RAG>
 __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV) {
   using C = FwdCfg<HD>;
   tma_prefetch_desc(&p.tmQ);
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
   tma_prefetch_desc(&p.tmO);
-  const int total = total_items<PACK>(p, C::NT);
+  const int total = total_items<PACK, RAG>(p, C::NT);
   const int G = gridDim.x;
   const uint64_t lim = p.wait_limit_ns;
   int kv = 0;     // running count of K/V tiles loaded by this CTA
@@ -194,9 +247,9 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
   for (int k = 0; k * G < total && !aborted; ++k) {
     const int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;
-    const FwdWork<C::NT, CAUSAL, PACK> wk(item, p);
+    const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;  // a key range with nothing to do (every role skips it)
-    const int kv_bh = wk.bh / p.group;  // grouped K/V heads: query head bh reads K/V head bh / g
+    const int kv_bh = wk.kv_head(p);
     // Q_t's smem was the previous item's O staging: wait until its store read
     // it. The item's first K/V tile is issued before that wait so it loads
     // while the previous epilogue runs. Each slot has its own q_full, and the
@@ -217,7 +270,7 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
 #pragma unroll
         for (int c = 0; c < C::CHUNKS; ++c)
           tma_load_3d(sQ + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmQ, &sh.q_full[t], c * 64,
-                      wk.qt[t] * rows_per_head<PACK>(p), wk.bh);
+                      wk.q_row(p, t), wk.q_head(t));
         q_item = items;
         q_mask |= 1u << t;
       }
@@ -232,8 +285,7 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
       mbar_arrive_expect_tx(&sh.k_full[ks], C::TILE_BYTES);
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c)
-        tma_load_3d(sK + ks * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmK, &sh.k_full[ks], c * 64, (wk.kv0 + j) * 128,
-                    kv_bh);
+        tma_load_3d(sK + ks * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmK, &sh.k_full[ks], c * 64, wk.kv_row(j), kv_bh);
       ++k_issued;
       if (j == 0) {
         if (!load_q()) {
@@ -246,13 +298,13 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
         // sequences, whose items hold only a few key tiles.
         const int next = (k + 1) * G < total ? sched_item(k + 1, blockIdx.x, G) : total;
         if (next < total) {
-          const FwdWork<C::NT, CAUSAL, PACK> wn(next, p);
+          const FwdWork<C::NT, CAUSAL, PACK, RAG> wn(next, p);
 #pragma unroll
           for (int t = 0; t < C::NT; ++t) {
             if (wn.nkv == 0 || wn.last_kv[t] < 0) continue;
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
-              tma_prefetch_l2_3d(&p.tmQ, c * 64, wn.qt[t] * rows_per_head<PACK>(p), wn.bh);
+              tma_prefetch_l2_3d(&p.tmQ, c * 64, wn.q_row(p, t), wn.q_head(t));
           }
         }
       }
@@ -264,8 +316,7 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
       mbar_arrive_expect_tx(&sh.v_full[vs], C::TILE_BYTES);
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c)
-        tma_load_3d(sV + vs * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmV, &sh.v_full[vs], c * 64, (wk.kv0 + j) * 128,
-                    kv_bh);
+        tma_load_3d(sV + vs * C::TILE_BYTES + c * C::CHUNK_BYTES, &p.tmV, &sh.v_full[vs], c * 64, wk.kv_row(j), kv_bh);
       ++v_issued;
     }
     if (aborted) break;
@@ -285,7 +336,7 @@ __device__ void fwd_load_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, ui
 // ---------------------------------------------------------------------------
 // MMA issuer (one thread)
 // ---------------------------------------------------------------------------
-template <int HD, bool CAUSAL, bool PACK>
+template <int HD, bool CAUSAL, bool PACK, bool RAG>
 __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uint8_t* sK, uint8_t* sV,
                              uint32_t tmem) {
   using C = FwdCfg<HD>;
@@ -293,10 +344,19 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   constexpr uint32_t kIdescPV = make_idesc_bf16_f32(128, HD, false, true);
   const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
   const uint64_t lim = p.wait_limit_ns;
-  const int total = total_items<PACK>(p, C::NT);
+  const int total = total_items<PACK, RAG>(p, C::NT);
   const int G = gridDim.x;
 
+  // Packed sequences: the whole warp walks the items (it clears the rows of V
+  // behind a sequence's last key), one lane issues.
+  const bool lead = !RAG || lane_id() == 0;
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
+    return RAG ? __all_sync(0xffffffffu, ok) : ok;
+  };
+
   auto issue_s = [&](int t, int g) {  // g: running K/V tile index
+    if (!lead) return;
     const uint32_t qa = q_addr + t * C::TILE_BYTES;
     const uint32_t ka = k_addr + (g % C::KST) * C::TILE_BYTES;
     const uint64_t qd = make_smem_desc_sw128(qa, 16, 1024), kd = make_smem_desc_sw128(ka, 16, 1024);
@@ -307,17 +367,18 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
     }
     umma_commit(&sh.s_full[t]);
   };
-  auto issue_pv = [&](int t, int g, bool first) {
+  auto issue_pv = [&](int t, int g, bool first, int steps) {  // steps: of 16 keys
+    if (!lead) return;
     const uint64_t vd = make_smem_desc_sw128(v_addr + (g % C::VST) * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
-      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
+      if (!RAG || ks < steps) umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
               (!first || ks > 0) ? 1u : 0u);
     umma_commit(&sh.pv_done[t]);
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_FWD_MMA);
-    drain_mmas(&sh.mma_drain, lim);
+    if (lead) drain_mmas(&sh.mma_drain, lim);
   };
 
   int kv = 0;             // running K/V tile index
@@ -326,32 +387,43 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   for (int k = 0; k * G < total; ++k) {
     const int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;
-    const FwdWork<C::NT, CAUSAL, PACK> wk(item, p);
+    const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;
-    if (!mbar_wait(&sh.k_full[kv % C::KST], (kv / C::KST) & 1, &sh.abort_flag, lim)) return fail();
+    if (!wait(&sh.k_full[kv % C::KST], (kv / C::KST) & 1)) return fail();
     tc_fence_after_sync();
 #pragma unroll
     for (int t = 0; t < C::NT; ++t) {
       if (wk.last_kv[t] < 0) continue;
       // S_t(0) overwrites S_t / P~_t of the previous item: its last PV must be done.
-      if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim))
+      if (C::P_ALIAS && cnt[t] > 0 && !wait(&sh.pv_done[t], (cnt[t] - 1) & 1))
         return fail();
-      if (!mbar_wait(&sh.q_full[t], items & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.q_full[t], items & 1)) return fail();
       tc_fence_after_sync();
       issue_s(t, kv);
     }
-    umma_commit(&sh.k_empty[kv % C::KST]);
+    if (lead) umma_commit(&sh.k_empty[kv % C::KST]);
 
     for (int j = 0; j < wk.nkv; ++j) {
       const int g = kv + j;
       const int vs = g % C::VST;
-      if (!mbar_wait(&sh.v_full[vs], (g / C::VST) & 1, &sh.abort_flag, lim)) return fail();
+      if (!wait(&sh.v_full[vs], (g / C::VST) & 1)) return fail();
+      // The last tile of a sequence ends in rows of the next one, whatever they
+      // hold: whole steps of 16 keys are left out of the product, and the rows
+      // of the last step taken are cleared (their weights are 0, but 0 * NaN).
+      int steps = 8;
+      if constexpr (RAG) {
+        const int held = wk.len - j * 128;
+        if (held < 128) {
+          steps = (held + 15) >> 4;
+          clear_rows<C::CHUNKS, C::CHUNK_BYTES>(v_addr + vs * C::TILE_BYTES, held, 16 * steps);
+        }
+      }
       const bool has_next = j + 1 < wk.nkv;
       const int gn = g + 1;
       bool k_next_ready = false;
       auto wait_k_next = [&]() -> bool {
         if (k_next_ready) return true;
-        if (!mbar_wait(&sh.k_full[gn % C::KST], (gn / C::KST) & 1, &sh.abort_flag, lim)) return false;
+        if (!wait(&sh.k_full[gn % C::KST], (gn / C::KST) & 1)) return false;
         tc_fence_after_sync();
         k_next_ready = true;
         return true;
@@ -359,24 +431,24 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
 #pragma unroll
       for (int t = 0; t < C::NT; ++t) {
         if (j > wk.last_kv[t]) continue;
-        if (!mbar_wait(&sh.p_full[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+        if (!wait(&sh.p_full[t], (cnt[t] + j) & 1)) return fail();
         // PV_t(0) overwrites O~_t: the previous item's epilogue must have read it.
-        if (j == 0 && items > 0 && !mbar_wait(&sh.o_free[t], (items - 1) & 1, &sh.abort_flag, lim)) return fail();
+        if (j == 0 && items > 0 && !wait(&sh.o_free[t], (items - 1) & 1)) return fail();
         tc_fence_after_sync();
-        issue_pv(t, g, j == 0);
+        issue_pv(t, g, j == 0, steps);
         if (has_next && j + 1 <= wk.last_kv[t]) {
           if (!wait_k_next()) return fail();
           // d = 128: S_t(j+1) overwrites the TMEM columns P_t(j) is read
           // from, so it follows PV_t(j) directly, before the other tile's PV:
           // tile t's products then run while the other tile is in its
           // softmax (the two tiles alternate instead of moving in lockstep).
-          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return fail();
+          if (C::P_ALIAS && !wait(&sh.pv_done[t], (cnt[t] + j) & 1)) return fail();
           tc_fence_after_sync();
           issue_s(t, gn);
         }
       }
-      if (has_next) umma_commit(&sh.k_empty[gn % C::KST]);
-      umma_commit(&sh.v_empty[vs]);
+      if (lead && has_next) umma_commit(&sh.k_empty[gn % C::KST]);
+      if (lead) umma_commit(&sh.v_empty[vs]);
     }
 #pragma unroll
     for (int t = 0; t < C::NT; ++t)
@@ -386,13 +458,13 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  drain_mmas(&sh.mma_drain, lim);
+  if (lead) drain_mmas(&sh.mma_drain, lim);
 }
 
 // ---------------------------------------------------------------------------
 // Softmax + correction + epilogue (warpgroup t owns query-tile slot t)
 // ---------------------------------------------------------------------------
-template <int HD, bool CAUSAL, bool PACK>
+template <int HD, bool CAUSAL, bool PACK, bool RAG>
 __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uint32_t tmem, int t) {
   using C = FwdCfg<HD>;
   const int r = threadIdx.x & 127;
@@ -400,11 +472,9 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
   const uint32_t tS = tmem + lane_base + C::s_col(t);
   const uint32_t tP = tmem + lane_base + C::p_col(t);
   const uint32_t tO = tmem + lane_base + C::o_col(t);
-  const int Nq = p.Nq, Nk = p.Nk;
-  const int Tk = (Nk + 127) / 128;
   const float c2 = p.scale_log2;
   const uint64_t lim = p.wait_limit_ns;
-  const int total = total_items<PACK>(p, C::NT);
+  const int total = total_items<PACK, RAG>(p, C::NT);
   const int G = gridDim.x;
   uint8_t* stage = sQ + t * C::TILE_BYTES;  // O staging: Q_t once its last S MMA is done
   // After a timed-out wait a warp stops working but keeps passing every named
@@ -416,14 +486,16 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
   for (int k = 0; k * G < total; ++k) {
     const int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;
-    const FwdWork<C::NT, CAUSAL, PACK> wk(item, p);
+    const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;
     const int qt = wk.qt[t];
     const int last_kv = wk.last_kv[t];
     // this thread's query: position `row` of head `head` (rph is a power of two)
     const int rph = rows_per_head<PACK>(p);
     const int row = qt * rph + (r & (rph - 1));
-    const int head = wk.bh + r / rph;
+    const int head = wk.q_head(t) + r / rph;
+    const int Nq = wk.n_queries(p), Nk = wk.n_keys(p);
+    const int Tk = (Nk + 127) / 128;
 
     float m2 = -INFINITY;  // reference max of S * scale * log2(e)
     float l = 0.f;         // running sum of P~ (unrounded fp32)
@@ -454,10 +526,10 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       // boundary crosses (key > row + causal_off).
       const int a = wk.kv0 + j;  // absolute key tile
       const bool mask_tail = (a == Tk - 1) && (Nk & 127);
-      const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + p.causal_off);
+      const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + (RAG ? 0 : p.causal_off));
       if (mask_tail || mask_diag) {
         int lim_col = Nk - 1 - a * 128;
-        if (CAUSAL) lim_col = min(lim_col, row + p.causal_off - a * 128);
+        if (CAUSAL) lim_col = min(lim_col, row + (RAG ? 0 : p.causal_off) - a * 128);
 #pragma unroll
         for (int i = 0; i < 128; ++i)
           if (i > lim_col) s[i] = -INFINITY;
@@ -478,7 +550,8 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       // rescaled); otherwise P~ = 2^(S c - m2) <= 2^kRescaleSlack. Either way
       // O~ / l is the same in exact arithmetic.
       const float m_run = fmaxf(m2, mx * c2);
-      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack);
+      // Rows behind a packed sequence's last one, another's, have no say in it.
+      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && (!RAG || row < Nq));
       const float m_ref = move ? m_run : m2;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m2 - m_use);  // 0 on the first block, 1 when the reference is kept
@@ -535,7 +608,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     // never reads it.
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     const float lse_row = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
-    if (alive && active && p.splits > 1) {
+    if (!RAG && alive && active && p.splits > 1) {
       // fp32 partial of this key range, straight from TMEM to the workspace
       float* dst = p.o_part + ((static_cast<size_t>(wk.s) * p.BH + head) * Nq + row) * HD;
 #pragma unroll 1
@@ -578,7 +651,12 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
         }
       }
       fence_proxy_async_smem();
-      if (row < Nq) p.lse[static_cast<size_t>(head) * Nq + row] = lse_row;
+      if (row < Nq) {
+        if constexpr (RAG)
+          p.lse[static_cast<size_t>(head) * p.Nq + wk.row0 + row] = lse_row;
+        else
+          p.lse[static_cast<size_t>(head) * Nq + row] = lse_row;
+      }
     } else {
       // No query tile in this slot: nothing waits for this warpgroup, so it
       // first waits for the item's Q load. That keeps its q_free / o_free
@@ -591,11 +669,29 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       mbar_arrive(&sh.o_free[t]);
     }
     named_barrier_sync(1 + t, 128);
+    // Packed sequences: the rows past a sequence's last one are the next one's,
+    // so its last tile leaves through plain stores, a row by HD / 8 lanes.
+    const bool cut = RAG && active && qt * 128 + 128 > Nq;
+    if constexpr (RAG) {
+      if (cut) {
+        constexpr int UNITS = HD / 8;
+        if (alive && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
+          __nv_bfloat16* dst = p.o + static_cast<long long>(wk.row0 + qt * 128) * p.o_strides[0] + head * p.o_strides[1];
+          const uint32_t from = smem_u32(stage);
+          for (int i = r; i < (Nq - qt * 128) * UNITS; i += 128) {
+            const int y = i / UNITS, x = i % UNITS;
+            *reinterpret_cast<uint4*>(dst + y * p.o_strides[0] + 8 * x) =
+                ld_shared_v4(from + (x >> 3) * C::CHUNK_BYTES + sw128_offset(y, x & 7));
+          }
+        }
+        named_barrier_sync(1 + t, 128);
+      }
+    }
     if (r == 0) {
-      if (alive && active && p.splits == 1 && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
+      if (!cut && alive && active && (RAG || p.splits == 1) && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
 #pragma unroll
         for (int c = 0; c < C::CHUNKS; ++c)
-          tma_store_3d(&p.tmO, stage + c * C::CHUNK_BYTES, c * 64, qt * rph, wk.bh);
+          tma_store_3d(&p.tmO, stage + c * C::CHUNK_BYTES, c * 64, wk.q_row(p, t), wk.q_head(t));
         tma_store_commit();
         tma_store_wait_read_all();  // the staging can be overwritten by the next Q tile
       }
@@ -607,7 +703,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
   if (r == 0) tma_store_wait_all();  // O stores complete before the CTA can exit
 }
 
-template <int HD, bool CAUSAL, bool PACK>
+template <int HD, bool CAUSAL, bool PACK, bool RAG>
 __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_constant__ FwdLaunch p) {
   using C = FwdCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
@@ -619,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5;
   // Split key ranges: the combine kernel queued next may take SMs as this
   // grid's CTAs leave them (it waits for this grid before it reads).
-  if (p.splits > 1) griddep_launch_dependents();
+  if (!RAG && p.splits > 1) griddep_launch_dependents();
+  if (RAG && blockIdx.x == 0 && threadIdx.x == 0 && !packed_plan_ok(p.plan, p.Nq)) record_bad_index(p.status, WHERE_PACKED);
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) mbar_init(&sh.q_full[t], 1);
@@ -651,11 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_consta
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) fwd_load_role<HD, CAUSAL, PACK>(p, sh, sQ, sK, sV);
+    if (lane_id() == 0) fwd_load_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, sK, sV);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) fwd_mma_role<HD, CAUSAL, PACK>(p, sh, sQ, sK, sV, tmem);
+    if (RAG || lane_id() == 0) fwd_mma_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, sK, sV, tmem);
   } else if (warp < 4 * C::NT) {
-    fwd_softmax_role<HD, CAUSAL, PACK>(p, sh, sQ, tmem, warp >> 2);
+    fwd_softmax_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, tmem, warp >> 2);
   }
 
   tc_fence_before_sync();
@@ -664,15 +761,18 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_consta
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int HD, bool CAUSAL, bool PACK>
+template <int HD, bool CAUSAL, bool PACK, bool RAG = false>
 cudaError_t launch_fwd_t(const FwdLaunch& a, cudaStream_t stream) {
   using C = FwdCfg<HD>;
-  auto kern = fa_fwd_kernel<HD, CAUSAL, PACK>;
+  auto kern = fa_fwd_kernel<HD, CAUSAL, PACK, RAG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int rph = PACK ? a.rph : 128;
   const int Tq = (a.Nq + rph - 1) / rph;
-  const long long items = static_cast<long long>(a.BH / (PACK ? a.pack : 1)) * ((Tq + C::NT - 1) / C::NT) * a.splits;
+  // Packed sequences: the plan, on the device, knows how many items there are
+  // (at most one for each row and head).
+  const long long items = RAG ? static_cast<long long>(a.Nq) * a.BH
+                              : static_cast<long long>(a.BH / (PACK ? a.pack : 1)) * ((Tq + C::NT - 1) / C::NT) * a.splits;
   // Persistent: one CTA per SM (the smem footprint allows no more), each
   // looping over its share of the items.
   const long long grid = items < a.num_sms ? items : a.num_sms;

@@ -2,6 +2,7 @@
 // translation units. Host-side only; no torch types anywhere.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
@@ -31,8 +32,12 @@ enum : uint32_t {
   WHERE_KV8_CONVERT = 42,
   WHERE_KV8_MMA = 43,
   WHERE_KV8_SOFTMAX = 44,
+  WHERE_PACKED_PLAN = 51,
+  WHERE_PACKED = 52,
   WHERE_PROBE = 99,
 };
+
+struct PackedPlan;  // fa_packed.cuh
 
 // Tiles of the [B*H][N][d] bf16 tensors, as seen by TMA: 128 rows x 64
 // columns per box, 128-byte swizzle.
@@ -54,6 +59,11 @@ struct FwdLaunch {
   uint64_t wait_limit_ns;
   int num_sms;
   uint32_t debug_skip;  // test hook: role (WHERE_*) whose first arrival block 0 leaves out; 0 = none
+  // packed sequences (launch_fwd_ragged): tensors are [rows][heads][d] at their own
+  // strides, Nq = Nk the rows, BH the query heads
+  const PackedPlan* plan;
+  long long o_strides[2];  // of a row and a head, in elements
+  int pair_heads;          // the two query tiles of a CTA are two heads' (an even group) instead of one head's
 };
 
 struct BwdLaunch {
@@ -84,6 +94,10 @@ struct BwdLaunch {
   // stream, which must be the dK/dV pass of the same call (it reads nothing
   // that pass writes); it still completes only after that pass has.
   int overlap_prev;
+  // packed sequences (`plan` set): N rows, BH and BHkv heads; D and lse2 are [BH][N],
+  // kv_part [chunks][BHkv][N][d] with `chunks` in sched[4]
+  const PackedPlan* plan;
+  long long dq_strides[2], dk_strides[2], dv_strides[2];  // of a row and a head, in elements
 };
 
 // Checks of the sizes, flag and scale common to every entry point; *empty is
@@ -110,6 +124,26 @@ cudaError_t allow_smem(Kernel kern, int bytes, int device, std::atomic<uint64_t>
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
+// [rows][heads][d] bf16 at the given strides of a row and a head (in elements),
+// boxes of box_rows rows of a head x 64 columns, 128-byte swizzle (fa_api.cu).
+bool make_rows_map(CUtensorMap* m, const void* base, int rows, int heads, int d, const long long (&strides)[2],
+                   unsigned box_rows);
+fa_status_t check_heads(int Hq, int Hkv);  // grouped K/V heads: Hkv >= 1 dividing Hq (fa_api.cu)
+// Do rows of d elements at these strides stay apart? Sorted by stride, each
+// dimension has to step over everything the smaller ones cover.
+template <int N>
+bool rows_apart(const int (&size)[N], const long long (&stride)[N], int d) {
+  int o[N];
+  for (int i = 0; i < N; ++i) o[i] = i;
+  std::sort(o, o + N, [&](int a, int b) { return stride[a] < stride[b]; });
+  long long span = d;
+  for (int i : o) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < span) return false;
+    span += (size[i] - 1) * stride[i];
+  }
+  return true;
+}
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Launchers (defined in the kernel translation units). Return cudaSuccess or
@@ -117,6 +151,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_fwd_combine(const FwdLaunch& a, cudaStream_t stream);  // splits > 1: merge the partials
 cudaError_t launch_fwd_packed(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_pack.cu: pack > 1
+cudaError_t launch_fwd_ragged(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_ragged.cu: plan set
 cudaError_t launch_bwd_pre(const BwdLaunch& a, cudaStream_t stream);   // D, base-2 L, zero dQ accumulator
 cudaError_t launch_bwd_main(const BwdLaunch& a, cudaStream_t stream);  // dK, dV; dQ into the accumulator
 cudaError_t launch_bwd_post(const BwdLaunch& a, cudaStream_t stream);  // dQ = bf16(accumulator)

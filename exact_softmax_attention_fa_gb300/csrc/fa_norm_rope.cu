@@ -1,5 +1,6 @@
 // Per-head RMS norm of queries and keys with the position rotation in the same
-// pass, and its gradients (fa_norm_rope_fwd / _bwd of fa.h).
+// pass, and its gradients (fa_norm_rope_fwd / _bwd and fa_norm_rope_axes_fwd /
+// _bwd of fa.h).
 //
 //   z = x r w, r = 1/sqrt(mean(x^2) + eps);  y = R(pos) z
 //   g = R(pos)^T dy, h = g w, dx = r (h - x r^2 mean(h x)), dw = sum g x r
@@ -59,6 +60,8 @@ struct NormRope {
   int N, tokens, H[3], chunks[3];  // chunks: lane groups a token needs for q, k, v
   int rot, half, table_rows;
   float eps;
+  int axes;                    // positions hold this many planes of [B][N] (rotation by axes)
+  uint32_t axis[8];            // the axis of pair i: bits 2 (i % 16) of word i / 16
 };
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -120,6 +123,31 @@ struct Lane {
     s[0] = make_float2(y.x, y.y), s[1] = make_float2(y.z, y.w);
   }
 
+  // Angles of a lane whose four pairs follow axes: pair i at the position of its
+  // own axis. Where they share one, as in a table whose axes have their pairs in
+  // blocks, the four come as one vector; else entry by entry.
+  __device__ __forceinline__ void load_angles(const NormRope& p, const int (&pos)[4]) {
+    if (!turned) return;
+    const uint32_t ax = p.axis[angle >> 4] >> (2 * (angle & 15)) & 255u;
+    auto at = [&](int i) {
+      const uint32_t t = ax >> (2 * i) & 3u;
+      return t < 2 ? (t == 0 ? pos[0] : pos[1]) : (t == 2 ? pos[2] : pos[3]);
+    };
+    if (ax == (ax & 3u) * 0x55u) {
+      load_angles(p, at(0));
+      return;
+    }
+    float x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const size_t e = static_cast<size_t>(at(i)) * p.half + angle + i;
+      x[i] = __ldg(p.cos_t + e);
+      y[i] = __ldg(p.sin_t + e);
+    }
+    c[0] = make_float2(x[0], x[1]), c[1] = make_float2(x[2], x[3]);
+    s[0] = make_float2(y[0], y[1]), s[1] = make_float2(y[2], y[3]);
+  }
+
   // z <- R z (BACK: R^T z)
   template <bool BACK>
   __device__ __forceinline__ void rotate(Cols& z) const {
@@ -170,11 +198,29 @@ struct Lane {
   }
 };
 
-__device__ __forceinline__ int position(const NormRope& p, int token, int n) {
-  return p.positions ? __ldg(p.positions + token) : n;
+// The token's angles into the lane; false, recorded once, where a position is outside the tables.
+template <bool AXES, class L>
+__device__ __forceinline__ bool take_angles(L& lane, const NormRope& p, int token, int n, uint32_t where) {
+  bool ok = true;
+  if constexpr (AXES) {
+    int pos[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (a < p.axes) {
+        pos[a] = __ldg(p.positions + static_cast<size_t>(a) * p.tokens + token);
+        ok = ok && pos[a] >= 0 && pos[a] < p.table_rows;
+      }
+    if (ok) lane.load_angles(p, pos);
+  } else {
+    const int pos = p.positions ? __ldg(p.positions + token) : n;
+    ok = pos >= 0 && pos < p.table_rows;
+    if (ok) lane.load_angles(p, pos);
+  }
+  if (!ok && lane.angle == 0) record_bad_index(p.status, where);
+  return ok;
 }
 
-template <int D, bool INTER, bool NORM>
+template <int D, bool INTER, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __grid_constant__ NormRope p) {
   Lane<D, INTER> L;
   L.init(p);
@@ -201,14 +247,7 @@ __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __
       if (u < nh) L.store(dst + u * step, raw[u][0], raw[u][1]);
     return;
   }
-  if (p.rot > 0) {
-    const int pos = position(p, token, n);
-    if (pos < 0 || pos >= p.table_rows) {
-      if (L.angle == 0) record_bad_index(p.status, WHERE_NORM_ROPE);
-      return;
-    }
-    L.load_angles(p, pos);
-  }
+  if (p.rot > 0 && !take_angles<AXES>(L, p, token, n, WHERE_NORM_ROPE)) return;
   float2 w[4];
   if (NORM) L.load_weights(p, kind, w);
 #pragma unroll
@@ -234,7 +273,7 @@ __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __
 // next two on their way. Each lane sums dw of its 8 columns over the rows it
 // meets; the block's lane groups are added in order, and norm_rope_dw_kernel
 // adds the blocks in order, so dw does not depend on timing.
-template <int D, bool INTER, bool NORM>
+template <int D, bool INTER, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
   constexpr int GROUPS = kThreads / (D / 8), SIDE = kBwdSide;
   __shared__ float red[GROUPS][D];
@@ -271,14 +310,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
         }
     };
     fetch(0);
-    if (kind < 2 && p.rot > 0) {
-      const int pos = position(p, token, n);
-      if (pos < 0 || pos >= p.table_rows) {
-        if (L.angle == 0) record_bad_index(p.status, WHERE_NORM_ROPE_BWD);
-        continue;
-      }
-      L.load_angles(p, pos);
-    }
+    if (kind < 2 && p.rot > 0 && !take_angles<AXES>(L, p, token, n, WHERE_NORM_ROPE_BWD)) continue;
 #pragma unroll 1
     for (int h = 0; h < nh; h += SIDE) {
       uint2 g_now[SIDE][2], x_now[SIDE][2];
@@ -355,40 +387,46 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
   }
 }
 
+template <bool BACK, int D, bool INTER, bool NORM>
+cudaError_t launch_norm_rope_t(const NormRope& a, int blocks, cudaStream_t stream) {
+  if (a.axes) {
+    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, true><<<blocks, kThreads, 0, stream>>>(a);
+    else norm_rope_fwd_kernel<D, INTER, NORM, true><<<blocks, kFwdThreads, 0, stream>>>(a);
+  } else {
+    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, false><<<blocks, kThreads, 0, stream>>>(a);
+    else norm_rope_fwd_kernel<D, INTER, NORM, false><<<blocks, kFwdThreads, 0, stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+template <bool BACK, int D>
+cudaError_t launch_norm_rope_d(const NormRope& a, int interleaved, int blocks, cudaStream_t stream) {
+  if (a.w[0])
+    return interleaved ? launch_norm_rope_t<BACK, D, true, true>(a, blocks, stream)
+                       : launch_norm_rope_t<BACK, D, false, true>(a, blocks, stream);
+  return interleaved ? launch_norm_rope_t<BACK, D, true, false>(a, blocks, stream)
+                     : launch_norm_rope_t<BACK, D, false, false>(a, blocks, stream);
+}
+
 template <bool BACK>
 cudaError_t launch_norm_rope(const NormRope& a, int d, int interleaved, int blocks, cudaStream_t stream) {
-#define FA_NORM_ROPE_KERNEL(D, I, N) (BACK ? norm_rope_bwd_kernel<D, I, N> : norm_rope_fwd_kernel<D, I, N>)
-#define FA_NORM_ROPE(D)                                                                                     \
-  if (d == D) {                                                                                             \
-    auto kern = a.w[0] ? (interleaved ? FA_NORM_ROPE_KERNEL(D, true, true) : FA_NORM_ROPE_KERNEL(D, false, true)) \
-                       : (interleaved ? FA_NORM_ROPE_KERNEL(D, true, false) : FA_NORM_ROPE_KERNEL(D, false, false)); \
-    kern<<<blocks, BACK ? kThreads : kFwdThreads, 0, stream>>>(a);                                          \
-    return cudaGetLastError();                                                                              \
+  switch (d) {
+    case 64: return launch_norm_rope_d<BACK, 64>(a, interleaved, blocks, stream);
+    case 128: return launch_norm_rope_d<BACK, 128>(a, interleaved, blocks, stream);
+    case 256: return launch_norm_rope_d<BACK, 256>(a, interleaved, blocks, stream);
+    default: return cudaErrorInvalidValue;
   }
-  FA_NORM_ROPE(64)
-  FA_NORM_ROPE(128)
-  FA_NORM_ROPE(256)
-#undef FA_NORM_ROPE
-#undef FA_NORM_ROPE_KERNEL
-  return cudaErrorInvalidValue;
 }
 
-// Do rows of d elements at these strides stay apart? Sorted by stride, each
-// dimension has to step over everything the smaller ones cover.
-bool rows_apart(const int (&size)[3], const long long (&stride)[3], int d) {
-  int o[3] = {0, 1, 2};
-  std::sort(o, o + 3, [&](int a, int b) { return stride[a] < stride[b]; });
-  long long span = d;
-  for (int i : o) {
-    if (size[i] <= 1) continue;
-    if (stride[i] < span) return false;
-    span += (size[i] - 1) * stride[i];
-  }
-  return true;
-}
+// The axis of each pair: `axis` null for a rotation by one position, else a host
+// array of rot / 2 entries below n_axes, and positions for each axis are needed.
+struct Axes {
+  const unsigned char* axis;
+  int n;
+};
 
 // Checks and arguments shared by the two directions.
-fa_status_t prepare(const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
+fa_status_t prepare(const Axes* axes, const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
                     const float* sin_t, int table_rows, const int* positions, int B, int Hq, int Hkv, int N, int d,
                     int rot, int interleaved, float eps, bool with_v, int heads, bool* empty, NormRope* a) {
   if (B < 0 || Hq < 0 || Hkv < 0 || N < 0 || table_rows < 0) return FA_ERR_INVALID_ARG;
@@ -404,6 +442,14 @@ fa_status_t prepare(const long long* strides, const void* wq, const void* wk, in
   if (rot > 0) {
     if (!cos_t || !sin_t || table_rows == 0 || (!positions && N > table_rows)) return FA_ERR_INVALID_ARG;
     if (!aligned(cos_t, 16) || !aligned(sin_t, 16) || !aligned(positions, 4)) return FA_ERR_MISALIGNED;
+    if (axes) {
+      if (!axes->axis || !positions || axes->n < 1 || axes->n > 4) return FA_ERR_INVALID_ARG;
+      a->axes = axes->n;
+      for (int i = 0; i < rot / 2; ++i) {
+        if (axes->axis[i] >= axes->n) return FA_ERR_INVALID_ARG;
+        a->axis[i / 16] |= static_cast<uint32_t>(axes->axis[i]) << (2 * (i % 16));
+      }
+    }
   }
   if (!aligned(wq, 16) || !aligned(wk, 16)) return FA_ERR_MISALIGNED;
   if (!strides) return FA_ERR_INVALID_ARG;
@@ -459,14 +505,24 @@ using namespace fa;
 
 extern "C" {
 
-fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_in, const long long* strides,
-                             const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
-                             int table_rows, const int* positions, void* q, void* k, void* v, int B, int Hq, int Hkv,
-                             int N, int d, int rot, int interleaved, float eps, cudaStream_t stream) {
+size_t fa_norm_rope_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d) {
+  if (B <= 0 || Hq < 0 || Hkv < 0 || Hq + static_cast<long long>(Hkv) == 0 || N <= 0) return 0;
+  if (d != 64 && d != 128 && d != 256) return 0;
+  return static_cast<size_t>(2) * kMaxBwdBlocks * d * sizeof(float);
+}
+
+}  // extern "C"
+
+namespace {
+
+fa_status_t norm_rope_fwd(const Axes* axes, const void* q_in, const void* k_in, const void* v_in, const long long* strides,
+                          const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
+                          int table_rows, const int* positions, void* q, void* k, void* v, int B, int Hq, int Hkv,
+                          int N, int d, int rot, int interleaved, float eps, cudaStream_t stream) {
   NormRope a{};
   bool empty = false;
   if ((v_in == nullptr) != (v == nullptr)) return FA_ERR_INVALID_ARG;
-  fa_status_t st = prepare(strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv, N, d, rot,
+  fa_status_t st = prepare(axes, strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv, N, d, rot,
                            interleaved, eps, v != nullptr, kHeads, &empty, &a);
   if (st != FA_OK || empty) return st;
   const void* in[3] = {q_in, k_in, v_in};
@@ -489,22 +545,16 @@ fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_i
   return from_cuda(launch_norm_rope<false>(a, d, interleaved, static_cast<int>((units + groups - 1) / groups), stream));
 }
 
-size_t fa_norm_rope_bwd_workspace_size(int B, int Hq, int Hkv, int N, int d) {
-  if (B <= 0 || Hq < 0 || Hkv < 0 || Hq + static_cast<long long>(Hkv) == 0 || N <= 0) return 0;
-  if (d != 64 && d != 128 && d != 256) return 0;
-  return static_cast<size_t>(2) * kMaxBwdBlocks * d * sizeof(float);
-}
-
-fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
-                             const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
-                             const float* sin_t, int table_rows, const int* positions, void* dq_in, void* dk_in,
-                             void* dv_in, const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv,
-                             int N, int d, int rot, int interleaved, float eps, void* workspace,
-                             size_t workspace_bytes, cudaStream_t stream) {
+fa_status_t norm_rope_bwd(const Axes* axes, const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
+                          const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
+                          const float* sin_t, int table_rows, const int* positions, void* dq_in, void* dk_in,
+                          void* dv_in, const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv,
+                          int N, int d, int rot, int interleaved, float eps, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
   NormRope a{};
   bool empty = false;
   if ((dv == nullptr) != (dv_in == nullptr)) return FA_ERR_INVALID_ARG;
-  fa_status_t st = prepare(wq ? strides : out_strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv,
+  fa_status_t st = prepare(axes, wq ? strides : out_strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, B, Hq, Hkv,
                            N, d, rot, interleaved, eps, dv != nullptr, kBwdHeads, &empty, &a);
   if (st != FA_OK) return st;
   const bool norm = wq != nullptr;
@@ -524,7 +574,7 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
       if (!aligned(in[t], 16) || !aligned(out[t], 16)) return FA_ERR_MISALIGNED;
       st = take_strides(out_strides, t, B, a.H[t], N, a.ds[t]);
       if (st != FA_OK) return st;
-      if (!rows_apart({B, a.H[t], N}, a.ds[t], d)) return FA_ERR_INVALID_ARG;
+      if (!rows_apart<3>({B, a.H[t], N}, a.ds[t], d)) return FA_ERR_INVALID_ARG;
       a.dy[t] = static_cast<const __nv_bfloat16*>(in[t]);
       a.dx[t] = static_cast<__nv_bfloat16*>(out[t]);
       if (norm && t < 2) {
@@ -564,6 +614,52 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
   cfg.numAttrs = 1;
   return from_cuda(cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.part), dwq, dwk,
                                       a.blocks[0], a.blocks[1], d));
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_norm_rope_fwd(const void* q_in, const void* k_in, const void* v_in, const long long* strides,
+                             const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
+                             int table_rows, const int* positions, void* q, void* k, void* v, int B, int Hq, int Hkv,
+                             int N, int d, int rot, int interleaved, float eps, cudaStream_t stream) {
+  return norm_rope_fwd(nullptr, q_in, k_in, v_in, strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, q, k,
+                       v, B, Hq, Hkv, N, d, rot, interleaved, eps, stream);
+}
+
+fa_status_t fa_norm_rope_axes_fwd(const void* q_in, const void* k_in, const void* v_in, const long long* strides,
+                                  const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
+                                  int table_rows, const int* positions, const unsigned char* axes, int n_axes, void* q,
+                                  void* k, void* v, int B, int Hq, int Hkv, int N, int d, int rot, int interleaved,
+                                  float eps, cudaStream_t stream) {
+  const Axes a{axes, n_axes};
+  return norm_rope_fwd(&a, q_in, k_in, v_in, strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions, q, k, v, B,
+                       Hq, Hkv, N, d, rot, interleaved, eps, stream);
+}
+
+fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
+                             const long long* strides, const void* wq, const void* wk, int w_bf16, const float* cos_t,
+                             const float* sin_t, int table_rows, const int* positions, void* dq_in, void* dk_in,
+                             void* dv_in, const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv,
+                             int N, int d, int rot, int interleaved, float eps, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+  return norm_rope_bwd(nullptr, dq, dk, dv, q_in, k_in, strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions,
+                       dq_in, dk_in, dv_in, out_strides, dwq, dwk, B, Hq, Hkv, N, d, rot, interleaved, eps, workspace,
+                       workspace_bytes, stream);
+}
+
+fa_status_t fa_norm_rope_axes_bwd(const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
+                                  const long long* strides, const void* wq, const void* wk, int w_bf16,
+                                  const float* cos_t, const float* sin_t, int table_rows, const int* positions,
+                                  const unsigned char* axes, int n_axes, void* dq_in, void* dk_in, void* dv_in,
+                                  const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv, int N,
+                                  int d, int rot, int interleaved, float eps, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  const Axes a{axes, n_axes};
+  return norm_rope_bwd(&a, dq, dk, dv, q_in, k_in, strides, wq, wk, w_bf16, cos_t, sin_t, table_rows, positions,
+                       dq_in, dk_in, dv_in, out_strides, dwq, dwk, B, Hq, Hkv, N, d, rot, interleaved, eps, workspace,
+                       workspace_bytes, stream);
 }
 
 }  // extern "C"

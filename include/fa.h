@@ -397,6 +397,89 @@ fa_status_t fa_norm_rope_bwd(const void* dq, const void* dk, const void* dv, con
                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The same rotation by several axes (time, height and width of the tokens of
+ * images and video): pair i turns by the position of its own axis,
+ *   c = cos_t[pos[axis[i]]][i],  s = sin_t[pos[axis[i]]][i].
+ *   positions : int32 [n_axes][B][N], not null. A token with any position outside the
+ *            tables is treated as in fa_norm_rope_fwd.
+ *   axes   : HOST array of rot / 2 entries below n_axes: the axis of each pair, in
+ *            blocks, taking turns, or as it may be
+ *   n_axes : 1 to 4 (with rot = 0 axes and n_axes are not used)
+ * The tables hold pair i's angle at every position in column i, so axes that each
+ * begin their frequencies anew are a matter of the tables. All else as for
+ * fa_norm_rope_fwd and fa_norm_rope_bwd (whose workspace size serves here too).
+ */
+fa_status_t fa_norm_rope_axes_fwd(const void* q_in, const void* k_in, const void* v_in, const long long* strides,
+                                  const void* wq, const void* wk, int w_bf16, const float* cos_t, const float* sin_t,
+                                  int table_rows, const int* positions, const unsigned char* axes, int n_axes, void* q,
+                                  void* k, void* v, int B, int Hq, int Hkv, int N, int d, int rot, int interleaved,
+                                  float eps, cudaStream_t stream);
+fa_status_t fa_norm_rope_axes_bwd(const void* dq, const void* dk, const void* dv, const void* q_in, const void* k_in,
+                                  const long long* strides, const void* wq, const void* wk, int w_bf16,
+                                  const float* cos_t, const float* sin_t, int table_rows, const int* positions,
+                                  const unsigned char* axes, int n_axes, void* dq_in, void* dk_in, void* dv_in,
+                                  const long long* out_strides, float* dwq, float* dwk, int B, int Hq, int Hkv, int N,
+                                  int d, int rot, int interleaved, float eps, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * Attention over packed sequences of different lengths (whole prompts, documents
+ * of a training batch, the patches of images): the forward and backward pass of
+ * fa_fwd_gqa and fa_bwd_gqa for every sequence by itself, without padding.
+ *   cu_seqlens : int32 [B + 1], device memory; sequence b is rows cu_seqlens[b] ..
+ *            cu_seqlens[b + 1] - 1 of the `rows` rows of every tensor. A sequence
+ *            may be empty, and rows before the first and behind the last may
+ *            belong to none.
+ *   strides : HOST array, for each tensor the elements from a row to the next and
+ *            from a head to the next (fa_fwd_packed: q, k, v, o; fa_bwd_packed:
+ *            q, k, v, o, dO and, as grad_strides, dq, dk, dv): row n of head h
+ *            starts at base + n*row stride + h*head stride, its d values
+ *            contiguous. Positive multiples of 8 below 2^38; a dimension of size 1
+ *            may have any. So the views of a packed projection need no copy, and
+ *            neither do tensors with the heads outside. The rows of an output may
+ *            not overlap each other (FA_ERR_INVALID_ARG) or an input.
+ *
+ * fa_packed_plan lists the batch's work on the device, most work first. It
+ * depends on the lengths alone: one plan serves all layers of a step and both
+ * directions, from any number of streams, and no call reads lengths on the host.
+ *   plan   : out, fa_packed_plan_size(B, rows) bytes of device memory, 256-byte
+ *            aligned. cu_seqlens is not read after this call.
+ *   causal : the mask of the calls it is for. A plan serves the other mask too;
+ *            only the order of the work is then not the best.
+ *   Lengths that are not 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= rows are
+ *   recorded as FA_ERR_INDEX (role 51) and make a plan without sequences.
+ *
+ * fa_fwd_packed:
+ *   q, o : bf16 [rows][Hq][d]; k, v : bf16 [rows][Hkv][d], at the given strides
+ *   lse  : out, fp32 [Hq][rows], natural log
+ *   plan : of the same `rows` (else the call does nothing but record FA_ERR_INDEX, role 52)
+ *   Hq   : a multiple of Hkv; query head h reads K/V head floor(h / (Hq / Hkv))
+ *   fill : 0: rows of no sequence are left as they were; 1: they become zeros
+ *   What rows of other sequences, or of none, hold is of no effect on a sequence,
+ *   infinities and NaN included.
+ * fa_bwd_packed:
+ *   o, lse, dO : in, as fa_fwd_packed writes o and lse; dq, dk, dv : out, bf16
+ *   workspace : fa_bwd_packed_workspace_size() bytes, 256-byte aligned. (What it needs in
+ *            any case is 256 + 2 * (4 * rows * Hq rounded up to 256); the rest
+ *            lets a group's heads be split over several SMs.)
+ *   dk and dv are sums over the heads of a group; all outputs are bitwise
+ *   reproducible on one kind of device with one size of workspace (a split
+ *   group's heads are summed in parts), whatever the plan's order.
+ * rows * Hq must be below 2^31. rows = 0 or Hq = 0 is a no-op.
+ */
+size_t fa_packed_plan_size(int B, int rows); /* 0 for negative sizes */
+fa_status_t fa_packed_plan(const int* cu_seqlens, int B, int rows, int causal, void* plan, size_t plan_bytes,
+                           cudaStream_t stream);
+fa_status_t fa_fwd_packed(const void* q, const void* k, const void* v, const long long* strides, void* o, float* lse,
+                          const void* plan, int rows, int Hq, int Hkv, int d, int causal, float scale, int fill,
+                          cudaStream_t stream);
+size_t fa_bwd_packed_workspace_size(int rows, int Hq, int Hkv, int d); /* 0 for invalid or empty sizes */
+fa_status_t fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                          const long long* strides, void* dq, void* dk, void* dv, const long long* grad_strides,
+                          const void* plan, int rows, int Hq, int Hkv, int d, int causal, float scale, int fill,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * A paged key/value cache in 8 bits, for serving: e4m3 codes with one scale
  * for each page (block of `page` tokens) and head.
  *   k_cache, v_cache : uint8 [num_pages][Hkv][page][d], e4m3 codes, 16-byte
