@@ -62,6 +62,11 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int kernel_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int HD>
@@ -88,6 +93,7 @@ struct BwdCfg {
 struct BwdShared {
   uint64_t kv_full;
   uint64_t qdo_full[4], qdo_empty[4];
+  TailShared tail;  // packed sequences
   uint64_t s_full, dp_full, pa_ready, ds_ready, pv_done, dq_full, dq_free, acc_done;
   uint64_t acc_free;  // dK, dV of the previous item read out of TMEM
   uint64_t mma_drain;  // the MMA thread's last commit: all its MMAs done before the CTA exits
@@ -397,20 +403,8 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
   const uint64_t lim = p.wait_limit_ns;
   const int total = bwd_total_items<RAG>(p);
 
-  // Packed sequences: the whole warp walks the items (it clears the rows of Q
-  // and dO behind a sequence's last query), one lane issues.
-  const bool lead = !RAG || lane_id() == 0;
-  auto wait = [&](uint64_t* bar, int parity) -> bool {
-    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
-    return RAG ? __all_sync(0xffffffffu, ok) : ok;
-  };
-  auto commit = [&](uint64_t* bar) {
-    if (lead) umma_commit(bar);
-  };
-
   // D[tmem] = A (128 x HD, K-major) * B (128 x HD, K-major)^T
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_addr) {
-    if (!lead) return;
     const uint64_t ad = make_smem_desc_sw128(a_addr, 16, 1024), bd = make_smem_desc_sw128(b_addr, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
@@ -420,82 +414,78 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    if (lead) drain_mmas(&sh.mma_drain, lim);
+    drain_mmas(&sh.mma_drain, lim);
   };
 
   int g = 0, items = 0;
+  TailCalls tail;
   while (true) {
-    const int item = RAG ? take_item_warp(sh, items, lim) : take_item(sh, items, lim);
+    const int item = take_item(sh, items, lim);
     if (item < 0) return fail();
     if (item >= total) break;
     const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int s0 = g % C::QST;
     typename BwdWork<CAUSAL, RAG>::Pos pos = wk.first();
-    // Steps of 16 queries of tile i in the products over queries. A sequence's
-    // last tile ends in rows of the next one, whatever they hold: whole steps of
-    // them are left out, and those in the last step taken are cleared (their
-    // weights are 0, but 0 * NaN).
+    // steps of 16 queries of tile i in the products over queries
     auto take_tile = [&](int slot, int i) -> int {
       if constexpr (RAG) {
         const int held = wk.n - i * 128;
         if (held >= 128) return 8;
-        const int steps = (held + 15) >> 4;
-        clear_rows<C::CHUNKS, C::CHUNK_BYTES>(q_addr + slot * C::TILE_BYTES, held, 16 * steps);
-        clear_rows<C::CHUNKS, C::CHUNK_BYTES>(do_addr + slot * C::TILE_BYTES, held, 16 * steps);
-        return steps;
+        tail.ask(sh.tail, held, q_addr + slot * C::TILE_BYTES, do_addr + slot * C::TILE_BYTES);
+        return (held + 15) >> 4;
       }
       return 8;
     };
-    if (!wait(&sh.kv_full, items & 1) ||
-        !wait(&sh.qdo_full[s0], (g / C::QST) & 1))
+    if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) ||
+        !mbar_wait(&sh.qdo_full[s0], (g / C::QST) & 1, &sh.abort_flag, lim))
       return fail();
     int steps = take_tile(s0, pos.i), next_steps = 8;
     // Region A held the previous item's last P^T, region B its last dQ.
-    if (g > 0 && !wait(&sh.pv_done, (g - 1) & 1)) return fail();
+    if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
+    if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
     issue_sq(C::REG_A, k_addr, q_addr + s0 * C::TILE_BYTES);  // S^T(first)
-    commit(&sh.s_full);
-    if (DQ && g > 0 && !wait(&sh.dq_free, (g - 1) & 1)) return fail();
+    umma_commit(&sh.s_full);
+    if (DQ && g > 0 && !mbar_wait(&sh.dq_free, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
     issue_sq(C::REG_B, v_addr, do_addr + s0 * C::TILE_BYTES);  // dP^T(first)
-    commit(&sh.dp_full);
+    umma_commit(&sh.dp_full);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const int s = g % C::QST;
       const bool has_next = n + 1 < n_iter;
       const int s1 = (g + 1) % C::QST;
       const uint32_t qa = q_addr + s * C::TILE_BYTES, doa = do_addr + s * C::TILE_BYTES;
-      if (!wait(&sh.pa_ready, g & 1)) return fail();
-      if (n == 0 && items > 0 && !wait(&sh.acc_free, (items - 1) & 1)) return fail();
+      if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
+      if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dV += P^T dO_n; P^T (bf16) sits in columns [0,32) and [64,96) of region A
       const uint64_t dod = make_smem_desc_sw128(doa, C::CHUNK_BYTES, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DV_COL, tmem + C::REG_A + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dod, ks * 2048), kIdescAcc,
-                (n > 0 || ks > 0) ? 1u : 0u);
-      commit(&sh.pv_done);
+      issue_steps<8, RAG>(steps, [&](int ks) {
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dod, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+      });
+      umma_commit(&sh.pv_done);
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
-        if (!wait(&sh.qdo_full[s1], ((g + 1) / C::QST) & 1)) return fail();
+        if (!mbar_wait(&sh.qdo_full[s1], ((g + 1) / C::QST) & 1, &sh.abort_flag, lim)) return fail();
         if constexpr (RAG) {
           wk.advance(pos);
           next_steps = take_tile(s1, pos.i);
         }
-        if (!wait(&sh.pv_done, g & 1)) return fail();
+        if (!mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
+        if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         issue_sq(C::REG_A, k_addr, q_addr + s1 * C::TILE_BYTES);
-        commit(&sh.s_full);
+        umma_commit(&sh.s_full);
       }
-      if (!wait(&sh.ds_ready, g & 1)) return fail();
+      if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dK += dS^T Q_n
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qa, C::CHUNK_BYTES, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048),
-                kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+      issue_steps<8, RAG>(steps, [&](int ks) {
+        umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+      });
       if constexpr (DQ) {
         // dQ_n into region B. d = 128: dQ_n^T = K_j^T dS^T (head-dim columns on
         // the lanes, queries along the columns), so the drain's reductions
@@ -511,23 +501,24 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
           else
             umma_ss(tmem + C::REG_B, ds_mn, k_mn, kIdescDq, ks > 0 ? 1u : 0u);
         }
-        commit(&sh.dq_full);
+        umma_commit(&sh.dq_full);
       }
-      commit(&sh.qdo_empty[s]);
+      umma_commit(&sh.qdo_empty[s]);
       if (has_next) {
-        if (DQ && !wait(&sh.dq_free, g & 1)) return fail();
+        if (DQ && !mbar_wait(&sh.dq_free, g & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         issue_sq(C::REG_B, v_addr, do_addr + s1 * C::TILE_BYTES);  // dP^T(n+1) over the drained dQ_n
-        commit(&sh.dp_full);
+        umma_commit(&sh.dp_full);
       }
       if constexpr (RAG) steps = next_steps;
     }
-    commit(&sh.acc_done);
+    umma_commit(&sh.acc_done);
     ++items;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (lead) drain_mmas(&sh.mma_drain, lim);
+  if (RAG) tail.finish(sh.tail);
+  drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w (w = 0, 1) owns query columns [64w, 64w + 64) of every tile:
@@ -855,7 +846,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
 }
 
 template <int HD, bool CAUSAL, bool DQ, bool RAG>
-__global__ void __launch_bounds__(kThreads, 1) fa_bwd_kernel(const __grid_constant__ BwdLaunch p) {
+__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_kernel(const __grid_constant__ BwdLaunch p) {
   using C = BwdCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ BwdShared sh;
@@ -889,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_kernel(const __grid_consta
     mbar_init(&sh.dq_free, 256 + debug_extra(p.debug_skip, WHERE_BWD_DQ));
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
+    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
@@ -909,7 +901,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_kernel(const __grid_consta
   if (warp == kLoadWarp) {
     if (lane_id() == 0) bwd_load_role<HD, CAUSAL, RAG>(p, sh, sK, sV, sQ, sdO);
   } else if (warp == kMmaWarp) {
-    if (RAG || lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ, RAG>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
+    if (lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ, RAG>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
+  } else if (RAG && warp == kTailWarp) {
+    tail_role<C::CHUNKS, C::CHUNK_BYTES>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     bwd_softmax_role<HD, CAUSAL, DQ, RAG>(p, sh, sDS, sLD, sDQ, tmem, wg);
   }
@@ -942,7 +936,7 @@ cudaError_t launch_main_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.BH) * T;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  kern<<<static_cast<unsigned>(grid), kThreads, C::SMEM_BYTES, stream>>>(a);
+  kern<<<static_cast<unsigned>(grid), kernel_threads<RAG>(), C::SMEM_BYTES, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -56,6 +56,11 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int kernel_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr int kItemConsumers = 1 + 256;  // the MMA thread and the softmax threads
 
 struct Cfg256 {
@@ -80,6 +85,7 @@ struct Shared256 {
   uint64_t qo_full, qo_empty;        // Q_i, the other half
   uint64_t doh_full, doh_empty;      // dO_i[:, h]
   uint64_t doo_full, doo_empty;      // dO_i, the other half
+  TailShared tail;  // packed sequences
   uint64_t s_full, dp_full, pa_ready, ds_ready, pv_done, acc_done, acc_free;
   uint64_t dq_full[2], dq_free[2];   // dQ^T buffer n & 1
   uint64_t mma_drain;                // the MMA thread's last commit: all its MMAs done before the CTA exits
@@ -292,25 +298,14 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
                  doh_addr = smem_u32(sDOh), doo_addr = smem_u32(sDOo), ds_addr = smem_u32(sDS);
   const uint64_t lim = p.wait_limit_ns;
   const int total = total_items256<RAG>(p);
-  // Packed sequences: the whole warp walks the items (it clears the rows of Q
-  // and dO behind a sequence's last query), one lane issues.
-  const bool lead = !RAG || lane_id() == 0;
-  auto wait = [&](uint64_t* bar, int parity) -> bool {
-    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
-    return RAG ? __all_sync(0xffffffffu, ok) : ok;
-  };
-  auto commit = [&](uint64_t* bar) {
-    if (lead) umma_commit(bar);
-  };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    if (lead) drain_mmas(&sh.mma_drain, lim);
+    drain_mmas(&sh.mma_drain, lim);
   };
 
   // D[tmem] = A (128 keys x 256, K-major, resident) * B (64 queries x 256,
   // K-major, in the h and other-half slots)^T, chunks of 64 columns in order.
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_h, uint32_t b_o, int h) {
-    if (!lead) return;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint64_t ad = make_smem_desc_sw128(a_addr + c * C::KV_CHUNK, 16, 1024);
@@ -321,119 +316,121 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
     }
   };
   auto wait_s_operands = [&](int n) -> bool {
-    return wait(&sh.qh_full[n % C::QH_SLOTS], (n / C::QH_SLOTS) & 1) &&
-           wait(&sh.qo_full, n & 1);
+    return mbar_wait(&sh.qh_full[n % C::QH_SLOTS], (n / C::QH_SLOTS) & 1, &sh.abort_flag, lim) &&
+           mbar_wait(&sh.qo_full, n & 1, &sh.abort_flag, lim);
   };
   auto wait_dp_operands = [&](int n) -> bool {
-    return wait(&sh.doo_full, n & 1) && wait(&sh.doh_full, n & 1);
+    return mbar_wait(&sh.doo_full, n & 1, &sh.abort_flag, lim) && mbar_wait(&sh.doh_full, n & 1, &sh.abort_flag, lim);
   };
   auto issue_s = [&](int n, int h) {
     issue_sq(C::REG_S, k_addr, qh_addr + (n % C::QH_SLOTS) * C::HALF_BYTES, qo_addr, h);
-    commit(&sh.s_full);
-    commit(&sh.qo_empty);  // the other half of Q_n is read by S^T(n) only
+    umma_commit(&sh.s_full);
+    umma_commit(&sh.qo_empty);  // the other half of Q_n is read by S^T(n) only
   };
   auto issue_dp = [&](int h) {
     issue_sq(C::REG_DP, v_addr, doh_addr, doo_addr, h);
-    commit(&sh.dp_full);
-    commit(&sh.doo_empty);
+    umma_commit(&sh.dp_full);
+    umma_commit(&sh.doo_empty);
   };
 
   int g = 0, items = 0;
+  TailCalls tail;
   while (true) {
-    const int item = RAG ? take_item_warp(sh, items, lim) : take_item(sh, items, lim);
+    const int item = take_item(sh, items, lim);
     if (item < 0) return fail();
     if (item >= total) break;
     const Work256<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int h = wk.h;
     typename Work256<CAUSAL, RAG>::Pos pos = wk.first();
-    // Steps of 16 queries of tile i in the products over queries (fa_bwd.cu):
-    // the rows behind a sequence's last query are left out, or cleared where a
-    // step holds some of both.
+    // steps of 16 queries of tile i in the products over queries
     auto tile_steps = [&](int i) -> int { return RAG ? min(4, (wk.len(p) - i * C::BQ + 15) >> 4) : 4; };
-    auto clear_tail = [&](uint32_t half_tile, int i) {
+    // the rows of a half tile of query tile i behind the sequence's last query, if any, are cleared
+    auto clean = [&](uint32_t half_tile, int i) -> bool {
       if constexpr (RAG) {
         const int held = wk.n - i * C::BQ;
-        if (held < C::BQ) clear_rows<2, C::Q_CHUNK>(half_tile, held, (held + 15) / 16 * 16);
+        if (held < C::BQ) tail.ask(sh.tail, held, half_tile);
+        return tail.wait(sh.tail, &sh.abort_flag, lim);
       }
+      return true;
     };
-    if (!wait(&sh.kv_full, items & 1) || !wait_s_operands(g)) return fail();
+    auto q_clean = [&](int n, int i) { return clean(qh_addr + (n % C::QH_SLOTS) * C::HALF_BYTES, i); };
+    if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) || !wait_s_operands(g)) return fail();
     // S^T overwrites the previous item's last P^T: dV must have read it.
-    if (g > 0 && !wait(&sh.pv_done, (g - 1) & 1)) return fail();
+    if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
-    clear_tail(qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES, pos.i);
+    if (!q_clean(g, pos.i)) return fail();
     issue_s(g, h);
     // dP^T overwrites the previous item's last dP^T, which phase B read
     // before ds_ready (waited for in the previous item's last step).
     if (!wait_dp_operands(g)) return fail();
-    clear_tail(doh_addr, pos.i);
+    if (!clean(doh_addr, pos.i)) return fail();
     int steps = tile_steps(pos.i);
     tc_fence_after_sync();
     issue_dp(h);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const bool has_next = n + 1 < n_iter;
-      if (!wait(&sh.pa_ready, g & 1)) return fail();
+      if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
       // the first dV / dK of an item overwrite the accumulators: the previous
       // item's epilogue must have read them
-      if (n == 0 && items > 0 && !wait(&sh.acc_free, (items - 1) & 1)) return fail();
+      if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dV half += P^T dO_n[:, h]; P^T (bf16) in columns [0,16) and [32,48) of REG_S
       const uint64_t dod = make_smem_desc_sw128(doh_addr, C::Q_CHUNK, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048),
-                kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
-      commit(&sh.pv_done);
-      commit(&sh.doh_empty);
+      issue_steps<4, RAG>(steps, [&](int ks) {
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+      });
+      umma_commit(&sh.pv_done);
+      umma_commit(&sh.doh_empty);
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
-        if (!wait_s_operands(g + 1) || !wait(&sh.pv_done, g & 1)) return fail();
+        if (!wait_s_operands(g + 1) || !mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         if constexpr (RAG) {
           wk.advance(pos);
-          clear_tail(qh_addr + ((g + 1) % C::QH_SLOTS) * C::HALF_BYTES, pos.i);
+          if (!q_clean(g + 1, pos.i)) return fail();
         }
         issue_s(g + 1, h);
       }
-      if (!wait(&sh.ds_ready, g & 1)) return fail();
+      if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dK half += dS^T Q_n[:, h]
       const uint32_t qh = qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES;
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qh, C::Q_CHUNK, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc,
-                (n > 0 || ks > 0) ? 1u : 0u);
-      commit(&sh.qh_empty[g % C::QH_SLOTS]);
+      issue_steps<4, RAG>(steps, [&](int ks) {
+        umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+      });
+      umma_commit(&sh.qh_empty[g % C::QH_SLOTS]);
       if constexpr (DQ) {
         // dQ_n^T half = K_j[:, h]^T dS^T into buffer g & 1, once the drain of
         // tile g - 2 has read it
         const int b = g & 1;
-        if (g >= 2 && !wait(&sh.dq_free[b], ((g >> 1) - 1) & 1)) return fail();
+        if (g >= 2 && !mbar_wait(&sh.dq_free[b], ((g >> 1) - 1) & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         const uint64_t kd = make_smem_desc_sw128(k_addr + 2 * h * C::KV_CHUNK, C::KV_CHUNK, 1024);
         const uint64_t dsm = make_smem_desc_sw128(ds_addr, C::DS_BYTES, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           umma_ss(tmem + C::dq_col(b), desc_add(kd, ks * 2048), desc_add(dsm, ks * 2048), kIdescDq, ks > 0 ? 1u : 0u);
-        commit(&sh.dq_full[b]);
+        umma_commit(&sh.dq_full[b]);
       }
       if (has_next) {
         // dP^T(n+1): phase B(n) has read dP^T(n) (ds_ready above)
         if (!wait_dp_operands(g + 1)) return fail();
-        clear_tail(doh_addr, pos.i);
+        if (!clean(doh_addr, pos.i)) return fail();
         steps = tile_steps(pos.i);
         tc_fence_after_sync();
         issue_dp(h);
       }
     }
-    commit(&sh.acc_done);
+    umma_commit(&sh.acc_done);
     ++items;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (lead) drain_mmas(&sh.mma_drain, lim);
+  if (RAG) tail.finish(sh.tail);
+  drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w (w = 0, 1) owns queries [32w, 32w + 32) of every 64-row tile;
@@ -663,7 +660,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 }
 
 template <bool CAUSAL, bool DQ, bool RAG>
-__global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_constant__ BwdLaunch p) {
+__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(const __grid_constant__ BwdLaunch p) {
   using C = Cfg256;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ Shared256 sh;
@@ -704,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_con
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
+    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
@@ -724,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_con
   if (warp == kLoadWarp) {
     if (lane_id() == 0) load_role<CAUSAL, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo);
   } else if (warp == kMmaWarp) {
-    if (RAG || lane_id() == 0) mma_role<CAUSAL, DQ, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
+    if (lane_id() == 0) mma_role<CAUSAL, DQ, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
+  } else if (RAG && warp == kTailWarp) {
+    tail_role<2, C::Q_CHUNK>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     softmax_role<CAUSAL, DQ, RAG>(p, sh, sDS, sLD, tmem, warp >> 2);
   }
@@ -744,7 +744,7 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.BHkv) * (RAG ? a.N : (a.N + 127) / 128) * 2;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  kern<<<static_cast<unsigned>(grid), kThreads, Cfg256::SMEM_BYTES, stream>>>(a);
+  kern<<<static_cast<unsigned>(grid), kernel_threads<RAG>(), Cfg256::SMEM_BYTES, stream>>>(a);
   return cudaGetLastError();
 }
 

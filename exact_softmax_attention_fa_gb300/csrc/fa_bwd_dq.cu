@@ -40,6 +40,11 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int kernel_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr int kItemConsumers = 1 + 256;  // the MMA thread and the softmax threads
 
 template <int HD>
@@ -63,6 +68,7 @@ struct DqCfg {
 struct DqShared {
   uint64_t q_full, q_free;
   uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2];
+  TailShared tail;  // packed sequences
   uint64_t s_full[2];  // per S buffer
   // ds_ready[t & 1]: dS(t) is in TMEM. Two barriers, because the softmax can
   // finish tile t+1 (it needs only dP(t+1), issued before the MMA thread
@@ -214,20 +220,8 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   const uint64_t lim = p.wait_limit_ns;
   const int total = dq_total_items<RAG>(p);
 
-  // Packed sequences: the whole warp walks the items (it clears the rows of K
-  // behind a sequence's last key), one lane issues.
-  const bool lead = !RAG || lane_id() == 0;
-  auto wait = [&](uint64_t* bar, int parity) -> bool {
-    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
-    return RAG ? __all_sync(0xffffffffu, ok) : ok;
-  };
-  auto commit = [&](uint64_t* bar) {
-    if (lead) umma_commit(bar);
-  };
-
   // D[tmem] = A (128 x HD, K-major) * B (128 x HD, K-major)^T
   auto issue_sq = [&](uint32_t d_col, uint32_t a_addr, uint32_t b_addr) {
-    if (!lead) return;
     const uint64_t ad = make_smem_desc_sw128(a_addr, 16, 1024), bd = make_smem_desc_sw128(b_addr, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
@@ -237,7 +231,7 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    if (lead) drain_mmas(&sh.mma_drain, lim);
+    drain_mmas(&sh.mma_drain, lim);
   };
 
   // S(t) into buffer t & 1, which tile t - 2 used.
@@ -246,75 +240,71 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   // including the product of tile t - 2 whose dS sat in buffer t & 1.
   auto issue_s = [&](int t, int kvi, int done_tile) -> bool {  // kvi: the tile's index in the K/V stream
     const int stage = kvi % C::KST;
-    if (!wait(&sh.k_full[stage], (kvi / C::KST) & 1)) return false;
-    if (t >= 2 && !wait(&sh.dq_done, done_tile & 1)) return false;
+    if (!mbar_wait(&sh.k_full[stage], (kvi / C::KST) & 1, &sh.abort_flag, lim)) return false;
+    if (t >= 2 && !mbar_wait(&sh.dq_done, done_tile & 1, &sh.abort_flag, lim)) return false;
     tc_fence_after_sync();
     issue_sq(C::s_col(t & 1), q_addr, k_addr + stage * C::TILE_BYTES);
-    commit(&sh.s_full[t & 1]);
+    umma_commit(&sh.s_full[t & 1]);
     return true;
   };
   // dP(t) over dP(t - 1): wait until phase B(t - 1) loaded it.
   auto issue_dp = [&](int t, int kvi) -> bool {
     const int stage = kvi % C::VST;
-    if (!wait(&sh.v_full[stage], (kvi / C::VST) & 1)) return false;
-    if (t >= 1 && !wait(&sh.dp_free, (t - 1) & 1)) return false;
+    if (!mbar_wait(&sh.v_full[stage], (kvi / C::VST) & 1, &sh.abort_flag, lim)) return false;
+    if (t >= 1 && !mbar_wait(&sh.dp_free, (t - 1) & 1, &sh.abort_flag, lim)) return false;
     tc_fence_after_sync();
     issue_sq(C::DP_COL, do_addr, v_addr + stage * C::TILE_BYTES);
-    commit(&sh.dp_full);
-    commit(&sh.v_empty[stage]);  // V_j is read by dP(j) only
+    umma_commit(&sh.dp_full);
+    umma_commit(&sh.v_empty[stage]);  // V_j is read by dP(j) only
     return true;
   };
 
   int u = 0, kv = 0, t = 0;
+  TailCalls tail;
   while (true) {
-    const int item = RAG ? take_item_warp(sh, u, lim) : take_item(sh, u, lim);
+    const int item = take_item(sh, u, lim);
     if (item < 0) return fail();
     if (item >= total) break;
     const DqWork<CAUSAL, RAG> wk(item, p);
-    if (!wait(&sh.q_full, u & 1) || !issue_s(t, kv, t - 1) || !issue_dp(t, kv))
+    if (!mbar_wait(&sh.q_full, u & 1, &sh.abort_flag, lim) || !issue_s(t, kv, t - 1) ||
+        !issue_dp(t, kv))
       return fail();
-    if (wk.nkv == 1) commit(&sh.q_free);
+    if (wk.nkv == 1) umma_commit(&sh.q_free);
     // Per tile t: S(t+1) as soon as its K tile is in, dP(t+1) once phase B(t)
     // has read dP(t), dQ += dS(t) K once phase B(t) has written dS(t).
     for (int j = 0; j < wk.nkv; ++j, ++kv, ++t) {
       const int s = kv % C::KST;
       if (j + 1 < wk.nkv) {
         if (!issue_s(t + 1, kv + 1, t - 1) || !issue_dp(t + 1, kv + 1)) return fail();
-        if (j + 2 == wk.nkv) commit(&sh.q_free);  // the item's last S and dP are issued
+        if (j + 2 == wk.nkv) umma_commit(&sh.q_free);  // the item's last S and dP are issued
       }
-      if (!wait(&sh.ds_ready[t & 1], (t >> 1) & 1)) return fail();
+      if (RAG && wk.len(p) - j * 128 < 128) {  // once S(t) has read K_j
+        if (!mbar_wait(&sh.s_full[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return fail();
+        tail.ask(sh.tail, wk.len(p) - j * 128, k_addr + s * C::TILE_BYTES);
+      }
+      if (!mbar_wait(&sh.ds_ready[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
       // the first dQ product of an item overwrites the accumulator: the
       // previous item's epilogue must have read it
-      if (j == 0 && u > 0 && !wait(&sh.acc_free, (u - 1) & 1)) return fail();
+      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dS (bf16 pairs) sits in columns [0, 32) and [64, 96) of S buffer t & 1:
       // keys 16 ks .. 16 ks + 15 are 8 columns at 64 (ks / 4) + 8 (ks % 4)
-      // A sequence's last key tile ends in rows of the next one, whatever they
-      // hold: whole steps of 16 keys are left out of the product, and the rows of
-      // the last step taken are cleared (their dS is 0, but 0 * NaN). S(j) has
-      // read the tile; its columns of those keys are masked.
-      int steps = 8;
-      if constexpr (RAG) {
-        const int held = wk.n - j * 128;
-        if (held < 128) {
-          steps = (held + 15) >> 4;
-          clear_rows<C::CHUNKS, C::CHUNK_BYTES>(k_addr + s * C::TILE_BYTES, held, 16 * steps);
-        }
-      }
+      const int steps = RAG ? std::min(8, (wk.len(p) - j * 128 + 15) >> 4) : 8;  // of 16 keys
       const uint64_t kd = make_smem_desc_sw128(k_addr + s * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048),
-                kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
-      commit(&sh.dq_done);
-      commit(&sh.k_empty[s]);
+      issue_steps<8, RAG>(steps, [&](int ks) {
+        umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
+      });
+      umma_commit(&sh.dq_done);
+      umma_commit(&sh.k_empty[s]);
     }
-    commit(&sh.acc_done);
+    umma_commit(&sh.acc_done);
     ++u;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (lead) drain_mmas(&sh.mma_drain, lim);
+  if (RAG) tail.finish(sh.tail);
+  drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w owns key columns [64w, 64w + 64) of every tile; thread r owns
@@ -477,7 +467,7 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
 }
 
 template <int HD, bool CAUSAL, bool RAG>
-__global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_constant__ BwdLaunch p) {
+__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq_kernel(const __grid_constant__ BwdLaunch p) {
   using C = DqCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ DqShared sh;
@@ -508,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_con
     mbar_init(&sh.dq_done, 1);
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
+    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
@@ -528,7 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq_kernel(const __grid_con
   if (warp == kLoadWarp) {
     if (lane_id() == 0) dq_load_role<HD, CAUSAL, RAG>(p, sh, sQ, sdO, sK, sV);
   } else if (warp == kMmaWarp) {
-    if (RAG || lane_id() == 0) dq_mma_role<HD, CAUSAL, RAG>(p, sh, sQ, sdO, sK, sV, tmem);
+    if (lane_id() == 0) dq_mma_role<HD, CAUSAL, RAG>(p, sh, sQ, sdO, sK, sV, tmem);
+  } else if (RAG && warp == kTailWarp) {
+    tail_role<C::CHUNKS, C::CHUNK_BYTES>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     dq_softmax_role<HD, CAUSAL, RAG>(p, sh, tmem, warp >> 2);
   }
@@ -553,7 +546,7 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long grid = items < a.num_sms ? items : a.num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kernel_threads<RAG>());
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -47,6 +47,11 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int kernel_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr int kItemConsumers = 1 + 256;  // the MMA thread and the softmax threads
 
 struct Dq256Cfg {
@@ -62,6 +67,7 @@ struct Dq256Cfg {
 struct Dq256Shared {
   uint64_t q_full, q_free;
   uint64_t ring_full[Dq256Cfg::RING], ring_empty[Dq256Cfg::RING];
+  TailShared tail;  // packed sequences
   uint64_t s_full, s_free, dp_full, ds_ready, dq_done, acc_done, acc_free;
   uint64_t mma_drain;  // the MMA thread's last commit: all its MMAs done before the CTA exits
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
@@ -225,23 +231,14 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
   const uint32_t q_addr = smem_u32(sQ), do_addr = smem_u32(sdO), ring_addr = smem_u32(sRing);
   const uint64_t lim = p.wait_limit_ns;
   const int total = dq_total_items<RAG>(p);
-  // Packed sequences: the whole warp walks the items (it clears the rows of K
-  // behind a sequence's last key), one lane issues.
-  const bool lead = !RAG || lane_id() == 0;
-  auto wait = [&](uint64_t* bar, int parity) -> bool {
-    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
-    return RAG ? __all_sync(0xffffffffu, ok) : ok;
-  };
-  auto commit = [&](uint64_t* bar) {
-    if (lead) umma_commit(bar);
-  };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
-    if (lead) drain_mmas(&sh.mma_drain, lim);
+    drain_mmas(&sh.mma_drain, lim);
   };
   int pos = 0;  // ring chunks consumed
+  TailCalls tail;
   auto wait_chunk = [&](int k) -> bool {
-    return wait(&sh.ring_full[k % C::RING], (k / C::RING) & 1);
+    return mbar_wait(&sh.ring_full[k % C::RING], (k / C::RING) & 1, &sh.abort_flag, lim);
   };
   auto slot_addr = [&](int k) -> uint32_t { return ring_addr + (k % C::RING) * C::CHUNK_BYTES; };
   // D = A (128 x 256 resident, K-major) * (4 ring chunks, K-major)^T; each
@@ -255,88 +252,85 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
       const uint64_t bd = make_smem_desc_sw128(slot_addr(pos), 16, 1024);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        if (lead) umma_ss(tmem + d_col, desc_add(ad, ks * 32), desc_add(bd, ks * 32), kIdescSq, (c > 0 || ks > 0) ? 1u : 0u);
-      commit(&sh.ring_empty[pos % C::RING]);
+        umma_ss(tmem + d_col, desc_add(ad, ks * 32), desc_add(bd, ks * 32), kIdescSq, (c > 0 || ks > 0) ? 1u : 0u);
+      umma_commit(&sh.ring_empty[pos % C::RING]);
     }
     return true;
   };
   // dQ += dS K_t: two N = 128 halves of the head dimension, each reading an
   // even-aligned pair of ring chunks as one MN-major B operand.
-  // held: keys of the sequence from tile t on (fa_bwd_dq.cu: those behind its last
-  // are left out, or cleared where a step of 16 holds some of both).
+  // held: keys of the sequence from tile t on.
   auto issue_dq = [&](bool first, int held) -> bool {
     const int steps = RAG ? min(8, (held + 15) >> 4) : 8;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half, pos += 2) {
       if (!wait_chunk(pos) || !wait_chunk(pos + 1)) return false;
       if constexpr (RAG) {
-        if (held < 128) {
-          clear_rows<1, C::CHUNK_BYTES>(slot_addr(pos), held, 16 * steps);
-          clear_rows<1, C::CHUNK_BYTES>(slot_addr(pos + 1), held, 16 * steps);
-        }
+        if (held < 128) tail.ask(sh.tail, held, slot_addr(pos), slot_addr(pos + 1));
+        if (!tail.wait(sh.tail, &sh.abort_flag, lim)) return false;
       }
       tc_fence_after_sync();
       const uint64_t kd = make_smem_desc_sw128(slot_addr(pos), C::CHUNK_BYTES, 1024);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        if (lead && (!RAG || ks < steps)) umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8,
-                desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
-      commit(&sh.ring_empty[pos % C::RING]);
-      commit(&sh.ring_empty[(pos + 1) % C::RING]);
+      issue_steps<8, RAG>(steps, [&](int ks) {
+        umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
+      });
+      umma_commit(&sh.ring_empty[pos % C::RING]);
+      umma_commit(&sh.ring_empty[(pos + 1) % C::RING]);
     }
     return true;
   };
 
   int u = 0, t = 0;  // items, key tiles (global)
   while (true) {
-    const int item = RAG ? take_item_warp(sh, u, lim) : take_item(sh, u, lim);
+    const int item = take_item(sh, u, lim);
     if (item < 0) return fail();
     if (item >= total) break;
     const Dq256Work<CAUSAL, RAG> wk(item, p);
-    if (!wait(&sh.q_full, u & 1)) return fail();
+    if (!mbar_wait(&sh.q_full, u & 1, &sh.abort_flag, lim)) return fail();
     // S(first): the previous item's last dQ product has read dS from the dP
     // columns, and phase A read its S, before that product was issued.
-    if (t > 0 && !wait(&sh.s_free, (t - 1) & 1)) return fail();
+    if (t > 0 && !mbar_wait(&sh.s_free, (t - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
     if (!issue_sq(C::S_COL, q_addr)) return fail();
-    commit(&sh.s_full);
+    umma_commit(&sh.s_full);
     // dP(first) overwrites the previous item's last dS: its dQ product is done
-    if (t > 0 && !wait(&sh.dq_done, (t - 1) & 1)) return fail();
+    if (t > 0 && !mbar_wait(&sh.dq_done, (t - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
     if (!issue_sq(C::DP_COL, do_addr)) return fail();
-    commit(&sh.dp_full);
-    if (wk.nkv == 1) commit(&sh.q_free);
+    umma_commit(&sh.dp_full);
+    if (wk.nkv == 1) umma_commit(&sh.q_free);
     for (int j = 0; j < wk.nkv; ++j, ++t) {
       const bool has_next = j + 1 < wk.nkv;
       if (has_next) {
         // S(t+1) once phase A(t) has read S(t)
-        if (!wait(&sh.s_free, t & 1)) return fail();
+        if (!mbar_wait(&sh.s_free, t & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         if (!issue_sq(C::S_COL, q_addr)) return fail();
-        commit(&sh.s_full);
+        umma_commit(&sh.s_full);
       }
-      if (!wait(&sh.ds_ready, t & 1)) return fail();
+      if (!mbar_wait(&sh.ds_ready, t & 1, &sh.abort_flag, lim)) return fail();
       // the first dQ product of an item overwrites the accumulator: the
       // previous item's epilogue must have read it
-      if (j == 0 && u > 0 && !wait(&sh.acc_free, (u - 1) & 1)) return fail();
+      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       if (!issue_dq(j == 0, wk.len(p) - j * 128)) return fail();
-      commit(&sh.dq_done);
+      umma_commit(&sh.dq_done);
       if (has_next) {
         // dP(t+1) overwrites dS(t): wait for the dQ product to have read it
-        if (!wait(&sh.dq_done, t & 1)) return fail();
+        if (!mbar_wait(&sh.dq_done, t & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
         if (!issue_sq(C::DP_COL, do_addr)) return fail();
-        commit(&sh.dp_full);
-        if (j + 2 == wk.nkv) commit(&sh.q_free);  // the item's last S and dP are issued
+        umma_commit(&sh.dp_full);
+        if (j + 2 == wk.nkv) umma_commit(&sh.q_free);  // the item's last S and dP are issued
       }
     }
-    commit(&sh.acc_done);
+    umma_commit(&sh.acc_done);
     ++u;
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (lead) drain_mmas(&sh.mma_drain, lim);
+  if (RAG) tail.finish(sh.tail);
+  drain_mmas(&sh.mma_drain, lim);
 }
 
 // Warpgroup w owns key columns [64w, 64w + 64) of every key tile; thread r
@@ -493,7 +487,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
 }
 
 template <bool CAUSAL, bool RAG>
-__global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_constant__ BwdLaunch p) {
+__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq256_kernel(const __grid_constant__ BwdLaunch p) {
   using C = Dq256Cfg;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ Dq256Shared sh;
@@ -518,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_
     mbar_init(&sh.dq_done, 1);
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
+    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
@@ -538,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd_dq256_kernel(const __grid_
   if (warp == kLoadWarp) {
     if (lane_id() == 0) dq256_load_role<CAUSAL, RAG>(p, sh, sQ, sdO, sRing);
   } else if (warp == kMmaWarp) {
-    if (RAG || lane_id() == 0) dq256_mma_role<CAUSAL, RAG>(p, sh, sQ, sdO, sRing, tmem);
+    if (lane_id() == 0) dq256_mma_role<CAUSAL, RAG>(p, sh, sQ, sdO, sRing, tmem);
+  } else if (RAG && warp == kTailWarp) {
+    tail_role<1, C::CHUNK_BYTES>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     dq256_softmax_role<CAUSAL, RAG>(p, sh, tmem, warp >> 2);
   }
@@ -563,7 +560,7 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long grid = items < a.num_sms ? items : a.num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kernel_threads<RAG>());
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
@@ -57,11 +58,18 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int fwd_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr float kLn2 = 0.69314718055994530942f;
 // Largest growth of a row max (in base-2 units of the scaled scores) absorbed
 // without rescaling: P~ <= 2^8 is exact in bf16's exponent range and l, O~
 // stay far from fp32 overflow.
 constexpr float kRescaleSlack = 8.0f;
+
+constexpr int kStageBytes = 32 * 128;  // packed sequences: a warp's O on its way out, 32 rows x 64 columns
 
 template <int HD>
 struct FwdCfg {
@@ -77,12 +85,16 @@ struct FwdCfg {
   __host__ __device__ static constexpr uint32_t p_col(int t) {
     return HD == 64 ? 384u + uint32_t(t) * 64u : (HD == 128 ? uint32_t(t) * 128u : 128u);
   }
-  static constexpr int SMEM_BYTES = (NT + KST + VST) * TILE_BYTES + 1024;
+  template <bool RAG>
+  static constexpr int smem_bytes() {
+    return (NT + KST + VST) * TILE_BYTES + (RAG ? NT * 4 * kStageBytes : 0) + 1024;
+  }
 };
 
 struct FwdShared {
   uint64_t q_full[2], q_free[2];  // per query-tile slot
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  TailShared tail;  // packed sequences
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t mma_drain;  // the MMA thread's last commit: all its MMAs done before the CTA exits
   uint32_t tmem_base;
@@ -153,6 +165,8 @@ struct FwdWork {
     }
   }
   // Where slot t's query tile and the item's key tile j lie, as TMA coordinates
+  __device__ __forceinline__ int tile(int t) const { return qt[t]; }
+  __device__ __forceinline__ int last(int t) const { return last_kv[t]; }
   __device__ __forceinline__ int q_row(const FwdLaunch& p, int t) const { return qt[t] * rows_per_head<PACK>(p); }
   __device__ __forceinline__ int q_head(int) const { return bh; }
   __device__ __forceinline__ int kv_row(int j) const { return (kv0 + j) * 128; }
@@ -193,7 +207,10 @@ struct FwdWork<NT, CAUSAL, false, true> {
       nkv = max(nkv, last_kv[t] + 1);
     }
   }
-  __device__ __forceinline__ int q_row(const FwdLaunch&, int t) const { return row0 + qt[t] * 128; }
+  // (a slot number known at run time would put the arrays into local memory)
+  __device__ __forceinline__ int tile(int t) const { return t == 0 ? qt[0] : qt[NT - 1]; }
+  __device__ __forceinline__ int last(int t) const { return t == 0 ? last_kv[0] : last_kv[NT - 1]; }
+  __device__ __forceinline__ int q_row(const FwdLaunch&, int t) const { return row0 + tile(t) * 128; }
   __device__ __forceinline__ int q_head(int t) const { return bh + t * hs; }
   __device__ __forceinline__ int kv_row(int j) const { return row0 + j * 128; }
   __device__ __forceinline__ int kv_head(const FwdLaunch& p) const { return bh / p.group; }
@@ -347,16 +364,7 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   const int total = total_items<PACK, RAG>(p, C::NT);
   const int G = gridDim.x;
 
-  // Packed sequences: the whole warp walks the items (it clears the rows of V
-  // behind a sequence's last key), one lane issues.
-  const bool lead = !RAG || lane_id() == 0;
-  auto wait = [&](uint64_t* bar, int parity) -> bool {
-    const bool ok = mbar_wait(bar, parity, &sh.abort_flag, lim);
-    return RAG ? __all_sync(0xffffffffu, ok) : ok;
-  };
-
   auto issue_s = [&](int t, int g) {  // g: running K/V tile index
-    if (!lead) return;
     const uint32_t qa = q_addr + t * C::TILE_BYTES;
     const uint32_t ka = k_addr + (g % C::KST) * C::TILE_BYTES;
     const uint64_t qd = make_smem_desc_sw128(qa, 16, 1024), kd = make_smem_desc_sw128(ka, 16, 1024);
@@ -367,63 +375,73 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
     }
     umma_commit(&sh.s_full[t]);
   };
-  auto issue_pv = [&](int t, int g, bool first, int steps) {  // steps: of 16 keys
-    if (!lead) return;
+  auto issue_pv = [&](int t, int g, bool first, int steps, auto last_tile) {  // steps: of 16 keys
     const uint64_t vd = make_smem_desc_sw128(v_addr + (g % C::VST) * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      if (!RAG || ks < steps) umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
-              (!first || ks > 0) ? 1u : 0u);
+    issue_steps<8, RAG && decltype(last_tile)::value>(steps, [&](int ks) {
+      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV, (!first || ks > 0) ? 1u : 0u);
+    });
     umma_commit(&sh.pv_done[t]);
   };
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_FWD_MMA);
-    if (lead) drain_mmas(&sh.mma_drain, lim);
+    drain_mmas(&sh.mma_drain, lim);
   };
 
   int kv = 0;             // running K/V tile index
   int items = 0;          // items processed
   int cnt[2] = {0, 0};    // running S / P / PV count per query-tile slot
+  TailCalls tail;
   for (int k = 0; k * G < total; ++k) {
     const int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;
     const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;
-    if (!wait(&sh.k_full[kv % C::KST], (kv / C::KST) & 1)) return fail();
+    if (!mbar_wait(&sh.k_full[kv % C::KST], (kv / C::KST) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
 #pragma unroll
     for (int t = 0; t < C::NT; ++t) {
-      if (wk.last_kv[t] < 0) continue;
+      if (wk.last_kv[t] < 0) {
+        if (RAG) {  // an empty slot's phases keep step with the load thread's
+          if (!mbar_wait(&sh.q_full[t], items & 1, &sh.abort_flag, lim)) return fail();
+          mbar_arrive(&sh.q_free[t]);
+        }
+        continue;
+      }
       // S_t(0) overwrites S_t / P~_t of the previous item: its last PV must be done.
-      if (C::P_ALIAS && cnt[t] > 0 && !wait(&sh.pv_done[t], (cnt[t] - 1) & 1))
+      if (C::P_ALIAS && cnt[t] > 0 && !mbar_wait(&sh.pv_done[t], (cnt[t] - 1) & 1, &sh.abort_flag, lim))
         return fail();
-      if (!wait(&sh.q_full[t], items & 1)) return fail();
+      if (!mbar_wait(&sh.q_full[t], items & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       issue_s(t, kv);
     }
-    if (lead) umma_commit(&sh.k_empty[kv % C::KST]);
+    umma_commit(&sh.k_empty[kv % C::KST]);
 
-    for (int j = 0; j < wk.nkv; ++j) {
+    // Key tile j. LAST: the item's last one, which over packed sequences may end in
+    // rows of the next sequence. (Tests for that in every step cost the MMA thread
+    // 5% of the forward's time at 8192 keys.)
+    auto step = [&](int j, auto last_tile) -> bool {
+      constexpr bool LAST = decltype(last_tile)::value;
       const int g = kv + j;
       const int vs = g % C::VST;
-      if (!wait(&sh.v_full[vs], (g / C::VST) & 1)) return fail();
-      // The last tile of a sequence ends in rows of the next one, whatever they
-      // hold: whole steps of 16 keys are left out of the product, and the rows
-      // of the last step taken are cleared (their weights are 0, but 0 * NaN).
-      int steps = 8;
-      if constexpr (RAG) {
-        const int held = wk.len - j * 128;
+      if (!mbar_wait(&sh.v_full[vs], (g / C::VST) & 1, &sh.abort_flag, lim)) return false;
+      int steps = 8;  // of 16 keys
+      if constexpr (RAG && LAST) {
+        const int held = wk.n_keys(p) - j * 128;
         if (held < 128) {
           steps = (held + 15) >> 4;
-          clear_rows<C::CHUNKS, C::CHUNK_BYTES>(v_addr + vs * C::TILE_BYTES, held, 16 * steps);
+          tail.ask(sh.tail, held, v_addr + vs * C::TILE_BYTES);
         }
+        // every S of the item is issued, and the epilogue does not use Q's smem
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t)
+          if (wk.last_kv[t] >= 0) umma_commit(&sh.q_free[t]);
       }
-      const bool has_next = j + 1 < wk.nkv;
+      const bool has_next = RAG ? !LAST : j + 1 < wk.nkv;
       const int gn = g + 1;
       bool k_next_ready = false;
       auto wait_k_next = [&]() -> bool {
         if (k_next_ready) return true;
-        if (!wait(&sh.k_full[gn % C::KST], (gn / C::KST) & 1)) return false;
+        if (!mbar_wait(&sh.k_full[gn % C::KST], (gn / C::KST) & 1, &sh.abort_flag, lim)) return false;
         tc_fence_after_sync();
         k_next_ready = true;
         return true;
@@ -431,24 +449,34 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
 #pragma unroll
       for (int t = 0; t < C::NT; ++t) {
         if (j > wk.last_kv[t]) continue;
-        if (!wait(&sh.p_full[t], (cnt[t] + j) & 1)) return fail();
+        if (!mbar_wait(&sh.p_full[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return false;
+        if (RAG && LAST && !tail.wait(sh.tail, &sh.abort_flag, lim)) return false;
         // PV_t(0) overwrites O~_t: the previous item's epilogue must have read it.
-        if (j == 0 && items > 0 && !wait(&sh.o_free[t], (items - 1) & 1)) return fail();
+        if (j == 0 && items > 0 && !mbar_wait(&sh.o_free[t], (items - 1) & 1, &sh.abort_flag, lim)) return false;
         tc_fence_after_sync();
-        issue_pv(t, g, j == 0, steps);
+        issue_pv(t, g, j == 0, steps, last_tile);
         if (has_next && j + 1 <= wk.last_kv[t]) {
-          if (!wait_k_next()) return fail();
+          if (!wait_k_next()) return false;
           // d = 128: S_t(j+1) overwrites the TMEM columns P_t(j) is read
           // from, so it follows PV_t(j) directly, before the other tile's PV:
           // tile t's products then run while the other tile is in its
           // softmax (the two tiles alternate instead of moving in lockstep).
-          if (C::P_ALIAS && !wait(&sh.pv_done[t], (cnt[t] + j) & 1)) return fail();
+          if (C::P_ALIAS && !mbar_wait(&sh.pv_done[t], (cnt[t] + j) & 1, &sh.abort_flag, lim)) return false;
           tc_fence_after_sync();
           issue_s(t, gn);
         }
       }
-      if (lead && has_next) umma_commit(&sh.k_empty[gn % C::KST]);
-      if (lead) umma_commit(&sh.v_empty[vs]);
+      if (has_next) umma_commit(&sh.k_empty[gn % C::KST]);
+      umma_commit(&sh.v_empty[vs]);
+      return true;
+    };
+    if constexpr (RAG) {
+      for (int j = 0; j + 1 < wk.nkv; ++j)
+        if (!step(j, std::false_type())) return fail();
+      if (!step(wk.nkv - 1, std::true_type())) return fail();
+    } else {
+      for (int j = 0; j < wk.nkv; ++j)
+        if (!step(j, std::true_type())) return fail();
     }
 #pragma unroll
     for (int t = 0; t < C::NT; ++t)
@@ -458,12 +486,76 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (lead) drain_mmas(&sh.mma_drain, lim);
+  if (RAG) tail.finish(sh.tail);
+  drain_mmas(&sh.mma_drain, lim);
 }
 
 // ---------------------------------------------------------------------------
 // Softmax + correction + epilogue (warpgroup t owns query-tile slot t)
 // ---------------------------------------------------------------------------
+// O and L of a packed sequence's query tile. Each warp brings its 32 rows out by
+// itself, 64 columns at a time through 4 KB of its own: no warp waits for another,
+// and the Q tile's smem, which the unpacked kernel stages O in, is free for the
+// next item's Q as soon as the last S has read it (short sequences spend most of
+// their time at such waits). Whole rows leave by TMA; in the warp where the
+// sequence ends, whose next rows are another's, by plain stores of whole lines.
+// (Rows straight from TMEM to global memory, a thread each, put 32 lines into
+// every store: 256 sequences of 128 rows, 32 + 8 heads: 169 us instead of 124.)
+template <int HD, bool CAUSAL>
+__device__ __forceinline__ void fwd_store_ragged(const FwdLaunch& p, FwdShared& sh, uint8_t* stage, uint32_t tO, int t,
+                                                 int r, int item, float m2, float l) {
+  asm volatile("" : "+r"(item));  // the entry is read again, not kept
+  const FwdWork<FwdCfg<HD>::NT, CAUSAL, false, true> wk(item, p);
+  const int lane = r & 31, first = wk.tile(t) * 128 + (r & ~31), head = wk.q_head(t);
+  const int held = wk.len - first;  // rows of this warp that the sequence has
+  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+  const uint32_t buf = smem_u32(stage);
+#pragma unroll 1
+  for (int c = 0; c < HD; c += 64) {
+    uint32_t w[32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t o[32];
+      tmem_ld32(tO + c + 32 * h, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        w[16 * h + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv_l, __uint_as_float(o[2 * e + 1]) * inv_l);
+    }
+    if (c + 64 >= HD) {  // O~_t fully read: the next item's first PV may overwrite it
+      tc_fence_before_sync();
+      mbar_arrive(&sh.o_free[t]);
+    }
+    if (held <= 0) continue;
+    if (lane == 0) tma_store_wait_read_all();  // the store before has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      st_shared_v4(buf + sw128_offset(lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    if (held >= 32) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tmO, stage, c, wk.row0 + first, head);
+        tma_store_commit();
+      }
+    } else {
+      __syncwarp();
+      __nv_bfloat16* dst = p.o + static_cast<long long>(wk.row0 + first) * p.o_strides[0] + head * p.o_strides[1] + c;
+      uint4 x[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) x[y] = ld_shared_v4(buf + sw128_offset(4 * y + (lane >> 3), lane & 7));
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (4 * y + (lane >> 3) < held)
+          *reinterpret_cast<uint4*>(dst + (4 * y + (lane >> 3)) * p.o_strides[0] + 8 * (lane & 7)) = x[y];
+      __syncwarp();
+    }
+  }
+  if (lane < held)
+    p.lse[static_cast<size_t>(head) * p.Nq + wk.row0 + first + lane] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+}
+
 template <int HD, bool CAUSAL, bool PACK, bool RAG>
 __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uint32_t tmem, int t) {
   using C = FwdCfg<HD>;
@@ -472,11 +564,15 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
   const uint32_t tS = tmem + lane_base + C::s_col(t);
   const uint32_t tP = tmem + lane_base + C::p_col(t);
   const uint32_t tO = tmem + lane_base + C::o_col(t);
+  const int Nq = p.Nq, Nk = p.Nk;
+  const int Tk = (Nk + 127) / 128;
   const float c2 = p.scale_log2;
   const uint64_t lim = p.wait_limit_ns;
   const int total = total_items<PACK, RAG>(p, C::NT);
   const int G = gridDim.x;
-  uint8_t* stage = sQ + t * C::TILE_BYTES;  // O staging: Q_t once its last S MMA is done
+  // O staging: Q_t once its last S MMA is done; packed sequences: 4 KB a warp behind the V ring
+  uint8_t* stage = RAG ? sQ + (C::NT + C::KST + C::VST) * C::TILE_BYTES + (threadIdx.x >> 5) * kStageBytes
+                       : sQ + t * C::TILE_BYTES;
   // After a timed-out wait a warp stops working but keeps passing every named
   // barrier and arrival, so the warpgroup's barrier counts stay matched.
   bool alive = true;
@@ -488,14 +584,16 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     if (item >= total) continue;
     const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;
-    const int qt = wk.qt[t];
-    const int last_kv = wk.last_kv[t];
+    const int qt = wk.tile(t);
+    const int last_kv = wk.last(t);
     // this thread's query: position `row` of head `head` (rph is a power of two)
     const int rph = rows_per_head<PACK>(p);
     const int row = qt * rph + (r & (rph - 1));
-    const int head = wk.q_head(t) + r / rph;
-    const int Nq = wk.n_queries(p), Nk = wk.n_keys(p);
-    const int Tk = (Nk + 127) / 128;
+    const int head = wk.bh + r / rph;
+    // Packed sequences: the last key the row sees, -1 for a row behind the sequence.
+    // What else the epilogue needs it looks up again: held through the loop it
+    // costs registers there.
+    const int last_key = !RAG || row >= wk.n_queries(p) ? -1 : (CAUSAL ? row : wk.n_keys(p) - 1);
 
     float m2 = -INFINITY;  // reference max of S * scale * log2(e)
     float l = 0.f;         // running sum of P~ (unrounded fp32)
@@ -526,10 +624,11 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       // boundary crosses (key > row + causal_off).
       const int a = wk.kv0 + j;  // absolute key tile
       const bool mask_tail = (a == Tk - 1) && (Nk & 127);
-      const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + (RAG ? 0 : p.causal_off));
-      if (mask_tail || mask_diag) {
-        int lim_col = Nk - 1 - a * 128;
-        if (CAUSAL) lim_col = min(lim_col, row + (RAG ? 0 : p.causal_off) - a * 128);
+      const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + p.causal_off);
+      // Packed sequences: both are the query tile's last key tile.
+      if (RAG ? j == last_kv : (mask_tail || mask_diag)) {
+        int lim_col = RAG ? last_key - a * 128 : Nk - 1 - a * 128;
+        if (!RAG && CAUSAL) lim_col = min(lim_col, row + p.causal_off - a * 128);
 #pragma unroll
         for (int i = 0; i < 128; ++i)
           if (i > lim_col) s[i] = -INFINITY;
@@ -551,7 +650,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       // O~ / l is the same in exact arithmetic.
       const float m_run = fmaxf(m2, mx * c2);
       // Rows behind a packed sequence's last one, another's, have no say in it.
-      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && (!RAG || row < Nq));
+      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && (!RAG || last_key >= 0));
       const float m_ref = move ? m_run : m2;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m2 - m_use);  // 0 on the first block, 1 when the reference is kept
@@ -603,12 +702,21 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
     }
     tc_fence_after_sync();
+    if constexpr (RAG) {
+      if (alive && active) fwd_store_ragged<HD, CAUSAL>(p, sh, stage, tO, t, r, item, m2, l);
+      // (No query tile in this slot: the MMA thread waits for this arrival only at
+      // the slot's next tile, which this warpgroup cannot have passed.)
+      if (!alive || !active) mbar_arrive(&sh.o_free[t]);
+      if (active) cnt += last_kv + 1;
+      ++items;
+      continue;
+    }
     // A row that saw no key of this range (possible only when the keys are
     // split) has l = 0: its partial is O = 0, L = -inf, and the combine step
     // never reads it.
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     const float lse_row = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
-    if (!RAG && alive && active && p.splits > 1) {
+    if (alive && active && p.splits > 1) {
       // fp32 partial of this key range, straight from TMEM to the workspace
       float* dst = p.o_part + ((static_cast<size_t>(wk.s) * p.BH + head) * Nq + row) * HD;
 #pragma unroll 1
@@ -651,12 +759,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
         }
       }
       fence_proxy_async_smem();
-      if (row < Nq) {
-        if constexpr (RAG)
-          p.lse[static_cast<size_t>(head) * p.Nq + wk.row0 + row] = lse_row;
-        else
-          p.lse[static_cast<size_t>(head) * Nq + row] = lse_row;
-      }
+      if (row < Nq) p.lse[static_cast<size_t>(head) * Nq + row] = lse_row;
     } else {
       // No query tile in this slot: nothing waits for this warpgroup, so it
       // first waits for the item's Q load. That keeps its q_free / o_free
@@ -669,29 +772,11 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       mbar_arrive(&sh.o_free[t]);
     }
     named_barrier_sync(1 + t, 128);
-    // Packed sequences: the rows past a sequence's last one are the next one's,
-    // so its last tile leaves through plain stores, a row by HD / 8 lanes.
-    const bool cut = RAG && active && qt * 128 + 128 > Nq;
-    if constexpr (RAG) {
-      if (cut) {
-        constexpr int UNITS = HD / 8;
-        if (alive && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
-          __nv_bfloat16* dst = p.o + static_cast<long long>(wk.row0 + qt * 128) * p.o_strides[0] + head * p.o_strides[1];
-          const uint32_t from = smem_u32(stage);
-          for (int i = r; i < (Nq - qt * 128) * UNITS; i += 128) {
-            const int y = i / UNITS, x = i % UNITS;
-            *reinterpret_cast<uint4*>(dst + y * p.o_strides[0] + 8 * x) =
-                ld_shared_v4(from + (x >> 3) * C::CHUNK_BYTES + sw128_offset(y, x & 7));
-          }
-        }
-        named_barrier_sync(1 + t, 128);
-      }
-    }
     if (r == 0) {
-      if (!cut && alive && active && (RAG || p.splits == 1) && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
+      if (alive && active && p.splits == 1 && !*reinterpret_cast<volatile int*>(&sh.abort_flag)) {
 #pragma unroll
         for (int c = 0; c < C::CHUNKS; ++c)
-          tma_store_3d(&p.tmO, stage + c * C::CHUNK_BYTES, c * 64, wk.q_row(p, t), wk.q_head(t));
+          tma_store_3d(&p.tmO, stage + c * C::CHUNK_BYTES, c * 64, qt * rph, wk.bh);
         tma_store_commit();
         tma_store_wait_read_all();  // the staging can be overwritten by the next Q tile
       }
@@ -700,11 +785,11 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     if (active) cnt += last_kv + 1;
     ++items;
   }
-  if (r == 0) tma_store_wait_all();  // O stores complete before the CTA can exit
+  if (RAG ? lane_id() == 0 : r == 0) tma_store_wait_all();  // O stores complete before the CTA can exit
 }
 
 template <int HD, bool CAUSAL, bool PACK, bool RAG>
-__global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_constant__ FwdLaunch p) {
+__global__ void __launch_bounds__(fwd_threads<RAG>(), 1) fa_fwd_kernel(const __grid_constant__ FwdLaunch p) {
   using C = FwdCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ FwdShared sh;
@@ -734,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_consta
       mbar_init(&sh.o_free[t], 128);
       mbar_init(&sh.q_free[t], 1);
     }
+    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     sh.abort_flag = 0;
     fence_mbarrier_init();
@@ -750,7 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_fwd_kernel(const __grid_consta
   if (warp == kLoadWarp) {
     if (lane_id() == 0) fwd_load_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, sK, sV);
   } else if (warp == kMmaWarp) {
-    if (RAG || lane_id() == 0) fwd_mma_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, sK, sV, tmem);
+    if (lane_id() == 0) fwd_mma_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, sK, sV, tmem);
+  } else if (RAG && warp == kTailWarp) {
+    tail_role<C::CHUNKS, C::CHUNK_BYTES>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else if (warp < 4 * C::NT) {
     fwd_softmax_role<HD, CAUSAL, PACK, RAG>(p, sh, sQ, tmem, warp >> 2);
   }
@@ -765,7 +853,7 @@ template <int HD, bool CAUSAL, bool PACK, bool RAG = false>
 cudaError_t launch_fwd_t(const FwdLaunch& a, cudaStream_t stream) {
   using C = FwdCfg<HD>;
   auto kern = fa_fwd_kernel<HD, CAUSAL, PACK, RAG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::template smem_bytes<RAG>());
   if (e != cudaSuccess) return e;
   const int rph = PACK ? a.rph : 128;
   const int Tq = (a.Nq + rph - 1) / rph;
@@ -776,7 +864,7 @@ cudaError_t launch_fwd_t(const FwdLaunch& a, cudaStream_t stream) {
   // Persistent: one CTA per SM (the smem footprint allows no more), each
   // looping over its share of the items.
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  kern<<<static_cast<unsigned>(grid), kThreads, C::SMEM_BYTES, stream>>>(a);
+  kern<<<static_cast<unsigned>(grid), fwd_threads<RAG>(), C::template smem_bytes<RAG>(), stream>>>(a);
   return cudaGetLastError();
 }
 

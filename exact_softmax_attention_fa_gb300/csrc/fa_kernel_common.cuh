@@ -102,17 +102,6 @@ __device__ __forceinline__ int take_item(Shared& sh, int u, uint64_t lim) {
   return item;
 }
 
-// The same for a whole warp that counts as one consumer.
-template <class Shared>
-__device__ __forceinline__ int take_item_warp(Shared& sh, int u, uint64_t lim) {
-  const int s = u % kItemSlots;
-  if (!__all_sync(0xffffffffu, mbar_wait(&sh.item_full[s], (u / kItemSlots) & 1, &sh.abort_flag, lim))) return -1;
-  const int item = *reinterpret_cast<volatile int*>(&sh.item_ring[s]);
-  __syncwarp();
-  if (lane_id() == 0) mbar_arrive(&sh.item_empty[s]);
-  return item;
-}
-
 __device__ __forceinline__ int claim_item(uint32_t* ctr) {
   return static_cast<int>(gridDim.x) + static_cast<int>(atomicAdd(ctr, 1u));
 }

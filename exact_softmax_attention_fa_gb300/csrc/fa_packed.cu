@@ -395,7 +395,7 @@ fa_status_t fa_fwd_packed(const void* q, const void* k, const void* v, const lon
   if (st != FA_OK) return st;
   FwdLaunch a{};
   if (!make_rows_map(&a.tmQ, q, rows, Hq, d, s[0], 128) || !make_rows_map(&a.tmK, k, rows, Hkv, d, s[1], 128) ||
-      !make_rows_map(&a.tmV, v, rows, Hkv, d, s[2], 128) || !make_rows_map(&a.tmO, o, rows, Hq, d, s[3], 128))
+      !make_rows_map(&a.tmV, v, rows, Hkv, d, s[2], 128) || !make_rows_map(&a.tmO, o, rows, Hq, d, s[3], 32))
     return FA_ERR_CUDA;
   a.lse = lse;
   a.o = static_cast<__nv_bfloat16*>(o);
