@@ -501,26 +501,23 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
 // sequence ends, whose next rows are another's, by plain stores of whole lines.
 // (Rows straight from TMEM to global memory, a thread each, put 32 lines into
 // every store: 256 sequences of 128 rows, 32 + 8 heads: 169 us instead of 124.)
-template <int HD, bool CAUSAL>
+template <int HD>
 __device__ __forceinline__ void fwd_store_ragged(const FwdLaunch& p, FwdShared& sh, uint8_t* stage, uint32_t tO, int t,
-                                                 int r, int item, float m2, float l) {
-  asm volatile("" : "+r"(item));  // the entry is read again, not kept
-  const FwdWork<FwdCfg<HD>::NT, CAUSAL, false, true> wk(item, p);
-  const int lane = r & 31, first = wk.tile(t) * 128 + (r & ~31), head = wk.q_head(t);
-  const int held = wk.len - first;  // rows of this warp that the sequence has
-  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+                                                 int lane, int held, int grow, int head, float inv_l) {
   const uint32_t buf = smem_u32(stage);
 #pragma unroll 1
   for (int c = 0; c < HD; c += 64) {
     uint32_t w[32];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t o[32];
-      tmem_ld32(tO + c + 32 * h, o);
+    {
+      uint32_t a[32], b[32];
+      tmem_ld32(tO + c, a);
+      tmem_ld32(tO + c + 32, b);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        w[16 * h + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv_l, __uint_as_float(o[2 * e + 1]) * inv_l);
+      for (int e = 0; e < 16; ++e) {
+        w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * inv_l, __uint_as_float(a[2 * e + 1]) * inv_l);
+        w[16 + e] = pack_bf16x2(__uint_as_float(b[2 * e]) * inv_l, __uint_as_float(b[2 * e + 1]) * inv_l);
+      }
     }
     if (c + 64 >= HD) {  // O~_t fully read: the next item's first PV may overwrite it
       tc_fence_before_sync();
@@ -536,12 +533,12 @@ __device__ __forceinline__ void fwd_store_ragged(const FwdLaunch& p, FwdShared& 
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(&p.tmO, stage, c, wk.row0 + first, head);
+        tma_store_3d(&p.tmO, stage, c, grow, head);
         tma_store_commit();
       }
     } else {
       __syncwarp();
-      __nv_bfloat16* dst = p.o + static_cast<long long>(wk.row0 + first) * p.o_strides[0] + head * p.o_strides[1] + c;
+      __nv_bfloat16* dst = p.o + static_cast<long long>(grow) * p.o_strides[0] + head * p.o_strides[1] + c;
       uint4 x[8];
 #pragma unroll
       for (int y = 0; y < 8; ++y) x[y] = ld_shared_v4(buf + sw128_offset(4 * y + (lane >> 3), lane & 7));
@@ -549,11 +546,8 @@ __device__ __forceinline__ void fwd_store_ragged(const FwdLaunch& p, FwdShared& 
       for (int y = 0; y < 8; ++y)
         if (4 * y + (lane >> 3) < held)
           *reinterpret_cast<uint4*>(dst + (4 * y + (lane >> 3)) * p.o_strides[0] + 8 * (lane & 7)) = x[y];
-      __syncwarp();
     }
   }
-  if (lane < held)
-    p.lse[static_cast<size_t>(head) * p.Nq + wk.row0 + first + lane] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int HD, bool CAUSAL, bool PACK, bool RAG>
@@ -580,7 +574,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
   int items = 0;  // items processed (those with work)
 
   for (int k = 0; k * G < total; ++k) {
-    const int item = sched_item(k, blockIdx.x, G);
+    int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;
     const FwdWork<C::NT, CAUSAL, PACK, RAG> wk(item, p);
     if (wk.nkv == 0) continue;
@@ -590,14 +584,15 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     const int rph = rows_per_head<PACK>(p);
     const int row = qt * rph + (r & (rph - 1));
     const int head = wk.bh + r / rph;
-    // Packed sequences: the last key the row sees, -1 for a row behind the sequence.
-    // What else the epilogue needs it looks up again: held through the loop it
-    // costs registers there.
-    const int last_key = !RAG || row >= wk.n_queries(p) ? -1 : (CAUSAL ? row : wk.n_keys(p) - 1);
+    // Packed sequences: the last column of the query tile's last key tile that the
+    // row sees (-1: a row behind the sequence). What else the epilogue needs it
+    // looks up again: held through the loop it costs registers there.
+    const int last_col =
+        !RAG || row >= wk.n_queries(p) ? -1 : (CAUSAL ? r : min(127, wk.n_keys(p) - 1 - last_kv * 128));
 
     float m2 = -INFINITY;  // reference max of S * scale * log2(e)
     float l = 0.f;         // running sum of P~ (unrounded fp32)
-    for (int j = 0; j <= last_kv; ++j) {
+    for (int j = 0; j <= last_kv - (RAG ? 1 : 0); ++j) {
       alive = alive && __all_sync(0xffffffffu, mbar_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim));
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
@@ -625,10 +620,10 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       const int a = wk.kv0 + j;  // absolute key tile
       const bool mask_tail = (a == Tk - 1) && (Nk & 127);
       const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + p.causal_off);
-      // Packed sequences: both are the query tile's last key tile.
-      if (RAG ? j == last_kv : (mask_tail || mask_diag)) {
-        int lim_col = RAG ? last_key - a * 128 : Nk - 1 - a * 128;
-        if (!RAG && CAUSAL) lim_col = min(lim_col, row + p.causal_off - a * 128);
+      // (over packed sequences both are the query tile's last key tile, taken below)
+      if (!RAG && (mask_tail || mask_diag)) {
+        int lim_col = Nk - 1 - a * 128;
+        if (CAUSAL) lim_col = min(lim_col, row + p.causal_off - a * 128);
 #pragma unroll
         for (int i = 0; i < 128; ++i)
           if (i > lim_col) s[i] = -INFINITY;
@@ -650,7 +645,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       // O~ / l is the same in exact arithmetic.
       const float m_run = fmaxf(m2, mx * c2);
       // Rows behind a packed sequence's last one, another's, have no say in it.
-      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && (!RAG || last_key >= 0));
+      const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && (!RAG || last_col >= 0));
       const float m_ref = move ? m_run : m2;
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float alpha = ex2_approx(m2 - m_use);  // 0 on the first block, 1 when the reference is kept
@@ -693,6 +688,116 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       mbar_arrive(&sh.p_full[t]);
     }
 
+    if constexpr (RAG) {
+      // The last key tile, in 32-column steps: columns that no row of the warp sees
+      // (right of a causal diagonal, behind the last key) cost nothing but the zeros
+      // that the product reads, and only steps that a limit crosses are masked.
+      // Short sequences are all last tiles.
+      const bool active = last_kv >= 0;
+      if (active) {
+        alive = alive &&
+                __all_sync(0xffffffffu, mbar_wait(&sh.s_full[t], (cnt + last_kv) & 1, &sh.abort_flag, lim));
+        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
+      }
+      if (alive && active) {
+        tc_fence_after_sync();
+        const int held = min(128, wk.n_keys(p) - last_kv * 128);              // keys of the tile
+        const int seen = CAUSAL ? min(held, 32 * ((r >> 5) + 1)) : held;     // columns that the warp sees
+        float s[128];
+        {
+          uint32_t a[32], b[32], c[32], d[32];
+          tmem_ld32(tS + 0, a);
+          tmem_ld32(tS + 32, b);
+          tmem_ld32(tS + 64, c);
+          tmem_ld32(tS + 96, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(a[i]);
+            s[32 + i] = __uint_as_float(b[i]);
+            s[64 + i] = __uint_as_float(c[i]);
+            s[96 + i] = __uint_as_float(d[i]);
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < seen) {
+            if ((CAUSAL && c == (r >> 5)) || 32 * c + 32 > held) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i > last_col) s[32 * c + i] = -INFINITY;
+            }
+            float m0 = mx, m1 = s[32 * c];
+#pragma unroll
+            for (int i = 1; i < 31; i += 4) {
+              m0 = fmax3(m0, s[32 * c + i], s[32 * c + i + 1]);
+              if (i + 2 < 31) m1 = fmax3(m1, s[32 * c + i + 2], s[32 * c + i + 3]);
+            }
+            mx = fmax3(m0, m1, s[32 * c + 31]);
+          }
+        const float m_run = fmaxf(m2, mx * c2);
+        const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && last_col >= 0);
+        const float m_ref = move ? m_run : m2;
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const float alpha = ex2_approx(m2 - m_use);
+        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          if (32 * c < seen) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = ffma2_bcast(s[32 * c + 2 * i], s[32 * c + 2 * i + 1], c2, -m_use);
+              const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              if (i & 1) sum_b = fadd2(sum_b, e); else sum_a = fadd2(sum_a, e);
+              pk[i] = pack_bf16x2(e.x, e.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+          }
+          if (32 * c < held) tmem_st16(tP + 16 * c, pk);
+        }
+        const float2 sum2 = fadd2(sum_a, sum_b);
+        l = l * alpha + (sum2.x + sum2.y);
+        if (last_kv > 0 && move) {
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + c, o);
+          }
+        }
+        m2 = m_ref;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(&sh.p_full[t]);
+
+        // L, and where O goes, while the last product runs.
+        asm volatile("" : "+r"(item));  // the entry is read again, not kept
+        const FwdWork<C::NT, CAUSAL, PACK, RAG> wo(item, p);
+        const int first = wo.tile(t) * 128 + (r & ~31), o_head = wo.q_head(t), grow = wo.q_row(p, t) + (r & ~31);
+        const int rows = wo.n_queries(p) - first;  // of this warp that the sequence has
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        if ((r & 31) < rows)
+          p.lse[static_cast<size_t>(o_head) * p.Nq + grow + (r & 31)] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+        alive = __all_sync(0xffffffffu, mbar_wait(&sh.pv_done[t], (cnt + last_kv) & 1, &sh.abort_flag, lim));
+        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
+        tc_fence_after_sync();
+        if (alive) fwd_store_ragged<HD>(p, sh, stage, tO, t, r & 31, rows, grow, o_head, inv_l);
+      }
+      // (No query tile in this slot: the MMA thread waits for this arrival only at
+      // the slot's next tile, which this warpgroup cannot have passed.)
+      if (!alive || !active) mbar_arrive(&sh.o_free[t]);
+      if (active) cnt += last_kv + 1;
+      ++items;
+      continue;
+    }
+
     // Epilogue: wait for the last O~ += P~ V, normalise, store through the
     // (now free) Q_t smem; then hand O~_t and Q_t's smem back to the MMA and
     // load threads for the next item.
@@ -702,15 +807,6 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
     }
     tc_fence_after_sync();
-    if constexpr (RAG) {
-      if (alive && active) fwd_store_ragged<HD, CAUSAL>(p, sh, stage, tO, t, r, item, m2, l);
-      // (No query tile in this slot: the MMA thread waits for this arrival only at
-      // the slot's next tile, which this warpgroup cannot have passed.)
-      if (!alive || !active) mbar_arrive(&sh.o_free[t]);
-      if (active) cnt += last_kv + 1;
-      ++items;
-      continue;
-    }
     // A row that saw no key of this range (possible only when the keys are
     // split) has l = 0: its partial is O = 0, L = -inf, and the combine step
     // never reads it.
