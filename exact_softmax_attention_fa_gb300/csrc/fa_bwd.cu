@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "fa_internal.h"
@@ -418,7 +419,7 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
   };
 
   int g = 0, items = 0;
-  TailCalls tail;
+  TailCalls<true> tail;
   while (true) {
     const int item = take_item(sh, items, lim);
     if (item < 0) return fail();
@@ -426,21 +427,17 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
     const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int s0 = g % C::QST;
-    typename BwdWork<CAUSAL, RAG>::Pos pos = wk.first();
-    // steps of 16 queries of tile i in the products over queries
-    auto take_tile = [&](int slot, int i) -> int {
-      if constexpr (RAG) {
-        const int held = wk.n - i * 128;
-        if (held >= 128) return 8;
-        tail.ask(sh.tail, held, q_addr + slot * C::TILE_BYTES, do_addr + slot * C::TILE_BYTES);
-        return (held + 15) >> 4;
-      }
-      return 8;
-    };
+    // Packed sequences: steps of 16 queries that a product over the last query tile
+    // takes (8: all), and tiles of the stream until the next such tile. (Walking
+    // the stream here too cost this thread, whose waits and issues are the chain
+    // that a tile takes, 5% of the kernel's time.)
+    const int held = RAG ? wk.len(p) - (wk.T - 1) * 128 : 128;
+    int until = held < 128 ? wk.nq - 1 : INT_MAX;
+    auto ask = [&](int slot) { tail.ask(sh.tail, held, q_addr + slot * C::TILE_BYTES, do_addr + slot * C::TILE_BYTES); };
     if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) ||
         !mbar_wait(&sh.qdo_full[s0], (g / C::QST) & 1, &sh.abort_flag, lim))
       return fail();
-    int steps = take_tile(s0, pos.i), next_steps = 8;
+    if (RAG && until == 0) ask(s0);
     // Region A held the previous item's last P^T, region B its last dQ.
     if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
     if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
@@ -456,6 +453,7 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
       const int s = g % C::QST;
       const bool has_next = n + 1 < n_iter;
       const int s1 = (g + 1) % C::QST;
+      const int steps = RAG && until == 0 ? (held + 15) >> 4 : 8;
       const uint32_t qa = q_addr + s * C::TILE_BYTES, doa = do_addr + s * C::TILE_BYTES;
       if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
       if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
@@ -469,10 +467,7 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
         if (!mbar_wait(&sh.qdo_full[s1], ((g + 1) / C::QST) & 1, &sh.abort_flag, lim)) return fail();
-        if constexpr (RAG) {
-          wk.advance(pos);
-          next_steps = take_tile(s1, pos.i);
-        }
+        if (RAG && (until == 0 ? until = wk.nq - 1 : --until) == 0) ask(s1);
         if (!mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
         if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
@@ -510,7 +505,6 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
         issue_sq(C::REG_B, v_addr, do_addr + s1 * C::TILE_BYTES);  // dP^T(n+1) over the drained dQ_n
         umma_commit(&sh.dp_full);
       }
-      if constexpr (RAG) steps = next_steps;
     }
     umma_commit(&sh.acc_done);
     ++items;
@@ -552,13 +546,14 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
 
   // L2 / D of query tile i of head bh for this warpgroup's 64 columns:
   // thread r < 64 loads L2[r], thread r >= 64 loads D[r - 64] * scale.
-  // Queries behind a packed sequence's last one get L2 = +inf (weight 0) and D = 0.
+  // Queries behind a packed sequence's last one get L2 = +inf and D = 0, and their
+  // rows of Q and dO are cleared: S = 0 gives weight 0, and dP = 0 makes dS = 0.
   auto fetch_ld = [&](const BwdWork<CAUSAL, RAG>& wk, int bh, int i) -> float {
     if constexpr (RAG) {
       const int q = i * 128 + 64 * w + (r & 63);
-      if (q >= wk.n) return r < 64 ? INFINITY : 0.f;
-      const size_t at = static_cast<size_t>(bh) * p.N + wk.row0 + q;
-      return r < 64 ? __ldg(p.lse2 + at) : __ldg(p.D + at) * sc;
+      const float* from = (r < 64 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
+      const float x = __ldg(from + min(q, wk.n - 1));
+      return r < 64 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
     }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * 128 + 64 * w;
     return r < 64 ? __ldg(p.lse2 + row + r) : __ldg(p.D + row + (r - 64)) * sc;
@@ -600,10 +595,10 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     }
     // Only the key-tail tile and the causal diagonal tile need masking:
     // query (64w + c) sees key r only if 64w + c >= r.
-    const bool key_valid = wk.j * 128 + r < wk.len(p);
-    // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
-    const int c_hi = RAG ? wk.len(p) - i * 128 - 64 * w : 64;
-    const bool masked = !key_valid || (CAUSAL && i == wk.j) || (RAG && c_hi < 64);
+    // (Over packed sequences a key behind the last one stays: its row of P^T and
+    // dS^T reaches only its own row of dV and dK, which is not written.)
+    const bool key_valid = RAG || wk.j * 128 + r < wk.len(p);
+    const bool masked = !key_valid || (CAUSAL && i == wk.j);
     const int c_lo = !key_valid ? 64 : ((CAUSAL && i == wk.j) ? r - 64 * w : 0);
     // Three passes over the row (exponent arguments, exponentials, bf16
     // pairs) give the scheduler long runs of independent instructions.
@@ -622,7 +617,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     if (masked) {
 #pragma unroll
       for (int c = 0; c < 64; ++c)
-        if (c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
+        if (c < c_lo) pv[c] = 0.f;
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
@@ -633,7 +628,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   };
 
   // ---- phase B: dS^T = P^T o (dP^T - D) * scale -> smem (bf16, swizzled)
-  auto phase_b = [&](const BwdWork<CAUSAL, RAG>& wk, int i, int g) {
+  auto phase_b = [&](int g) {
     // the scaled D values, read from smem while dP^T is still being computed
     // (as the logsumexps in phase A)
     float4 dvv[kPrefetchStats ? 16 : 1];
@@ -664,14 +659,6 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
         const float2 ds23 = fmul2(p23, g23);
         dk[c4 / 2] = pack_bf16x2(ds01.x, ds01.y);
         dk[c4 / 2 + 1] = pack_bf16x2(ds23.x, ds23.y);
-      }
-      if constexpr (RAG) {
-        // dP of queries behind the sequence's last may be infinite or NaN
-        const int held = wk.len(p) - i * 128 - 64 * w - 32 * h;
-        if (held < 32) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
-        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -822,7 +809,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       typename BwdWork<CAUSAL, RAG>::Pos nxt = cur;
       wk.advance(nxt);
       const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
-      phase_b(wk, cur.i, g + n);
+      phase_b(g + n);
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         sLD[w * 128 + r] = next_ld;
@@ -903,7 +890,7 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_kernel(const 
   } else if (warp == kMmaWarp) {
     if (lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ, RAG>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
   } else if (RAG && warp == kTailWarp) {
-    tail_role<C::CHUNKS, C::CHUNK_BYTES>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
+    tail_role<C::CHUNKS, C::CHUNK_BYTES, 128>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     bwd_softmax_role<HD, CAUSAL, DQ, RAG>(p, sh, sDS, sLD, sDQ, tmem, wg);
   }

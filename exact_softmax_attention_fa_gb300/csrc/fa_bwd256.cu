@@ -43,7 +43,9 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
@@ -334,7 +336,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
   };
 
   int g = 0, items = 0;
-  TailCalls tail;
+  TailCalls<false> tail;
   while (true) {
     const int item = take_item(sh, items, lim);
     if (item < 0) return fail();
@@ -342,35 +344,30 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
     const Work256<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     const int h = wk.h;
-    typename Work256<CAUSAL, RAG>::Pos pos = wk.first();
-    // steps of 16 queries of tile i in the products over queries
-    auto tile_steps = [&](int i) -> int { return RAG ? min(4, (wk.len(p) - i * C::BQ + 15) >> 4) : 4; };
-    // the rows of a half tile of query tile i behind the sequence's last query, if any, are cleared
-    auto clean = [&](uint32_t half_tile, int i) -> bool {
-      if constexpr (RAG) {
-        const int held = wk.n - i * C::BQ;
-        if (held < C::BQ) tail.ask(sh.tail, held, half_tile);
-        return tail.wait(sh.tail, &sh.abort_flag, lim);
-      }
-      return true;
+    // Packed sequences: as in fa_bwd.cu, steps of 16 queries that a product over the
+    // last query tile takes, and tiles of the stream until the next such tile.
+    const int held = RAG ? wk.len(p) - (wk.T64 - 1) * C::BQ : C::BQ;
+    int until = held < C::BQ ? wk.T64 - 1 - wk.i0 : INT_MAX;
+    auto clean = [&](uint32_t half_tile) -> bool {
+      tail.ask(sh.tail, held, half_tile);
+      return tail.wait(sh.tail, &sh.abort_flag, lim);
     };
-    auto q_clean = [&](int n, int i) { return clean(qh_addr + (n % C::QH_SLOTS) * C::HALF_BYTES, i); };
     if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) || !wait_s_operands(g)) return fail();
     // S^T overwrites the previous item's last P^T: dV must have read it.
     if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
-    if (!q_clean(g, pos.i)) return fail();
+    if (RAG && until == 0 && !clean(qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES)) return fail();
     issue_s(g, h);
     // dP^T overwrites the previous item's last dP^T, which phase B read
     // before ds_ready (waited for in the previous item's last step).
     if (!wait_dp_operands(g)) return fail();
-    if (!clean(doh_addr, pos.i)) return fail();
-    int steps = tile_steps(pos.i);
+    if (RAG && until == 0 && !clean(doh_addr)) return fail();
     tc_fence_after_sync();
     issue_dp(h);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const bool has_next = n + 1 < n_iter;
+      const int steps = RAG && until == 0 ? (held + 15) >> 4 : 4;
       if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
       // the first dV / dK of an item overwrite the accumulators: the previous
       // item's epilogue must have read them
@@ -387,10 +384,9 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
         if (!wait_s_operands(g + 1) || !mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
-        if constexpr (RAG) {
-          wk.advance(pos);
-          if (!q_clean(g + 1, pos.i)) return fail();
-        }
+        if (RAG && (until == 0 ? until = wk.T64 - 1 - wk.i0 : --until) == 0 &&
+            !clean(qh_addr + ((g + 1) % C::QH_SLOTS) * C::HALF_BYTES))
+          return fail();
         issue_s(g + 1, h);
       }
       if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
@@ -418,8 +414,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       if (has_next) {
         // dP^T(n+1): phase B(n) has read dP^T(n) (ds_ready above)
         if (!wait_dp_operands(g + 1)) return fail();
-        if (!clean(doh_addr, pos.i)) return fail();
-        steps = tile_steps(pos.i);
+        if (RAG && until == 0 && !clean(doh_addr)) return fail();
         tc_fence_after_sync();
         issue_dp(h);
       }
@@ -460,10 +455,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   auto fetch_ld = [&](const Work256<CAUSAL, RAG>& wk, int bh, int i) -> float {
     if constexpr (RAG) {
       const int q = i * C::BQ + 32 * w + (r & 31);
-      if (r >= 64) return 0.f;
-      if (q >= wk.n) return r < 32 ? INFINITY : 0.f;
-      const size_t at = static_cast<size_t>(bh) * p.N + wk.row0 + q;
-      return r < 32 ? __ldg(p.lse2 + at) : __ldg(p.D + at) * sc;
+      const float* from = (r < 32 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
+      const float x = __ldg(from + min(q, wk.n - 1));
+      return r < 32 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
     }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * C::BQ + 32 * w;
     if (r < 32) return __ldg(p.lse2 + row + r);
@@ -486,9 +480,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     // key 128j + r is seen by query 64i + 32w + c if it exists and (causal)
     // is not after the query: c >= c_lo
     const int key = wk.j * 128 + r;
-    const bool key_valid = key < wk.len(p);
-    // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
-    const int c_hi = RAG ? wk.len(p) - i * C::BQ - 32 * w : 32;
+    const bool key_valid = RAG || key < wk.len(p);  // see fa_bwd.cu
     const int c_lo = CAUSAL ? key - i * C::BQ - 32 * w : 0;
     float pv[32];
 #pragma unroll
@@ -503,7 +495,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) pv[c] = ex2_approx(pv[c]);
-    if (!key_valid || (CAUSAL && c_lo > 0) || (RAG && c_hi < 32)) {
+    if (!key_valid || (CAUSAL && c_lo > 0) || (RAG && i == wk.T64 - 1)) {
+      // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
+      const int c_hi = RAG ? wk.len(p) - i * C::BQ - 32 * w : 32;
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         if (!key_valid || c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
@@ -517,7 +511,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   };
 
   // ---- phase B: dS^T = P^T o (dP^T - D) * scale -> smem row r, queries [32w, 32w + 32)
-  auto phase_b = [&](const Work256<CAUSAL, RAG>& wk, int i, int g) {
+  // CUT: a packed sequence's last query tile. (One test a tile, around the whole
+  // phase: inside it keeps the compiler from overlapping the TMEM loads.)
+  auto phase_b = [&](const Work256<CAUSAL, RAG>& wk, int i, int g, auto cut) {
     wait_all(&sh.dp_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t dpv[32];
@@ -536,13 +532,11 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
       dk[c4 / 2] = pack_bf16x2(ds01.x, ds01.y);
       dk[c4 / 2 + 1] = pack_bf16x2(ds23.x, ds23.y);
     }
-    if constexpr (RAG) {
+    if constexpr (decltype(cut)::value) {
       // dP of queries behind the sequence's last may be infinite or NaN
       const int held = wk.len(p) - i * C::BQ - 32 * w;
-      if (held < 32) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
-      }
+      for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -636,7 +630,10 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
       typename Work256<CAUSAL, RAG>::Pos nxt = cur;
       wk.advance(nxt);
       const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
-      phase_b(wk, cur.i, g + n);
+      if (RAG && cur.i == wk.T64 - 1)
+        phase_b(wk, cur.i, g + n, std::bool_constant<RAG>());
+      else
+        phase_b(wk, cur.i, g + n, std::false_type());
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         if (r < 64) sLD[w * 64 + r] = next_ld;

@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
@@ -260,7 +261,7 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
   };
 
   int u = 0, kv = 0, t = 0;
-  TailCalls tail;
+  TailCalls<false> tail;
   while (true) {
     const int item = take_item(sh, u, lim);
     if (item < 0) return fail();
@@ -272,32 +273,39 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
     if (wk.nkv == 1) umma_commit(&sh.q_free);
     // Per tile t: S(t+1) as soon as its K tile is in, dP(t+1) once phase B(t)
     // has read dP(t), dQ += dS(t) K once phase B(t) has written dS(t).
-    for (int j = 0; j < wk.nkv; ++j, ++kv, ++t) {
+    // LAST: the item's last tile, which over packed sequences may end in rows of the
+    // next sequence (see the forward).
+    auto step = [&](int j, auto last_tile) -> bool {
+      constexpr bool LAST = decltype(last_tile)::value;
       const int s = kv % C::KST;
-      if (j + 1 < wk.nkv) {
-        if (!issue_s(t + 1, kv + 1, t - 1) || !issue_dp(t + 1, kv + 1)) return fail();
+      if (RAG ? !LAST : j + 1 < wk.nkv) {
+        if (!issue_s(t + 1, kv + 1, t - 1) || !issue_dp(t + 1, kv + 1)) return false;
         if (j + 2 == wk.nkv) umma_commit(&sh.q_free);  // the item's last S and dP are issued
       }
-      if (RAG && wk.len(p) - j * 128 < 128) {  // once S(t) has read K_j
-        if (!mbar_wait(&sh.s_full[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return fail();
+      int steps = 8;  // of 16 keys
+      if (RAG && LAST && wk.len(p) - j * 128 < 128) {  // once S(t) has read K_j
+        steps = (wk.len(p) - j * 128 + 15) >> 4;
+        if (!mbar_wait(&sh.s_full[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return false;
         tail.ask(sh.tail, wk.len(p) - j * 128, k_addr + s * C::TILE_BYTES);
       }
-      if (!mbar_wait(&sh.ds_ready[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return fail();
-      if (RAG && !tail.wait(sh.tail, &sh.abort_flag, lim)) return fail();
+      if (!mbar_wait(&sh.ds_ready[t & 1], (t >> 1) & 1, &sh.abort_flag, lim)) return false;
+      if (RAG && LAST && !tail.wait(sh.tail, &sh.abort_flag, lim)) return false;
       // the first dQ product of an item overwrites the accumulator: the
       // previous item's epilogue must have read it
-      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return false;
       tc_fence_after_sync();
       // dS (bf16 pairs) sits in columns [0, 32) and [64, 96) of S buffer t & 1:
       // keys 16 ks .. 16 ks + 15 are 8 columns at 64 (ks / 4) + 8 (ks % 4)
-      const int steps = RAG ? std::min(8, (wk.len(p) - j * 128 + 15) >> 4) : 8;  // of 16 keys
       const uint64_t kd = make_smem_desc_sw128(k_addr + s * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
-      issue_steps<8, RAG>(steps, [&](int ks) {
+      issue_steps<8, RAG && LAST>(steps, [&](int ks) {
         umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.dq_done);
       umma_commit(&sh.k_empty[s]);
-    }
+      return true;
+    };
+    for (int j = 0; j < wk.nkv; ++j, ++kv, ++t)
+      if (!(RAG && j + 1 < wk.nkv ? step(j, std::false_type()) : step(j, std::true_type()))) return fail();
     umma_commit(&sh.acc_done);
     ++u;
   }

@@ -236,7 +236,7 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
     drain_mmas(&sh.mma_drain, lim);
   };
   int pos = 0;  // ring chunks consumed
-  TailCalls tail;
+  TailCalls<false> tail;
   auto wait_chunk = [&](int k) -> bool {
     return mbar_wait(&sh.ring_full[k % C::RING], (k / C::RING) & 1, &sh.abort_flag, lim);
   };
@@ -259,19 +259,20 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
   };
   // dQ += dS K_t: two N = 128 halves of the head dimension, each reading an
   // even-aligned pair of ring chunks as one MN-major B operand.
-  // held: keys of the sequence from tile t on.
+  // held: keys of the sequence in the tile, if it is the item's last one and cut short.
   auto issue_dq = [&](bool first, int held) -> bool {
-    const int steps = RAG ? min(8, (held + 15) >> 4) : 8;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half, pos += 2) {
       if (!wait_chunk(pos) || !wait_chunk(pos + 1)) return false;
       if constexpr (RAG) {
-        if (held < 128) tail.ask(sh.tail, held, slot_addr(pos), slot_addr(pos + 1));
-        if (!tail.wait(sh.tail, &sh.abort_flag, lim)) return false;
+        if (held < 128) {
+          tail.ask(sh.tail, held, slot_addr(pos), slot_addr(pos + 1));
+          if (!tail.wait(sh.tail, &sh.abort_flag, lim)) return false;
+        }
       }
       tc_fence_after_sync();
       const uint64_t kd = make_smem_desc_sw128(slot_addr(pos), C::CHUNK_BYTES, 1024);
-      issue_steps<8, RAG>(steps, [&](int ks) {
+      issue_steps<8, RAG>((held + 15) >> 4, [&](int ks) {
         umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.ring_empty[pos % C::RING]);
@@ -313,7 +314,7 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
       // previous item's epilogue must have read it
       if (j == 0 && u > 0 && !mbar_wait(&sh.acc_free, (u - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
-      if (!issue_dq(j == 0, wk.len(p) - j * 128)) return fail();
+      if (!issue_dq(j == 0, RAG && !has_next ? min(128, wk.len(p) - j * 128) : 128)) return fail();
       umma_commit(&sh.dq_done);
       if (has_next) {
         // dP(t+1) overwrites dS(t): wait for the dQ product to have read it

@@ -390,7 +390,7 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   int kv = 0;             // running K/V tile index
   int items = 0;          // items processed
   int cnt[2] = {0, 0};    // running S / P / PV count per query-tile slot
-  TailCalls tail;
+  TailCalls<false> tail;
   for (int k = 0; k * G < total; ++k) {
     const int item = sched_item(k, blockIdx.x, G);
     if (item >= total) continue;

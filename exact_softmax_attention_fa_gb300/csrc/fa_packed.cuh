@@ -61,7 +61,8 @@ __device__ __forceinline__ void tail_init(TailShared& t) {
 // The clearing warp. A wait for the next request is no sign of a failure however
 // long it takes: the MMA thread's own waits are bounded, and it ends with a last
 // request or with the abort flag. The number of waits is bounded all the same.
-template <int CHUNKS, int CHUNK_BYTES>
+// ALL_ROWS: 0, or the rows of a tile, all of which from the sequence's end on are cleared.
+template <int CHUNKS, int CHUNK_BYTES, int ALL_ROWS = 0>
 __device__ void tail_role(TailShared& t, const int* abort_flag, uint64_t lim) {
   constexpr int kMostWaits = 1 << 16;
   for (int n = 0, waits = 0; waits < kMostWaits;) {
@@ -72,7 +73,7 @@ __device__ void tail_role(TailShared& t, const int* abort_flag, uint64_t lim) {
     }
     const int held = *reinterpret_cast<volatile int*>(&t.held);
     if (held == 0) return;
-    const int units = (((held + 15) & ~15) - held) * 8;  // of 16 bytes, in a chunk
+    const int units = ((ALL_ROWS ? ALL_ROWS : (held + 15) & ~15) - held) * 8;  // of 16 bytes, in a chunk
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t tile = *reinterpret_cast<volatile uint32_t*>(&t.tile[k]);
@@ -88,12 +89,13 @@ __device__ void tail_role(TailShared& t, const int* abort_flag, uint64_t lim) {
 }
 
 // The MMA thread's side: ask, and wait until it is done. A tile whose last step
-// is whole asks for nothing.
+// is whole asks for nothing unless all rows are cleared.
+template <bool ALL>
 struct TailCalls {
   int asked = 0;
   bool open = false;
   __device__ __forceinline__ void ask(TailShared& t, int held, uint32_t tile0, uint32_t tile1 = 0) {
-    if (!(held & 15)) return;
+    if (!ALL && !(held & 15)) return;
     *reinterpret_cast<volatile uint32_t*>(&t.tile[0]) = tile0;
     *reinterpret_cast<volatile uint32_t*>(&t.tile[1]) = tile1;
     *reinterpret_cast<volatile int*>(&t.held) = held;
