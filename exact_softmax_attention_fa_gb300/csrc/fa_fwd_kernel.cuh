@@ -228,7 +228,8 @@ template <bool PACK, bool RAG>
 __device__ __forceinline__ int total_items(const FwdLaunch& p, int NT) {
   if constexpr (RAG) {
     if (!packed_plan_ok(p.plan, p.Nq)) return 0;
-    return NT > 1 && !p.pair_heads ? p.plan->n_pairs * p.BH : p.plan->n_tiles * (p.BH / (NT > 1 ? 2 : 1));
+    const int s = p.plan->n_short;  // not this kernel's
+    return NT > 1 && !p.pair_heads ? (p.plan->n_pairs - s) * p.BH : (p.plan->n_tiles - s) * (p.BH / (NT > 1 ? 2 : 1));
   }
   const int rph = rows_per_head<PACK>(p);
   const int Tq = (p.Nq + rph - 1) / rph;
@@ -895,9 +896,11 @@ __global__ void __launch_bounds__(fwd_threads<RAG>(), 1) fa_fwd_kernel(const __g
   uint8_t* sV = sK + C::KST * C::TILE_BYTES;
   const int warp = threadIdx.x >> 5;
   // Split key ranges: the combine kernel queued next may take SMs as this
-  // grid's CTAs leave them (it waits for this grid before it reads).
-  if (!RAG && p.splits > 1) griddep_launch_dependents();
+  // grid's CTAs leave them (it waits for this grid before it reads). Packed
+  // sequences: so may the kernel for the short ones.
+  if (RAG || p.splits > 1) griddep_launch_dependents();
   if (RAG && blockIdx.x == 0 && threadIdx.x == 0 && !packed_plan_ok(p.plan, p.Nq)) record_bad_index(p.status, WHERE_PACKED);
+  if (RAG && total_items<PACK, RAG>(p, C::NT) == 0) return;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) mbar_init(&sh.q_full[t], 1);

@@ -100,6 +100,17 @@ struct BwdLaunch {
   long long dq_strides[2], dk_strides[2], dv_strides[2];  // of a row and a head, in elements
 };
 
+// The short sequences of a packed batch (fa_packed_short.cu).
+struct ShortLaunch {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* o;
+  float* lse;
+  long long q_st[2], k_st[2], v_st[2], o_st[2];  // strides of a row and a head, in elements
+  const PackedPlan* plan;
+  int rows, Hq, Hkv, device, num_sms;
+  float scale_log2;
+};
+
 // Checks of the sizes, flag and scale common to every entry point; *empty is
 // set when the problem has no rows (fa_api.cu).
 fa_status_t check_common(int B, int H, int N, int d, int causal, float scale, bool* empty);
@@ -151,6 +162,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_fwd_combine(const FwdLaunch& a, cudaStream_t stream);  // splits > 1: merge the partials
 cudaError_t launch_fwd_packed(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_pack.cu: pack > 1
+cudaError_t launch_fwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream);  // fa_packed_short.cu
 cudaError_t launch_fwd_ragged(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_ragged.cu: plan set
 cudaError_t launch_bwd_pre(const BwdLaunch& a, cudaStream_t stream);   // D, base-2 L, zero dQ accumulator
 cudaError_t launch_bwd_main(const BwdLaunch& a, cudaStream_t stream);  // dK, dV; dQ into the accumulator

@@ -37,7 +37,7 @@ constexpr int kOwnTiles = 8;  // a lane lists its own sequence up to this length
 
 struct PlanShared {
   int bin[2][kBins];
-  int max_tiles;
+  int max_tiles, n_short;
   unsigned long long causal, full;
 };
 
@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   __shared__ PlanShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    sh.max_tiles = 0;
+    sh.max_tiles = sh.n_short = 0;
     sh.causal = sh.full = 0;
   }
   __syncthreads();
   bool bad = false;
-  int most = 0;
+  int most = 0, n_short = 0;
   unsigned long long sum_c = 0, sum_f = 0;
   for (int b = tid; b < B; b += kPlanThreads) {
     const int from = cu[b], to = cu[b + 1];
@@ -67,15 +67,17 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
     most = max(most, static_cast<int>(T));
     sum_c += T * (T + 1) / 2;
     sum_f += T * T;
+    n_short += to > from && to - from <= kShortRows;
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       record_bad_index(status, WHERE_PACKED_PLAN);
-      *plan = PackedPlan{kPackedMagic, rows, 0, 0, pairs_at, 0, 0, 0, 0, 0};
+      *plan = PackedPlan{kPackedMagic, rows, 0, 0, 0, pairs_at, 0, 0, 0, 0, 0};
     }
     return;
   }
   atomicMax(&sh.max_tiles, most);
+  if (n_short) atomicAdd(&sh.n_short, n_short);
   if (sum_f) {
     atomicAdd(&sh.causal, sum_c);
     atomicAdd(&sh.full, sum_f);
@@ -83,15 +85,18 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   __syncthreads();
   const int longest = sh.max_tiles;
   int shift = 0;
-  while ((longest >> shift) >= kBins) ++shift;
-  const int bins = (longest >> shift) + 1;
+  while (((longest + (1 << shift) - 1) >> shift) >= kBins) ++shift;
+  const int bins = ((longest + (1 << shift) - 1) >> shift) + 1;
   for (int i = tid; i < 2 * bins; i += kPlanThreads) sh.bin[i >= bins][i % bins] = 0;
   __syncthreads();
 
   // visit(list, first row, length, index, work) for every tile (list 0) and pair of tiles (1)
   auto each = [&](auto visit) {
-    auto tile = [&](int row0, int n, int T, int i) { visit(0, row0, n, i, causal ? i + 1 : T); };
-    auto pair = [&](int row0, int n, int T, int w) { visit(1, row0, n, w, causal ? min(2 * w + 2, T) : T); };
+    // (short sequences, which have lists to themselves, count as no work)
+    auto tile = [&](int row0, int n, int T, int i) { visit(0, row0, n, i, n <= kShortRows ? 0 : causal ? i + 1 : T); };
+    auto pair = [&](int row0, int n, int T, int w) {
+      visit(1, row0, n, w, n <= kShortRows ? 0 : causal ? min(2 * w + 2, T) : T);
+    };
     for (long long b0 = 32 * warp; b0 < B; b0 += kPlanThreads) {
       const bool in = b0 + lane < B;
       const int row0 = in ? cu[b0 + lane] : 0, n = in ? cu[b0 + lane + 1] - row0 : 0;
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
       }
     }
   };
-  each([&](int list, int, int, int, int work) { atomicAdd(&sh.bin[list][work >> shift], 1); });
+  each([&](int list, int, int, int, int work) { atomicAdd(&sh.bin[list][(work + (1 << shift) - 1) >> shift], 1); });
   __syncthreads();
   // first place of each bin: what the bins of more work hold
   __shared__ int count[2];
@@ -139,11 +144,11 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   __syncthreads();
   int4* list0 = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(plan) + kPackedHead);
   each([&](int list, int row0, int n, int index, int work) {
-    const int at = atomicAdd(&sh.bin[list][work >> shift], 1);
+    const int at = atomicAdd(&sh.bin[list][(work + (1 << shift) - 1) >> shift], 1);
     list0[(list ? pairs_at : 0) + at] = make_int4(row0, n, index, 0);
   });
   if (tid == 0)
-    *plan = PackedPlan{kPackedMagic, rows, count[0], count[1], pairs_at, longest, B > 0 ? cu[0] : 0, B > 0 ? cu[B] : 0,
+    *plan = PackedPlan{kPackedMagic, rows, count[0], count[1], sh.n_short, pairs_at, longest, B > 0 ? cu[0] : 0, B > 0 ? cu[B] : 0,
                        sh.causal, sh.full};
 }
 
@@ -416,6 +421,24 @@ fa_status_t fa_fwd_packed(const void* q, const void* k, const void* v, const lon
   a.num_sms = dev.num_sms;
   a.debug_skip = dev.debug_skip;
   cudaError_t e = launch_fwd_ragged(a, stream);
+  ShortLaunch sl{};
+  sl.q = static_cast<const __nv_bfloat16*>(q);
+  sl.k = static_cast<const __nv_bfloat16*>(k);
+  sl.v = static_cast<const __nv_bfloat16*>(v);
+  sl.o = a.o;
+  sl.lse = lse;
+  std::copy(s[0], s[0] + 2, sl.q_st);
+  std::copy(s[1], s[1] + 2, sl.k_st);
+  std::copy(s[2], s[2] + 2, sl.v_st);
+  std::copy(s[3], s[3] + 2, sl.o_st);
+  sl.plan = a.plan;
+  sl.rows = rows;
+  sl.Hq = Hq;
+  sl.Hkv = Hkv;
+  sl.device = dev.device;
+  sl.num_sms = dev.num_sms;
+  sl.scale_log2 = a.scale_log2;
+  if (e == cudaSuccess) e = launch_fwd_short(sl, d, causal, stream);
   if (e == cudaSuccess && fill) {
     PackedFill f{};
     f.x[0] = a.o;

@@ -14,16 +14,19 @@ namespace fa {
 // their pairs of neighbouring tiles. Both are ordered by the work of a query
 // tile, most first: the key tiles it sees, which are index + 1 of a causal plan
 // and all the sequence's else. (A causal key tile sees what is behind it, so
-// the same list read with j = last - index is ordered for them too.)
+// the same list read with j = last - index is ordered for them too.) Sequences of
+// kShortRows rows or fewer stand at the end of both lists.
 struct PackedPlan {
   uint32_t magic;
   int rows;               // rows of the tensors it was made for
   int n_tiles, n_pairs;
+  int n_short;            // sequences at the end of either list
   int pairs_at;           // first entry of the second list
   int max_tiles;          // tiles of the longest sequence
   int row_begin, row_end; // rows that belong to a sequence
   unsigned long long causal_products, full_products;  // (query tile, key tile) pairs per head
 };
+constexpr int kShortRows = 64;  // up to here a sequence is fa_packed_short.cu's (forward)
 constexpr uint32_t kPackedMagic = 0x46415031u;
 constexpr int kPackedHead = 256;  // bytes before the lists
 

@@ -1,0 +1,235 @@
+// Attention of the short sequences of a packed batch (kShortRows rows or fewer),
+// for sm_103a.
+//
+// The tcgen05 kernel's chain of steps per query tile (a load, S, the softmax, the
+// second product, O on its way out) takes about 4 us whatever the tile holds, and
+// tensor memory has room for two such chains on an SM: 256 sequences of 16 rows
+// with 32 heads took it 109 us, their bytes 13. Sequences this short hold too
+// little for that tensor core: here a block of four warps takes one sequence and
+// one K/V head, K and V (at most 32 KB at d = 128) go to shared memory once for all
+// query heads of the group, and each warp takes 16 query rows at a time through
+// warp-level products, S and O in registers. Rows are counted through the heads of
+// the group, so that a sequence of a few rows fills the products with several
+// heads. Four blocks share an SM and hide each other's loads.
+// All keys of a row are in one pass: plain softmax, statistics in fp32, the
+// weights rounded to bf16 for the second product, the sum from the unrounded ones.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "fa_packed.cuh"
+#include "warp_mma.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int HD>
+struct ShortCfg {
+  static constexpr int UNITS = HD / 8;  // 16-byte units of a row
+  static constexpr int TILE = kShortRows * HD * 2;
+  static constexpr int WARP_TILE = 16 * HD * 2;
+  static constexpr int SMEM = 2 * TILE + kWarps * WARP_TILE;
+  static constexpr int PER_SM = HD == 64 ? 5 : (HD == 128 ? 4 : 2);
+};
+
+// A batch's rows of one head: base + row * row stride.
+__device__ __forceinline__ const __nv_bfloat16* head_rows(const __nv_bfloat16* p, const long long (&st)[2], int row,
+                                                          int head) {
+  return p + static_cast<long long>(row) * st[0] + head * st[1];
+}
+
+template <int HD, bool CAUSAL>
+__global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
+    packed_short_fwd_kernel(const __grid_constant__ ShortLaunch p) {
+  using C = ShortCfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sK = smem_u32(smem), sV = sK + C::TILE, sQ = sV + C::TILE + warp * C::WARP_TILE;
+  const int n_short = packed_plan_ok(p.plan, p.rows) ? p.plan->n_short : 0;
+  const int4* list = packed_tiles(p.plan) + (p.plan->n_tiles - n_short);
+  const int group = p.Hq / p.Hkv;
+  for (int item = blockIdx.x; item < n_short * p.Hkv; item += gridDim.x) {
+    const int e = item / p.Hkv, hk = item - e * p.Hkv;
+    const int4 x = __ldg(list + e);
+    const int row0 = x.x, n = x.y, n16 = (n + 15) & ~15, R = group * n;
+    const __nv_bfloat16 *kp = head_rows(p.k, p.k_st, row0, hk), *vp = head_rows(p.v, p.v_st, row0, hk);
+    for (int i = threadIdx.x; i < n16 * C::UNITS; i += 32 * kWarps) {
+      const int r = i / C::UNITS, u = i % C::UNITS;
+      const bool in = r < n;
+      cp_async16_or_zero(sK + tile_at<HD>(r, u), kp + (in ? r : 0) * p.k_st[0] + 8 * u, in);
+      cp_async16_or_zero(sV + tile_at<HD>(r, u), vp + (in ? r : 0) * p.v_st[0] + 8 * u, in);
+    }
+    cp_async_group();
+    bool waited = false;
+    for (int blk = warp; 16 * blk < R || !waited; blk += kWarps) {
+      const int first = 16 * blk;
+      if (first < R) {
+        // 16 query rows: a row by UNITS lanes (d = 256: by all, twice)
+        constexpr int LPR = C::UNITS < 32 ? C::UNITS : 32, RPI = 32 / LPR;
+#pragma unroll
+        for (int i = 0; i < 16; i += RPI) {
+          const int r = i + lane / LPR, at = first + r, head = at / n, pos = at - head * n;
+          const bool in = at < R;
+          const __nv_bfloat16* src = head_rows(p.q, p.q_st, row0 + (in ? pos : 0), hk * group + (in ? head : 0));
+#pragma unroll
+          for (int u = lane % LPR; u < C::UNITS; u += LPR) cp_async16_or_zero(sQ + tile_at<HD>(r, u), src + 8 * u, in);
+        }
+      }
+      cp_async_group();
+      cp_async_wait_groups<0>();
+      if (!waited) __syncthreads();  // K and V are in
+      waited = true;
+      __syncwarp();
+      if (first >= R) break;
+
+      // the thread's two rows: place in the sequence, keys they see
+      int pos[2], head[2], sees[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = first + (lane >> 2) + 8 * i;
+        head[i] = at / n;
+        pos[i] = at - head[i] * n;
+        sees[i] = at < R ? (CAUSAL ? pos[i] + 1 : n) : 0;
+      }
+      // keys that some row of the block sees
+      const int last = min(first + 15, R - 1), wraps = last / n != first / n;
+      const int keys = CAUSAL && !wraps ? last % n + 1 : n;
+
+      float s[kShortRows / 16][2][4];
+#pragma unroll
+      for (int c = 0; c < kShortRows / 16; ++c)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[c][b][i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint4 a = load_matrices(sQ + tile_at<HD>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+        for (int c = 0; c < kShortRows / 16; ++c)
+          if (16 * c < keys) {
+            const uint4 b = load_matrices(
+                sK + tile_at<HD>(16 * c + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+            mma_bf16(s[c][0], a, b.x, b.y);
+            mma_bf16(s[c][1], a, b.z, b.w);
+          }
+      }
+      __syncwarp();  // Q is read: its place takes O
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kShortRows / 16; ++c)
+        if (16 * c < keys) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = 16 * c + 8 * b + 2 * (lane & 3) + (i & 1);
+              if (col >= sees[i >> 1]) s[c][b][i] = -INFINITY;
+              m[i >> 1] = fmaxf(m[i >> 1], s[c][b][i]);
+            }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+        m[i] = m[i] == -INFINITY ? 0.f : m[i] * p.scale_log2;
+      }
+      float o[HD / 8][4];
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kShortRows / 16; ++c)
+        if (16 * c < keys) {
+          float e[2][4];
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[b][i] = ex2_approx(fmaf(s[c][b][i], p.scale_log2, -m[i >> 1]));
+              l[i >> 1] += e[b][i];
+            }
+          const uint4 a = make_uint4(pack_bf16x2(e[0][0], e[0][1]), pack_bf16x2(e[0][2], e[0][3]),
+                                     pack_bf16x2(e[1][0], e[1][1]), pack_bf16x2(e[1][2], e[1][3]));
+#pragma unroll
+          for (int j = 0; j < HD / 16; ++j) {
+            const uint4 b = load_matrices_t(
+                sV + tile_at<HD>(16 * c + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4)));
+            mma_bf16(o[2 * j], a, b.x, b.y);
+            mma_bf16(o[2 * j + 1], a, b.z, b.w);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const int r = (lane >> 2) + 8 * i;
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j)
+          st_shared_b32(sQ + tile_at<HD>(r, j) + 4 * (lane & 3), pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv));
+        if (sees[i] > 0 && (lane & 3) == 0)
+          p.lse[static_cast<size_t>(hk * group + head[i]) * p.rows + row0 + pos[i]] =
+              l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+      }
+      __syncwarp();
+      {
+        constexpr int LPR = C::UNITS < 32 ? C::UNITS : 32, RPI = 32 / LPR;
+#pragma unroll
+        for (int i = 0; i < 16; i += RPI) {
+          const int r = i + lane / LPR, at = first + r, hh = at / n, pp = at - hh * n;
+          if (at < R) {
+            __nv_bfloat16* dst = p.o + static_cast<long long>(row0 + pp) * p.o_st[0] + (hk * group + hh) * p.o_st[1];
+#pragma unroll
+            for (int u = lane % LPR; u < C::UNITS; u += LPR)
+              *reinterpret_cast<uint4*>(dst + 8 * u) = ld_shared_v4(sQ + tile_at<HD>(r, u));
+          }
+        }
+      }
+      __syncwarp();  // O is read before the next rows' Q comes in
+    }
+    __syncthreads();  // every warp is done with K and V
+  }
+  // Launched to overlap the kernel for the other sequences: work queued after this
+  // one may read what that one writes.
+  if (threadIdx.x == 0) griddep_wait();
+}
+
+template <int HD, bool CAUSAL>
+cudaError_t launch_short_fwd(const ShortLaunch& a, cudaStream_t stream) {
+  using C = ShortCfg<HD>;
+  auto kern = packed_short_fwd_kernel<HD, CAUSAL>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, a.device, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      std::min<long long>(static_cast<long long>(a.rows) * a.Hkv, static_cast<long long>(a.num_sms) * C::PER_SM)));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream) {
+  switch (d) {
+    case 64: return causal ? launch_short_fwd<64, true>(a, stream) : launch_short_fwd<64, false>(a, stream);
+    case 128: return causal ? launch_short_fwd<128, true>(a, stream) : launch_short_fwd<128, false>(a, stream);
+    case 256: return causal ? launch_short_fwd<256, true>(a, stream) : launch_short_fwd<256, false>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fa
