@@ -56,27 +56,37 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
     const int e = item / p.Hkv, hk = item - e * p.Hkv;
     const int4 x = __ldg(list + e);
     const int row0 = x.x, n = x.y, n16 = (n + 15) & ~15, R = group * n;
-    const __nv_bfloat16 *kp = head_rows(p.k, p.k_st, row0, hk), *vp = head_rows(p.v, p.v_st, row0, hk);
-    for (int i = threadIdx.x; i < n16 * C::UNITS; i += 32 * kWarps) {
-      const int r = i / C::UNITS, u = i % C::UNITS;
-      const bool in = r < n;
-      cp_async16_or_zero(sK + tile_at<HD>(r, u), kp + (in ? r : 0) * p.k_st[0] + 8 * u, in);
-      cp_async16_or_zero(sV + tile_at<HD>(r, u), vp + (in ? r : 0) * p.v_st[0] + 8 * u, in);
+    {
+      // a row by UNITS threads, STEP rows at a time
+      constexpr int STEP = 32 * kWarps / C::UNITS;
+      const int r0 = threadIdx.x / C::UNITS, u = threadIdx.x % C::UNITS;
+      const __nv_bfloat16 *kp = head_rows(p.k, p.k_st, row0, hk) + 8 * u, *vp = head_rows(p.v, p.v_st, row0, hk) + 8 * u;
+      const __nv_bfloat16 *ks = kp + r0 * p.k_st[0], *vs = vp + r0 * p.v_st[0];
+      for (int r = r0; r < n16; r += STEP, ks += STEP * p.k_st[0], vs += STEP * p.v_st[0]) {
+        const bool in = r < n;
+        cp_async16_or_zero(sK + tile_at<HD>(r, u), in ? ks : kp, in);
+        cp_async16_or_zero(sV + tile_at<HD>(r, u), in ? vs : vp, in);
+      }
     }
     cp_async_group();
+    const __nv_bfloat16* q = head_rows(p.q, p.q_st, row0, hk * group);
+    __nv_bfloat16* o_rows = p.o + static_cast<long long>(row0) * p.o_st[0] + hk * group * p.o_st[1];
     bool waited = false;
     for (int blk = warp; 16 * blk < R || !waited; blk += kWarps) {
       const int first = 16 * blk;
+      // Lane i knows row i of the block: 256 times its head in the group, plus its
+      // place in the sequence; negative behind the last row.
+      const int mine = first + (lane & 15);
+      const int place = mine < R ? mine / n * 256 + mine % n : -1;
+      constexpr int LPR = C::UNITS < 32 ? C::UNITS : 32, RPI = 32 / LPR;  // a row by LPR lanes
       if (first < R) {
-        // 16 query rows: a row by UNITS lanes (d = 256: by all, twice)
-        constexpr int LPR = C::UNITS < 32 ? C::UNITS : 32, RPI = 32 / LPR;
 #pragma unroll
         for (int i = 0; i < 16; i += RPI) {
-          const int r = i + lane / LPR, at = first + r, head = at / n, pos = at - head * n;
-          const bool in = at < R;
-          const __nv_bfloat16* src = head_rows(p.q, p.q_st, row0 + (in ? pos : 0), hk * group + (in ? head : 0));
+          const int r = i + lane / LPR, at = __shfl_sync(0xffffffffu, place, r);
+          const __nv_bfloat16* src = q + (at & 255) * p.q_st[0] + (at >> 8) * p.q_st[1];
 #pragma unroll
-          for (int u = lane % LPR; u < C::UNITS; u += LPR) cp_async16_or_zero(sQ + tile_at<HD>(r, u), src + 8 * u, in);
+          for (int u = lane % LPR; u < C::UNITS; u += LPR)
+            cp_async16_or_zero(sQ + tile_at<HD>(r, u), (at < 0 ? q : src) + 8 * u, at >= 0);
         }
       }
       cp_async_group();
@@ -87,17 +97,16 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
       if (first >= R) break;
 
       // the thread's two rows: place in the sequence, keys they see
-      int pos[2], head[2], sees[2];
+      int at[2], sees[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int at = first + (lane >> 2) + 8 * i;
-        head[i] = at / n;
-        pos[i] = at - head[i] * n;
-        sees[i] = at < R ? (CAUSAL ? pos[i] + 1 : n) : 0;
+        at[i] = __shfl_sync(0xffffffffu, place, (lane >> 2) + 8 * i);
+        sees[i] = at[i] < 0 ? 0 : (CAUSAL ? (at[i] & 255) + 1 : n);
       }
       // keys that some row of the block sees
-      const int last = min(first + 15, R - 1), wraps = last / n != first / n;
-      const int keys = CAUSAL && !wraps ? last % n + 1 : n;
+      const int last = __shfl_sync(0xffffffffu, place, min(15, R - 1 - first));
+      const bool wraps = last >> 8 != __shfl_sync(0xffffffffu, place, 0) >> 8;
+      const int keys = CAUSAL && !wraps ? (last & 255) + 1 : n;
 
       float s[kShortRows / 16][2][4];
 #pragma unroll
@@ -174,21 +183,18 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
         for (int j = 0; j < HD / 8; ++j)
           st_shared_b32(sQ + tile_at<HD>(r, j) + 4 * (lane & 3), pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv));
         if (sees[i] > 0 && (lane & 3) == 0)
-          p.lse[static_cast<size_t>(hk * group + head[i]) * p.rows + row0 + pos[i]] =
+          p.lse[static_cast<size_t>(hk * group + (at[i] >> 8)) * p.rows + row0 + (at[i] & 255)] =
               l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
       }
       __syncwarp();
-      {
-        constexpr int LPR = C::UNITS < 32 ? C::UNITS : 32, RPI = 32 / LPR;
 #pragma unroll
-        for (int i = 0; i < 16; i += RPI) {
-          const int r = i + lane / LPR, at = first + r, hh = at / n, pp = at - hh * n;
-          if (at < R) {
-            __nv_bfloat16* dst = p.o + static_cast<long long>(row0 + pp) * p.o_st[0] + (hk * group + hh) * p.o_st[1];
+      for (int i = 0; i < 16; i += RPI) {
+        const int r = i + lane / LPR, to = __shfl_sync(0xffffffffu, place, r);
+        if (to >= 0) {
+          __nv_bfloat16* dst = o_rows + (to & 255) * p.o_st[0] + (to >> 8) * p.o_st[1];
 #pragma unroll
-            for (int u = lane % LPR; u < C::UNITS; u += LPR)
-              *reinterpret_cast<uint4*>(dst + 8 * u) = ld_shared_v4(sQ + tile_at<HD>(r, u));
-          }
+          for (int u = lane % LPR; u < C::UNITS; u += LPR)
+            *reinterpret_cast<uint4*>(dst + 8 * u) = ld_shared_v4(sQ + tile_at<HD>(r, u));
         }
       }
       __syncwarp();  // O is read before the next rows' Q comes in
