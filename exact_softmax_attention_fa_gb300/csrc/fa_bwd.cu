@@ -190,7 +190,7 @@ struct BwdWork<CAUSAL, true> {
 template <bool RAG>
 __device__ __forceinline__ int bwd_total_items(const BwdLaunch& p) {
   if constexpr (RAG)
-    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BHkv * static_cast<int>(__ldg(p.sched + 4)) : 0;
+    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BHkv * static_cast<int>(__ldg(p.sched + 4)) : 0;
   else
     return p.BHkv * p.chunks * ((p.N + 127) / 128);
 }
@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_kernel(const 
   // Without dQ this pass writes nothing the dQ kernel reads, so a dQ kernel
   // queued behind it may take SMs as soon as this grid's CTAs leave them.
   if constexpr (!DQ) griddep_launch_dependents();
+  if (RAG && bwd_total_items<RAG>(p) == 0) return;
   const int wg = warp >> 2;
 
   if (threadIdx.x == 0) {
@@ -916,7 +917,9 @@ template <int HD, bool CAUSAL, bool DQ, bool RAG = false>
 cudaError_t launch_main_t(const BwdLaunch& a, cudaStream_t stream) {
   using C = BwdCfg<HD>;
   auto kern = fa_bwd_kernel<HD, CAUSAL, DQ, RAG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = RAG ? allow_smem(kern, C::SMEM_BYTES, a.device, done)
+                      : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // Packed sequences: the plan, on the device, knows how many items there are.
   const int T = RAG ? a.N : (a.N + 127) / 128;

@@ -174,7 +174,7 @@ struct Work256<CAUSAL, true> {
 template <bool RAG>
 __device__ __forceinline__ int total_items256(const BwdLaunch& p) {
   if constexpr (RAG)
-    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BHkv * 2 : 0;
+    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BHkv * 2 : 0;
   else
     return p.BHkv * ((p.N + 127) / 128) * 2;
 }
@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
   // Without dQ this pass writes nothing the dQ kernel reads, so a dQ kernel
   // queued behind it may take SMs as soon as this grid's CTAs leave them.
   if constexpr (!DQ) griddep_launch_dependents();
+  if (RAG && total_items256<RAG>(p) == 0) return;
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.kv_full, 1);
@@ -735,7 +736,9 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
 template <bool CAUSAL, bool DQ, bool RAG = false>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   auto kern = fa_bwd256_kernel<CAUSAL, DQ, RAG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg256::SMEM_BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = RAG ? allow_smem(kern, Cfg256::SMEM_BYTES, a.device, done)
+                      : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg256::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // Packed sequences: the plan, on the device, knows how many items there are.
   const long long items = static_cast<long long>(a.BHkv) * (RAG ? a.N : (a.N + 127) / 128) * 2;

@@ -128,7 +128,7 @@ struct DqWork<CAUSAL, true> {
 template <bool RAG>
 __device__ __forceinline__ int dq_total_items(const BwdLaunch& p) {
   if constexpr (RAG)
-    return packed_plan_ok(p.plan, p.N) ? p.plan->n_tiles * p.BH : 0;
+    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BH : 0;
   else
     return p.BH * ((p.N + 127) / 128);
 }
@@ -485,6 +485,11 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq_kernel(con
   uint8_t* sK = sdO + C::TILE_BYTES;
   uint8_t* sV = sK + C::KST * C::TILE_BYTES;
   const int warp = threadIdx.x >> 5;
+  if (RAG) griddep_launch_dependents();  // the short sequences' kernel
+  if (RAG && dq_total_items<RAG>(p) == 0) {
+    if (threadIdx.x == 0) griddep_wait();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, 1);
@@ -547,7 +552,9 @@ template <int HD, bool CAUSAL, bool RAG = false>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   using C = DqCfg<HD>;
   auto kern = fa_bwd_dq_kernel<HD, CAUSAL, RAG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = RAG ? allow_smem(kern, C::SMEM_BYTES, a.device, done)
+                      : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // Packed sequences: the plan, on the device, knows how many items there are.
   const long long items = static_cast<long long>(a.BH) * (RAG ? a.N : (a.N + 127) / 128);

@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(fwd_threads<RAG>(), 1) fa_fwd_kernel(const __g
   // sequences: so may the kernel for the short ones.
   if (RAG || p.splits > 1) griddep_launch_dependents();
   if (RAG && blockIdx.x == 0 && threadIdx.x == 0 && !packed_plan_ok(p.plan, p.Nq)) record_bad_index(p.status, WHERE_PACKED);
-  if (RAG && total_items<PACK, RAG>(p, C::NT) == 0) return;
+  if (RAG && static_cast<int>(blockIdx.x) >= total_items<PACK, RAG>(p, C::NT)) return;  // nothing in any round
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) mbar_init(&sh.q_full[t], 1);
@@ -952,7 +952,8 @@ template <int HD, bool CAUSAL, bool PACK, bool RAG = false>
 cudaError_t launch_fwd_t(const FwdLaunch& a, cudaStream_t stream) {
   using C = FwdCfg<HD>;
   auto kern = fa_fwd_kernel<HD, CAUSAL, PACK, RAG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::template smem_bytes<RAG>());
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = RAG ? allow_smem(kern, C::template smem_bytes<RAG>(), a.device, done) : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::template smem_bytes<RAG>());
   if (e != cudaSuccess) return e;
   const int rph = PACK ? a.rph : 128;
   const int Tq = (a.Nq + rph - 1) / rph;

@@ -63,6 +63,7 @@ struct FwdLaunch {
   // strides, Nq = Nk the rows, BH the query heads
   const PackedPlan* plan;
   long long o_strides[2];  // of a row and a head, in elements
+  int device;
   int pair_heads;          // the two query tiles of a CTA are two heads' (an even group) instead of one head's
 };
 
@@ -98,17 +99,19 @@ struct BwdLaunch {
   // kv_part [chunks][BHkv][N][d] with `chunks` in sched[4]
   const PackedPlan* plan;
   long long dq_strides[2], dk_strides[2], dv_strides[2];  // of a row and a head, in elements
+  int device;
 };
 
 // The short sequences of a packed batch (fa_packed_short.cu).
 struct ShortLaunch {
-  const __nv_bfloat16 *q, *k, *v;
-  __nv_bfloat16* o;
+  const __nv_bfloat16 *q, *k, *v, *dO;
+  __nv_bfloat16 *o, *dq, *dk, *dv;  // forward: o is written; backward: dq, dk, dv
   float* lse;
-  long long q_st[2], k_st[2], v_st[2], o_st[2];  // strides of a row and a head, in elements
+  // strides of a row and a head, in elements
+  long long q_st[2], k_st[2], v_st[2], o_st[2], do_st[2], dq_st[2], dk_st[2], dv_st[2];
   const PackedPlan* plan;
   int rows, Hq, Hkv, device, num_sms;
-  float scale_log2;
+  float scale, scale_log2;
 };
 
 // Checks of the sizes, flag and scale common to every entry point; *empty is
@@ -163,6 +166,7 @@ cudaError_t launch_fwd(const FwdLaunch& a, cudaStream_t stream);
 cudaError_t launch_fwd_combine(const FwdLaunch& a, cudaStream_t stream);  // splits > 1: merge the partials
 cudaError_t launch_fwd_packed(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_pack.cu: pack > 1
 cudaError_t launch_fwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream);  // fa_packed_short.cu
+cudaError_t launch_bwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream);
 cudaError_t launch_fwd_ragged(const FwdLaunch& a, cudaStream_t stream);   // fa_fwd_ragged.cu: plan set
 cudaError_t launch_bwd_pre(const BwdLaunch& a, cudaStream_t stream);   // D, base-2 L, zero dQ accumulator
 cudaError_t launch_bwd_main(const BwdLaunch& a, cudaStream_t stream);  // dK, dV; dQ into the accumulator

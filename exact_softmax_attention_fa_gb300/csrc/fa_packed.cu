@@ -190,15 +190,16 @@ __device__ int packed_chunks(const PackedRows& a) {
   return best;
 }
 
-// D = rowsum(dO o O) from the stored bf16, and L * log2(e): d / 8 lanes a row,
-// 4 rows of one head at a time. HBM-bound (reads 4 d + 4 bytes a row and head).
+// D = rowsum(dO o O) from the stored bf16, and L * log2(e), of the tiles' rows (the
+// short sequences' kernel forms its own): d / 8 lanes a row, kPreRows rows of one
+// head at a time. HBM-bound (reads 4 d + 4 bytes a row and head).
 constexpr int kPreRows = 4;
 
 template <int HD>
 __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__ PackedRows a) {
-  constexpr int LPR = HD / 8, RPB = 256 / LPR * kPreRows;
+  constexpr int LPR = HD / 8, STEP = 256 / LPR, PARTS = 128 / (STEP * kPreRows);
   const bool ok = packed_plan_ok(a.plan, a.rows);
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (blockIdx.x == 0) {
     if (threadIdx.x < 4) a.sched[threadIdx.x] = 0u;
     if (threadIdx.x == 0) {
       a.sched[4] = ok ? packed_chunks(a) : 1;
@@ -206,67 +207,75 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__
     }
   }
   if (!ok) return;
-  const int h = blockIdx.y, sub = threadIdx.x % LPR;
-  const int first = blockIdx.x * RPB + threadIdx.x / LPR, step = 256 / LPR;
-  const int begin = a.plan->row_begin, end = a.plan->row_end;
-  uint4 x[kPreRows], y[kPreRows];
+  const int sub = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const long long items = static_cast<long long>(a.plan->n_tiles - a.plan->n_short) * a.Hq * PARTS;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t part = static_cast<uint32_t>(item % PARTS), t = static_cast<uint32_t>(item / PARTS);
+    const int4 x = __ldg(packed_tiles(a.plan) + t / a.Hq);
+    const int h = t % a.Hq, first = 128 * x.z + part * STEP * kPreRows + r0;
+    const __nv_bfloat16* po = a.o + static_cast<long long>(x.x) * a.o_st[0] + h * a.o_st[1] + 8 * sub;
+    const __nv_bfloat16* pd = a.dO + static_cast<long long>(x.x) * a.do_st[0] + h * a.do_st[1] + 8 * sub;
+    const size_t at = static_cast<size_t>(h) * a.rows + x.x;
+    uint4 y[kPreRows], z[kPreRows];
 #pragma unroll
-  for (int i = 0; i < kPreRows; ++i) {
-    const int n = first + i * step;
-    if (n < begin || n >= end) continue;
-    x[i] = __ldg(reinterpret_cast<const uint4*>(a.o + n * a.o_st[0] + h * a.o_st[1]) + sub);
-    y[i] = __ldg(reinterpret_cast<const uint4*>(a.dO + n * a.do_st[0] + h * a.do_st[1]) + sub);
-  }
-#pragma unroll
-  for (int i = 0; i < kPreRows; ++i) {
-    const int n = first + i * step;
-    const uint32_t* xs = reinterpret_cast<const uint32_t*>(&x[i]);
-    const uint32_t* ys = reinterpret_cast<const uint32_t*>(&y[i]);
-    float acc = 0.f;
-    if (n >= begin && n < end) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 p = unpack_bf16x2(xs[k]), q = unpack_bf16x2(ys[k]);
-        acc = fmaf(p.x, q.x, acc);
-        acc = fmaf(p.y, q.y, acc);
-      }
+    for (int i = 0; i < kPreRows; ++i) {
+      const int n = first + i * STEP;
+      if (n >= x.y) continue;
+      y[i] = __ldg(reinterpret_cast<const uint4*>(po + n * a.o_st[0]));
+      z[i] = __ldg(reinterpret_cast<const uint4*>(pd + n * a.do_st[0]));
     }
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (n >= begin && n < end && sub == 0) {
-      const size_t at = static_cast<size_t>(h) * a.rows + n;
-      a.D[at] = acc;
-      a.lse2[at] = a.lse[at] * kLog2e;
+    for (int i = 0; i < kPreRows; ++i) {
+      const int n = first + i * STEP;
+      const uint32_t* ys = reinterpret_cast<const uint32_t*>(&y[i]);
+      const uint32_t* zs = reinterpret_cast<const uint32_t*>(&z[i]);
+      float acc = 0.f;
+      if (n < x.y) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack_bf16x2(ys[k]), w = unpack_bf16x2(zs[k]);
+          acc = fmaf(v.x, w.x, acc);
+          acc = fmaf(v.y, w.y, acc);
+        }
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (n < x.y && sub == 0) {
+        a.D[at + n] = acc;
+        a.lse2[at + n] = a.lse[at + n] * kLog2e;
+      }
     }
   }
 }
 
-// Where a group was split, dK, dV = bf16 of the sum of the chunks' fp32
-// partials in chunk order (bitwise reproducible). 8 elements a thread and step.
+// Where a group was split, dK, dV = bf16 of the sum of the chunks' fp32 partials
+// in chunk order (bitwise reproducible): a tile's rows of one head at a time, 8
+// elements a thread.
 __global__ void __launch_bounds__(256) packed_kv_sum_kernel(const __grid_constant__ BwdLaunch p) {
   griddep_wait();
   if (!packed_plan_ok(p.plan, p.N)) return;
   const int chunks = static_cast<int>(p.sched[4]);
   if (chunks == 1) return;
-  const int begin = p.plan->row_begin, n = p.plan->row_end - begin, units = p.d / 8;
+  const int units = p.d / 8, heads = 2 * p.BHkv, items = (p.plan->n_tiles - p.plan->n_short) * heads;
   const size_t len = static_cast<size_t>(p.BHkv) * p.N * p.d;
-  const long long all = 2ll * p.BHkv * n * units, step = static_cast<long long>(gridDim.x) * 256;
-  for (long long v = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; v < all; v += step) {
-    const int col = static_cast<int>(v % units) * 8;
-    const long long r = v / units;
-    const int row = begin + static_cast<int>(r % n), hh = static_cast<int>(r / n);
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int4 x = __ldg(packed_tiles(p.plan) + item / heads);
+    const int hh = item % heads, first = x.x + 128 * x.z, rows = min(128, x.y - 128 * x.z);
     const bool is_v = hh >= p.BHkv;
     const int h = is_v ? hh - p.BHkv : hh;
-    const float* src = p.kv_part + (is_v ? chunks * len : 0) + (static_cast<size_t>(h) * p.N + row) * p.d + col;
-    float4 a = ldg_f4(src), b = ldg_f4(src + 4);
-    for (int c = 1; c < chunks; ++c) {
-      const float4 a2 = ldg_f4(src + c * len), b2 = ldg_f4(src + c * len + 4);
-      a.x += a2.x, a.y += a2.y, a.z += a2.z, a.w += a2.w;
-      b.x += b2.x, b.y += b2.y, b.z += b2.z, b.w += b2.w;
-    }
     const long long* st = is_v ? p.dv_strides : p.dk_strides;
-    *reinterpret_cast<uint4*>((is_v ? p.dv : p.dk) + row * st[0] + h * st[1] + col) =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    for (int i = threadIdx.x; i < rows * units; i += 256) {
+      const int row = first + i / units, col = i % units * 8;
+      const float* src = p.kv_part + (is_v ? chunks * len : 0) + (static_cast<size_t>(h) * p.N + row) * p.d + col;
+      float4 a = ldg_f4(src), b = ldg_f4(src + 4);
+      for (int c = 1; c < chunks; ++c) {
+        const float4 a2 = ldg_f4(src + c * len), b2 = ldg_f4(src + c * len + 4);
+        a.x += a2.x, a.y += a2.y, a.z += a2.z, a.w += a2.w;
+        b.x += b2.x, b.y += b2.y, b.z += b2.z, b.w += b2.w;
+      }
+      *reinterpret_cast<uint4*>((is_v ? p.dv : p.dk) + row * st[0] + h * st[1] + col) =
+          make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    }
   }
 }
 
@@ -346,8 +355,9 @@ cudaError_t launch_fill(const PackedFill& f, int num_sms, cudaStream_t stream) {
 
 template <int HD>
 cudaError_t launch_packed_pre(const PackedRows& a, cudaStream_t stream) {
-  constexpr int RPB = 256 / (HD / 8) * kPreRows;
-  packed_pre_kernel<HD><<<dim3((a.rows + RPB - 1) / RPB, a.Hq), 256, 0, stream>>>(a);
+  // four blocks an SM: the rows on their way at once
+  const long long most = static_cast<long long>(a.rows) * a.Hq;
+  packed_pre_kernel<HD><<<static_cast<unsigned>(std::min<long long>(most, 4 * a.num_sms)), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -410,6 +420,7 @@ fa_status_t fa_fwd_packed(const void* q, const void* k, const void* v, const lon
   a.BH = Hq;
   a.group = Hq / Hkv;
   a.pair_heads = a.group % 2 == 0;
+  a.device = dev.device;
   a.pack = 1;
   a.rph = 128;
   a.splits = 1;
@@ -509,6 +520,7 @@ fa_status_t fa_bwd_packed(const void* q, const void* k, const void* v, const voi
   std::copy(gs[2], gs[2] + 2, a.dv_strides);
   a.plan = static_cast<const PackedPlan*>(plan);
   a.deterministic = 1;
+  a.device = dev.device;
   a.status = dev.status;
   a.N = rows;
   a.BH = Hq;
@@ -545,6 +557,27 @@ fa_status_t fa_bwd_packed(const void* q, const void* k, const void* v, const voi
   if (e == cudaSuccess) e = launch_bwd_main(a, stream);  // dK, dV
   a.overlap_prev = 1;
   if (e == cudaSuccess) e = launch_bwd_dq(a, stream);
+  ShortLaunch sl{};
+  sl.q = static_cast<const __nv_bfloat16*>(q);
+  sl.k = static_cast<const __nv_bfloat16*>(k);
+  sl.v = static_cast<const __nv_bfloat16*>(v);
+  sl.o = const_cast<__nv_bfloat16*>(r.o);
+  sl.dO = r.dO;
+  sl.lse = const_cast<float*>(lse);
+  sl.dq = a.dq;
+  sl.dk = a.dk;
+  sl.dv = a.dv;
+  long long* to[8] = {sl.q_st, sl.k_st, sl.v_st, sl.o_st, sl.do_st, sl.dq_st, sl.dk_st, sl.dv_st};
+  for (int i = 0; i < 8; ++i) std::copy(i < 5 ? s[i] : gs[i - 5], (i < 5 ? s[i] : gs[i - 5]) + 2, to[i]);
+  sl.plan = a.plan;
+  sl.rows = rows;
+  sl.Hq = Hq;
+  sl.Hkv = Hkv;
+  sl.device = dev.device;
+  sl.num_sms = dev.num_sms;
+  sl.scale = scale;
+  sl.scale_log2 = a.scale_log2;
+  if (e == cudaSuccess) e = launch_bwd_short(sl, d, causal, stream);
   if (e == cudaSuccess && r.max_chunks > 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4 * dev.num_sms);

@@ -26,7 +26,7 @@ struct PackedPlan {
   int row_begin, row_end; // rows that belong to a sequence
   unsigned long long causal_products, full_products;  // (query tile, key tile) pairs per head
 };
-constexpr int kShortRows = 64;  // up to here a sequence is fa_packed_short.cu's (forward)
+constexpr int kShortRows = 64;  // up to here a sequence is fa_packed_short.cu's
 constexpr uint32_t kPackedMagic = 0x46415031u;
 constexpr int kPackedHead = 256;  // bytes before the lists
 

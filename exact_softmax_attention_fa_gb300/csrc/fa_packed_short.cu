@@ -206,18 +206,228 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
   if (threadIdx.x == 0) griddep_wait();
 }
 
+// ---------------------------------------------------------------------------
+// Backward: a block of eight warps takes one sequence and one K/V head, and the
+// rows of all its query heads, 64 at a time. S and dP are formed once (the tcgen05
+// path forms them twice, for dK, dV and for dQ), P and dS go through shared memory,
+// and dK, dV stay in registers until the group's last rows:
+//   1. warp (r, h): rows 16 r, keys 32 h: S, dP, P = 2^(S scale log2e - L log2e),
+//      dS = P (dP - D) scale, both to shared memory in bf16
+//   2. warp (r, 0): dV of keys 16 r += P^T dO;  warp (r, 1): dK += dS^T Q;
+//      both: dQ of rows 16 r = dS K, half of the columns each
+// D comes from O and dO as they are loaded, so no kernel runs before this one.
+// ---------------------------------------------------------------------------
+constexpr int kBwdWarps = 8;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int HD>
+struct ShortBwdCfg {
+  static constexpr int UNITS = HD / 8;
+  static constexpr int TILE = kShortRows * HD * 2;
+  static constexpr int P_TILE = 64 * 64 * 2;
+  static constexpr int SMEM = 4 * TILE + 2 * P_TILE + 2 * 64 * 4;
+  static constexpr int PER_SM = HD == 256 ? 1 : 2;
+};
+
 template <int HD, bool CAUSAL>
-cudaError_t launch_short_fwd(const ShortLaunch& a, cudaStream_t stream) {
-  using C = ShortCfg<HD>;
-  auto kern = packed_short_fwd_kernel<HD, CAUSAL>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kern, C::SMEM, a.device, done);
-  if (e != cudaSuccess) return e;
+__global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
+    packed_short_bwd_kernel(const __grid_constant__ ShortLaunch p) {
+  using C = ShortBwdCfg<HD>;
+  constexpr int THREADS = 32 * kBwdWarps, STEP = THREADS / C::UNITS;  // a row by UNITS threads, STEP rows at a time
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rq = warp & 3, half = warp >> 2;
+  const uint32_t sK = smem_u32(smem), sV = sK + C::TILE, sQ = sV + C::TILE, sO = sQ + C::TILE, sP = sO + C::TILE,
+                 sS = sP + C::P_TILE;
+  float* sD = reinterpret_cast<float*>(smem + 4 * C::TILE + 2 * C::P_TILE);
+  float* sL = sD + 64;
+  const int r0 = threadIdx.x / C::UNITS, u = threadIdx.x % C::UNITS;
+  const int n_short = packed_plan_ok(p.plan, p.rows) ? p.plan->n_short : 0;
+  const int4* list = packed_tiles(p.plan) + (p.plan->n_tiles - n_short);
+  const int group = p.Hq / p.Hkv;
+  for (int item = blockIdx.x; item < n_short * p.Hkv; item += gridDim.x) {
+    const int e = item / p.Hkv, hk = item - e * p.Hkv;
+    const int4 x = __ldg(list + e);
+    const int row0 = x.x, n = x.y, n16 = (n + 15) & ~15, R = group * n;
+    {
+      const __nv_bfloat16 *kp = head_rows(p.k, p.k_st, row0, hk) + 8 * u, *vp = head_rows(p.v, p.v_st, row0, hk) + 8 * u;
+      for (int r = r0; r < n16; r += STEP) {
+        const bool in = r < n;
+        cp_async16_or_zero(sK + tile_at<HD>(r, u), kp + (in ? r : 0) * p.k_st[0], in);
+        cp_async16_or_zero(sV + tile_at<HD>(r, u), vp + (in ? r : 0) * p.v_st[0], in);
+      }
+    }
+    const __nv_bfloat16* q = head_rows(p.q, p.q_st, row0, hk * group) + 8 * u;
+    const __nv_bfloat16* dO = head_rows(p.dO, p.do_st, row0, hk * group) + 8 * u;
+    const __nv_bfloat16* o = head_rows(p.o, p.o_st, row0, hk * group) + 8 * u;
+    float acc[HD / 8][4];  // dV or dK of 16 keys
+#pragma unroll
+    for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+
+#pragma unroll 1
+    for (int base = 0; base < R; base += 64) {
+      const int rows = min(64, R - base), rows16 = (rows + 15) & ~15;
+      for (int r = r0; r < rows16; r += STEP) {
+        const int at = base + r, head = at / n, pos = at - head * n;
+        const bool in = r < rows;
+        cp_async16_or_zero(sQ + tile_at<HD>(r, u), in ? q + pos * p.q_st[0] + head * p.q_st[1] : q, in);
+        cp_async16_or_zero(sO + tile_at<HD>(r, u), in ? dO + pos * p.do_st[0] + head * p.do_st[1] : dO, in);
+      }
+      cp_async_group();
+      // D and L of the rows, from O as it arrives and this thread's own piece of dO
+#pragma unroll 1
+      for (int r = r0; r < rows16; r += STEP) {
+        const int at = base + r, head = at / n, pos = at - head * n;
+        uint4 a = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) a = __ldg(reinterpret_cast<const uint4*>(o + pos * p.o_st[0] + head * p.o_st[1]));
+        if (r == r0) cp_async_wait_groups<0>();
+        const uint4 b = ld_shared_v4(sO + tile_at<HD>(r, u));
+        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = unpack_bf16x2(as[i]), z = unpack_bf16x2(bs[i]);
+          d = fmaf(y.x, z.x, d);
+          d = fmaf(y.y, z.y, d);
+        }
+#pragma unroll
+        for (int s = (C::UNITS < 32 ? C::UNITS : 32) / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+        if (u == 0) {
+          sD[r] = r < rows ? d : 0.f;
+          sL[r] = r < rows ? p.lse[static_cast<size_t>(hk * group + head) * p.rows + row0 + pos] * kLog2e : 0.f;
+        }
+      }
+      __syncthreads();
+
+      if (16 * rq < rows && 32 * half < n16) {
+        float s[2][2][4], dp[2][2][4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[c][b][i] = dp[c][b][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t a_at = tile_at<HD>(16 * rq + (lane & 15), 2 * k + (lane >> 4));
+          const uint4 a = load_matrices(sQ + a_at), g = load_matrices(sO + a_at);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (32 * half + 16 * c < n16) {
+              const uint32_t b_at =
+                  tile_at<HD>(32 * half + 16 * c + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1));
+              const uint4 b = load_matrices(sK + b_at), v = load_matrices(sV + b_at);
+              mma_bf16(s[c][0], a, b.x, b.y);
+              mma_bf16(s[c][1], a, b.z, b.w);
+              mma_bf16(dp[c][0], g, v.x, v.y);
+              mma_bf16(dp[c][1], g, v.z, v.w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 16 * rq + (lane >> 2) + 8 * i, at = base + r;
+          const int sees = r >= rows ? 0 : (CAUSAL ? at % n + 1 : n);
+          const float L = sL[r], D = sD[r];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (32 * half + 16 * c < n16) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                float w[2], ds[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int col = 32 * half + 16 * c + 8 * b + 2 * (lane & 3) + z;
+                  const bool in = col < sees;
+                  w[z] = in ? ex2_approx(fmaf(s[c][b][2 * i + z], p.scale_log2, -L)) : 0.f;
+                  ds[z] = in ? w[z] * (dp[c][b][2 * i + z] - D) * p.scale : 0.f;
+                }
+                const uint32_t to = tile_at<64>(r, 4 * half + 2 * c + b) + 4 * (lane & 3);
+                st_shared_b32(sP + to, pack_bf16x2(w[0], w[1]));
+                st_shared_b32(sS + to, pack_bf16x2(ds[0], ds[1]));
+              }
+            }
+        }
+      }
+      __syncthreads();
+
+      if (16 * rq < n16) {
+        const uint32_t from = half ? sS : sP, with = half ? sQ : sO;
+#pragma unroll 1
+        for (int k = 0; k < rows16; k += 16) {
+          const uint4 a = load_matrices_t(from + tile_at<64>(k + (lane & 7) + ((lane >> 4) << 3), 2 * rq + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int j = 0; j < HD / 16; ++j) {
+            const uint4 b = load_matrices_t(with + tile_at<HD>(k + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4)));
+            mma_bf16(acc[2 * j], a, b.x, b.y);
+            mma_bf16(acc[2 * j + 1], a, b.z, b.w);
+          }
+        }
+      }
+      float dq[HD / 16][4];
+#pragma unroll
+      for (int j = 0; j < HD / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dq[j][i] = 0.f;
+      if (16 * rq < rows) {
+#pragma unroll 1
+        for (int k = 0; k < n16; k += 16) {
+          const uint4 a = load_matrices(sS + tile_at<64>(16 * rq + (lane & 15), k / 8 + (lane >> 4)));
+#pragma unroll
+          for (int j = 0; j < HD / 32; ++j) {
+            const uint4 b = load_matrices_t(
+                sK + tile_at<HD>(k + (lane & 7) + (((lane >> 3) & 1) << 3), half * (HD / 16) + 2 * j + (lane >> 4)));
+            mma_bf16(dq[2 * j], a, b.x, b.y);
+            mma_bf16(dq[2 * j + 1], a, b.z, b.w);
+          }
+        }
+      }
+      __syncthreads();  // Q is read: its place takes dQ
+      if (16 * rq < rows) {
+#pragma unroll
+        for (int j = 0; j < HD / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            st_shared_b32(sQ + tile_at<HD>(16 * rq + (lane >> 2) + 8 * i, half * (HD / 16) + j) + 4 * (lane & 3),
+                          pack_bf16x2(dq[j][2 * i], dq[j][2 * i + 1]));
+      }
+      __syncthreads();
+      for (int r = r0; r < rows; r += STEP) {
+        const int at = base + r, head = at / n, pos = at - head * n;
+        *reinterpret_cast<uint4*>(p.dq + static_cast<long long>(row0 + pos) * p.dq_st[0] +
+                                  (hk * group + head) * p.dq_st[1] + 8 * u) = ld_shared_v4(sQ + tile_at<HD>(r, u));
+      }
+      __syncthreads();  // before the next rows come in
+    }
+    if (16 * rq < n16) {
+      const uint32_t to = half ? sQ : sO;
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          st_shared_b32(to + tile_at<HD>(16 * rq + (lane >> 2) + 8 * i, j) + 4 * (lane & 3),
+                        pack_bf16x2(acc[j][2 * i], acc[j][2 * i + 1]));
+    }
+    __syncthreads();
+    for (int r = r0; r < n; r += STEP) {
+      *reinterpret_cast<uint4*>(p.dk + static_cast<long long>(row0 + r) * p.dk_st[0] + hk * p.dk_st[1] + 8 * u) =
+          ld_shared_v4(sQ + tile_at<HD>(r, u));
+      *reinterpret_cast<uint4*>(p.dv + static_cast<long long>(row0 + r) * p.dv_st[0] + hk * p.dv_st[1] + 8 * u) =
+          ld_shared_v4(sO + tile_at<HD>(r, u));
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) griddep_wait();  // as the forward
+}
+
+// Queue a kernel so that it takes SMs as the kernel before it leaves them.
+template <class Kernel>
+cudaError_t launch_beside(Kernel kern, const ShortLaunch& a, int threads, int smem, int per_sm, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(
-      std::min<long long>(static_cast<long long>(a.rows) * a.Hkv, static_cast<long long>(a.num_sms) * C::PER_SM)));
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = C::SMEM;
+      std::min<long long>(static_cast<long long>(a.rows) * a.Hkv, static_cast<long long>(a.num_sms) * per_sm)));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -227,6 +437,26 @@ cudaError_t launch_short_fwd(const ShortLaunch& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <int HD, bool CAUSAL>
+cudaError_t launch_short_fwd(const ShortLaunch& a, cudaStream_t stream) {
+  using C = ShortCfg<HD>;
+  auto kern = packed_short_fwd_kernel<HD, CAUSAL>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, a.device, done);
+  if (e != cudaSuccess) return e;
+  return launch_beside(kern, a, 32 * kWarps, C::SMEM, C::PER_SM, stream);
+}
+
+template <int HD, bool CAUSAL>
+cudaError_t launch_short_bwd(const ShortLaunch& a, cudaStream_t stream) {
+  using C = ShortBwdCfg<HD>;
+  auto kern = packed_short_bwd_kernel<HD, CAUSAL>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, a.device, done);
+  if (e != cudaSuccess) return e;
+  return launch_beside(kern, a, 32 * kBwdWarps, C::SMEM, C::PER_SM, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_fwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream) {
@@ -234,6 +464,15 @@ cudaError_t launch_fwd_short(const ShortLaunch& a, int d, int causal, cudaStream
     case 64: return causal ? launch_short_fwd<64, true>(a, stream) : launch_short_fwd<64, false>(a, stream);
     case 128: return causal ? launch_short_fwd<128, true>(a, stream) : launch_short_fwd<128, false>(a, stream);
     case 256: return causal ? launch_short_fwd<256, true>(a, stream) : launch_short_fwd<256, false>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_bwd_short(const ShortLaunch& a, int d, int causal, cudaStream_t stream) {
+  switch (d) {
+    case 64: return causal ? launch_short_bwd<64, true>(a, stream) : launch_short_bwd<64, false>(a, stream);
+    case 128: return causal ? launch_short_bwd<128, true>(a, stream) : launch_short_bwd<128, false>(a, stream);
+    case 256: return causal ? launch_short_bwd<256, true>(a, stream) : launch_short_bwd<256, false>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
