@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import struct
 import threading
 
 from ._lib import load, check, FAError, header_functions, STATUS_NAMES  # noqa: F401
@@ -423,7 +424,8 @@ def _devices(*tensors):
     return {t.get_device() for t in tensors if t is not None}
 
 
-_Strides = ctypes.c_longlong * 9
+# Host arrays of strides as the C ABI takes them (bytes: a third of the time of a ctypes array).
+_strides6, _strides8, _strides9, _strides10 = (struct.Struct(f"{n}q").pack for n in (6, 8, 9, 10))
 _NO_STRIDES = (0, 0, 0, 1)
 
 
@@ -534,7 +536,7 @@ def _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v,
     if axes is not None:
         name, by_axes = "fa_norm_rope_axes_fwd", _axes(axes, positions, rot)
     check(name, getattr(load(), name)(
-        q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(wq), _ptr(wk), w_bf16,
+        q_in.data_ptr(), k_in.data_ptr(), _ptr(v_in), _strides9(*sq[:3], *sk[:3], *sv[:3]), _ptr(wq), _ptr(wk), w_bf16,
         _ptr(cos), _ptr(sin), rows, _ptr(positions), *by_axes, q.data_ptr(), k.data_ptr(), _ptr(v), B, Hq, Hkv, N, d,
         rot, 1 if interleaved else 0, eps, _stream_handle(stream)))
 
@@ -597,9 +599,9 @@ def _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq
     if axes is not None:
         name, by_axes = "fa_norm_rope_axes_bwd", _axes(axes, positions, rot)
     check(name, getattr(load(), name)(
-        dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), _Strides(*xq[:3], *xk[:3]), _ptr(wq), _ptr(wk),
+        dq.data_ptr(), dk.data_ptr(), _ptr(dv), _ptr(q_in), _ptr(k_in), _strides9(*xq[:3], *xk[:3], 0, 0, 0), _ptr(wq), _ptr(wk),
         w_bf16, _ptr(cos), _ptr(sin), rows, _ptr(positions), *by_axes, dq_in.data_ptr(), dk_in.data_ptr(), _ptr(dv_in),
-        _Strides(*sq[:3], *sk[:3], *sv[:3]), _ptr(dwq), _ptr(dwk), B, Hq, Hkv, N, d, rot, 1 if interleaved else 0, eps,
+        _strides9(*sq[:3], *sk[:3], *sv[:3]), _ptr(dwq), _ptr(dwk), B, Hq, Hkv, N, d, rot, 1 if interleaved else 0, eps,
         *_ws(workspace), _stream_handle(stream)))
 
 
@@ -623,41 +625,38 @@ def fa_packed_plan(cu_seqlens, rows: int, causal: bool, plan, stream=None) -> No
                                                   1 if causal else 0, *_ws(plan), _stream_handle(stream)))
 
 
-_RowStrides4, _RowStrides5, _RowStrides3 = ctypes.c_longlong * 8, ctypes.c_longlong * 10, ctypes.c_longlong * 6
-
-
-def _packed_dims(q, k, plan, rows_of_k, lse, *rest):
-    """(rows, Hq, Hkv, d) of a call over packed sequences, after the checks of its tensors: rest and
-    rows_of_k are (name, tensor) of q's and of k's shape."""
+def _packed_refuse(q, k, plan, lse, of_q, of_k):
     import torch
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("expected [rows, H, d] tensors")
-    rows, Hq, d = qs = q.shape
-    Hkv, ks, bf = k.shape[1], (rows, k.shape[1], d), torch.bfloat16
-    if Hkv < 1 or Hq % Hkv != 0:
-        raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({Hkv})")
-    of_q, of_k = [t for _, t in rest], [t for _, t in rows_of_k]
-    if not (q.dtype == bf and all([t.dtype == bf and t.shape == qs and t.stride(2) == 1 for t in of_q])
-            and all([t.dtype == bf and t.shape == ks and t.stride(2) == 1 for t in of_k]) and q.stride(2) == 1
-            and lse.dtype == torch.float32 and lse.shape == (Hq, rows) and lse.is_contiguous()
-            and plan.dtype == torch.uint8 and plan.is_contiguous()
-            and _devices(q, plan, lse, *of_q, *of_k) == {torch.cuda.current_device()}):
-        _refuse([("q", q, (bf,), qs, False)] + [(n, t, (bf,), qs, False) for n, t in rest]
-                + [(n, t, (bf,), ks, False) for n, t in rows_of_k]
-                + [("lse", lse, (torch.float32,), (Hq, rows), True), ("plan", plan, (torch.uint8,), plan.shape, True)])
-    return rows, Hq, Hkv, d
+    (rows, Hq, d), bf = q.shape, (torch.bfloat16,)
+    qs, ks = (rows, Hq, d), (rows, k.shape[1], d)
+    if ks[1] < 1 or Hq % ks[1] != 0:
+        raise ValueError(f"the query heads ({Hq}) must be a multiple of the K/V heads ({ks[1]})")
+    _refuse([("q", q, bf, qs, False), ("k", k, bf, ks, False)] + [(n, t, bf, qs, False) for n, t in of_q]
+            + [(n, t, bf, ks, False) for n, t in of_k]
+            + [("lse", lse, (torch.float32,), (Hq, rows), True), ("plan", plan, (torch.uint8,), plan.shape, True)])
 
 
 def fa_fwd_packed(q, k, v, o, lse, plan, causal: bool, scale: float, fill: bool = False, stream=None) -> None:
     """fa_fwd_packed of the C ABI: q, o [rows, Hq, d], k, v [rows, Hkv, d] with any strides and contiguous
     last dimension (views of a packed projection), lse float32 [Hq, rows]; plan a PackedPlan (or the
     tensor that fa_packed_plan filled) of the same rows. fill: zeros in the rows of no sequence."""
-    plan = getattr(plan, "buffer", plan)
-    rows, Hq, Hkv, d = _packed_dims(q, k, plan, (("k", k), ("v", v)), lse, ("o", o))
+    import torch
+    plan, bf = getattr(plan, "buffer", plan), torch.bfloat16
+    qs, ks = q.shape, k.shape
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), o.stride()
+    if not (len(qs) == len(ks) == 3 and q.dtype == k.dtype == v.dtype == o.dtype == bf and o.shape == qs and v.shape == ks
+            and ks[0] == qs[0] and ks[2] == qs[2] and ks[1] > 0 and qs[1] % ks[1] == 0
+            and sq[2] == sk[2] == sv[2] == so[2] == 1
+            and lse.dtype == torch.float32 and lse.shape == (qs[1], qs[0]) and lse.is_contiguous()
+            and plan.dtype == torch.uint8 and plan.is_contiguous()
+            and _devices(q, k, v, o, lse, plan) == {torch.cuda.current_device()}):
+        _packed_refuse(q, k, plan, lse, (("o", o),), (("v", v),))
     check("fa_fwd_packed", load().fa_fwd_packed(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        _RowStrides4(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), o.data_ptr(), lse.data_ptr(),
-        plan.data_ptr(), rows, Hq, Hkv, d, 1 if causal else 0, scale, 1 if fill else 0, _stream_handle(stream)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides8(*sq[:2], *sk[:2], *sv[:2], *so[:2]), o.data_ptr(),
+        lse.data_ptr(), plan.data_ptr(), qs[0], qs[1], ks[1], qs[2], 1 if causal else 0, scale, 1 if fill else 0,
+        _stream_handle(stream)))
 
 
 def fa_bwd_packed_workspace_size(rows: int, Hq: int, Hkv: int, d: int) -> int:
@@ -669,17 +668,26 @@ def fa_bwd_packed(q, k, v, o, lse, do, dq, dk, dv, plan, causal: bool, scale: fl
     """fa_bwd_packed of the C ABI: q, o, do, dq [rows, Hq, d] and k, v, dk, dv [rows, Hkv, d] with any strides
     and contiguous last dimension (dq, dk, dv may be the views of one packed gradient), lse and plan as
     in the forward, workspace a CUDA uint8 tensor of at least fa_bwd_packed_workspace_size() bytes."""
-    plan = getattr(plan, "buffer", plan)
-    rows, Hq, Hkv, d = _packed_dims(q, k, plan, (("k", k), ("v", v), ("dk", dk), ("dv", dv)), lse, ("o", o), ("do", do),
-                                    ("dq", dq))
-    if not (_bytes(workspace) and _devices(q, workspace) == {q.get_device()}):
-        _refuse((("workspace", workspace, (workspace.dtype,) if _bytes(workspace) else (), workspace.shape, True),))
+    import torch
+    plan, bf = getattr(plan, "buffer", plan), torch.bfloat16
+    qs, ks = q.shape, k.shape
+    sq, sk, sv, so, sg = q.stride(), k.stride(), v.stride(), o.stride(), do.stride()
+    tq, tk, tv = dq.stride(), dk.stride(), dv.stride()
+    if not (len(qs) == len(ks) == 3 and q.dtype == k.dtype == v.dtype == o.dtype == do.dtype == dq.dtype == dk.dtype
+            == dv.dtype == bf and o.shape == do.shape == dq.shape == qs and v.shape == dk.shape == dv.shape == ks
+            and ks[0] == qs[0] and ks[2] == qs[2] and ks[1] > 0 and qs[1] % ks[1] == 0
+            and sq[2] == sk[2] == sv[2] == so[2] == sg[2] == tq[2] == tk[2] == tv[2] == 1
+            and lse.dtype == torch.float32 and lse.shape == (qs[1], qs[0]) and lse.is_contiguous()
+            and plan.dtype == torch.uint8 and plan.is_contiguous() and _bytes(workspace)
+            and _devices(q, k, v, o, lse, do, dq, dk, dv, plan, workspace) == {torch.cuda.current_device()}):
+        if workspace is not None and not _bytes(workspace):
+            _refuse((("workspace", workspace, (torch.uint8,), workspace.shape, True),))
+        _packed_refuse(q, k, plan, lse, (("o", o), ("do", do), ("dq", dq)), (("v", v), ("dk", dk), ("dv", dv)))
     check("fa_bwd_packed", load().fa_bwd_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
-        _RowStrides5(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2], *do.stride()[:2]),
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _RowStrides3(*dq.stride()[:2], *dk.stride()[:2], *dv.stride()[:2]),
-        plan.data_ptr(), rows, Hq, Hkv, d, 1 if causal else 0, scale, 1 if fill else 0, *_ws(workspace),
-        _stream_handle(stream)))
+        _strides10(*sq[:2], *sk[:2], *sv[:2], *so[:2], *sg[:2]), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        _strides6(*tq[:2], *tk[:2], *tv[:2]), plan.data_ptr(), qs[0], qs[1], ks[1], qs[2], 1 if causal else 0, scale,
+        1 if fill else 0, *_ws(workspace), _stream_handle(stream)))
 
 
 def _kv8_dims(k_cache, v_cache, k_scale, v_scale, page_table, lens, counts, *rows):

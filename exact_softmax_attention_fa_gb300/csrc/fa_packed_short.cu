@@ -268,21 +268,32 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
 #pragma unroll 1
     for (int base = 0; base < R; base += 64) {
       const int rows = min(64, R - base), rows16 = (rows + 15) & ~15;
-      for (int r = r0; r < rows16; r += STEP) {
+      // this thread's rows: Q and dO on their way to shared memory, its pieces of O
+      // and L to registers, all at once
+      constexpr int MINE = 64 / STEP;
+      uint4 o_piece[MINE];
+      float L_mine[MINE];
+#pragma unroll
+      for (int m = 0; m < MINE; ++m) {
+        const int r = r0 + m * STEP;
+        o_piece[m] = make_uint4(0u, 0u, 0u, 0u);
+        L_mine[m] = 0.f;
+        if (r >= rows16) break;
         const int at = base + r, head = at / n, pos = at - head * n;
         const bool in = r < rows;
         cp_async16_or_zero(sQ + tile_at<HD>(r, u), in ? q + pos * p.q_st[0] + head * p.q_st[1] : q, in);
         cp_async16_or_zero(sO + tile_at<HD>(r, u), in ? dO + pos * p.do_st[0] + head * p.do_st[1] : dO, in);
+        if (in) o_piece[m] = __ldg(reinterpret_cast<const uint4*>(o + pos * p.o_st[0] + head * p.o_st[1]));
+        if (in && u == 0) L_mine[m] = __ldg(p.lse + static_cast<size_t>(hk * group + head) * p.rows + row0 + pos) * kLog2e;
       }
       cp_async_group();
-      // D and L of the rows, from O as it arrives and this thread's own piece of dO
-#pragma unroll 1
-      for (int r = r0; r < rows16; r += STEP) {
-        const int at = base + r, head = at / n, pos = at - head * n;
-        uint4 a = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) a = __ldg(reinterpret_cast<const uint4*>(o + pos * p.o_st[0] + head * p.o_st[1]));
-        if (r == r0) cp_async_wait_groups<0>();
-        const uint4 b = ld_shared_v4(sO + tile_at<HD>(r, u));
+      cp_async_wait_groups<0>();
+      // D of the rows, from this thread's pieces of O and of dO (which it copied itself)
+#pragma unroll
+      for (int m = 0; m < MINE; ++m) {
+        const int r = r0 + m * STEP;
+        if (r >= rows16) break;
+        const uint4 a = o_piece[m], b = ld_shared_v4(sO + tile_at<HD>(r, u));
         const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
         float d = 0.f;
 #pragma unroll
@@ -294,8 +305,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
 #pragma unroll
         for (int s = (C::UNITS < 32 ? C::UNITS : 32) / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
         if (u == 0) {
-          sD[r] = r < rows ? d : 0.f;
-          sL[r] = r < rows ? p.lse[static_cast<size_t>(hk * group + head) * p.rows + row0 + pos] * kLog2e : 0.f;
+          sD[r] = d;
+          sL[r] = L_mine[m];
         }
       }
       __syncthreads();
