@@ -848,8 +848,11 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_kernel(const 
   const int warp = threadIdx.x >> 5;
   // Without dQ this pass writes nothing the dQ kernel reads, so a dQ kernel
   // queued behind it may take SMs as soon as this grid's CTAs leave them.
+  // (Packed sequences: this grid is itself launched to overlap the end of the one
+  // that forms D and L, and lets the next one start only when that is complete.)
+  if (RAG) griddep_wait();
   if constexpr (!DQ) griddep_launch_dependents();
-  if (RAG && bwd_total_items<RAG>(p) == 0) return;
+  if (RAG && static_cast<int>(blockIdx.x) >= bwd_total_items<RAG>(p)) return;  // no item is left for this CTA
   const int wg = warp >> 2;
 
   if (threadIdx.x == 0) {
@@ -926,8 +929,17 @@ cudaError_t launch_main_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.BH) * T;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  kern<<<static_cast<unsigned>(grid), kernel_threads<RAG>(), C::SMEM_BYTES, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kernel_threads<RAG>());
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = RAG ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int HD>

@@ -673,8 +673,11 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
   const int warp = threadIdx.x >> 5;
   // Without dQ this pass writes nothing the dQ kernel reads, so a dQ kernel
   // queued behind it may take SMs as soon as this grid's CTAs leave them.
+  // (Packed sequences: this grid is itself launched to overlap the end of the one
+  // that forms D and L, and lets the next one start only when that is complete.)
+  if (RAG) griddep_wait();
   if constexpr (!DQ) griddep_launch_dependents();
-  if (RAG && total_items256<RAG>(p) == 0) return;
+  if (RAG && static_cast<int>(blockIdx.x) >= total_items256<RAG>(p)) return;  // no item is left for this CTA
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.kv_full, 1);
@@ -744,8 +747,17 @@ cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.BHkv) * (RAG ? a.N : (a.N + 127) / 128) * 2;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  kern<<<static_cast<unsigned>(grid), kernel_threads<RAG>(), Cfg256::SMEM_BYTES, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kernel_threads<RAG>());
+  cfg.dynamicSmemBytes = Cfg256::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = RAG ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace

@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq_kernel(con
   uint8_t* sV = sK + C::KST * C::TILE_BYTES;
   const int warp = threadIdx.x >> 5;
   if (RAG) griddep_launch_dependents();  // the short sequences' kernel
-  if (RAG && dq_total_items<RAG>(p) == 0) {
+  if (RAG && static_cast<int>(blockIdx.x) >= dq_total_items<RAG>(p)) {  // no item is left for this CTA
     if (threadIdx.x == 0) griddep_wait();
     return;
   }

@@ -198,6 +198,7 @@ constexpr int kPreRows = 4;
 template <int HD>
 __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__ PackedRows a) {
   constexpr int LPR = HD / 8, STEP = 256 / LPR, PARTS = 128 / (STEP * kPreRows);
+  griddep_launch_dependents();
   const bool ok = packed_plan_ok(a.plan, a.rows);
   if (blockIdx.x == 0) {
     if (threadIdx.x < 4) a.sched[threadIdx.x] = 0u;

@@ -225,7 +225,7 @@ struct ShortBwdCfg {
   static constexpr int UNITS = HD / 8;
   static constexpr int TILE = kShortRows * HD * 2;
   static constexpr int P_TILE = 64 * 64 * 2;
-  static constexpr int SMEM = 4 * TILE + 2 * P_TILE + 2 * 64 * 4;
+  static constexpr int SMEM = 4 * TILE + 2 * P_TILE + 3 * 64 * 4;
   static constexpr int PER_SM = HD == 256 ? 1 : 2;
 };
 
@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
                  sS = sP + C::P_TILE;
   float* sD = reinterpret_cast<float*>(smem + 4 * C::TILE + 2 * C::P_TILE);
   float* sL = sD + 64;
+  int* sAt = reinterpret_cast<int*>(sL + 64);  // 256 * head + place of each row, negative behind the last
   const int r0 = threadIdx.x / C::UNITS, u = threadIdx.x % C::UNITS;
   const int n_short = packed_plan_ok(p.plan, p.rows) ? p.plan->n_short : 0;
   const int4* list = packed_tiles(p.plan) + (p.plan->n_tiles - n_short);
@@ -268,6 +269,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
 #pragma unroll 1
     for (int base = 0; base < R; base += 64) {
       const int rows = min(64, R - base), rows16 = (rows + 15) & ~15;
+      if (threadIdx.x < 64) {
+        const int at = base + threadIdx.x;
+        sAt[threadIdx.x] = at < R ? at / n * 256 + at % n : -1;
+      }
+      __syncthreads();
       // this thread's rows: Q and dO on their way to shared memory, its pieces of O
       // and L to registers, all at once
       constexpr int MINE = 64 / STEP;
@@ -279,8 +285,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
         o_piece[m] = make_uint4(0u, 0u, 0u, 0u);
         L_mine[m] = 0.f;
         if (r >= rows16) break;
-        const int at = base + r, head = at / n, pos = at - head * n;
-        const bool in = r < rows;
+        const int at = sAt[r], head = at >> 8, pos = at & 255;
+        const bool in = at >= 0;
         cp_async16_or_zero(sQ + tile_at<HD>(r, u), in ? q + pos * p.q_st[0] + head * p.q_st[1] : q, in);
         cp_async16_or_zero(sO + tile_at<HD>(r, u), in ? dO + pos * p.do_st[0] + head * p.do_st[1] : dO, in);
         if (in) o_piece[m] = __ldg(reinterpret_cast<const uint4*>(o + pos * p.o_st[0] + head * p.o_st[1]));
@@ -337,8 +343,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int r = 16 * rq + (lane >> 2) + 8 * i, at = base + r;
-          const int sees = r >= rows ? 0 : (CAUSAL ? at % n + 1 : n);
+          const int r = 16 * rq + (lane >> 2) + 8 * i, at = sAt[r];
+          const int sees = at < 0 ? 0 : (CAUSAL ? (at & 255) + 1 : n);
           const float L = sL[r], D = sD[r];
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
       }
       __syncthreads();
       for (int r = r0; r < rows; r += STEP) {
-        const int at = base + r, head = at / n, pos = at - head * n;
+        const int at = sAt[r], head = at >> 8, pos = at & 255;
         *reinterpret_cast<uint4*>(p.dq + static_cast<long long>(row0 + pos) * p.dq_st[0] +
                                   (hk * group + head) * p.dq_st[1] + 8 * u) = ld_shared_v4(sQ + tile_at<HD>(r, u));
       }
