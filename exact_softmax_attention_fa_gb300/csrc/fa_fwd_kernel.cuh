@@ -593,7 +593,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
 
     float m2 = -INFINITY;  // reference max of S * scale * log2(e)
     float l = 0.f;         // running sum of P~ (unrounded fp32)
-    for (int j = 0; j <= last_kv - (RAG ? 1 : 0); ++j) {
+    for (int j = 0; j <= last_kv; ++j) {
       alive = alive && __all_sync(0xffffffffu, mbar_wait(&sh.s_full[t], (cnt + j) & 1, &sh.abort_flag, lim));
       if (!alive) {
         record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
@@ -621,13 +621,20 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       const int a = wk.kv0 + j;  // absolute key tile
       const bool mask_tail = (a == Tk - 1) && (Nk & 127);
       const bool mask_diag = CAUSAL && (a * 128 + 127 > qt * rph + p.causal_off);
-      // (over packed sequences both are the query tile's last key tile, taken below)
       if (!RAG && (mask_tail || mask_diag)) {
         int lim_col = Nk - 1 - a * 128;
         if (CAUSAL) lim_col = min(lim_col, row + p.causal_off - a * 128);
 #pragma unroll
         for (int i = 0; i < 128; ++i)
           if (i > lim_col) s[i] = -INFINITY;
+      }
+      if constexpr (RAG) {
+        // Packed sequences: both are the query tile's last key tile.
+        if (__builtin_expect(j == last_kv, 0)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > last_col) s[i] = -INFINITY;
+        }
       }
       // columns 0-7 seed four accumulators, then 8-127 two at a time each
       float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]), mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
@@ -690,94 +697,8 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     }
 
     if constexpr (RAG) {
-      // The last key tile, in 32-column steps: columns that no row of the warp sees
-      // (right of a causal diagonal, behind the last key) cost nothing but the zeros
-      // that the product reads, and only steps that a limit crosses are masked.
-      // Short sequences are all last tiles.
       const bool active = last_kv >= 0;
-      if (active) {
-        alive = alive &&
-                __all_sync(0xffffffffu, mbar_wait(&sh.s_full[t], (cnt + last_kv) & 1, &sh.abort_flag, lim));
-        if (!alive) record_timeout(p.status, &sh.abort_flag, WHERE_FWD_SOFTMAX);
-      }
       if (alive && active) {
-        tc_fence_after_sync();
-        const int held = min(128, wk.n_keys(p) - last_kv * 128);              // keys of the tile
-        const int seen = CAUSAL ? min(held, 32 * ((r >> 5) + 1)) : held;     // columns that the warp sees
-        float s[128];
-        {
-          uint32_t a[32], b[32], c[32], d[32];
-          tmem_ld32(tS + 0, a);
-          tmem_ld32(tS + 32, b);
-          tmem_ld32(tS + 64, c);
-          tmem_ld32(tS + 96, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            s[i] = __uint_as_float(a[i]);
-            s[32 + i] = __uint_as_float(b[i]);
-            s[64 + i] = __uint_as_float(c[i]);
-            s[96 + i] = __uint_as_float(d[i]);
-          }
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (32 * c < seen) {
-            if ((CAUSAL && c == (r >> 5)) || 32 * c + 32 > held) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * c + i > last_col) s[32 * c + i] = -INFINITY;
-            }
-            float m0 = mx, m1 = s[32 * c];
-#pragma unroll
-            for (int i = 1; i < 31; i += 4) {
-              m0 = fmax3(m0, s[32 * c + i], s[32 * c + i + 1]);
-              if (i + 2 < 31) m1 = fmax3(m1, s[32 * c + i + 2], s[32 * c + i + 3]);
-            }
-            mx = fmax3(m0, m1, s[32 * c + 31]);
-          }
-        const float m_run = fmaxf(m2, mx * c2);
-        const bool move = __any_sync(0xffffffffu, m_run > m2 + kRescaleSlack && last_col >= 0);
-        const float m_ref = move ? m_run : m2;
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const float alpha = ex2_approx(m2 - m_use);
-        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-          if (32 * c < seen) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = ffma2_bcast(s[32 * c + 2 * i], s[32 * c + 2 * i + 1], c2, -m_use);
-              const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-              if (i & 1) sum_b = fadd2(sum_b, e); else sum_a = fadd2(sum_a, e);
-              pk[i] = pack_bf16x2(e.x, e.y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0u;
-          }
-          if (32 * c < held) tmem_st16(tP + 16 * c, pk);
-        }
-        const float2 sum2 = fadd2(sum_a, sum_b);
-        l = l * alpha + (sum2.x + sum2.y);
-        if (last_kv > 0 && move) {
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tO + c, o);
-          }
-        }
-        m2 = m_ref;
-        tmem_st_wait();
-        tc_fence_before_sync();
-        mbar_arrive(&sh.p_full[t]);
-
         // L, and where O goes, while the last product runs.
         asm volatile("" : "+r"(item));  // the entry is read again, not kept
         const FwdWork<C::NT, CAUSAL, PACK, RAG> wo(item, p);
