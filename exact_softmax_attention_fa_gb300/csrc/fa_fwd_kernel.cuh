@@ -591,6 +591,15 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
     const int last_col =
         !RAG || row >= wk.n_queries(p) ? -1 : (CAUSAL ? r : min(127, wk.n_keys(p) - 1 - last_kv * 128));
 
+    // where this warp's rows of O go: the first one's place, how many the sequence
+    // has (at most 32) and the head
+    int grow = 0;
+    uint32_t place = 0;
+    if constexpr (RAG) {
+      const int left = wk.n_queries(p) - (qt * 128 + (r & ~31));
+      grow = wk.q_row(p, t) + (r & ~31);
+      place = static_cast<uint32_t>(max(0, min(32, left))) << 26 | static_cast<uint32_t>(wk.q_head(t));
+    }
     float m2 = -INFINITY;  // reference max of S * scale * log2(e)
     float l = 0.f;         // running sum of P~ (unrounded fp32)
     for (int j = 0; j <= last_kv; ++j) {
@@ -700,10 +709,7 @@ __device__ void fwd_softmax_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ,
       const bool active = last_kv >= 0;
       if (alive && active) {
         // L, and where O goes, while the last product runs.
-        asm volatile("" : "+r"(item));  // the entry is read again, not kept
-        const FwdWork<C::NT, CAUSAL, PACK, RAG> wo(item, p);
-        const int first = wo.tile(t) * 128 + (r & ~31), o_head = wo.q_head(t), grow = wo.q_row(p, t) + (r & ~31);
-        const int rows = wo.n_queries(p) - first;  // of this warp that the sequence has
+        const int rows = static_cast<int>(place >> 26), o_head = static_cast<int>(place & 0x3ffffffu);
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         if ((r & 31) < rows)
           p.lse[static_cast<size_t>(o_head) * p.Nq + grow + (r & 31)] = l > 0.f ? (m2 + log2f(l)) * kLn2 : -INFINITY;

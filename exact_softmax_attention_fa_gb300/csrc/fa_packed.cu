@@ -316,6 +316,7 @@ constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 fa_status_t check_packed(int rows, int Hq, int Hkv, int d, int causal, float scale, bool* empty) {
   fa_status_t st = check_common(1, Hq, rows, d, causal, scale, empty);
   if (st == FA_OK) st = check_heads(Hq, Hkv);
+  if (st == FA_OK && Hq > 65535) st = FA_ERR_INVALID_ARG;  // a head's number shares a register with a count
   // work items are counted in 32 bits
   if (st == FA_OK && static_cast<long long>(rows) * Hq >= (1ll << 31)) st = FA_ERR_INVALID_ARG;
   return st;

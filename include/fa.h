@@ -465,7 +465,7 @@ fa_status_t fa_norm_rope_axes_bwd(const void* dq, const void* dk, const void* dv
  *   dk and dv are sums over the heads of a group; all outputs are bitwise
  *   reproducible on one kind of device with one size of workspace (a split
  *   group's heads are summed in parts), whatever the plan's order.
- * rows * Hq must be below 2^31. rows = 0 or Hq = 0 is a no-op.
+ * rows * Hq must be below 2^31, Hq at most 65535. rows = 0 or Hq = 0 is a no-op.
  */
 size_t fa_packed_plan_size(int B, int rows); /* 0 for negative sizes */
 fa_status_t fa_packed_plan(const int* cu_seqlens, int B, int rows, int causal, void* plan, size_t plan_bytes,

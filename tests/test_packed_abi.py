@@ -58,7 +58,8 @@ def but(at, value, base=GOOD):
 def test_forward_refusals(lib):
     for kw in (dict(rows=-1), dict(Hq=-4), dict(Hkv=-1), dict(Hkv=0), dict(Hkv=3), dict(causal=2), dict(scale=0.0),
                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(fill=2), dict(fill=-1),
-               dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(lse=0), dict(plan=0), dict(rows=1 << 29)):
+               dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(lse=0), dict(plan=0), dict(rows=1 << 29),
+               dict(rows=1, Hq=65536, Hkv=1)):
         assert fwd(lib, **kw) == INVALID, kw
     for d in (0, 32, 96, 512):
         assert fwd(lib, d=d) == UNSUPPORTED
