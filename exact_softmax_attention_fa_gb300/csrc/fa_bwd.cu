@@ -620,8 +620,15 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
         if (c < c_lo) pv[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
-    tmem_st32(tA, pk);  // columns [64w, 64w + 32): already read
+    for (int c = 0; c < 32; ++c) pk[c] = keep_weights<RAG>(pv[2 * c], pv[2 * c + 1]);
+    if constexpr (RAG) {
+      uint32_t pb[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
+      tmem_st32(tA, pb);
+    } else {
+      tmem_st32(tA, pk);  // columns [64w, 64w + 32): already read
+    }
     tmem_st_wait();
     tc_fence_before_sync();
     mbar_arrive(&sh.pa_ready);
@@ -649,8 +656,8 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
         const float4 dd = kPrefetchStats ? dvv[kPrefetchStats ? (32 * h + c4) / 4 : 0]
                                          : *reinterpret_cast<const float4*>(ld_d + 32 * h + c4);
         const float dv4[4] = {dd.x, dd.y, dd.z, dd.w};
-        const float2 p01 = unpack_bf16x2(pk[16 * h + c4 / 2]);
-        const float2 p23 = unpack_bf16x2(pk[16 * h + c4 / 2 + 1]);
+        const float2 p01 = kept_weights<RAG>(pk[16 * h + c4 / 2]);
+        const float2 p23 = kept_weights<RAG>(pk[16 * h + c4 / 2 + 1]);
         const float2 g01 =
             ffma2_bcast_mul(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dv4[0], -dv4[1]);
         const float2 g23 =

@@ -503,8 +503,15 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
         if (!key_valid || c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
-    tmem_st16(tA, pk);  // columns [32w, 32w + 16): already read
+    for (int c = 0; c < 16; ++c) pk[c] = keep_weights<RAG>(pv[2 * c], pv[2 * c + 1]);
+    if constexpr (RAG) {
+      uint32_t pb[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
+      tmem_st16(tA, pb);
+    } else {
+      tmem_st16(tA, pk);  // columns [32w, 32w + 16): already read
+    }
     tmem_st_wait();
     tc_fence_before_sync();
     mbar_arrive(&sh.pa_ready);
@@ -523,8 +530,8 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 #pragma unroll
     for (int c4 = 0; c4 < 32; c4 += 4) {
       const float4 dd = *reinterpret_cast<const float4*>(ld_d + c4);
-      const float2 p01 = unpack_bf16x2(pk[c4 / 2]);
-      const float2 p23 = unpack_bf16x2(pk[c4 / 2 + 1]);
+      const float2 p01 = kept_weights<RAG>(pk[c4 / 2]);
+      const float2 p23 = kept_weights<RAG>(pk[c4 / 2 + 1]);
       const float2 g01 = ffma2_bcast_mul(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dd.x, -dd.y);
       const float2 g23 = ffma2_bcast_mul(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dd.z, -dd.w);
       const float2 ds01 = fmul2(p01, g01);

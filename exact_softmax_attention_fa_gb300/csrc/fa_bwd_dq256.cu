@@ -412,8 +412,8 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
             for (int q = 0; q < 4; ++q)
               if (c4 + q >= c_hi) pv[c4 + q] = 0.f;
           }
-          pk[c4 / 2] = pack_bf16x2(pv[c4], pv[c4 + 1]);
-          pk[c4 / 2 + 1] = pack_bf16x2(pv[c4 + 2], pv[c4 + 3]);
+          pk[c4 / 2] = keep_weights<RAG>(pv[c4], pv[c4 + 1]);
+          pk[c4 / 2 + 1] = keep_weights<RAG>(pv[c4 + 2], pv[c4 + 3]);
         }
       }
       // ---- phase B: dS into the first 32 columns of this warpgroup's half
@@ -428,8 +428,8 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
           tmem_ld_wait();
 #pragma unroll
           for (int c4 = 0; c4 < 32; c4 += 4) {
-            const float2 p01 = unpack_bf16x2(pk[16 * h2 + c4 / 2]);
-            const float2 p23 = unpack_bf16x2(pk[16 * h2 + c4 / 2 + 1]);
+            const float2 p01 = kept_weights<RAG>(pk[16 * h2 + c4 / 2]);
+            const float2 p23 = kept_weights<RAG>(pk[16 * h2 + c4 / 2 + 1]);
             const float2 g01 = ffma2_bcast(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dsc);
             const float2 g23 = ffma2_bcast(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dsc);
             const float2 d01 = fmul2(p01, g01);
