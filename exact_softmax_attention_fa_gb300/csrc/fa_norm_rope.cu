@@ -15,10 +15,12 @@
 // (bytes in flight), and the token's angles are read once for all of them.
 //
 // At B = 2, N = 8192, 16 heads for q, k and v, d = 128: forward 65 us, 6.3 TB/s or
-// 0.92 of the copy rate; backward 111 us, 4.9 TB/s. The backward holds dy, x and the
-// dw of its columns in registers, which leaves 16 warps an SM; it waits for
-// loads (more rows on their way, more or fewer warps, and a unit's first rows
-// fetched behind the unit before all measured within 2%).
+// 0.92 of the copy rate; backward 100 us, 5.4 TB/s (without weights, whose rows are
+// two instead of three, 63 us and 6.4 TB/s). With the weights' gradients the backward
+// is held up by its instructions (230 for two rows of a warp; it issues in 0.62 of the
+// cycles of 16 warps an SM): one head at a time, its two sums together and a warp's
+// lane groups in step (shuffles of whole warps) took 109 us where two heads at a time
+// through registers took 119; two interleaved heads, which spill, 134; 24 warps 124.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,9 +37,10 @@ namespace {
 constexpr int kFwdThreads = 64;      // 256: 69.3, 128: 67.3 instead of 65.0 us (B = 2, N = 8192, 16 heads, d = 128)
 constexpr int kThreads = 256;        // backward
 constexpr int kHeads = 4;            // heads of one token per lane group, forward
-constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward: kBwdSide at a time
-constexpr int kBwdSide = 2;
+constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward
+constexpr int kBwdRing = 6;         // heads on their way to a lane group: 48 KB a block
 constexpr int kBwdPerSm = 2;         // blocks of the backward on an SM
+constexpr int kBwdSmem = kBwdRing * 2 * kThreads * 16;
 constexpr int kMaxBwdBlocks = kBwdPerSm * 152;  // partial sums of dw, for q and k each
 
 struct NormRope {
@@ -78,6 +81,22 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// Asynchronous copies of 16 bytes to shared memory, past L1, in groups that end in order.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
 // Two groups of four columns: pairs 0, 1 and pairs 2, 3 (two columns an operation).
 struct Cols {
   float2 f[4];
@@ -113,6 +132,8 @@ struct Lane {
       b = a + p.half;
     }
     angle = 4 * j;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = s[i] = make_float2(0.f, 0.f);
   }
 
   __device__ __forceinline__ void load_angles(const NormRope& p, int pos) {
@@ -198,25 +219,33 @@ struct Lane {
   }
 };
 
-// The token's angles into the lane; false, recorded once, where a position is outside the tables.
-template <bool AXES, class L>
-__device__ __forceinline__ bool take_angles(L& lane, const NormRope& p, int token, int n, uint32_t where) {
-  bool ok = true;
-  if constexpr (AXES) {
-    int pos[4] = {0, 0, 0, 0};
+// A token's position, or its one for each axis.
+template <bool AXES>
+struct Place {
+  int pos[AXES ? 4 : 1];
+  __device__ __forceinline__ void load(const NormRope& p, int token, int n) {
+    if constexpr (AXES) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-      if (a < p.axes) {
-        pos[a] = __ldg(p.positions + static_cast<size_t>(a) * p.tokens + token);
-        ok = ok && pos[a] >= 0 && pos[a] < p.table_rows;
-      }
-    if (ok) lane.load_angles(p, pos);
-  } else {
-    const int pos = p.positions ? __ldg(p.positions + token) : n;
-    ok = pos >= 0 && pos < p.table_rows;
-    if (ok) lane.load_angles(p, pos);
+      for (int a = 0; a < 4; ++a) pos[a] = a < p.axes ? __ldg(p.positions + static_cast<size_t>(a) * p.tokens + token) : 0;
+    } else {
+      pos[0] = p.positions ? __ldg(p.positions + token) : n;
+    }
   }
-  if (!ok && lane.angle == 0) record_bad_index(p.status, where);
+};
+
+// Its angles into the lane; false, recorded once, where a position is outside the tables.
+template <bool AXES, class L>
+__device__ __forceinline__ bool take_angles(L& lane, const NormRope& p, const Place<AXES>& at, uint32_t where) {
+  bool ok = true;
+#pragma unroll
+  for (int a = 0; a < (AXES ? 4 : 1); ++a)
+    if (!AXES || a < p.axes) ok = ok && at.pos[a] >= 0 && at.pos[a] < p.table_rows;
+  if (ok) {
+    if constexpr (AXES) lane.load_angles(p, at.pos);
+    else lane.load_angles(p, at.pos[0]);
+  } else if (lane.angle == 0) {
+    record_bad_index(p.status, where);
+  }
   return ok;
 }
 
@@ -247,7 +276,11 @@ __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __
       if (u < nh) L.store(dst + u * step, raw[u][0], raw[u][1]);
     return;
   }
-  if (p.rot > 0 && !take_angles<AXES>(L, p, token, n, WHERE_NORM_ROPE)) return;
+  if (p.rot > 0) {
+    Place<AXES> at;
+    at.load(p, token, n);
+    if (!take_angles(L, p, at, WHERE_NORM_ROPE)) return;
+  }
   float2 w[4];
   if (NORM) L.load_weights(p, kind, w);
 #pragma unroll
@@ -269,93 +302,160 @@ __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __
 }
 
 // Persistent: the blocks are shared out over q, k and v by their work, and a
-// lane group takes up to kBwdHeads heads of one token, two at a time with the
-// next two on their way. Each lane sums dw of its 8 columns over the rows it
-// meets; the block's lane groups are added in order, and norm_rope_dw_kernel
-// adds the blocks in order, so dw does not depend on timing.
+// lane group takes up to kBwdHeads heads of one token. Its rows come through a ring
+// in shared memory, kBwdRing heads ahead and on into its next unit; the unit's angles
+// are read a unit ahead, its positions two. Each lane sums dw of its 8 columns over
+// the rows it meets; the block's lane groups are added in order, and
+// norm_rope_dw_kernel adds the blocks in order, so dw does not depend on timing.
 template <int D, bool INTER, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
-  constexpr int GROUPS = kThreads / (D / 8), SIDE = kBwdSide;
-  __shared__ float red[GROUPS][D];
+  constexpr int GROUPS = kThreads / (D / 8);
+  extern __shared__ uint4 ring[];  // [kBwdRing][dy, x][kThreads]; after the last row [GROUPS][D] floats
   griddep_launch_dependents();
   Lane<D, INTER> L;
   L.init(p);
   const int group = threadIdx.x / L.LPR;
   int block = blockIdx.x, kind = 0;
   while (block >= p.blocks[kind]) block -= p.blocks[kind++];
-  const int chunks = p.chunks[kind], heads = p.H[kind], n_blocks = p.blocks[kind];
-  const long long units = static_cast<long long>(p.tokens) * chunks;
+  const int chunks = p.chunks[kind], heads = p.H[kind];
+  const long long units = static_cast<long long>(p.tokens) * chunks, next = static_cast<long long>(p.blocks[kind]) * GROUPS;
   const long long step = static_cast<long long>(p.N) * D, x_step = p.xs[kind][1], d_step = p.ds[kind][1];
-  const bool norm = NORM && kind < 2;
+  const bool norm = NORM && kind < 2, turn = kind < 2 && p.rot > 0;
+  auto token_of = [&](long long unit) { return static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks)); };
   float2 dw[4], w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
   if (norm) L.load_weights(p, kind, w);
-#pragma unroll 1
-  for (long long unit = static_cast<long long>(block) * GROUPS + group; unit < units;
-       unit += static_cast<long long>(n_blocks) * GROUPS) {
-    const int token = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks));
-    const int h0 = (static_cast<int>(unit) - token * chunks) * kBwdHeads, nh = min(kBwdHeads, heads - h0);
-    const int b = token / p.N, n = token - b * p.N;
-    const __nv_bfloat16* gy = p.dy[kind] + (static_cast<size_t>(b) * heads + h0) * step + static_cast<size_t>(n) * D;
-    const __nv_bfloat16* src = norm ? p.x[kind] + b * p.xs[kind][0] + h0 * x_step + n * p.xs[kind][2] : nullptr;
-    __nv_bfloat16* out = p.dx[kind] + b * p.ds[kind][0] + h0 * d_step + n * p.ds[kind][2];
-    uint2 g_raw[SIDE][2], x_raw[SIDE][2];
-    auto fetch = [&](int h) {
-#pragma unroll
-      for (int u = 0; u < SIDE; ++u)
-        if (h + u < nh) {
-          L.load(gy + (h + u) * step, g_raw[u]);
-          if (norm) L.load(src + (h + u) * x_step, x_raw[u]);
-        }
-    };
-    fetch(0);
-    if (kind < 2 && p.rot > 0 && !take_angles<AXES>(L, p, token, n, WHERE_NORM_ROPE_BWD)) continue;
-#pragma unroll 1
-    for (int h = 0; h < nh; h += SIDE) {
-      uint2 g_now[SIDE][2], x_now[SIDE][2];
-#pragma unroll
-      for (int u = 0; u < SIDE; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          g_now[u][e] = g_raw[u][e];
-          if (norm) x_now[u][e] = x_raw[u][e];
-        }
-      fetch(h + SIDE);
-#pragma unroll
-      for (int u = 0; u < SIDE; ++u) {
-        if (h + u >= nh) break;
-        __nv_bfloat16* row = out + (h + u) * d_step;
-        if (kind == 2) {
-          L.store(row, g_now[u][0], g_now[u][1]);
-          continue;
-        }
-        Cols g;
-        g.unpack(g_now[u][0], g_now[u][1]);
-        L.template rotate<true>(g);
-        if (NORM) {
-          Cols x, gw;
-          x.unpack(x_now[u][0], x_now[u][1]);
-          float2 ss = fmul2(x.f[0], x.f[0]), hx = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i > 0) ss = fma2(x.f[i], x.f[i], ss);
-            gw.f[i] = fmul2(g.f[i], w[i]);
-            hx = fma2(gw.f[i], x.f[i], hx);
-          }
-          const float r = rsqrtf(L.sum(ss.x + ss.y) * (1.f / D) + p.eps);
-          const float m = -L.sum(hx.x + hx.y) * (1.f / D) * r * r * r;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dw[i] = fma2(fmul2(g.f[i], both(r)), x.f[i], dw[i]);
-            g.f[i] = fma2(gw.f[i], both(r), fmul2(x.f[i], both(m)));
-          }
-        }
-        L.store(row, g.pack(0), g.pack(1));
+
+  // The rows on their way: the next one to ask for, and the unit's heads behind it.
+  const long long first = static_cast<long long>(block) * GROUPS + group;
+  long long ahead = first;
+  const __nv_bfloat16 *gy = nullptr, *src = nullptr;
+  int left = 0;
+  constexpr uint32_t SLOT = 2 * kThreads * 16, X = kThreads * 16;
+  // the slot to read next, which the row kBwdRing later then takes, and the lane's
+  // places in a slot: what it copies, and the columns it reads
+  uint32_t slot = smem_u32(ring);
+  const uint32_t end = slot + kBwdRing * SLOT, to = 16 * threadIdx.x, from = 16 * group * L.LPR;
+  const uint32_t from_a = from + 2 * L.a, from_b = from + 2 * L.b;
+  auto open = [&] {
+    if (ahead >= units) return;
+    const int token = token_of(ahead), h0 = (static_cast<int>(ahead) - token * chunks) * kBwdHeads;
+    const int b = token / p.N, n = token - b * p.N, col = 8 * (threadIdx.x % L.LPR);
+    left = min(kBwdHeads, heads - h0);
+    gy = p.dy[kind] + (static_cast<size_t>(b) * heads + h0) * step + static_cast<size_t>(n) * D + col;
+    if (norm) src = p.x[kind] + b * p.xs[kind][0] + h0 * x_step + n * p.xs[kind][2] + col;
+  };
+  auto fetch = [&] {
+    if (left > 0) {
+      cp_async16(slot + to, gy);
+      gy += step;
+      if (norm) {
+        cp_async16(slot + to + X, src);
+        src += x_step;
       }
+      if (--left == 0) {
+        ahead += next;
+        open();
+      }
+    }
+    cp_async_commit();
+    slot += SLOT;
+    if (slot == end) slot -= kBwdRing * SLOT;
+  };
+  open();
+#pragma unroll 1
+  for (int i = 0; i < kBwdRing; ++i) fetch();
+  Place<AXES> at{};
+  Lane<D, INTER> turns = L;  // the next unit's angles
+  bool ok = true;
+  auto place = [&](long long unit) {
+    if (unit >= units) return;
+    const int token = token_of(unit);
+    at.load(p, token, token % p.N);
+  };
+  if (turn && first < units) {
+    place(first);
+    ok = take_angles(turns, p, at, WHERE_NORM_ROPE_BWD);
+    place(first + next);
+  }
+  // A warp's groups go round together, so that its shuffles take whole warps: a
+  // group that has no row left, or no angles, goes on and leaves its result.
+  const long long warp_first = first - (threadIdx.x % 32) / L.LPR;
+#pragma unroll 1
+  for (long long at_unit = 0; warp_first + at_unit < units; at_unit += next) {
+    const long long unit = first + at_unit;
+    int nh = 0;
+    __nv_bfloat16* out = nullptr;
+    if (unit < units) {
+      const int token = token_of(unit);
+      const int h0 = (static_cast<int>(unit) - token * chunks) * kBwdHeads;
+      const int b = token / p.N, n = token - b * p.N;
+      nh = min(kBwdHeads, heads - h0);
+      out = p.dx[kind] + b * p.ds[kind][0] + h0 * d_step + n * p.ds[kind][2];
+    }
+    const bool write = ok;
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) L.c[i] = turns.c[i], L.s[i] = turns.s[i];
+      if (unit + next < units) ok = take_angles(turns, p, at, WHERE_NORM_ROPE_BWD);
+      place(unit + 2 * next);
+    }
+    int most = nh;
+#pragma unroll
+    for (int o = L.LPR; o < 32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+#pragma unroll 1
+    for (int h = 0; h < most; ++h, out += d_step) {
+      const bool held = h < nh, wanted = held && write;
+      cp_async_wait<kBwdRing - 1>();
+      __syncwarp();
+      const uint2 g_now[2] = {ld_shared_v2(slot + from_a), ld_shared_v2(slot + from_b)};
+      uint2 x_now[2];
+      if (norm) {
+        x_now[0] = ld_shared_v2(slot + from_a + X);
+        x_now[1] = ld_shared_v2(slot + from_b + X);
+      }
+      __syncwarp();
+      if (held) fetch();
+      if (kind == 2) {
+        if (wanted) L.store(out, g_now[0], g_now[1]);
+        continue;
+      }
+      Cols g;
+      g.unpack(g_now[0], g_now[1]);
+      L.template rotate<true>(g);
+      if (NORM) {
+        Cols x, gw;
+        x.unpack(x_now[0], x_now[1]);
+        float2 ss = fmul2(x.f[0], x.f[0]), hx = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i > 0) ss = fma2(x.f[i], x.f[i], ss);
+          gw.f[i] = fmul2(g.f[i], w[i]);
+          hx = fma2(gw.f[i], x.f[i], hx);
+        }
+        float sum_x = ss.x + ss.y, sum_h = hx.x + hx.y;
+#pragma unroll
+        for (int o = L.LPR / 2; o > 0; o >>= 1) {
+          sum_x += __shfl_xor_sync(0xffffffffu, sum_x, o);
+          sum_h += __shfl_xor_sync(0xffffffffu, sum_h, o);
+        }
+        const float r = rsqrtf(sum_x * (1.f / D) + p.eps);
+        const float m = -sum_h * (1.f / D) * r * r * r;
+        if (wanted) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dw[i] = fma2(fmul2(g.f[i], both(r)), x.f[i], dw[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g.f[i] = fma2(gw.f[i], both(r), fmul2(x.f[i], both(m)));
+      }
+      if (wanted) L.store(out, g.pack(0), g.pack(1));
     }
   }
   if (norm) {
+    cp_async_wait<0>();
+    __syncthreads();
+    float(*red)[D] = reinterpret_cast<float(*)[D]>(ring);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float2*>(&red[group][(i < 2 ? L.a : L.b - 4) + 2 * i]) = dw[i];
@@ -390,10 +490,10 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
 template <bool BACK, int D, bool INTER, bool NORM>
 cudaError_t launch_norm_rope_t(const NormRope& a, int blocks, cudaStream_t stream) {
   if (a.axes) {
-    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, true><<<blocks, kThreads, 0, stream>>>(a);
+    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, true><<<blocks, kThreads, kBwdSmem, stream>>>(a);
     else norm_rope_fwd_kernel<D, INTER, NORM, true><<<blocks, kFwdThreads, 0, stream>>>(a);
   } else {
-    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, false><<<blocks, kThreads, 0, stream>>>(a);
+    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, false><<<blocks, kThreads, kBwdSmem, stream>>>(a);
     else norm_rope_fwd_kernel<D, INTER, NORM, false><<<blocks, kFwdThreads, 0, stream>>>(a);
   }
   return cudaGetLastError();
