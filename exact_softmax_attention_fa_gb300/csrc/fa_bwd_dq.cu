@@ -485,9 +485,9 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq_kernel(con
   uint8_t* sK = sdO + C::TILE_BYTES;
   uint8_t* sV = sK + C::KST * C::TILE_BYTES;
   const int warp = threadIdx.x >> 5;
-  if (RAG) griddep_launch_dependents();  // the short sequences' kernel
+  if (RAG) griddep_launch_dependents();  // the kernel that joins a split group's sums
   if (RAG && static_cast<int>(blockIdx.x) >= dq_total_items<RAG>(p)) {  // no item is left for this CTA
-    if (threadIdx.x == 0) griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) griddep_wait();
     return;
   }
 
@@ -544,8 +544,9 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq_kernel(con
   tc_fence_after_sync();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
   // Launched to overlap the dK/dV pass (overlap_prev), this grid must not
-  // complete before that pass has: work queued after it may read dK and dV.
-  if (threadIdx.x == 0) griddep_wait();
+  // complete before that pass has: work queued after it may read dK and dV. (Over
+  // packed sequences one block waits and the others leave their SMs.)
+  if ((!RAG || blockIdx.x == 0) && threadIdx.x == 0) griddep_wait();
 }
 
 template <int HD, bool CAUSAL, bool RAG = false>

@@ -497,9 +497,9 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq256_kernel(
   uint8_t* sdO = sQ + C::TILE_BYTES;
   uint8_t* sRing = sdO + C::TILE_BYTES;
   const int warp = threadIdx.x >> 5;
-  if (RAG) griddep_launch_dependents();  // the short sequences' kernel
+  if (RAG) griddep_launch_dependents();  // the kernel that joins a split group's sums
   if (RAG && static_cast<int>(blockIdx.x) >= dq_total_items<RAG>(p)) {  // no item is left for this CTA
-    if (threadIdx.x == 0) griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) griddep_wait();
     return;
   }
 
@@ -551,8 +551,9 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_dq256_kernel(
   tc_fence_after_sync();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
   // Launched to overlap the dK/dV pass (overlap_prev), this grid must not
-  // complete before that pass has: work queued after it may read dK and dV.
-  if (threadIdx.x == 0) griddep_wait();
+  // complete before that pass has: work queued after it may read dK and dV. (Over
+  // packed sequences one block waits and the others leave their SMs.)
+  if ((!RAG || blockIdx.x == 0) && threadIdx.x == 0) griddep_wait();
 }
 
 template <bool CAUSAL, bool RAG = false>

@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
     __syncthreads();  // every warp is done with K and V
   }
   // Launched to overlap the kernel for the other sequences: work queued after this
-  // one may read what that one writes.
-  if (threadIdx.x == 0) griddep_wait();
+  // one may read what that one writes. One block that waits keeps the grid from
+  // ending; the others leave their SMs to the kernels behind.
+  if (blockIdx.x == 0 && threadIdx.x == 0) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -232,6 +233,7 @@ struct ShortBwdCfg {
 template <int HD, bool CAUSAL>
 __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
     packed_short_bwd_kernel(const __grid_constant__ ShortLaunch p) {
+  griddep_launch_dependents();  // the dQ kernel
   using C = ShortBwdCfg<HD>;
   constexpr int THREADS = 32 * kBwdWarps, STEP = THREADS / C::UNITS;  // a row by UNITS threads, STEP rows at a time
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) griddep_wait();  // as the forward
+  if (blockIdx.x == 0 && threadIdx.x == 0) griddep_wait();  // as the forward
 }
 
 // Queue a kernel so that it takes SMs as the kernel before it leaves them.
