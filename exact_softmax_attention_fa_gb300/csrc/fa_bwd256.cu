@@ -448,7 +448,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   const uint32_t tB = tmem + lane_base + C::REG_DP + 32 * w;
   const int total = total_items256<RAG>(p);
   bool alive = true;
-  uint32_t pk[16];  // P^T of the current tile (bf16 pairs, as written to TMEM): dS uses the same rounding
+  // P^T of the current tile (bf16 pairs, as written to TMEM: dS uses the same rounding;
+  // over packed sequences fp32, three of up to 2501 rows 610 us, by pairs 627)
+  Weights<32, RAG, RAG ? 32 : 0> pk;
 
   // thread r < 32 loads L2 of query 32w + r of the tile, 32 <= r < 64 its scaled D
   // Queries behind a packed sequence's last one get L2 = +inf (weight 0) and D = 0.
@@ -503,14 +505,14 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
         if (!key_valid || c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 16; ++c) pk[c] = keep_weights<RAG>(pv[2 * c], pv[2 * c + 1]);
+    for (int c = 0; c < 32; c += 2) pk.put(c, pv[c], pv[c + 1]);
     if constexpr (RAG) {
       uint32_t pb[16];
 #pragma unroll
       for (int c = 0; c < 16; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
       tmem_st16(tA, pb);
     } else {
-      tmem_st16(tA, pk);  // columns [32w, 32w + 16): already read
+      tmem_st16(tA, pk.two);  // columns [32w, 32w + 16): already read
     }
     tmem_st_wait();
     tc_fence_before_sync();
@@ -530,8 +532,8 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 #pragma unroll
     for (int c4 = 0; c4 < 32; c4 += 4) {
       const float4 dd = *reinterpret_cast<const float4*>(ld_d + c4);
-      const float2 p01 = kept_weights<RAG>(pk[c4 / 2]);
-      const float2 p23 = kept_weights<RAG>(pk[c4 / 2 + 1]);
+      const float2 p01 = pk.get(c4);
+      const float2 p23 = pk.get(c4 + 2);
       const float2 g01 = ffma2_bcast_mul(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dd.x, -dd.y);
       const float2 g23 = ffma2_bcast_mul(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dd.z, -dd.w);
       const float2 ds01 = fmul2(p01, g01);

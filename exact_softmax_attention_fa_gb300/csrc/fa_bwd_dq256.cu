@@ -352,7 +352,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
   const uint32_t bar_id = 1 + w;
   const int total = dq_total_items<RAG>(p);
   bool alive = true;
-  uint32_t pk[32];  // P of the current tile, bf16 pairs
+  Weights<64, RAG, 0> pk;  // P of the current tile, by pairs (32 in fp32: no change)
 
   auto wait_all = [&](uint64_t* bar, int parity, int where) {
     alive = alive && __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort_flag, lim));
@@ -412,8 +412,8 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
             for (int q = 0; q < 4; ++q)
               if (c4 + q >= c_hi) pv[c4 + q] = 0.f;
           }
-          pk[c4 / 2] = keep_weights<RAG>(pv[c4], pv[c4 + 1]);
-          pk[c4 / 2 + 1] = keep_weights<RAG>(pv[c4 + 2], pv[c4 + 3]);
+          pk.put(c4, pv[c4], pv[c4 + 1]);
+          pk.put(c4 + 2, pv[c4 + 2], pv[c4 + 3]);
         }
       }
       // ---- phase B: dS into the first 32 columns of this warpgroup's half
@@ -428,8 +428,8 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
           tmem_ld_wait();
 #pragma unroll
           for (int c4 = 0; c4 < 32; c4 += 4) {
-            const float2 p01 = kept_weights<RAG>(pk[16 * h2 + c4 / 2]);
-            const float2 p23 = kept_weights<RAG>(pk[16 * h2 + c4 / 2 + 1]);
+            const float2 p01 = pk.get(32 * h2 + c4);
+            const float2 p23 = pk.get(32 * h2 + c4 + 2);
             const float2 g01 = ffma2_bcast(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dsc);
             const float2 g23 = ffma2_bcast(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dsc);
             const float2 d01 = fmul2(p01, g01);
