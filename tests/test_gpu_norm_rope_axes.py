@@ -31,6 +31,10 @@ CASES = [  # B, Hq, Hkv, N, d, the axis of each pair, interleaved, weights
     (1, 9, 3, 70, 256, blocks(1, 127), True, "float32"),
     (2, 7, 0, 11, 128, blocks(3, 29, 32), False, "float32"),
     (16, 32, 8, 1, 128, blocks(16, 24, 24), False, "float32"),
+    # tokens of several units with different numbers of heads beside each other in a warp
+    (2, 20, 3, 97, 64, [i % 3 for i in range(32)], False, "float32"),
+    (1, 13, 11, 600, 64, blocks(10, 22), True, "bfloat16"),
+    (3, 20, 9, 203, 128, blocks(64), False, "float32"),
 ]
 
 

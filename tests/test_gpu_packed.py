@@ -75,6 +75,13 @@ def test_split_groups():
     check(Batch([700, 20], 6, 1, 64, BASE_SEED + 961), False)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 1)])
+def test_around_the_short_kernels_limit(Hq, Hkv, causal, d):
+    check(Batch([63, 65, 64, 66, 1, 62], Hq, Hkv, d, BASE_SEED + 970), causal)
+
+
 def test_layouts():
     """Heads outside, tokens outside, and a packed projection: the same bits."""
     import exact_softmax_attention_fa_gb300 as fa
@@ -251,6 +258,90 @@ def test_captured_step_replays_with_other_lengths():
         want = run(x, True, 0.1)
         for a, c in zip(got, (want[0], want[1], *want[2])):
             assert torch.equal(a, c)
+
+
+def test_graphs_of_two_batches_share_a_workspace():
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    bs = [Batch(lens, 8, 2, 128, BASE_SEED + 25 + i) for i, lens in enumerate(([700, 40, 260], [10, 600, 64, 65, 261]))]
+    want = [run(b, True, 0.1) for b in bs]
+    assert bs[0].rows == bs[1].rows
+    ws = torch.empty(fa.fa_bwd_packed_workspace_size(1000, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    made = []
+    for b in bs:
+        plan = fa.PackedPlan(b.d_cu, b.rows)
+        o, lse, grad = torch.empty_like(b.d_do), torch.empty(8, b.rows, device="cuda"), torch.empty_like(b.qkv)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fa.fa_fwd_packed(b.d_q, b.d_k, b.d_v, o, lse, plan, True, 0.1)
+            fa.fa_bwd_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, grad[:, :8], grad[:, 8:10], grad[:, 10:], plan, True,
+                             0.1, ws)
+        made.append((graph, plan, o, lse, grad))
+    for _ in range(3):
+        for graph, _, o, lse, grad in made:
+            for t in (o, lse, grad):
+                t.fill_(7.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, o, lse, grad), w in zip(made, want):
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+            for x, y in zip((grad[:, :8], grad[:, 8:10], grad[:, 10:]), w[2]):
+                assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(16, 1, 128), (8, 8, 64), (4, 1, 256)])
+def test_work_queued_behind_sees_final_results(Hq, Hkv, d):
+    """The kernels of a call overlap each other; copies queued right behind it are of what all of them have written."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    b = Batch([1200, 30, 64, 5, 500] + [20] * 100, Hq, Hkv, d, BASE_SEED + 35)
+    plan = fa.PackedPlan(b.d_cu, b.rows)
+    o, lse = torch.empty_like(b.d_do), torch.empty(Hq, b.rows, device="cuda")
+    grad = torch.empty_like(b.qkv)
+    ws = torch.empty(fa.fa_bwd_packed_workspace_size(b.rows, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    copies = []
+    for _ in range(12):
+        for t in (o, lse, grad):
+            t.fill_(7.0)
+        fa.fa_fwd_packed(b.d_q, b.d_k, b.d_v, o, lse, plan, True, 0.1)
+        kept = [o.clone(), lse.clone()]
+        fa.fa_bwd_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, grad[:, :Hq], grad[:, Hq:Hq + Hkv], grad[:, Hq + Hkv:], plan,
+                         True, 0.1, ws)
+        copies.append(kept + [grad.clone()])
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == 0
+    for c in copies:
+        for x, y in zip(c, (o, lse, grad)):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_further_apart_than_32_bits(d):
+    """Every tensor a view of one whose rows lie 2^24 elements apart: the last rows are 2^31 elements behind the
+    first and more. The same bits as from tensors of their own."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    Hq, Hkv = 4, 2
+    b = Batch([140, 20, 1], Hq, Hkv, d, BASE_SEED + 36)
+    want = run(b, True, 0.1)
+    wide = torch.empty(b.rows << 24, dtype=torch.bfloat16, device="cuda")
+    place = [0]
+
+    def view(heads):
+        t = wide.as_strided((b.rows, heads, d), (1 << 24, d, 1), place[0])
+        place[0] += heads * d
+        return t
+
+    q, k, v, do, o, dq, dk, dv = (view(h) for h in (Hq, Hkv, Hkv, Hq, Hq, Hq, Hkv, Hkv))
+    for t, x in ((q, b.d_q), (k, b.d_k), (v, b.d_v), (do, b.d_do)):
+        t.copy_(x)
+    plan, lse = fa.PackedPlan(b.d_cu, b.rows), torch.empty(Hq, b.rows, device="cuda")
+    ws = torch.empty(fa.fa_bwd_packed_workspace_size(b.rows, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_packed(q, k, v, o, lse, plan, True, 0.1)
+    fa.fa_bwd_packed(q, k, v, o, lse, do, dq, dk, dv, plan, True, 0.1, ws)
+    assert fa.fa_get_device_status() == 0
+    for x, y in zip((o, lse, dq, dk, dv), (want[0], want[1], *want[2])):
+        assert torch.equal(x, y)
 
 
 def test_two_streams_share_a_plan():
