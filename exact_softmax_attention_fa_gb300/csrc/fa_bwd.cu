@@ -440,7 +440,9 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
     // that a tile takes, 5% of the kernel's time.)
     const int held = RAG ? wk.len(p) - (wk.T - 1) * 128 : 128;
     int until = held < 128 ? wk.nq - 1 : INT_MAX;
-    auto ask = [&](int slot) { tail.ask(sh.tail, held, q_addr + slot * C::TILE_BYTES, do_addr + slot * C::TILE_BYTES); };
+    auto ask = [&](int slot) {
+      tail.ask(sh.tail, held, q_addr + slot * C::TILE_BYTES, do_addr + slot * C::TILE_BYTES);
+    };
     if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) ||
         !mbar_wait(&sh.qdo_full[s0], (g / C::QST) & 1, &sh.abort_flag, lim))
       return fail();
@@ -468,7 +470,8 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
       // dV += P^T dO_n; P^T (bf16) sits in the first half of each warpgroup's columns of region A
       const uint64_t dod = make_smem_desc_sw128(doa, C::CHUNK_BYTES, 1024);
       issue_steps<8, RAG>(steps, [&](int ks) {
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + Warps<HD, RAG>::step_col(ks), desc_add(dod, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + Warps<HD, RAG>::step_col(ks), desc_add(dod, ks * 2048), kIdescAcc,
+                (n > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.pv_done);
       if (has_next) {
@@ -484,9 +487,11 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
       if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
       // dK += dS^T Q_n
-      const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qa, C::CHUNK_BYTES, 1024);
+      const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024);
+      const uint64_t qmn = make_smem_desc_sw128(qa, C::CHUNK_BYTES, 1024);
       issue_steps<8, RAG>(steps, [&](int ks) {
-        umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+        umma_ss(tmem + C::DK_COL, desc_add(dsk, (ks >> 2) * C::CHUNK_BYTES + (ks & 3) * 32), desc_add(qmn, ks * 2048),
+                kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
       });
       if constexpr (DQ) {
         // dQ_n into region B. d = 128: dQ_n^T = K_j^T dS^T (head-dim columns on

@@ -376,7 +376,8 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       // dV half += P^T dO_n[:, h]; P^T (bf16) in columns [0,16) and [32,48) of REG_S
       const uint64_t dod = make_smem_desc_sw128(doh_addr, C::Q_CHUNK, 1024);
       issue_steps<4, RAG>(steps, [&](int ks) {
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048), kIdescAcc,
+                (n > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.pv_done);
       umma_commit(&sh.doh_empty);
@@ -395,7 +396,8 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       const uint32_t qh = qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES;
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qh, C::Q_CHUNK, 1024);
       issue_steps<4, RAG>(steps, [&](int ks) {
-        umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
+        umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc,
+                (n > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.qh_empty[g % C::QH_SLOTS]);
       if constexpr (DQ) {

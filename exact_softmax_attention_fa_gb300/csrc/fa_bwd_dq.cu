@@ -298,7 +298,8 @@ __device__ void dq_mma_role(const BwdLaunch& p, DqShared& sh, uint8_t* sQ, uint8
       // keys 16 ks .. 16 ks + 15 are 8 columns at 64 (ks / 4) + 8 (ks % 4)
       const uint64_t kd = make_smem_desc_sw128(k_addr + s * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
       issue_steps<8, RAG && LAST>(steps, [&](int ks) {
-        umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
+        umma_ts(tmem + C::DQ_COL, tmem + C::s_col(t & 1) + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048),
+                kIdescDq, (j > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.dq_done);
       umma_commit(&sh.k_empty[s]);

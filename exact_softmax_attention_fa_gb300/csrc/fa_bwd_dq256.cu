@@ -273,7 +273,8 @@ __device__ void dq256_mma_role(const BwdLaunch& p, Dq256Shared& sh, uint8_t* sQ,
       tc_fence_after_sync();
       const uint64_t kd = make_smem_desc_sw128(slot_addr(pos), C::CHUNK_BYTES, 1024);
       issue_steps<8, RAG>((held + 15) >> 4, [&](int ks) {
-        umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
+        umma_ts(tmem + C::DQ_COL + 128 * half, tmem + C::DP_COL + (ks >> 2) * 64 + (ks & 3) * 8,
+                desc_add(kd, ks * 2048), kIdescDq, (!first || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.ring_empty[pos % C::RING]);
       umma_commit(&sh.ring_empty[(pos + 1) % C::RING]);

@@ -379,7 +379,8 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
   auto issue_pv = [&](int t, int g, bool first, int steps, auto last_tile) {  // steps: of 16 keys
     const uint64_t vd = make_smem_desc_sw128(v_addr + (g % C::VST) * C::TILE_BYTES, C::CHUNK_BYTES, 1024);
     issue_steps<8, RAG && decltype(last_tile)::value>(steps, [&](int ks) {
-      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV, (!first || ks > 0) ? 1u : 0u);
+      umma_ts(tmem + C::o_col(t), tmem + C::p_col(t) + ks * 8, desc_add(vd, ks * 2048), kIdescPV,
+              (!first || ks > 0) ? 1u : 0u);
     });
     umma_commit(&sh.pv_done[t]);
   };
@@ -826,7 +827,8 @@ __global__ void __launch_bounds__(fwd_threads<RAG>(), 1) fa_fwd_kernel(const __g
   // grid's CTAs leave them (it waits for this grid before it reads). Packed
   // sequences: so may the kernel for the short ones.
   if (RAG || p.splits > 1) griddep_launch_dependents();
-  if (RAG && blockIdx.x == 0 && threadIdx.x == 0 && !packed_plan_ok(p.plan, p.Nq)) record_bad_index(p.status, WHERE_PACKED);
+  if (RAG && blockIdx.x == 0 && threadIdx.x == 0 && !packed_plan_ok(p.plan, p.Nq))
+    record_bad_index(p.status, WHERE_PACKED);
   if (RAG && static_cast<int>(blockIdx.x) >= total_items<PACK, RAG>(p, C::NT)) return;  // nothing in any round
 
   if (threadIdx.x == 0) {
@@ -880,7 +882,9 @@ cudaError_t launch_fwd_t(const FwdLaunch& a, cudaStream_t stream) {
   using C = FwdCfg<HD>;
   auto kern = fa_fwd_kernel<HD, CAUSAL, PACK, RAG>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = RAG ? allow_smem(kern, C::template smem_bytes<RAG>(), a.device, done) : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::template smem_bytes<RAG>());
+  constexpr int smem = C::template smem_bytes<RAG>();
+  cudaError_t e = RAG ? allow_smem(kern, smem, a.device, done)
+                      : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int rph = PACK ? a.rph : 128;
   const int Tq = (a.Nq + rph - 1) / rph;

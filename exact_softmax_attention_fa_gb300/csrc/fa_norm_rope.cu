@@ -16,11 +16,12 @@
 //
 // At B = 2, N = 8192, 16 heads for q, k and v, d = 128: forward 65 us, 6.3 TB/s or
 // 0.92 of the copy rate; backward 100 us, 5.4 TB/s (without weights, whose rows are
-// two instead of three, 63 us and 6.4 TB/s). With the weights' gradients the backward
-// is held up by its instructions (230 for two rows of a warp; it issues in 0.62 of the
+// two instead of three, 71 us, 5.7 TB/s). With the weights' gradients the backward is
+// held up by its instructions (230 for two rows of a warp; it issues in 0.62 of the
 // cycles of 16 warps an SM): one head at a time, its two sums together and a warp's
-// lane groups in step (shuffles of whole warps) took 109 us where two heads at a time
-// through registers took 119; two interleaved heads, which spill, 134; 24 warps 124.
+// lane groups in step (shuffles of whole warps) took 109 us, with L2 flushed, where two
+// heads at a time through registers took 119, two interleaved heads, which spill, 134,
+// and 24 warps 124.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,6 +39,8 @@ constexpr int kFwdThreads = 64;      // 256: 69.3, 128: 67.3 instead of 65.0 us 
 constexpr int kThreads = 256;        // backward
 constexpr int kHeads = 4;            // heads of one token per lane group, forward
 constexpr int kBwdHeads = 8;         // heads of one token per lane group, backward
+constexpr int kBwdSide = 2;          // of them at a time, where they do not come through the ring
+constexpr int kRingUnits = 5;        // units a lane group from which on rows come through the ring
 constexpr int kBwdRing = 6;         // heads on their way to a lane group: 48 KB a block
 constexpr int kBwdPerSm = 2;         // blocks of the backward on an SM
 constexpr int kBwdSmem = kBwdRing * 2 * kThreads * 16;
@@ -226,7 +229,8 @@ struct Place {
   __device__ __forceinline__ void load(const NormRope& p, int token, int n) {
     if constexpr (AXES) {
 #pragma unroll
-      for (int a = 0; a < 4; ++a) pos[a] = a < p.axes ? __ldg(p.positions + static_cast<size_t>(a) * p.tokens + token) : 0;
+      for (int a = 0; a < 4; ++a)
+        pos[a] = a < p.axes ? __ldg(p.positions + static_cast<size_t>(a) * p.tokens + token) : 0;
     } else {
       pos[0] = p.positions ? __ldg(p.positions + token) : n;
     }
@@ -302,13 +306,118 @@ __global__ void __launch_bounds__(kFwdThreads, 16) norm_rope_fwd_kernel(const __
 }
 
 // Persistent: the blocks are shared out over q, k and v by their work, and a
-// lane group takes up to kBwdHeads heads of one token. Its rows come through a ring
-// in shared memory, kBwdRing heads ahead and on into its next unit; the unit's angles
-// are read a unit ahead, its positions two. Each lane sums dw of its 8 columns over
-// the rows it meets; the block's lane groups are added in order, and
-// norm_rope_dw_kernel adds the blocks in order, so dw does not depend on timing.
+// lane group takes up to kBwdHeads heads of one token, two at a time with the
+// next two on their way. Each lane sums dw of its 8 columns over the rows it
+// meets; the block's lane groups are added in order, and norm_rope_dw_kernel
+// adds the blocks in order, so dw does not depend on timing.
 template <int D, bool INTER, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
+  constexpr int GROUPS = kThreads / (D / 8), SIDE = kBwdSide;
+  __shared__ float red[GROUPS][D];
+  griddep_launch_dependents();
+  Lane<D, INTER> L;
+  L.init(p);
+  const int group = threadIdx.x / L.LPR;
+  int block = blockIdx.x, kind = 0;
+  while (block >= p.blocks[kind]) block -= p.blocks[kind++];
+  const int chunks = p.chunks[kind], heads = p.H[kind], n_blocks = p.blocks[kind];
+  const long long units = static_cast<long long>(p.tokens) * chunks;
+  const long long step = static_cast<long long>(p.N) * D, x_step = p.xs[kind][1], d_step = p.ds[kind][1];
+  const bool norm = NORM && kind < 2;
+  float2 dw[4], w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
+  if (norm) L.load_weights(p, kind, w);
+#pragma unroll 1
+  for (long long unit = static_cast<long long>(block) * GROUPS + group; unit < units;
+       unit += static_cast<long long>(n_blocks) * GROUPS) {
+    const int token = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks));
+    const int h0 = (static_cast<int>(unit) - token * chunks) * kBwdHeads, nh = min(kBwdHeads, heads - h0);
+    const int b = token / p.N, n = token - b * p.N;
+    const __nv_bfloat16* gy = p.dy[kind] + (static_cast<size_t>(b) * heads + h0) * step + static_cast<size_t>(n) * D;
+    const __nv_bfloat16* src = norm ? p.x[kind] + b * p.xs[kind][0] + h0 * x_step + n * p.xs[kind][2] : nullptr;
+    __nv_bfloat16* out = p.dx[kind] + b * p.ds[kind][0] + h0 * d_step + n * p.ds[kind][2];
+    uint2 g_raw[SIDE][2], x_raw[SIDE][2];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u)
+        if (h + u < nh) {
+          L.load(gy + (h + u) * step, g_raw[u]);
+          if (norm) L.load(src + (h + u) * x_step, x_raw[u]);
+        }
+    };
+    fetch(0);
+    if (kind < 2 && p.rot > 0) {
+      Place<AXES> at;
+      at.load(p, token, n);
+      if (!take_angles(L, p, at, WHERE_NORM_ROPE_BWD)) continue;
+    }
+#pragma unroll 1
+    for (int h = 0; h < nh; h += SIDE) {
+      uint2 g_now[SIDE][2], x_now[SIDE][2];
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          g_now[u][e] = g_raw[u][e];
+          if (norm) x_now[u][e] = x_raw[u][e];
+        }
+      fetch(h + SIDE);
+#pragma unroll
+      for (int u = 0; u < SIDE; ++u) {
+        if (h + u >= nh) break;
+        __nv_bfloat16* row = out + (h + u) * d_step;
+        if (kind == 2) {
+          L.store(row, g_now[u][0], g_now[u][1]);
+          continue;
+        }
+        Cols g;
+        g.unpack(g_now[u][0], g_now[u][1]);
+        L.template rotate<true>(g);
+        if (NORM) {
+          Cols x, gw;
+          x.unpack(x_now[u][0], x_now[u][1]);
+          float2 ss = fmul2(x.f[0], x.f[0]), hx = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i > 0) ss = fma2(x.f[i], x.f[i], ss);
+            gw.f[i] = fmul2(g.f[i], w[i]);
+            hx = fma2(gw.f[i], x.f[i], hx);
+          }
+          const float r = rsqrtf(L.sum(ss.x + ss.y) * (1.f / D) + p.eps);
+          const float m = -L.sum(hx.x + hx.y) * (1.f / D) * r * r * r;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dw[i] = fma2(fmul2(g.f[i], both(r)), x.f[i], dw[i]);
+            g.f[i] = fma2(gw.f[i], both(r), fmul2(x.f[i], both(m)));
+          }
+        }
+        L.store(row, g.pack(0), g.pack(1));
+      }
+    }
+  }
+  if (norm) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float2*>(&red[group][(i < 2 ? L.a : L.b - 4) + 2 * i]) = dw[i];
+    __syncthreads();
+    for (int col = threadIdx.x; col < D; col += kThreads) {
+      float t = 0.f;
+      for (int g = 0; g < GROUPS; ++g) t += red[g][col];
+      p.part[static_cast<size_t>(blockIdx.x) * D + col] = t;
+    }
+  }
+}
+
+// The same sums in the same order for many units: their rows come through a ring in
+// shared memory, kBwdRing heads ahead and on into the next unit, whose angles are
+// read a unit ahead and its positions two, and a head is worked on at a time. (16
+// heads each of q, k and v, d = 128, us with this kernel and the one above, by tokens:
+// 1024 14.3 and 13.1, 3300 26.8 and 27.0, 4096 32.5 and 33.9, 16384 100 and 111;
+// without weights 3300 13.3 and 12.0, 4096 16.2 and 22.6, 16384 71 and 91. Hence from
+// kRingUnits units a lane group on, which are 4032 of these tokens.)
+template <int D, bool INTER, bool NORM, bool AXES>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_ring_kernel(const __grid_constant__ NormRope p) {
   constexpr int GROUPS = kThreads / (D / 8);
   extern __shared__ uint4 ring[];  // [kBwdRing][dy, x][kThreads]; after the last row [GROUPS][D] floats
   griddep_launch_dependents();
@@ -318,14 +427,16 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
   int block = blockIdx.x, kind = 0;
   while (block >= p.blocks[kind]) block -= p.blocks[kind++];
   const int chunks = p.chunks[kind], heads = p.H[kind];
-  const long long units = static_cast<long long>(p.tokens) * chunks, next = static_cast<long long>(p.blocks[kind]) * GROUPS;
+  const long long units = static_cast<long long>(p.tokens) * chunks;
+  const long long next = static_cast<long long>(p.blocks[kind]) * GROUPS;
   const long long step = static_cast<long long>(p.N) * D, x_step = p.xs[kind][1], d_step = p.ds[kind][1];
   const bool norm = NORM && kind < 2, turn = kind < 2 && p.rot > 0;
-  auto token_of = [&](long long unit) { return static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks)); };
+  auto token_of = [&](long long unit) {
+    return static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks));
+  };
   float2 dw[4], w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
-  if (norm) L.load_weights(p, kind, w);
 
   // The rows on their way: the next one to ask for, and the unit's heads behind it.
   const long long first = static_cast<long long>(block) * GROUPS + group;
@@ -363,22 +474,24 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
     slot += SLOT;
     if (slot == end) slot -= kBwdRing * SLOT;
   };
-  open();
-#pragma unroll 1
-  for (int i = 0; i < kBwdRing; ++i) fetch();
   Place<AXES> at{};
-  Lane<D, INTER> turns = L;  // the next unit's angles
-  bool ok = true;
   auto place = [&](long long unit) {
     if (unit >= units) return;
     const int token = token_of(unit);
     at.load(p, token, token % p.N);
   };
+  Lane<D, INTER> turns = L;  // the next unit's angles
+  bool ok = true;
+  // the first unit's positions are on their way while its rows are asked for
+  if (turn) place(first);
+  open();
+#pragma unroll 1
+  for (int i = 0; i < kBwdRing; ++i) fetch();
   if (turn && first < units) {
-    place(first);
     ok = take_angles(turns, p, at, WHERE_NORM_ROPE_BWD);
     place(first + next);
   }
+  if (norm) L.load_weights(p, kind, w);
   // A warp's groups go round together, so that its shuffles take whole warps: a
   // group that has no row left, or no angles, goes on and leaves its result.
   const long long warp_first = first - (threadIdx.x % 32) / L.LPR;
@@ -487,13 +600,22 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
   }
 }
 
+template <int D, bool INTER, bool NORM, bool AXES>
+void launch_bwd(const NormRope& a, int blocks, cudaStream_t stream) {
+  const long long units = static_cast<long long>(a.tokens) * (a.chunks[0] + a.chunks[1] + a.chunks[2]);
+  if (units < static_cast<long long>(kRingUnits) * blocks * (kThreads / (D / 8)))
+    norm_rope_bwd_kernel<D, INTER, NORM, AXES><<<blocks, kThreads, 0, stream>>>(a);
+  else
+    norm_rope_bwd_ring_kernel<D, INTER, NORM, AXES><<<blocks, kThreads, kBwdSmem, stream>>>(a);
+}
+
 template <bool BACK, int D, bool INTER, bool NORM>
 cudaError_t launch_norm_rope_t(const NormRope& a, int blocks, cudaStream_t stream) {
   if (a.axes) {
-    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, true><<<blocks, kThreads, kBwdSmem, stream>>>(a);
+    if constexpr (BACK) launch_bwd<D, INTER, NORM, true>(a, blocks, stream);
     else norm_rope_fwd_kernel<D, INTER, NORM, true><<<blocks, kFwdThreads, 0, stream>>>(a);
   } else {
-    if constexpr (BACK) norm_rope_bwd_kernel<D, INTER, NORM, false><<<blocks, kThreads, kBwdSmem, stream>>>(a);
+    if constexpr (BACK) launch_bwd<D, INTER, NORM, false>(a, blocks, stream);
     else norm_rope_fwd_kernel<D, INTER, NORM, false><<<blocks, kFwdThreads, 0, stream>>>(a);
   }
   return cudaGetLastError();

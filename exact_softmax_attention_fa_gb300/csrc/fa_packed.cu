@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
     list0[(list ? pairs_at : 0) + at] = make_int4(row0, n, index, 0);
   });
   if (tid == 0)
-    *plan = PackedPlan{kPackedMagic, rows, count[0], count[1], sh.n_short, pairs_at, longest, B > 0 ? cu[0] : 0, B > 0 ? cu[B] : 0,
-                       sh.causal, sh.full};
+    *plan = PackedPlan{kPackedMagic, rows,    count[0],            count[1],            sh.n_short,
+                       pairs_at,     longest, B > 0 ? cu[0] : 0,   B > 0 ? cu[B] : 0,   sh.causal,
+                       sh.full};
 }
 
 // ---------------------------------------------------------------------------

@@ -35,6 +35,11 @@ CASES = [  # B, Hq, Hkv, N, d, the axis of each pair, interleaved, weights
     (2, 20, 3, 97, 64, [i % 3 for i in range(32)], False, "float32"),
     (1, 13, 11, 600, 64, blocks(10, 22), True, "bfloat16"),
     (3, 20, 9, 203, 128, blocks(64), False, "float32"),
+    # five units and more for each of the lane groups of 304 blocks: the backward's ring
+    (1, 1, 1, 4100, 256, blocks(1, 127), True, "float32"),
+    (2, 1, 1, 4100, 128, [i % 3 for i in range(64)], False, "bfloat16"),
+    (1, 20, 3, 9800, 64, [i % 2 for i in range(24)], False, "float32"),
+    (1, 1, 1, 8200, 128, blocks(20, 44), False, None),
 ]
 
 
@@ -144,6 +149,43 @@ def test_a_position_outside_the_tables_on_any_axis(axis, bad):
     fa.fa_norm_rope_axes_bwd(q, k, v, None, None, None, None, cos, sin, pos, axes, *out, None, None, None)
     assert fa.fa_get_device_status_detail()[:2] == (FA_ERR_INDEX, 22)
     assert (out[0][1, :, 4] == 7).all() and (out[1][1, :, 4] == 7).all()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_a_position_outside_the_tables_among_many(norm):
+    """As above in the backward for many units: the other tokens' gradients stay, the weights' sums leave it out."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    N, d, axes = 4100, 256, bytes([i % 2 for i in range(128)])
+    x, _ = nr.packed(1, N, 3, d, BASE_SEED + 420)
+    dy, _ = nr.packed(1, N, 3, d, BASE_SEED + 421, 1.0)
+    cos, sin, _, _ = nr.tables(ROWS, d)
+    pos = torch.randint(0, ROWS, (2, 1, N), dtype=torch.int32, device="cuda")
+    (wq, _), (wk, _) = nr.weights(d, 3, torch.float32), nr.weights(d, 4, torch.float32)
+    bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+    bad[[0, 1, 700, 2431, 2432, 4099]] = True
+
+    def run(dy, pos):
+        g = [t.contiguous() for t in nr.split(dy, 1, 1)]
+        out = [torch.full_like(t, 7.0) for t in g]
+        q, k, _ = nr.split(x, 1, 1)
+        *_, dwq, dwk = fa.norm_rope_backward(*g, q if norm else None, k if norm else None, wq if norm else None,
+                                             wk if norm else None, cos, sin, pos, out, axes=axes)
+        return out, dwq, dwk
+
+    zeroed = dy.clone()
+    nr.split(zeroed, 1, 1)[0][0, 0, bad] = 0  # tokens whose gradient is nothing add nothing
+    nr.split(zeroed, 1, 1)[1][0, 0, bad] = 0
+    want, dwq, dwk = run(zeroed, pos)
+    assert fa.fa_get_device_status() == 0
+    pos[1, 0, bad] = ROWS
+    got, bad_q, bad_k = run(dy, pos)
+    assert fa.fa_get_device_status_detail()[:2] == (FA_ERR_INDEX, 22)
+    for t in range(2):
+        assert (got[t][0, 0, bad] == 7).all() and torch.equal(got[t][0, 0, ~bad], want[t][0, 0, ~bad])
+    assert torch.equal(got[2], nr.split(dy, 1, 1)[2])
+    if norm:
+        assert torch.equal(bad_q, dwq) and torch.equal(bad_k, dwk)
 
 
 def test_binding_refuses():
