@@ -998,6 +998,7 @@ cudaError_t launch_bwd_pre(const BwdLaunch& a, cudaStream_t stream) {
 cudaError_t launch_bwd_main(const BwdLaunch& a, cudaStream_t stream) {
   if (a.plan && a.d == 64)
     return a.causal ? launch_main_t<64, true, false, true>(a, stream) : launch_main_t<64, false, false, true>(a, stream);
+  if (a.plan && a.d == 256) return launch_bwd_main_ragged256(a, stream);
   if (a.plan && a.d == 128)
     return a.causal ? launch_main_t<128, true, false, true>(a, stream) : launch_main_t<128, false, false, true>(a, stream);
   switch (a.d) {

@@ -43,13 +43,10 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
-#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
-#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -58,11 +55,6 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kLoadWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
-template <bool RAG>
-constexpr int kernel_threads() {
-  return RAG ? kThreads + 32 : kThreads;
-}
 constexpr int kItemConsumers = 1 + 256;  // the MMA thread and the softmax threads
 
 struct Cfg256 {
@@ -87,7 +79,6 @@ struct Shared256 {
   uint64_t qo_full, qo_empty;        // Q_i, the other half
   uint64_t doh_full, doh_empty;      // dO_i[:, h]
   uint64_t doo_full, doo_empty;      // dO_i, the other half
-  TailShared tail;  // packed sequences
   uint64_t s_full, dp_full, pa_ready, ds_ready, pv_done, acc_done, acc_free;
   uint64_t dq_full[2], dq_free[2];   // dQ^T buffer n & 1
   uint64_t mma_drain;                // the MMA thread's last commit: all its MMAs done before the CTA exits
@@ -102,13 +93,10 @@ struct Shared256 {
 // (query head bh*g + t), the 64-row query tiles i0 .. T64-1 (causal:
 // i0 = 2j). Causal items are numbered most-work-first; the two halves of a
 // key tile are adjacent (they read the same query stream).
-template <bool CAUSAL, bool RAG>
+template <bool CAUSAL>
 struct Work256 {
   int bh, j, h, i0, T64, g;
-  static constexpr int row0 = 0;  // the sequence's first row
-  __device__ __forceinline__ int len(const BwdLaunch& p) const { return p.N; }
-  __device__ Work256(int item, const BwdLaunch& p) {
-    const int BHkv = p.BHkv, N = p.N, group = p.group;
+  __device__ Work256(int item, int BHkv, int N, int group) {
     const int T = (N + 127) / 128;
     T64 = (N + 63) / 64;
     if (CAUSAL) {
@@ -138,46 +126,7 @@ struct Work256 {
   }
 };
 
-// The same over packed sequences: an entry of the plan's list is a sequence's
-// key tile j, both halves of every K/V head of it items.
-template <bool CAUSAL>
-struct Work256<CAUSAL, true> {
-  int bh, j, h, i0, T64, g, row0, n;
-  __device__ __forceinline__ int len(const BwdLaunch&) const { return n; }
-  __device__ Work256(int item, const BwdLaunch& p) {
-    const uint32_t units = 2 * p.BHkv;
-    const int e = static_cast<int>(static_cast<uint32_t>(item) / units);
-    const int rem = item - e * static_cast<int>(units);
-    const int4 x = __ldg(packed_tiles(p.plan) + e);
-    row0 = x.x;
-    n = x.y;
-    T64 = (n + 63) >> 6;
-    j = CAUSAL ? ((n + 127) >> 7) - 1 - x.z : x.z;
-    bh = rem >> 1;
-    h = rem & 1;
-    i0 = CAUSAL ? 2 * j : 0;
-    g = p.group;
-  }
-  __device__ int n_iter() const { return g * (T64 - i0); }
-  struct Pos {
-    int bh, i;
-  };
-  __device__ Pos first() const { return Pos{bh * g, i0}; }
-  __device__ void advance(Pos& p) const {
-    if (++p.i == T64) {
-      p.i = i0;
-      ++p.bh;
-    }
-  }
-};
-
-template <bool RAG>
-__device__ __forceinline__ int total_items256(const BwdLaunch& p) {
-  if constexpr (RAG)
-    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BHkv * 2 : 0;
-  else
-    return p.BHkv * ((p.N + 127) / 128) * 2;
-}
+__device__ __forceinline__ int total_items256(const BwdLaunch& p) { return p.BHkv * ((p.N + 127) / 128) * 2; }
 
 // Smem address of chunk c (0..3, 64 columns of the head dimension) of a
 // query tile's Q (or dO) for an item of half h: in the h half's slot or in
@@ -189,7 +138,7 @@ __device__ __forceinline__ uint32_t half_chunk(uint32_t h_slot, uint32_t o_slot,
 // TMA producer (one thread). Per query tile: Q's h half, Q's other half,
 // dO's other half, dO's h half (the order in which their slots free up);
 // per item K_j and V_j once every MMA of the previous item has completed.
-template <bool CAUSAL, bool RAG>
+template <bool CAUSAL>
 __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQh, uint8_t* sQo,
                           uint8_t* sDOh, uint8_t* sDOo) {
   using C = Cfg256;
@@ -197,49 +146,48 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
   tma_prefetch_desc(&p.tmK);
   tma_prefetch_desc(&p.tmV);
   tma_prefetch_desc(&p.tmdO);
-  const int total = total_items256<RAG>(p);
+  const int total = total_items256(p);
   const uint64_t lim = p.wait_limit_ns;
   int g = 0, items = 0, kv_issued = 0;
   int issued = 0;  // query tiles whose four half tiles were all issued
   int parts = 0;   // half tiles of tile `issued` issued before an abort (0..3)
   bool aborted = false;
   // the two 64-column chunks of half `half` of a 64-row tile of `map`
-  auto load_half = [&](uint64_t* bar, uint8_t* dst, const CUtensorMap* map, int half, int row, int bh) {
+  auto load_half = [&](uint64_t* bar, uint8_t* dst, const CUtensorMap* map, int half, int i, int bh) {
     mbar_arrive_expect_tx(bar, C::HALF_BYTES);
-    tma_load_3d(dst, map, bar, 128 * half, row, bh);
-    tma_load_3d(dst + C::Q_CHUNK, map, bar, 128 * half + 64, row, bh);
+    tma_load_3d(dst, map, bar, 128 * half, i * C::BQ, bh);
+    tma_load_3d(dst + C::Q_CHUNK, map, bar, 128 * half + 64, i * C::BQ, bh);
   };
-  auto load_tile = [&](int n, const typename Work256<CAUSAL, RAG>::Pos& pos, int h, int row0) -> bool {
-    const int row = row0 + pos.i * C::BQ;
+  auto load_tile = [&](int n, const typename Work256<CAUSAL>::Pos& pos, int h) -> bool {
     const int s = n % C::QH_SLOTS;
     parts = 0;
     if (n >= C::QH_SLOTS && !mbar_wait(&sh.qh_empty[s], ((n / C::QH_SLOTS) - 1) & 1, &sh.abort_flag, lim))
       return false;
-    load_half(&sh.qh_full[s], sQh + s * C::HALF_BYTES, &p.tmQ, h, row, pos.bh);
+    load_half(&sh.qh_full[s], sQh + s * C::HALF_BYTES, &p.tmQ, h, pos.i, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.qo_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.qo_full, sQo, &p.tmQ, 1 - h, row, pos.bh);
+    load_half(&sh.qo_full, sQo, &p.tmQ, 1 - h, pos.i, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.doo_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.doo_full, sDOo, &p.tmdO, 1 - h, row, pos.bh);
+    load_half(&sh.doo_full, sDOo, &p.tmdO, 1 - h, pos.i, pos.bh);
     ++parts;
     if (n > 0 && !mbar_wait(&sh.doh_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load_half(&sh.doh_full, sDOh, &p.tmdO, h, row, pos.bh);
+    load_half(&sh.doh_full, sDOh, &p.tmdO, h, pos.i, pos.bh);
     parts = 0;
     ++issued;
     return true;
   };
-  int item = blockIdx.x;
+  int item = blockIdx.x;  // the grid never exceeds the item count
   while (!aborted) {
     if (!publish_item(sh, items, item, lim)) {
       aborted = true;
       break;
     }
     if (item >= total) break;
-    const Work256<CAUSAL, RAG> wk(item, p);
+    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
     const int n_iter = wk.n_iter();
-    typename Work256<CAUSAL, RAG>::Pos pos = wk.first();
-    if (!load_tile(g, pos, wk.h, wk.row0)) {
+    typename Work256<CAUSAL>::Pos pos = wk.first();
+    if (!load_tile(g, pos, wk.h)) {
       aborted = true;
       break;
     }
@@ -252,14 +200,14 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
       mbar_arrive_expect_tx(&sh.kv_full, 2 * C::KV_BYTES);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        tma_load_3d(sK + c * C::KV_CHUNK, &p.tmK, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
-        tma_load_3d(sV + c * C::KV_CHUNK, &p.tmV, &sh.kv_full, c * 64, wk.row0 + wk.j * 128, wk.bh);
+        tma_load_3d(sK + c * C::KV_CHUNK, &p.tmK, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
+        tma_load_3d(sV + c * C::KV_CHUNK, &p.tmV, &sh.kv_full, c * 64, wk.j * 128, wk.bh);
       }
       ++kv_issued;
     }
     for (int n = 1; n < n_iter; ++n) {
       wk.advance(pos);
-      if (!load_tile(g + n, pos, wk.h, wk.row0)) {
+      if (!load_tile(g + n, pos, wk.h)) {
         aborted = true;
         break;
       }
@@ -289,7 +237,7 @@ __device__ void load_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_
 }
 
 // One thread issues every MMA (order in the file header).
-template <bool CAUSAL, bool DQ, bool RAG>
+template <bool CAUSAL, bool DQ>
 __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t* sV, uint8_t* sQh, uint8_t* sQo,
                          uint8_t* sDOh, uint8_t* sDOo, uint8_t* sDS, uint32_t tmem) {
   using C = Cfg256;
@@ -299,7 +247,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
   const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV), qh_addr = smem_u32(sQh), qo_addr = smem_u32(sQo),
                  doh_addr = smem_u32(sDOh), doo_addr = smem_u32(sDOo), ds_addr = smem_u32(sDS);
   const uint64_t lim = p.wait_limit_ns;
-  const int total = total_items256<RAG>(p);
+  const int total = total_items256(p);
   auto fail = [&]() {
     record_timeout(p.status, &sh.abort_flag, WHERE_BWD_MMA);
     drain_mmas(&sh.mma_drain, lim);
@@ -336,38 +284,26 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
   };
 
   int g = 0, items = 0;
-  TailCalls<false> tail;
   while (true) {
     const int item = take_item(sh, items, lim);
     if (item < 0) return fail();
     if (item >= total) break;
-    const Work256<CAUSAL, RAG> wk(item, p);
+    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
     const int n_iter = wk.n_iter();
     const int h = wk.h;
-    // Packed sequences: as in fa_bwd.cu, steps of 16 queries that a product over the
-    // last query tile takes, and tiles of the stream until the next such tile.
-    const int held = RAG ? wk.len(p) - (wk.T64 - 1) * C::BQ : C::BQ;
-    int until = held < C::BQ ? wk.T64 - 1 - wk.i0 : INT_MAX;
-    auto clean = [&](uint32_t half_tile) -> bool {
-      tail.ask(sh.tail, held, half_tile);
-      return tail.wait(sh.tail, &sh.abort_flag, lim);
-    };
     if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) || !wait_s_operands(g)) return fail();
     // S^T overwrites the previous item's last P^T: dV must have read it.
     if (g > 0 && !mbar_wait(&sh.pv_done, (g - 1) & 1, &sh.abort_flag, lim)) return fail();
     tc_fence_after_sync();
-    if (RAG && until == 0 && !clean(qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES)) return fail();
     issue_s(g, h);
     // dP^T overwrites the previous item's last dP^T, which phase B read
     // before ds_ready (waited for in the previous item's last step).
     if (!wait_dp_operands(g)) return fail();
-    if (RAG && until == 0 && !clean(doh_addr)) return fail();
     tc_fence_after_sync();
     issue_dp(h);
 
     for (int n = 0; n < n_iter; ++n, ++g) {
       const bool has_next = n + 1 < n_iter;
-      const int steps = RAG && until == 0 ? (held + 15) >> 4 : 4;
       if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
       // the first dV / dK of an item overwrite the accumulators: the previous
       // item's epilogue must have read them
@@ -375,19 +311,16 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       tc_fence_after_sync();
       // dV half += P^T dO_n[:, h]; P^T (bf16) in columns [0,16) and [32,48) of REG_S
       const uint64_t dod = make_smem_desc_sw128(doh_addr, C::Q_CHUNK, 1024);
-      issue_steps<4, RAG>(steps, [&](int ks) {
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048), kIdescAcc,
-                (n > 0 || ks > 0) ? 1u : 0u);
-      });
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_S + (ks >> 1) * 32 + (ks & 1) * 8, desc_add(dod, ks * 2048),
+                kIdescAcc, (n > 0 || ks > 0) ? 1u : 0u);
       umma_commit(&sh.pv_done);
       umma_commit(&sh.doh_empty);
       if (has_next) {
         // S^T(n+1) overwrites P^T(n): wait until dV(n) has read it.
         if (!wait_s_operands(g + 1) || !mbar_wait(&sh.pv_done, g & 1, &sh.abort_flag, lim)) return fail();
         tc_fence_after_sync();
-        if (RAG && (until == 0 ? until = wk.T64 - 1 - wk.i0 : --until) == 0 &&
-            !clean(qh_addr + ((g + 1) % C::QH_SLOTS) * C::HALF_BYTES))
-          return fail();
         issue_s(g + 1, h);
       }
       if (!mbar_wait(&sh.ds_ready, g & 1, &sh.abort_flag, lim)) return fail();
@@ -395,10 +328,10 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       // dK half += dS^T Q_n[:, h]
       const uint32_t qh = qh_addr + (g % C::QH_SLOTS) * C::HALF_BYTES;
       const uint64_t dsk = make_smem_desc_sw128(ds_addr, 16, 1024), qmn = make_smem_desc_sw128(qh, C::Q_CHUNK, 1024);
-      issue_steps<4, RAG>(steps, [&](int ks) {
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
         umma_ss(tmem + C::DK_COL, desc_add(dsk, ks * 32), desc_add(qmn, ks * 2048), kIdescAcc,
                 (n > 0 || ks > 0) ? 1u : 0u);
-      });
       umma_commit(&sh.qh_empty[g % C::QH_SLOTS]);
       if constexpr (DQ) {
         // dQ_n^T half = K_j[:, h]^T dS^T into buffer g & 1, once the drain of
@@ -416,7 +349,6 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
       if (has_next) {
         // dP^T(n+1): phase B(n) has read dP^T(n) (ds_ready above)
         if (!wait_dp_operands(g + 1)) return fail();
-        if (RAG && until == 0 && !clean(doh_addr)) return fail();
         tc_fence_after_sync();
         issue_dp(h);
       }
@@ -426,7 +358,6 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
   }
   // Normally the epilogues have waited for the last products; if a softmax
   // warpgroup gave up, nothing has.
-  if (RAG) tail.finish(sh.tail);
   drain_mmas(&sh.mma_drain, lim);
 }
 
@@ -435,7 +366,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared256& sh, uint8_t* sK, uint8_t
 // 128h + r in the dQ drain. Order per tile n: B(n), A(n+1), drain(n). After
 // an item's last tile warpgroup 0 writes its dK half and warpgroup 1 its dV
 // half straight from TMEM.
-template <bool CAUSAL, bool DQ, bool RAG>
+template <bool CAUSAL, bool DQ>
 __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, float* sLD, uint32_t tmem, int w) {
   using C = Cfg256;
   const int r = threadIdx.x & 127;
@@ -448,21 +379,12 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   const uint32_t bar_id = 1 + w;
   const uint32_t tA = tmem + lane_base + C::REG_S + 32 * w;
   const uint32_t tB = tmem + lane_base + C::REG_DP + 32 * w;
-  const int total = total_items256<RAG>(p);
+  const int total = total_items256(p);
   bool alive = true;
-  // P^T of the current tile (bf16 pairs, as written to TMEM: dS uses the same rounding;
-  // over packed sequences fp32, three of up to 2501 rows 610 us, by pairs 627)
-  Weights<32, RAG, RAG ? 32 : 0> pk;
+  uint32_t pk[16];  // P^T of the current tile (bf16 pairs, as written to TMEM): dS uses the same rounding
 
   // thread r < 32 loads L2 of query 32w + r of the tile, 32 <= r < 64 its scaled D
-  // Queries behind a packed sequence's last one get L2 = +inf (weight 0) and D = 0.
-  auto fetch_ld = [&](const Work256<CAUSAL, RAG>& wk, int bh, int i) -> float {
-    if constexpr (RAG) {
-      const int q = i * C::BQ + 32 * w + (r & 31);
-      const float* from = (r < 32 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
-      const float x = __ldg(from + min(q, wk.n - 1));
-      return r < 32 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
-    }
+  auto fetch_ld = [&](int bh, int i) -> float {
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * C::BQ + 32 * w;
     if (r < 32) return __ldg(p.lse2 + row + r);
     if (r < 64) return __ldg(p.D + row + (r - 32)) * sc;
@@ -475,7 +397,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   };
 
   // ---- phase A of query tile i (global tile g): P^T -> TMEM (bf16)
-  auto phase_a = [&](const Work256<CAUSAL, RAG>& wk, int i, int g) {
+  auto phase_a = [&](const Work256<CAUSAL>& wk, int i, int g) {
     wait_all(&sh.s_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t a[32];
@@ -484,7 +406,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     // key 128j + r is seen by query 64i + 32w + c if it exists and (causal)
     // is not after the query: c >= c_lo
     const int key = wk.j * 128 + r;
-    const bool key_valid = RAG || key < wk.len(p);  // see fa_bwd.cu
+    const bool key_valid = key < p.N;
     const int c_lo = CAUSAL ? key - i * C::BQ - 32 * w : 0;
     float pv[32];
 #pragma unroll
@@ -499,32 +421,21 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) pv[c] = ex2_approx(pv[c]);
-    if (!key_valid || (CAUSAL && c_lo > 0) || (RAG && i == wk.T64 - 1)) {
-      // queries of this warpgroup's half that the sequence has (S of those behind may be anything)
-      const int c_hi = RAG ? wk.len(p) - i * C::BQ - 32 * w : 32;
+    if (!key_valid || (CAUSAL && c_lo > 0)) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (!key_valid || c < c_lo || (RAG && c >= c_hi)) pv[c] = 0.f;
+        if (!key_valid || c < c_lo) pv[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) pk.put(c, pv[c], pv[c + 1]);
-    if constexpr (RAG) {
-      uint32_t pb[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
-      tmem_st16(tA, pb);
-    } else {
-      tmem_st16(tA, pk.two);  // columns [32w, 32w + 16): already read
-    }
+    for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
+    tmem_st16(tA, pk);  // columns [32w, 32w + 16): already read
     tmem_st_wait();
     tc_fence_before_sync();
     mbar_arrive(&sh.pa_ready);
   };
 
   // ---- phase B: dS^T = P^T o (dP^T - D) * scale -> smem row r, queries [32w, 32w + 32)
-  // CUT: a packed sequence's last query tile. (One test a tile, around the whole
-  // phase: inside it keeps the compiler from overlapping the TMEM loads.)
-  auto phase_b = [&](const Work256<CAUSAL, RAG>& wk, int i, int g, auto cut) {
+  auto phase_b = [&](int g) {
     wait_all(&sh.dp_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t dpv[32];
@@ -534,20 +445,14 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 #pragma unroll
     for (int c4 = 0; c4 < 32; c4 += 4) {
       const float4 dd = *reinterpret_cast<const float4*>(ld_d + c4);
-      const float2 p01 = pk.get(c4);
-      const float2 p23 = pk.get(c4 + 2);
+      const float2 p01 = unpack_bf16x2(pk[c4 / 2]);
+      const float2 p23 = unpack_bf16x2(pk[c4 / 2 + 1]);
       const float2 g01 = ffma2_bcast_mul(__uint_as_float(dpv[c4]), __uint_as_float(dpv[c4 + 1]), sc, -dd.x, -dd.y);
       const float2 g23 = ffma2_bcast_mul(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dd.z, -dd.w);
       const float2 ds01 = fmul2(p01, g01);
       const float2 ds23 = fmul2(p23, g23);
       dk[c4 / 2] = pack_bf16x2(ds01.x, ds01.y);
       dk[c4 / 2 + 1] = pack_bf16x2(ds23.x, ds23.y);
-    }
-    if constexpr (decltype(cut)::value) {
-      // dP of queries behind the sequence's last may be infinite or NaN
-      const int held = wk.len(p) - i * C::BQ - 32 * w;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) dk[c] &= (2 * c < held ? 0xFFFFu : 0u) | (2 * c + 1 < held ? 0xFFFF0000u : 0u);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -576,18 +481,12 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
 
   // ---- item epilogue: w = 0 writes the dK half, w = 1 the dV half; thread r
   // writes key row r (rows past N are skipped)
-  auto epilogue = [&](const Work256<CAUSAL, RAG>& wk, int items) {
+  auto epilogue = [&](const Work256<CAUSAL>& wk, int items) {
     wait_all(&sh.acc_done, items & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     const int key = wk.j * 128 + r;
     const uint32_t t = tmem + lane_base + (w == 0 ? C::DK_COL : C::DV_COL);
-    __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv) + 128 * wk.h;
-    if constexpr (RAG) {
-      const long long* st = w == 0 ? p.dk_strides : p.dv_strides;
-      dst += static_cast<long long>(wk.row0 + key) * st[0] + wk.bh * st[1];
-    } else {
-      dst += (static_cast<size_t>(wk.bh) * p.N + key) * C::HD;
-    }
+    __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv) + (static_cast<size_t>(wk.bh) * p.N + key) * C::HD + 128 * wk.h;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
       uint32_t v[32];
@@ -597,7 +496,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
         tc_fence_before_sync();
         mbar_arrive(&sh.acc_free);
       }
-      if (key < wk.len(p)) {
+      if (key < p.N) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           *reinterpret_cast<uint4*>(dst + c + 8 * u) =
@@ -624,27 +523,24 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   int item = next_item(0);
   float ld = 0.f;
   if (item < total) {
-    const Work256<CAUSAL, RAG> wk0(item, p);
-    const typename Work256<CAUSAL, RAG>::Pos f0 = wk0.first();
-    ld = fetch_ld(wk0, f0.bh, f0.i);
+    const Work256<CAUSAL> wk0(item, p.BHkv, p.N, p.group);
+    const typename Work256<CAUSAL>::Pos f0 = wk0.first();
+    ld = fetch_ld(f0.bh, f0.i);
   }
   while (item < total) {
-    const Work256<CAUSAL, RAG> wk(item, p);
+    const Work256<CAUSAL> wk(item, p.BHkv, p.N, p.group);
     const int n_iter = wk.n_iter();
     if (items > 0) named_barrier_sync(bar_id, 128);  // the previous item's L2 / D reads are done
     if (r < 64) sLD[w * 64 + r] = ld;
     named_barrier_sync(bar_id, 128);
-    typename Work256<CAUSAL, RAG>::Pos cur = wk.first();
+    typename Work256<CAUSAL>::Pos cur = wk.first();
     phase_a(wk, cur.i, g);
     for (int n = 0; n < n_iter; ++n) {
       const bool has_next = n + 1 < n_iter;
-      typename Work256<CAUSAL, RAG>::Pos nxt = cur;
+      typename Work256<CAUSAL>::Pos nxt = cur;
       wk.advance(nxt);
-      const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
-      if (RAG && cur.i == wk.T64 - 1)
-        phase_b(wk, cur.i, g + n, std::bool_constant<RAG>());
-      else
-        phase_b(wk, cur.i, g + n, std::false_type());
+      const float next_ld = has_next ? fetch_ld(nxt.bh, nxt.i) : 0.f;  // lands during phase B
+      phase_b(g + n);
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         if (r < 64) sLD[w * 64 + r] = next_ld;
@@ -656,9 +552,9 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
     }
     const int item_next = next_item(items + 1);
     if (item_next < total) {
-      const Work256<CAUSAL, RAG> wk1(item_next, p);
-      const typename Work256<CAUSAL, RAG>::Pos f1 = wk1.first();
-      ld = fetch_ld(wk1, f1.bh, f1.i);  // lands during the epilogue
+      const Work256<CAUSAL> wk1(item_next, p.BHkv, p.N, p.group);
+      const typename Work256<CAUSAL>::Pos f1 = wk1.first();
+      ld = fetch_ld(f1.bh, f1.i);  // lands during the epilogue
     }
     epilogue(wk, items);
     g += n_iter;
@@ -667,8 +563,8 @@ __device__ void softmax_role(const BwdLaunch& p, Shared256& sh, uint8_t* sDS, fl
   }
 }
 
-template <bool CAUSAL, bool DQ, bool RAG>
-__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(const __grid_constant__ BwdLaunch p) {
+template <bool CAUSAL, bool DQ>
+__global__ void __launch_bounds__(kThreads, 1) fa_bwd256_kernel(const __grid_constant__ BwdLaunch p) {
   using C = Cfg256;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ Shared256 sh;
@@ -684,11 +580,7 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
   const int warp = threadIdx.x >> 5;
   // Without dQ this pass writes nothing the dQ kernel reads, so a dQ kernel
   // queued behind it may take SMs as soon as this grid's CTAs leave them.
-  // (Packed sequences: this grid is itself launched to overlap the end of the one
-  // that forms D and L, and lets the next one start only when that is complete.)
-  if (RAG) griddep_wait();
   if constexpr (!DQ) griddep_launch_dependents();
-  if (RAG && static_cast<int>(blockIdx.x) >= total_items256<RAG>(p)) return;  // no item is left for this CTA
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.kv_full, 1);
@@ -713,7 +605,6 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
-    if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
@@ -732,13 +623,11 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
   const uint32_t tmem = sh.tmem_base;
 
   if (warp == kLoadWarp) {
-    if (lane_id() == 0) load_role<CAUSAL, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo);
+    if (lane_id() == 0) load_role<CAUSAL>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo);
   } else if (warp == kMmaWarp) {
-    if (lane_id() == 0) mma_role<CAUSAL, DQ, RAG>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
-  } else if (RAG && warp == kTailWarp) {
-    tail_role<2, C::Q_CHUNK>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
+    if (lane_id() == 0) mma_role<CAUSAL, DQ>(p, sh, sK, sV, sQh, sQo, sDOh, sDOo, sDS, tmem);
   } else {
-    softmax_role<CAUSAL, DQ, RAG>(p, sh, sDS, sLD, tmem, warp >> 2);
+    softmax_role<CAUSAL, DQ>(p, sh, sDS, sLD, tmem, warp >> 2);
   }
 
   tc_fence_before_sync();
@@ -747,34 +636,21 @@ __global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd256_kernel(con
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <bool CAUSAL, bool DQ, bool RAG = false>
+template <bool CAUSAL, bool DQ>
 cudaError_t launch_t(const BwdLaunch& a, cudaStream_t stream) {
-  auto kern = fa_bwd256_kernel<CAUSAL, DQ, RAG>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = RAG ? allow_smem(kern, Cfg256::SMEM_BYTES, a.device, done)
-                      : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg256::SMEM_BYTES);
+  auto kern = fa_bwd256_kernel<CAUSAL, DQ>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg256::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  // Packed sequences: the plan, on the device, knows how many items there are.
-  const long long items = static_cast<long long>(a.BHkv) * (RAG ? a.N : (a.N + 127) / 128) * 2;
+  const long long items = static_cast<long long>(a.BHkv) * ((a.N + 127) / 128) * 2;
   // Persistent: one CTA per SM (the smem footprint allows no more).
   const long long grid = items < a.num_sms ? items : a.num_sms;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kernel_threads<RAG>());
-  cfg.dynamicSmemBytes = Cfg256::SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = RAG ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  kern<<<static_cast<unsigned>(grid), kThreads, Cfg256::SMEM_BYTES, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_main_d256(const BwdLaunch& a, cudaStream_t stream) {
-  if (a.plan) return a.causal ? launch_t<true, false, true>(a, stream) : launch_t<false, false, true>(a, stream);
   if (a.deterministic)
     return a.causal ? launch_t<true, false>(a, stream) : launch_t<false, false>(a, stream);
   return a.causal ? launch_t<true, true>(a, stream) : launch_t<false, true>(a, stream);
