@@ -7,12 +7,13 @@
 // item both, three products of 64 queries a tile instead of four, and three phases
 // of the softmax warps instead of four.
 //   - K_j and (dK items) V_j stay in shared memory for the item, 64 KB each. Query
-//     tiles of 64 rows stream through two slots of Q and one of dO (32 KB each). That
-//     leaves no room for dS^T, which goes to TMEM as the A operand of dK += dS^T Q, as
-//     P^T does for dV += P^T dO.
+//     tiles of 64 rows stream through two slots of Q and one of dO (32 KB each), for
+//     dV items two of dO: the second is V_j's place (with one, each tile waited for
+//     its dO, and a dV item took longer than a dK item). That leaves no room for dS^T,
+//     which goes to TMEM as the A operand of dK += dS^T Q, as P^T does for dV += P^T dO.
 //   - P stays in registers in fp32 between the phases of a dK item.
 //   - MMA order per query tile n: S^T(n+1) once phase A(n) has S^T(n) in registers;
-//     dV(n), or dK(n) after phase B(n) and then dP^T(n+1). A commit covers all that
+//     dV(n) after phase A(n), or dK(n) after phase B(n) and then dP^T(n+1). A commit covers all that
 //     was issued before it: s_full(n) says that dV(n-2) has read its P^T, dp_full(n)
 //     that dK(n-1) has read its dS^T.
 // Three sequences of up to 2501 rows, 8 + 2 heads, no mask: TIME1 us with its dQ kernel
@@ -58,10 +59,15 @@ struct Cfg {
 struct Shared {
   uint64_t kv_full;
   uint64_t q_full[2], q_empty[2];  // slot n % 2
-  uint64_t do_full, do_empty;
+  uint64_t do_full[2], do_empty[2];  // dO: slot n % 2 of a dV item's tile n, slot 0 of a dK item's
   TailShared tail;
-  uint64_t s_full, pa_ready;   // every tile
-  uint64_t dp_full, ds_ready;  // tiles of dK items
+  uint64_t s_full, s_read;     // S^T is there, and in registers
+  // P^T (dV items) or dS^T (dK items) is in its buffer, tile n in n & 1. Two barriers,
+  // because a dV item's softmax can finish tile n + 1 (S^T(n+1) is issued before the
+  // MMA thread waits for P^T(n)) before that wait starts, and on one barrier the wait
+  // would then see two completed phases. Tile n + 2 needs S^T(n+2), issued after it.
+  uint64_t x_ready[2];
+  uint64_t dp_full;            // tiles of dK items
   uint64_t acc_done, acc_free;
   uint64_t mma_drain;  // the MMA thread's last commit: all its MMAs done before the CTA exits
   uint64_t item_full[kItemSlots], item_empty[kItemSlots];
@@ -121,22 +127,26 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
   const int total = total_items(p);
   const uint64_t lim = p.wait_limit_ns;
   int g = 0, items = 0, kv_issued = 0;
-  int q_issued = 0, do_issued = 0;  // query tiles
+  int q_issued = 0, do_issued[2] = {0, 0};  // loads into the slots
   bool aborted = false;
   auto load = [&](uint64_t* bar, uint8_t* dst, const CUtensorMap* map, int row, int bh) {
     mbar_arrive_expect_tx(bar, C::Q_BYTES);
 #pragma unroll
     for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * C::Q_CHUNK, map, bar, c * 64, row, bh);
   };
-  auto load_tile = [&](int n, const typename Work<CAUSAL>::Pos& pos, int row0) -> bool {
-    const int row = row0 + pos.i * C::BQ, s = n % C::Q_SLOTS;
+  auto load_do = [&](int s, int row, int bh) -> bool {
+    if (do_issued[s] > 0 && !mbar_wait(&sh.do_empty[s], (do_issued[s] - 1) & 1, &sh.abort_flag, lim)) return false;
+    load(&sh.do_full[s], s ? sV : sdO, &p.tmdO, row, bh);
+    ++do_issued[s];
+    return true;
+  };
+  // n: the tile's number, i: its number in the item
+  auto load_tile = [&](int n, int i, const Work<CAUSAL>& wk, const typename Work<CAUSAL>::Pos& pos) -> bool {
+    const int row = wk.row0 + pos.i * C::BQ, s = n % C::Q_SLOTS;
     if (n >= C::Q_SLOTS && !mbar_wait(&sh.q_empty[s], ((n / C::Q_SLOTS) - 1) & 1, &sh.abort_flag, lim)) return false;
     load(&sh.q_full[s], sQ + s * C::Q_BYTES, &p.tmQ, row, pos.bh);
     ++q_issued;
-    if (n > 0 && !mbar_wait(&sh.do_empty, (n - 1) & 1, &sh.abort_flag, lim)) return false;
-    load(&sh.do_full, sdO, &p.tmdO, row, pos.bh);
-    ++do_issued;
-    return true;
+    return !wk.dk && (i & 1) ? load_do(1, row, pos.bh) : load_do(0, row, pos.bh);
   };
   int item = blockIdx.x;
   while (!aborted) {
@@ -148,7 +158,8 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
     const Work<CAUSAL> wk(item, p);
     const int n_iter = wk.n_iter();
     typename Work<CAUSAL>::Pos pos = wk.first();
-    if (!load_tile(g, pos, wk.row0) ||
+    // (a first tile uses slot 0 of dO: slot 1 is V_j's place until then)
+    if (!load_tile(g, 0, wk, pos) ||
         (items > 0 && !mbar_wait(&sh.acc_done, (items - 1) & 1, &sh.abort_flag, lim))) {
       aborted = true;
       break;
@@ -164,7 +175,7 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
     }
     for (int n = 1; n < n_iter && !aborted; ++n) {
       wk.advance(pos);
-      aborted = !load_tile(g + n, pos, wk.row0);
+      aborted = !load_tile(g + n, n, wk, pos);
     }
     if (aborted) break;
     g += n_iter;
@@ -177,7 +188,8 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
   // may wait for them): the latest phase issued into each slot.
   for (int n = std::max(0, q_issued - C::Q_SLOTS); n < q_issued; ++n)
     drain_wait(&sh.q_full[n % C::Q_SLOTS], (n / C::Q_SLOTS) & 1, lim);
-  if (do_issued > 0) drain_wait(&sh.do_full, (do_issued - 1) & 1, lim);
+  for (int s = 0; s < 2; ++s)
+    if (do_issued[s] > 0) drain_wait(&sh.do_full[s], (do_issued[s] - 1) & 1, lim);
   if (kv_issued > 0) drain_wait(&sh.kv_full, (kv_issued - 1) & 1, lim);
 }
 
@@ -215,7 +227,8 @@ __device__ void mma_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* s
     });
   };
 
-  int g = 0, gk = 0, items = 0;  // tiles, tiles of dK items
+  int g = 0, items = 0;  // tiles
+  int d0 = 0, d1 = 0;    // tiles of dO in slot 0 and 1
   TailCalls<false> tail;
   while (true) {
     const int item = take_item(sh, items, lim);
@@ -232,7 +245,7 @@ __device__ void mma_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* s
       tail.ask(sh.tail, held, tile);
       return tail.wait(sh.tail, &sh.abort_flag, lim);
     };
-    // S^T(n): the S region is free, phase A(n - 1) has read it (pa_ready)
+    // S^T(n): the S region is free, phase A(n - 1) has read it (s_read)
     auto issue_s = [&](int n, bool cut) -> bool {
       const int s = n % C::Q_SLOTS;
       if (!mbar_wait(&sh.q_full[s], (n / C::Q_SLOTS) & 1, &sh.abort_flag, lim)) return false;
@@ -243,38 +256,39 @@ __device__ void mma_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* s
       if (!dk) umma_commit(&sh.q_empty[s]);
       return true;
     };
-    // dP^T(n): phase B(n - 1) has read the last one (ds_ready)
-    auto issue_dp = [&](int n) -> bool {
-      if (!mbar_wait(&sh.do_full, n & 1, &sh.abort_flag, lim)) return false;
+    // the next dP^T: phase B(n - 1) has read the last one (x_ready)
+    auto issue_dp = [&]() -> bool {
+      if (!mbar_wait(&sh.do_full[0], d0++ & 1, &sh.abort_flag, lim)) return false;
       tc_fence_after_sync();
       issue_sq(C::DP_COL, v_addr, do_addr);
       umma_commit(&sh.dp_full);
-      umma_commit(&sh.do_empty);
+      umma_commit(&sh.do_empty[0]);
       return true;
     };
     if (!mbar_wait(&sh.kv_full, items & 1, &sh.abort_flag, lim) || !issue_s(g, until == 0)) return fail();
-    if (dk && !issue_dp(g)) return fail();
+    if (dk && !issue_dp()) return fail();
     for (int n = 0; n < n_iter; ++n, ++g) {
       const bool has_next = n + 1 < n_iter, cut = until == 0;
       const int steps = cut ? (held + 15) >> 4 : 4;
-      if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
+      if (!mbar_wait(&sh.s_read, g & 1, &sh.abort_flag, lim)) return fail();
       if (has_next && !issue_s(g + 1, (cut ? until = wk.T64 - 1 - wk.i0 : --until) == 0)) return fail();
       // the first product of an item overwrites the accumulator: the previous item's
       // epilogue must have read it
       if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
+      if (!mbar_wait(&sh.x_ready[g & 1], (g >> 1) & 1, &sh.abort_flag, lim)) return fail();
       if (dk) {
-        if (!mbar_wait(&sh.ds_ready, gk & 1, &sh.abort_flag, lim)) return fail();
-        ++gk;
         tc_fence_after_sync();
         issue_acc(steps, g & 1, q_addr + (g % C::Q_SLOTS) * C::Q_BYTES, n == 0);
         umma_commit(&sh.q_empty[g % C::Q_SLOTS]);
-        if (has_next && !issue_dp(g + 1)) return fail();
+        if (has_next && !issue_dp()) return fail();
       } else {
-        if (!mbar_wait(&sh.do_full, g & 1, &sh.abort_flag, lim)) return fail();
-        if (cut && !clean(do_addr)) return fail();
+        const int s = n & 1;
+        const uint32_t from = s ? v_addr : do_addr;
+        if (!mbar_wait(&sh.do_full[s], (s ? d1++ : d0++) & 1, &sh.abort_flag, lim)) return fail();
+        if (cut && !clean(from)) return fail();
         tc_fence_after_sync();
-        issue_acc(steps, g & 1, do_addr, n == 0);
-        umma_commit(&sh.do_empty);
+        issue_acc(steps, g & 1, from, n == 0);
+        umma_commit(&sh.do_empty[s]);
       }
     }
     umma_commit(&sh.acc_done);
@@ -323,17 +337,16 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
   };
 
   // ---- phase A of query tile i (global tile g): P^T in registers, and for dV in TMEM
-  // (bf16). For dK the next S^T may come as soon as this one is in registers.
+  // (bf16). The next S^T may come as soon as this one is in registers (where dV's came
+  // after P^T was stored, 503 us instead of TIME1).
   auto phase_a = [&](const Work<CAUSAL>& wk, int i, int g) {
     wait_all(&sh.s_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     uint32_t a[32];
     tmem_ld32(tS, a);
     tmem_ld_wait();
-    if (wk.dk) {
-      tc_fence_before_sync();
-      mbar_arrive(&sh.pa_ready);
-    }
+    tc_fence_before_sync();
+    mbar_arrive(&sh.s_read);
     // key 128j + r is seen by query 64i + 32w + c if (causal) it is not after the
     // query: c >= c_lo. (A key behind the sequence's last one stays: its row of P^T
     // and dS^T reaches only its own row of dV and dK, which is not written.)
@@ -364,7 +377,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
       tmem_st16(tX + 32 * (g & 1), pb);
       tmem_st_wait();
       tc_fence_before_sync();
-      mbar_arrive(&sh.pa_ready);
+      mbar_arrive(&sh.x_ready[g & 1]);
     }
   };
 
@@ -397,7 +410,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
     tmem_st16(tX + 32 * (g & 1), dk);
     tmem_st_wait();
     tc_fence_before_sync();
-    mbar_arrive(&sh.ds_ready);
+    mbar_arrive(&sh.x_ready[g & 1]);
   };
 
   // ---- item epilogue: columns [128w, 128w + 128) of dK or dV; thread r writes key row
@@ -514,14 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_bwd256_ragged_kernel(const __g
     for (int s = 0; s < C::Q_SLOTS; ++s) {
       mbar_init(&sh.q_full[s], 1);
       mbar_init(&sh.q_empty[s], 1);
+      mbar_init(&sh.do_full[s], 1);
+      mbar_init(&sh.do_empty[s], 1);
     }
-    mbar_init(&sh.do_full, 1);
-    mbar_init(&sh.do_empty, 1);
     // test hook: the S or P barrier waits for one arrival too many
     mbar_init(&sh.s_full, 1 + debug_extra(p.debug_skip, WHERE_BWD_MMA));
     mbar_init(&sh.dp_full, 1);
-    mbar_init(&sh.pa_ready, 256 + debug_extra(p.debug_skip, WHERE_BWD_SOFTMAX));
-    mbar_init(&sh.ds_ready, 256);
+    mbar_init(&sh.s_read, 256);
+    for (int b = 0; b < 2; ++b)
+      mbar_init(&sh.x_ready[b], 256 + (b == 0 ? debug_extra(p.debug_skip, WHERE_BWD_SOFTMAX) : 0u));
     mbar_init(&sh.acc_done, 1);
     mbar_init(&sh.acc_free, 256);
     tail_init(sh.tail);
