@@ -26,8 +26,8 @@ LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pack.cu", "fa_fwd_ragged.cu", "fa_bwd.cu", "fa_bwd256.cu",
-           "fa_bwd256_ragged.cu", "fa_bwd_dq.cu", "fa_bwd_dq256.cu", "fa_host.cu", "fa_packed.cu", "fa_packed_short.cu", "fa_norm_rope.cu", "fa_kv8.cu", "fa_fwd_kv8.cu",
-           "fa_fwd_kv8_tile.cu"]
+           "fa_bwd256_ragged.cu", "fa_bwd_dq.cu", "fa_bwd_dq256.cu", "fa_host.cu", "fa_packed.cu",
+           "fa_packed_short.cu", "fa_norm_rope.cu", "fa_kv8.cu", "fa_fwd_kv8.cu", "fa_fwd_kv8_tile.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                            "--expt-relaxed-constexpr", "-I", INCLUDE]

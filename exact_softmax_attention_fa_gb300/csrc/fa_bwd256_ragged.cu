@@ -16,9 +16,9 @@
 //     dV(n) after phase A(n), or dK(n) after phase B(n) and then dP^T(n+1). A commit covers all that
 //     was issued before it: s_full(n) says that dV(n-2) has read its P^T, dp_full(n)
 //     that dK(n-1) has read its dS^T.
-// Three sequences of up to 2501 rows, 8 + 2 heads, no mask: TIME1 us with its dQ kernel
-// instead of 610 with halves. What bounds it: the products of 64 queries, which take
-// the pipe as long as those of 128 do, and the hand-offs between them.
+// Three sequences of up to 2501 rows, 8 + 2 heads, no mask: 486 us with its dQ kernel
+// instead of 610 with halves. A dK tile takes 1.6 us, of which its products 1.3 (those
+// of 64 queries take the pipe as long as those of 128 do), a dV tile 1.45.
 // TMEM columns (512 allocated): dV or dK [0, 256), S^T [256, 320), dP^T [320, 384),
 // P^T or dS^T in two buffers [384, 416) and [416, 448) (tile n in buffer n & 1).
 #include <cuda_bf16.h>
@@ -140,13 +140,12 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
     ++do_issued[s];
     return true;
   };
-  // n: the tile's number, i: its number in the item
-  auto load_tile = [&](int n, int i, const Work<CAUSAL>& wk, const typename Work<CAUSAL>::Pos& pos) -> bool {
-    const int row = wk.row0 + pos.i * C::BQ, s = n % C::Q_SLOTS;
+  auto load_q = [&](int n, int row, int bh) -> bool {  // n: the tile's number
+    const int s = n % C::Q_SLOTS;
     if (n >= C::Q_SLOTS && !mbar_wait(&sh.q_empty[s], ((n / C::Q_SLOTS) - 1) & 1, &sh.abort_flag, lim)) return false;
-    load(&sh.q_full[s], sQ + s * C::Q_BYTES, &p.tmQ, row, pos.bh);
+    load(&sh.q_full[s], sQ + s * C::Q_BYTES, &p.tmQ, row, bh);
     ++q_issued;
-    return !wk.dk && (i & 1) ? load_do(1, row, pos.bh) : load_do(0, row, pos.bh);
+    return true;
   };
   int item = blockIdx.x;
   while (!aborted) {
@@ -157,9 +156,10 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
     if (item >= total) break;
     const Work<CAUSAL> wk(item, p);
     const int n_iter = wk.n_iter();
-    typename Work<CAUSAL>::Pos pos = wk.first();
+    typename Work<CAUSAL>::Pos pos = wk.first(), q_pos = pos;
+    auto row_of = [&](const typename Work<CAUSAL>::Pos& at) { return wk.row0 + at.i * C::BQ; };
     // (a first tile uses slot 0 of dO: slot 1 is V_j's place until then)
-    if (!load_tile(g, 0, wk, pos) ||
+    if (!load_q(g, row_of(pos), pos.bh) || !load_do(0, row_of(pos), pos.bh) ||
         (items > 0 && !mbar_wait(&sh.acc_done, (items - 1) & 1, &sh.abort_flag, lim))) {
       aborted = true;
       break;
@@ -173,9 +173,19 @@ __device__ void load_role(const BwdLaunch& p, Shared& sh, uint8_t* sK, uint8_t* 
       }
       ++kv_issued;
     }
+    // In the order in which the slots free up: dO_n after dP^T(n-1) and Q_(n+1) after
+    // dK(n-1); for dV Q_(n+1) after S^T(n-1) and dO_n after dV(n-2).
+    int q_next = 1;
+    auto next_q = [&]() -> bool {
+      if (q_next >= n_iter) return true;
+      wk.advance(q_pos);
+      return load_q(g + q_next++, row_of(q_pos), q_pos.bh);
+    };
+    if (!next_q()) aborted = true;
     for (int n = 1; n < n_iter && !aborted; ++n) {
       wk.advance(pos);
-      aborted = !load_tile(g + n, n, wk, pos);
+      aborted = wk.dk ? !load_do(0, row_of(pos), pos.bh) || !next_q()
+                      : !next_q() || !((n & 1) ? load_do(1, row_of(pos), pos.bh) : load_do(0, row_of(pos), pos.bh));
     }
     if (aborted) break;
     g += n_iter;
@@ -338,7 +348,7 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
 
   // ---- phase A of query tile i (global tile g): P^T in registers, and for dV in TMEM
   // (bf16). The next S^T may come as soon as this one is in registers (where dV's came
-  // after P^T was stored, 503 us instead of TIME1).
+  // after P^T was stored, 503 us instead of 491).
   auto phase_a = [&](const Work<CAUSAL>& wk, int i, int g) {
     wait_all(&sh.s_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
@@ -469,13 +479,13 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
     if (items > 0) named_barrier_sync(bar_id, 128);  // the previous item's L2 / D reads are done
     if (r < 64) ld_l2[r] = ld;
     named_barrier_sync(bar_id, 128);
-    typename Work<CAUSAL>::Pos cur = wk.first();
+    // the next tile's L2 and D land during phase A (a dV item has no phase B)
+    typename Work<CAUSAL>::Pos cur = wk.first(), nxt = cur;
+    wk.advance(nxt);
+    float next_ld = n_iter > 1 ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;
     phase_a(wk, cur.i, g);
     for (int n = 0; n < n_iter; ++n) {
       const bool has_next = n + 1 < n_iter;
-      typename Work<CAUSAL>::Pos nxt = cur;
-      wk.advance(nxt);
-      const float next_ld = has_next ? fetch_ld(wk, nxt.bh, nxt.i) : 0.f;  // lands during phase B
       if (wk.dk) {
         if (cur.i == wk.T64 - 1)
           phase_b(wk, cur.i, g + n, gk + n, std::true_type());
@@ -486,9 +496,11 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
         if (r < 64) ld_l2[r] = next_ld;
         named_barrier_sync(bar_id, 128);
-        phase_a(wk, nxt.i, g + n + 1);
+        cur = nxt;
+        wk.advance(nxt);
+        if (n + 2 < n_iter) next_ld = fetch_ld(wk, nxt.bh, nxt.i);
+        phase_a(wk, cur.i, g + n + 1);
       }
-      cur = nxt;
     }
     const int item_next = next_item(items + 1);
     if (item_next < total) {
