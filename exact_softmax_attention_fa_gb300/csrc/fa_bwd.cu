@@ -60,23 +60,14 @@ namespace {
 
 // Warps: 0-3 and 4-7 softmax + dQ drain (query columns 0-63 / 64-127),
 // 8 TMA loads, 9 MMA issue.
-// Over packed sequences one more that clears rows, and at d = 64 four softmax
-// warpgroups of 32 columns each: a tile's chain through them is the shorter, which
-// took the backward of eight sequences of up to 4096 rows from 912 to 833 us. (At
-// d = 128 a thread's 96 registers are too few for its statistics to be read ahead:
-// 1773 us instead of 1763, 848 instead of 856 for sequences of up to 256 rows.)
-template <int HD, bool RAG>
-struct Warps {
-  static constexpr int kGroups = RAG && HD == 64 ? 4 : 2;
-  static constexpr int kCols = 128 / kGroups;  // query columns of a warpgroup
-  static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kLoad = 4 * kGroups, kMma = kLoad + 1, kTail = kLoad + 2;
-  static constexpr int kThreads = 32 * (RAG ? kTail + 1 : kMma + 1);
-  static constexpr int kItemConsumers = 1 + kSoftmax;  // the MMA thread and the softmax threads
-  // region A's column of step ks of the dV product: 16 queries' bf16 pairs, which sit
-  // in the first half of each warpgroup's columns
-  __device__ static constexpr uint32_t step_col(int ks) { return ks / (kCols / 16) * kCols + ks % (kCols / 16) * 8; }
-};
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;  // packed sequences alone; registers are dealt out for 12 warps either way
+template <bool RAG>
+constexpr int kernel_threads() {
+  return RAG ? kThreads + 32 : kThreads;
+}
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int HD>
@@ -206,7 +197,9 @@ __device__ __forceinline__ int bwd_total_items(const BwdLaunch& p) {
 
 // Dynamic schedule (fa_kernel_common.cuh): items are claimed from sched[0..1]
 // of the workspace, so CTAs that run ahead take more items and causal items
-// come heaviest first.
+// come heaviest first. Consumers of the item queue: the MMA thread and the
+// 256 softmax threads.
+constexpr int kItemConsumers = 1 + 256;
 
 // Grouped K/V heads split over several work items: dK, dV = bf16 of the sum
 // of the chunks' fp32 partials, added in chunk order (bitwise reproducible).
@@ -467,10 +460,10 @@ __device__ void bwd_mma_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sK, uin
       if (!mbar_wait(&sh.pa_ready, g & 1, &sh.abort_flag, lim)) return fail();
       if (n == 0 && items > 0 && !mbar_wait(&sh.acc_free, (items - 1) & 1, &sh.abort_flag, lim)) return fail();
       tc_fence_after_sync();
-      // dV += P^T dO_n; P^T (bf16) sits in the first half of each warpgroup's columns of region A
+      // dV += P^T dO_n; P^T (bf16) sits in columns [0,32) and [64,96) of region A
       const uint64_t dod = make_smem_desc_sw128(doa, C::CHUNK_BYTES, 1024);
       issue_steps<8, RAG>(steps, [&](int ks) {
-        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + Warps<HD, RAG>::step_col(ks), desc_add(dod, ks * 2048), kIdescAcc,
+        umma_ts(tmem + C::DV_COL, tmem + C::REG_A + (ks >> 2) * 64 + (ks & 3) * 8, desc_add(dod, ks * 2048), kIdescAcc,
                 (n > 0 || ks > 0) ? 1u : 0u);
       });
       umma_commit(&sh.pv_done);
@@ -543,20 +536,25 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   const float c2 = p.scale_log2;
   const float sc = p.scale;
   const uint64_t lim = p.wait_limit_ns;
-  constexpr int COLS = Warps<HD, RAG>::kCols;
-  const uint32_t ds_chunk = smem_u32(sDS) + w * COLS / 64 * C::CHUNK_BYTES;  // queries COLS w .. COLS (w + 1) - 1
-  const int ds_unit = w * COLS % 64 / 8;
-  float* ld_l2 = sLD + w * 2 * COLS;  // COLS base-2 logsumexps, then COLS scaled D values
-  float* ld_d = ld_l2 + COLS;
+  const uint32_t ds_chunk = smem_u32(sDS) + w * C::CHUNK_BYTES;  // queries 64w .. 64w+63
+  float* ld_l2 = sLD + w * 128;  // 64 base-2 logsumexps, then 64 scaled D values
+  float* ld_d = ld_l2 + 64;
   const uint32_t bar_id = 1 + w;
-  const uint32_t tA = tmem + lane_base + C::REG_A + COLS * w;
-  const uint32_t tB = tmem + lane_base + C::REG_B + COLS * w;
+  const uint32_t tA = tmem + lane_base + C::REG_A + 64 * w;
+  const uint32_t tB = tmem + lane_base + C::REG_B + 64 * w;
   const int total = bwd_total_items<RAG>(p);
   bool alive = true;
-  constexpr bool kPrefetchStats = !DQ && HD == 128;
+  // Over packed sequences half of the statistics are read ahead, at d = 64 too, and
+  // the weights stay in fp32, which takes no packing: sequences of up to 8192 rows, 32
+  // + 8 heads of d = 128, 1669 us with the dQ kernel, 1735 with a quarter of them, 1745
+  // with all and the weights two in a register; 4096 rows, 16 + 4 heads of d = 64, 890,
+  // with none 964, in four warpgroups of 32 columns 925.
+  constexpr bool kPrefetchStats = !DQ && (HD == 128 || RAG);
+  constexpr int kAhead = RAG ? 8 : 16;  // of 16 vectors
   // P^T of the current tile as the bf16 pairs written to TMEM, kept from
   // phase A to phase B: dS uses the same rounded P as the dV MMA.
-  Weights<COLS, RAG, RAG && HD == 128 ? 8 : 0> pk;  // (four more registers; 0: 1760 us instead of 1745)
+  // (Over packed sequences in fp32.)
+  Weights<64, RAG> pk;
 
   // L2 / D of query tile i of head bh for this warpgroup's 64 columns:
   // thread r < 64 loads L2[r], thread r >= 64 loads D[r - 64] * scale.
@@ -564,11 +562,10 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   // rows of Q and dO are cleared: S = 0 gives weight 0, and dP = 0 makes dS = 0.
   auto fetch_ld = [&](const BwdWork<CAUSAL, RAG>& wk, int bh, int i) -> float {
     if constexpr (RAG) {
-      if (r >= 2 * COLS) return 0.f;
-      const int q = i * 128 + COLS * w + (r & (COLS - 1));
-      const float* from = (r < COLS ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
+      const int q = i * 128 + 64 * w + (r & 63);
+      const float* from = (r < 64 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
       const float x = __ldg(from + min(q, wk.n - 1));
-      return r < COLS ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
+      return r < 64 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
     }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * 128 + 64 * w;
     return r < 64 ? __ldg(p.lse2 + row + r) : __ldg(p.D + row + (r - 64)) * sc;
@@ -589,18 +586,15 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     // phase's critical path: measured ~800 of ~1600 cycles at d = 128). Only
     // where the registers allow it (d = 128 without dQ); elsewhere they are
     // read in the loop.
-    float4 lv[kPrefetchStats ? COLS / 4 : 1];
+    float4 lv[kPrefetchStats ? kAhead : 1];
     if constexpr (kPrefetchStats) {
 #pragma unroll
-      for (int c = 0; c < COLS / 4; ++c) lv[c] = *reinterpret_cast<const float4*>(ld_l2 + 4 * c);
+      for (int c = 0; c < kAhead; ++c) lv[c] = *reinterpret_cast<const float4*>(ld_l2 + 4 * c);
     }
     wait_all(&sh.s_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
-    float pv[COLS];
-    if constexpr (COLS == 32) {
-      tmem_ld32(tA, *reinterpret_cast<uint32_t(*)[32]>(pv));
-      tmem_ld_wait();
-    } else {
+    float pv[64];
+    {
       uint32_t a[32], b[32];
       tmem_ld32(tA, a);
       tmem_ld32(tA + 32, b);
@@ -612,17 +606,18 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       }
     }
     // Only the key-tail tile and the causal diagonal tile need masking:
-    // query (COLS w + c) sees key r only if COLS w + c >= r.
+    // query (64w + c) sees key r only if 64w + c >= r.
     // (Over packed sequences a key behind the last one stays: its row of P^T and
     // dS^T reaches only its own row of dV and dK, which is not written.)
     const bool key_valid = RAG || wk.j * 128 + r < wk.len(p);
     const bool masked = !key_valid || (CAUSAL && i == wk.j);
-    const int c_lo = !key_valid ? COLS : ((CAUSAL && i == wk.j) ? r - COLS * w : 0);
+    const int c_lo = !key_valid ? 64 : ((CAUSAL && i == wk.j) ? r - 64 * w : 0);
     // Three passes over the row (exponent arguments, exponentials, bf16
     // pairs) give the scheduler long runs of independent instructions.
 #pragma unroll
-    for (int c4 = 0; c4 < COLS; c4 += 4) {
-      const float4 l = kPrefetchStats ? lv[kPrefetchStats ? c4 / 4 : 0] : *reinterpret_cast<const float4*>(ld_l2 + c4);
+    for (int c4 = 0; c4 < 64; c4 += 4) {
+      const float4 l = kPrefetchStats && c4 / 4 < kAhead ? lv[kPrefetchStats ? c4 / 4 % kAhead : 0]
+                                                         : *reinterpret_cast<const float4*>(ld_l2 + c4);
       const float2 x01 = ffma2_bcast_mul(pv[c4], pv[c4 + 1], c2, -l.x, -l.y);
       const float2 x23 = ffma2_bcast_mul(pv[c4 + 2], pv[c4 + 3], c2, -l.z, -l.w);
       pv[c4] = x01.x;
@@ -631,20 +626,19 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       pv[c4 + 3] = x23.y;
     }
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) pv[c] = ex2_approx(pv[c]);
+    for (int c = 0; c < 64; ++c) pv[c] = ex2_approx(pv[c]);
     if (masked) {
 #pragma unroll
-      for (int c = 0; c < COLS; ++c)
+      for (int c = 0; c < 64; ++c)
         if (c < c_lo) pv[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < COLS; c += 2) pk.put(c, pv[c], pv[c + 1]);
+    for (int c = 0; c < 64; c += 2) pk.put(c, pv[c], pv[c + 1]);
     if constexpr (RAG) {
-      uint32_t pb[COLS / 2];
+      uint32_t pb[32];
 #pragma unroll
-      for (int c = 0; c < COLS / 2; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
-      if constexpr (COLS == 32) tmem_st16(tA, pb);
-      else tmem_st32(tA, pb);
+      for (int c = 0; c < 32; ++c) pb[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
+      tmem_st32(tA, pb);
     } else {
       tmem_st32(tA, pk.two);  // columns [64w, 64w + 32): already read
     }
@@ -657,23 +651,24 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   auto phase_b = [&](int g) {
     // the scaled D values, read from smem while dP^T is still being computed
     // (as the logsumexps in phase A)
-    float4 dvv[kPrefetchStats ? COLS / 4 : 1];
+    float4 dvv[kPrefetchStats ? kAhead : 1];
     if constexpr (kPrefetchStats) {
 #pragma unroll
-      for (int c = 0; c < COLS / 4; ++c) dvv[c] = *reinterpret_cast<const float4*>(ld_d + 4 * c);
+      for (int c = 0; c < kAhead; ++c) dvv[c] = *reinterpret_cast<const float4*>(ld_d + 4 * c);
     }
     wait_all(&sh.dp_full, g & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
 #pragma unroll
-    for (int h = 0; h < COLS / 32; ++h) {
+    for (int h = 0; h < 2; ++h) {
       uint32_t dpv[32];
       tmem_ld32(tB + 32 * h, dpv);
       tmem_ld_wait();
       uint32_t dk[16];
 #pragma unroll
       for (int c4 = 0; c4 < 32; c4 += 4) {
-        const float4 dd = kPrefetchStats ? dvv[kPrefetchStats ? (32 * h + c4) / 4 : 0]
-                                         : *reinterpret_cast<const float4*>(ld_d + 32 * h + c4);
+        const float4 dd = kPrefetchStats && (32 * h + c4) / 4 < kAhead
+                              ? dvv[kPrefetchStats ? (32 * h + c4) / 4 % kAhead : 0]
+                              : *reinterpret_cast<const float4*>(ld_d + 32 * h + c4);
         const float dv4[4] = {dd.x, dd.y, dd.z, dd.w};
         const float2 p01 = pk.get(32 * h + c4);
         const float2 p23 = pk.get(32 * h + c4 + 2);
@@ -688,7 +683,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        st_shared_v4(ds_chunk + sw128_offset(r, ds_unit + 4 * h + u), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+        st_shared_v4(ds_chunk + sw128_offset(r, 4 * h + u), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
     }
     fence_proxy_async_smem();
     tc_fence_before_sync();
@@ -750,26 +745,24 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     wait_all(&sh.acc_done, items & 1, WHERE_BWD_SOFTMAX);
     if (!alive) return;
     const int key = wk.j * 128 + r;
-    const uint32_t t = tmem + lane_base + ((w & 1) == 0 ? C::DK_COL : C::DV_COL);
-    constexpr int PART = HD / (Warps<HD, RAG>::kGroups / 2);  // columns of the accumulator, from `begin`
-    const int begin = (w >> 1) * PART;
+    const uint32_t t = tmem + lane_base + (w == 0 ? C::DK_COL : C::DV_COL);
     const bool written = key < wk.len(p);
     const size_t row = static_cast<size_t>(wk.bh) * p.N + wk.row0 + key;
     const int chunks = RAG ? p.group / wk.gs : p.chunks;
     if (chunks == 1) {
-      __nv_bfloat16* dst = ((w & 1) == 0 ? p.dk : p.dv);
+      __nv_bfloat16* dst = (w == 0 ? p.dk : p.dv);
       if constexpr (RAG) {
-        const long long* st = (w & 1) == 0 ? p.dk_strides : p.dv_strides;
+        const long long* st = w == 0 ? p.dk_strides : p.dv_strides;
         dst += static_cast<long long>(wk.row0 + key) * st[0] + wk.bh * st[1];
       } else {
         dst += row * HD;
       }
 #pragma unroll 1
-      for (int c = begin; c < begin + PART; c += 32) {
+      for (int c = 0; c < HD; c += 32) {
         uint32_t v[32];
         tmem_ld32(t + c, v);
         tmem_ld_wait();
-        if (c + 32 == begin + PART) {  // both accumulators read: the next item may overwrite them
+        if (c + 32 == HD) {  // both accumulators read: the next item may overwrite them
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
@@ -785,13 +778,13 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       }
     } else {
       const size_t part_len = static_cast<size_t>(chunks) * p.BHkv * p.N * HD;
-      float* part = p.kv_part + ((w & 1) == 0 ? 0 : part_len) + (static_cast<size_t>(wk.c) * p.BHkv * p.N + row) * HD;
+      float* part = p.kv_part + (w == 0 ? 0 : part_len) + (static_cast<size_t>(wk.c) * p.BHkv * p.N + row) * HD;
 #pragma unroll 1
-      for (int c = begin; c < begin + PART; c += 32) {
+      for (int c = 0; c < HD; c += 32) {
         uint32_t v[32];
         tmem_ld32(t + c, v);
         tmem_ld_wait();
-        if (c + 32 == begin + PART) {
+        if (c + 32 == HD) {
           tc_fence_before_sync();
           mbar_arrive(&sh.acc_free);
         }
@@ -828,7 +821,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     const BwdWork<CAUSAL, RAG> wk(item, p);
     const int n_iter = wk.n_iter();
     if (items > 0) named_barrier_sync(bar_id, 128);  // the previous item's L2 / D reads are done
-    if (r < 2 * COLS) ld_l2[r] = ld;
+    sLD[w * 128 + r] = ld;
     named_barrier_sync(bar_id, 128);
     typename BwdWork<CAUSAL, RAG>::Pos cur = wk.first();
     phase_a(wk, cur.i, g);
@@ -840,7 +833,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
       phase_b(g + n);
       if (has_next) {
         named_barrier_sync(bar_id, 128);  // every thread is done reading this tile's L2 / D
-        if (r < 2 * COLS) ld_l2[r] = next_ld;
+        sLD[w * 128 + r] = next_ld;
         named_barrier_sync(bar_id, 128);
         phase_a(wk, nxt.i, g + n + 1);
       }
@@ -861,7 +854,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
 }
 
 template <int HD, bool CAUSAL, bool DQ, bool RAG>
-__global__ void __launch_bounds__(Warps<HD, RAG>::kThreads, 1) fa_bwd_kernel(const __grid_constant__ BwdLaunch p) {
+__global__ void __launch_bounds__(kernel_threads<RAG>(), 1) fa_bwd_kernel(const __grid_constant__ BwdLaunch p) {
   using C = BwdCfg<HD>;
   extern __shared__ uint8_t smem_dyn[];
   __shared__ BwdShared sh;
@@ -892,23 +885,23 @@ __global__ void __launch_bounds__(Warps<HD, RAG>::kThreads, 1) fa_bwd_kernel(con
     // test hook: the S, P or dQ barrier waits for one arrival too many
     mbar_init(&sh.s_full, 1 + debug_extra(p.debug_skip, WHERE_BWD_MMA));
     mbar_init(&sh.dp_full, 1);
-    mbar_init(&sh.pa_ready, Warps<HD, RAG>::kSoftmax + debug_extra(p.debug_skip, WHERE_BWD_SOFTMAX));
-    mbar_init(&sh.ds_ready, Warps<HD, RAG>::kSoftmax);
+    mbar_init(&sh.pa_ready, 256 + debug_extra(p.debug_skip, WHERE_BWD_SOFTMAX));
+    mbar_init(&sh.ds_ready, 256);
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.dq_full, 1);
     mbar_init(&sh.dq_free, 256 + debug_extra(p.debug_skip, WHERE_BWD_DQ));
     mbar_init(&sh.acc_done, 1);
-    mbar_init(&sh.acc_free, Warps<HD, RAG>::kSoftmax);
+    mbar_init(&sh.acc_free, 256);
     if (RAG) tail_init(sh.tail);
     mbar_init(&sh.mma_drain, 1);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(&sh.item_full[s], 1);
-      mbar_init(&sh.item_empty[s], Warps<HD, RAG>::kItemConsumers);
+      mbar_init(&sh.item_empty[s], kItemConsumers);
     }
     sh.abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == Warps<HD, RAG>::kMma) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
@@ -917,11 +910,11 @@ __global__ void __launch_bounds__(Warps<HD, RAG>::kThreads, 1) fa_bwd_kernel(con
   tc_fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
 
-  if (warp == Warps<HD, RAG>::kLoad) {
+  if (warp == kLoadWarp) {
     if (lane_id() == 0) bwd_load_role<HD, CAUSAL, RAG>(p, sh, sK, sV, sQ, sdO);
-  } else if (warp == Warps<HD, RAG>::kMma) {
+  } else if (warp == kMmaWarp) {
     if (lane_id() == 0) bwd_mma_role<HD, CAUSAL, DQ, RAG>(p, sh, sK, sV, sQ, sdO, sDS, tmem);
-  } else if (RAG && warp == Warps<HD, RAG>::kTail) {
+  } else if (RAG && warp == kTailWarp) {
     tail_role<C::CHUNKS, C::CHUNK_BYTES, 128>(sh.tail, &sh.abort_flag, p.wait_limit_ns);
   } else {
     bwd_softmax_role<HD, CAUSAL, DQ, RAG>(p, sh, sDS, sLD, sDQ, tmem, wg);
@@ -930,7 +923,7 @@ __global__ void __launch_bounds__(Warps<HD, RAG>::kThreads, 1) fa_bwd_kernel(con
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == Warps<HD, RAG>::kMma) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int HD>
@@ -959,7 +952,7 @@ cudaError_t launch_main_t(const BwdLaunch& a, cudaStream_t stream) {
   const long long grid = items < a.num_sms ? items : a.num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(Warps<HD, RAG>::kThreads);
+  cfg.blockDim = dim3(kernel_threads<RAG>());
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -333,9 +333,9 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
   const uint32_t bar_id = 1 + w;
   const int total = dq_total_items<RAG>(p);
   bool alive = true;
-  // P of the current tile, by pairs; over packed sequences half of them in fp32 (64
-  // sequences of 512 rows, 32 + 8 heads: 675 us, with none 684)
-  Weights<64, RAG, RAG ? 32 : 0> pk;
+  // P of the current tile, bf16 pairs; over packed sequences fp32 (8 sequences of up to
+  // 4096 rows, d = 64: 811 us with dK and dV, half of them by pairs of 16 bits 828)
+  Weights<64, RAG> pk;
 
   auto wait_all = [&](uint64_t* bar, int parity, int where) {
     alive = alive && __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort_flag, lim));

@@ -353,7 +353,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
   const uint32_t bar_id = 1 + w;
   const int total = dq_total_items<RAG>(p);
   bool alive = true;
-  Weights<64, RAG, 0> pk;  // P of the current tile, by pairs (32 in fp32: no change)
+  Weights<64, RAG> pk;  // P of the current tile: bf16 pairs, over packed sequences fp32
 
   auto wait_all = [&](uint64_t* bar, int parity, int where) {
     alive = alive && __all_sync(0xffffffffu, mbar_wait(bar, parity, &sh.abort_flag, lim));

@@ -42,39 +42,27 @@ __device__ __forceinline__ bool packed_plan_ok(const PackedPlan* p, int rows) {
 
 // ---------------------------------------------------------------------------
 // Backward: a thread's N weights P of a tile that dS = P (dP - D) takes stay in
-// registers between the two phases of the tile, as the bf16 pairs that the dV product
-// reads. Over packed sequences that second rounding, as large as dS's own, is left out
-// (with it the gradients of random inputs are 0.28% off in the mean, so 0.24%): WHOLE
-// of them are kept in fp32, as many as there are registers for, and the others two in
-// a register with 10 bits each. A weight lies in [0, 2) (its row's own L is above each
-// of its scores but for rounding), so that the sign and the exponent's top bit are
-// zero: the 16 bits below them, 7 of the exponent and 9 of the mantissa, are kept, down
-// to 2^-126. The lower one is rounded to nearest (2^-10 instead of 2^-8). The upper one
-// is cut and read back with the lower one's bits behind it, which stand for the digits
-// that are gone: off by less than 2^-9, both ways alike, and one operation less in a
-// pass that these operations hold up (sequences of up to 8192 rows, d = 128: 1763 us,
-// with a mask 1838, in bf16 1696). A weight of 0 reads back as less than 2^-134. A NaN
-// among the scores reaches dS through D, which holds it as well.
+// registers between the two phases of the tile. The dense kernels keep the bf16 pairs
+// that the dV product reads; over packed sequences they stay in fp32, without that
+// second rounding, which is as large as dS's own (with it the gradients of random
+// inputs are 0.28% off in the mean, so 0.24%).
 // ---------------------------------------------------------------------------
-template <int N, bool RAG, int WHOLE>
+template <int N, bool RAG>
 struct Weights {
-  uint32_t two[N > WHOLE ? (N - WHOLE) / 2 : 1];
-  float one[WHOLE ? WHOLE : 1];
+  uint32_t two[RAG ? 1 : N / 2];
+  float one[RAG ? N : 1];
   // columns c and c + 1 (c even, known to the compiler)
   __device__ __forceinline__ void put(int c, float a, float b) {
-    if (c < WHOLE) {
+    if constexpr (RAG) {
       one[c] = a;
       one[c + 1] = b;
-    } else if (RAG) {
-      two[(c - WHOLE) / 2] = __byte_perm(__float_as_uint(a) * 4 + 0x8000u, __float_as_uint(b) * 4, 0x7632);
     } else {
       two[c / 2] = pack_bf16x2(a, b);
     }
   }
   __device__ __forceinline__ float2 get(int c) const {
-    if (c < WHOLE) return make_float2(one[c], one[c + 1]);
-    const uint32_t v = two[(c - WHOLE) / 2];
-    return RAG ? make_float2(__uint_as_float((v & 0xffffu) << 14), __uint_as_float(v >> 2)) : unpack_bf16x2(v);
+    if constexpr (RAG) return make_float2(one[c], one[c + 1]);
+    else return unpack_bf16x2(two[c / 2]);
   }
 };
 

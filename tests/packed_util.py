@@ -8,9 +8,8 @@ The bounds are per element and count half steps of bf16 (2^-8 of a value):
    (and the sum of the row likewise); exponentials and the fp32 sums are within 2^-18.
  - dV = P^T dO: the same rounding of P, P = exp(S - L) with the stored L (half a
    step of fp32 of |L|, 2^-24 |L|, moves a weight by as much).
- - dS = P o (dP - D), with P to 10 bits (a whole step is 2^-9 at most) and rounded
-   to bf16: 2^-8 + 2^-9 of |dS|, and P times what the fp32 sums dP and D (d terms
-   each) are off. dQ = scale dS K, dK = scale dS^T Q.
+ - dS = P o (dP - D), with P in fp32 and rounded to bf16: 2^-8 of |dS|, and P times
+   what the fp32 sums dP and D (d terms each) are off. dQ = scale dS K, dK = scale dS^T Q.
  - The exponential returns 0 where its result is below the smallest normal fp32
    number: every weight may be off by 2^-126 more, which counts where a key has
    no larger one (its dV is then 0 instead of, say, 1e-40, as are the terms of dQ and dK).
@@ -24,7 +23,6 @@ from attn_inputs import bf16_bits_to_f64, f32_to_bf16_bits
 from gpu_util import to_device
 
 H16 = 2.0 ** -8
-H9 = 2.0 ** -9
 TINY = 2.0 ** -126
 
 
@@ -115,7 +113,7 @@ def backward_ref(b, o, lse, causal, scale):
             ds = p * (dp - D)
             rel = d * 2.0 ** -23 * mag.max(-1, keepdims=True) + 2.0 ** -23 * np.abs(L) + 2.0 ** -18  # of a weight
             off = d * 2.0 ** -23 * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o[r, h])).sum(-1, keepdims=True))
-            ds_off = (H16 + H9 + H16 * H9 + rel) * np.abs(ds) + 1.01 * p * off + TINY * (1 + np.abs(dp - D))
+            ds_off = (H16 + rel) * np.abs(ds) + 1.01 * p * off + TINY * (1 + np.abs(dp - D))
             dq[r, h] = scale * (ds @ k)
             bq[r, h] = H16 * np.abs(dq[r, h]) + 1.01 * scale * (ds_off @ np.abs(k))
             dk[r, h // g] += scale * (ds.T @ q)

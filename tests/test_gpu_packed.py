@@ -102,7 +102,7 @@ def test_layouts():
 
 
 def test_a_single_sequence_is_the_dense_call():
-    """The same bits, but for dQ and dK: their dS takes weights of 10 bits instead of bf16's 8."""
+    """The same bits, but for dQ and dK: their dS takes weights in fp32 instead of bf16."""
     import exact_softmax_attention_fa_gb300 as fa
     import torch
     b = Batch([515], 3, 3, 128, BASE_SEED + 11)
