@@ -421,7 +421,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
       // of the dP columns (already read)
       wait_all(&sh.dp_full, t & 1, WHERE_BWD_SOFTMAX);
       if (alive) {
-        uint32_t ds[32];
+        uint32_t ds[RAG ? 16 : 32];  // over packed sequences a half at a time
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
           uint32_t dpv[32];
@@ -435,19 +435,21 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
             const float2 g23 = ffma2_bcast(__uint_as_float(dpv[c4 + 2]), __uint_as_float(dpv[c4 + 3]), sc, -dsc);
             const float2 d01 = fmul2(p01, g01);
             const float2 d23 = fmul2(p23, g23);
-            ds[16 * h2 + c4 / 2] = pack_bf16x2(d01.x, d01.y);
-            ds[16 * h2 + c4 / 2 + 1] = pack_bf16x2(d23.x, d23.y);
+            ds[(RAG ? 0 : 16 * h2) + c4 / 2] = pack_bf16x2(d01.x, d01.y);
+            ds[(RAG ? 0 : 16 * h2) + c4 / 2 + 1] = pack_bf16x2(d23.x, d23.y);
           }
-        }
-        if constexpr (RAG) {
-          // dP of keys behind the sequence's last may be infinite or NaN
-          const int keys = wk.len(p) - j * 128 - 64 * w;
-          if (keys < 64) {
+          if constexpr (RAG) {
+            // dP of keys behind the sequence's last may be infinite or NaN
+            const int keys = wk.len(p) - j * 128 - 64 * w - 32 * h2;
+            if (keys < 32) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ds[c] &= (2 * c < keys ? 0xFFFFu : 0u) | (2 * c + 1 < keys ? 0xFFFF0000u : 0u);
+              for (int c = 0; c < 16; ++c)
+                ds[c] &= (2 * c < keys ? 0xFFFFu : 0u) | (2 * c + 1 < keys ? 0xFFFF0000u : 0u);
+            }
+            tmem_st16(tDP + 16 * h2, ds);
           }
         }
-        tmem_st32(tDP, ds);
+        if constexpr (!RAG) tmem_st32(tDP, ds);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&sh.ds_ready);
