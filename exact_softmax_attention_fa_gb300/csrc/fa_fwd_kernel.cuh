@@ -502,7 +502,7 @@ __device__ void fwd_mma_role(const FwdLaunch& p, FwdShared& sh, uint8_t* sQ, uin
 // their time at such waits). Whole rows leave by TMA; in the warp where the
 // sequence ends, whose next rows are another's, by plain stores of whole lines.
 // (Rows straight from TMEM to global memory, a thread each, put 32 lines into
-// every store: 256 sequences of 128 rows, 32 + 8 heads: 169 us instead of 124.)
+// every store: 256 sequences of 128 rows, 32 + 8 heads: 169 us instead of 134.)
 template <int HD>
 __device__ __forceinline__ void fwd_store_ragged(const FwdLaunch& p, FwdShared& sh, uint8_t* stage, uint32_t tO, int t,
                                                  int lane, int held, int grow, int head, float inv_l) {

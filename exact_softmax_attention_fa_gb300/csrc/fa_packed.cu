@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   bool bad = false;
   int most = 0, n_short = 0;
   unsigned long long sum_c = 0, sum_f = 0;
-  for (int b = tid; b < B; b += kPlanThreads) {
+  for (long long b = tid; b < B; b += kPlanThreads) {
     const int from = cu[b], to = cu[b + 1];
     if (from < 0 || to < from || to > rows) {
       bad = true;
