@@ -344,6 +344,35 @@ def test_rows_further_apart_than_32_bits(d):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+def test_every_sm_busy_for_long(causal, d):
+    """Many items of many tiles on every SM, where the warps of a kernel drift apart as far as they can: no wait gives
+    up, every run has the same bits, and O, L and dV those of the dense call."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    lens, H = [2900, 4096, 1999, 3500, 2333, 3201], 12
+    g = torch.Generator(device="cuda").manual_seed(BASE_SEED + 980 + d)
+    x = torch.randn(sum(lens), 4 * H, d, generator=g, device="cuda").bfloat16()
+    q, k, v, do = x.split(H, 1)
+    cu = torch.tensor(starts(lens), device="cuda")
+    plan = fa.PackedPlan(cu, sum(lens), causal)
+    first = None
+    for _ in range(3):
+        o, lse = fa.forward_packed(q, k, v, plan)
+        got = (o, lse, *fa.backward_packed(q, k, v, o, lse, do, plan))
+        assert fa.fa_get_device_status_detail() == (0, 0, 0, 0)
+        first = first or got
+        for a, b in zip(got, first):
+            assert torch.equal(a, b)
+    for r in (slice(0, 2900), slice(8995, 12495)):
+        one = [t[r].transpose(0, 1)[None].contiguous() for t in (q, k, v, do)]
+        o2, l2 = fa.forward(*one[:3], causal=causal)
+        dv2 = fa.backward(*one[:3], o2, l2, one[3], causal=causal)[2]
+        assert torch.equal(o2[0].transpose(0, 1), first[0][r]) and torch.equal(l2[0], first[1][:, r])
+        assert torch.equal(dv2[0].transpose(0, 1), first[4][r])
+
+
 def test_two_streams_share_a_plan():
     import exact_softmax_attention_fa_gb300 as fa
     import torch
