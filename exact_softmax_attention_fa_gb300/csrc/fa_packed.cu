@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(256) packed_kv_sum_kernel(const __grid_constan
   }
 }
 
-// Zeros in the rows that belong to no sequence: a row of a head by d / 8 threads.
+// Zeros in the rows that belong to no sequence: a row of a head by d / 8 threads. (A
+// plan that was not made for these rows names none, and the call writes nothing.)
 struct PackedFill {
   __nv_bfloat16* x[3];
   long long st[3][2];
@@ -301,8 +302,8 @@ struct PackedFill {
 };
 
 __global__ void __launch_bounds__(256) packed_fill_kernel(const __grid_constant__ PackedFill a) {
-  const bool ok = packed_plan_ok(a.plan, a.rows);
-  const int begin = ok ? a.plan->row_begin : 0, end = ok ? a.plan->row_end : 0;
+  if (!packed_plan_ok(a.plan, a.rows)) return;
+  const int begin = a.plan->row_begin, end = a.plan->row_end;
   const int empty = a.rows - (end - begin), units = a.d / 8;
   const int heads = a.heads[0] + a.heads[1] + a.heads[2];
   const long long all = static_cast<long long>(empty) * heads * units, step = static_cast<long long>(gridDim.x) * 256;

@@ -1,0 +1,30 @@
+"""The plan of a packed batch as the calls take it: made for other rows, never made, dropped early."""
+
+import pytest
+
+from packed_util import Batch
+
+pytestmark = pytest.mark.gpu
+
+FA_ERR_INDEX = 8
+SEED = 91000
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_plan_of_other_rows_or_none_leaves_everything_with_fill(d):
+    """fill = 1 clears the rows of no sequence; a plan that is not of these rows says nothing about them."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    b = Batch([100, 30], 2, 2, d, SEED + d, tail=2)
+    plan = fa.PackedPlan(b.d_cu, b.rows + 1)
+    shape = (b.rows, 2, d)
+    for p in (plan, torch.zeros_like(plan.buffer)):
+        o, lse = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((2, b.rows), 7.0, device="cuda")
+        fa.fa_fwd_packed(b.d_q, b.d_k, b.d_v, o, lse, p, True, 0.1, fill=True)
+        assert fa.fa_get_device_status_detail()[:2] == (FA_ERR_INDEX, 52)
+        assert (o == 7).all() and (lse == 7).all()
+        ws = torch.empty(fa.fa_bwd_packed_workspace_size(b.rows, 2, 2, d), dtype=torch.uint8, device="cuda")
+        grads = [torch.full_like(o, 7.0) for _ in range(3)]
+        fa.fa_bwd_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, *grads, p, True, 0.1, ws, fill=True)
+        assert fa.fa_get_device_status_detail()[:2] == (FA_ERR_INDEX, 52)
+        assert all((g == 7).all() for g in grads)
