@@ -907,12 +907,21 @@ class PackedPlan:
         fa_packed_plan(cu_seqlens, self.rows, self.causal, self.buffer, stream)
 
 
+def _packed_rows(q, plan):
+    """(rows, Hq, d) of a call with `plan`, which has to be of the same rows: the library would answer another one with a
+    word in the device status and outputs that nothing has written. (A bare tensor does not tell its rows.)"""
+    rows, Hq, d = q.shape
+    if isinstance(plan, PackedPlan) and plan.rows != rows:
+        raise ValueError(f"the plan was made for {plan.rows} rows, the tensors have {rows}")
+    return rows, Hq, d
+
+
 def forward_packed(q, k, v, plan, causal: bool | None = None, scale: float | None = None, stream=None):
     """O [rows, Hq, d] (bf16) and L [Hq, rows] (fp32) of packed sequences (fa_fwd_packed): q [rows, Hq, d], k, v
-    [rows, Hkv, d], plan a PackedPlan, whose mask is taken unless `causal` is given. Rows of no sequence
-    become zeros."""
+    [rows, Hkv, d], plan a PackedPlan of as many rows, whose mask is taken unless `causal` is given. Rows of no
+    sequence become zeros."""
     import torch
-    rows, Hq, d = q.shape
+    rows, Hq, d = _packed_rows(q, plan)
     with _on_stream(stream):
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
@@ -928,7 +937,7 @@ def backward_packed(q, k, v, o, lse, do, plan, causal: bool | None = None, scale
     out: (dq, dk, dv) to write, e.g. the views of one packed gradient; None allocates contiguous ones.
     """
     import torch
-    rows, Hq, d = q.shape
+    rows, Hq, d = _packed_rows(q, plan)
     with _on_stream(stream):
         if out is None:
             out = tuple(torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in (q, k, v))

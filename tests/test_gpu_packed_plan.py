@@ -28,3 +28,18 @@ def test_a_plan_of_other_rows_or_none_leaves_everything_with_fill(d):
         fa.fa_bwd_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, *grads, p, True, 0.1, ws, fill=True)
         assert fa.fa_get_device_status_detail()[:2] == (FA_ERR_INDEX, 52)
         assert all((g == 7).all() for g in grads)
+
+
+def test_forward_and_backward_refuse_a_plan_of_other_rows():
+    import exact_softmax_attention_fa_gb300 as fa
+    b = Batch([100, 30], 2, 2, 64, SEED, tail=2)
+    plan = fa.PackedPlan(b.d_cu, b.rows)
+    o, lse = fa.forward_packed(b.d_q, b.d_k, b.d_v, plan)
+    fa.backward_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, plan)
+    for rows in (b.rows + 1, b.rows + 500):
+        other = fa.PackedPlan(b.d_cu, rows)
+        with pytest.raises(ValueError, match="rows"):
+            fa.forward_packed(b.d_q, b.d_k, b.d_v, other)
+        with pytest.raises(ValueError, match="rows"):
+            fa.backward_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, other)
+    assert fa.fa_get_device_status() == 0
