@@ -153,12 +153,15 @@ struct BwdWork {
 
 // The same over packed sequences: an entry of the plan's list is a sequence's
 // key tile j, every K/V head and chunk of it an item. The list is ordered by
-// the query tiles that see a key tile.
+// the query tiles that see a key tile. (The number of chunks, sched[4], D and L come
+// from the kernel before, beside whose end this grid is already resident: ordinary
+// loads behind the wait for it, since the read-only path wants data that stays as it
+// is while the kernel lives.)
 template <bool CAUSAL>
 struct BwdWork<CAUSAL, true> {
   int bh, c, j, i0, T, nq, gs, q0, row0, n;
   __device__ BwdWork(int item, const BwdLaunch& p) {
-    const uint32_t chunks = __ldg(p.sched + 4), units = p.BHkv * chunks;
+    const uint32_t chunks = p.sched[4], units = p.BHkv * chunks;
     const int e = static_cast<int>(static_cast<uint32_t>(item) / units);
     const uint32_t unit = static_cast<uint32_t>(item) - e * units;
     const int4 x = __ldg(packed_tiles(p.plan) + e);
@@ -190,7 +193,7 @@ struct BwdWork<CAUSAL, true> {
 template <bool RAG>
 __device__ __forceinline__ int bwd_total_items(const BwdLaunch& p) {
   if constexpr (RAG)
-    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BHkv * static_cast<int>(__ldg(p.sched + 4)) : 0;
+    return packed_plan_ok(p.plan, p.N) ? (p.plan->n_tiles - p.plan->n_short) * p.BHkv * static_cast<int>(p.sched[4]) : 0;
   else
     return p.BHkv * p.chunks * ((p.N + 127) / 128);
 }
@@ -564,7 +567,7 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
     if constexpr (RAG) {
       const int q = i * 128 + 64 * w + (r & 63);
       const float* from = (r < 64 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
-      const float x = __ldg(from + min(q, wk.n - 1));
+      const float x = from[min(q, wk.n - 1)];
       return r < 64 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
     }
     const size_t row = static_cast<size_t>(bh) * p.Npad + i * 128 + 64 * w;

@@ -333,11 +333,12 @@ __device__ void softmax_role(const BwdLaunch& p, Shared& sh, float* sLD, uint32_
 
   // thread r < 32 loads L2 of query 32w + r of the tile, 32 <= r < 64 its scaled D.
   // Queries behind the sequence's last one get L2 = +inf (weight 0) and D = 0.
+  // (Ordinary loads: this grid is resident while the kernel before still writes them.)
   auto fetch_ld = [&](const Work<CAUSAL>& wk, int bh, int i) -> float {
     if (r >= 64) return 0.f;
     const int q = i * C::BQ + 32 * w + (r & 31);
     const float* from = (r < 32 ? p.lse2 : p.D) + static_cast<size_t>(bh) * p.N + wk.row0;
-    const float x = __ldg(from + min(q, wk.n - 1));
+    const float x = from[min(q, wk.n - 1)];
     return r < 32 ? (q < wk.n ? x : INFINITY) : (q < wk.n ? x * sc : 0.f);
   };
   auto wait_all = [&](uint64_t* bar, int parity, int where) {

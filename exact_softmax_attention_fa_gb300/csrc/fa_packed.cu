@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const __grid_constant__
 
 // Where a group was split, dK, dV = bf16 of the sum of the chunks' fp32 partials
 // in chunk order (bitwise reproducible): a tile's rows of one head at a time, 8
-// elements a thread.
+// elements a thread. (Ordinary loads: this grid is resident while the partials are
+// still being written, which the read-only path does not allow.)
 __global__ void __launch_bounds__(256) packed_kv_sum_kernel(const __grid_constant__ BwdLaunch p) {
   griddep_wait();
   if (!packed_plan_ok(p.plan, p.N)) return;
@@ -278,9 +279,10 @@ __global__ void __launch_bounds__(256) packed_kv_sum_kernel(const __grid_constan
     for (int i = threadIdx.x; i < rows * units; i += 256) {
       const int row = first + i / units, col = i % units * 8;
       const float* src = p.kv_part + (is_v ? chunks * len : 0) + (static_cast<size_t>(h) * p.N + row) * p.d + col;
-      float4 a = ldg_f4(src), b = ldg_f4(src + 4);
+      auto part = [&](size_t at) { return *reinterpret_cast<const float4*>(src + at); };
+      float4 a = part(0), b = part(4);
       for (int c = 1; c < chunks; ++c) {
-        const float4 a2 = ldg_f4(src + c * len), b2 = ldg_f4(src + c * len + 4);
+        const float4 a2 = part(c * len), b2 = part(c * len + 4);
         a.x += a2.x, a.y += a2.y, a.z += a2.z, a.w += a2.w;
         b.x += b2.x, b.y += b2.y, b.z += b2.z, b.w += b2.w;
       }
