@@ -14,14 +14,14 @@ namespace {
 // One warp per query row, HD / 32 consecutive columns per lane; ranges that
 // hold no key the row sees are not read. HBM-bound.
 template <int HD>
-__global__ void __launch_bounds__(256) fwd_combine_kernel(const float* __restrict__ o_part,
-                                                          const float* __restrict__ lse_part,
+__global__ void __launch_bounds__(256) fwd_combine_kernel(const float* o_part, const float* lse_part,
                                                           __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
                                                           int BH, int Nq, int Nk, int causal, int causal_off,
                                                           int splits, int keys_per_split) {
   constexpr int PER = HD / 32;
   // Launched to overlap the forward's last round: its partials are final
-  // only once that grid has completed.
+  // only once that grid has completed. (They are read by ordinary loads: the
+  // read-only path wants data that stays as it is while the kernel lives.)
   griddep_wait();
   const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
@@ -31,18 +31,18 @@ __global__ void __launch_bounds__(256) fwd_combine_kernel(const float* __restric
   const int n = min(splits, last_key / keys_per_split + 1);
   const size_t plane = static_cast<size_t>(BH) * Nq;
   float m = -INFINITY;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, __ldg(lse_part + s * plane + row));
+  for (int s = 0; s < n; ++s) m = fmaxf(m, lse_part[s * plane + row]);
   float acc[PER];
 #pragma unroll
   for (int k = 0; k < PER; ++k) acc[k] = 0.f;
   float sum = 0.f;
   for (int s = 0; s < n; ++s) {
-    const float wgt = expf(__ldg(lse_part + s * plane + row) - m);
+    const float wgt = expf(lse_part[s * plane + row] - m);
     sum += wgt;
     const float* src = o_part + (s * plane + row) * HD + lane * PER;
 #pragma unroll
     for (int k = 0; k < PER; k += 2) {
-      const float2 v = __ldg(reinterpret_cast<const float2*>(src + k));
+      const float2 v = *reinterpret_cast<const float2*>(src + k);
       acc[k] = fmaf(wgt, v.x, acc[k]);
       acc[k + 1] = fmaf(wgt, v.y, acc[k + 1]);
     }

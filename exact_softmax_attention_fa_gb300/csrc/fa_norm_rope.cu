@@ -582,8 +582,10 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_ring_kernel
 }
 
 // dw[kind][col] = sum over the blocks of their partial sums, in 32 interleaved
-// runs of them in block order, in 64 bits. One block per 32 columns.
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, float* dwq, float* dwk,
+// runs of them in block order, in 64 bits. One block per 32 columns. (`part` is not
+// __restrict__: the pass before still writes it when this grid becomes resident, and
+// the read-only path wants data that stays as it is while the kernel lives.)
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, float* dwq, float* dwk,
                                                             int q_blocks, int k_blocks, int D) {
   __shared__ double red[32][32];
   griddep_wait();  // launched to overlap the pass that writes the partial sums

@@ -57,3 +57,20 @@ def test_packed_backward(name, where, written):
     text = block(source(name), *where)
     for arg in read_only_loads(text):
         assert not set(written) & set(re.findall(r"\w+", arg)), arg
+
+
+JOINING = [
+    ("fa_fwd.cu", r"void __launch_bounds__\(256\) fwd_combine_kernel\(", ("o_part", "lse_part", "src")),
+    ("fa_norm_rope.cu", r"void __launch_bounds__\(1024\) norm_rope_dw_kernel\(", ("part",)),
+    ("fa_fwd_kv8.cu", r"kv8_combine_kernel\(", ("part", "part_ml")),
+    ("fa_fwd_kv8_tile.cu", r"kv8_tile_combine_kernel\(", ("part", "part_ml", "run")),
+]
+
+
+@pytest.mark.parametrize("name,where,written", JOINING, ids=lambda x: x if isinstance(x, str) and "." in x else None)
+def test_joining_kernels(name, where, written):
+    text = block(source(name), where)
+    for arg in read_only_loads(text):
+        assert not set(written) & set(re.findall(r"\w+", arg)), arg
+    for parameter in re.findall(r"const [\w ]+\* *__restrict__ (\w+)", text):
+        assert parameter not in written, parameter
