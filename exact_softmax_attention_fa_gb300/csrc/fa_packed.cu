@@ -320,8 +320,13 @@ __global__ void __launch_bounds__(256) packed_fill_kernel(const __grid_constant_
   }
 }
 
-int plan_tiles(int B, int rows) { return rows / 128 + std::min(B, rows); }
-int plan_pairs(int B, int rows) { return rows / 256 + std::min(B, rows); }
+// Entries that a plan has room for: full tiles, and one begun tile (and pair) a
+// sequence. Their places are counted in 32 bits.
+long long plan_tiles(int B, int rows) { return static_cast<long long>(rows / 128) + std::min(B, rows); }
+long long plan_pairs(int B, int rows) { return static_cast<long long>(rows / 256) + std::min(B, rows); }
+bool plan_fits(int B, int rows) {
+  return B >= 0 && rows >= 0 && plan_tiles(B, rows) + plan_pairs(B, rows) < (1ll << 31);
+}
 
 constexpr size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -384,13 +389,13 @@ using namespace fa;
 extern "C" {
 
 size_t fa_packed_plan_size(int B, int rows) {
-  if (B < 0 || rows < 0) return 0;
-  return kPackedHead + (static_cast<size_t>(plan_tiles(B, rows)) + plan_pairs(B, rows)) * sizeof(int4);
+  if (!plan_fits(B, rows)) return 0;
+  return kPackedHead + static_cast<size_t>(plan_tiles(B, rows) + plan_pairs(B, rows)) * sizeof(int4);
 }
 
 fa_status_t fa_packed_plan(const int* cu_seqlens, int B, int rows, int causal, void* plan, size_t plan_bytes,
                            cudaStream_t stream) {
-  if (B < 0 || rows < 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+  if (!plan_fits(B, rows) || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
   if (B > 0 && !cu_seqlens) return FA_ERR_INVALID_ARG;
   if (!aligned(cu_seqlens, 4)) return FA_ERR_MISALIGNED;
   if (!plan || plan_bytes < fa_packed_plan_size(B, rows)) return FA_ERR_WORKSPACE;
@@ -399,7 +404,7 @@ fa_status_t fa_packed_plan(const int* cu_seqlens, int B, int rows, int causal, v
   const fa_status_t st = device_info(&dev);
   if (st != FA_OK) return st;
   packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_seqlens, B, rows, causal, static_cast<PackedPlan*>(plan),
-                                                    plan_tiles(B, rows), dev.status);
+                                                    static_cast<int>(plan_tiles(B, rows)), dev.status);
   return from_cuda(cudaGetLastError());
 }
 

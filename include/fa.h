@@ -443,7 +443,8 @@ fa_status_t fa_norm_rope_axes_bwd(const void* dq, const void* dk, const void* dv
  * depends on the lengths alone: one plan serves all layers of a step and both
  * directions, from any number of streams, and no call reads lengths on the host.
  *   plan   : out, fa_packed_plan_size(B, rows) bytes of device memory, 256-byte
- *            aligned. cu_seqlens is not read after this call.
+ *            aligned. cu_seqlens is not read after this call. (2 min(B, rows) + rows / 128 + rows / 256
+ *            entries of 16 bytes, below 2^31 of them, else FA_ERR_INVALID_ARG.)
  *   causal : the mask of the calls it is for. A plan serves the other mask too;
  *            only the order of the work is then not the best.
  *   Lengths that are not 0 <= cu_seqlens[b] <= cu_seqlens[b + 1] <= rows are
@@ -467,7 +468,7 @@ fa_status_t fa_norm_rope_axes_bwd(const void* dq, const void* dk, const void* dv
  *   group's heads are summed in parts), whatever the plan's order.
  * rows * Hq must be below 2^31, Hq at most 65535. rows = 0 or Hq = 0 is a no-op.
  */
-size_t fa_packed_plan_size(int B, int rows); /* 0 for negative sizes */
+size_t fa_packed_plan_size(int B, int rows); /* 0 for negative sizes, and for plans of 2^31 entries or more */
 fa_status_t fa_packed_plan(const int* cu_seqlens, int B, int rows, int causal, void* plan, size_t plan_bytes,
                            cudaStream_t stream);
 fa_status_t fa_fwd_packed(const void* q, const void* k, const void* v, const long long* strides, void* o, float* lse,

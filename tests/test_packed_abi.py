@@ -141,3 +141,14 @@ def test_axes_backward_has_the_checks_of_the_forward(lib):
     for kw in (dict(n=0), dict(n=5), dict(axes=None), dict(positions=0), dict(axes=bytes([1] * 32))):
         assert call(**kw) == INVALID, kw
     assert call(positions=P + 1) == MISALIGNED
+
+
+def test_plan_sizes_beyond_32_bits(lib):
+    size, most = lib.fa_packed_plan_size, 2**31 - 1
+    fits = 2**30 - 2**24  # 2 B + rows / 128 + rows / 256 just below 2^31 at B = rows
+    for B, rows in ((most, most), (1 << 30, most), (most, 2**31 - 2**23)):
+        assert size(B, rows) == 0, (B, rows)
+        assert plan(lib, B=B, rows=rows, size=1 << 62) == INVALID, (B, rows)
+    for B, rows in ((fits, fits), (1, most), (most, 1000)):
+        assert size(B, rows) == 256 + 16 * (rows // 128 + rows // 256 + 2 * min(B, rows))
+        assert plan(lib, B=B, rows=rows, size=size(B, rows) - 1) == WORKSPACE, (B, rows)
