@@ -487,7 +487,11 @@ def _axes(axes, positions, rot):
     """The C arguments for the axes: the bytes, one a pair, and how many planes the positions have."""
     if positions is None:
         raise ValueError("positions are needed for a rotation by axes: int32 [axes, B, N]")
-    axes = bytes(axes)
+    if not isinstance(axes, bytes):  # number by number: bytes() makes n into n zeros, and of an array what its memory holds
+        try:
+            axes = bytes(list(axes))
+        except TypeError:
+            raise ValueError("axes must be a sequence of whole numbers, one for each rotated pair") from None
     if 2 * len(axes) != rot:
         raise ValueError(f"axes has {len(axes)} entries, expected one for each of the {rot // 2} rotated pairs")
     return axes, positions.shape[0]

@@ -1,0 +1,36 @@
+"""How the binding of the rotation by axes takes its axes and positions."""
+
+import numpy as np
+import pytest
+
+import test_gpu_norm_rope as nr
+
+pytestmark = pytest.mark.gpu
+
+SEED, ROWS = 92000, 40
+
+
+def case(seed):
+    import torch
+    x, _ = nr.packed(2, 9, 6, 64, seed)
+    cos, sin, _, _ = nr.tables(ROWS, 64)
+    pos = torch.tensor(np.random.default_rng(seed).integers(0, ROWS, (3, 2, 9)), dtype=torch.int32, device="cuda")
+    return nr.split(x, 4, 1), cos, sin, pos
+
+
+def test_axes_by_number():
+    """An integer turned every pair by axis 0, and an array of 64-bit numbers was taken by its bytes."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    views, cos, sin, pos = case(SEED)
+    axes = [i % 3 for i in range(32)]
+    want = fa.norm_rope(*views, None, None, cos, sin, pos, axes=axes)
+    for same in (bytes(axes), np.array(axes), np.array(axes, np.int32), torch.tensor(axes)):
+        for x, y in zip(fa.norm_rope(*views, None, None, cos, sin, pos, axes=same), want):
+            assert torch.equal(x, y)
+    for bad in (32, np.int64(32), np.zeros(4, np.int64), np.zeros(8, np.int32)):
+        with pytest.raises(ValueError):
+            fa.norm_rope(*views, None, None, cos, sin, pos, axes=bad)
+        with pytest.raises(ValueError):
+            fa.norm_rope_backward(*want, *views[:2], None, None, cos, sin, pos, axes=bad)
+    assert fa.fa_get_device_status() == 0

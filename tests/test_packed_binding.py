@@ -1,5 +1,6 @@
 """What the binding of the packed operators refuses before it touches a device."""
 
+import numpy as np
 import pytest
 
 import exact_softmax_attention_fa_gb300 as fa
@@ -24,3 +25,22 @@ def test_a_plan_of_other_rows_is_refused(rows):
         fa.backward_packed(x, x, x, x, lse, x, plan_of(rows))
     with pytest.raises(ValueError, match="rows"):
         fa.backward_packed(x, x, x, x, lse, x, plan_of(rows), out=(x, x, x), workspace=torch.zeros(1, dtype=torch.uint8))
+
+
+AXES = [0, 1, 2, 1, 0, 2, 2, 2]
+
+
+@pytest.mark.parametrize("kind", [list, tuple, bytes, bytearray, iter, np.int64, np.int32, np.uint8, np.int8, torch.tensor],
+                         ids=lambda k: k.__name__)
+def test_axes_are_taken_number_by_number(kind):
+    positions = torch.zeros(3, 1, 4, dtype=torch.int32)
+    axes = np.array(AXES, dtype=kind) if isinstance(kind, type) and issubclass(kind, np.generic) else kind(AXES)
+    assert fa._axes(axes, positions, 16) == (bytes(AXES), 3)
+
+
+@pytest.mark.parametrize("axes", [8, np.int64(8), True, 8.0, [0.0] * 8, "00000000", [None] * 8, [-1] * 8, [256] * 8, [0] * 7,
+                                  np.zeros(1, np.int64), np.zeros(2, np.int32), torch.zeros(8), object()], ids=repr)
+def test_what_is_no_axes(axes):
+    """An integer is no sequence, and an array's bytes are not its numbers (2 int32 are 8 bytes)."""
+    with pytest.raises(ValueError):
+        fa._axes(axes, torch.zeros(1, 1, 4, dtype=torch.int32), 16)
