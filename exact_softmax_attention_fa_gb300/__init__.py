@@ -497,6 +497,11 @@ def _axes(axes, positions, rot):
     return axes, positions.shape[0]
 
 
+def _need_axes(axes):
+    if axes is None:  # which would be the rotation by one position
+        raise ValueError("axes are needed: one for each rotated pair")
+
+
 def fa_norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, q, k, v, interleaved: bool = False,
                      eps: float = 1e-6, stream=None) -> None:
     """fa_norm_rope_fwd of the C ABI: q_in [B, Hq, N, d], k_in, v_in [B, Hkv, N, d] with any
@@ -512,6 +517,7 @@ def fa_norm_rope_axes_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q
                           eps: float = 1e-6, stream=None) -> None:
     """fa_norm_rope_axes_fwd of the C ABI: fa_norm_rope_fwd with positions int32 [axes, B, N] and axes, a sequence
     of whole numbers (or bytes, which need no conversion): the axis of each of the rot / 2 pairs."""
+    _need_axes(axes)
     _norm_rope_fwd(q_in, k_in, v_in, wq, wk, cos, sin, positions, axes, q, k, v, interleaved, eps, stream)
 
 
@@ -564,6 +570,7 @@ def fa_norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, dq_in,
 def fa_norm_rope_axes_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq_in, dk_in, dv_in, dwq, dwk,
                           workspace, interleaved: bool = False, eps: float = 1e-6, stream=None) -> None:
     """fa_norm_rope_axes_bwd of the C ABI: fa_norm_rope_bwd with positions and axes as fa_norm_rope_axes_fwd."""
+    _need_axes(axes)
     _norm_rope_bwd(dq, dk, dv, q_in, k_in, wq, wk, cos, sin, positions, axes, dq_in, dk_in, dv_in, dwq, dwk, workspace,
                    interleaved, eps, stream)
 

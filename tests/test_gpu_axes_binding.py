@@ -34,3 +34,16 @@ def test_axes_by_number():
         with pytest.raises(ValueError):
             fa.norm_rope_backward(*want, *views[:2], None, None, cos, sin, pos, axes=bad)
     assert fa.fa_get_device_status() == 0
+
+
+def test_the_calls_by_axes_need_axes():
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    views, cos, sin, pos = case(SEED + 1)
+    out = [torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda") for t in views]
+    with pytest.raises(ValueError, match="axes"):
+        fa.fa_norm_rope_axes_fwd(*views, None, None, cos, sin, pos[0].contiguous(), None, *out)
+    with pytest.raises(ValueError, match="axes"):
+        fa.fa_norm_rope_axes_bwd(*out, None, None, None, None, cos, sin, pos[0].contiguous(), None, *out, None, None, None)
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in out)

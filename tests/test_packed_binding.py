@@ -44,3 +44,13 @@ def test_what_is_no_axes(axes):
     """An integer is no sequence, and an array's bytes are not its numbers (2 int32 are 8 bytes)."""
     with pytest.raises(ValueError):
         fa._axes(axes, torch.zeros(1, 1, 4, dtype=torch.int32), 16)
+
+
+def test_the_calls_by_axes_need_axes():
+    """Without them they would be the calls by one position."""
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    cos, pos = torch.zeros(8, 32), torch.zeros(1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="axes"):
+        fa.fa_norm_rope_axes_fwd(x, x, x, None, None, cos, cos, pos, None, x, x, x)
+    with pytest.raises(ValueError, match="axes"):
+        fa.fa_norm_rope_axes_bwd(x, x, x, None, None, None, None, cos, cos, pos, None, x, x, x, None, None, None)
