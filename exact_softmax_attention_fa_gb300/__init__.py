@@ -484,7 +484,10 @@ def _norm_rope_ok(wq, wk, cos, sin, positions, B, N, d, axes=None):
 
 
 def _axes(axes, positions, rot):
-    """The C arguments for the axes: the bytes, one a pair, and how many planes the positions have."""
+    """The C arguments for the axes: the bytes, one a pair, and how many planes the positions have. Without a rotation
+    neither is used."""
+    if rot == 0:
+        return None, 0
     if positions is None:
         raise ValueError("positions are needed for a rotation by axes: int32 [axes, B, N]")
     if not isinstance(axes, bytes):  # number by number: bytes() makes n into n zeros, and of an array what its memory holds

@@ -47,3 +47,19 @@ def test_the_calls_by_axes_need_axes():
         fa.fa_norm_rope_axes_bwd(*out, None, None, None, None, cos, sin, pos[0].contiguous(), None, *out, None, None, None)
     torch.cuda.synchronize()
     assert all((t == 7).all() for t in out)
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_without_a_rotation_axes_and_positions_are_not_used(norm):
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    views, _, _, pos = case(SEED + 2)
+    w = nr.weights(64, SEED + 2, torch.float32)[0] if norm else None
+    want = fa.norm_rope(*views, w, w)
+    back = fa.norm_rope_backward(*want, *views[:2], w, w)
+    for axes, p in (([], None), ([0] * 32, None), ([], pos)):
+        for x, y in zip(fa.norm_rope(*views, w, w, None, None, p, axes=axes), want):
+            assert torch.equal(x, y)
+        got = fa.norm_rope_backward(*want, *views[:2], w, w, None, None, p, axes=axes)
+        assert all(x is y is None or torch.equal(x, y) for x, y in zip(got, back))
+    assert fa.fa_get_device_status() == 0

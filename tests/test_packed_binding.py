@@ -54,3 +54,11 @@ def test_the_calls_by_axes_need_axes():
         fa.fa_norm_rope_axes_fwd(x, x, x, None, None, cos, cos, pos, None, x, x, x)
     with pytest.raises(ValueError, match="axes"):
         fa.fa_norm_rope_axes_bwd(x, x, x, None, None, None, None, cos, cos, pos, None, x, x, x, None, None, None)
+
+
+def test_without_a_rotation_axes_and_positions_are_not_used():
+    for axes in ([], b"", [0] * 32, 7):
+        for positions in (None, torch.zeros(3, 1, 4, dtype=torch.int32)):
+            assert fa._axes(axes, positions, 0) == (None, 0)
+    with pytest.raises(ValueError, match="positions"):
+        fa._axes([0] * 8, None, 16)
