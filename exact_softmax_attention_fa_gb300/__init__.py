@@ -657,7 +657,7 @@ def fa_fwd_packed(q, k, v, o, lse, plan, causal: bool, scale: float, fill: bool 
     last dimension (views of a packed projection), lse float32 [Hq, rows]; plan a PackedPlan (or the
     tensor that fa_packed_plan filled) of the same rows. fill: zeros in the rows of no sequence."""
     import torch
-    plan, bf = getattr(plan, "buffer", plan), torch.bfloat16
+    made, plan, bf = plan, getattr(plan, "buffer", plan), torch.bfloat16
     qs, ks = q.shape, k.shape
     sq, sk, sv, so = q.stride(), k.stride(), v.stride(), o.stride()
     if not (len(qs) == len(ks) == 3 and q.dtype == k.dtype == v.dtype == o.dtype == bf and o.shape == qs and v.shape == ks
@@ -667,6 +667,8 @@ def fa_fwd_packed(q, k, v, o, lse, plan, causal: bool, scale: float, fill: bool 
             and plan.dtype == torch.uint8 and plan.is_contiguous()
             and _devices(q, k, v, o, lse, plan) == {torch.cuda.current_device()}):
         _packed_refuse(q, k, plan, lse, (("o", o),), (("v", v),))
+    if isinstance(made, PackedPlan):
+        made._used_on(stream)
     check("fa_fwd_packed", load().fa_fwd_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides8(*sq[:2], *sk[:2], *sv[:2], *so[:2]), o.data_ptr(),
         lse.data_ptr(), plan.data_ptr(), qs[0], qs[1], ks[1], qs[2], 1 if causal else 0, scale, 1 if fill else 0,
@@ -683,7 +685,7 @@ def fa_bwd_packed(q, k, v, o, lse, do, dq, dk, dv, plan, causal: bool, scale: fl
     and contiguous last dimension (dq, dk, dv may be the views of one packed gradient), lse and plan as
     in the forward, workspace a CUDA uint8 tensor of at least fa_bwd_packed_workspace_size() bytes."""
     import torch
-    plan, bf = getattr(plan, "buffer", plan), torch.bfloat16
+    made, plan, bf = plan, getattr(plan, "buffer", plan), torch.bfloat16
     qs, ks = q.shape, k.shape
     sq, sk, sv, so, sg = q.stride(), k.stride(), v.stride(), o.stride(), do.stride()
     tq, tk, tv = dq.stride(), dk.stride(), dv.stride()
@@ -697,6 +699,8 @@ def fa_bwd_packed(q, k, v, o, lse, do, dq, dk, dv, plan, causal: bool, scale: fl
         if workspace is not None and not _bytes(workspace):
             _refuse((("workspace", workspace, (torch.uint8,), workspace.shape, True),))
         _packed_refuse(q, k, plan, lse, (("o", o), ("do", do), ("dq", dq)), (("v", v), ("dk", dk), ("dv", dv)))
+    if isinstance(made, PackedPlan):
+        made._used_on(stream)
     check("fa_bwd_packed", load().fa_bwd_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
         _strides10(*sq[:2], *sk[:2], *sv[:2], *so[:2], *sg[:2]), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
@@ -904,8 +908,9 @@ class PackedPlan:
 
     cu_seqlens: int32 [B + 1] on the device; sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the
     `rows` rows of q, k, v. Make one for each batch and use it in every layer and both directions, on any
-    stream that is ordered behind the one it was made on. `update` takes the next batch's lengths into the
-    same memory, so that a captured graph of a step can be replayed with them.
+    stream that is ordered behind the one it was made on; the last reference to it may go while calls that
+    take it are still queued (not while a captured graph of them lives). `update` takes the next batch's lengths
+    into the same memory, so that a captured graph of a step can be replayed with them.
     """
 
     def __init__(self, cu_seqlens, rows: int, causal: bool = True, stream=None):
@@ -914,11 +919,26 @@ class PackedPlan:
         with _on_stream(stream):
             self.buffer = torch.empty(max(1, fa_packed_plan_size(max(0, self.B), max(0, rows))), dtype=torch.uint8,
                                       device=cu_seqlens.device)
+        self._streams = {_stream_handle(stream)} if self.buffer.is_cuda else set()
         fa_packed_plan(cu_seqlens, rows, causal, self.buffer, stream)
 
     def update(self, cu_seqlens, stream=None) -> None:
         """List the work of other lengths of the same number of sequences (or fewer) and rows."""
+        self._used_on(stream)
         fa_packed_plan(cu_seqlens, self.rows, self.causal, self.buffer, stream)
+
+
+    def _used_on(self, stream):
+        """The plan's memory is not given away before the work queued on this stream is done with it. (Entries that
+        something else has overwritten would send the kernels anywhere.)"""
+        import torch
+        handle = _stream_handle(stream)
+        if handle in self._streams:
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        self.buffer.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        self._streams.add(handle)
 
 
 def _packed_rows(q, plan):

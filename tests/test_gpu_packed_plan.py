@@ -71,3 +71,51 @@ def test_calls_behind_one_another_share_a_workspace(d):
     assert fa.fa_get_device_status() == 0
     for i, grads in enumerate(got):
         assert all(torch.equal(x, y) for x, y in zip(grads, alone[i % 4][1]))
+
+
+def test_a_plan_dropped_while_another_stream_uses_it():
+    """Made on one stream, used on another that is far behind, and dropped: nothing gets the plan's memory until then."""
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    b = Batch([300, 40, 129], 4, 2, 64, SEED + 30)
+    want = fa.forward_packed(b.d_q, b.d_k, b.d_v, fa.PackedPlan(b.d_cu, b.rows))
+    want_grads = fa.backward_packed(b.d_q, b.d_k, b.d_v, *want, b.d_do, fa.PackedPlan(b.d_cu, b.rows))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = fa.PackedPlan(b.d_cu, b.rows)
+    at, n = plan.buffer.data_ptr(), plan.buffer.numel()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    o, lse = fa.forward_packed(b.d_q, b.d_k, b.d_v, plan, stream=side)
+    grads = fa.backward_packed(b.d_q, b.d_k, b.d_v, o, lse, b.d_do, plan, stream=side)
+    del plan
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    assert not side.query()
+    assert all(t.data_ptr() + n <= at or at + n <= t.data_ptr() for t in others)
+    torch.cuda.synchronize()
+    for x, y in zip((o, lse, *grads), (*want, *want_grads)):
+        assert torch.equal(x, y)
+    assert fa.fa_get_device_status() == 0
+
+
+def test_a_plan_made_outside_serves_a_captured_step():
+    import exact_softmax_attention_fa_gb300 as fa
+    import torch
+    b = Batch([300, 40, 129], 4, 2, 64, SEED + 31)
+    plan = fa.PackedPlan(b.d_cu, b.rows)
+    want = fa.forward_packed(b.d_q, b.d_k, b.d_v, plan)
+    want_grads = fa.backward_packed(b.d_q, b.d_k, b.d_v, *want, b.d_do, plan)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.forward_packed(b.d_q, b.d_k, b.d_v, plan)
+        got_grads = fa.backward_packed(b.d_q, b.d_k, b.d_v, *got, b.d_do, plan)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((*got, *got_grads), (*want, *want_grads)):
+            assert torch.equal(x, y)
+            x.zero_()
+    del graph, plan
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == 0

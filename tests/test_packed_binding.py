@@ -62,3 +62,72 @@ def test_without_a_rotation_axes_and_positions_are_not_used():
             assert fa._axes(axes, positions, 0) == (None, 0)
     with pytest.raises(ValueError, match="positions"):
         fa._axes([0] * 8, None, 16)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class Buffer:
+    """The plan's memory as the binding looks at it."""
+    dtype, shape = torch.uint8, (1 << 20,)
+
+    def __init__(self):
+        self.recorded = []
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return -1
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def numel(self):
+        return 1 << 20
+
+    def element_size(self):
+        return 1
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+class Library:
+    """Calls that do nothing but say which stream they were given."""
+
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 256
+        return lambda *a: self.streams.append(a[-1]) or 0
+
+
+def test_a_plans_memory_waits_for_every_stream_that_uses_it(monkeypatch):
+    """A plan is dropped as soon as the last call is queued, and its memory came from the stream it was made on: without
+    a word to the allocator that stream's next tensor could take it while another stream's kernels still read it."""
+    lib = Library()
+    monkeypatch.setattr(fa, "load", lambda: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 11, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(11))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    plan = plan_of(10)
+    plan.buffer, plan._streams = Buffer(), {11}
+    x, lse, ws = torch.zeros(10, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 10), torch.zeros(8, dtype=torch.uint8)
+    forward = lambda stream: fa.fa_fwd_packed(x, x, x, x, lse, plan, True, 0.1, stream=stream)
+    backward = lambda stream: fa.fa_bwd_packed(x, x, x, x, lse, x, x, x, x, plan, True, 0.1, ws, stream=stream)
+    forward(None), backward(None)
+    assert plan.buffer.recorded == []  # the stream it was made on
+    forward(Stream(12)), forward(12), backward(Stream(12))
+    assert plan.buffer.recorded == [12]
+    backward(13)
+    plan.update(torch.zeros(2, dtype=torch.int32), Stream(14))
+    assert plan.buffer.recorded == [12, 13, 14] and lib.streams == [11, 11, 12, 12, 12, 13, 14]
+    with pytest.raises(ValueError):  # a refused call uses nothing
+        fa.fa_fwd_packed(x, x[:3], x, x, lse, plan, True, 0.1, stream=15)
+    assert plan.buffer.recorded == [12, 13, 14]
