@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
         cp_async16_or_zero(sV + tile_at<HD>(r, u), in ? vs : vp, in);
       }
     }
-    cp_async_group();
+    cp_async_commit();
     const __nv_bfloat16* q = head_rows(p.q, p.q_st, row0, hk * group);
     __nv_bfloat16* o_rows = p.o + static_cast<long long>(row0) * p.o_st[0] + hk * group * p.o_st[1];
     bool waited = false;
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(32 * kWarps, ShortCfg<HD>::PER_SM)
             cp_async16_or_zero(sQ + tile_at<HD>(r, u), (at < 0 ? q : src) + 8 * u, at >= 0);
         }
       }
-      cp_async_group();
-      cp_async_wait_groups<0>();
+      cp_async_commit();
+      cp_async_wait<0>();
       if (!waited) __syncthreads();  // K and V are in
       waited = true;
       __syncwarp();
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, ShortBwdCfg<HD>::PER_SM)
         if (in) o_piece[m] = __ldg(reinterpret_cast<const uint4*>(o + pos * p.o_st[0] + head * p.o_st[1]));
         if (in && u == 0) L_mine[m] = __ldg(p.lse + static_cast<size_t>(hk * group + head) * p.rows + row0 + pos) * kLog2e;
       }
-      cp_async_group();
-      cp_async_wait_groups<0>();
+      cp_async_commit();
+      cp_async_wait<0>();
       // D of the rows, from this thread's pieces of O and of dO (which it copied itself)
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {

@@ -1,6 +1,5 @@
 // Warp-level pieces of the kernels for short packed sequences: bf16 matrix
-// products of a warp, the loads that feed them from shared memory, and
-// asynchronous copies into it.
+// products of a warp, and the loads that feed them from shared memory.
 #pragma once
 
 #include <cstdint>
@@ -8,16 +7,6 @@
 #include "sm103_ptx.cuh"
 
 namespace fa {
-
-// 16 bytes from global to shared memory; zeros where `valid` is false (nothing is read then).
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void cp_async_wait_groups() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
 
 // Four 8 x 8 matrices of 16-bit values: lane 8 i + j gives the address of row j of
 // matrix i; lane l receives elements (l / 4, 2 (l % 4) + {0, 1}) of each, or of
