@@ -548,10 +548,11 @@ __device__ void bwd_softmax_role(const BwdLaunch& p, BwdShared& sh, uint8_t* sDS
   const int total = bwd_total_items<RAG>(p);
   bool alive = true;
   // Over packed sequences half of the statistics are read ahead, at d = 64 too, and
-  // the weights stay in fp32, which takes no packing: sequences of up to 8192 rows, 32
-  // + 8 heads of d = 128, 1669 us with the dQ kernel, 1735 with a quarter of them, 1745
-  // with all and the weights two in a register; 4096 rows, 16 + 4 heads of d = 64, 890,
-  // with none 964, in four warpgroups of 32 columns 925.
+  // the weights stay in fp32, which takes no packing: four sequences of 1197 to 7129
+  // rows, 32 + 8 heads of d = 128, 1669 us with the dQ kernel, 1735 with a quarter of
+  // them, 1745 with all and the weights two in a register (later steps in that kernel
+  // made it 1653); eight of 2347 to 4096 rows, 16 + 4 heads of d = 64, 890, with none
+  // 964, in four warpgroups of 32 columns 925.
   constexpr bool kPrefetchStats = !DQ && (HD == 128 || RAG);
   constexpr int kAhead = RAG ? 8 : 16;  // of 16 vectors
   // P^T of the current tile as the bf16 pairs written to TMEM, kept from

@@ -333,8 +333,8 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
   const uint32_t bar_id = 1 + w;
   const int total = dq_total_items<RAG>(p);
   bool alive = true;
-  // P of the current tile, bf16 pairs; over packed sequences fp32 (8 sequences of up to
-  // 4096 rows, d = 64: 811 us with dK and dV, half of them by pairs of 16 bits 828)
+  // P of the current tile, bf16 pairs; over packed sequences fp32 (8 sequences of 2149 to
+  // 3800 rows, 16 + 4 heads, d = 64: 811 us with dK and dV, half of them by pairs of 16 bits 828)
   Weights<64, RAG> pk;
 
   auto wait_all = [&](uint64_t* bar, int parity, int where) {
@@ -359,6 +359,8 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
     const DqWork<CAUSAL, RAG> wk(item, p);
     const int row = wk.i * 128 + r;
     const bool held = !RAG || row < wk.len(p);
+    // (D and L through the read-only path: the pass before this one has waited for the
+    // kernel that writes them before it let this grid start.)
     const size_t srow = RAG ? static_cast<size_t>(wk.bh) * p.N + wk.row0 + row : static_cast<size_t>(wk.bh) * p.Npad + row;
     const float l2 = held ? __ldg(p.lse2 + srow) : INFINITY;  // +inf on padding rows: their P is 0
     const float dsc = held ? __ldg(p.D + srow) * sc : 0.f;
@@ -406,7 +408,8 @@ __device__ void dq_softmax_role(const BwdLaunch& p, DqShared& sh, uint32_t tmem,
       // S buffer t & 1 (phase A has read them)
       wait_all(&sh.dp_full, t & 1, WHERE_BWD_SOFTMAX);
       if (alive) {
-        uint32_t ds[RAG ? 16 : 32];  // over packed sequences a half at a time (1636 -> 1626 us, 8192 rows)
+        // over packed sequences a half at a time (4 of 1197 to 7129 rows, d = 128: 1636 -> 1626 us)
+        uint32_t ds[RAG ? 16 : 32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t dpv[32];

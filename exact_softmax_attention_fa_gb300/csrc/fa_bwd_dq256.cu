@@ -376,6 +376,7 @@ __device__ void dq256_softmax_role(const BwdLaunch& p, Dq256Shared& sh, uint32_t
     const Dq256Work<CAUSAL, RAG> wk(item, p);
     const int row = wk.i * 128 + r;
     const bool held = !RAG || row < wk.len(p);
+    // (D and L through the read-only path: complete before this grid starts, as in fa_bwd_dq.cu)
     const size_t srow = RAG ? static_cast<size_t>(wk.bh) * p.N + wk.row0 + row : static_cast<size_t>(wk.bh) * p.Npad + row;
     const float l2 = held ? __ldg(p.lse2 + srow) : INFINITY;  // +inf on padding rows: their P is 0
     const float dsc = held ? __ldg(p.D + srow) * sc : 0.f;

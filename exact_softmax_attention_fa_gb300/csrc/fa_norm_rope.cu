@@ -405,7 +405,13 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
 // heads each of q, k and v, d = 128, us with this kernel and the one above, by tokens:
 // 1024 14.3 and 13.1, 3300 26.8 and 27.0, 4096 32.5 and 33.9, 16384 100 and 111;
 // without weights 3300 13.3 and 12.0, 4096 16.2 and 22.6, 16384 71 and 91. Hence from
-// kRingUnits units a lane group on, which are 4032 of these tokens.)
+// kRingUnits units a lane group on, which are 4040 of these tokens on 152 SMs. With few
+// heads a token, whose units are short, the rule holds as well: 16384 tokens of 6 + 2
+// heads of d = 256 with weights 68 and 80, without 42 and 51, of 8 + 1 of d = 128 58 and
+// 70, 36 and 44, of one each of d = 64, just over the limit, 16.4 and 17.1, 10.3 and 11.1.
+// Up to 6.6 units some with weights are the slower by up to 1.7 us, 9416 tokens of 6 + 2
+// heads of d = 128 32.8 and 31.1, others the faster by as much or more, as many tokens of
+// 8 + 2 32.9 and 36.3.)
 template <int D, bool INTER, bool NORM, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_ring_kernel(const __grid_constant__ NormRope p) {
   constexpr int GROUPS = kThreads / (D / 8);
